@@ -28,6 +28,8 @@ def _dtype_code(t) -> int:
         return B.DLC_DATA_BFLOAT16
     if t.dtype == torch.float64:
         return B.DLC_DATA_DOUBLE
+    if t.dtype == torch.float8_e4m3fn:
+        return B.DLC_DATA_FLOAT8_E4M3
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
@@ -330,6 +332,242 @@ def activation_forward(handle: Handle, x, y, *, mode="relu", coef=0.0, alpha=1.0
         return op(x, y, alpha=alpha, beta=beta)
     finally:
         op.close()
+
+
+LINEAR_ACT_MODES = {"identity": B.DLC_ACTIVATION_IDENTITY, "relu": B.DLC_ACTIVATION_RELU,
+                    "sigmoid": B.DLC_ACTIVATION_SIGMOID, "tanh": B.DLC_ACTIVATION_TANH,
+                    "silu": B.DLC_ACTIVATION_SILU, "gelu": B.DLC_ACTIVATION_GELU}
+
+
+def _ptr(t) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+class _ChannelOp:
+    """Descriptors and workspace of one channel operator, built once from
+    example tensors for repeated calls on the same shapes, strides, types and
+    16-byte alignment.  Activations are [rows, channels] matrices or 4-D
+    tensors with ``axes`` ("NHWC" or "NCHW"); weights are [K, C] matrices or
+    4-D filters with R = S = 1.  Calls check what each pointer may be (vectors
+    are dense FP32), launch on the handle's stream and return no copies."""
+
+    def __init__(self, handle: Handle, axes: str):
+        self.handle = handle
+        self.axes = axes
+        self._tensors, self._filters = [], []
+        self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
+
+    def _act_desc(self, t):
+        """Descriptor of an activation tensor (None for an absent one)."""
+        if t is None:
+            return None
+        if t.dim() == 2:
+            (rows, c), (rs, cs) = t.shape, t.stride()
+            sizes, strides = (rows, c, 1, 1), (rs, cs, 0, 0)
+        else:
+            sizes, strides = _logical(t, self.axes, "NCHW")
+        d = B.dlcCreateTensorDescriptor()
+        self._tensors.append(d)
+        B.dlcSetTensor4dDescriptorEx(d, _dtype_code(t), *sizes, *strides)
+        return d
+
+    def _weight_desc(self, t):
+        if t is None:
+            return None
+        if not t.is_contiguous():
+            raise ValueError("filter tensors must be dense (contiguous)")
+        if t.dim() not in (2, 4) or (t.dim() == 4 and t.numel() != t.shape[0] * max(t.shape[1:])):
+            raise ValueError("weights are [K, C] or filters with R = S = 1")
+        d = B.dlcCreateFilterDescriptor()
+        self._filters.append(d)
+        B.dlcSetFilter4dDescriptor(d, _dtype_code(t), B.DLC_TENSOR_NCHW, t.shape[0],
+                                   t.numel() // t.shape[0], 1, 1)
+        return d
+
+    def _set_workspace(self, nbytes: int, device):
+        import torch
+        self._ws_bytes = nbytes
+        if nbytes:
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            self._ws_ptr = self.workspace.data_ptr()
+
+    @staticmethod
+    def _vector(t, n: int, what: str) -> int:
+        """Pointer of an optional dense FP32 vector of n elements."""
+        import torch
+        if t is None:
+            return 0
+        if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{what} must be a dense float32 vector of {n} elements")
+        return t.data_ptr()
+
+    @staticmethod
+    def _given(t, desc, what: str) -> int:
+        """Pointer of a tensor whose descriptor was (or was not) set up."""
+        if t is not None and desc is None:
+            raise ValueError(f"{what} was not among the example tensors")
+        return t.data_ptr() if t is not None else 0
+
+    def close(self):
+        for d in self._tensors:
+            B.dlcDestroyTensorDescriptor(d)
+        for d in self._filters:
+            B.dlcDestroyFilterDescriptor(d)
+        self._tensors, self._filters = [], []
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class RmsNormForward(_ChannelOp):
+    """total = x + residual; y = gamma * total / rms(total) through
+    dlcRmsNormForward; an E4M3 y comes with one scale per row."""
+
+    def __init__(self, handle: Handle, x, y, *, residual=None, total=None, eps: float = 1e-6,
+                 axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.eps = float(eps)
+        self.x_desc, self.y_desc = self._act_desc(x), self._act_desc(y)
+        self.r_desc, self.t_desc = self._act_desc(residual), self._act_desc(total)
+        self.channels = B.dlcGetTensor4dDescriptor(self.x_desc)[2]
+        self.rows = x.numel() // self.channels
+
+    def __call__(self, x, gamma, y, residual=None, total=None, scale=None):
+        B.dlcRmsNormForward(self.handle.h, self.eps, self.x_desc, x.data_ptr(), self.r_desc,
+                            self._given(residual, self.r_desc, "residual"),
+                            self._vector(gamma, self.channels, "gamma"), self.t_desc,
+                            self._given(total, self.t_desc, "total"), self.y_desc, y.data_ptr(),
+                            self._vector(scale, self.rows, "scale"))
+        return y
+
+
+class RmsNormBackward(_ChannelOp):
+    """dx (the gradient of x and of the residual) and dgamma of RmsNormForward
+    through dlcRmsNormBackward; dtotal is the gradient that reaches the sum by
+    other ways."""
+
+    def __init__(self, handle: Handle, dy, total, dx, *, dtotal=None, eps: float = 1e-6,
+                 axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.eps = float(eps)
+        self.dy_desc, self.t_desc = self._act_desc(dy), self._act_desc(total)
+        self.dx_desc, self.dt_desc = self._act_desc(dx), self._act_desc(dtotal)
+        self.channels = B.dlcGetTensor4dDescriptor(self.t_desc)[2]
+        self._set_workspace(B.dlcGetRmsNormBackwardWorkspaceSize(handle.h, self.t_desc), total.device)
+
+    def __call__(self, dy, total, gamma, dx, dgamma=None, dtotal=None):
+        B.dlcRmsNormBackward(self.handle.h, self.eps, self.dy_desc, dy.data_ptr(), self.t_desc,
+                             total.data_ptr(), self._vector(gamma, self.channels, "gamma"),
+                             self.dt_desc, self._given(dtotal, self.dt_desc, "dtotal"), self.dx_desc,
+                             dx.data_ptr(), self._vector(dgamma, self.channels, "dgamma"),
+                             self._ws_ptr, self._ws_bytes)
+        return dx
+
+
+class _Product(_ChannelOp):
+    _forward = _workspace = _kernel_of = None
+
+    def __init__(self, handle, x, w, y, act, residual, z, axes):
+        super().__init__(handle, axes)
+        self.act = LINEAR_ACT_MODES[act]
+        self.x_desc, self.w_desc, self.y_desc = self._act_desc(x), self._weight_desc(w), self._act_desc(y)
+        self.r_desc, self.z_desc = self._act_desc(residual), self._act_desc(z)
+        self.filters = w.shape[0]
+        self.rows = x.numel() // (w.numel() // w.shape[0])
+        self._set_workspace(self._workspace(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
+                                            w.data_ptr(), self.y_desc, y.data_ptr()), x.device)
+
+    def kernel(self, x=None, w=None, y=None) -> str:
+        return B.KERNEL_NAMES[self._kernel_of(self.handle.h, self.x_desc, _ptr(x), self.w_desc,
+                                              _ptr(w), self.y_desc, _ptr(y))]
+
+
+class LinearForward(_Product):
+    """y = act(x w^T + bias) + residual through dlcLinearForward, w being
+    [K, C]; E4M3 x and w take one scale per row and per filter.  z, where
+    given, receives the activation's argument for LinearBackward."""
+    _workspace = staticmethod(B.dlcGetLinearForwardWorkspaceSize)
+    _kernel_of = staticmethod(B.dlcGetLinearForwardKernel)
+
+    def __init__(self, handle: Handle, x, w, y, *, act: str = "identity", residual=None, z=None,
+                 axes: str = "NHWC"):
+        super().__init__(handle, x, w, y, act, residual, z, axes)
+
+    def __call__(self, x, w, y, bias=None, residual=None, z=None, x_scale=None, w_scale=None):
+        B.dlcLinearForward(self.handle.h, self.x_desc, x.data_ptr(),
+                           self._vector(x_scale, self.rows, "x_scale"), self.w_desc, w.data_ptr(),
+                           self._vector(w_scale, self.filters, "w_scale"),
+                           self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
+                           self._given(z, self.z_desc, "z"), self.r_desc,
+                           self._given(residual, self.r_desc, "residual"), self.y_desc, y.data_ptr(),
+                           self._ws_ptr, self._ws_bytes)
+        return y
+
+
+class GatedForward(_Product):
+    """y = act(gate) * up through dlcGatedForward: w is [2F, C], F gate filters
+    and then F up filters, z = [gate, up] = x w^T + bias."""
+    _workspace = staticmethod(B.dlcGetGatedForwardWorkspaceSize)
+    _kernel_of = staticmethod(B.dlcGetGatedForwardKernel)
+
+    def __init__(self, handle: Handle, x, w, y, *, act: str = "silu", z=None, axes: str = "NHWC"):
+        super().__init__(handle, x, w, y, act, None, z, axes)
+
+    def __call__(self, x, w, y, bias=None, z=None, x_scale=None, w_scale=None):
+        B.dlcGatedForward(self.handle.h, self.x_desc, x.data_ptr(),
+                          self._vector(x_scale, self.rows, "x_scale"), self.w_desc, w.data_ptr(),
+                          self._vector(w_scale, self.filters, "w_scale"),
+                          self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
+                          self._given(z, self.z_desc, "z"), self.y_desc, y.data_ptr(), self._ws_ptr,
+                          self._ws_bytes)
+        return y
+
+
+class _ProductBackward(_ChannelOp):
+    _backward = _workspace = None
+
+    def __init__(self, handle, x, w, dy, dx, dw, z, act, axes):
+        super().__init__(handle, axes)
+        self.act = LINEAR_ACT_MODES[act]
+        self.x_desc, self.w_desc, self.dy_desc = self._act_desc(x), self._weight_desc(w), self._act_desc(dy)
+        self.dx_desc, self.dw_desc, self.z_desc = self._act_desc(dx), self._weight_desc(dw), self._act_desc(z)
+        self.filters = w.shape[0]
+        self._set_workspace(self._workspace(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
+                                            w.data_ptr(), self.act, self.z_desc, self.dy_desc,
+                                            dy.data_ptr()), x.device)
+
+    def __call__(self, x, w, dy, dx=None, dw=None, dbias=None, z=None):
+        self._backward(self.handle.h, self.x_desc, x.data_ptr(), self.w_desc, w.data_ptr(), self.act,
+                       self.z_desc, self._given(z, self.z_desc, "z"), self.dy_desc, dy.data_ptr(),
+                       self.dx_desc, self._given(dx, self.dx_desc, "dx"), self.dw_desc,
+                       self._given(dw, self.dw_desc, "dw"),
+                       self._vector(dbias, self.filters, "dbias"), self._ws_ptr, self._ws_bytes)
+        return dx, dw, dbias
+
+
+class LinearBackward(_ProductBackward):
+    """dx, dw and dbias of LinearForward through dlcLinearBackward, each where
+    its tensor is given; z is what the forward call wrote (not needed for the
+    identity).  The residual's gradient is dy."""
+    _backward = staticmethod(B.dlcLinearBackward)
+    _workspace = staticmethod(B.dlcGetLinearBackwardWorkspaceSize)
+
+    def __init__(self, handle: Handle, x, w, dy, dx=None, dw=None, *, z=None, act: str = "identity",
+                 axes: str = "NHWC"):
+        super().__init__(handle, x, w, dy, dx, dw, z, act, axes)
+
+
+class GatedBackward(_ProductBackward):
+    """dx, dw and dbias of GatedForward through dlcGatedBackward."""
+    _backward = staticmethod(B.dlcGatedBackward)
+    _workspace = staticmethod(B.dlcGetGatedBackwardWorkspaceSize)
+
+    def __init__(self, handle: Handle, x, w, dy, dx=None, dw=None, *, z=None, act: str = "silu",
+                 axes: str = "NHWC"):
+        super().__init__(handle, x, w, dy, dx, dw, z, act, axes)
 
 
 def output_dim(x, w, *, x_axes="NCHW", w_axes="KCRS", pads=(0, 0, 0, 0), stride=(1, 1),

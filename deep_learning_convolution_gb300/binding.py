@@ -30,6 +30,7 @@ DLC_STATUS_ALLOC_FAILED = 6
 DLC_DATA_FLOAT = 0
 DLC_DATA_BFLOAT16 = 1
 DLC_DATA_DOUBLE = 2
+DLC_DATA_FLOAT8_E4M3 = 3
 DLC_TENSOR_NCHW = 0
 DLC_TENSOR_NHWC = 1
 DLC_MATH_FP32 = 0
@@ -43,6 +44,8 @@ DLC_ACTIVATION_RELU = 1
 DLC_ACTIVATION_SIGMOID = 2
 DLC_ACTIVATION_TANH = 3
 DLC_ACTIVATION_CLIPPED_RELU = 4
+DLC_ACTIVATION_SILU = 5
+DLC_ACTIVATION_GELU = 6
 DLC_POOLING_MAX = 0
 DLC_POOLING_AVERAGE_COUNT_INCLUDE_PADDING = 1
 DLC_POOLING_AVERAGE_COUNT_EXCLUDE_PADDING = 2
@@ -127,6 +130,29 @@ SIGNATURES = {
     "dlcDebugWaitTimeoutSelfTest": [_h, c_int],
     "dlcConvolutionForwardNoAlloc": [c_void_p, _pf, _h, c_void_p, _h, c_void_p, _h, _pf, _h,
                                      c_void_p, c_void_p],
+    "dlcRmsNormForward": [_h, c_double, _h, c_void_p, _h, c_void_p, c_void_p, _h, c_void_p, _h,
+                          c_void_p, c_void_p],
+    "dlcGetRmsNormBackwardWorkspaceSize": [_h, _h, POINTER(c_size_t)],
+    "dlcRmsNormBackward": [_h, c_double, _h, c_void_p, _h, c_void_p, c_void_p, _h, c_void_p, _h,
+                           c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcLinearForward": [_h, _h, c_void_p, c_void_p, _h, c_void_p, c_void_p, c_void_p, c_int, _h,
+                         c_void_p, _h, c_void_p, _h, c_void_p, c_void_p, c_size_t],
+    "dlcGetLinearForwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, _h, c_void_p,
+                                         POINTER(c_size_t)],
+    "dlcGetLinearForwardKernel": [_h, _h, c_void_p, _h, c_void_p, _h, c_void_p, _pi],
+    "dlcLinearBackward": [_h, _h, c_void_p, _h, c_void_p, c_int, _h, c_void_p, _h, c_void_p, _h,
+                          c_void_p, _h, c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcGetLinearBackwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, c_int, _h, _h, c_void_p,
+                                          POINTER(c_size_t)],
+    "dlcGatedForward": [_h, _h, c_void_p, c_void_p, _h, c_void_p, c_void_p, c_void_p, c_int, _h,
+                        c_void_p, _h, c_void_p, c_void_p, c_size_t],
+    "dlcGetGatedForwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, _h, c_void_p,
+                                        POINTER(c_size_t)],
+    "dlcGetGatedForwardKernel": [_h, _h, c_void_p, _h, c_void_p, _h, c_void_p, _pi],
+    "dlcGatedBackward": [_h, _h, c_void_p, _h, c_void_p, c_int, _h, c_void_p, _h, c_void_p, _h,
+                         c_void_p, _h, c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcGetGatedBackwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, c_int, _h, _h, c_void_p,
+                                         POINTER(c_size_t)],
 }
 _RESTYPES = {"dlcGetErrorString": c_char_p}
 
@@ -451,3 +477,86 @@ def dlcActivationForward(handle, mode, coef, alpha, x_desc, x_ptr, beta, y_desc,
     a, b = c_float(alpha), c_float(beta)
     _call("dlcActivationForward", handle, int(mode), c_double(coef), byref(a), x_desc,
           c_void_p(x_ptr), byref(b), y_desc, c_void_p(y_ptr))
+
+
+# ---------------------------------------------------------------------------
+# channel operators: device pointers as integers (0: absent), descriptors of
+# absent tensors None
+# ---------------------------------------------------------------------------
+
+def _bytes(name, *args) -> int:
+    n = c_size_t()
+    _call(name, *args, byref(n))
+    return n.value
+
+
+def _kernel(name, *args) -> int:
+    k = c_int()
+    _call(name, *args, byref(k))
+    return k.value
+
+
+def dlcRmsNormForward(handle, epsilon, xDesc, x, residualDesc, residual, gamma, totalDesc, total,
+                      yDesc, y, scale):
+    _call("dlcRmsNormForward", handle, epsilon, xDesc, x, residualDesc, residual, gamma, totalDesc,
+          total, yDesc, y, scale)
+
+
+def dlcGetRmsNormBackwardWorkspaceSize(handle, totalDesc) -> int:
+    return _bytes("dlcGetRmsNormBackwardWorkspaceSize", handle, totalDesc)
+
+
+def dlcRmsNormBackward(handle, epsilon, dyDesc, dy, totalDesc, total, gamma, dtotalDesc, dtotal,
+                       dxDesc, dx, dgamma, workspace, workspaceBytes):
+    _call("dlcRmsNormBackward", handle, epsilon, dyDesc, dy, totalDesc, total, gamma, dtotalDesc,
+          dtotal, dxDesc, dx, dgamma, workspace, workspaceBytes)
+
+
+def dlcLinearForward(handle, xDesc, x, xScale, wDesc, w, wScale, bias, act, zDesc, z, residualDesc,
+                     residual, yDesc, y, workspace, workspaceBytes):
+    _call("dlcLinearForward", handle, xDesc, x, xScale, wDesc, w, wScale, bias, act, zDesc, z,
+          residualDesc, residual, yDesc, y, workspace, workspaceBytes)
+
+
+def dlcGetLinearForwardWorkspaceSize(handle, xDesc, x, wDesc, w, yDesc, y) -> int:
+    return _bytes("dlcGetLinearForwardWorkspaceSize", handle, xDesc, x, wDesc, w, yDesc, y)
+
+
+def dlcGetLinearForwardKernel(handle, xDesc, x, wDesc, w, yDesc, y) -> int:
+    return _kernel("dlcGetLinearForwardKernel", handle, xDesc, x, wDesc, w, yDesc, y)
+
+
+def dlcLinearBackward(handle, xDesc, x, wDesc, w, act, zDesc, z, dyDesc, dy, dxDesc, dx, dwDesc, dw,
+                      dbias, workspace, workspaceBytes):
+    _call("dlcLinearBackward", handle, xDesc, x, wDesc, w, act, zDesc, z, dyDesc, dy, dxDesc, dx,
+          dwDesc, dw, dbias, workspace, workspaceBytes)
+
+
+def dlcGetLinearBackwardWorkspaceSize(handle, xDesc, x, wDesc, w, act, zDesc, dyDesc, dy) -> int:
+    return _bytes("dlcGetLinearBackwardWorkspaceSize", handle, xDesc, x, wDesc, w, act, zDesc,
+                  dyDesc, dy)
+
+
+def dlcGatedForward(handle, xDesc, x, xScale, wDesc, w, wScale, bias, act, zDesc, z, yDesc, y,
+                    workspace, workspaceBytes):
+    _call("dlcGatedForward", handle, xDesc, x, xScale, wDesc, w, wScale, bias, act, zDesc, z, yDesc,
+          y, workspace, workspaceBytes)
+
+
+def dlcGetGatedForwardWorkspaceSize(handle, xDesc, x, wDesc, w, yDesc, y) -> int:
+    return _bytes("dlcGetGatedForwardWorkspaceSize", handle, xDesc, x, wDesc, w, yDesc, y)
+
+
+def dlcGetGatedForwardKernel(handle, xDesc, x, wDesc, w, yDesc, y) -> int:
+    return _kernel("dlcGetGatedForwardKernel", handle, xDesc, x, wDesc, w, yDesc, y)
+
+
+def dlcGatedBackward(handle, xDesc, x, wDesc, w, act, zDesc, z, dyDesc, dy, dxDesc, dx, dwDesc, dw,
+                     dbias, workspace, workspaceBytes):
+    _call("dlcGatedBackward", handle, xDesc, x, wDesc, w, act, zDesc, z, dyDesc, dy, dxDesc, dx,
+          dwDesc, dw, dbias, workspace, workspaceBytes)
+
+
+def dlcGetGatedBackwardWorkspaceSize(handle, xDesc, x, wDesc, w, act, zDesc, dyDesc, dy) -> int:
+    return _bytes("dlcGetGatedBackwardWorkspaceSize", handle, xDesc, x, wDesc, w, act, zDesc, dyDesc,
+                  dy)

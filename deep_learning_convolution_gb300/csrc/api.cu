@@ -32,7 +32,7 @@ int64_t out_extent(int64_t in, int64_t lo, int64_t hi, int64_t filt, int64_t dil
 size_t elt_size(dlcDataType_t t) { return (size_t)dlc_dtype_bytes(t); }
 
 bool valid_dtype(int t) {
-    return t == DLC_DATA_FLOAT || t == DLC_DATA_BFLOAT16 || t == DLC_DATA_DOUBLE;
+    return t == DLC_DATA_FLOAT || t == DLC_DATA_BFLOAT16 || t == DLC_DATA_DOUBLE || t == DLC_DATA_FLOAT8_E4M3;
 }
 
 // Storage of the two inputs allowed by a math mode.
@@ -47,37 +47,12 @@ bool math_takes(dlcMathType_t m, dlcDataType_t in) {
 }
 
 // Storage of the output allowed for given inputs: DOUBLE with DOUBLE, else
-// FLOAT or BFLOAT16.
+// FLOAT or BFLOAT16 (FLOAT8_E4M3 belongs to the channel operators alone).
 bool out_ok(dlcDataType_t in, dlcDataType_t out) {
+    if (in == DLC_DATA_FLOAT8_E4M3 || out == DLC_DATA_FLOAT8_E4M3) return false;
     return in == DLC_DATA_DOUBLE ? out == DLC_DATA_DOUBLE : out != DLC_DATA_DOUBLE;
 }
 bool valid_format(int f) { return f == DLC_TENSOR_NCHW || f == DLC_TENSOR_NHWC; }
-
-// Largest element offset reachable through (extent, stride) pairs.
-int64_t max_offset(const int64_t *ext, const int64_t *str, int nd) {
-    int64_t m = 0;
-    for (int i = 0; i < nd; ++i) m += (ext[i] - 1) * str[i];
-    return m;
-}
-
-// True if distinct index tuples map to distinct offsets (no self-overlap):
-// sorted by stride, each stride must reach past the span of the smaller ones.
-bool strides_injective(const int64_t *ext, const int64_t *str, int nd) {
-    int idx[4] = {0, 1, 2, 3};
-    std::sort(idx, idx + nd, [&](int a, int b) { return str[a] < str[b]; });
-    int64_t span = 0;  // max offset of the dims seen so far
-    for (int i = 0; i < nd; ++i) {
-        int d = idx[i];
-        if (ext[d] == 1) continue;
-        if (str[d] <= span) return false;
-        span += (ext[d] - 1) * str[d];
-    }
-    return true;
-}
-
-bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) {
-    return a0 < b1 && b0 < a1;
-}
 
 void filter_strides(const dlcFilterStruct *f, int64_t *ws) {
     if (f->format == DLC_TENSOR_NCHW) {  // KCRS
@@ -129,12 +104,12 @@ dlcStatus_t resolve(dlcTensorDescriptor_t xd, const void *x, dlcFilterDescriptor
     pb.w_mn = 0;
 
     const int64_t yext[4] = {pb.N, pb.K, pb.P, pb.Q};
-    if (!strides_injective(yext, pb.ys, 4)) return DLC_STATUS_BAD_PARAM;
+    if (!dlc_strides_injective(yext, pb.ys, 4)) return DLC_STATUS_BAD_PARAM;
     const int64_t xext[4] = {pb.N, pb.C, pb.H, pb.W};
     const int64_t wext[4] = {pb.K, pb.C, pb.R, pb.S};
-    const int64_t xmax = max_offset(xext, pb.xs, 4);
-    const int64_t wmax = max_offset(wext, pb.ws, 4);
-    const int64_t ymax = max_offset(yext, pb.ys, 4);
+    const int64_t xmax = dlc_max_offset(xext, pb.xs, 4);
+    const int64_t wmax = dlc_max_offset(wext, pb.ws, 4);
+    const int64_t ymax = dlc_max_offset(yext, pb.ys, 4);
     const int64_t lim = (int64_t)1 << 60;
     if (xmax >= lim || wmax >= lim || ymax >= lim) return DLC_STATUS_BAD_PARAM;
 
@@ -145,7 +120,7 @@ dlcStatus_t resolve(dlcTensorDescriptor_t xd, const void *x, dlcFilterDescriptor
         uintptr_t x0 = (uintptr_t)x, x1 = x0 + (uintptr_t)(xmax + 1) * ex;
         uintptr_t w0 = (uintptr_t)w, w1 = w0 + (uintptr_t)(wmax + 1) * ex;
         uintptr_t y0 = (uintptr_t)y, y1 = y0 + (uintptr_t)(ymax + 1) * ey;
-        if (ranges_overlap(x0, x1, y0, y1) || ranges_overlap(w0, w1, y0, y1))
+        if (dlc_ranges_overlap(x0, x1, y0, y1) || dlc_ranges_overlap(w0, w1, y0, y1))
             return DLC_STATUS_BAD_PARAM;
     }
     return DLC_STATUS_SUCCESS;
@@ -209,10 +184,10 @@ dlcStatus_t resolve_bwd(dlcTensorDescriptor_t xd, const void *x, dlcFilterDescri
     const int64_t xext[4] = {bp.N, bp.C, bp.H, bp.W};
     const int64_t wext[4] = {bp.K, bp.C, bp.R, bp.S};
     const int64_t yext[4] = {bp.N, bp.K, bp.P, bp.Q};
-    if (out == 0 && !strides_injective(xext, bp.xs, 4)) return DLC_STATUS_BAD_PARAM;
-    const int64_t xmax = max_offset(xext, bp.xs, 4);
-    const int64_t wmax = max_offset(wext, bp.ws, 4);
-    const int64_t ymax = max_offset(yext, bp.dys, 4);
+    if (out == 0 && !dlc_strides_injective(xext, bp.xs, 4)) return DLC_STATUS_BAD_PARAM;
+    const int64_t xmax = dlc_max_offset(xext, bp.xs, 4);
+    const int64_t wmax = dlc_max_offset(wext, bp.ws, 4);
+    const int64_t ymax = dlc_max_offset(yext, bp.dys, 4);
     const int64_t lim = (int64_t)1 << 60;
     if (xmax >= lim || wmax >= lim || ymax >= lim) return DLC_STATUS_BAD_PARAM;
     if (check_ptrs) {
@@ -222,8 +197,8 @@ dlcStatus_t resolve_bwd(dlcTensorDescriptor_t xd, const void *x, dlcFilterDescri
         const uintptr_t x0 = (uintptr_t)x, x1 = x0 + (uintptr_t)(xmax + 1) * ex;
         const uintptr_t w0 = (uintptr_t)w, w1 = w0 + (uintptr_t)(wmax + 1) * ew;
         const uintptr_t y0 = (uintptr_t)dy, y1 = y0 + (uintptr_t)(ymax + 1) * ey;
-        const bool bad = out == 0 ? (ranges_overlap(x0, x1, w0, w1) || ranges_overlap(x0, x1, y0, y1))
-                                  : (ranges_overlap(w0, w1, x0, x1) || ranges_overlap(w0, w1, y0, y1));
+        const bool bad = out == 0 ? (dlc_ranges_overlap(x0, x1, w0, w1) || dlc_ranges_overlap(x0, x1, y0, y1))
+                                  : (dlc_ranges_overlap(w0, w1, x0, x1) || dlc_ranges_overlap(w0, w1, y0, y1));
         if (bad) return DLC_STATUS_BAD_PARAM;
     }
     return DLC_STATUS_SUCCESS;
@@ -904,15 +879,15 @@ dlcStatus_t resolve_pool(dlcPoolingDescriptor_t d, dlcTensorDescriptor_t xd, con
     pp.x = x; pp.y = const_cast<void *>(y);
     pp.alpha = 1.0; pp.beta = 0.0;
     const int64_t xext[4] = {pp.N, pp.C, pp.H, pp.W}, yext[4] = {pp.N, pp.C, pp.P, pp.Q};
-    if (!strides_injective(yext, pp.ys, 4)) return DLC_STATUS_BAD_PARAM;
-    const int64_t xmax = max_offset(xext, pp.xs, 4), ymax = max_offset(yext, pp.ys, 4);
+    if (!dlc_strides_injective(yext, pp.ys, 4)) return DLC_STATUS_BAD_PARAM;
+    const int64_t xmax = dlc_max_offset(xext, pp.xs, 4), ymax = dlc_max_offset(yext, pp.ys, 4);
     if (xmax >= ((int64_t)1 << 60) || ymax >= ((int64_t)1 << 60)) return DLC_STATUS_BAD_PARAM;
     if (check_ptrs) {
         if (!x || !y) return DLC_STATUS_BAD_PARAM;
         const size_t ex = elt_size(pp.xdt), ey = elt_size(pp.ydt);
         if ((uintptr_t)x % ex || (uintptr_t)y % ey) return DLC_STATUS_BAD_PARAM;
         const uintptr_t x0 = (uintptr_t)x, y0 = (uintptr_t)y;
-        if (ranges_overlap(x0, x0 + (uintptr_t)(xmax + 1) * ex, y0, y0 + (uintptr_t)(ymax + 1) * ey))
+        if (dlc_ranges_overlap(x0, x0 + (uintptr_t)(xmax + 1) * ex, y0, y0 + (uintptr_t)(ymax + 1) * ey))
             return DLC_STATUS_BAD_PARAM;
     }
     return DLC_STATUS_SUCCESS;
@@ -968,15 +943,15 @@ dlcStatus_t dlcActivationForward(dlcHandle_t h, dlcActivationMode_t mode, double
         same = same && ap.xs[i] == ap.ys[i];
     }
     const int64_t ext[4] = {ap.N, ap.C, ap.H, ap.W};
-    if (!strides_injective(ext, ap.ys, 4)) return DLC_STATUS_BAD_PARAM;
-    const int64_t xmax = max_offset(ext, ap.xs, 4), ymax = max_offset(ext, ap.ys, 4);
+    if (!dlc_strides_injective(ext, ap.ys, 4)) return DLC_STATUS_BAD_PARAM;
+    const int64_t xmax = dlc_max_offset(ext, ap.xs, 4), ymax = dlc_max_offset(ext, ap.ys, 4);
     if (xmax >= ((int64_t)1 << 60) || ymax >= ((int64_t)1 << 60)) return DLC_STATUS_BAD_PARAM;
     const size_t ex = elt_size(ap.xdt), ey = elt_size(ap.ydt);
     if ((uintptr_t)x % ex || (uintptr_t)y % ey) return DLC_STATUS_BAD_PARAM;
     const bool in_place = x == y && same;
     const uintptr_t x0 = (uintptr_t)x, y0 = (uintptr_t)y;
     if (!in_place &&
-        ranges_overlap(x0, x0 + (uintptr_t)(xmax + 1) * ex, y0, y0 + (uintptr_t)(ymax + 1) * ey))
+        dlc_ranges_overlap(x0, x0 + (uintptr_t)(xmax + 1) * ex, y0, y0 + (uintptr_t)(ymax + 1) * ey))
         return DLC_STATUS_BAD_PARAM;
     ap.x = x; ap.y = y;
     ap.alpha = *alpha; ap.beta = *beta; ap.coef = coef;

@@ -1,0 +1,119 @@
+// channel.cuh -- shared pieces of the channel operators (RMS norm, linear
+// layer, gated projections): tensors seen as rows (pixels or tokens) by
+// channels, activations with their derivatives, and typed loads and stores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "internal.h"
+
+namespace dlc {
+
+// Element offset of row m's channel 0 (channel c is c * cs further).
+__device__ __forceinline__ long long row_off(const RowMap &r, long long m) {
+    if (r.uniform) return m * r.ld;
+    const long long n = m / r.hw;
+    const int rem = (int)(m - n * r.hw);
+    const int h = rem / r.w;
+    return n * r.s0 + h * r.s2 + (long long)(rem - h * r.w) * r.s3;
+}
+
+__device__ __forceinline__ float bf16_bits_f32(uint32_t b) { return __uint_as_float(b << 16); }
+
+// Two FP32 values rounded to nearest even into one word of BF16 (a in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two FP32 values rounded to nearest even into E4M3, saturating at +-448 (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Four E4M3 values of a word.
+__device__ __forceinline__ void unpack_e4m3(uint32_t w, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// One element of a FLOAT, BFLOAT16 or FLOAT8_E4M3 array as FP32, and back.
+__device__ __forceinline__ float load_elem(const void *p, int dt, long long i) {
+    if (dt == DLC_DATA_FLOAT) return static_cast<const float *>(p)[i];
+    if (dt == DLC_DATA_BFLOAT16) return bf16_bits_f32(static_cast<const unsigned short *>(p)[i]);
+    __nv_fp8_e4m3 v;
+    v.__x = static_cast<const unsigned char *>(p)[i];
+    return float(v);
+}
+
+__device__ __forceinline__ void store_elem(void *p, int dt, long long i, float v) {
+    if (dt == DLC_DATA_FLOAT)
+        static_cast<float *>(p)[i] = v;
+    else if (dt == DLC_DATA_BFLOAT16)
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<unsigned char *>(p)[i] = (unsigned char)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// f(v) of the linear and gated epilogues.  The quotients use the fast
+// exponential and division (a few units in the last place of FP32, far below
+// a BF16 rounding); SILU and GELU of -inf are -inf * 0 = NaN, as their formulas say.
+template <int ACT>
+__device__ __forceinline__ float act_f(float v) {
+    if constexpr (ACT == DLC_ACTIVATION_RELU) return v < 0.f ? 0.f : v;  // NaN stays NaN
+    if constexpr (ACT == DLC_ACTIVATION_SIGMOID) return __fdividef(1.f, 1.f + __expf(-v));
+    if constexpr (ACT == DLC_ACTIVATION_TANH) return tanhf(v);
+    if constexpr (ACT == DLC_ACTIVATION_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if constexpr (ACT == DLC_ACTIVATION_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    return v;
+}
+
+// f(v) and f'(v).
+template <int ACT>
+__device__ __forceinline__ void act_both(float v, float &f, float &df) {
+    if constexpr (ACT == DLC_ACTIVATION_RELU) {
+        f = v < 0.f ? 0.f : v;
+        df = v > 0.f ? 1.f : 0.f;
+    } else if constexpr (ACT == DLC_ACTIVATION_SIGMOID) {
+        f = __fdividef(1.f, 1.f + __expf(-v));
+        df = f * (1.f - f);
+    } else if constexpr (ACT == DLC_ACTIVATION_TANH) {
+        f = tanhf(v);
+        df = 1.f - f * f;
+    } else if constexpr (ACT == DLC_ACTIVATION_SILU) {
+        const float p = __fdividef(1.f, 1.f + __expf(-v));
+        f = v * p;
+        df = p * (1.f + v * (1.f - p));
+    } else if constexpr (ACT == DLC_ACTIVATION_GELU) {  // v Phi(v); Phi(v) + v phi(v)
+        const float p = 0.5f * (1.f + erff(v * 0.70710678118654752f));
+        f = v * p;
+        df = p + v * __expf(-0.5f * v * v) * 0.39894228040143268f;
+    } else {
+        f = v;
+        df = 1.f;
+    }
+}
+
+// Calls fn(std::integral_constant<int, ACT>) for a runtime activation.
+template <typename Fn>
+__device__ __forceinline__ void act_dispatch(int act, Fn fn) {
+    switch (act) {
+        case DLC_ACTIVATION_RELU: fn(std::integral_constant<int, DLC_ACTIVATION_RELU>{}); break;
+        case DLC_ACTIVATION_SIGMOID: fn(std::integral_constant<int, DLC_ACTIVATION_SIGMOID>{}); break;
+        case DLC_ACTIVATION_TANH: fn(std::integral_constant<int, DLC_ACTIVATION_TANH>{}); break;
+        case DLC_ACTIVATION_SILU: fn(std::integral_constant<int, DLC_ACTIVATION_SILU>{}); break;
+        case DLC_ACTIVATION_GELU: fn(std::integral_constant<int, DLC_ACTIVATION_GELU>{}); break;
+        default: fn(std::integral_constant<int, DLC_ACTIVATION_IDENTITY>{}); break;
+    }
+}
+
+}  // namespace dlc

@@ -5,7 +5,35 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dlc.h"
+
+// Largest element offset reachable through (extent, stride) pairs.
+inline int64_t dlc_max_offset(const int64_t *ext, const int64_t *str, int nd) {
+    int64_t m = 0;
+    for (int i = 0; i < nd; ++i) m += (ext[i] - 1) * str[i];
+    return m;
+}
+
+// True if distinct index tuples map to distinct offsets (no self-overlap):
+// sorted by stride, each stride must reach past the span of the smaller ones.
+inline bool dlc_strides_injective(const int64_t *ext, const int64_t *str, int nd) {
+    int idx[4] = {0, 1, 2, 3};
+    std::sort(idx, idx + nd, [&](int a, int b) { return str[a] < str[b]; });
+    int64_t span = 0;  // max offset of the dims seen so far
+    for (int i = 0; i < nd; ++i) {
+        int d = idx[i];
+        if (ext[d] == 1) continue;
+        if (str[d] <= span) return false;
+        span += (ext[d] - 1) * str[d];
+    }
+    return true;
+}
+
+inline bool dlc_ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) {
+    return a0 < b1 && b0 < a1;
+}
 
 struct dlcTensorStruct {
     int set = 0;
@@ -73,7 +101,7 @@ struct dlcContext {
 #define DLC_HANDLE_WPACK_BYTES (2 * 1024 * 1024)
 
 inline int dlc_dtype_bytes(dlcDataType_t t) {
-    return t == DLC_DATA_BFLOAT16 ? 2 : (t == DLC_DATA_DOUBLE ? 8 : 4);
+    return t == DLC_DATA_BFLOAT16 ? 2 : (t == DLC_DATA_DOUBLE ? 8 : (t == DLC_DATA_FLOAT8_E4M3 ? 1 : 4));
 }
 
 // A fully resolved forward problem (validated by the API layer).
@@ -188,3 +216,88 @@ dlcStatus_t dlc_preload_rowstack();
 bool dlc_rowstack_ok(const dlcContext *ctx, const ConvProblem &pb);
 dlcStatus_t dlc_launch_rowstack(dlcContext *ctx, const ConvProblem &pb);
 
+
+// ---- channel operators (channel_api.cu, rmsnorm.cu, gemm.cu) -------------------
+//
+// A tensor as rows (pixels n, h, w in order) by channels.
+struct RowMap {
+    long long s0, s2, s3, cs;  // strides of n, h, w and of the channel (elements)
+    long long ld;              // the rows' pitch when it is one number (uniform)
+    int hw, w;                 // h * w and w
+    int uniform;
+};
+
+// One tensor of a channel operator (p null: absent).
+struct RowTensor {
+    void *p = nullptr;
+    int dt = DLC_DATA_FLOAT;
+    RowMap m = {0, 0, 0, 1, 0, 1, 1, 1};
+};
+
+// RMS norm, forward and backward (validated by the API layer).
+struct RmsProblem {
+    long long rows;
+    int C;
+    float eps;
+    RowTensor x, r, t, y;  // input, residual (or absent), their sum (or absent), output
+    const float *gamma;
+    float *scale;          // one per row when y is E4M3
+};
+
+struct RmsBwdProblem {
+    long long rows;
+    int C;
+    float eps;
+    RowTensor dy, t, dt, dx;  // dt: gradient arriving at the sum, or absent
+    const float *gamma;
+    float *dgamma;            // or null
+    float *ws;                // per-block partial sums of dgamma
+};
+
+// An operand of a product: element (i, k) is row i, channel k of the tensor, or
+// row k, channel i where `trans` is set.
+struct GemmOperand {
+    RowTensor t;
+    int trans = 0;
+};
+
+// y[m, n] = act(sa[m] sb[n] sum_k a(m, k) b(n, k) + bias[n]) + r[m, n], and
+// z[m, n] the activation's argument; gated: b, sb, bias and z hold 2N entries
+// (gate n, then up N + n) and y[m, n] = act(gate) * up.
+struct GemmProblem {
+    long long M = 0, K = 0;
+    int N = 0, gated = 0, act = DLC_ACTIVATION_IDENTITY;
+    GemmOperand a, b;
+    const float *sa = nullptr, *sb = nullptr, *bias = nullptr;
+    RowTensor z, r, y;
+    char *ws = nullptr;  // dlc_gemm_workspace bytes
+};
+
+// dz = dy * act'(z), or both halves of a gated row: dz = [dy up act'(gate), dy act(gate)];
+// dbias = the sum of dz over the rows.
+struct ActGradProblem {
+    long long rows = 0;
+    int N = 0, gated = 0, act = DLC_ACTIVATION_IDENTITY;
+    RowTensor dy, z, dz;  // z absent for the identity; dz absent: only dbias
+    float *dbias = nullptr;
+    float *ws = nullptr;  // partial sums of dbias (dlc_act_grad_workspace bytes)
+};
+
+// gemm.cu
+dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g);
+size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g);
+dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g);
+// act_grad.cu
+size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p);
+dlcStatus_t dlc_launch_act_grad(dlcContext *ctx, const ActGradProblem &p);
+// out[c] = sum_b ws[b * C + c] in a fixed order (rmsnorm.cu)
+dlcStatus_t dlc_launch_column_sum(dlcContext *ctx, const float *ws, float *out, int C, int blocks);
+// rmsnorm.cu
+dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &p);
+size_t dlc_rms_bwd_workspace(const dlcContext *ctx, const RmsBwdProblem &p);
+dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &p);
+
+// One launch on the context's stream that may overlap the tail of the kernel
+// before it (see dlc_pdl_enabled); counts it.  Defined in channel_api.cu.
+dlcStatus_t dlc_launch(dlcContext *ctx, const void *kernel, dim3 grid, dim3 block, size_t smem, void **args,
+                       int cluster = 1);

@@ -1,6 +1,7 @@
 /*
  * dlc.h -- C ABI of the GB300 (sm_103a) 2-D convolution library: the forward
- * convolution, its two backward routines, pooling and activation forward.
+ * convolution, its two backward routines, pooling and activation forward, and
+ * the channel operators (RMS norm, linear and gated layers) with their gradients.
  *
  * The forward (FPROP) convolution layer is
  *
@@ -71,11 +72,15 @@ typedef enum {
 } dlcStatus_t;
 
 /* Storage type of x, w and y.  x and w must share it; y may be FLOAT or
- * BFLOAT16 independently (DOUBLE with DOUBLE inputs).  Bias is always FLOAT. */
+ * BFLOAT16 independently (DOUBLE with DOUBLE inputs).  Bias is always FLOAT.
+ * FLOAT8_E4M3 (8 bits: 4 of exponent, 3 of mantissa, largest value 448) is for
+ * the channel operators; the convolution, pooling and activation calls return
+ * NOT_SUPPORTED for it. */
 typedef enum {
     DLC_DATA_FLOAT = 0,
     DLC_DATA_BFLOAT16 = 1,
-    DLC_DATA_DOUBLE = 2
+    DLC_DATA_DOUBLE = 2,
+    DLC_DATA_FLOAT8_E4M3 = 3
 } dlcDataType_t;
 
 /* Layouts.  For activations NCHW / NHWC; for filters NCHW means KCRS and NHWC
@@ -108,13 +113,18 @@ typedef enum {
 
 /* Activation functions (cuDNN page, summary and method section).  The fused
  * convolution epilogue takes IDENTITY and RELU; dlcActivationForward takes
- * every mode: f(x) = x, max(0, x), 1 / (1 + e^-x), tanh x, min(max(0, x), coef). */
+ * the first five modes: f(x) = x, max(0, x), 1 / (1 + e^-x), tanh x,
+ * min(max(0, x), coef).  The linear and gated layers take all but
+ * CLIPPED_RELU, among them SILU, x / (1 + e^-x), and GELU, x Phi(x) with the
+ * standard normal distribution function Phi. */
 typedef enum {
     DLC_ACTIVATION_IDENTITY = 0,
     DLC_ACTIVATION_RELU = 1,
     DLC_ACTIVATION_SIGMOID = 2,
     DLC_ACTIVATION_TANH = 3,
-    DLC_ACTIVATION_CLIPPED_RELU = 4
+    DLC_ACTIVATION_CLIPPED_RELU = 4,
+    DLC_ACTIVATION_SILU = 5,
+    DLC_ACTIVATION_GELU = 6
 } dlcActivationMode_t;
 
 /* Pooling (cuDNN page, summary and method section): the largest value of the
@@ -491,6 +501,149 @@ dlcStatus_t dlcGetPoolingForwardKernel(dlcHandle_t handle, dlcPoolingDescriptor_
 dlcStatus_t dlcActivationForward(dlcHandle_t handle, dlcActivationMode_t mode, double coef,
                                  const float *alpha, dlcTensorDescriptor_t xDesc, const void *x,
                                  const float *beta, dlcTensorDescriptor_t yDesc, void *y);
+
+/* ---- channel operators -------------------------------------------------------
+ *
+ * What a network does with the channels of each pixel (or token) between
+ * convolutions: RMS norm with the residual's addition, linear layers (products
+ * over the channels) and gated projections, with their gradients.  No
+ * counterpart on the pages.
+ *
+ * A tensor [n, c, h, w] is read as rows (n, h, w) of c channels; a matrix of
+ * rows x channels is [rows, channels, 1, 1].  Any strides and alignment are
+ * taken; channels contiguous, rows at one pitch and 16-byte aligned are the
+ * fast layout.  Filters are [K, C, 1, 1], K rows of C channels.  Sums,
+ * statistics and activations run in FP32; BFLOAT16 and FLOAT8_E4M3 results are
+ * rounded once, to nearest even.  An FP8 row or filter stands for its values
+ * times its FLOAT scale.
+ *
+ * Pointers are device pointers; those marked optional may be NULL, and their
+ * descriptor is then ignored.  Outputs must not overlap other arguments
+ * (BAD_PARAM; the address ranges that strides reach count) but for the in-place
+ * uses named at each call.  A workspace is caller-owned, 256-byte aligned and
+ * of at least the queried size (else BAD_PARAM; NULL where that is 0); its
+ * contents need not be kept between calls.  The queries take pointers, which
+ * may be NULL (alignment then taken as satisfied): an operand the kernels
+ * cannot load in place is copied into the workspace first.  All calls are
+ * bitwise reproducible, can be captured in a CUDA graph, allocate nothing and
+ * are asynchronous on the handle's stream.
+ */
+
+/* total = x + residual;  y = gamma * total / sqrt(mean over channels of
+ * total^2 + epsilon), from the unrounded total.  x, residual (optional), total
+ * (optional output): FLOAT or BFLOAT16 independently; gamma: FLOAT, one per
+ * channel.  y: FLOAT, BFLOAT16, or FLOAT8_E4M3 with scale[row] = max over
+ * channels of |y| / 448 (FLOAT, one per row in order n, h, w; required then and
+ * NULL otherwise; max |y| counts as at least 1e-30, so a row of zeros gives
+ * zeros).  NaN or infinity in a row makes that row NaN or zero, no other.
+ * total may be x or residual in place (same descriptor values).  epsilon >= 0. */
+dlcStatus_t dlcRmsNormForward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t xDesc,
+                              const void *x, dlcTensorDescriptor_t residualDesc,
+                              const void *residual, const float *gamma,
+                              dlcTensorDescriptor_t totalDesc, void *total,
+                              dlcTensorDescriptor_t yDesc, void *y, float *scale);
+
+/* Workspace of dlcRmsNormBackward when dgamma is wanted (0 bytes otherwise). */
+dlcStatus_t dlcGetRmsNormBackwardWorkspaceSize(dlcHandle_t handle,
+                                               dlcTensorDescriptor_t totalDesc, size_t *bytes);
+
+/* Gradient of the norm at total, which is also that of x and of residual:
+ *   dx = dtotal + rho * dy * gamma - total * rho^3 * mean(dy * gamma * total)
+ *   dgamma = sum over rows of dy * total * rho,  rho = 1 / sqrt(mean(total^2) + epsilon)
+ * dtotal (optional): the gradient that reaches total by other ways (the residual
+ * stream); dx may be dtotal in place.  dgamma (FLOAT) is optional.  Tensors
+ * FLOAT or BFLOAT16 independently. */
+dlcStatus_t dlcRmsNormBackward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t dyDesc,
+                               const void *dy, dlcTensorDescriptor_t totalDesc, const void *total,
+                               const float *gamma, dlcTensorDescriptor_t dtotalDesc,
+                               const void *dtotal, dlcTensorDescriptor_t dxDesc, void *dx,
+                               float *dgamma, void *workspace, size_t workspaceBytes);
+
+/* Linear layer: z[m, k] = xScale[m] * wScale[k] * sum_c x[m, c] * w[k, c] + bias[k],
+ * y = act(z) + residual.
+ * x and w: both BFLOAT16 (xScale and wScale NULL), or both FLOAT8_E4M3 with
+ * FLOAT scales, one per row and one per filter.  bias (FLOAT), z and residual
+ * are optional; z (an output, what the backward pass reads), residual and y are
+ * FLOAT or BFLOAT16 independently.  residual may be y in place (same descriptor
+ * values).  act: any but CLIPPED_RELU (NOT_SUPPORTED). */
+dlcStatus_t dlcLinearForward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                             const float *xScale, dlcFilterDescriptor_t wDesc, const void *w,
+                             const float *wScale, const float *bias, dlcActivationMode_t act,
+                             dlcTensorDescriptor_t zDesc, void *z,
+                             dlcTensorDescriptor_t residualDesc, const void *residual,
+                             dlcTensorDescriptor_t yDesc, void *y, void *workspace,
+                             size_t workspaceBytes);
+
+dlcStatus_t dlcGetLinearForwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                             const void *x, dlcFilterDescriptor_t wDesc,
+                                             const void *w, dlcTensorDescriptor_t yDesc,
+                                             const void *y, size_t *bytes);
+
+/* Kernel that multiplies in dlcLinearForward (diagnostic; pointers may be NULL). */
+dlcStatus_t dlcGetLinearForwardKernel(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                      const void *x, dlcFilterDescriptor_t wDesc, const void *w,
+                                      dlcTensorDescriptor_t yDesc, const void *y,
+                                      dlcKernel_t *kernel);
+
+/* Gradients of the linear layer; that of residual is dy itself.
+ *   dz = dy * act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz
+ * dz enters the products rounded to BFLOAT16; dbias sums its FP32 values.  x and
+ * w: BFLOAT16; dy, dx, dw and z: FLOAT or BFLOAT16 independently; dbias: FLOAT.
+ * dx, dw and dbias are each optional, one at least is wanted.  z is what the
+ * forward call wrote, not read for IDENTITY (may be NULL then). */
+dlcStatus_t dlcLinearBackward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                              dlcFilterDescriptor_t wDesc, const void *w, dlcActivationMode_t act,
+                              dlcTensorDescriptor_t zDesc, const void *z,
+                              dlcTensorDescriptor_t dyDesc, const void *dy,
+                              dlcTensorDescriptor_t dxDesc, void *dx, dlcFilterDescriptor_t dwDesc,
+                              void *dw, float *dbias, void *workspace, size_t workspaceBytes);
+
+/* Workspace for any subset of the three gradients. */
+dlcStatus_t dlcGetLinearBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                              const void *x, dlcFilterDescriptor_t wDesc,
+                                              const void *w, dlcActivationMode_t act,
+                                              dlcTensorDescriptor_t zDesc,
+                                              dlcTensorDescriptor_t dyDesc, const void *dy,
+                                              size_t *bytes);
+
+/* Gated projections: w holds 2F filters, F gates and then F ups, and so do
+ * bias, wScale and z;  with z as in the linear layer,
+ *   y[m, f] = act(z[m, f]) * z[m, F + f].
+ * Types, optional arguments and activations as for dlcLinearForward. */
+dlcStatus_t dlcGatedForward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                            const float *xScale, dlcFilterDescriptor_t wDesc, const void *w,
+                            const float *wScale, const float *bias, dlcActivationMode_t act,
+                            dlcTensorDescriptor_t zDesc, void *z, dlcTensorDescriptor_t yDesc,
+                            void *y, void *workspace, size_t workspaceBytes);
+
+dlcStatus_t dlcGetGatedForwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                            const void *x, dlcFilterDescriptor_t wDesc,
+                                            const void *w, dlcTensorDescriptor_t yDesc,
+                                            const void *y, size_t *bytes);
+
+/* Kernel that multiplies in dlcGatedForward (diagnostic; pointers may be NULL). */
+dlcStatus_t dlcGetGatedForwardKernel(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                                     dlcFilterDescriptor_t wDesc, const void *w,
+                                     dlcTensorDescriptor_t yDesc, const void *y,
+                                     dlcKernel_t *kernel);
+
+/* Gradients of the gated projections (z is required):
+ *   dz = [dy * up * act'(gate), dy * act(gate)];  dx = dz w;  dw = dz^T x;
+ *   dbias = sum over rows of dz
+ * with types and optional arguments as for dlcLinearBackward. */
+dlcStatus_t dlcGatedBackward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                             dlcFilterDescriptor_t wDesc, const void *w, dlcActivationMode_t act,
+                             dlcTensorDescriptor_t zDesc, const void *z,
+                             dlcTensorDescriptor_t dyDesc, const void *dy,
+                             dlcTensorDescriptor_t dxDesc, void *dx, dlcFilterDescriptor_t dwDesc,
+                             void *dw, float *dbias, void *workspace, size_t workspaceBytes);
+
+dlcStatus_t dlcGetGatedBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                             const void *x, dlcFilterDescriptor_t wDesc,
+                                             const void *w, dlcActivationMode_t act,
+                                             dlcTensorDescriptor_t zDesc,
+                                             dlcTensorDescriptor_t dyDesc, const void *dy,
+                                             size_t *bytes);
 
 /* ---- self test of the device error path ---------------------------------- */
 
