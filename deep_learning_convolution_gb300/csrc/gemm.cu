@@ -1,4 +1,32 @@
-// gemm.cu -- the products of the linear and gated layers.
+// gemm.cu -- the products of the linear and gated layers on pairs of SMs.
+//
+//   y[m, n] = act(sa[m] sb[n] sum_k a(m, k) b(n, k) + bias[n]) + r[m, n]
+//   gated: y[m, n] = act(gate) * up, gate and up from rows n and N + n of b
+//
+// tcgen05.mma with cta_group::2: a cluster of two CTAs owns a tile of 256 rows
+// and BN columns; each CTA brings its own 128 rows of a and half of the BN
+// rows of b by TMA, and one MMA of M = 256, N = BN reads both CTAs' shared
+// memory.  In the gated form the leader's half of b holds the gate's filters
+// and the other CTA's the up filters of the same BN / 2 outputs, so gate and
+// up of an output meet in one thread's accumulator row (columns j and
+// BN / 2 + j) and neither projection touches memory before their product.
+//
+// The backward products read operands along their other axis (dx: w by
+// channels; dw: both by rows): BF16 blocks of 64 x 64 with the output index
+// contiguous, the tensor core's MN-major form, so nothing is transposed in
+// memory.
+//
+// Few tiles leave most pairs idle: the reduction is then split into ranges
+// whose FP32 partial tiles go to the workspace, and a second kernel adds them
+// in a fixed order and applies the epilogue.
+//
+// Roles (11 warps a CTA): warp 0 lane 0 loads a, warp 2 lane 0 loads b, warp 1
+// lane 0 of the leader issues the MMAs into one of two TMEM accumulators,
+// warps 3-10 (two per quarter of the TMEM lanes, alternate 32-column chunks)
+// run the epilogue of the other one.  Every wait is bounded.
+#include <atomic>
+#include <cstring>
+
 #include "channel.cuh"
 #include "ptx.cuh"
 
@@ -6,77 +34,815 @@ namespace {
 
 using namespace dlc;
 
-constexpr int DT = 64, DK = 16;  // tile of 64 x 64 outputs, 16 of the reduction at a time
+constexpr int GP_ROWS = 128;                    // rows of a per CTA
+constexpr int GP_LINE = 128;                    // bytes of a stage's operand rows (one swizzle span)
+constexpr int GP_A_BYTES = GP_ROWS * GP_LINE;   // 16 KiB
+constexpr int GP_ATOM = 64 * GP_LINE;           // MN-major: 64 indices x 64 of the reduction
+constexpr int GP_EPI_WARP0 = 3, GP_EPI_WARPS = 8;
+constexpr int GP_THREADS = (GP_EPI_WARP0 + GP_EPI_WARPS) * 32;
+constexpr int GP_MAX_SMEM = 232448, GP_BAR_AREA = 256, GP_MAX_STAGES = 8;
 
-__device__ __forceinline__ float operand(const GemmOperand &o, long long i, long long k) {
-    return o.trans ? load_elem(o.t.p, o.t.dt, row_off(o.t.m, k) + i * o.t.m.cs)
-                   : load_elem(o.t.p, o.t.dt, row_off(o.t.m, i) + k * o.t.m.cs);
+struct GpParams {
+    long long M;
+    int N, act;
+    int BN, nout;                 // accumulator columns of a tile, outputs of a tile (gated: BN / 2)
+    int stages, num_kb;
+    int m_tiles, n_tiles, tiles, splits, units;
+    int raw;                      // FP32 partial tiles to the workspace (splits > 1), no epilogue
+    uint32_t b_stage;             // bytes of one CTA's half of b per stage
+    int b_atoms;                  // MN-major b: 64-index blocks per CTA
+    uint32_t idesc, tmem_cols, acc_stride;
+    uint32_t epi_buf;             // bytes of one epilogue staging buffer
+    const float *sa, *sb, *bias;
+    RowTensor z, r, y;
+    int y_tma, z_tma, r_vec;
+    int *err;
+    unsigned long long timeout_ns;
+};
+
+struct GpUnit {
+    long long m0;
+    int nt, split, kb0, kb1;
+};
+
+// Unit u: a tile (tiles in groups of eight row blocks, so that the pairs that
+// run together share rows of both operands in the L2) and a range of k-blocks.
+__device__ __forceinline__ GpUnit gp_unit(const GpParams &p, int u) {
+    GpUnit w;
+    const int t = u / p.splits;
+    w.split = u - t * p.splits;
+    const int per = 8 * p.n_tiles, grp = t / per, in = t - grp * per;
+    const int rows = min(8, p.m_tiles - grp * 8);
+    w.nt = in / rows;
+    w.m0 = (long long)(grp * 8 + in - w.nt * rows) * (2 * GP_ROWS);
+    w.kb0 = (int)((long long)p.num_kb * w.split / p.splits);
+    w.kb1 = (int)((long long)p.num_kb * (w.split + 1) / p.splits);
+    return w;
 }
 
-// Any types, strides and sizes: FP32 products and sums on the CUDA cores, a
-// thread holding 4 x 4 outputs (and as many up projections).
-template <bool GATED>
-__global__ void __launch_bounds__(256) gemm_direct_kernel(const __grid_constant__ GemmProblem g) {
-    griddep_launch_dependents();
-    __shared__ float sa[DK][DT + 1], sb[GATED ? 2 : 1][DK][DT + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long m0 = (long long)blockIdx.x * DT;
-    const int n0 = (int)blockIdx.y * DT;
-    griddep_wait();
-    float acc[GATED ? 2 : 1][4][4] = {};
-    for (long long k0 = 0; k0 < g.K; k0 += DK) {
-        for (int i = threadIdx.x; i < DT * DK; i += 256) {
-            const int r = i / DK, k = i % DK;
-            const bool kin = k0 + k < g.K;
-            sa[k][r] = kin && m0 + r < g.M ? operand(g.a, m0 + r, k0 + k) : 0.f;
-            sb[0][k][r] = kin && n0 + r < g.N ? operand(g.b, n0 + r, k0 + k) : 0.f;
-            if (GATED) sb[1][k][r] = kin && n0 + r < g.N ? operand(g.b, (long long)g.N + n0 + r, k0 + k) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < DK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[0][i][j] = fmaf(sa[k][ty * 4 + i], sb[0][k][tx * 4 + j], acc[0][i][j]);
-                    if (GATED) acc[GATED][i][j] = fmaf(sa[k][ty * 4 + i], sb[GATED][k][tx * 4 + j], acc[GATED][i][j]);
-                }
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i) {
-        const long long m = m0 + ty * 4 + i;
-        if (m >= g.M) break;
-        const float s = g.sa ? g.sa[m] : 1.f;
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tx * 4 + j;
-            if (n >= g.N) break;
-            float v = acc[0][i][j] * s * (g.sb ? g.sb[n] : 1.f) + (g.bias ? g.bias[n] : 0.f);
-            const long long zo = g.z.p ? row_off(g.z.m, m) : 0;
-            if (g.z.p) store_elem(g.z.p, g.z.dt, zo + n * g.z.m.cs, v);
-            float u = 1.f;
-            if (GATED) {
-                const int n2 = g.N + n;
-                u = acc[GATED][i][j] * s * (g.sb ? g.sb[n2] : 1.f) + (g.bias ? g.bias[n2] : 0.f);
-                if (g.z.p) store_elem(g.z.p, g.z.dt, zo + n2 * g.z.m.cs, u);
+// One operand's loads: A's 128 rows of this CTA, or its half of B.
+template <bool IS_A, bool MN, bool GATED, int BK>
+__device__ void gp_produce(const GpParams &p, uint32_t rank, const CUtensorMap *tm, uint32_t smem, uint64_t *full,
+                           uint64_t *empty, const WaitCtl &ctl) {
+    const uint32_t bytes = IS_A ? (uint32_t)GP_A_BYTES : p.b_stage;
+    const uint32_t tx = 2u * (GP_A_BYTES + p.b_stage);  // both CTAs' bytes land on the leader's barrier
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    int stage = 0;
+    uint32_t ph = 0;
+    for (int u = (int)cluster_id_x(); u < p.units; u += (int)num_clusters_x()) {
+        const GpUnit w = gp_unit(p, u);
+        int i0;  // first index of this CTA's rows (or of its 64-index blocks)
+        if (IS_A)
+            i0 = (int)w.m0 + (int)rank * GP_ROWS;
+        else if (GATED)
+            i0 = w.nt * p.nout + (int)rank * p.N;
+        else
+            i0 = w.nt * p.BN + (int)rank * (p.BN / 2);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+            if (!mbar_wait(&empty[stage], ph ^ 1u, ctl, 21)) return;
+            if (IS_A && rank == 0) mbar_arrive_expect_tx(&full[stage], tx);
+            const uint32_t dst = smem + (uint32_t)stage * bytes, bar = full0 + 8u * (uint32_t)stage;
+            if (MN) {
+                const int atoms = IS_A ? 2 : p.b_atoms;
+                for (int a = 0; a < atoms; ++a) tma_load_2d_pair(dst + (uint32_t)a * GP_ATOM, tm, bar, i0 + 64 * a, kb * BK);
+            } else {
+                tma_load_2d_pair(dst, tm, bar, kb * BK, i0);
             }
-            act_dispatch(g.act, [&](auto act) { v = act_f<decltype(act)::value>(v); });
-            if (GATED) v *= u;
-            if (g.r.p) v += load_elem(g.r.p, g.r.dt, row_off(g.r.m, m) + n * g.r.m.cs);
-            store_elem(g.y.p, g.y.dt, row_off(g.y.m, m) + n * g.y.m.cs, v);
+            if (++stage == p.stages) stage = 0, ph ^= 1u;
         }
     }
+}
+
+template <bool E4M3, bool A_MN, bool B_MN>
+__device__ void gp_mma(const GpParams &p, uint32_t tmem_base, uint32_t sA, uint32_t sB, uint64_t *full,
+                       uint64_t *empty, uint64_t *tfull, uint64_t *tempty, uint64_t *mma_done, const WaitCtl &ctl) {
+    // K-major rows advance 32 bytes per MMA; MN-major blocks 16 rows of 128 bytes
+    const uint64_t a0 = A_MN ? sw128_mnmajor_desc(sA, GP_ATOM) : sw128_kmajor_desc(sA);
+    const uint64_t b0 = B_MN ? sw128_mnmajor_desc(sB, GP_ATOM) : sw128_kmajor_desc(sB);
+    constexpr uint64_t a_k = A_MN ? 16 * GP_LINE / 16 : 2, b_k = B_MN ? 16 * GP_LINE / 16 : 2;
+    const uint64_t a_step = GP_A_BYTES >> 4, b_step = p.b_stage >> 4;
+    int stage = 0, it = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = (int)cluster_id_x(); ok && u < p.units; u += (int)num_clusters_x(), ++it) {
+        const GpUnit w = gp_unit(p, u);
+        const int buf = it & 1;
+        if (!mbar_wait_cluster(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, ctl, 23)) {  // both CTAs' epilogues
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem_base + (uint32_t)buf * p.acc_stride;
+        uint32_t acc = 0;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+            if (!mbar_wait(&full[stage], ph, ctl, 24)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint64_t ad = a0 + a_step * (uint32_t)stage, bd = b0 + b_step * (uint32_t)stage;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (E4M3)
+                    umma_e4m3_pair(d, ad + a_k * j, bd + b_k * j, p.idesc, acc);
+                else
+                    umma_bf16_pair(d, ad + a_k * j, bd + b_k * j, p.idesc, acc);
+                acc = 1;
+            }
+            umma_commit_pair(&empty[stage], 3);  // both CTAs' slots free once these are done
+            if (++stage == p.stages) stage = 0, ph ^= 1u;
+        }
+        if (!ok) break;
+        umma_commit_pair(&tfull[buf], 3);  // both CTAs' accumulator rows are ready
+    }
+    if (!ok) {
+        // gave up: loads issued for stages not consumed land on these barriers;
+        // wait for them briefly so that no copy outlives the CTAs
+        volatile int dummy = 0;
+        const WaitCtl brief{&dummy, p.err, 50000000ull};
+        for (int j = 0; j < p.stages; ++j) {
+            if (!mbar_wait(&full[stage], ph, brief, 94)) break;
+            if (++stage == p.stages) stage = 0, ph ^= 1u;
+        }
+    }
+    umma_commit_pair(mma_done, 3);  // every MMA issued completes before tensor memory is released
+}
+
+// ---- epilogue --------------------------------------------------------------------
+
+// sa[m] sb[n] acc + bias[n], columns n .. n+31 of a row (sb and bias start at
+// the column's own filter; columns past `cols` are not read).
+__device__ __forceinline__ void gp_scale_bias(float (&v)[32], float sa, const float *sb, const float *bias, int cols) {
+    if (sb) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= sa * (i < cols ? __ldg(sb + i) : 0.f);
+    }
+    if (bias) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += i < cols ? __ldg(bias + i) : 0.f;
+    }
+}
+
+// One warp's stores of 32 x 32 blocks: staged in shared memory, swizzled as the
+// tensor map expects, then one bulk tensor store; or, for layouts that TMA
+// cannot write, row by row with a lane per column.
+struct GpStore {
+    uint32_t bufs, buf_bytes;
+    int nbuf, lane;
+    long long row0;      // first row of the warp
+    long long M;
+
+    __device__ __forceinline__ uint32_t next() {
+        const uint32_t sb = bufs + (uint32_t)(nbuf & 1) * buf_bytes;
+        if (nbuf >= 2) {  // the store issued from this buffer two groups ago
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+        }
+        ++nbuf;
+        return sb;
+    }
+
+    __device__ __forceinline__ void stage_f32(uint32_t sb, const float (&v)[32]) const {
+        const uint32_t rowp = sb + (uint32_t)lane * 128u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + (((uint32_t)j ^ (lane & 7)) << 4)),
+                         "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                         : "memory");
+    }
+
+    __device__ __forceinline__ void tma(const CUtensorMap *tm, bool bf16, const float (&v)[32], int col, int plane) {
+        if (row0 >= M) return;
+        const uint32_t sb = next();
+        if (bf16) {  // rows of 64 bytes, 64-byte swizzle
+            const uint32_t rowp = sb + (uint32_t)lane * 64u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 rowp + (((uint32_t)j ^ ((uint32_t)(lane >> 1) & 3u)) << 4)),
+                             "r"(pack_bf16(v[8 * j], v[8 * j + 1])), "r"(pack_bf16(v[8 * j + 2], v[8 * j + 3])),
+                             "r"(pack_bf16(v[8 * j + 4], v[8 * j + 5])), "r"(pack_bf16(v[8 * j + 6], v[8 * j + 7]))
+                             : "memory");
+        } else {
+            stage_f32(sb, v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // rows past M and columns past N are not written
+            tma_store_3d_s(tm, sb, col, (int)row0, plane);
+            bulk_commit_group();
+        }
+    }
+
+    // `off`: this lane's row offset in t; `col`: column in t of v[0]; `cols` of them exist
+    __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols) {
+        if (row0 >= M) return;
+        const uint32_t sb = next();
+        stage_f32(sb, v);
+        __syncwarp();
+        const int n = (int)min(32LL, M - row0);
+        for (int r = 0; r < n; ++r) {
+            const long long ro = __shfl_sync(0xffffffffu, off, r);
+            float f;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(sb + (uint32_t)r * 128u +
+                         ((((uint32_t)lane >> 2) ^ ((uint32_t)r & 7u)) << 4) + ((uint32_t)lane & 3u) * 4u) : "memory");
+            if (lane < cols) store_elem(t.p, t.dt, ro + (col + lane) * t.m.cs, f);
+        }
+        __syncwarp();
+        if (lane == 0) bulk_commit_group();  // an empty group keeps the buffers' turn
+    }
+};
+
+__device__ __forceinline__ void gp_add_residual(const GpParams &p, float (&v)[32], long long off, int n, int cols) {
+    if (p.r_vec && cols >= 32) {
+        if (p.r.dt == DLC_DATA_BFLOAT16) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.r.p) + off + n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 w = q[j];
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[8 * j + 2 * i] += __uint_as_float(u[i] << 16);
+                    v[8 * j + 2 * i + 1] += __uint_as_float(u[i] & 0xffff0000u);
+                }
+            }
+        } else {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.r.p) + off + n);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 w = q[j];
+                v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < cols) v[i] += load_elem(p.r.p, p.r.dt, off + (long long)(n + i) * p.r.m.cs);
+    }
+}
+
+template <bool GATED>
+__device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
+                            uint32_t epi_smem, const CUtensorMap *tmY, const CUtensorMap *tmZ, const WaitCtl &ctl) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3;                      // TMEM lanes 32*quad .. 32*quad+31
+    const int part = (warp - GP_EPI_WARP0) >> 2;    // even or odd 32-column chunks
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    GpStore st;
+    st.bufs = epi_smem + (uint32_t)(warp - GP_EPI_WARP0) * 2u * p.epi_buf;
+    st.buf_bytes = p.epi_buf;
+    st.nbuf = 0;
+    st.lane = lane;
+    st.M = p.M;
+    int it = 0;
+    for (int u = (int)cluster_id_x(); u < p.units; u += (int)num_clusters_x(), ++it) {
+        const GpUnit w = gp_unit(p, u);
+        const int buf = it & 1;
+        const long long m = w.m0 + (long long)rank * GP_ROWS + quad * 32 + lane;
+        st.row0 = m - lane;
+        const bool valid = m < p.M;
+        const int n0 = w.nt * p.nout;
+        // row offsets and the row's scale, worked out before the accumulator is ready
+        long long zo = 0, ro = 0, yo = 0;
+        float sa = 1.f;
+        if (valid && !p.raw) {
+            if (p.z.p && !p.z_tma) zo = row_off(p.z.m, m);
+            if (p.r.p) ro = row_off(p.r.m, m);
+            if (!p.y_tma) yo = row_off(p.y.m, m);
+            if (p.sa) sa = __ldg(p.sa + m);
+        }
+        int okw = 0;
+        if (lane == 0) okw = mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, ctl, 25) ? 1 : 0;
+        okw = __shfl_sync(0xffffffffu, okw, 0);
+        if (!okw) break;
+        __syncwarp();
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * p.acc_stride;
+        for (int c0 = 32 * part; c0 < p.nout && n0 + c0 < p.N; c0 += 64) {
+            const int n = n0 + c0, cols = p.N - n;
+            float v[32], up[GATED ? 32 : 1];
+            {
+                uint32_t a[32];
+                tmem_ld_32x32b_x32(taddr + (uint32_t)c0, a);
+                if constexpr (GATED) {
+                    uint32_t b[32];
+                    tmem_ld_32x32b_x32(taddr + (uint32_t)(p.nout + c0), b);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(b[i]);
+                } else {
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+            }
+            if (p.raw) {
+                st.tma(tmY, false, v, n, GATED ? 2 * w.split : w.split);
+                if constexpr (GATED) st.tma(tmY, false, up, n, 2 * w.split + 1);
+                continue;
+            }
+            gp_scale_bias(v, sa, p.sb ? p.sb + n : nullptr, p.bias ? p.bias + n : nullptr, cols);
+            if constexpr (GATED)
+                gp_scale_bias(up, sa, p.sb ? p.sb + p.N + n : nullptr, p.bias ? p.bias + p.N + n : nullptr, cols);
+            if (p.z.p) {
+                if (p.z_tma) {
+                    st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, v, n, 0);
+                    if constexpr (GATED) st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, up, n, 1);
+                } else {
+                    st.rows(p.z, zo, v, n, cols);
+                    if constexpr (GATED) st.rows(p.z, zo, up, (long long)p.N + n, cols);
+                }
+            }
+            act_dispatch(p.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = act_f<decltype(act)::value>(v[i]);
+            });
+            if constexpr (GATED) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= up[i];
+            }
+            if (p.r.p && valid) gp_add_residual(p, v, ro, n, cols);
+            if (p.y_tma)
+                st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
+            else
+                st.rows(p.y, yo, v, n, cols);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_tmem_free(tempty0 + 8u * (uint32_t)buf);
+    }
+    if (lane == 0) bulk_wait_group_read<0>();  // staged stores have read shared memory before the CTA exits
+    __syncwarp();
+}
+
+template <bool E4M3, bool A_MN, bool B_MN, bool GATED>
+__global__ void __launch_bounds__(GP_THREADS, 1)
+    gemm_pair_kernel(const __grid_constant__ GpParams p, const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
+                     const __grid_constant__ CUtensorMap tmZ) {
+    constexpr int BK = E4M3 ? GP_LINE : GP_LINE / 2;
+    griddep_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in both CTAs
+    const int ST = p.stages;
+    uint8_t *smB = smem + (size_t)ST * GP_A_BYTES;
+    uint8_t *epi = smB + (size_t)ST * p.b_stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(epi + GP_EPI_WARPS * 2 * p.epi_buf);
+    uint64_t *empty = full + ST;
+    uint64_t *tfull = empty + ST;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1u);   // the leader's expect-tx arrival (+ both CTAs' bytes)
+            mbar_init(&empty[i], 1u);  // the leader's multicast commit
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1u);
+            mbar_init(&tempty[i], 2u * GP_EPI_WARPS);  // every epilogue warp of both CTAs
+        }
+        mbar_init(mma_done, 1u);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, p.tmem_cols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any remote arrival
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const WaitCtl ctl{abort_flag, p.err, p.timeout_ns};
+    const uint32_t sA = smem_u32(smem), sB = smem_u32(smB);
+    griddep_wait();  // no global memory before the grid ahead of this one is done
+
+    if (warp == 0) {
+        if (lane == 0) gp_produce<true, A_MN, GATED, BK>(p, rank, &tmA, sA, full, empty, ctl);
+    } else if (warp == 2) {
+        if (lane == 0) gp_produce<false, B_MN, GATED, BK>(p, rank, &tmB, sB, full, empty, ctl);
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0)
+            gp_mma<E4M3, A_MN, B_MN>(p, tmem_base, sA, sB, full, empty, tfull, tempty, mma_done, ctl);
+        if (lane == 0) {  // the leader's final commit reaches both CTAs
+            volatile int dummy = 0;
+            const WaitCtl fin{&dummy, p.err, p.timeout_ns};
+            mbar_wait(mma_done, 0u, fin, 93);
+        }
+    } else {
+        gp_epilogue<GATED>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, ctl);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the pair's MMAs or loads may touch it
+    tc_fence_after_sync();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, p.tmem_cols);
+}
+
+// ---- split reductions ----------------------------------------------------------------
+
+struct FinishParams {
+    GemmProblem g;
+    const float *part;  // [splits][halves][M][ld] FP32
+    long long ld;
+    int splits;
+    int vec;            // y, z and r take 4-element accesses
+};
+
+__device__ __forceinline__ void fin_load4(const RowTensor &t, long long off, int n, int cols, bool vec, float (&v)[4]) {
+    if (vec && cols >= 4) {
+        if (t.dt == DLC_DATA_BFLOAT16) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(t.p) + off + n);
+            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + n);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < cols ? load_elem(t.p, t.dt, off + (long long)(n + i) * t.m.cs) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void fin_store4(const RowTensor &t, long long off, long long n, int cols, bool vec,
+                                           const float (&v)[4]) {
+    if (vec && cols >= 4) {
+        if (t.dt == DLC_DATA_BFLOAT16)
+            *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(t.p) + off + n) =
+                make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off + n) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < cols) store_elem(t.p, t.dt, off + (n + i) * t.m.cs, v[i]);
+    }
+}
+
+// Adds the partial tiles in the order of their ranges and applies the
+// epilogue: four columns of a row a thread.
+__global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishParams f) {
+    griddep_launch_dependents();
+    const GemmProblem &g = f.g;
+    const int per_row = (int)(f.ld / 4);
+    const long long total = g.M * per_row;
+    const int halves = g.gated ? 2 : 1;
+    const long long plane = g.M * f.ld;
+    griddep_wait();
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
+        const long long m = i / per_row;
+        const int n = (int)(i - m * per_row) * 4, cols = g.N - n;
+        float v[2][4];
+        for (int h = 0; h < halves; ++h) {
+            const float *src = f.part + h * plane + m * f.ld + n;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int sp = 0; sp < f.splits; ++sp) {
+                const float4 q = *reinterpret_cast<const float4 *>(src + (long long)sp * halves * plane);
+                s[0] += q.x, s[1] += q.y, s[2] += q.z, s[3] += q.w;
+            }
+            const float sa = g.sa ? __ldg(g.sa + m) : 1.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long k = (long long)h * g.N + n + j;
+                if (j < cols) {
+                    if (g.sb) s[j] *= sa * __ldg(g.sb + k);
+                    if (g.bias) s[j] += __ldg(g.bias + k);
+                }
+                v[h][j] = s[j];
+            }
+            if (g.z.p) fin_store4(g.z, row_off(g.z.m, m), (long long)h * g.N + n, cols, f.vec && (h == 0 || g.N % 4 == 0), v[h]);
+        }
+        act_dispatch(g.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[0][j] = act_f<decltype(act)::value>(v[0][j]);
+        });
+        if (g.gated) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[0][j] *= v[1][j];
+        }
+        if (g.r.p) {
+            float r[4];
+            fin_load4(g.r, row_off(g.r.m, m), n, cols, f.vec, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[0][j] += r[j];
+        }
+        fin_store4(g.y, row_off(g.y.m, m), n, cols, f.vec, v[0]);
+    }
+}
+
+// ---- operands that TMA cannot load ------------------------------------------------------
+
+// dst: [rows][ld] dense, ld * E a multiple of 16 bytes; src: any strides.  The
+// reads run along the source's contiguous axis, the writes along channels.
+template <typename E>
+__global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
+                                                        long long rows, int C) {
+    griddep_launch_dependents();
+    __shared__ E tile[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long r0 = (long long)blockIdx.x * 32;
+    const bool along_c = src.m.cs == 1;
+    const E *s = static_cast<const E *>(src.p);
+    griddep_wait();
+    for (int c0 = (int)blockIdx.y * 32; c0 < C; c0 += (int)gridDim.y * 32) {
+        __syncthreads();
+        for (int i = warp; i < 32; i += 8) {
+            const long long r = r0 + (along_c ? i : lane);
+            const int c = c0 + (along_c ? lane : i);
+            if (r < rows && c < C) tile[along_c ? i : lane][along_c ? lane : i] = s[row_off(src.m, r) + (long long)c * src.m.cs];
+        }
+        __syncthreads();
+        for (int i = warp; i < 32; i += 8)
+            if (r0 + i < rows && c0 + lane < C) dst[(r0 + i) * ld + c0 + lane] = tile[i][lane];
+    }
+}
+
+// ---- host side ---------------------------------------------------------------------------
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Rows of `ch` channels TMA can load: channels contiguous, one pitch (at least
+// a row), 16-byte aligned.
+bool tma_rows(const RowTensor &t, long long rows, long long ch) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    return t.m.cs == 1 && t.m.uniform && (uintptr_t)t.p % 16 == 0 &&
+           (rows == 1 || ((t.m.ld * e) % 16 == 0 && t.m.ld >= ch && t.m.ld * e < (1LL << 40)));
+}
+
+// Rows of halves x `n` channels that TMA can store (each half its own plane).
+bool tma_store_rows(const RowTensor &t, long long rows, int n, int halves) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    return tma_rows(t, rows, (long long)n * halves) && (halves == 1 || ((long long)n * e) % 16 == 0);
+}
+
+bool vec4_rows(const RowTensor &t) {
+    if (!t.p) return true;
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    auto mult = [&](long long s) { return (s * e) % (4 * e) == 0; };
+    return t.m.cs == 1 && (uintptr_t)t.p % (4 * e) == 0 &&
+           (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
+}
+
+bool vec16_rows(const RowTensor &t) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    auto mult = [&](long long s) { return (s * e) % 16 == 0; };
+    return t.m.cs == 1 && (uintptr_t)t.p % 16 == 0 &&
+           (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
+}
+
+struct GemmPlan {
+    int bn, nout, splits, m_tiles, n_tiles, num_kb;
+    long long a_rows, b_rows;
+    int a_ch, b_ch;             // channels of the operands' rows
+    bool pack_a, pack_b;
+    size_t a_off, b_off, part_off, bytes;
+    long long part_ld;
+};
+
+GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
+    GemmPlan p;
+    const int nb = g.gated ? 2 * g.N : g.N;
+    const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
+    const int e = e4m3 ? 1 : 2, bk = GP_LINE / e;
+    p.a_rows = g.a.trans ? g.K : g.M;
+    p.a_ch = (int)(g.a.trans ? g.M : g.K);
+    p.b_rows = g.b.trans ? g.K : nb;
+    p.b_ch = (int)(g.b.trans ? nb : g.K);
+    p.pack_a = !tma_rows(g.a.t, p.a_rows, p.a_ch);
+    p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
+    p.num_kb = (int)((g.K + bk - 1) / bk);
+    p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
+    // Tile width and split from a small model of the time, in units of one
+    // k-block of a 256-column tile: narrower tiles load more per product, a
+    // unit's first loads and last epilogue are not hidden, partial sums cost
+    // their bytes and a launch.
+    const int pairs = ctx->sm_count / 2;
+    double best = 1e30;
+    p.bn = 256;
+    p.splits = 1;
+    for (int bn : {256, 128, 64}) {
+        if (bn == 64 && g.b.trans) continue;  // MN-major halves are whole 64-index blocks
+        if (bn == 64 && g.gated) continue;    // whole 32-output chunks for both epilogue parts
+        const int nout = g.gated ? bn / 2 : bn;
+        const long long tiles = (long long)p.m_tiles * ((g.N + nout - 1) / nout);
+        const double t_kb = bn == 256 ? 1.0 : bn == 128 ? 0.62 : 0.45;
+        for (int s = 1; s <= 16 && s <= p.num_kb; ++s) {
+            if (s > 1 && tiles * s > 2 * pairs) break;
+            const double waves = (double)((tiles * s + pairs - 1) / pairs);
+            double t = waves * ((p.num_kb + s - 1) / s) * t_kb + 6.0 + (waves - 1) * 1.0;
+            if (s > 1) t += 9.0 + (double)s * g.M * nb * 8.0 / 2.5e6;  // FP32 written and read through the L2
+            if (t < best) best = t, p.bn = bn, p.splits = s;
+        }
+    }
+    p.nout = g.gated ? p.bn / 2 : p.bn;
+    p.n_tiles = (g.N + p.nout - 1) / p.nout;
+    auto packed = [&](long long rows, int ch) { return round256((size_t)rows * ((ch * e + 15) / 16 * 16)); };
+    size_t off = 0;
+    p.a_off = off;
+    if (p.pack_a) off += packed(p.a_rows, p.a_ch);
+    p.b_off = off;
+    if (p.pack_b) off += packed(p.b_rows, p.b_ch);
+    p.part_off = off;
+    p.part_ld = ((long long)g.N + 3) / 4 * 4;
+    if (p.splits > 1) off += round256((size_t)p.splits * (g.gated ? 2 : 1) * g.M * p.part_ld * 4);
+    p.bytes = off;
+    return p;
+}
+
+dlcStatus_t pack_rows(dlcContext *ctx, RowTensor &t, long long rows, int ch, char *dst) {
+    const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    RowTensor src = t;
+    long long ld = (long long)((ch * e + 15) / 16 * 16) / e;
+    const long long blocks = (rows + 31) / 32;
+    // enough blocks to fill the GPU, each walking the rest of its rows' channels
+    const int gy = (int)std::min<long long>((ch + 31) / 32, std::max<long long>(1, (long long)ctx->sm_count * 16 / blocks));
+    void *d = dst;
+    void *args[] = {&src, &d, &ld, &rows, &ch};
+    if (blocks > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    const void *k = e == 1 ? (const void *)pack_rows_kernel<unsigned char> : (const void *)pack_rows_kernel<unsigned short>;
+    const dlcStatus_t st = dlc_launch(ctx, k, dim3((unsigned)blocks, (unsigned)gy), dim3(256), 0, args);
+    t.p = dst;
+    t.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
+    return st;
+}
+
+bool encode(const dlcContext *ctx, CUtensorMap *tm, const RowTensor &t, int nd, const cuuint64_t *dim, long long plane,
+            cuuint32_t box0, cuuint32_t box1, CUtensorMapSwizzle swz) {
+    const cuuint64_t e = (cuuint64_t)dlc_dtype_bytes((dlcDataType_t)t.dt);
+    const cuuint64_t str[2] = {(cuuint64_t)t.m.ld * e, (cuuint64_t)plane * e};
+    const cuuint32_t box[3] = {box0, box1, 1}, ones[3] = {1, 1, 1};
+    const CUtensorMapDataType dt = t.dt == DLC_DATA_FLOAT ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : t.dt == DLC_DATA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return ctx->encode_tiled(tm, dt, (cuuint32_t)nd, t.p, dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A row operand's map: K-major boxes of 128 bytes x `box_rows` rows, or
+// MN-major blocks of 64 channels x 64 rows.
+bool encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperand &o, long long rows, int ch, int box_rows) {
+    RowTensor t = o.t;
+    const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    if (rows == 1) t.m.ld = ((long long)ch * e + 15) / 16 * 16 / e;
+    const cuuint64_t dim[2] = {(cuuint64_t)ch, (cuuint64_t)rows};
+    return encode(ctx, tm, t, 2, dim, 0, (cuuint32_t)(GP_LINE / e), (cuuint32_t)(o.trans ? 64 : box_rows),
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// An output's map: `halves` planes of [M][N], 32 x 32 blocks.
+bool encode_output(const dlcContext *ctx, CUtensorMap *tm, const RowTensor &o, long long M, int N, int planes,
+                   long long plane) {
+    RowTensor t = o;
+    if (M == 1) t.m.ld = ((long long)N * planes + 15) / 16 * 16;
+    const cuuint64_t dim[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)planes};
+    return encode(ctx, tm, t, 3, dim, planes > 1 ? plane : t.m.ld, 32, 32,
+                  t.dt == DLC_DATA_FLOAT ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+const void *pair_kernel(bool e4m3, bool a_mn, bool b_mn, bool gated) {
+    if (gated)
+        return e4m3 ? (const void *)gemm_pair_kernel<true, false, false, true>
+                    : (const void *)gemm_pair_kernel<false, false, false, true>;
+    if (e4m3) return (const void *)gemm_pair_kernel<true, false, false, false>;
+    if (a_mn) return (const void *)gemm_pair_kernel<false, true, true, false>;
+    return b_mn ? (const void *)gemm_pair_kernel<false, false, true, false>
+                : (const void *)gemm_pair_kernel<false, false, false, false>;
+}
+
+// Pairs that the device holds at once (each CTA takes an SM's shared memory);
+// a property of the device, asked once.
+int resident_pairs(const dlcContext *ctx, const void *kern, size_t smem) {
+    static std::atomic<int> known{0};
+    int n = known.load();
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(ctx->sm_count / 2 * 2));
+    cfg.blockDim = dim3(GP_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return std::max(1, ctx->sm_count / 2);
+    }
+    known.store(n);
+    return n;
+}
+
+dlcStatus_t launch_pair(dlcContext *ctx, GemmProblem g, const GemmPlan &pl) {
+    const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
+    const int nb = g.gated ? 2 * g.N : g.N;
+    if (pl.pack_a) {
+        const dlcStatus_t st = pack_rows(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
+        if (st != DLC_STATUS_SUCCESS) return st;
+    }
+    if (pl.pack_b) {
+        const dlcStatus_t st = pack_rows(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
+        if (st != DLC_STATUS_SUCCESS) return st;
+    }
+    GpParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = g.M;
+    p.N = g.N;
+    p.act = g.act;
+    p.BN = pl.bn;
+    p.nout = pl.nout;
+    p.num_kb = pl.num_kb;
+    p.m_tiles = pl.m_tiles;
+    p.n_tiles = pl.n_tiles;
+    if ((long long)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    p.tiles = pl.m_tiles * pl.n_tiles;
+    p.splits = pl.splits;
+    p.units = p.tiles * p.splits;
+    p.raw = pl.splits > 1;
+    p.b_atoms = pl.bn / 128;
+    p.b_stage = (uint32_t)(pl.bn / 2) * GP_LINE;
+    p.sa = g.sa;
+    p.sb = g.sb;
+    p.bias = g.bias;
+    p.z = g.z;
+    p.r = g.r;
+    p.y = g.y;
+    p.r_vec = g.r.p && vec16_rows(g.r);
+    p.err = ctx->d_err;
+    p.timeout_ns = ctx->timeout_ns;
+    const uint32_t fmt = e4m3 ? 0u : 1u;
+    p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)g.a.trans << 15) | ((uint32_t)g.b.trans << 16) |
+              ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((2 * GP_ROWS) >> 4) << 24);
+    p.tmem_cols = (uint32_t)std::max(32, 2 * pl.bn);
+    p.acc_stride = p.tmem_cols / 2;
+
+    CUtensorMap ta, tb, ty, tz;
+    std::memset(&ty, 0, sizeof(ty));
+    std::memset(&tz, 0, sizeof(tz));
+    if (!encode_operand(ctx, &ta, g.a, pl.a_rows, pl.a_ch, GP_ROWS) ||
+        !encode_operand(ctx, &tb, g.b, pl.b_rows, pl.b_ch, pl.bn / 2))
+        return DLC_STATUS_EXECUTION_FAILED;
+    bool f32_stage = false;
+    if (p.raw) {
+        RowTensor part;
+        part.p = g.ws + pl.part_off;
+        part.dt = DLC_DATA_FLOAT;
+        part.m.ld = pl.part_ld;
+        if (!encode_output(ctx, &ty, part, g.M, g.N, pl.splits * (g.gated ? 2 : 1), g.M * pl.part_ld))
+            return DLC_STATUS_EXECUTION_FAILED;
+        f32_stage = true;
+    } else {
+        p.y_tma = tma_store_rows(g.y, g.M, g.N, 1);
+        p.z_tma = g.z.p && tma_store_rows(g.z, g.M, g.N, g.gated ? 2 : 1);
+        if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, g.N, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
+        if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
+        f32_stage = !p.y_tma || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
+    }
+    p.epi_buf = f32_stage ? 4096 : 2048;
+    const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
+    const int stage_bytes = GP_A_BYTES + (int)p.b_stage;
+    p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - 1024 - GP_BAR_AREA - epi_bytes) / stage_bytes);
+    const size_t smem = 1024 + (size_t)p.stages * stage_bytes + epi_bytes + GP_BAR_AREA;
+    const void *kern = pair_kernel(e4m3, g.a.trans != 0, g.b.trans != 0, g.gated != 0);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return DLC_STATUS_EXECUTION_FAILED;
+    }
+    const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);
+    void *args[] = {&p, &ta, &tb, &ty, &tz};
+    dlcStatus_t st = dlc_launch(ctx, kern, dim3((unsigned)(2 * clusters)), dim3(GP_THREADS), smem, args, 2);
+    if (st != DLC_STATUS_SUCCESS || !p.raw) return st;
+    FinishParams f;
+    f.g = g;
+    f.part = reinterpret_cast<const float *>(g.ws + pl.part_off);
+    f.ld = pl.part_ld;
+    f.splits = pl.splits;
+    f.vec = vec4_rows(g.y) && vec4_rows(g.z) && vec4_rows(g.r);
+    const long long items = g.M * (pl.part_ld / 4);
+    const long long blocks = std::min<long long>((items + 255) / 256, (long long)ctx->sm_count * 8);
+    void *fargs[] = {&f};
+    return dlc_launch(ctx, (const void *)gemm_finish_kernel, dim3((unsigned)blocks), dim3(256), 0, fargs);
 }
 
 }  // namespace
 
-dlcKernel_t dlc_gemm_variant(const dlcContext *, const GemmProblem &) { return DLC_KERNEL_DIRECT; }
+dlcKernel_t dlc_gemm_variant(const dlcContext *, const GemmProblem &) { return DLC_KERNEL_GEMM_PAIR; }
 
-size_t dlc_gemm_workspace(const dlcContext *, const GemmProblem &) { return 0; }
+size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g) { return plan_gemm(ctx, g).bytes; }
 
-dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &pb) {
-    GemmProblem g = pb;
-    void *args[] = {&g};
-    return dlc_launch(ctx, g.gated ? (const void *)gemm_direct_kernel<true> : (const void *)gemm_direct_kernel<false>,
-                      dim3((unsigned)((g.M + DT - 1) / DT), (unsigned)((g.N + DT - 1) / DT)), dim3(256), 0, args);
-}
+dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g) { return launch_pair(ctx, g, plan_gemm(ctx, g)); }

@@ -158,10 +158,12 @@ typedef enum {
                                      reduction, both operands MN-major from TMA */
     DLC_KERNEL_POOL_NHWC = 9,     /* pooling with channels innermost: 16-byte vectors of
                                      channels per thread */
-    DLC_KERNEL_TC_ROWSTACK = 10   /* TF32, channel-planar (NCHW) x, unit horizontal stride,
+    DLC_KERNEL_TC_ROWSTACK = 10,  /* TF32, channel-planar (NCHW) x, unit horizontal stride,
                                      up to 64 filters: filters stacked over output rows as the
                                      MMA's M side, output pixels (per phase q mod 4) as N,
                                      read in place from shifted copies of input rows */
+    DLC_KERNEL_GEMM_PAIR = 11     /* channel operators: tcgen05 products on pairs of SMs, 256 rows
+                                     a tile, operands by TMA */
 } dlcKernel_t;
 
 /* Device error codes recorded by kernels (dlcGetLastDeviceError). */
