@@ -23,71 +23,184 @@ constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_FLOOR = 1e-30f;  // max |y| of an all-zero row counts as this
 constexpr int RMS_THREADS = 256;
 constexpr int RMS_MAX_WARPS = 32;
+// Blocks of 256 threads an SM is to hold (what the registers are limited for).
+constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 
-// W consecutive elements (n <= W of them inside the row) as FP32.  W = 8: the
-// address is 16-byte aligned; a partial vector is read element by element, so
+// E = V * W values of one row held by a thread: V vectors of W consecutive
+// channels.  W = 8 (16-byte aligned) or 1.
+template <int W, int V>
+struct Cols {
+    int c[V];   // first channel of each vector, 0 where the vector is past the row
+    int n[V];   // channels of it that exist, 0 .. W
+    __device__ __forceinline__ Cols(int t, int tpr, int C) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int at = (t + j * tpr) * W;
+            n[j] = min(max(C - at, 0), W);
+            c[j] = n[j] ? at : 0;
+        }
+    }
+};
+
+// V vectors of a row as FP32; a partial vector is read element by element, so
 // nothing past the row is touched.
-template <int W>
-__device__ __forceinline__ void load_vec(const RowTensor &t, long long off, int n, float *v) {
-    if constexpr (W == 1) {
-        v[0] = n > 0 ? load_elem(t.p, t.dt, off) : 0.f;
-    } else {
-        if (n >= W) {
+template <int W, int V>
+__device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float *v = f + j * W;
+        if (W == 8 && k.n[j] == W) {
             if (t.dt == DLC_DATA_BFLOAT16) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off);
+                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                }
+                for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
             } else {
-                const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off);
-                const float4 a = f[0], b = f[1];
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-                v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const float4 a = p[i];
+                    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+                }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = i < n ? load_elem(t.p, t.dt, off + i) : 0.f;
+            for (int i = 0; i < W; ++i) v[i] = i < k.n[j] ? load_elem(t.p, t.dt, off + k.c[j] + i) : 0.f;
         }
     }
 }
+
+// A thread's next rows of T tensors.  BF (all of them BF16, W = 8): copied
+// asynchronously into a ring of S rows in shared memory, of which a thread
+// reads back only what it copied itself (no barrier), so S - 1 rows of every
+// thread are in flight; otherwise one row ahead, in registers.
+template <int W, int V, bool BF, int T, int S>
+struct Rows {
+    float next[T][V * W];
+    static constexpr int AHEAD = 1;
+    __device__ __forceinline__ void start(uint32_t) {}
+    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<W, V> &cols) {
+        load_row<W, V>(t, off, cols, next[k]);
+    }
+    __device__ __forceinline__ void commit() {}
+    __device__ __forceinline__ void take(float (&f)[T][V * W]) {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int i = 0; i < V * W; ++i) f[k][i] = next[k][i];
+    }
+    static size_t smem(int) { return 0; }
+};
+
+template <int V, int T, int S>
+struct Rows<8, V, true, T, S> {
+    uint32_t base, put, get, vec, row;  // this thread's slot 0, the rows to fill and to read, bytes between vectors / rows
+    static constexpr int AHEAD = S - 1;
+    __device__ __forceinline__ void start(uint32_t smem) {
+        base = smem + threadIdx.x * 16u;
+        vec = 16u * blockDim.x;
+        row = (uint32_t)(T * V) * vec;
+        put = get = 0;
+    }
+    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<8, V> &cols) {
+        const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
+#pragma unroll
+        for (int j = 0; j < V; ++j) cp_async_16(base + put + (uint32_t)(k * V + j) * vec, p + cols.c[j], 2u * (uint32_t)cols.n[j]);
+    }
+    __device__ __forceinline__ void commit() {
+        cp_async_commit();
+        put = put == row * (S - 1) ? 0 : put + row;
+    }
+    __device__ __forceinline__ void take(float (&f)[T][V * 8]) {
+        cp_async_wait<S - 2>();
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(base + get + (uint32_t)(k * V + j) * vec)
+                             : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = unpack_bf16(w[i]);
+                    f[k][8 * j + 2 * i] = u.x, f[k][8 * j + 2 * i + 1] = u.y;
+                }
+            }
+        get = get == row * (S - 1) ? 0 : get + row;
+    }
+    static size_t smem(int threads) { return (size_t)S * T * V * 16 * threads; }
+};
+
+// Rows of the ring.  Measured, 100352 x 512 forward / 25088 x 1024 backward, BF16:
+// 3 rows at 4 / 2 blocks an SM 74.5 / 40.0 us; 4 rows 77.6 / 41.1; one row ahead
+// in registers 109 us forward.
+template <int MAXT>
+constexpr int ring_rows() { return MAXT > 512 ? 2 : 3; }
+
+// Row offsets of one tensor along a thread's rows: added up where the rows
+// have one pitch, worked out from n, h and w otherwise.
+struct RowWalk {
+    long long off, inc;
+    __device__ __forceinline__ RowWalk(const RowMap &m, long long row, long long step) : off(row * m.ld), inc(step * m.ld) {}
+    __device__ __forceinline__ long long at(const RowMap &m, long long row) const { return m.uniform ? off : row_off(m, row); }
+    __device__ __forceinline__ void next() { off += inc; }
+};
 
 template <int W>
 __device__ __forceinline__ void store_vec(const RowTensor &t, long long off, int n, const float *v) {
-    if constexpr (W == 1) {
-        if (n > 0) store_elem(t.p, t.dt, off, v[0]);
-    } else {
-        if (n >= W) {
-            if (t.dt == DLC_DATA_BFLOAT16) {
-                *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) =
-                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-            } else if (t.dt == DLC_DATA_FLOAT) {
-                float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off);
-                f[0] = make_float4(v[0], v[1], v[2], v[3]);
-                f[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(t.p) + off) =
-                    make_uint2(pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16),
-                               pack_e4m3(v[4], v[5]) | (pack_e4m3(v[6], v[7]) << 16));
-            }
+    if (W == 8 && n == W) {
+        if (t.dt == DLC_DATA_BFLOAT16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (t.dt == DLC_DATA_FLOAT) {
+            float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off);
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) f[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
-            for (int i = 0; i < W; ++i)
-                if (i < n) store_elem(t.p, t.dt, off + i, v[i]);
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i)
+                w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
+            *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(t.p) + off) = make_uint2(w[0], w[1]);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (i < n) store_elem(t.p, t.dt, off + i, v[i]);
     }
 }
 
-template <int W>
-__device__ __forceinline__ void load_gamma(const float *gamma, int c, int C, float *v) {
+template <int W, int V>
+__device__ __forceinline__ void store_row(const RowTensor &t, long long off, const Cols<W, V> &k, const float (&f)[V * W]) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = c + i < C ? __ldg(gamma + c + i) : 0.f;
+    for (int j = 0; j < V; ++j) store_vec<W>(t, off + k.c[j], k.n[j], f + j * W);
+}
+
+__device__ __forceinline__ float2 pair(const float *f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
+__device__ __forceinline__ void set_pair(float *f, int i, float2 v) { f[2 * i] = v.x, f[2 * i + 1] = v.y; }
+
+template <int W>
+__device__ __forceinline__ void load_gamma(const float *gamma, int c, int C, bool vec, float *v) {
+    if (W == 8 && vec && c + W <= C) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(gamma + c) + i);
+            v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = c + i < C ? __ldg(gamma + c + i) : 0.f;
+    }
 }
 
 // (sum of a, sum or maximum of b) over the `tpr` threads of a row: a power of
-// two, within a warp or whole warps.  All of the block's threads call it; the
-// buffer alternates between calls, so one barrier per call is enough.
+// two, within a warp or whole warps.  The row's threads meet at a named
+// barrier of their own; the buffer alternates between calls, so one barrier a
+// call is enough.
 template <bool MAX_B>
 __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 (*buf)[RMS_MAX_WARPS], int parity) {
     for (int o = (tpr < 32 ? tpr : 32) / 2; o > 0; o /= 2) {
@@ -96,9 +209,9 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 (
         b = MAX_B ? fmaxf(b, ob) : b + ob;
     }
     if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * (tpr >> 5);
+        const int warp = threadIdx.x >> 5, slot = threadIdx.x / tpr, first = slot * (tpr >> 5);
         if ((threadIdx.x & 31) == 0) buf[parity][warp] = make_float2(a, b);
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
         a = 0.f, b = 0.f;
         for (int i = 0; i < (tpr >> 5); ++i) {
             const float2 v = buf[parity][first + i];
@@ -109,111 +222,142 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 (
     return make_float2(a, b);
 }
 
-// 1 / scale and scale of an E4M3 row whose largest |y| is `amax` (NaN stays NaN).
+// The scale of an E4M3 row whose largest |y| is `amax` (NaN stays NaN).
 __device__ __forceinline__ float e4m3_scale(float amax) {
     return (amax < SCALE_FLOOR ? SCALE_FLOOR : amax) / E4M3_MAX;
 }
 
 // Rows in registers: `tpr` threads a row, V vectors of W channels a thread.
-template <int W, int V>
-__global__ void __launch_bounds__(1024) rms_rows_kernel(const __grid_constant__ RmsProblem p, int tpr) {
+// The next row's loads are issued before this row's reduction waits.
+template <int W, int V, bool BF, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
+    rms_rows_kernel(const __grid_constant__ RmsProblem p, int tpr, int gamma_vec) {
     griddep_launch_dependents();
     __shared__ float2 buf[2][RMS_MAX_WARPS];
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    extern __shared__ uint4 ring_s[];
+    constexpr int E = V * W;
+    const Cols<W, V> cols(t, tpr, p.C);
+    const float inv_c = 1.f / (float)p.C;
+    const bool e4m3 = p.y.dt == DLC_DATA_FLOAT8_E4M3;
+    float g[E];
+#pragma unroll
+    for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
     griddep_wait();
-    int parity = 0;
-    for (long long row0 = (long long)blockIdx.x * rpb; row0 < p.rows; row0 += (long long)gridDim.x * rpb, parity ^= 1) {
-        const long long row = row0 + slot;
+    Rows<W, V, BF, 2, ring_rows<MAXT>()> rows;
+    rows.start(smem_u32(ring_s));
+    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
+    RowWalk wx(p.x.m, row, step), wr(p.r.m, row, step), wt(p.t.m, row, step), wy(p.y.m, row, step);
+    auto fetch = [&]() {
+        if (ahead < p.rows) {
+            rows.fetch(p.x, 0, wx.at(p.x.m, ahead), cols);
+            if (p.r.p) rows.fetch(p.r, 1, wr.at(p.r.m, ahead), cols);
+        }
+        rows.commit();
+        ahead += step;
+        wx.next();
+        wr.next();
+    };
+    for (int i = 0; i < rows.AHEAD; ++i) fetch();
+    // every thread of the block makes the same number of rounds
+    for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wt.next(), wy.next()) {
         const bool on = row < p.rows;
-        const long long xo = on ? row_off(p.x.m, row) : 0;
-        const long long ro = on && p.r.p ? row_off(p.r.m, row) : 0;
-        float v[V][W];
-        float sq = 0.f, mx = 0.f;
+        float f[2][E];
+        rows.take(f);
+        float *v = f[0];
+        if (p.r.p) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (t + j * tpr) * W, n = on ? p.C - c : 0;
-            load_vec<W>(p.x, xo + c, n, v[j]);
-            if (p.r.p) {
-                float r[W];
-                load_vec<W>(p.r, ro + c, n, r);
-#pragma unroll
-                for (int i = 0; i < W; ++i) v[j][i] += r[i];
-            }
+            for (int i = 0; i < E / 2; ++i) set_pair(v, i, add2(pair(v, i), pair(f[1], i)));
         }
-        if (p.t.p && on) {
-            const long long to = row_off(p.t.m, row);
+        if (p.t.p && on) store_row<W, V>(p.t, wt.at(p.t.m, row), cols, f[0]);
+        fetch();
+        float2 sq = make_float2(0.f, 0.f);
+        float mx = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (t + j * tpr) * W;
-                store_vec<W>(p.t, to + c, p.C - c, v[j]);
-            }
+        for (int i = 0; i < E / 2; ++i) {
+            sq = fma2(pair(v, i), pair(v, i), sq);
+            set_pair(v, i, mul2(pair(v, i), pair(g, i)));
         }
+        if (e4m3) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float g[W];
-            load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, g);
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                sq = fmaf(v[j][i], v[j][i], sq);
-                v[j][i] *= g[i];
-                mx = fmaxf(mx, fabsf(v[j][i]));
-            }
+            for (int i = 0; i < E; ++i) mx = fmaxf(mx, fabsf(v[i]));
         }
-        const float2 red = row_reduce<true>(sq, mx, tpr, buf, parity);
+        const float2 red = row_reduce<true>(sq.x + sq.y, mx, tpr, buf, parity);
         if (!on) continue;
-        float f = rsqrtf(red.x / (float)p.C + p.eps);
-        if (p.y.dt == DLC_DATA_FLOAT8_E4M3) {
-            const float s = e4m3_scale(red.y * f);
+        float rho = rsqrtf(red.x * inv_c + p.eps);
+        if (e4m3) {
+            const float s = e4m3_scale(red.y * rho);
             if (t == 0) p.scale[row] = s;
-            f = f / s;
+            rho = rho / s;
         }
-        const long long yo = row_off(p.y.m, row);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (t + j * tpr) * W;
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[j][i] *= f;
-            store_vec<W>(p.y, yo + c, p.C - c, v[j]);
-        }
+        for (int i = 0; i < E / 2; ++i) set_pair(v, i, mul2(pair(v, i), make_float2(rho, rho)));
+        store_row<W, V>(p.y, wy.at(p.y.m, row), cols, f[0]);
     }
 }
 
-// The remaining layouts (channels not contiguous, or too many for registers):
-// 32 rows a block, one per lane, the channels dealt to eight warps; the row is
-// read twice, the sum t recomputed (so t may overwrite x or r in place).
+// The remaining layouts, two passes over a row.  LANES (channels apart): 32
+// rows a block, one per lane, the channels dealt to eight warps, so neighbouring
+// rows share the loads.  Otherwise (a row too long for registers): one row a
+// block, its channels dealt to the threads.  The second pass recomputes t (so t
+// may overwrite x or r in place).
+template <bool LANES>
+struct AnyMap {
+    static constexpr int ROWS = LANES ? 32 : 1, STEP = LANES ? 8 : RMS_THREADS;
+    static __device__ __forceinline__ int row() { return LANES ? (int)(threadIdx.x & 31) : 0; }
+    static __device__ __forceinline__ int first() { return LANES ? (int)(threadIdx.x >> 5) : (int)threadIdx.x; }
+    // sums a (and sums or maximises b) over the threads of this thread's row
+    template <bool MAX_B>
+    static __device__ float2 join(float a, float b, float2 (*part)[32]) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (!LANES) {
+            for (int o = 16; o > 0; o /= 2) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                const float ob = __shfl_xor_sync(0xffffffffu, b, o);
+                b = MAX_B ? fmaxf(b, ob) : b + ob;
+            }
+        }
+        __syncthreads();
+        part[warp][lane] = make_float2(a, b);
+        __syncthreads();
+        a = 0.f, b = 0.f;
+        for (int i = 0; i < RMS_THREADS / 32; ++i) {
+            const float2 v = part[i][lane];
+            a += v.x;
+            b = MAX_B ? fmaxf(b, v.y) : b + v.y;
+        }
+        return make_float2(a, b);
+    }
+};
+
+template <bool LANES>
 __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_constant__ RmsProblem p) {
+    using M = AnyMap<LANES>;
     griddep_launch_dependents();
-    __shared__ float2 part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float2 part[RMS_THREADS / 32][32];
     griddep_wait();
-    for (long long row0 = (long long)blockIdx.x * 32; row0 < p.rows; row0 += (long long)gridDim.x * 32) {
-        const long long row = row0 + lane;
+    for (long long row0 = (long long)blockIdx.x * M::ROWS; row0 < p.rows; row0 += (long long)gridDim.x * M::ROWS) {
+        const long long row = row0 + M::row();
         const bool on = row < p.rows;
         const long long xo = on ? row_off(p.x.m, row) : 0, ro = on && p.r.p ? row_off(p.r.m, row) : 0;
         float sq = 0.f, mx = 0.f;
-        for (int c = warp; on && c < p.C; c += 8) {
+        for (int c = M::first(); on && c < p.C; c += M::STEP) {
             float v = load_elem(p.x.p, p.x.dt, xo + c * p.x.m.cs);
             if (p.r.p) v += load_elem(p.r.p, p.r.dt, ro + c * p.r.m.cs);
             sq = fmaf(v, v, sq);
             mx = fmaxf(mx, fabsf(v * __ldg(p.gamma + c)));
         }
-        part[warp][lane] = make_float2(sq, mx);
-        __syncthreads();
-        sq = 0.f, mx = 0.f;
-        for (int i = 0; i < 8; ++i) {
-            sq += part[i][lane].x;
-            mx = fmaxf(mx, part[i][lane].y);
-        }
-        __syncthreads();
+        const float2 red = M::template join<true>(sq, mx, part);
         if (!on) continue;
-        float f = rsqrtf(sq / (float)p.C + p.eps);
+        float f = rsqrtf(red.x / (float)p.C + p.eps);
         if (p.y.dt == DLC_DATA_FLOAT8_E4M3) {
-            const float s = e4m3_scale(mx * f);
-            if (warp == 0) p.scale[row] = s;
+            const float s = e4m3_scale(red.y * f);
+            if (M::first() == 0) p.scale[row] = s;
             f = f / s;
         }
         const long long to = p.t.p ? row_off(p.t.m, row) : 0, yo = row_off(p.y.m, row);
-        for (int c = warp; c < p.C; c += 8) {
+        for (int c = M::first(); c < p.C; c += M::STEP) {
             float v = load_elem(p.x.p, p.x.dt, xo + c * p.x.m.cs);
             if (p.r.p) v += load_elem(p.r.p, p.r.dt, ro + c * p.r.m.cs);
             if (p.t.p) store_elem(p.t.p, p.t.dt, to + c * p.t.m.cs, v);
@@ -224,71 +368,74 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
 
 // Backward, rows in registers.  Each thread adds up dgamma of its own channels
 // over the rows it visits; a block writes one partial row of sums.
-template <int W, int V>
-__global__ void __launch_bounds__(1024) rms_bwd_rows_kernel(const __grid_constant__ RmsBwdProblem p, int tpr) {
+template <int W, int V, bool BF, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
+    rms_bwd_rows_kernel(const __grid_constant__ RmsBwdProblem p, int tpr, int gamma_vec) {
     griddep_launch_dependents();
     __shared__ float2 buf[2][RMS_MAX_WARPS];
-    extern __shared__ float acc_s[];  // [rows per block][C], to join the block's row slots
+    extern __shared__ uint4 ring_s[];
+    constexpr int E = V * W;
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    const Cols<W, V> cols(t, tpr, p.C);
+    const float inv_c = 1.f / (float)p.C;
+    float g[E], acc[E];
+#pragma unroll
+    for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
     griddep_wait();
-    float acc[V][W];
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[j][i] = 0.f;
-    int parity = 0;
-    for (long long row0 = (long long)blockIdx.x * rpb; row0 < p.rows; row0 += (long long)gridDim.x * rpb, parity ^= 1) {
-        const long long row = row0 + slot;
+    Rows<W, V, BF, 3, ring_rows<MAXT>()> rows;
+    rows.start(smem_u32(ring_s));
+    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
+    RowWalk wy(p.dy.m, row, step), wt(p.t.m, row, step), ws(p.dt.m, row, step), wx(p.dx.m, row, step);
+    auto fetch = [&]() {
+        if (ahead < p.rows) {
+            rows.fetch(p.dy, 0, wy.at(p.dy.m, ahead), cols);
+            rows.fetch(p.t, 1, wt.at(p.t.m, ahead), cols);
+            if (p.dt.p) rows.fetch(p.dt, 2, ws.at(p.dt.m, ahead), cols);
+        }
+        rows.commit();
+        ahead += step;
+        wy.next();
+        wt.next();
+        ws.next();
+    };
+    for (int i = 0; i < rows.AHEAD; ++i) fetch();
+    for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wx.next()) {
         const bool on = row < p.rows;
-        const long long yo = on ? row_off(p.dy.m, row) : 0, to = on ? row_off(p.t.m, row) : 0;
-        float d[V][W], v[V][W];
-        float sq = 0.f, dot = 0.f;
+        float f[3][E];
+        rows.take(f);
+        float2 sq = make_float2(0.f, 0.f), dot = sq;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (t + j * tpr) * W, n = on ? p.C - c : 0;
-            load_vec<W>(p.dy, yo + c, n, d[j]);
-            load_vec<W>(p.t, to + c, n, v[j]);
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 v = pair(f[1], i);
+            sq = fma2(v, v, sq);
+            dot = fma2(mul2(pair(f[0], i), pair(g, i)), v, dot);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float g[W];
-            load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, g);
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                sq = fmaf(v[j][i], v[j][i], sq);
-                dot = fmaf(d[j][i] * g[i], v[j][i], dot);
-            }
-        }
-        const float2 red = row_reduce<false>(sq, dot, tpr, buf, parity);
+        fetch();
+        const float2 red = row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, buf, parity);
         if (!on) continue;
-        const float rho = rsqrtf(red.x / (float)p.C + p.eps);
-        const float k = rho * rho * rho * (red.y / (float)p.C);
-        const long long xo = row_off(p.dx.m, row), so = p.dt.p ? row_off(p.dt.m, row) : 0;
+        const float rho = rsqrtf(red.x * inv_c + p.eps);
+        const float k = -(rho * rho * rho * (red.y * inv_c));
+        const float2 rho2 = make_float2(rho, rho), k2 = make_float2(k, k);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (t + j * tpr) * W, n = p.C - c;
-            float g[W], s[W];
-            load_gamma<W>(p.gamma, c, p.C, g);
-#pragma unroll
-            for (int i = 0; i < W; ++i) s[i] = 0.f;
-            if (p.dt.p) load_vec<W>(p.dt, so + c, n, s);
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                acc[j][i] = fmaf(d[j][i] * rho, v[j][i], acc[j][i]);
-                s[i] += rho * d[j][i] * g[i] - v[j][i] * k;
-            }
-            store_vec<W>(p.dx, xo + c, n, s);
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 d = mul2(pair(f[0], i), rho2), v = pair(f[1], i);
+            set_pair(acc, i, fma2(d, v, pair(acc, i)));
+            const float2 s = p.dt.p ? pair(f[2], i) : make_float2(0.f, 0.f);
+            set_pair(f[2], i, fma2(d, pair(g, i), fma2(v, k2, s)));
         }
+        store_row<W, V>(p.dx, wx.at(p.dx.m, row), cols, f[2]);
     }
     if (!p.dgamma) return;
-    if (rpb > 1) {
+    if (rpb > 1) {  // join the block's row slots, in the ring's place: [slot][C]
+        float *acc_s = reinterpret_cast<float *>(ring_s);
+        cp_async_wait<0>();
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const int c = (t + j * tpr) * W + i;
-                if (c < p.C) acc_s[(long long)slot * p.C + c] = acc[j][i];
-            }
+        for (int i = 0; i < E; ++i)
+            if (i % W < cols.n[i / W]) acc_s[(long long)slot * p.C + cols.c[i / W] + i % W] = acc[i];
         __syncthreads();
         for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
             float s = 0.f;
@@ -297,47 +444,37 @@ __global__ void __launch_bounds__(1024) rms_bwd_rows_kernel(const __grid_constan
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const int c = (t + j * tpr) * W + i;
-                if (c < p.C) p.ws[(long long)blockIdx.x * p.C + c] = acc[j][i];
-            }
+        for (int i = 0; i < E; ++i)
+            if (i % W < cols.n[i / W]) p.ws[(long long)blockIdx.x * p.C + cols.c[i / W] + i % W] = acc[i];
     }
 }
 
-// Backward for the remaining layouts: one row a lane as above.  A block's
-// dgamma is summed over its rows by warp shuffles, one channel at a time, into
-// its row of partial sums (only its own warp touches a channel).
+// Backward for the remaining layouts.  A block's dgamma collects in its row of
+// partial sums, a channel always through the same thread (LANES: its warp's
+// rows joined by shuffles).
+template <bool LANES>
 __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_constant__ RmsBwdProblem p) {
+    using M = AnyMap<LANES>;
     griddep_launch_dependents();
-    __shared__ float2 part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float2 part[RMS_THREADS / 32][32];
     griddep_wait();
     bool first = true;
-    for (long long row0 = (long long)blockIdx.x * 32; row0 < p.rows; row0 += (long long)gridDim.x * 32) {
-        const long long row = row0 + lane;
+    for (long long row0 = (long long)blockIdx.x * M::ROWS; row0 < p.rows; row0 += (long long)gridDim.x * M::ROWS) {
+        const long long row = row0 + M::row();
         const bool on = row < p.rows;
         const long long yo = on ? row_off(p.dy.m, row) : 0, to = on ? row_off(p.t.m, row) : 0;
         float sq = 0.f, dot = 0.f;
-        for (int c = warp; on && c < p.C; c += 8) {
+        for (int c = M::first(); on && c < p.C; c += M::STEP) {
             const float v = load_elem(p.t.p, p.t.dt, to + c * p.t.m.cs);
             const float d = load_elem(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs) * __ldg(p.gamma + c);
             sq = fmaf(v, v, sq);
             dot = fmaf(d, v, dot);
         }
-        part[warp][lane] = make_float2(sq, dot);
-        __syncthreads();
-        sq = 0.f, dot = 0.f;
-        for (int i = 0; i < 8; ++i) {
-            sq += part[i][lane].x;
-            dot += part[i][lane].y;
-        }
-        __syncthreads();
-        const float rho = on ? rsqrtf(sq / (float)p.C + p.eps) : 0.f;
-        const float k = rho * rho * rho * (dot / (float)p.C);
+        const float2 red = M::template join<false>(sq, dot, part);
+        const float rho = on ? rsqrtf(red.x / (float)p.C + p.eps) : 0.f;
+        const float k = rho * rho * rho * (red.y / (float)p.C);
         const long long xo = on ? row_off(p.dx.m, row) : 0, so = on && p.dt.p ? row_off(p.dt.m, row) : 0;
-        for (int c = warp; c < p.C; c += 8) {
+        for (int c = M::first(); c < p.C; c += M::STEP) {
             float a = 0.f;
             if (on) {
                 const float v = load_elem(p.t.p, p.t.dt, to + c * p.t.m.cs);
@@ -348,8 +485,9 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
                 store_elem(p.dx.p, p.dx.dt, xo + c * p.dx.m.cs, s);
             }
             if (p.dgamma) {
-                for (int o = 16; o > 0; o /= 2) a += __shfl_xor_sync(0xffffffffu, a, o);
-                if (lane == 0) {
+                if (LANES)
+                    for (int o = 16; o > 0; o /= 2) a += __shfl_xor_sync(0xffffffffu, a, o);
+                if (!LANES || M::row() == 0) {
                     float *w = p.ws + (long long)blockIdx.x * p.C + c;
                     *w = first ? a : *w + a;
                 }
@@ -380,7 +518,8 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *ws, float 
 // ---- host side ---------------------------------------------------------------
 
 struct RowPlan {
-    int w = 0, v = 0;  // channels per vector (0: the any-layout kernel), vectors per thread
+    int w = 0, v = 0;  // channels per vector (0: the two-pass kernels), vectors per thread
+    bool lanes = false;
     int tpr = 0, threads = 0;
     long long blocks = 0;
 };
@@ -397,52 +536,81 @@ bool vec_ok(const RowTensor &t) {
 
 bool contiguous(const RowTensor &t) { return !t.p || t.m.cs == 1; }
 
-RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, int v_max, int sm_count) {
+RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, int per_sm, int sm_count) {
     RowPlan r;
     r.threads = RMS_THREADS;
+    r.lanes = !cs1;
     if (cs1) {
         r.w = vec ? 8 : 1;
+        const int v_max = vec ? 2 : 8;
         const long long nv = (C + r.w - 1) / r.w;
-        // vectors a thread: few for short rows (more threads a row), v_max at most
-        int v = 1, tpr = 8;
+        int v = vec ? 1 : 2, tpr = 8;
         while (tpr < 32 && tpr * v < nv) tpr *= 2;
         while (v < v_max && tpr * v < nv && tpr == 32) v *= 2;
         while (tpr < 1024 && (long long)tpr * v < nv) tpr *= 2;
-        if ((long long)tpr * v < nv) r.w = 0;
-        r.v = v;
+        if ((long long)tpr * v < nv) r.w = 0;  // longer than a block's registers
+        r.v = v == 4 ? 8 : v;
         r.tpr = tpr;
         if (r.w && tpr > RMS_THREADS) r.threads = tpr;
     }
-    const int rpb = r.w ? r.threads / r.tpr : 32;
+    const int rpb = r.w ? r.threads / r.tpr : (r.lanes ? 32 : 1);
     const long long need = (rows + rpb - 1) / rpb;
-    const long long most = (long long)sm_count * (2048 / r.threads);
+    const long long most = (long long)sm_count * (r.w ? (r.threads > RMS_THREADS ? 1 : per_sm) : 4);
     r.blocks = need < most ? need : most;
     return r;
 }
 
 RowPlan plan_fwd(const dlcContext *ctx, const RmsProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
-                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), 4, ctx->sm_count);
+                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), RMS_FWD_BLOCKS, ctx->sm_count);
 }
 
 RowPlan plan_bwd(const dlcContext *ctx, const RmsBwdProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.dy) && contiguous(p.t) && contiguous(p.dt) && contiguous(p.dx),
-                     vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), 2, ctx->sm_count);
+                     vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), RMS_BWD_BLOCKS, ctx->sm_count);
 }
 
-const void *fwd_kernel(const RowPlan &r) {
-    if (!r.w) return (const void *)rms_any_kernel;
-    if (r.w == 8)
-        return r.v == 1 ? (const void *)rms_rows_kernel<8, 1>
-                        : r.v == 2 ? (const void *)rms_rows_kernel<8, 2> : (const void *)rms_rows_kernel<8, 4>;
-    return r.v == 1 ? (const void *)rms_rows_kernel<1, 1>
-                    : r.v == 2 ? (const void *)rms_rows_kernel<1, 2> : (const void *)rms_rows_kernel<1, 4>;
+bool is_bf16(const RowTensor &t) { return !t.p || t.dt == DLC_DATA_BFLOAT16; }
+
+struct RowKernel {
+    const void *fn;
+    size_t smem;
+};
+
+// More than 48 KiB of shared memory (the static part included) has to be asked for.
+bool allow_smem(const RowKernel &k, size_t smem) {
+    if (smem <= 47 * 1024) return true;
+    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
 }
 
-const void *bwd_kernel(const RowPlan &r) {
-    if (!r.w) return (const void *)rms_bwd_any_kernel;
-    if (r.w == 8) return r.v == 1 ? (const void *)rms_bwd_rows_kernel<8, 1> : (const void *)rms_bwd_rows_kernel<8, 2>;
-    return r.v == 1 ? (const void *)rms_bwd_rows_kernel<1, 1> : (const void *)rms_bwd_rows_kernel<1, 2>;
+template <int W, int V, bool BF, int MAXT>
+RowKernel fwd_entry(const RowPlan &r) {
+    return {(const void *)rms_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 2, ring_rows<MAXT>()>::smem(r.threads)};
+}
+
+template <int W, bool BF>
+RowKernel fwd_kernel(const RowPlan &r) {
+    constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
+    if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r);
+    if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r);
+    if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r);
+    return fwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
+}
+
+template <int W, int V, bool BF, int MAXT>
+RowKernel bwd_entry(const RowPlan &r) {
+    return {(const void *)rms_bwd_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 3, ring_rows<MAXT>()>::smem(r.threads)};
+}
+
+template <int W, bool BF>
+RowKernel bwd_kernel(const RowPlan &r) {
+    constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
+    if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r);
+    if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r);
+    if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r);
+    return bwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
 }
 
 }  // namespace
@@ -450,14 +618,19 @@ const void *bwd_kernel(const RowPlan &r) {
 dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
     const RowPlan r = plan_fwd(ctx, pb);
     RmsProblem p = pb;
-    int tpr = r.tpr;
-    void *args[] = {&p, &tpr};
-    return dlc_launch(ctx, fwd_kernel(r), dim3((unsigned)r.blocks), dim3((unsigned)r.threads), 0, args);
+    int tpr = r.tpr, gamma_vec = (uintptr_t)p.gamma % 16 == 0;
+    void *args[] = {&p, &tpr, &gamma_vec};
+    const RowKernel k =
+        r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
+        : r.w == 1 ? fwd_kernel<1, false>(r)
+        : is_bf16(p.x) && is_bf16(p.r) ? fwd_kernel<8, true>(r) : fwd_kernel<8, false>(r);
+    if (!allow_smem(k, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
+    return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
 
 size_t dlc_rms_bwd_workspace(const dlcContext *ctx, const RmsBwdProblem &p) {
     // the most blocks of any layout's plan, so that the pointers' alignment does not matter
-    const long long most = (long long)ctx->sm_count * (2048 / RMS_THREADS);
+    const long long most = (long long)ctx->sm_count * 4;
     const long long blocks = p.rows < most ? p.rows : most;
     return (size_t)blocks * p.C * sizeof(float);
 }
@@ -465,11 +638,16 @@ size_t dlc_rms_bwd_workspace(const dlcContext *ctx, const RmsBwdProblem &p) {
 dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
     const RowPlan r = plan_bwd(ctx, pb);
     RmsBwdProblem p = pb;
-    int tpr = r.tpr;
-    void *args[] = {&p, &tpr};
+    int tpr = r.tpr, gamma_vec = (uintptr_t)p.gamma % 16 == 0;
+    void *args[] = {&p, &tpr, &gamma_vec};
+    const RowKernel k =
+        r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_bwd_any_kernel<true> : (const void *)rms_bwd_any_kernel<false>, 0}
+        : r.w == 1 ? bwd_kernel<1, false>(r)
+        : is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt) ? bwd_kernel<8, true>(r) : bwd_kernel<8, false>(r);
     const int rpb = r.w ? r.threads / r.tpr : 1;
-    const size_t smem = rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0;
-    dlcStatus_t st = dlc_launch(ctx, bwd_kernel(r), dim3((unsigned)r.blocks), dim3((unsigned)r.threads), smem, args);
+    const size_t smem = std::max(k.smem, rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0);
+    if (!allow_smem(k, smem)) return DLC_STATUS_EXECUTION_FAILED;
+    dlcStatus_t st = dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), smem, args);
     if (st != DLC_STATUS_SUCCESS || !p.dgamma) return st;
     return dlc_launch_column_sum(ctx, p.ws, p.dgamma, p.C, (int)r.blocks);
 }
