@@ -61,6 +61,7 @@ DLC_KERNEL_TC_WGRAD = 8
 DLC_KERNEL_POOL_NHWC = 9
 DLC_KERNEL_TC_ROWSTACK = 10
 DLC_KERNEL_GEMM_PAIR = 11
+DLC_KERNEL_FEW_ROWS = 12
 DLC_DEVERR_NONE = 0
 DLC_DEVERR_WAIT_TIMEOUT = 1
 
@@ -70,7 +71,8 @@ KERNEL_NAMES = {DLC_KERNEL_NONE: "none", DLC_KERNEL_FFMA: "ffma",
                 DLC_KERNEL_TC_IM2COL_PAIR: "tc_im2col_pair", DLC_KERNEL_DIRECT: "direct",
                 DLC_KERNEL_TC_WGRAD: "tc_wgrad", DLC_KERNEL_POOL_NHWC: "pool_nhwc",
                 DLC_KERNEL_TC_ROWSTACK: "tc_rowstack",
-                DLC_KERNEL_GEMM_PAIR: "gemm_pair"}
+                DLC_KERNEL_GEMM_PAIR: "gemm_pair",
+                DLC_KERNEL_FEW_ROWS: "few_rows"}
 
 _h = c_void_p          # opaque handle / descriptor
 _ph = POINTER(c_void_p)

@@ -64,6 +64,40 @@ __device__ __forceinline__ void store_elem(void *p, int dt, long long i, float v
         static_cast<unsigned char *>(p)[i] = (unsigned char)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
 
+// Four consecutive channels n .. n+3 of a row, `cols` of which exist; `vec`:
+// the tensor takes four-element accesses (dlc_vec4_rows).
+__device__ __forceinline__ void load4(const RowTensor &t, long long off, int n, int cols, bool vec,
+                                      float (&v)[4]) {
+    if (vec && cols >= 4) {
+        if (t.dt == DLC_DATA_BFLOAT16) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(t.p) + off + n);
+            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + n);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < cols ? load_elem(t.p, t.dt, off + (long long)(n + i) * t.m.cs) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void store4(const RowTensor &t, long long off, long long n, int cols, bool vec,
+                                           const float (&v)[4]) {
+    if (vec && cols >= 4) {
+        if (t.dt == DLC_DATA_BFLOAT16)
+            *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(t.p) + off + n) =
+                make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off + n) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < cols) store_elem(t.p, t.dt, off + (n + i) * t.m.cs, v[i]);
+    }
+}
+
 // Two FP32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     unsigned long long d;

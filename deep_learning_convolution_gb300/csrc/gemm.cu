@@ -28,6 +28,7 @@
 #include <cstring>
 
 #include "channel.cuh"
+#include "gemm.h"
 #include "ptx.cuh"
 
 namespace {
@@ -462,37 +463,6 @@ struct FinishParams {
     int vec;            // y, z and r take 4-element accesses
 };
 
-__device__ __forceinline__ void fin_load4(const RowTensor &t, long long off, int n, int cols, bool vec, float (&v)[4]) {
-    if (vec && cols >= 4) {
-        if (t.dt == DLC_DATA_BFLOAT16) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(t.p) + off + n);
-            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + n);
-            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < cols ? load_elem(t.p, t.dt, off + (long long)(n + i) * t.m.cs) : 0.f;
-    }
-}
-
-__device__ __forceinline__ void fin_store4(const RowTensor &t, long long off, long long n, int cols, bool vec,
-                                           const float (&v)[4]) {
-    if (vec && cols >= 4) {
-        if (t.dt == DLC_DATA_BFLOAT16)
-            *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(t.p) + off + n) =
-                make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off + n) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < cols) store_elem(t.p, t.dt, off + (n + i) * t.m.cs, v[i]);
-    }
-}
-
 // Adds the partial tiles in the order of their ranges and applies the
 // epilogue: four columns of a row a thread.
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishParams f) {
@@ -524,7 +494,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
                 }
                 v[h][j] = s[j];
             }
-            if (g.z.p) fin_store4(g.z, row_off(g.z.m, m), (long long)h * g.N + n, cols, f.vec && (h == 0 || g.N % 4 == 0), v[h]);
+            if (g.z.p) store4(g.z, row_off(g.z.m, m), (long long)h * g.N + n, cols, f.vec && (h == 0 || g.N % 4 == 0), v[h]);
         }
         act_dispatch(g.act, [&](auto act) {
 #pragma unroll
@@ -536,11 +506,11 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
         }
         if (g.r.p) {
             float r[4];
-            fin_load4(g.r, row_off(g.r.m, m), n, cols, f.vec, r);
+            load4(g.r, row_off(g.r.m, m), n, cols, f.vec, r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[0][j] += r[j];
         }
-        fin_store4(g.y, row_off(g.y.m, m), n, cols, f.vec, v[0]);
+        store4(g.y, row_off(g.y.m, m), n, cols, f.vec, v[0]);
     }
 }
 
@@ -589,14 +559,6 @@ bool tma_store_rows(const RowTensor &t, long long rows, int n, int halves) {
     return tma_rows(t, rows, (long long)n * halves) && (halves == 1 || ((long long)n * e) % 16 == 0);
 }
 
-bool vec4_rows(const RowTensor &t) {
-    if (!t.p) return true;
-    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
-    auto mult = [&](long long s) { return (s * e) % (4 * e) == 0; };
-    return t.m.cs == 1 && (uintptr_t)t.p % (4 * e) == 0 &&
-           (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
-}
-
 bool vec16_rows(const RowTensor &t) {
     const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
     auto mult = [&](long long s) { return (s * e) % 16 == 0; };
@@ -604,11 +566,13 @@ bool vec16_rows(const RowTensor &t) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
+constexpr int FEW_ROWS = 128;
+
 struct GemmPlan {
     int bn, nout, splits, m_tiles, n_tiles, num_kb;
     long long a_rows, b_rows;
     int a_ch, b_ch;             // channels of the operands' rows
-    bool pack_a, pack_b;
+    bool pack_a, pack_b, few_rows;
     size_t a_off, b_off, part_off, bytes;
     long long part_ld;
 };
@@ -626,6 +590,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
+    p.few_rows = g.M <= FEW_ROWS && !g.a.trans && !g.b.trans;
     // Tile width and split from a small model of the time, in units of one
     // k-block of a 256-column tile: narrower tiles load more per product, a
     // unit's first loads and last epilogue are not hidden, partial sums cost
@@ -658,7 +623,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     if (p.pack_b) off += packed(p.b_rows, p.b_ch);
     p.part_off = off;
     p.part_ld = ((long long)g.N + 3) / 4 * 4;
-    if (p.splits > 1) off += round256((size_t)p.splits * (g.gated ? 2 : 1) * g.M * p.part_ld * 4);
+    if (p.splits > 1 && !p.few_rows) off += round256((size_t)p.splits * (g.gated ? 2 : 1) * g.M * p.part_ld * 4);
     p.bytes = off;
     return p;
 }
@@ -690,17 +655,6 @@ bool encode(const dlcContext *ctx, CUtensorMap *tm, const RowTensor &t, int nd, 
                                                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return ctx->encode_tiled(tm, dt, (cuuint32_t)nd, t.p, dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A row operand's map: K-major boxes of 128 bytes x `box_rows` rows, or
-// MN-major blocks of 64 channels x 64 rows.
-bool encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperand &o, long long rows, int ch, int box_rows) {
-    RowTensor t = o.t;
-    const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
-    if (rows == 1) t.m.ld = ((long long)ch * e + 15) / 16 * 16 / e;
-    const cuuint64_t dim[2] = {(cuuint64_t)ch, (cuuint64_t)rows};
-    return encode(ctx, tm, t, 2, dim, 0, (cuuint32_t)(GP_LINE / e), (cuuint32_t)(o.trans ? 64 : box_rows),
-                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // An output's map: `halves` planes of [M][N], 32 x 32 blocks.
@@ -748,17 +702,8 @@ int resident_pairs(const dlcContext *ctx, const void *kern, size_t smem) {
     return n;
 }
 
-dlcStatus_t launch_pair(dlcContext *ctx, GemmProblem g, const GemmPlan &pl) {
+dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &pl) {
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
-    const int nb = g.gated ? 2 * g.N : g.N;
-    if (pl.pack_a) {
-        const dlcStatus_t st = pack_rows(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
-        if (st != DLC_STATUS_SUCCESS) return st;
-    }
-    if (pl.pack_b) {
-        const dlcStatus_t st = pack_rows(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
-        if (st != DLC_STATUS_SUCCESS) return st;
-    }
     GpParams p;
     std::memset(&p, 0, sizeof(p));
     p.M = g.M;
@@ -794,8 +739,8 @@ dlcStatus_t launch_pair(dlcContext *ctx, GemmProblem g, const GemmPlan &pl) {
     CUtensorMap ta, tb, ty, tz;
     std::memset(&ty, 0, sizeof(ty));
     std::memset(&tz, 0, sizeof(tz));
-    if (!encode_operand(ctx, &ta, g.a, pl.a_rows, pl.a_ch, GP_ROWS) ||
-        !encode_operand(ctx, &tb, g.b, pl.b_rows, pl.b_ch, pl.bn / 2))
+    if (!dlc_encode_operand(ctx, &ta, g.a, pl.a_rows, pl.a_ch, GP_ROWS) ||
+        !dlc_encode_operand(ctx, &tb, g.b, pl.b_rows, pl.b_ch, pl.bn / 2))
         return DLC_STATUS_EXECUTION_FAILED;
     bool f32_stage = false;
     if (p.raw) {
@@ -832,7 +777,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, GemmProblem g, const GemmPlan &pl) {
     f.part = reinterpret_cast<const float *>(g.ws + pl.part_off);
     f.ld = pl.part_ld;
     f.splits = pl.splits;
-    f.vec = vec4_rows(g.y) && vec4_rows(g.z) && vec4_rows(g.r);
+    f.vec = dlc_vec4_rows(g.y) && dlc_vec4_rows(g.z) && dlc_vec4_rows(g.r);
     const long long items = g.M * (pl.part_ld / 4);
     const long long blocks = std::min<long long>((items + 255) / 256, (long long)ctx->sm_count * 8);
     void *fargs[] = {&f};
@@ -841,8 +786,33 @@ dlcStatus_t launch_pair(dlcContext *ctx, GemmProblem g, const GemmPlan &pl) {
 
 }  // namespace
 
-dlcKernel_t dlc_gemm_variant(const dlcContext *, const GemmProblem &) { return DLC_KERNEL_GEMM_PAIR; }
+// A row operand's map: K-major boxes of 128 bytes x `box_rows` rows, or
+// MN-major blocks of 64 channels x 64 rows.
+bool dlc_encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperand &o, long long rows, int ch, int box_rows) {
+    RowTensor t = o.t;
+    const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    if (rows == 1) t.m.ld = ((long long)ch * e + 15) / 16 * 16 / e;
+    const cuuint64_t dim[2] = {(cuuint64_t)ch, (cuuint64_t)rows};
+    return encode(ctx, tm, t, 2, dim, 0, (cuuint32_t)(GP_LINE / e), (cuuint32_t)(o.trans ? 64 : box_rows),
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
+    return plan_gemm(ctx, g).few_rows ? DLC_KERNEL_FEW_ROWS : DLC_KERNEL_GEMM_PAIR;
+}
 
 size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g) { return plan_gemm(ctx, g).bytes; }
 
-dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g) { return launch_pair(ctx, g, plan_gemm(ctx, g)); }
+dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &pb) {
+    GemmProblem g = pb;
+    const GemmPlan pl = plan_gemm(ctx, g);
+    if (pl.pack_a) {
+        const dlcStatus_t st = pack_rows(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
+        if (st != DLC_STATUS_SUCCESS) return st;
+    }
+    if (pl.pack_b) {
+        const dlcStatus_t st = pack_rows(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
+        if (st != DLC_STATUS_SUCCESS) return st;
+    }
+    return pl.few_rows ? dlc_launch_few_rows(ctx, g) : launch_pair(ctx, g, pl);
+}

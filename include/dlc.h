@@ -162,8 +162,10 @@ typedef enum {
                                      up to 64 filters: filters stacked over output rows as the
                                      MMA's M side, output pixels (per phase q mod 4) as N,
                                      read in place from shifted copies of input rows */
-    DLC_KERNEL_GEMM_PAIR = 11     /* channel operators: tcgen05 products on pairs of SMs, 256 rows
+    DLC_KERNEL_GEMM_PAIR = 11,    /* channel operators: tcgen05 products on pairs of SMs, 256 rows
                                      a tile, operands by TMA */
+    DLC_KERNEL_FEW_ROWS = 12      /* channel operators: tcgen05 products with the filters as the
+                                     MMA's M side, the reduction split over a cluster */
 } dlcKernel_t;
 
 /* Device error codes recorded by kernels (dlcGetLastDeviceError). */
