@@ -6,50 +6,27 @@
 //
 // It reads dy and z once and writes dz once, which bounds it: a warp handles
 // 256 neighbouring channels of a row, eight a thread (16-byte accesses of
-// BF16), eight rows a block at a time, the column sums staying in registers.
+// BF16), a block eight rows at a time; each thread copies its next rows into
+// shared memory asynchronously, and the column sums stay in its registers.
 #include "channel.cuh"
 #include "ptx.cuh"
+#include "row_ring.cuh"
 
 namespace {
 
 using namespace dlc;
 
 constexpr int AG_WARPS = 8;
-
-template <int W>
-__device__ __forceinline__ void ag_load(const RowTensor &t, long long off, int n, float *v) {
-    if (W == 8 && n >= W) {
-        if (t.dt == DLC_DATA_BFLOAT16) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-            const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off);
-#pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-                const float4 a = f[i];
-                v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = i < n ? load_elem(t.p, t.dt, off + i * t.m.cs) : 0.f;
-    }
-}
+constexpr int AG_BLOCKS = 3;  // blocks an SM holds
+constexpr int AG_RING = 4;    // rows of the ring (one in use, three in flight)
 
 // dz is dense BF16 with rows of a multiple of 16 bytes, so only the vector's
 // own channels decide between the two stores.
 template <int W>
-__device__ __forceinline__ void ag_store(const RowTensor &t, long long off, int n, const float *v) {
-    if (W == 8 && n >= W) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void ag_store(const RowTensor &t, long long off, int n, const float (&v)[W]) {
+    if (W == 8 && n == W) {
+        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -57,73 +34,89 @@ __device__ __forceinline__ void ag_store(const RowTensor &t, long long off, int 
     }
 }
 
-// W = 8: vectors; W = 1: single elements of any strides and alignment.
-template <int W, int ACT, bool GATED>
-__device__ __forceinline__ void ag_rows(const ActGradProblem &p, float (&sum)[2][8]) {
+// A vector's channels (W = 8), or one element at any stride (W = 1).  BF: dy and
+// z in BF16, vectors.
+template <int W, int ACT, bool GATED, bool SUM, bool BF>
+__device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, float (&sum)[GATED ? 2 : 1][W]) {
+    constexpr bool READS_Z = GATED || ACT != DLC_ACTIVATION_IDENTITY;
+    constexpr int T = 1 + (READS_Z ? 1 : 0) + (GATED ? 1 : 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = ((int)blockIdx.x * 32 + lane) * W, n = p.N - c;
-    for (long long row = (long long)blockIdx.y * AG_WARPS + warp; row < p.rows; row += (long long)gridDim.y * AG_WARPS) {
-        if (n <= 0) continue;
-        float dy[W], z[W], u[W], a[W], b[W];
-        ag_load<W>(p.dy, row_off(p.dy.m, row) + (long long)c * p.dy.m.cs, n, dy);
-        if (p.z.p) {
-            const long long zo = row_off(p.z.m, row);
-            ag_load<W>(p.z, zo + (long long)c * p.z.m.cs, n, z);
-            if (GATED) ag_load<W>(p.z, zo + (long long)(p.N + c) * p.z.m.cs, n, u);
+    const Cols<W, 1> cols((int)blockIdx.x * 32 + lane, 0, p.N);
+    const int n = cols.n[0];
+    const long long c = cols.c[0];
+    const long long step = (long long)gridDim.y * AG_WARPS;
+    long long row = (long long)blockIdx.y * AG_WARPS + warp, ahead = row;
+    if (n <= 0) return;
+    RowWalk wy(p.dy.m, row, step), wz(p.z.m, row, step), wd(p.dz.m, row, step);
+    Rows<W, 1, BF, T, AG_RING> rows;
+    rows.start(ring);
+    const long long up = (long long)p.N * p.z.m.cs;
+    auto fetch = [&]() {
+        if (ahead < p.rows) {
+            rows.fetch(p.dy, 0, wy.at(p.dy.m, ahead), cols);
+            if constexpr (READS_Z) rows.fetch(p.z, 1, wz.at(p.z.m, ahead), cols);
+            if constexpr (GATED) rows.fetch(p.z, 2, wz.at(p.z.m, ahead) + up, cols);
         }
+        rows.commit();
+        ahead += step;
+        wy.next();
+        wz.next();
+    };
+    for (int i = 0; i < rows.AHEAD; ++i) fetch();
+    for (; row < p.rows; row += step, wd.next()) {
+        float f[T][W];
+        rows.take(f);
+        fetch();
+        float b[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            if (GATED) {
-                float f, df;
-                act_both<ACT>(z[i], f, df);
-                a[i] = dy[i] * u[i] * df;
-                b[i] = dy[i] * f;
-                sum[1][i] += b[i];
-            } else if (ACT == DLC_ACTIVATION_IDENTITY) {
-                a[i] = dy[i];
-            } else {
-                float f, df;
-                act_both<ACT>(z[i], f, df);
-                a[i] = dy[i] * df;
+            float a = 0.f, da = 1.f;
+            if constexpr (READS_Z) act_both<ACT>(f[1][i], a, da);
+            if constexpr (GATED) {
+                b[i] = f[0][i] * a;
+                f[0][i] *= f[2][i] * da;
+                if (SUM) sum[1][i] += b[i];
+            } else if constexpr (READS_Z) {
+                f[0][i] *= da;
             }
-            sum[0][i] += a[i];
+            if (SUM) sum[0][i] += f[0][i];
         }
         if (p.dz.p) {
-            const long long zo = row_off(p.dz.m, row);
-            ag_store<W>(p.dz, zo + c, n, a);
-            if (GATED) ag_store<W>(p.dz, zo + p.N + c, n, b);
+            const long long zo = wd.at(p.dz.m, row) + c;
+            ag_store<W>(p.dz, zo, n, f[0]);
+            if constexpr (GATED) ag_store<W>(p.dz, zo + p.N, n, b);
         }
     }
 }
 
-template <int W>
-__global__ void __launch_bounds__(AG_WARPS * 32) act_grad_kernel(const __grid_constant__ ActGradProblem p) {
+template <int W, bool GATED, bool SUM, bool BF>
+__global__ void __launch_bounds__(AG_WARPS * 32, AG_BLOCKS) act_grad_kernel(const __grid_constant__ ActGradProblem p) {
     griddep_launch_dependents();
-    __shared__ float part[AG_WARPS][32 * W];
-    float sum[2][8];
-    for (int h = 0; h < 2; ++h)
-        for (int i = 0; i < 8; ++i) sum[h][i] = 0.f;
-    griddep_wait();
-    act_dispatch(p.act, [&](auto act) {
-        if (p.gated)
-            ag_rows<W, decltype(act)::value, true>(p, sum);
-        else
-            ag_rows<W, decltype(act)::value, false>(p, sum);
-    });
-    if (!p.dbias) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int width = p.gated ? 2 * p.N : p.N;
-    for (int h = 0; h < (p.gated ? 2 : 1); ++h) {
-        __syncthreads();
+    extern __shared__ uint4 ring_s[];
+    float sum[GATED ? 2 : 1][W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) part[warp][lane * W + i] = sum[h][i];
-        __syncthreads();
-        for (int j = threadIdx.x; j < 32 * W; j += AG_WARPS * 32) {
-            const int c = (int)blockIdx.x * 32 * W + j;
-            if (c >= p.N) continue;
-            float s = 0.f;
-            for (int w = 0; w < AG_WARPS; ++w) s += part[w][j];
-            p.ws[(long long)blockIdx.y * width + h * p.N + c] = s;
+    for (int h = 0; h < (GATED ? 2 : 1); ++h)
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum[h][i] = 0.f;
+    griddep_wait();
+    act_dispatch(p.act, [&](auto act) { ag_rows<W, decltype(act)::value, GATED, SUM, BF>(p, smem_u32(ring_s), sum); });
+    if constexpr (SUM) {
+        __shared__ float part[AG_WARPS][32 * W];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        constexpr int HALVES = GATED ? 2 : 1;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < W; ++i) part[warp][lane * W + i] = sum[h][i];
+            __syncthreads();
+            for (int j = threadIdx.x; j < 32 * W; j += AG_WARPS * 32) {
+                const int c = (int)blockIdx.x * 32 * W + j;
+                if (c >= p.N) continue;
+                float s = 0.f;
+                for (int w = 0; w < AG_WARPS; ++w) s += part[w][j];
+                p.ws[(long long)blockIdx.y * HALVES * p.N + h * p.N + c] = s;
+            }
         }
     }
 }
@@ -141,6 +134,12 @@ bool ag_vec(const RowTensor &t, int n) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
+template <int W, bool BF>
+const void *ag_kernel(const ActGradProblem &p) {
+    if (p.gated) return p.dbias ? (const void *)act_grad_kernel<W, true, true, BF> : (const void *)act_grad_kernel<W, true, false, BF>;
+    return p.dbias ? (const void *)act_grad_kernel<W, false, true, BF> : (const void *)act_grad_kernel<W, false, false, BF>;
+}
+
 AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
     AgPlan g;
     // a gated row's second half starts N channels in: its vectors need that aligned too
@@ -148,7 +147,7 @@ AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
     g.w = ag_vec(p.dy, 0) && ag_vec(p.z, n) && ag_vec(p.dz, n) ? 8 : 1;
     g.gx = (unsigned)((p.N + 32 * g.w - 1) / (32 * g.w));
     const long long strips = (p.rows + AG_WARPS - 1) / AG_WARPS;
-    const long long want = std::max<long long>(1, (long long)ctx->sm_count * 8 / g.gx);
+    const long long want = std::max<long long>(1, (long long)ctx->sm_count * AG_BLOCKS / g.gx);
     g.gy = (unsigned)std::min(std::min(strips, want), 65535LL);
     return g;
 }
@@ -158,7 +157,7 @@ AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
 size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p) {
     // either vector width's number of row strips
     const long long strips = (p.rows + AG_WARPS - 1) / AG_WARPS;
-    const long long want = std::max<long long>(1, (long long)ctx->sm_count * 8 / std::max(1, (p.N + 255) / 256));
+    const long long want = std::max<long long>(1, (long long)ctx->sm_count * AG_BLOCKS / std::max(1, (p.N + 255) / 256));
     return (size_t)std::min(std::min(strips, want), 65535LL) * (p.gated ? 2 : 1) * p.N * sizeof(float);
 }
 
@@ -166,8 +165,15 @@ dlcStatus_t dlc_launch_act_grad(dlcContext *ctx, const ActGradProblem &pb) {
     const AgPlan g = ag_plan(ctx, pb);
     ActGradProblem p = pb;
     void *args[] = {&p};
-    const void *kern = g.w == 8 ? (const void *)act_grad_kernel<8> : (const void *)act_grad_kernel<1>;
-    const dlcStatus_t st = dlc_launch(ctx, kern, dim3(g.gx, g.gy), dim3(AG_WARPS * 32), 0, args);
+    const bool bf = g.w == 8 && p.dy.dt == DLC_DATA_BFLOAT16 && (!p.z.p || p.z.dt == DLC_DATA_BFLOAT16);
+    const void *kern = bf ? ag_kernel<8, true>(p) : g.w == 8 ? ag_kernel<8, false>(p) : ag_kernel<1, false>(p);
+    const size_t smem = bf ? (size_t)AG_RING * (p.gated ? 3 : p.z.p ? 2 : 1) * 16 * AG_WARPS * 32 : 0;
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return DLC_STATUS_EXECUTION_FAILED;
+    }
+    const dlcStatus_t st = dlc_launch(ctx, kern, dim3(g.gx, g.gy), dim3(AG_WARPS * 32), smem, args);
     if (st != DLC_STATUS_SUCCESS || !p.dbias) return st;
     return dlc_launch_column_sum(ctx, p.ws, p.dbias, p.gated ? 2 * p.N : p.N, (int)g.gy);
 }

@@ -7,13 +7,13 @@
 // moves 16 KiB of filters for 2 KiB and up of rows and pads neither much.  A
 // gated tile takes 128 gate and 128 up filters into two accumulators.  Where
 // there are fewer tiles than SMs, a cluster of up to eight CTAs shares a tile,
-// each with a range of the reduction; the partial sums stay in shared memory
-// and every CTA adds up its share of the rows over the cluster, always in the
-// same order, and applies the epilogue.  Nothing but the outputs is written to
+// each with a range of the reduction; the partial sums stay in shared memory,
+// every CTA adds up its share of the rows over the cluster, always in the same
+// order, and applies the epilogue.  Nothing but the outputs is written to
 // memory and there is one launch.
 //
-// Roles (8 warps): warp 0 lane 0 loads, warp 1 lane 0 issues the MMAs; all warps
-// read the accumulators (two per quarter of the TMEM lanes) and join the partial
+// Roles (16 warps): warp 0 lane 0 loads, warp 1 lane 0 issues the MMAs; all warps
+// read the accumulators (four per quarter of the TMEM lanes) and join the partial
 // sums, a warp a row, a lane four filters.  Every wait is bounded.
 #include <cstring>
 
@@ -28,9 +28,9 @@ using namespace dlc;
 constexpr int FR_FILTERS = 128;
 constexpr int FR_LINE = 128;                        // bytes of an operand row per k-block
 constexpr int FR_W_BYTES = FR_FILTERS * FR_LINE;    // 16 KiB
-constexpr int FR_THREADS = 256;
+constexpr int FR_THREADS = 512;
 constexpr int FR_MAX_STAGES = 12, FR_MAX_SPLITS = 8;  // (a cluster of eight is portable)
-constexpr int FR_SMEM = 212 * 1024, FR_BAR_AREA = 512;
+constexpr int FR_SMEM = 226 * 1024;
 
 struct FrParams {
     long long M;
@@ -44,6 +44,77 @@ struct FrParams {
     int *err;
     unsigned long long timeout_ns;
 };
+
+// Adds up the partial sums of rows j0 .. j0+count-1 of a tile over the cluster,
+// in the order of their ranges, and applies the epilogue: a warp a row, a lane
+// four filters.  `sums`: a CTA's partial sums, [half][row][filter], at the same
+// address in each.  A launch runs this code once or a few times, so fetching it
+// counts: it is kept short (unrolled over rows it took 2.1 us a pass of four
+// rows, most of it instruction fetches).
+template <bool GATED>
+__device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int split, long long m0, int n, int j0,
+                                        int count, const float (&sb)[GATED ? 2 : 1][4],
+                                        const float (&bias)[GATED ? 2 : 1][4]) {
+    constexpr int HALVES = GATED ? 2 : 1, AT_ONCE = 4;  // ranges loaded before they are added
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = p.N - n;
+    const uint32_t half = (uint32_t)p.rows * FR_FILTERS * 4u;
+#pragma unroll 1
+    for (int j = warp; j < count; j += FR_THREADS / 32) {
+        const long long m = m0 + j0 + j;
+        const float sa = p.sa ? __ldg(p.sa + m) : 1.f;
+        const uint32_t at = sums + ((uint32_t)(j0 + j) * FR_FILTERS + 4u * (uint32_t)lane) * 4u;
+        float v[HALVES][4];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = 0.f;
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.splits; s0 += AT_ONCE) {
+            float4 q[AT_ONCE][HALVES];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    const uint32_t a = at + (uint32_t)h * half;
+                    if (s0 + i == split)
+                        q[i][h] = ld_shared_f32x4(a);
+                    else if (s0 + i < p.splits)
+                        q[i][h] = ld_cluster_f32x4(mapa_shared(a, (uint32_t)(s0 + i)));
+                }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+                    if (s0 + i < p.splits)
+                        v[h][0] += q[i][h].x, v[h][1] += q[i][h].y, v[h][2] += q[i][h].z, v[h][3] += q[i][h].w;
+        }
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = fmaf(v[h][i], sa * sb[h][i], bias[h][i]);
+        if (p.z.p) {
+            const long long zo = row_off(p.z.m, m);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) store4(p.z, zo, (long long)h * p.N + n, cols, h ? p.z2_vec : p.z_vec, v[h]);
+        }
+        float y[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
+        act_dispatch(p.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = act_f<decltype(act)::value>(y[i]);
+        });
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] *= v[HALVES - 1][i];
+        }
+        if (p.r.p) {
+            float w[4];
+            load4(p.r, row_off(p.r.m, m), n, cols, p.r_vec, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] += w[i];
+        }
+        store4(p.y, row_off(p.y.m, m), n, cols, p.y_vec, y);
+    }
+}
 
 template <bool E4M3, bool GATED>
 __global__ void __launch_bounds__(FR_THREADS, 1)
@@ -64,7 +135,17 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     const long long m0 = (long long)blockIdx.y * p.rows;
     const int kb0 = (int)((long long)p.num_kb * split / p.splits);
     const int kb1 = (int)((long long)p.num_kb * (split + 1) / p.splits);
+    auto load = [&](int kb, int stage) {
+        mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
+        const uint32_t dst = smem + (uint32_t)stage * p.stage_bytes;
+        tma_load_2d(dst, &tmW, &full[stage], kb * BK, n0);
+        if (GATED) tma_load_2d(dst + FR_W_BYTES, &tmW, &full[stage], kb * BK, p.N + n0);
+        tma_load_2d(dst + HALVES * FR_W_BYTES, &tmX, &full[stage], kb * BK, (int)m0);
+    };
+    const int first = min(kb1, kb0 + p.stages);  // the blocks that need no free stage
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmX);
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&full[i], 1u);
             mbar_init(&empty[i], 1u);
@@ -72,8 +153,8 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
         mbar_init(&done, 1u);
         abort_flag = 0;
         fence_mbar_init();
-        prefetch_tmap(&tmW);
-        prefetch_tmap(&tmX);
+        griddep_wait();
+        for (int kb = kb0; kb < first; ++kb) load(kb, kb - kb0);
     }
     if (warp == 1) {
         tmem_alloc(&tmem_slot, p.tmem_cols);
@@ -87,15 +168,11 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     griddep_wait();
 
     if (warp == 0 && lane == 0) {
-        int stage = 0;
-        uint32_t ph = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        int stage = first - kb0 == p.stages ? 0 : first - kb0;
+        uint32_t ph = 1;
+        for (int kb = first; kb < kb1; ++kb) {
             if (!mbar_wait(&empty[stage], ph ^ 1u, ctl, 31)) break;
-            mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-            const uint32_t dst = smem + (uint32_t)stage * p.stage_bytes;
-            tma_load_2d(dst, &tmW, &full[stage], kb * BK, n0);
-            if (GATED) tma_load_2d(dst + FR_W_BYTES, &tmW, &full[stage], kb * BK, p.N + n0);
-            tma_load_2d(dst + HALVES * FR_W_BYTES, &tmX, &full[stage], kb * BK, (int)m0);
+            load(kb, stage);
             if (++stage == p.stages) stage = 0, ph ^= 1u;
         }
     } else if (warp == 1 && lane == 0) {
@@ -155,75 +232,35 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     __syncwarp();
     tc_fence_after_sync();
     // partial sums to shared memory, where the operands were: [half][row][filter]
-    const uint32_t plane = (uint32_t)p.rows * FR_FILTERS * 4u;
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h)
-        for (int c = 16 * (warp >> 2); c < p.rows; c += 32) {
-            const int quad = warp & 3;
+    {
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t mine = smem + (uint32_t)((warp & 3) * 32 + lane) * 4u;
+        const int total = HALVES * p.rows;  // accumulator columns (a multiple of 16)
+#pragma unroll 1
+        for (int c = 16 * (warp >> 2); c < total; c += 4 * FR_THREADS / 32) {
             uint32_t v[16];
-            tmem_ld_32x32b_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * p.rows + c), v);
+            tmem_ld_32x32b_x16(lanes + (uint32_t)c, v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem + (uint32_t)h * plane +
-                             ((uint32_t)(c + i) * FR_FILTERS + (uint32_t)(quad * 32 + lane)) * 4u), "r"(v[i]) : "memory");
-        }
-    __syncwarp();
-    tc_fence_before_sync();
-    cluster_sync();
-    tc_fence_after_sync();
-    good = good && abort_flag == 0;
-    // this CTA's rows of the tile, a warp a row
-    const int per = (p.rows + p.splits - 1) / p.splits;
-    const int j1 = min(min(p.rows, (split + 1) * per), (int)min((long long)p.rows, p.M - m0));
-    if (good && cols > 0) {
-        for (int j = split * per + warp; j < j1; j += FR_THREADS / 32) {
-            const long long m = m0 + j;
-            const float sa = p.sa ? __ldg(p.sa + m) : 1.f;
-            float v[HALVES][4];
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                const uint32_t at = smem + (uint32_t)h * plane + ((uint32_t)j * FR_FILTERS + (uint32_t)f) * 4u;
-                float4 q[FR_MAX_SPLITS];
-#pragma unroll
-                for (int s = 0; s < FR_MAX_SPLITS; ++s)
-                    if (s < p.splits) q[s] = ld_cluster_f32x4(mapa_shared(at, (uint32_t)s));
-                float t[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-                for (int s = 1; s < FR_MAX_SPLITS; ++s)
-                    if (s < p.splits) t[0] += q[s].x, t[1] += q[s].y, t[2] += q[s].z, t[3] += q[s].w;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[h][i] = fmaf(t[i], sa * sb[h][i], bias[h][i]);
-            }
-            if (p.z.p) {
-                const long long zo = row_off(p.z.m, m);
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h) store4(p.z, zo, (long long)h * p.N + n, cols, h ? p.z2_vec : p.z_vec, v[h]);
-            }
-            float y[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
-            act_dispatch(p.act, [&](auto act) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = act_f<decltype(act)::value>(y[i]);
-            });
-            if (GATED) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] *= v[HALVES - 1][i];
-            }
-            if (p.r.p) {
-                float r[4];
-                load4(p.r, row_off(p.r.m, m), n, cols, p.r_vec, r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] += r[i];
-            }
-            store4(p.y, row_off(p.y.m, m), n, cols, p.y_vec, y);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)(c + i) * FR_FILTERS * 4u), "r"(v[i]) : "memory");
         }
     }
-    __syncwarp();
     tc_fence_before_sync();
-    cluster_sync();  // no CTA leaves while another reads its partial sums
-    tc_fence_after_sync();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();  // the cluster's partial sums are in place
+    good = good && abort_flag == 0;
+    const int per = (p.rows + p.splits - 1) / p.splits, j0 = split * per;
+    const int count = (int)min((long long)min(per, p.rows - j0), p.M - m0 - j0);
+    if (good && cols > 0) fr_join<GATED>(p, smem, split, m0, n, j0, count, sb, bias);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();  // no CTA leaves while another reads its partial sums
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
+
+size_t own_bytes(bool gated, int rows) { return (size_t)(gated ? 2 : 1) * FR_FILTERS * 4 * rows; }
 
 }  // namespace
 
@@ -234,6 +271,7 @@ FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g) {
     p.rows = (int)std::min<long long>(FR_FILTERS, (g.M + 15) / 16 * 16);
     p.filter_tiles = (g.N + FR_FILTERS - 1) / FR_FILTERS;
     p.row_tiles = (int)((g.M + p.rows - 1) / p.rows);
+    // more CTAs a tile while SMs are idle, each with two k-blocks at least
     const long long tiles = (long long)p.filter_tiles * p.row_tiles;
     p.splits = 1;
     while (p.splits < FR_MAX_SPLITS && tiles * (p.splits + 1) <= ctx->sm_count && (p.splits + 1) * 2 <= p.num_kb) ++p.splits;
@@ -253,8 +291,11 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
     p.rows = pl.rows;
     const int halves = g.gated ? 2 : 1;
     p.stage_bytes = (uint32_t)(halves * FR_W_BYTES + pl.rows * FR_LINE);
+    // (stages carry the filters' stream: one row of 2048 -> 2 x 8192 took 15.4 us
+    // with six of them, 16.4 with five)
     p.stages = std::min(FR_MAX_STAGES, (FR_SMEM - 1024) / (int)p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, (pl.num_kb + pl.splits - 1) / pl.splits));
+    const size_t smem = 1024 + std::max((size_t)p.stages * p.stage_bytes, own_bytes(g.gated != 0, pl.rows));
     p.sa = g.sa;
     p.sb = g.sb;
     p.bias = g.bias;
@@ -276,8 +317,6 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
     if (!dlc_encode_operand(ctx, &tw, g.b, nb, (int)g.K, FR_FILTERS) ||
         !dlc_encode_operand(ctx, &tx, g.a, g.M, (int)g.K, pl.rows))
         return DLC_STATUS_EXECUTION_FAILED;
-    const size_t need = std::max((size_t)p.stages * p.stage_bytes, (size_t)halves * pl.rows * FR_FILTERS * 4);
-    const size_t smem = need + 1024;
     const void *kern = g.gated ? (e4m3 ? (const void *)gemm_rows_kernel<true, true> : (const void *)gemm_rows_kernel<false, true>)
                                : (e4m3 ? (const void *)gemm_rows_kernel<true, false> : (const void *)gemm_rows_kernel<false, false>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {

@@ -534,6 +534,13 @@ __device__ __forceinline__ void mbar_arrive_tmem_free(uint32_t caddr) {
                  : "memory");
 }
 
+// The two halves of a cluster barrier: every thread of every CTA arrives, then
+// waits (warp-converged; other work may stand between them).
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
@@ -545,6 +552,15 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(caddr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
                  : "memory");
     return v;
 }

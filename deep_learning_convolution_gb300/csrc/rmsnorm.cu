@@ -14,6 +14,7 @@
 // scale comes from the same reduction as the sum of squares.
 #include "channel.cuh"
 #include "ptx.cuh"
+#include "row_ring.cuh"
 
 namespace {
 
@@ -26,127 +27,11 @@ constexpr int RMS_MAX_WARPS = 32;
 // Blocks of 256 threads an SM is to hold (what the registers are limited for).
 constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 
-// E = V * W values of one row held by a thread: V vectors of W consecutive
-// channels.  W = 8 (16-byte aligned) or 1.
-template <int W, int V>
-struct Cols {
-    int c[V];   // first channel of each vector, 0 where the vector is past the row
-    int n[V];   // channels of it that exist, 0 .. W
-    __device__ __forceinline__ Cols(int t, int tpr, int C) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int at = (t + j * tpr) * W;
-            n[j] = min(max(C - at, 0), W);
-            c[j] = n[j] ? at : 0;
-        }
-    }
-};
-
-// V vectors of a row as FP32; a partial vector is read element by element, so
-// nothing past the row is touched.
-template <int W, int V>
-__device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float *v = f + j * W;
-        if (W == 8 && k.n[j] == W) {
-            if (t.dt == DLC_DATA_BFLOAT16) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
-            } else {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
-#pragma unroll
-                for (int i = 0; i < W / 4; ++i) {
-                    const float4 a = p[i];
-                    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = i < k.n[j] ? load_elem(t.p, t.dt, off + k.c[j] + i) : 0.f;
-        }
-    }
-}
-
-// A thread's next rows of T tensors.  BF (all of them BF16, W = 8): copied
-// asynchronously into a ring of S rows in shared memory, of which a thread
-// reads back only what it copied itself (no barrier), so S - 1 rows of every
-// thread are in flight; otherwise one row ahead, in registers.
-template <int W, int V, bool BF, int T, int S>
-struct Rows {
-    float next[T][V * W];
-    static constexpr int AHEAD = 1;
-    __device__ __forceinline__ void start(uint32_t) {}
-    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<W, V> &cols) {
-        load_row<W, V>(t, off, cols, next[k]);
-    }
-    __device__ __forceinline__ void commit() {}
-    __device__ __forceinline__ void take(float (&f)[T][V * W]) {
-#pragma unroll
-        for (int k = 0; k < T; ++k)
-#pragma unroll
-            for (int i = 0; i < V * W; ++i) f[k][i] = next[k][i];
-    }
-    static size_t smem(int) { return 0; }
-};
-
-template <int V, int T, int S>
-struct Rows<8, V, true, T, S> {
-    uint32_t base, put, get, vec, row;  // this thread's slot 0, the rows to fill and to read, bytes between vectors / rows
-    static constexpr int AHEAD = S - 1;
-    __device__ __forceinline__ void start(uint32_t smem) {
-        base = smem + threadIdx.x * 16u;
-        vec = 16u * blockDim.x;
-        row = (uint32_t)(T * V) * vec;
-        put = get = 0;
-    }
-    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<8, V> &cols) {
-        const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
-#pragma unroll
-        for (int j = 0; j < V; ++j) cp_async_16(base + put + (uint32_t)(k * V + j) * vec, p + cols.c[j], 2u * (uint32_t)cols.n[j]);
-    }
-    __device__ __forceinline__ void commit() {
-        cp_async_commit();
-        put = put == row * (S - 1) ? 0 : put + row;
-    }
-    __device__ __forceinline__ void take(float (&f)[T][V * 8]) {
-        cp_async_wait<S - 2>();
-#pragma unroll
-        for (int k = 0; k < T; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(base + get + (uint32_t)(k * V + j) * vec)
-                             : "memory");
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 u = unpack_bf16(w[i]);
-                    f[k][8 * j + 2 * i] = u.x, f[k][8 * j + 2 * i + 1] = u.y;
-                }
-            }
-        get = get == row * (S - 1) ? 0 : get + row;
-    }
-    static size_t smem(int threads) { return (size_t)S * T * V * 16 * threads; }
-};
-
 // Rows of the ring.  Measured, 100352 x 512 forward / 25088 x 1024 backward, BF16:
 // 3 rows at 4 / 2 blocks an SM 74.5 / 40.0 us; 4 rows 77.6 / 41.1; one row ahead
 // in registers 109 us forward.
 template <int MAXT>
 constexpr int ring_rows() { return MAXT > 512 ? 2 : 3; }
-
-// Row offsets of one tensor along a thread's rows: added up where the rows
-// have one pitch, worked out from n, h and w otherwise.
-struct RowWalk {
-    long long off, inc;
-    __device__ __forceinline__ RowWalk(const RowMap &m, long long row, long long step) : off(row * m.ld), inc(step * m.ld) {}
-    __device__ __forceinline__ long long at(const RowMap &m, long long row) const { return m.uniform ? off : row_off(m, row); }
-    __device__ __forceinline__ void next() { off += inc; }
-};
 
 template <int W>
 __device__ __forceinline__ void store_vec(const RowTensor &t, long long off, int n, const float *v) {
@@ -497,22 +382,24 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
     }
 }
 
-// out[c] = the sum of the blocks' partial rows, in a fixed order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float *ws, float *out, int C, int blocks) {
+// out[c] = the sum of the blocks' partial rows, in a fixed order: 32 columns a
+// block, the partial rows dealt to its 32 warps.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *ws, float *out, int C, int blocks) {
     griddep_launch_dependents();
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (int)blockIdx.x * 32 + lane;
     griddep_wait();
     float s = 0.f;
-    if (c < C)
-        for (int b = warp; b < blocks; b += 8) s += ws[(long long)b * C + c];
+    if (c < C) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += 32) s += ws[(long long)b * C + c];
+    }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < C) {
-        for (int i = 1; i < 8; ++i) s += part[i][lane];
-        out[c] = s;
-    }
+    s = part[lane][warp];  // column `warp`
+    for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && (int)blockIdx.x * 32 + warp < C) out[(int)blockIdx.x * 32 + warp] = s;
 }
 
 // ---- host side ---------------------------------------------------------------
@@ -654,5 +541,5 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
 
 dlcStatus_t dlc_launch_column_sum(dlcContext *ctx, const float *ws, float *out, int C, int blocks) {
     void *args[] = {&ws, &out, &C, &blocks};
-    return dlc_launch(ctx, (const void *)column_sum_kernel, dim3((unsigned)((C + 31) / 32)), dim3(256), 0, args);
+    return dlc_launch(ctx, (const void *)column_sum_kernel, dim3((unsigned)((C + 31) / 32)), dim3(1024), 0, args);
 }

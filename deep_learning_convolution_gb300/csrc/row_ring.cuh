@@ -1,0 +1,126 @@
+// row_ring.cuh -- how the row-wise kernels read: vectors of a row per thread,
+// the next rows prefetched, offsets that step from row to row.
+#pragma once
+
+#include "channel.cuh"
+#include "ptx.cuh"
+
+namespace dlc {
+
+// E = V * W values of one row held by a thread: V vectors of W consecutive
+// channels.  W = 8 (contiguous, 16-byte aligned) or 1 (any stride).
+template <int W, int V>
+struct Cols {
+    int c[V];   // first channel of each vector, 0 where the vector is past the row
+    int n[V];   // channels of it that exist, 0 .. W
+    __device__ __forceinline__ Cols(int t, int tpr, int C) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int at = (t + j * tpr) * W;
+            n[j] = min(max(C - at, 0), W);
+            c[j] = n[j] ? at : 0;
+        }
+    }
+};
+
+// V vectors of a row as FP32; a partial vector is read element by element, so
+// nothing past the row is touched.
+template <int W, int V>
+__device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float *v = f + j * W;
+        if (W == 8 && k.n[j] == W) {
+            if (t.dt == DLC_DATA_BFLOAT16) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
+            } else {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const float4 a = p[i];
+                    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i < k.n[j] ? load_elem(t.p, t.dt, off + (k.c[j] + i) * t.m.cs) : 0.f;
+        }
+    }
+}
+
+// A thread's next rows of T tensors.  BF (all of them BF16, W = 8): copied
+// asynchronously into a ring of S rows in shared memory, of which a thread
+// reads back only what it copied itself (no barrier), so S - 1 rows of every
+// thread are in flight; otherwise one row ahead, in registers.
+template <int W, int V, bool BF, int T, int S>
+struct Rows {
+    float next[T][V * W];
+    static constexpr int AHEAD = 1;
+    __device__ __forceinline__ void start(uint32_t) {}
+    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<W, V> &cols) {
+        load_row<W, V>(t, off, cols, next[k]);
+    }
+    __device__ __forceinline__ void commit() {}
+    __device__ __forceinline__ void take(float (&f)[T][V * W]) {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int i = 0; i < V * W; ++i) f[k][i] = next[k][i];
+    }
+    static size_t smem(int) { return 0; }
+};
+
+template <int V, int T, int S>
+struct Rows<8, V, true, T, S> {
+    uint32_t base, put, get, vec, row;  // this thread's slot 0, the rows to fill and to read, bytes between vectors / rows
+    static constexpr int AHEAD = S - 1;
+    __device__ __forceinline__ void start(uint32_t smem) {
+        base = smem + threadIdx.x * 16u;
+        vec = 16u * blockDim.x;
+        row = (uint32_t)(T * V) * vec;
+        put = get = 0;
+    }
+    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<8, V> &cols) {
+        const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
+#pragma unroll
+        for (int j = 0; j < V; ++j) cp_async_16(base + put + (uint32_t)(k * V + j) * vec, p + cols.c[j], 2u * (uint32_t)cols.n[j]);
+    }
+    __device__ __forceinline__ void commit() {
+        cp_async_commit();
+        put = put == row * (S - 1) ? 0 : put + row;
+    }
+    __device__ __forceinline__ void take(float (&f)[T][V * 8]) {
+        cp_async_wait<S - 2>();
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(base + get + (uint32_t)(k * V + j) * vec)
+                             : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = unpack_bf16(w[i]);
+                    f[k][8 * j + 2 * i] = u.x, f[k][8 * j + 2 * i + 1] = u.y;
+                }
+            }
+        get = get == row * (S - 1) ? 0 : get + row;
+    }
+    static size_t smem(int threads) { return (size_t)S * T * V * 16 * threads; }
+};
+
+// Row offsets of one tensor along a thread's rows: added up where the rows
+// have one pitch, worked out from n, h and w otherwise.
+struct RowWalk {
+    long long off, inc;
+    __device__ __forceinline__ RowWalk(const RowMap &m, long long row, long long step) : off(row * m.ld), inc(step * m.ld) {}
+    __device__ __forceinline__ long long at(const RowMap &m, long long row) const { return m.uniform ? off : row_off(m, row); }
+    __device__ __forceinline__ void next() { off += inc; }
+};
+
+}  // namespace dlc
