@@ -16,9 +16,10 @@
 // contiguous, the tensor core's MN-major form, so nothing is transposed in
 // memory.
 //
-// Few tiles leave most pairs idle: the reduction is then split into ranges
-// whose FP32 partial tiles go to the workspace, and a second kernel adds them
-// in a fixed order and applies the epilogue.
+// The tiles of a last wave that would leave most pairs idle (all tiles, where
+// there are few) have their reduction split into ranges whose FP32 partial tiles
+// go to the workspace; a second kernel adds them in a fixed order and applies the
+// epilogue.
 //
 // Roles (11 warps a CTA): warp 0 lane 0 loads a, warp 2 lane 0 loads b, warp 1
 // lane 0 of the leader issues the MMAs into one of two TMEM accumulators,
@@ -48,8 +49,8 @@ struct GpParams {
     int N, act;
     int BN, nout;                 // accumulator columns of a tile, outputs of a tile (gated: BN / 2)
     int stages, num_kb;
-    int m_tiles, n_tiles, tiles, splits, units;
-    int raw;                      // FP32 partial tiles to the workspace (splits > 1), no epilogue
+    int m_tiles, n_tiles, units;
+    int full_tiles, splits;       // tiles from full_tiles on: `splits` units each, FP32 partial sums, no epilogue
     uint32_t b_stage;             // bytes of one CTA's half of b per stage
     int b_atoms;                  // MN-major b: 64-index blocks per CTA
     uint32_t idesc, tmem_cols, acc_stride;
@@ -63,21 +64,33 @@ struct GpParams {
 
 struct GpUnit {
     long long m0;
-    int nt, split, kb0, kb1;
+    int nt, plane, kb0, kb1;  // plane: of the partial sums, or -1 for a whole tile
 };
 
-// Unit u: a tile (tiles in groups of eight row blocks, so that the pairs that
-// run together share rows of both operands in the L2) and a range of k-blocks.
+// Rows and column tile of tile t: groups of eight row blocks, so that the pairs
+// that run together share rows of both operands in the L2.
+__host__ __device__ __forceinline__ void gp_tile(int t, int m_tiles, int n_tiles, long long &m0, int &nt) {
+    const int per = 8 * n_tiles, grp = t / per, in = t - grp * per;
+    const int rows = m_tiles - grp * 8 < 8 ? m_tiles - grp * 8 : 8;
+    nt = in / rows;
+    m0 = (long long)(grp * 8 + in - nt * rows) * (2 * GP_ROWS);
+}
+
 __device__ __forceinline__ GpUnit gp_unit(const GpParams &p, int u) {
     GpUnit w;
-    const int t = u / p.splits;
-    w.split = u - t * p.splits;
-    const int per = 8 * p.n_tiles, grp = t / per, in = t - grp * per;
-    const int rows = min(8, p.m_tiles - grp * 8);
-    w.nt = in / rows;
-    w.m0 = (long long)(grp * 8 + in - w.nt * rows) * (2 * GP_ROWS);
-    w.kb0 = (int)((long long)p.num_kb * w.split / p.splits);
-    w.kb1 = (int)((long long)p.num_kb * (w.split + 1) / p.splits);
+    int t = u, split = 0;
+    w.plane = -1;
+    w.kb0 = 0;
+    w.kb1 = p.num_kb;
+    if (u >= p.full_tiles) {
+        w.plane = u - p.full_tiles;
+        const int tail = w.plane / p.splits;
+        split = w.plane - tail * p.splits;
+        t = p.full_tiles + tail;
+        w.kb0 = (int)((long long)p.num_kb * split / p.splits);
+        w.kb1 = (int)((long long)p.num_kb * (split + 1) / p.splits);
+    }
+    gp_tile(t, p.m_tiles, p.n_tiles, w.m0, w.nt);
     return w;
 }
 
@@ -235,6 +248,19 @@ struct GpStore {
         }
     }
 
+    // one block of a tile's partial sums
+    __device__ __forceinline__ void partial(const CUtensorMap *tm, const float (&v)[32], int col, int row, int plane) {
+        if (row0 >= M) return;
+        const uint32_t sb = next();
+        stage_f32(sb, v);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d_s(tm, sb, col, row, plane);
+            bulk_commit_group();
+        }
+    }
+
     // `off`: this lane's row offset in t; `col`: column in t of v[0]; `cols` of them exist
     __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols) {
         if (row0 >= M) return;
@@ -285,7 +311,8 @@ __device__ __forceinline__ void gp_add_residual(const GpParams &p, float (&v)[32
 
 template <bool GATED>
 __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
-                            uint32_t epi_smem, const CUtensorMap *tmY, const CUtensorMap *tmZ, const WaitCtl &ctl) {
+                            uint32_t epi_smem, const CUtensorMap *tmY, const CUtensorMap *tmZ, const CUtensorMap *tmP,
+                            const WaitCtl &ctl) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3;                      // TMEM lanes 32*quad .. 32*quad+31
     const int part = (warp - GP_EPI_WARP0) >> 2;    // even or odd 32-column chunks
@@ -307,7 +334,8 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
         // row offsets and the row's scale, worked out before the accumulator is ready
         long long zo = 0, ro = 0, yo = 0;
         float sa = 1.f;
-        if (valid && !p.raw) {
+        const bool raw = w.plane >= 0;
+        if (valid && !raw) {
             if (p.z.p && !p.z_tma) zo = row_off(p.z.m, m);
             if (p.r.p) ro = row_off(p.r.m, m);
             if (!p.y_tma) yo = row_off(p.y.m, m);
@@ -338,9 +366,9 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
             }
-            if (p.raw) {
-                st.tma(tmY, false, v, n, GATED ? 2 * w.split : w.split);
-                if constexpr (GATED) st.tma(tmY, false, up, n, 2 * w.split + 1);
+            if (raw) {
+                st.partial(tmP, v, c0, (int)rank * GP_ROWS + quad * 32, w.plane);
+                if constexpr (GATED) st.partial(tmP, up, p.nout + c0, (int)rank * GP_ROWS + quad * 32, w.plane);
                 continue;
             }
             gp_scale_bias(v, sa, p.sb ? p.sb + n : nullptr, p.bias ? p.bias + n : nullptr, cols);
@@ -381,7 +409,7 @@ template <bool E4M3, bool A_MN, bool B_MN, bool GATED>
 __global__ void __launch_bounds__(GP_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ GpParams p, const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
-                     const __grid_constant__ CUtensorMap tmZ) {
+                     const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmP) {
     constexpr int BK = E4M3 ? GP_LINE : GP_LINE / 2;
     griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
@@ -443,7 +471,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             mbar_wait(mma_done, 0u, fin, 93);
         }
     } else {
-        gp_epilogue<GATED>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, ctl);
+        gp_epilogue<GATED>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, &tmP, ctl);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -457,9 +485,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
 
 struct FinishParams {
     GemmProblem g;
-    const float *part;  // [splits][halves][M][ld] FP32
-    long long ld;
-    int splits;
+    const float *part;  // [tail tile][range][256][bn] FP32
+    int bn, nout, m_tiles, n_tiles, full_tiles, tail, splits;
     int vec;            // y, z and r take 4-element accesses
 };
 
@@ -468,20 +495,26 @@ struct FinishParams {
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishParams f) {
     griddep_launch_dependents();
     const GemmProblem &g = f.g;
-    const int per_row = (int)(f.ld / 4);
-    const long long total = g.M * per_row;
+    const int per_row = f.nout / 4, per_tile = 2 * GP_ROWS * per_row;
+    const long long total = (long long)f.tail * per_tile;
     const int halves = g.gated ? 2 : 1;
-    const long long plane = g.M * f.ld;
     griddep_wait();
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-        const long long m = i / per_row;
-        const int n = (int)(i - m * per_row) * 4, cols = g.N - n;
+        const int t = (int)(i / per_tile), in = (int)(i - (long long)t * per_tile);
+        const int r = in / per_row, c = (in - r * per_row) * 4;
+        long long m;
+        int nt;
+        gp_tile(f.full_tiles + t, f.m_tiles, f.n_tiles, m, nt);
+        m += r;
+        const int n = nt * f.nout + c, cols = g.N - n;
+        if (m >= g.M || cols <= 0) continue;
         float v[2][4];
         for (int h = 0; h < halves; ++h) {
-            const float *src = f.part + h * plane + m * f.ld + n;
+            const float *src = f.part + ((long long)t * f.splits * (2 * GP_ROWS) + r) * f.bn + h * f.nout + c;
             float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
             for (int sp = 0; sp < f.splits; ++sp) {
-                const float4 q = *reinterpret_cast<const float4 *>(src + (long long)sp * halves * plane);
+                const float4 q = *reinterpret_cast<const float4 *>(src + (long long)sp * (2 * GP_ROWS) * f.bn);
                 s[0] += q.x, s[1] += q.y, s[2] += q.z, s[3] += q.w;
             }
             const float sa = g.sa ? __ldg(g.sa + m) : 1.f;
@@ -566,15 +599,15 @@ bool vec16_rows(const RowTensor &t) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
-constexpr int FEW_ROWS = 128;
+constexpr int FEW_ROWS = 128, GP_MAX_SPLITS = 16;
 
 struct GemmPlan {
-    int bn, nout, splits, m_tiles, n_tiles, num_kb;
+    int bn, nout, m_tiles, n_tiles, num_kb;
+    int full_tiles, splits;     // tiles from full_tiles on are split
     long long a_rows, b_rows;
     int a_ch, b_ch;             // channels of the operands' rows
     bool pack_a, pack_b, few_rows;
     size_t a_off, b_off, part_off, bytes;
-    long long part_ld;
 };
 
 GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
@@ -591,30 +624,35 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     p.few_rows = g.M <= FEW_ROWS && !g.a.trans && !g.b.trans;
-    // Tile width and split from a small model of the time, in units of one
-    // k-block of a 256-column tile: narrower tiles load more per product, a
-    // unit's first loads and last epilogue are not hidden, partial sums cost
-    // their bytes and a launch.
+    // Tile width and split of the tail from a small model of the time, in units
+    // of one k-block of a pair (0.33-0.36 us).  A k-block takes almost as long for
+    // 64 columns as for 256 (the MMA thread's turn: measured 0.33 and 0.36 us), so
+    // tiles are wide and idle pairs are filled by splitting the reduction: that
+    // costs the partial sums' way through the L2 and a launch (about 4 us).
     const int pairs = ctx->sm_count / 2;
-    double best = 1e30;
-    p.bn = 256;
-    p.splits = 1;
-    for (int bn : {256, 128, 64}) {
-        if (bn == 64 && g.b.trans) continue;  // MN-major halves are whole 64-index blocks
-        if (bn == 64 && g.gated) continue;    // whole 32-output chunks for both epilogue parts
-        const int nout = g.gated ? bn / 2 : bn;
-        const long long tiles = (long long)p.m_tiles * ((g.N + nout - 1) / nout);
-        const double t_kb = bn == 256 ? 1.0 : bn == 128 ? 0.62 : 0.45;
-        for (int s = 1; s <= 16 && s <= p.num_kb; ++s) {
-            if (s > 1 && tiles * s > 2 * pairs) break;
-            const double waves = (double)((tiles * s + pairs - 1) / pairs);
-            double t = waves * ((p.num_kb + s - 1) / s) * t_kb + 6.0 + (waves - 1) * 1.0;
-            if (s > 1) t += 9.0 + (double)s * g.M * nb * 8.0 / 2.5e6;  // FP32 written and read through the L2
-            if (t < best) best = t, p.bn = bn, p.splits = s;
+    double best = 1e300;
+    for (int bn : {256, 192, 128, 64}) {
+        if (g.b.trans && bn % 128) continue;  // MN-major halves are whole 64-index blocks
+        if (g.gated && bn % 128) continue;    // and a gated half whole 64-output chunk pairs
+        const int nout = g.gated ? bn / 2 : bn, n_tiles = (g.N + nout - 1) / nout;
+        const long long tiles = (long long)p.m_tiles * n_tiles;
+        const double t_kb = 0.9 + 0.1 * bn / 256;
+        const long long tail = tiles % pairs, full = tiles - tail;
+        const double whole = (double)(full / pairs) * (p.num_kb * t_kb + 0.5);
+        for (int s = 1; s <= GP_MAX_SPLITS; ++s) {
+            double t = whole + 8.0;
+            if (s == 1) {
+                if (tail) t += p.num_kb * t_kb;
+            } else {
+                if (tail * s > pairs || 2 * s > p.num_kb) break;
+                t += (p.num_kb + s - 1) / s * t_kb + 12.0 + (double)tail * s * 256 * bn * 8 / 2.5e6;
+            }
+            if (t < best) best = t, p.bn = bn, p.splits = s, p.full_tiles = (int)std::min(s == 1 ? tiles : full, 0x7fffffffLL);
         }
     }
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
+    const long long tail = p.splits > 1 ? (long long)p.m_tiles * p.n_tiles - p.full_tiles : 0;
     auto packed = [&](long long rows, int ch) { return round256((size_t)rows * ((ch * e + 15) / 16 * 16)); };
     size_t off = 0;
     p.a_off = off;
@@ -622,8 +660,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.b_off = off;
     if (p.pack_b) off += packed(p.b_rows, p.b_ch);
     p.part_off = off;
-    p.part_ld = ((long long)g.N + 3) / 4 * 4;
-    if (p.splits > 1 && !p.few_rows) off += round256((size_t)p.splits * (g.gated ? 2 : 1) * g.M * p.part_ld * 4);
+    if (!p.few_rows) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
     p.bytes = off;
     return p;
 }
@@ -714,11 +751,11 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.num_kb = pl.num_kb;
     p.m_tiles = pl.m_tiles;
     p.n_tiles = pl.n_tiles;
-    if ((long long)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
-    p.tiles = pl.m_tiles * pl.n_tiles;
+    if ((long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    const int tail = pl.m_tiles * pl.n_tiles - pl.full_tiles;
+    p.full_tiles = pl.full_tiles;
     p.splits = pl.splits;
-    p.units = p.tiles * p.splits;
-    p.raw = pl.splits > 1;
+    p.units = pl.full_tiles + tail * pl.splits;
     p.b_atoms = pl.bn / 128;
     p.b_stage = (uint32_t)(pl.bn / 2) * GP_LINE;
     p.sa = g.sa;
@@ -733,31 +770,30 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     const uint32_t fmt = e4m3 ? 0u : 1u;
     p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)g.a.trans << 15) | ((uint32_t)g.b.trans << 16) |
               ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((2 * GP_ROWS) >> 4) << 24);
-    p.tmem_cols = (uint32_t)std::max(32, 2 * pl.bn);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < (uint32_t)(2 * pl.bn)) p.tmem_cols <<= 1;
     p.acc_stride = p.tmem_cols / 2;
 
-    CUtensorMap ta, tb, ty, tz;
+    CUtensorMap ta, tb, ty, tz, tp;
     std::memset(&ty, 0, sizeof(ty));
     std::memset(&tz, 0, sizeof(tz));
+    std::memset(&tp, 0, sizeof(tp));
     if (!dlc_encode_operand(ctx, &ta, g.a, pl.a_rows, pl.a_ch, GP_ROWS) ||
         !dlc_encode_operand(ctx, &tb, g.b, pl.b_rows, pl.b_ch, pl.bn / 2))
         return DLC_STATUS_EXECUTION_FAILED;
-    bool f32_stage = false;
-    if (p.raw) {
+    p.y_tma = tma_store_rows(g.y, g.M, g.N, 1);
+    p.z_tma = g.z.p && tma_store_rows(g.z, g.M, g.N, g.gated ? 2 : 1);
+    if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, g.N, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
+    if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
+    if (tail) {
         RowTensor part;
         part.p = g.ws + pl.part_off;
         part.dt = DLC_DATA_FLOAT;
-        part.m.ld = pl.part_ld;
-        if (!encode_output(ctx, &ty, part, g.M, g.N, pl.splits * (g.gated ? 2 : 1), g.M * pl.part_ld))
+        part.m.ld = pl.bn;
+        if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
-        f32_stage = true;
-    } else {
-        p.y_tma = tma_store_rows(g.y, g.M, g.N, 1);
-        p.z_tma = g.z.p && tma_store_rows(g.z, g.M, g.N, g.gated ? 2 : 1);
-        if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, g.N, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
-        if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
-        f32_stage = !p.y_tma || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
     }
+    const bool f32_stage = tail || !p.y_tma || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
     const int stage_bytes = GP_A_BYTES + (int)p.b_stage;
@@ -769,16 +805,21 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         return DLC_STATUS_EXECUTION_FAILED;
     }
     const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);
-    void *args[] = {&p, &ta, &tb, &ty, &tz};
+    void *args[] = {&p, &ta, &tb, &ty, &tz, &tp};
     dlcStatus_t st = dlc_launch(ctx, kern, dim3((unsigned)(2 * clusters)), dim3(GP_THREADS), smem, args, 2);
-    if (st != DLC_STATUS_SUCCESS || !p.raw) return st;
+    if (st != DLC_STATUS_SUCCESS || !tail) return st;
     FinishParams f;
     f.g = g;
     f.part = reinterpret_cast<const float *>(g.ws + pl.part_off);
-    f.ld = pl.part_ld;
+    f.bn = pl.bn;
+    f.nout = pl.nout;
+    f.m_tiles = pl.m_tiles;
+    f.n_tiles = pl.n_tiles;
+    f.full_tiles = pl.full_tiles;
+    f.tail = tail;
     f.splits = pl.splits;
     f.vec = dlc_vec4_rows(g.y) && dlc_vec4_rows(g.z) && dlc_vec4_rows(g.r);
-    const long long items = g.M * (pl.part_ld / 4);
+    const long long items = (long long)tail * 2 * GP_ROWS * (pl.nout / 4);
     const long long blocks = std::min<long long>((items + 255) / 256, (long long)ctx->sm_count * 8);
     void *fargs[] = {&f};
     return dlc_launch(ctx, (const void *)gemm_finish_kernel, dim3((unsigned)blocks), dim3(256), 0, fargs);
