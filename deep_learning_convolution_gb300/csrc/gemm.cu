@@ -184,16 +184,35 @@ __device__ void gp_mma(const GpParams &p, uint32_t tmem_base, uint32_t sA, uint3
 
 // ---- epilogue --------------------------------------------------------------------
 
+// 32 values of a vector from column n on (the same for every row of the warp):
+// 16-byte loads where the address allows them; columns past `cols` read as zero.
+__device__ __forceinline__ void gp_columns(const float *src, int cols, float (&v)[32]) {
+    if (cols >= 32 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(src) + i);
+            v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < cols ? __ldg(src + i) : 0.f;
+    }
+}
+
 // sa[m] sb[n] acc + bias[n], columns n .. n+31 of a row (sb and bias start at
-// the column's own filter; columns past `cols` are not read).
+// the column's own filter).
 __device__ __forceinline__ void gp_scale_bias(float (&v)[32], float sa, const float *sb, const float *bias, int cols) {
     if (sb) {
+        float c[32];
+        gp_columns(sb, cols, c);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= sa * (i < cols ? __ldg(sb + i) : 0.f);
+        for (int i = 0; i < 32; ++i) v[i] *= sa * c[i];
     }
     if (bias) {
+        float c[32];
+        gp_columns(bias, cols, c);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += i < cols ? __ldg(bias + i) : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] += c[i];
     }
 }
 
@@ -261,51 +280,71 @@ struct GpStore {
         }
     }
 
-    // `off`: this lane's row offset in t; `col`: column in t of v[0]; `cols` of them exist
-    __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols) {
+    // Row by row, a lane per column, eight rows at a time (their loads and stores
+    // are in flight together).  `off`: this lane's row offset in t; `col`: column
+    // in t of v[0], `cols` of them exist; r (or null), with `roff`: a residual
+    // added on the way.
+    __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols,
+                         const RowTensor *r, long long roff) {
         if (row0 >= M) return;
         const uint32_t sb = next();
         stage_f32(sb, v);
         __syncwarp();
         const int n = (int)min(32LL, M - row0);
-        for (int r = 0; r < n; ++r) {
-            const long long ro = __shfl_sync(0xffffffffu, off, r);
-            float f;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(sb + (uint32_t)r * 128u +
-                         ((((uint32_t)lane >> 2) ^ ((uint32_t)r & 7u)) << 4) + ((uint32_t)lane & 3u) * 4u) : "memory");
-            if (lane < cols) store_elem(t.p, t.dt, ro + (col + lane) * t.m.cs, f);
+        const bool in = lane < cols;
+        const long long tc = (col + lane) * t.m.cs, rc = r ? (col + lane) * r->m.cs : 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t row = (uint32_t)(i0 + i);
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[i]) : "r"(sb + row * 128u +
+                             ((((uint32_t)lane >> 2) ^ (row & 7u)) << 4) + ((uint32_t)lane & 3u) * 4u) : "memory");
+            }
+            if (r) {
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const long long ro = __shfl_sync(0xffffffffu, roff, i0 + i);
+                    w[i] = in && i0 + i < n ? load_elem(r->p, r->dt, ro + rc) : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] += w[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const long long to = __shfl_sync(0xffffffffu, off, i0 + i);
+                if (in && i0 + i < n) store_elem(t.p, t.dt, to + tc, f[i]);
+            }
         }
         __syncwarp();
         if (lane == 0) bulk_commit_group();  // an empty group keeps the buffers' turn
     }
 };
 
-__device__ __forceinline__ void gp_add_residual(const GpParams &p, float (&v)[32], long long off, int n, int cols) {
-    if (p.r_vec && cols >= 32) {
-        if (p.r.dt == DLC_DATA_BFLOAT16) {
-            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.r.p) + off + n);
+// v += the residual's 32 values at off + n (16-byte aligned, all of them exist).
+__device__ __forceinline__ void gp_add_residual(const RowTensor &r, float (&v)[32], long long off, int n) {
+    if (r.dt == DLC_DATA_BFLOAT16) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(r.p) + off + n);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 w = q[j];
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < 4; ++j) {
+            const uint4 w = q[j];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[8 * j + 2 * i] += __uint_as_float(u[i] << 16);
-                    v[8 * j + 2 * i + 1] += __uint_as_float(u[i] & 0xffff0000u);
-                }
-            }
-        } else {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.r.p) + off + n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 w = q[j];
-                v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack_bf16(u[i]);
+                v[8 * j + 2 * i] += f.x;
+                v[8 * j + 2 * i + 1] += f.y;
             }
         }
     } else {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + off + n);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < cols) v[i] += load_elem(p.r.p, p.r.dt, off + (long long)(n + i) * p.r.m.cs);
+        for (int j = 0; j < 8; ++j) {
+            const float4 w = q[j];
+            v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+        }
     }
 }
 
@@ -338,7 +377,7 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
         if (valid && !raw) {
             if (p.z.p && !p.z_tma) zo = row_off(p.z.m, m);
             if (p.r.p) ro = row_off(p.r.m, m);
-            if (!p.y_tma) yo = row_off(p.y.m, m);
+            yo = row_off(p.y.m, m);
             if (p.sa) sa = __ldg(p.sa + m);
         }
         int okw = 0;
@@ -379,8 +418,8 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
                     st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, v, n, 0);
                     if constexpr (GATED) st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, up, n, 1);
                 } else {
-                    st.rows(p.z, zo, v, n, cols);
-                    if constexpr (GATED) st.rows(p.z, zo, up, (long long)p.N + n, cols);
+                    st.rows(p.z, zo, v, n, cols, nullptr, 0);
+                    if constexpr (GATED) st.rows(p.z, zo, up, (long long)p.N + n, cols, nullptr, 0);
                 }
             }
             act_dispatch(p.act, [&](auto act) {
@@ -391,11 +430,12 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= up[i];
             }
-            if (p.r.p && valid) gp_add_residual(p, v, ro, n, cols);
-            if (p.y_tma)
+            if (p.y_tma && (!p.r.p || (p.r_vec && cols >= 32))) {
+                if (p.r.p && valid) gp_add_residual(p.r, v, ro, n);
                 st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
-            else
-                st.rows(p.y, yo, v, n, cols);
+            } else {
+                st.rows(p.y, yo, v, n, cols, p.r.p ? &p.r : nullptr, ro);
+            }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -549,26 +589,49 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
 
 // ---- operands that TMA cannot load ------------------------------------------------------
 
-// dst: [rows][ld] dense, ld * E a multiple of 16 bytes; src: any strides.  The
-// reads run along the source's contiguous axis, the writes along channels.
+// dst: [rows][ld] dense, ld * sizeof(E) a multiple of 16 bytes.  Channels
+// contiguous: a warp a row, units of the widest type that divides its address,
+// pitch and length, eight a lane in flight.
 template <typename E>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
-                                                        long long rows, int C) {
+__global__ void __launch_bounds__(256) pack_units_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
+                                                         long long rows, int C) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const E *s = static_cast<const E *>(src.p);
+    griddep_wait();
+    for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (long long)gridDim.x * 8) {
+        const E *from = s + row_off(src.m, r);
+        for (int c0 = (int)blockIdx.y * 256 + lane; c0 < C; c0 += (int)gridDim.y * 256) {
+            E v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i < C) v[i] = from[c0 + 32 * i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i < C) dst[r * ld + c0 + 32 * i] = v[i];
+        }
+    }
+}
+
+// Channels apart: 32 x 32 elements through shared memory, read along the rows
+// and written along the channels.
+template <typename E>
+__global__ void __launch_bounds__(256) pack_transposed_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
+                                                              long long rows, int C) {
     griddep_launch_dependents();
     __shared__ E tile[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long r0 = (long long)blockIdx.x * 32;
-    const bool along_c = src.m.cs == 1;
     const E *s = static_cast<const E *>(src.p);
     griddep_wait();
+    const long long ro = r0 + lane < rows ? row_off(src.m, r0 + lane) : 0;
     for (int c0 = (int)blockIdx.y * 32; c0 < C; c0 += (int)gridDim.y * 32) {
         __syncthreads();
-        for (int i = warp; i < 32; i += 8) {
-            const long long r = r0 + (along_c ? i : lane);
-            const int c = c0 + (along_c ? lane : i);
-            if (r < rows && c < C) tile[along_c ? i : lane][along_c ? lane : i] = s[row_off(src.m, r) + (long long)c * src.m.cs];
-        }
+#pragma unroll
+        for (int i = warp; i < 32; i += 8)
+            if (r0 + lane < rows && c0 + i < C) tile[lane][i] = s[ro + (long long)(c0 + i) * src.m.cs];
         __syncthreads();
+#pragma unroll
         for (int i = warp; i < 32; i += 8)
             if (r0 + i < rows && c0 + lane < C) dst[(r0 + i) * ld + c0 + lane] = tile[i][lane];
     }
@@ -599,7 +662,7 @@ bool vec16_rows(const RowTensor &t) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
-constexpr int FEW_ROWS = 128, GP_MAX_SPLITS = 16;
+constexpr int GP_MAX_SPLITS = 16;
 
 struct GemmPlan {
     int bn, nout, m_tiles, n_tiles, num_kb;
@@ -623,12 +686,13 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
-    p.few_rows = g.M <= FEW_ROWS && !g.a.trans && !g.b.trans;
-    // Tile width and split of the tail from a small model of the time, in units
-    // of one k-block of a pair (0.33-0.36 us).  A k-block takes almost as long for
-    // 64 columns as for 256 (the MMA thread's turn: measured 0.33 and 0.36 us), so
-    // tiles are wide and idle pairs are filled by splitting the reduction: that
-    // costs the partial sums' way through the L2 and a launch (about 4 us).
+    // Tile width, split of the tail, and which of the two kernels, from a model of
+    // the time in microseconds (constants measured back to back on 20 shapes from
+    // 16 x 512 -> 512 to 12000 x 192 -> 256; its choice is within 10 % of the best
+    // alternative on all of them but one, 20 % there).  A k-block takes a pair almost as long
+    // for 64 columns as for 256 (the MMA thread's turn), so tiles are wide and
+    // idle pairs are filled by splitting the reduction: that costs the partial
+    // sums' way through the L2 and a launch.
     const int pairs = ctx->sm_count / 2;
     double best = 1e300;
     for (int bn : {256, 192, 128, 64}) {
@@ -636,20 +700,24 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
         if (g.gated && bn % 128) continue;    // and a gated half whole 64-output chunk pairs
         const int nout = g.gated ? bn / 2 : bn, n_tiles = (g.N + nout - 1) / nout;
         const long long tiles = (long long)p.m_tiles * n_tiles;
-        const double t_kb = 0.9 + 0.1 * bn / 256;
+        const double kb = 0.32 + 0.04 * bn / 256, fixed = 3.4 + 1.2 * bn / 256;
         const long long tail = tiles % pairs, full = tiles - tail;
-        const double whole = (double)(full / pairs) * (p.num_kb * t_kb + 0.5);
+        const double whole = (double)(full / pairs) * (p.num_kb * kb + 0.15);
         for (int s = 1; s <= GP_MAX_SPLITS; ++s) {
-            double t = whole + 8.0;
+            double t = fixed + whole;
             if (s == 1) {
-                if (tail) t += p.num_kb * t_kb;
+                if (tail) t += p.num_kb * kb;
             } else {
                 if (tail * s > pairs || 2 * s > p.num_kb) break;
-                t += (p.num_kb + s - 1) / s * t_kb + 12.0 + (double)tail * s * 256 * bn * 8 / 2.5e6;
+                t += (p.num_kb + s - 1) / s * kb + 2.2 + (double)tail * s * 256 * bn * 8 / 7e6;
             }
             if (t < best) best = t, p.bn = bn, p.splits = s, p.full_tiles = (int)std::min(s == 1 ? tiles : full, 0x7fffffffLL);
         }
     }
+    // Up to 64 rows the filters' stream decides, which the few-row kernel carries
+    // at the memory's rate whatever the model says (one row of 2048 -> 2 x 8192:
+    // 15.4 us, the pair kernel 22).
+    p.few_rows = !g.a.trans && !g.b.trans && (g.M <= 64 || dlc_few_rows_plan(ctx, g).us < best);
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
     const long long tail = p.splits > 1 ? (long long)p.m_tiles * p.n_tiles - p.full_tiles : 0;
@@ -665,18 +733,46 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     return p;
 }
 
+// The widest unit (bytes) that every row's address and length are multiples of.
+int row_unit(const RowTensor &t, int ch) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    for (int u : {8, 4, 2}) {
+        auto mult = [&](long long s) { return (s * e) % u == 0; };
+        if ((uintptr_t)t.p % u == 0 && mult(ch) &&
+            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3))))
+            return std::max(u, (int)e);
+    }
+    return (int)e;
+}
+
 dlcStatus_t pack_rows(dlcContext *ctx, RowTensor &t, long long rows, int ch, char *dst) {
     const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    const long long ld = (long long)(((long long)ch * e + 15) / 16 * 16) / e;
     RowTensor src = t;
-    long long ld = (long long)((ch * e + 15) / 16 * 16) / e;
-    const long long blocks = (rows + 31) / 32;
-    // enough blocks to fill the GPU, each walking the rest of its rows' channels
-    const int gy = (int)std::min<long long>((ch + 31) / 32, std::max<long long>(1, (long long)ctx->sm_count * 16 / blocks));
     void *d = dst;
-    void *args[] = {&src, &d, &ld, &rows, &ch};
-    if (blocks > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
-    const void *k = e == 1 ? (const void *)pack_rows_kernel<unsigned char> : (const void *)pack_rows_kernel<unsigned short>;
-    const dlcStatus_t st = dlc_launch(ctx, k, dim3((unsigned)blocks, (unsigned)gy), dim3(256), 0, args);
+    const void *k;
+    dim3 grid;
+    long long ld_units = ld;
+    int c_units = ch;
+    if (t.m.cs == 1) {
+        const int u = row_unit(t, ch), per = u / e;
+        src.m.ld /= per, src.m.s0 /= per, src.m.s2 /= per, src.m.s3 /= per;
+        ld_units /= per;
+        c_units /= per;
+        k = u == 8 ? (const void *)pack_units_kernel<uint2> : u == 4 ? (const void *)pack_units_kernel<uint32_t>
+            : u == 2 ? (const void *)pack_units_kernel<unsigned short> : (const void *)pack_units_kernel<unsigned char>;
+        const long long gx = std::min<long long>((rows + 7) / 8, (long long)ctx->sm_count * 8);
+        const long long gy = std::min<long long>((c_units + 255) / 256, std::max<long long>(1, (long long)ctx->sm_count * 8 / gx));
+        grid = dim3((unsigned)gx, (unsigned)gy);
+    } else {
+        const long long gx = (rows + 31) / 32;
+        if (gx > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+        const long long gy = std::min<long long>((ch + 31) / 32, std::max<long long>(1, (long long)ctx->sm_count * 16 / gx));
+        k = e == 1 ? (const void *)pack_transposed_kernel<unsigned char> : (const void *)pack_transposed_kernel<unsigned short>;
+        grid = dim3((unsigned)gx, (unsigned)gy);
+    }
+    void *args[] = {&src, &d, &ld_units, &rows, &c_units};
+    const dlcStatus_t st = dlc_launch(ctx, k, grid, dim3(256), 0, args);
     t.p = dst;
     t.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
     return st;
@@ -793,7 +889,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
     }
-    const bool f32_stage = tail || !p.y_tma || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
+    const bool f32_stage = tail || !p.y_tma || g.r.p || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
     const int stage_bytes = GP_A_BYTES + (int)p.b_stage;

@@ -5,6 +5,7 @@
 
 struct FewRowsPlan {
     int num_kb, rows, filter_tiles, row_tiles, splits;
+    double us;  // expected time
 };
 
 // gemm_rows.cu: operands as TMA loads them (see gemm.cu's packing).

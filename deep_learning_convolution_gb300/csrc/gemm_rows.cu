@@ -15,6 +15,7 @@
 // Roles (16 warps): warp 0 lane 0 loads, warp 1 lane 0 issues the MMAs; all warps
 // read the accumulators (four per quarter of the TMEM lanes) and join the partial
 // sums, a warp a row, a lane four filters.  Every wait is bounded.
+#include <atomic>
 #include <cstring>
 
 #include "channel.cuh"
@@ -260,6 +261,34 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
 
+// Clusters of `size` CTAs (an SM each) that the device holds at once; a property
+// of the device, asked once.
+int resident_clusters(const dlcContext *ctx, int size) {
+    static std::atomic<int> known[FR_MAX_SPLITS + 1];
+    int n = known[size].load();
+    if (n > 0) return n;
+    const void *kern = (const void *)gemm_rows_kernel<false, false>;
+    const int smem = FR_SMEM;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(ctx->sm_count / size * size));
+    cfg.blockDim = dim3(FR_THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return std::max(1, ctx->sm_count / size);
+    }
+    known[size].store(n);
+    return n;
+}
+
 size_t own_bytes(bool gated, int rows) { return (size_t)(gated ? 2 : 1) * FR_FILTERS * 4 * rows; }
 
 }  // namespace
@@ -268,13 +297,25 @@ FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g) {
     FewRowsPlan p;
     const int e = dlc_dtype_bytes((dlcDataType_t)g.a.t.dt);
     p.num_kb = (int)((g.K * e + FR_LINE - 1) / FR_LINE);
-    p.rows = (int)std::min<long long>(FR_FILTERS, (g.M + 15) / 16 * 16);
+    const long long row_tiles = (g.M + FR_FILTERS - 1) / FR_FILTERS;
+    p.rows = (int)(((g.M + row_tiles - 1) / row_tiles + 15) / 16 * 16);
+    p.row_tiles = (int)std::min<long long>((g.M + p.rows - 1) / p.rows, 65535);
     p.filter_tiles = (g.N + FR_FILTERS - 1) / FR_FILTERS;
-    p.row_tiles = (int)((g.M + p.rows - 1) / p.rows);
-    // more CTAs a tile while SMs are idle, each with two k-blocks at least
     const long long tiles = (long long)p.filter_tiles * p.row_tiles;
+    // Time in microseconds (fitted like the pair kernel's, in gemm.cu): CTAs a
+    // tile against waves of clusters; the SMs of a GPC that a cluster does not
+    // fill stay idle, so fewer clusters of eight run at once than the SMs suggest.
+    const double share = p.rows / 128.0;
+    const double kb = g.gated ? 0.6 + 0.4 * share : 0.33 + 0.05 * share, fixed = g.gated ? 3.2 + 3.2 * share : 3.0 + 2.2 * share;
+    p.us = 1e300;
     p.splits = 1;
-    while (p.splits < FR_MAX_SPLITS && tiles * (p.splits + 1) <= ctx->sm_count && (p.splits + 1) * 2 <= p.num_kb) ++p.splits;
+    for (int s = 1; s <= FR_MAX_SPLITS && (s == 1 || 2 * s <= p.num_kb); ++s) {
+        const int at_once = resident_clusters(ctx, s);
+        const double waves = (double)((tiles + at_once - 1) / at_once);
+        const double t = waves * ((p.num_kb + s - 1) / s * kb + fixed + 0.1 * s);
+        if (t < p.us) p.us = t, p.splits = s;
+    }
+    if ((g.M + p.rows - 1) / p.rows > 65535) p.us = 1e300;  // more row tiles than a grid has
     return p;
 }
 
