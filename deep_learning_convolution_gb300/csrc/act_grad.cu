@@ -147,7 +147,8 @@ AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
     g.w = ag_vec(p.dy, 0) && ag_vec(p.z, n) && ag_vec(p.dz, n) ? 8 : 1;
     g.gx = (unsigned)((p.N + 32 * g.w - 1) / (32 * g.w));
     const long long strips = (p.rows + AG_WARPS - 1) / AG_WARPS;
-    const long long want = std::max<long long>(1, (long long)ctx->sm_count * AG_BLOCKS / g.gx);
+    // (single elements have fewer bytes in flight a block: more of them)
+    const long long want = std::max<long long>(1, (long long)ctx->sm_count * (g.w == 8 ? AG_BLOCKS : 8) / g.gx);
     g.gy = (unsigned)std::min(std::min(strips, want), 65535LL);
     return g;
 }
@@ -157,7 +158,8 @@ AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
 size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p) {
     // either vector width's number of row strips
     const long long strips = (p.rows + AG_WARPS - 1) / AG_WARPS;
-    const long long want = std::max<long long>(1, (long long)ctx->sm_count * AG_BLOCKS / std::max(1, (p.N + 255) / 256));
+    const long long want = std::max(std::max<long long>(1, (long long)ctx->sm_count * AG_BLOCKS / ((p.N + 255) / 256)),
+                                    (long long)ctx->sm_count * 8 / ((p.N + 31) / 32));
     return (size_t)std::min(std::min(strips, want), 65535LL) * (p.gated ? 2 : 1) * p.N * sizeof(float);
 }
 

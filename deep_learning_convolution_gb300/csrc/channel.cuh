@@ -55,6 +55,26 @@ __device__ __forceinline__ float load_elem(const void *p, int dt, long long i) {
     return float(v);
 }
 
+// n elements `stride` apart, FLOAT or BFLOAT16, as FP32; element i only where
+// in(i), zero elsewhere.  The storage type is looked at once, outside, so that
+// the loads are in flight together (a load behind its own branch is waited for
+// before the next one starts).
+template <int N, typename In>
+__device__ __forceinline__ void load_elems(const void *p, int dt, long long off, long long stride, In in, float *v) {
+    if (dt == DLC_DATA_BFLOAT16) {
+        const unsigned short *s = static_cast<const unsigned short *>(p) + off;
+        unsigned short w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = in(i) ? s[i * stride] : (unsigned short)0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = bf16_bits_f32(w[i]);
+    } else {
+        const float *s = static_cast<const float *>(p) + off;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = in(i) ? s[i * stride] : 0.f;
+    }
+}
+
 __device__ __forceinline__ void store_elem(void *p, int dt, long long i, float v) {
     if (dt == DLC_DATA_FLOAT)
         static_cast<float *>(p)[i] = v;
@@ -78,8 +98,7 @@ __device__ __forceinline__ void load4(const RowTensor &t, long long off, int n, 
             v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < cols ? load_elem(t.p, t.dt, off + (long long)(n + i) * t.m.cs) : 0.f;
+        load_elems<4>(t.p, t.dt, off + (long long)n * t.m.cs, t.m.cs, [&](int i) { return i < cols; }, v);
     }
 }
 

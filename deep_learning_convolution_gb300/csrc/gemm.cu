@@ -280,10 +280,11 @@ struct GpStore {
         }
     }
 
-    // Row by row, a lane per column, eight rows at a time (their loads and stores
+    // Row by row, a lane per column, sixteen rows at a time (their loads and stores
     // are in flight together).  `off`: this lane's row offset in t; `col`: column
     // in t of v[0], `cols` of them exist; r (or null), with `roff`: a residual
     // added on the way.
+    static constexpr int ROWS = 16;
     __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols,
                          const RowTensor *r, long long roff) {
         if (row0 >= M) return;
@@ -294,26 +295,35 @@ struct GpStore {
         const bool in = lane < cols;
         const long long tc = (col + lane) * t.m.cs, rc = r ? (col + lane) * r->m.cs : 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float f[8];
+        for (int i0 = 0; i0 < n; i0 += ROWS) {
+            float f[ROWS];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const uint32_t row = (uint32_t)(i0 + i);
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[i]) : "r"(sb + row * 128u +
                              ((((uint32_t)lane >> 2) ^ (row & 7u)) << 4) + ((uint32_t)lane & 3u) * 4u) : "memory");
             }
             if (r) {
-                float w[8];
+                long long ro[ROWS];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const long long ro = __shfl_sync(0xffffffffu, roff, i0 + i);
-                    w[i] = in && i0 + i < n ? load_elem(r->p, r->dt, ro + rc) : 0.f;
+                for (int i = 0; i < ROWS; ++i) ro[i] = __shfl_sync(0xffffffffu, roff, i0 + i) + rc;
+                if (r->dt == DLC_DATA_BFLOAT16) {  // (the type's branch outside: all loads in flight)
+                    unsigned short w[ROWS];
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i)
+                        w[i] = in && i0 + i < n ? static_cast<const unsigned short *>(r->p)[ro[i]] : (unsigned short)0;
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) f[i] += bf16_bits_f32(w[i]);
+                } else {
+                    float w[ROWS];
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) w[i] = in && i0 + i < n ? static_cast<const float *>(r->p)[ro[i]] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) f[i] += w[i];
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] += w[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const long long to = __shfl_sync(0xffffffffu, off, i0 + i);
                 if (in && i0 + i < n) store_elem(t.p, t.dt, to + tc, f[i]);
             }
@@ -323,30 +333,68 @@ struct GpStore {
     }
 };
 
-// v += the residual's 32 values at off + n (16-byte aligned, all of them exist).
-__device__ __forceinline__ void gp_add_residual(const RowTensor &r, float (&v)[32], long long off, int n) {
-    if (r.dt == DLC_DATA_BFLOAT16) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(r.p) + off + n);
+// The last few values of a row (fewer than a 16-byte vector); out of line, since
+// the code around them is on every tile's path.
+__device__ __noinline__ uint4 gp_last_bf16(const unsigned short *src, int n) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) w[i >> 1] |= (uint32_t)src[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __noinline__ float4 gp_last_f32(const float *src, int n) {
+    return make_float4(src[0], n > 1 ? src[1] : 0.f, n > 2 ? src[2] : 0.f, 0.f);
+}
+
+// A lane's 32 residual values of a chunk (16-byte aligned rows; columns past
+// `cols` are not read).  BF16 ones are loaded ahead of the chunk before, or of
+// the accumulator; FP32 ones, twice the registers, where they are added.
+struct GpResidual {
+    uint4 q[4];
+    int cols;
+
+    __device__ __forceinline__ void load(const RowTensor &r, bool on, long long off, int columns) {
+        cols = on && r.dt == DLC_DATA_BFLOAT16 ? columns : 0;
+        const unsigned short *src = static_cast<const unsigned short *>(r.p) + off;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint4 w = q[j];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack_bf16(u[i]);
-                v[8 * j + 2 * i] += f.x;
-                v[8 * j + 2 * i + 1] += f.y;
+            q[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * j + 8 <= cols) {
+                q[j] = *reinterpret_cast<const uint4 *>(src + 8 * j);
+            } else if (8 * j < cols) {
+                q[j] = gp_last_bf16(src + 8 * j, cols - 8 * j);
             }
         }
-    } else {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + off + n);
+    }
+
+    __device__ __forceinline__ void add(const RowTensor &r, float (&v)[32], long long off, int columns) const {
+        if (cols > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 w = q[j];
-            v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack_bf16(u[i]);
+                    v[8 * j + 2 * i] += f.x;
+                    v[8 * j + 2 * i + 1] += f.y;
+                }
+            }
+        } else {
+            const float *src = static_cast<const float *>(r.p) + off;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (4 * j + 4 <= columns) {
+                    const float4 w = *reinterpret_cast<const float4 *>(src + 4 * j);
+                    v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+                } else if (4 * j < columns) {
+                    const float4 w = gp_last_f32(src + 4 * j, columns - 4 * j);
+                    v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+                }
+            }
         }
     }
-}
+};
 
 template <bool GATED>
 __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
@@ -380,6 +428,10 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
             yo = row_off(p.y.m, m);
             if (p.sa) sa = __ldg(p.sa + m);
         }
+        // (a gated layer has no residual)
+        const bool res = !GATED && valid && !raw && p.r_vec && p.y_tma;
+        GpResidual rq;
+        if (!GATED) rq.load(p.r, res, ro + n0 + 32 * part, p.N - n0 - 32 * part);
         int okw = 0;
         if (lane == 0) okw = mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, ctl, 25) ? 1 : 0;
         okw = __shfl_sync(0xffffffffu, okw, 0);
@@ -430,8 +482,11 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= up[i];
             }
-            if (p.y_tma && (!p.r.p || (p.r_vec && cols >= 32))) {
-                if (p.r.p && valid) gp_add_residual(p.r, v, ro, n);
+            if (p.y_tma && (!p.r.p || p.r_vec)) {
+                if (!GATED) {
+                    if (res) rq.add(p.r, v, ro + n, cols);
+                    rq.load(p.r, res && c0 + 64 < p.nout, ro + n + 64, cols - 64);
+                }
                 st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
             } else {
                 st.rows(p.y, yo, v, n, cols, p.r.p ? &p.r : nullptr, ro);
@@ -589,26 +644,37 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
 
 // ---- operands that TMA cannot load ------------------------------------------------------
 
-// dst: [rows][ld] dense, ld * sizeof(E) a multiple of 16 bytes.  Channels
-// contiguous: a warp a row, units of the widest type that divides its address,
-// pitch and length, eight a lane in flight.
+// Operands copied to dense rows, each a multiple of 16 bytes long; both of a
+// product's in one launch (blockIdx.z).
+struct PackJob {
+    RowTensor src;      // strides in units
+    void *dst;
+    long long ld, rows; // of the destination, in units
+    int C, unit;        // units of a row, bytes of a unit
+    int transposed;     // channels apart
+    unsigned gx, gy;    // blocks of its own
+};
+
+struct PackParams {
+    PackJob job[2];
+};
+
+// Channels contiguous: a warp a row, eight units a lane in flight.
 template <typename E>
-__global__ void __launch_bounds__(256) pack_units_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
-                                                         long long rows, int C) {
-    griddep_launch_dependents();
+__device__ __forceinline__ void pack_units(const PackJob &p) {
     const int lane = threadIdx.x & 31;
-    const E *s = static_cast<const E *>(src.p);
-    griddep_wait();
-    for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (long long)gridDim.x * 8) {
-        const E *from = s + row_off(src.m, r);
-        for (int c0 = (int)blockIdx.y * 256 + lane; c0 < C; c0 += (int)gridDim.y * 256) {
+    const E *s = static_cast<const E *>(p.src.p);
+    E *dst = static_cast<E *>(p.dst);
+    for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < p.rows; r += (long long)p.gx * 8) {
+        const E *from = s + row_off(p.src.m, r);
+        for (int c0 = (int)blockIdx.y * 256 + lane; c0 < p.C; c0 += (int)p.gy * 256) {
             E v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + 32 * i < C) v[i] = from[c0 + 32 * i];
+                if (c0 + 32 * i < p.C) v[i] = from[c0 + 32 * i];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + 32 * i < C) dst[r * ld + c0 + 32 * i] = v[i];
+                if (c0 + 32 * i < p.C) dst[r * p.ld + c0 + 32 * i] = v[i];
         }
     }
 }
@@ -616,24 +682,43 @@ __global__ void __launch_bounds__(256) pack_units_kernel(const __grid_constant__
 // Channels apart: 32 x 32 elements through shared memory, read along the rows
 // and written along the channels.
 template <typename E>
-__global__ void __launch_bounds__(256) pack_transposed_kernel(const __grid_constant__ RowTensor src, E *dst, long long ld,
-                                                              long long rows, int C) {
-    griddep_launch_dependents();
-    __shared__ E tile[32][33];
+__device__ __forceinline__ void pack_transposed(const PackJob &p, E (*tile)[33]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long r0 = (long long)blockIdx.x * 32;
-    const E *s = static_cast<const E *>(src.p);
+    const E *s = static_cast<const E *>(p.src.p);
+    E *dst = static_cast<E *>(p.dst);
+    const long long ro = r0 + lane < p.rows ? row_off(p.src.m, r0 + lane) : 0;
+    for (int c0 = (int)blockIdx.y * 32; c0 < p.C; c0 += (int)p.gy * 32) {
+        __syncthreads();
+#pragma unroll
+        for (int i = warp; i < 32; i += 8)
+            if (r0 + lane < p.rows && c0 + i < p.C) tile[lane][i] = s[ro + (long long)(c0 + i) * p.src.m.cs];
+        __syncthreads();
+#pragma unroll
+        for (int i = warp; i < 32; i += 8)
+            if (r0 + i < p.rows && c0 + lane < p.C) dst[(r0 + i) * p.ld + c0 + lane] = tile[i][lane];
+    }
+}
+
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackParams params) {
+    griddep_launch_dependents();
+    __shared__ unsigned short tile[32][33];
+    const PackJob &p = params.job[blockIdx.z];
     griddep_wait();
-    const long long ro = r0 + lane < rows ? row_off(src.m, r0 + lane) : 0;
-    for (int c0 = (int)blockIdx.y * 32; c0 < C; c0 += (int)gridDim.y * 32) {
-        __syncthreads();
-#pragma unroll
-        for (int i = warp; i < 32; i += 8)
-            if (r0 + lane < rows && c0 + i < C) tile[lane][i] = s[ro + (long long)(c0 + i) * src.m.cs];
-        __syncthreads();
-#pragma unroll
-        for (int i = warp; i < 32; i += 8)
-            if (r0 + i < rows && c0 + lane < C) dst[(r0 + i) * ld + c0 + lane] = tile[i][lane];
+    if (blockIdx.x >= p.gx || blockIdx.y >= p.gy) return;
+    if (p.transposed) {
+        if (p.unit == 2)
+            pack_transposed<unsigned short>(p, tile);
+        else
+            pack_transposed<unsigned char>(p, reinterpret_cast<unsigned char(*)[33]>(tile));
+    } else if (p.unit == 8) {
+        pack_units<uint2>(p);
+    } else if (p.unit == 4) {
+        pack_units<uint32_t>(p);
+    } else if (p.unit == 2) {
+        pack_units<unsigned short>(p);
+    } else {
+        pack_units<unsigned char>(p);
     }
 }
 
@@ -745,37 +830,29 @@ int row_unit(const RowTensor &t, int ch) {
     return (int)e;
 }
 
-dlcStatus_t pack_rows(dlcContext *ctx, RowTensor &t, long long rows, int ch, char *dst) {
+// The copy of `t` ([rows][ch]) to `dst`; t becomes the copy.
+PackJob pack_job(const dlcContext *ctx, RowTensor &t, long long rows, int ch, char *dst) {
     const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
-    const long long ld = (long long)(((long long)ch * e + 15) / 16 * 16) / e;
-    RowTensor src = t;
-    void *d = dst;
-    const void *k;
-    dim3 grid;
-    long long ld_units = ld;
-    int c_units = ch;
-    if (t.m.cs == 1) {
-        const int u = row_unit(t, ch), per = u / e;
-        src.m.ld /= per, src.m.s0 /= per, src.m.s2 /= per, src.m.s3 /= per;
-        ld_units /= per;
-        c_units /= per;
-        k = u == 8 ? (const void *)pack_units_kernel<uint2> : u == 4 ? (const void *)pack_units_kernel<uint32_t>
-            : u == 2 ? (const void *)pack_units_kernel<unsigned short> : (const void *)pack_units_kernel<unsigned char>;
-        const long long gx = std::min<long long>((rows + 7) / 8, (long long)ctx->sm_count * 8);
-        const long long gy = std::min<long long>((c_units + 255) / 256, std::max<long long>(1, (long long)ctx->sm_count * 8 / gx));
-        grid = dim3((unsigned)gx, (unsigned)gy);
-    } else {
-        const long long gx = (rows + 31) / 32;
-        if (gx > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
-        const long long gy = std::min<long long>((ch + 31) / 32, std::max<long long>(1, (long long)ctx->sm_count * 16 / gx));
-        k = e == 1 ? (const void *)pack_transposed_kernel<unsigned char> : (const void *)pack_transposed_kernel<unsigned short>;
-        grid = dim3((unsigned)gx, (unsigned)gy);
-    }
-    void *args[] = {&src, &d, &ld_units, &rows, &c_units};
-    const dlcStatus_t st = dlc_launch(ctx, k, grid, dim3(256), 0, args);
+    const long long ld = (((long long)ch * e + 15) / 16 * 16) / e;
+    PackJob j;
+    j.src = t;
+    j.dst = dst;
+    j.rows = rows;
+    j.transposed = t.m.cs != 1;
+    j.unit = j.transposed ? e : row_unit(t, ch);
+    const int per = j.unit / e;
+    j.src.m.ld /= per, j.src.m.s0 /= per, j.src.m.s2 /= per, j.src.m.s3 /= per;
+    j.ld = ld / per;
+    j.C = ch / per;
+    // enough blocks to fill the GPU: rows first, then a row's channels
+    const long long most = (long long)ctx->sm_count * (j.transposed ? 16 : 8);
+    const long long gx = j.transposed ? (rows + 31) / 32 : std::min<long long>((rows + 7) / 8, most);
+    const long long spans = j.transposed ? (j.C + 31) / 32 : (j.C + 255) / 256;
+    j.gx = (unsigned)gx;
+    j.gy = (unsigned)std::min<long long>(spans, std::max<long long>(1, most / gx));
     t.p = dst;
     t.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
-    return st;
+    return j;
 }
 
 bool encode(const dlcContext *ctx, CUtensorMap *tm, const RowTensor &t, int nd, const cuuint64_t *dim, long long plane,
@@ -889,7 +966,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
     }
-    const bool f32_stage = tail || !p.y_tma || g.r.p || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
+    const bool f32_stage = tail || !p.y_tma || (g.r.p && !p.r_vec) || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
     const int stage_bytes = GP_A_BYTES + (int)p.b_stage;
@@ -943,12 +1020,15 @@ size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g) { return 
 dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &pb) {
     GemmProblem g = pb;
     const GemmPlan pl = plan_gemm(ctx, g);
-    if (pl.pack_a) {
-        const dlcStatus_t st = pack_rows(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
-        if (st != DLC_STATUS_SUCCESS) return st;
-    }
-    if (pl.pack_b) {
-        const dlcStatus_t st = pack_rows(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
+    if (pl.pack_a || pl.pack_b) {
+        PackParams pk;
+        int jobs = 0;
+        if (pl.pack_a) pk.job[jobs++] = pack_job(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
+        if (pl.pack_b) pk.job[jobs++] = pack_job(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
+        if (jobs == 1) pk.job[1] = pk.job[0];
+        const dim3 grid(std::max(pk.job[0].gx, pk.job[1].gx), std::max(pk.job[0].gy, pk.job[1].gy), (unsigned)jobs);
+        void *args[] = {&pk};
+        const dlcStatus_t st = dlc_launch(ctx, (const void *)pack_kernel, grid, dim3(256), 0, args);
         if (st != DLC_STATUS_SUCCESS) return st;
     }
     return pl.few_rows ? dlc_launch_few_rows(ctx, g) : launch_pair(ctx, g, pl);

@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
 // rows share the loads.  Otherwise (a row too long for registers): one row a
 // block, its channels dealt to the threads.  The second pass recomputes t (so t
 // may overwrite x or r in place).
+constexpr int AHEAD = 4;  // channels a thread loads at once
+
 template <bool LANES>
 struct AnyMap {
     static constexpr int ROWS = LANES ? 32 : 1, STEP = LANES ? 8 : RMS_THREADS;
@@ -227,11 +229,20 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
         const bool on = row < p.rows;
         const long long xo = on ? row_off(p.x.m, row) : 0, ro = on && p.r.p ? row_off(p.r.m, row) : 0;
         float sq = 0.f, mx = 0.f;
-        for (int c = M::first(); on && c < p.C; c += M::STEP) {
-            float v = load_elem(p.x.p, p.x.dt, xo + c * p.x.m.cs);
-            if (p.r.p) v += load_elem(p.r.p, p.r.dt, ro + c * p.r.m.cs);
-            sq = fmaf(v, v, sq);
-            mx = fmaxf(mx, fabsf(v * __ldg(p.gamma + c)));
+        float v[AHEAD], r[AHEAD];
+        for (int c = M::first(); on && c < p.C; c += AHEAD * M::STEP) {
+            const auto in = [&](int i) { return c + i * M::STEP < p.C; };
+            load_elems<AHEAD>(p.x.p, p.x.dt, xo + c * p.x.m.cs, M::STEP * p.x.m.cs, in, v);
+            if (p.r.p) {
+                load_elems<AHEAD>(p.r.p, p.r.dt, ro + c * p.r.m.cs, M::STEP * p.r.m.cs, in, r);
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) v[i] += r[i];
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                sq = fmaf(v[i], v[i], sq);
+                mx = fmaxf(mx, fabsf(v[i] * (in(i) ? __ldg(p.gamma + c + i * M::STEP) : 0.f)));
+            }
         }
         const float2 red = M::template join<true>(sq, mx, part);
         if (!on) continue;
@@ -242,11 +253,21 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
             f = f / s;
         }
         const long long to = p.t.p ? row_off(p.t.m, row) : 0, yo = row_off(p.y.m, row);
-        for (int c = M::first(); c < p.C; c += M::STEP) {
-            float v = load_elem(p.x.p, p.x.dt, xo + c * p.x.m.cs);
-            if (p.r.p) v += load_elem(p.r.p, p.r.dt, ro + c * p.r.m.cs);
-            if (p.t.p) store_elem(p.t.p, p.t.dt, to + c * p.t.m.cs, v);
-            store_elem(p.y.p, p.y.dt, yo + c * p.y.m.cs, v * __ldg(p.gamma + c) * f);
+        for (int c = M::first(); c < p.C; c += AHEAD * M::STEP) {
+            const auto in = [&](int i) { return c + i * M::STEP < p.C; };
+            load_elems<AHEAD>(p.x.p, p.x.dt, xo + c * p.x.m.cs, M::STEP * p.x.m.cs, in, v);
+            if (p.r.p) {
+                load_elems<AHEAD>(p.r.p, p.r.dt, ro + c * p.r.m.cs, M::STEP * p.r.m.cs, in, r);
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) v[i] += r[i];
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int ci = c + i * M::STEP;
+                if (ci >= p.C) break;
+                if (p.t.p) store_elem(p.t.p, p.t.dt, to + ci * p.t.m.cs, v[i]);
+                store_elem(p.y.p, p.y.dt, yo + ci * p.y.m.cs, v[i] * __ldg(p.gamma + ci) * f);
+            }
         }
     }
 }
@@ -349,32 +370,40 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
         const bool on = row < p.rows;
         const long long yo = on ? row_off(p.dy.m, row) : 0, to = on ? row_off(p.t.m, row) : 0;
         float sq = 0.f, dot = 0.f;
-        for (int c = M::first(); on && c < p.C; c += M::STEP) {
-            const float v = load_elem(p.t.p, p.t.dt, to + c * p.t.m.cs);
-            const float d = load_elem(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs) * __ldg(p.gamma + c);
-            sq = fmaf(v, v, sq);
-            dot = fmaf(d, v, dot);
+        float v[AHEAD], d[AHEAD], a[AHEAD];
+        for (int c = M::first(); on && c < p.C; c += AHEAD * M::STEP) {
+            const auto in = [&](int i) { return c + i * M::STEP < p.C; };
+            load_elems<AHEAD>(p.t.p, p.t.dt, to + c * p.t.m.cs, M::STEP * p.t.m.cs, in, v);
+            load_elems<AHEAD>(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs, M::STEP * p.dy.m.cs, in, d);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                sq = fmaf(v[i], v[i], sq);
+                dot = fmaf(d[i] * (in(i) ? __ldg(p.gamma + c + i * M::STEP) : 0.f), v[i], dot);
+            }
         }
         const float2 red = M::template join<false>(sq, dot, part);
         const float rho = on ? rsqrtf(red.x / (float)p.C + p.eps) : 0.f;
         const float k = rho * rho * rho * (red.y / (float)p.C);
         const long long xo = on ? row_off(p.dx.m, row) : 0, so = on && p.dt.p ? row_off(p.dt.m, row) : 0;
-        for (int c = M::first(); c < p.C; c += M::STEP) {
-            float a = 0.f;
-            if (on) {
-                const float v = load_elem(p.t.p, p.t.dt, to + c * p.t.m.cs);
-                const float d = load_elem(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs);
-                a = d * rho * v;
-                float s = p.dt.p ? load_elem(p.dt.p, p.dt.dt, so + c * p.dt.m.cs) : 0.f;
-                s += rho * d * __ldg(p.gamma + c) - v * k;
-                store_elem(p.dx.p, p.dx.dt, xo + c * p.dx.m.cs, s);
-            }
-            if (p.dgamma) {
+        for (int c = M::first(); c < p.C; c += AHEAD * M::STEP) {
+            const auto in = [&](int i) { return on && c + i * M::STEP < p.C; };
+            load_elems<AHEAD>(p.t.p, p.t.dt, to + c * p.t.m.cs, M::STEP * p.t.m.cs, in, v);
+            load_elems<AHEAD>(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs, M::STEP * p.dy.m.cs, in, d);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) a[i] = 0.f;
+            if (p.dt.p) load_elems<AHEAD>(p.dt.p, p.dt.dt, so + c * p.dt.m.cs, M::STEP * p.dt.m.cs, in, a);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int ci = c + i * M::STEP;
+                if (ci >= p.C) break;
+                if (on) store_elem(p.dx.p, p.dx.dt, xo + ci * p.dx.m.cs, a[i] + rho * d[i] * __ldg(p.gamma + ci) - v[i] * k);
+                if (!p.dgamma) continue;
+                float g = d[i] * rho * v[i];
                 if (LANES)
-                    for (int o = 16; o > 0; o /= 2) a += __shfl_xor_sync(0xffffffffu, a, o);
+                    for (int o = 16; o > 0; o /= 2) g += __shfl_xor_sync(0xffffffffu, g, o);
                 if (!LANES || M::row() == 0) {
-                    float *w = p.ws + (long long)blockIdx.x * p.C + c;
-                    *w = first ? a : *w + a;
+                    float *w = p.ws + (long long)blockIdx.x * p.C + ci;
+                    *w = first ? g : *w + g;
                 }
             }
         }

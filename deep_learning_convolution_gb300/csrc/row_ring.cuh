@@ -27,26 +27,40 @@ struct Cols {
 // nothing past the row is touched.
 template <int W, int V>
 __device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
+    if constexpr (W == 1) {
+        if (t.dt == DLC_DATA_BFLOAT16) {
+            const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
+            unsigned short w[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float *v = f + j * W;
-        if (W == 8 && k.n[j] == W) {
-            if (t.dt == DLC_DATA_BFLOAT16) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            for (int j = 0; j < V; ++j) w[j] = k.n[j] ? p[k.c[j] * t.m.cs] : (unsigned short)0;
 #pragma unroll
-                for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
-            } else {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
-#pragma unroll
-                for (int i = 0; i < W / 4; ++i) {
-                    const float4 a = p[i];
-                    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
-                }
-            }
+            for (int j = 0; j < V; ++j) f[j] = bf16_bits_f32(w[j]);
         } else {
+            const float *p = static_cast<const float *>(t.p) + off;
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = i < k.n[j] ? load_elem(t.p, t.dt, off + (k.c[j] + i) * t.m.cs) : 0.f;
+            for (int j = 0; j < V; ++j) f[j] = k.n[j] ? p[k.c[j] * t.m.cs] : 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float *v = f + j * W;
+            if (k.n[j] == W) {
+                if (t.dt == DLC_DATA_BFLOAT16) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
+                } else {
+                    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i) {
+                        const float4 a = p[i];
+                        v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+                    }
+                }
+            } else {
+                load_elems<W>(t.p, t.dt, off + k.c[j], 1, [&](int i) { return i < k.n[j]; }, v);
+            }
         }
     }
 }
