@@ -352,6 +352,8 @@ class _ChannelOp:
     are dense FP32), launch on the handle's stream and return no copies."""
 
     def __init__(self, handle: Handle, axes: str):
+        import torch
+        self._f32 = torch.float32
         self.handle = handle
         self.axes = axes
         self._tensors, self._filters = [], []
@@ -391,13 +393,11 @@ class _ChannelOp:
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
             self._ws_ptr = self.workspace.data_ptr()
 
-    @staticmethod
-    def _vector(t, n: int, what: str) -> int:
+    def _vector(self, t, n: int, what: str) -> int:
         """Pointer of an optional dense FP32 vector of n elements."""
-        import torch
         if t is None:
             return 0
-        if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        if t.dtype is not self._f32 or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{what} must be a dense float32 vector of {n} elements")
         return t.data_ptr()
 

@@ -62,6 +62,7 @@ DLC_KERNEL_POOL_NHWC = 9
 DLC_KERNEL_TC_ROWSTACK = 10
 DLC_KERNEL_GEMM_PAIR = 11
 DLC_KERNEL_FEW_ROWS = 12
+DLC_KERNEL_GEMV = 13
 DLC_DEVERR_NONE = 0
 DLC_DEVERR_WAIT_TIMEOUT = 1
 
@@ -72,7 +73,7 @@ KERNEL_NAMES = {DLC_KERNEL_NONE: "none", DLC_KERNEL_FFMA: "ffma",
                 DLC_KERNEL_TC_WGRAD: "tc_wgrad", DLC_KERNEL_POOL_NHWC: "pool_nhwc",
                 DLC_KERNEL_TC_ROWSTACK: "tc_rowstack",
                 DLC_KERNEL_GEMM_PAIR: "gemm_pair",
-                DLC_KERNEL_FEW_ROWS: "few_rows"}
+                DLC_KERNEL_FEW_ROWS: "few_rows", DLC_KERNEL_GEMV: "gemv"}
 
 _h = c_void_p          # opaque handle / descriptor
 _ph = POINTER(c_void_p)
@@ -207,7 +208,9 @@ def _check(name: str, status: int):
 
 
 def _call(name, *args):
-    _check(name, getattr(load_library(), name)(*args))
+    status = getattr(_lib or load_library(), name)(*args)
+    if status:
+        _check(name, status)
 
 
 # ---------------------------------------------------------------------------

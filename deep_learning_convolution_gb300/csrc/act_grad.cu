@@ -170,11 +170,7 @@ dlcStatus_t dlc_launch_act_grad(dlcContext *ctx, const ActGradProblem &pb) {
     const bool bf = g.w == 8 && p.dy.dt == DLC_DATA_BFLOAT16 && (!p.z.p || p.z.dt == DLC_DATA_BFLOAT16);
     const void *kern = bf ? ag_kernel<8, true>(p) : g.w == 8 ? ag_kernel<8, false>(p) : ag_kernel<1, false>(p);
     const size_t smem = bf ? (size_t)AG_RING * (p.gated ? 3 : p.z.p ? 2 : 1) * 16 * AG_WARPS * 32 : 0;
-    if (smem > 32 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return DLC_STATUS_EXECUTION_FAILED;
-    }
+    if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const dlcStatus_t st = dlc_launch(ctx, kern, dim3(g.gx, g.gy), dim3(AG_WARPS * 32), smem, args);
     if (st != DLC_STATUS_SUCCESS || !p.dbias) return st;
     return dlc_launch_column_sum(ctx, p.ws, p.dbias, p.gated ? 2 * p.N : p.N, (int)g.gy);

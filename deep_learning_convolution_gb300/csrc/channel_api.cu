@@ -3,6 +3,7 @@
 // projections, and their backward passes.  Validation, the split of a backward
 // pass into its products, and workspace layout; the kernels are in rmsnorm.cu,
 // gemm.cu and act_grad.cu.
+#include <atomic>
 #include <cstring>
 #include <initializer_list>
 
@@ -31,6 +32,38 @@ dlcStatus_t dlc_launch(dlcContext *ctx, const void *kernel, dim3 grid, dim3 bloc
     }
     ctx->launches += 1;
     return DLC_STATUS_SUCCESS;
+}
+
+bool dlc_allow_smem(const dlcContext *ctx, const void *kernel, size_t bytes) {
+    // what each kernel has been allowed so far (it is a property of the kernel
+    // and the device, not of a call); beyond the table's room it is set every time
+    struct Entry {
+        const void *kernel;
+        int device;
+        size_t bytes;
+    };
+    static Entry table[128];
+    static int used = 0;
+    static std::atomic_flag busy = ATOMIC_FLAG_INIT;
+    if (bytes <= 47 * 1024) return true;  // (48 KiB with the static part need no leave)
+    while (busy.test_and_set(std::memory_order_acquire)) {
+    }
+    Entry *e = nullptr;
+    for (int i = 0; i < used && !e; ++i)
+        if (table[i].kernel == kernel && table[i].device == ctx->device) e = &table[i];
+    bool ok = e && e->bytes >= bytes;
+    if (!ok) {
+        ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+        if (!ok) {
+            cudaGetLastError();
+        } else if (e) {
+            e->bytes = bytes;
+        } else if (used < 128) {
+            table[used++] = Entry{kernel, ctx->device, bytes};
+        }
+    }
+    busy.clear(std::memory_order_release);
+    return ok;
 }
 
 namespace {

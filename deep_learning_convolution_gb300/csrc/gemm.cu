@@ -754,7 +754,7 @@ struct GemmPlan {
     int full_tiles, splits;     // tiles from full_tiles on are split
     long long a_rows, b_rows;
     int a_ch, b_ch;             // channels of the operands' rows
-    bool pack_a, pack_b, few_rows;
+    bool pack_a, pack_b, few_rows, gemv;
     size_t a_off, b_off, part_off, bytes;
 };
 
@@ -767,8 +767,9 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.a_ch = (int)(g.a.trans ? g.M : g.K);
     p.b_rows = g.b.trans ? g.K : nb;
     p.b_ch = (int)(g.b.trans ? nb : g.K);
-    p.pack_a = !tma_rows(g.a.t, p.a_rows, p.a_ch);
-    p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
+    p.gemv = dlc_gemv_ok(g);
+    p.pack_a = !p.gemv && !tma_rows(g.a.t, p.a_rows, p.a_ch);
+    p.pack_b = !p.gemv && !tma_rows(g.b.t, p.b_rows, p.b_ch);
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     // Tile width, split of the tail, and which of the two kernels, from a model of
@@ -813,7 +814,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.b_off = off;
     if (p.pack_b) off += packed(p.b_rows, p.b_ch);
     p.part_off = off;
-    if (!p.few_rows) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
+    if (!p.few_rows && !p.gemv) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
     p.bytes = off;
     return p;
 }
@@ -973,10 +974,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - 1024 - GP_BAR_AREA - epi_bytes) / stage_bytes);
     const size_t smem = 1024 + (size_t)p.stages * stage_bytes + epi_bytes + GP_BAR_AREA;
     const void *kern = pair_kernel(e4m3, g.a.trans != 0, g.b.trans != 0, g.gated != 0);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return DLC_STATUS_EXECUTION_FAILED;
-    }
+    if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);
     void *args[] = {&p, &ta, &tb, &ty, &tz, &tp};
     dlcStatus_t st = dlc_launch(ctx, kern, dim3((unsigned)(2 * clusters)), dim3(GP_THREADS), smem, args, 2);
@@ -1012,7 +1010,8 @@ bool dlc_encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperan
 }
 
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
-    return plan_gemm(ctx, g).few_rows ? DLC_KERNEL_FEW_ROWS : DLC_KERNEL_GEMM_PAIR;
+    const GemmPlan p = plan_gemm(ctx, g);
+    return p.gemv ? DLC_KERNEL_GEMV : p.few_rows ? DLC_KERNEL_FEW_ROWS : DLC_KERNEL_GEMM_PAIR;
 }
 
 size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g) { return plan_gemm(ctx, g).bytes; }
@@ -1031,5 +1030,6 @@ dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &pb) {
         const dlcStatus_t st = dlc_launch(ctx, (const void *)pack_kernel, grid, dim3(256), 0, args);
         if (st != DLC_STATUS_SUCCESS) return st;
     }
+    if (pl.gemv) return dlc_launch_gemv(ctx, g);
     return pl.few_rows ? dlc_launch_few_rows(ctx, g) : launch_pair(ctx, g, pl);
 }

@@ -12,6 +12,11 @@ struct FewRowsPlan {
 FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g);
 dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g);
 
+// gemv.cu: a few rows on the CUDA cores, operands as they are.  Whether it is
+// the faster way, and the launch.
+bool dlc_gemv_ok(const GemmProblem &g);
+dlcStatus_t dlc_launch_gemv(dlcContext *ctx, const GemmProblem &g);
+
 // gemm.cu: a row operand's tensor map.
 bool dlc_encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperand &o, long long rows, int ch, int box_rows);
 

@@ -280,7 +280,7 @@ int resident_clusters(const dlcContext *ctx, int size) {
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+    if (!dlc_allow_smem(ctx, kern, (size_t)smem) ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         return std::max(1, ctx->sm_count / size);
@@ -360,10 +360,7 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
         return DLC_STATUS_EXECUTION_FAILED;
     const void *kern = g.gated ? (e4m3 ? (const void *)gemm_rows_kernel<true, true> : (const void *)gemm_rows_kernel<false, true>)
                                : (e4m3 ? (const void *)gemm_rows_kernel<true, false> : (const void *)gemm_rows_kernel<false, false>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return DLC_STATUS_EXECUTION_FAILED;
-    }
+    if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     void *args[] = {&p, &tw, &tx};
     return dlc_launch(ctx, kern, dim3((unsigned)(pl.filter_tiles * pl.splits), (unsigned)pl.row_tiles), dim3(FR_THREADS), smem,
                       args, pl.splits);

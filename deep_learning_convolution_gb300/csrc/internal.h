@@ -301,3 +301,6 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &p);
 // before it (see dlc_pdl_enabled); counts it.  Defined in channel_api.cu.
 dlcStatus_t dlc_launch(dlcContext *ctx, const void *kernel, dim3 grid, dim3 block, size_t smem, void **args,
                        int cluster = 1);
+// Lets a kernel of the channel operators use `bytes` of dynamic shared memory.
+// False where the device refuses.  Defined in channel_api.cu.
+bool dlc_allow_smem(const dlcContext *ctx, const void *kernel, size_t bytes);

@@ -493,14 +493,6 @@ struct RowKernel {
     size_t smem;
 };
 
-// More than 48 KiB of shared memory (the static part included) has to be asked for.
-bool allow_smem(const RowKernel &k, size_t smem) {
-    if (smem <= 47 * 1024) return true;
-    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) return true;
-    cudaGetLastError();
-    return false;
-}
-
 template <int W, int V, bool BF, int MAXT>
 RowKernel fwd_entry(const RowPlan &r) {
     return {(const void *)rms_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 2, ring_rows<MAXT>()>::smem(r.threads)};
@@ -540,7 +532,7 @@ dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
         : r.w == 1 ? fwd_kernel<1, false>(r)
         : is_bf16(p.x) && is_bf16(p.r) ? fwd_kernel<8, true>(r) : fwd_kernel<8, false>(r);
-    if (!allow_smem(k, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
+    if (!dlc_allow_smem(ctx, k.fn, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
     return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
 
@@ -562,7 +554,7 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
         : is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt) ? bwd_kernel<8, true>(r) : bwd_kernel<8, false>(r);
     const int rpb = r.w ? r.threads / r.tpr : 1;
     const size_t smem = std::max(k.smem, rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0);
-    if (!allow_smem(k, smem)) return DLC_STATUS_EXECUTION_FAILED;
+    if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;
     dlcStatus_t st = dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), smem, args);
     if (st != DLC_STATUS_SUCCESS || !p.dgamma) return st;
     return dlc_launch_column_sum(ctx, p.ws, p.dgamma, p.C, (int)r.blocks);

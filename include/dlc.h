@@ -164,8 +164,10 @@ typedef enum {
                                      read in place from shifted copies of input rows */
     DLC_KERNEL_GEMM_PAIR = 11,    /* channel operators: tcgen05 products on pairs of SMs, 256 rows
                                      a tile, operands by TMA */
-    DLC_KERNEL_FEW_ROWS = 12      /* channel operators: tcgen05 products with the filters as the
+    DLC_KERNEL_FEW_ROWS = 12,     /* channel operators: tcgen05 products with the filters as the
                                      MMA's M side, the reduction split over a cluster */
+    DLC_KERNEL_GEMV = 13          /* channel operators: up to four rows on the CUDA cores, filters
+                                     streamed by every warp */
 } dlcKernel_t;
 
 /* Device error codes recorded by kernels (dlcGetLastDeviceError). */
