@@ -44,12 +44,19 @@ constexpr int GP_EPI_WARP0 = 3, GP_EPI_WARPS = 8;
 constexpr int GP_THREADS = (GP_EPI_WARP0 + GP_EPI_WARPS) * 32;
 constexpr int GP_MAX_SMEM = 232448, GP_BAR_AREA = 256, GP_MAX_STAGES = 8;
 
+// Tiles in groups of eight row blocks (below), with the division by a group's size.
+struct GpTiles {
+    int m_tiles, n_tiles;
+    uint32_t per, mul, shift;  // tiles of a group; t / per = (t * mul) >> (32 + shift)
+};
+
 struct GpParams {
     long long M;
     int N, act;
     int BN, nout;                 // accumulator columns of a tile, outputs of a tile (gated: BN / 2)
     int stages, num_kb;
-    int m_tiles, n_tiles, units;
+    GpTiles tiles;
+    int units;
     int full_tiles, splits;       // tiles from full_tiles on: `splits` units each, FP32 partial sums, no epilogue
     uint32_t b_stage;             // bytes of one CTA's half of b per stage
     int b_atoms;                  // MN-major b: 64-index blocks per CTA
@@ -69,11 +76,13 @@ struct GpUnit {
 
 // Rows and column tile of tile t: groups of eight row blocks, so that the pairs
 // that run together share rows of both operands in the L2.
-__host__ __device__ __forceinline__ void gp_tile(int t, int m_tiles, int n_tiles, long long &m0, int &nt) {
-    const int per = 8 * n_tiles, grp = t / per, in = t - grp * per;
-    const int rows = m_tiles - grp * 8 < 8 ? m_tiles - grp * 8 : 8;
-    nt = in / rows;
-    m0 = (long long)(grp * 8 + in - nt * rows) * (2 * GP_ROWS);
+// (Divisions are worked out without the divide where they can be: they and the
+// kernel's other per-tile integer work are 1100 cycles of an epilogue otherwise.)
+__device__ __forceinline__ void gp_tile(const GpTiles &g, int t, int &mt, int &nt) {
+    const int grp = (int)(__umulhi((uint32_t)t, g.mul) >> g.shift), in = t - grp * (int)g.per;
+    const int rows = g.m_tiles - grp * 8;
+    nt = rows >= 8 ? in >> 3 : in / rows;
+    mt = grp * 8 + in - nt * (rows >= 8 ? 8 : rows);
 }
 
 __device__ __forceinline__ GpUnit gp_unit(const GpParams &p, int u) {
@@ -90,7 +99,9 @@ __device__ __forceinline__ GpUnit gp_unit(const GpParams &p, int u) {
         w.kb0 = (int)((long long)p.num_kb * split / p.splits);
         w.kb1 = (int)((long long)p.num_kb * (split + 1) / p.splits);
     }
-    gp_tile(t, p.m_tiles, p.n_tiles, w.m0, w.nt);
+    int mt;
+    gp_tile(p.tiles, t, mt, w.nt);
+    w.m0 = (long long)mt * (2 * GP_ROWS);
     return w;
 }
 
@@ -396,8 +407,8 @@ struct GpResidual {
     }
 };
 
-template <bool GATED>
-__device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
+template <bool GATED, int ACT>
+__device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
                             uint32_t epi_smem, const CUtensorMap *tmY, const CUtensorMap *tmZ, const CUtensorMap *tmP,
                             const WaitCtl &ctl) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -474,10 +485,8 @@ __device__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base
                     if constexpr (GATED) st.rows(p.z, zo, up, (long long)p.N + n, cols, nullptr, 0);
                 }
             }
-            act_dispatch(p.act, [&](auto act) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = act_f<decltype(act)::value>(v[i]);
-            });
+            for (int i = 0; i < 32; ++i) v[i] = act_f<ACT>(v[i]);
             if constexpr (GATED) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= up[i];
@@ -566,7 +575,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             mbar_wait(mma_done, 0u, fin, 93);
         }
     } else {
-        gp_epilogue<GATED>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, &tmP, ctl);
+        // (the activation's branch out here: a block's code is straight)
+        act_dispatch(p.act, [&](auto act) {
+            gp_epilogue<GATED, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, &tmP, ctl);
+        });
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -581,7 +593,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
 struct FinishParams {
     GemmProblem g;
     const float *part;  // [tail tile][range][256][bn] FP32
-    int bn, nout, m_tiles, n_tiles, full_tiles, tail, splits;
+    GpTiles tiles;
+    int bn, nout, full_tiles, tail, splits;
     int vec;            // y, z and r take 4-element accesses
 };
 
@@ -597,10 +610,9 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
         const int t = (int)(i / per_tile), in = (int)(i - (long long)t * per_tile);
         const int r = in / per_row, c = (in - r * per_row) * 4;
-        long long m;
-        int nt;
-        gp_tile(f.full_tiles + t, f.m_tiles, f.n_tiles, m, nt);
-        m += r;
+        int mt, nt;
+        gp_tile(f.tiles, f.full_tiles + t, mt, nt);
+        const long long m = (long long)mt * (2 * GP_ROWS) + r;
         const int n = nt * f.nout + c, cols = g.N - n;
         if (m >= g.M || cols <= 0) continue;
         float v[2][4];
@@ -913,6 +925,19 @@ int resident_pairs(const dlcContext *ctx, const void *kern, size_t smem) {
     return n;
 }
 
+GpTiles tiles_of(const GemmPlan &pl) {
+    GpTiles t;
+    t.m_tiles = pl.m_tiles;
+    t.n_tiles = pl.n_tiles;
+    // exact for tile numbers below 2^31: mul = ceil(2^(32 + shift) / per) with
+    // 2^shift >= per / 2 leaves an error below 2^31 * per / 2^(32 + shift) <= 1 ulp
+    t.per = 8u * (uint32_t)pl.n_tiles;
+    t.shift = 0;
+    while ((2ull << t.shift) < t.per) ++t.shift;
+    t.mul = (uint32_t)(((1ull << (32 + t.shift)) + t.per - 1) / t.per);
+    return t;
+}
+
 dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &pl) {
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
     GpParams p;
@@ -923,8 +948,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.BN = pl.bn;
     p.nout = pl.nout;
     p.num_kb = pl.num_kb;
-    p.m_tiles = pl.m_tiles;
-    p.n_tiles = pl.n_tiles;
+    p.tiles = tiles_of(pl);
     if ((long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     const int tail = pl.m_tiles * pl.n_tiles - pl.full_tiles;
     p.full_tiles = pl.full_tiles;
@@ -984,8 +1008,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     f.part = reinterpret_cast<const float *>(g.ws + pl.part_off);
     f.bn = pl.bn;
     f.nout = pl.nout;
-    f.m_tiles = pl.m_tiles;
-    f.n_tiles = pl.n_tiles;
+    f.tiles = p.tiles;
     f.full_tiles = pl.full_tiles;
     f.tail = tail;
     f.splits = pl.splits;
