@@ -33,36 +33,59 @@ constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 template <int MAXT>
 constexpr int ring_rows() { return MAXT > 512 ? 2 : 3; }
 
-template <int W>
-__device__ __forceinline__ void store_vec(const RowTensor &t, long long off, int n, const float *v) {
-    if (W == 8 && n == W) {
+// The row's vectors (W = 8), or its single elements a fixed step apart (W = 1).
+template <int W, int V>
+__device__ __forceinline__ void store_row(const RowTensor &t, long long off, const Cols<W, V> &k, const float (&f)[V * W]) {
+    if constexpr (W == 1) {
+        const long long at = off + k.c[0];
         if (t.dt == DLC_DATA_BFLOAT16) {
-            uint32_t w[4];
+            unsigned short *p = static_cast<unsigned short *>(t.p) + at;
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < V; ++j, p += k.step)
+                if (j < k.count) *p = (unsigned short)pack_bf16(f[j], 0.f);
         } else if (t.dt == DLC_DATA_FLOAT) {
-            float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(t.p) + off);
+            float *p = static_cast<float *>(t.p) + at;
 #pragma unroll
-            for (int i = 0; i < W / 4; ++i) f[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int j = 0; j < V; ++j, p += k.step)
+                if (j < k.count) *p = f[j];
         } else {
-            uint32_t w[2];
+            unsigned char *p = static_cast<unsigned char *>(t.p) + at;
 #pragma unroll
-            for (int i = 0; i < W / 4; ++i)
-                w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
-            *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(t.p) + off) = make_uint2(w[0], w[1]);
+            for (int j = 0; j < V; j += 2, p += 2 * k.step) {
+                const uint32_t q = pack_e4m3(f[j], f[j + 1]);
+                if (j < k.count) p[0] = (unsigned char)q;
+                if (j + 1 < k.count) p[k.step] = (unsigned char)(q >> 8);
+            }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (i < n) store_elem(t.p, t.dt, off + i, v[i]);
-    }
-}
-
-template <int W, int V>
-__device__ __forceinline__ void store_row(const RowTensor &t, long long off, const Cols<W, V> &k, const float (&f)[V * W]) {
+        for (int j = 0; j < V; ++j) {
+            const float *v = f + j * W;
+            const long long at = off + k.c[j];
+            if (k.n[j] == W) {
+                if (t.dt == DLC_DATA_BFLOAT16) {
+                    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < V; ++j) store_vec<W>(t, off + k.c[j], k.n[j], f + j * W);
+                    for (int i = 0; i < W / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                    *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else if (t.dt == DLC_DATA_FLOAT) {
+                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(t.p) + at);
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else {
+                    uint32_t w[2];
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i)
+                        w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
+                    *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(t.p) + at) = make_uint2(w[0], w[1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    if (i < k.n[j]) store_elem(t.p, t.dt, at + i, v[i]);
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ float2 pair(const float *f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
@@ -465,7 +488,7 @@ RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, int per_sm, int sm_
         while (v < v_max && tpr * v < nv && tpr == 32) v *= 2;
         while (tpr < 1024 && (long long)tpr * v < nv) tpr *= 2;
         if ((long long)tpr * v < nv) r.w = 0;  // longer than a block's registers
-        r.v = v == 4 ? 8 : v;
+        r.v = v;
         r.tpr = tpr;
         if (r.w && tpr > RMS_THREADS) r.threads = tpr;
     }
@@ -504,6 +527,7 @@ RowKernel fwd_kernel(const RowPlan &r) {
     if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r);
     if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r);
     if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r);
+    if (W == 1 && r.v == 4) return fwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r);
     return fwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
 }
 
@@ -518,6 +542,7 @@ RowKernel bwd_kernel(const RowPlan &r) {
     if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r);
     if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r);
     if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r);
+    if (W == 1 && r.v == 4) return bwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r);
     return bwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
 }
 

@@ -13,12 +13,17 @@ template <int W, int V>
 struct Cols {
     int c[V];   // first channel of each vector, 0 where the vector is past the row
     int n[V];   // channels of it that exist, 0 .. W
+    int count;  // vectors that exist (the first ones)
+    int step;   // channels from one vector to the next
     __device__ __forceinline__ Cols(int t, int tpr, int C) {
+        step = tpr * W;
+        count = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int at = (t + j * tpr) * W;
             n[j] = min(max(C - at, 0), W);
             c[j] = n[j] ? at : 0;
+            count += n[j] ? 1 : 0;
         }
     }
 };
@@ -27,18 +32,19 @@ struct Cols {
 // nothing past the row is touched.
 template <int W, int V>
 __device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
-    if constexpr (W == 1) {
+    if constexpr (W == 1) {  // single elements a fixed step apart
+        const long long at = off + k.c[0] * t.m.cs, step = k.step * t.m.cs;
         if (t.dt == DLC_DATA_BFLOAT16) {
-            const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
+            const unsigned short *p = static_cast<const unsigned short *>(t.p) + at;
             unsigned short w[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) w[j] = k.n[j] ? p[k.c[j] * t.m.cs] : (unsigned short)0;
+            for (int j = 0; j < V; ++j, p += step) w[j] = j < k.count ? *p : (unsigned short)0;
 #pragma unroll
             for (int j = 0; j < V; ++j) f[j] = bf16_bits_f32(w[j]);
         } else {
-            const float *p = static_cast<const float *>(t.p) + off;
+            const float *p = static_cast<const float *>(t.p) + at;
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = k.n[j] ? p[k.c[j] * t.m.cs] : 0.f;
+            for (int j = 0; j < V; ++j, p += step) f[j] = j < k.count ? *p : 0.f;
         }
     } else {
 #pragma unroll
