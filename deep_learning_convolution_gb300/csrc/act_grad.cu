@@ -49,7 +49,7 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
     if (n <= 0) return;
     RowWalk wy(p.dy.m, row, step), wz(p.z.m, row, step), wd(p.dz.m, row, step);
     Rows<W, 1, BF, T, AG_RING> rows;
-    rows.start(ring);
+    rows.start(ring, 0, 0, 0, 0);
     const long long up = (long long)p.N * p.z.m.cs;
     auto fetch = [&]() {
         if (ahead < p.rows) {
@@ -65,7 +65,7 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
     for (int i = 0; i < rows.AHEAD; ++i) fetch();
     for (; row < p.rows; row += step, wd.next()) {
         float f[T][W];
-        rows.take(f);
+        rows.take(f, cols, {});
         fetch();
         float b[W];
 #pragma unroll

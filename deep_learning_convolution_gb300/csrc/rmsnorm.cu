@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     const Cols<W, V> cols(t, tpr, p.C);
     const float inv_c = 1.f / (float)p.C;
     const bool e4m3 = p.y.dt == DLC_DATA_FLOAT8_E4M3;
+    griddep_wait();
     float g[E];
 #pragma unroll
     for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
-    griddep_wait();
     Rows<W, V, BF, 2, ring_rows<MAXT>()> rows;
-    rows.start(smem_u32(ring_s));
+    rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
     RowWalk wx(p.x.m, row, step), wr(p.r.m, row, step), wt(p.t.m, row, step), wy(p.y.m, row, step);
     auto fetch = [&]() {
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wt.next(), wy.next()) {
         const bool on = row < p.rows;
         float f[2][E];
-        rows.take(f);
+        const uint32_t offs[2] = {(uint32_t)(row * p.x.m.ld), (uint32_t)(row * p.r.m.ld)};
+        rows.take(f, cols, offs);
         float *v = f[0];
         if (p.r.p) {
 #pragma unroll
@@ -308,14 +309,14 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     const long long step = (long long)gridDim.x * rpb;
     const Cols<W, V> cols(t, tpr, p.C);
     const float inv_c = 1.f / (float)p.C;
+    griddep_wait();
     float g[E], acc[E];
 #pragma unroll
     for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    griddep_wait();
     Rows<W, V, BF, 3, ring_rows<MAXT>()> rows;
-    rows.start(smem_u32(ring_s));
+    rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
     RowWalk wy(p.dy.m, row, step), wt(p.t.m, row, step), ws(p.dt.m, row, step), wx(p.dx.m, row, step);
     auto fetch = [&]() {
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wx.next()) {
         const bool on = row < p.rows;
         float f[3][E];
-        rows.take(f);
+        const uint32_t offs[3] = {(uint32_t)(row * p.dy.m.ld), (uint32_t)(row * p.t.m.ld), (uint32_t)(row * p.dt.m.ld)};
+        rows.take(f, cols, offs);
         float2 sq = make_float2(0.f, 0.f), dot = sq;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
@@ -509,6 +511,12 @@ RowPlan plan_bwd(const dlcContext *ctx, const RmsBwdProblem &p) {
                      vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), RMS_BWD_BLOCKS, ctx->sm_count);
 }
 
+// Rows that may be copied in the 16-byte pieces they touch: the first row
+// starts one, so no piece starts before the tensor.
+bool pieces_ok(const RowTensor &t) {
+    return !t.p || (t.dt == DLC_DATA_BFLOAT16 && t.m.uniform && (uintptr_t)t.p % 16 == 0);
+}
+
 bool is_bf16(const RowTensor &t) { return !t.p || t.dt == DLC_DATA_BFLOAT16; }
 
 struct RowKernel {
@@ -517,33 +525,33 @@ struct RowKernel {
 };
 
 template <int W, int V, bool BF, int MAXT>
-RowKernel fwd_entry(const RowPlan &r) {
-    return {(const void *)rms_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 2, ring_rows<MAXT>()>::smem(r.threads)};
+RowKernel fwd_entry(const RowPlan &r, int C) {
+    return {(const void *)rms_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 2, ring_rows<MAXT>()>::smem(r.threads, r.tpr, C)};
 }
 
 template <int W, bool BF>
-RowKernel fwd_kernel(const RowPlan &r) {
+RowKernel fwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
-    if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r);
-    if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r);
-    if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r);
-    if (W == 1 && r.v == 4) return fwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r);
-    return fwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
+    if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r, C);
+    if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r, C);
+    if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r, C);
+    if (W == 1 && r.v == 4) return fwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r, C);
+    return fwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r, C);
 }
 
 template <int W, int V, bool BF, int MAXT>
-RowKernel bwd_entry(const RowPlan &r) {
-    return {(const void *)rms_bwd_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 3, ring_rows<MAXT>()>::smem(r.threads)};
+RowKernel bwd_entry(const RowPlan &r, int C) {
+    return {(const void *)rms_bwd_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 3, ring_rows<MAXT>()>::smem(r.threads, r.tpr, C)};
 }
 
 template <int W, bool BF>
-RowKernel bwd_kernel(const RowPlan &r) {
+RowKernel bwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
-    if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r);
-    if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r);
-    if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r);
-    if (W == 1 && r.v == 4) return bwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r);
-    return bwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r);
+    if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r, C);
+    if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r, C);
+    if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r, C);
+    if (W == 1 && r.v == 4) return bwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r, C);
+    return bwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r, C);
 }
 
 }  // namespace
@@ -555,8 +563,8 @@ dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
     void *args[] = {&p, &tpr, &gamma_vec};
     const RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
-        : r.w == 1 ? fwd_kernel<1, false>(r)
-        : is_bf16(p.x) && is_bf16(p.r) ? fwd_kernel<8, true>(r) : fwd_kernel<8, false>(r);
+        : r.w == 1 ? (pieces_ok(p.x) && pieces_ok(p.r) ? fwd_kernel<1, true>(r, p.C) : fwd_kernel<1, false>(r, p.C))
+        : is_bf16(p.x) && is_bf16(p.r) ? fwd_kernel<8, true>(r, p.C) : fwd_kernel<8, false>(r, p.C);
     if (!dlc_allow_smem(ctx, k.fn, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
     return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
@@ -575,8 +583,8 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
     void *args[] = {&p, &tpr, &gamma_vec};
     const RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_bwd_any_kernel<true> : (const void *)rms_bwd_any_kernel<false>, 0}
-        : r.w == 1 ? bwd_kernel<1, false>(r)
-        : is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt) ? bwd_kernel<8, true>(r) : bwd_kernel<8, false>(r);
+        : r.w == 1 ? (pieces_ok(p.dy) && pieces_ok(p.t) && pieces_ok(p.dt) ? bwd_kernel<1, true>(r, p.C) : bwd_kernel<1, false>(r, p.C))
+        : is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt) ? bwd_kernel<8, true>(r, p.C) : bwd_kernel<8, false>(r, p.C);
     const int rpb = r.w ? r.threads / r.tpr : 1;
     const size_t smem = std::max(k.smem, rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0);
     if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;

@@ -79,25 +79,25 @@ template <int W, int V, bool BF, int T, int S>
 struct Rows {
     float next[T][V * W];
     static constexpr int AHEAD = 1;
-    __device__ __forceinline__ void start(uint32_t) {}
+    __device__ __forceinline__ void start(uint32_t, int, int, int, int) {}
     __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<W, V> &cols) {
         load_row<W, V>(t, off, cols, next[k]);
     }
     __device__ __forceinline__ void commit() {}
-    __device__ __forceinline__ void take(float (&f)[T][V * W]) {
+    __device__ __forceinline__ void take(float (&f)[T][V * W], const Cols<W, V> &, const uint32_t (&)[T]) {
 #pragma unroll
         for (int k = 0; k < T; ++k)
 #pragma unroll
             for (int i = 0; i < V * W; ++i) f[k][i] = next[k][i];
     }
-    static size_t smem(int) { return 0; }
+    static size_t smem(int, int, int) { return 0; }
 };
 
 template <int V, int T, int S>
 struct Rows<8, V, true, T, S> {
     uint32_t base, put, get, vec, row;  // this thread's slot 0, the rows to fill and to read, bytes between vectors / rows
     static constexpr int AHEAD = S - 1;
-    __device__ __forceinline__ void start(uint32_t smem) {
+    __device__ __forceinline__ void start(uint32_t smem, int, int, int, int) {
         base = smem + threadIdx.x * 16u;
         vec = 16u * blockDim.x;
         row = (uint32_t)(T * V) * vec;
@@ -112,7 +112,7 @@ struct Rows<8, V, true, T, S> {
         cp_async_commit();
         put = put == row * (S - 1) ? 0 : put + row;
     }
-    __device__ __forceinline__ void take(float (&f)[T][V * 8]) {
+    __device__ __forceinline__ void take(float (&f)[T][V * 8], const Cols<8, V> &, const uint32_t (&)[T]) {
         cp_async_wait<S - 2>();
 #pragma unroll
         for (int k = 0; k < T; ++k)
@@ -131,7 +131,57 @@ struct Rows<8, V, true, T, S> {
             }
         get = get == row * (S - 1) ? 0 : get + row;
     }
-    static size_t smem(int threads) { return (size_t)S * T * V * 16 * threads; }
+    static size_t smem(int threads, int, int) { return (size_t)S * T * V * 16 * threads; }
+};
+
+// BF16 rows at a pitch that is no multiple of 16 bytes, from a 16-byte aligned
+// base: the 16-byte pieces that a row touches come asynchronously into a ring of
+// rows, dealt to the row's threads (the first piece starts in the row before,
+// the last one ends with the row), and each thread takes its elements from
+// there.  `offs`: the rows' element offsets, of which the low bits count.
+template <int V, int T, int S>
+struct Rows<1, V, true, T, S> {
+    uint32_t base, put, get, row;  // this group's slot 0, the rows to fill and to read, bytes of a row of one tensor
+    int t, tpr, C, group;
+    static constexpr int AHEAD = S - 1;
+    static __host__ __device__ uint32_t row_bytes(int C) { return ((uint32_t)C * 2u + 14u + 15u) / 16u * 16u; }
+    __device__ __forceinline__ void start(uint32_t smem, int thread, int threads, int slot, int channels) {
+        t = thread, tpr = threads, group = slot, C = channels;
+        row = row_bytes(C);
+        base = smem + (uint32_t)slot * (uint32_t)(S * T) * row;
+        put = get = 0;
+    }
+    __device__ __forceinline__ void fetch(const RowTensor &x, int k, long long off, const Cols<1, V> &) {
+        const char *p = static_cast<const char *>(x.p) + off * 2;
+        const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u, bytes = shift + 2u * (uint32_t)C;
+        p -= shift;
+        const uint32_t dst = base + put + (uint32_t)k * row;
+        for (uint32_t i = (uint32_t)t * 16u; i < bytes; i += (uint32_t)tpr * 16u) cp_async_16(dst + i, p + i, min(16u, bytes - i));
+    }
+    __device__ __forceinline__ void commit() {
+        cp_async_commit();
+        put = put == (uint32_t)(T * (S - 1)) * row ? 0 : put + (uint32_t)T * row;
+    }
+    __device__ __forceinline__ void take(float (&f)[T][V], const Cols<1, V> &cols, const uint32_t (&offs)[T]) {
+        cp_async_wait<S - 2>();
+        // every thread's pieces have arrived, and the row before has been read
+        if (tpr > 32)
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+        else
+            __syncwarp();
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            uint32_t at = base + get + (uint32_t)k * row + ((offs[k] * 2u) & 15u) + 2u * (uint32_t)t;
+#pragma unroll
+            for (int j = 0; j < V; ++j, at += 2u * (uint32_t)tpr) {
+                unsigned short w = 0;
+                if (j < cols.count) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at) : "memory");
+                f[k][j] = bf16_bits_f32(w);
+            }
+        }
+        get = get == (uint32_t)(T * (S - 1)) * row ? 0 : get + (uint32_t)T * row;
+    }
+    static size_t smem(int threads, int tpr, int C) { return (size_t)S * T * row_bytes(C) * (threads / tpr); }
 };
 
 // Row offsets of one tensor along a thread's rows: added up where the rows
