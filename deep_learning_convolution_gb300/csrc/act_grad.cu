@@ -23,15 +23,18 @@ constexpr int AG_RING = 4;    // rows of the ring (one in use, three in flight)
 // dz is dense BF16 with rows of a multiple of 16 bytes, so only the vector's
 // own channels decide between the two stores.
 template <int W>
-__device__ __forceinline__ void ag_store(const RowTensor &t, long long off, int n, const float (&v)[W]) {
-    if (W == 8 && n == W) {
-        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + off) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (i < n) store_elem(t.p, t.dt, off + i, v[i]);
+__device__ __forceinline__ void ag_store(char *at, int n, const float (&v)[W]) {
+    unsigned short *p = reinterpret_cast<unsigned short *>(at);
+    if constexpr (W == 8) {
+        if (n == W) {
+            *reinterpret_cast<uint4 *>(p) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            return;
+        }
     }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (i < n) p[i] = (unsigned short)pack_bf16(v[i], 0.f);
 }
 
 // A vector's channels (W = 8), or one element at any stride (W = 1).  BF: dy and
@@ -47,20 +50,21 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
     const long long step = (long long)gridDim.y * AG_WARPS;
     long long row = (long long)blockIdx.y * AG_WARPS + warp, ahead = row;
     if (n <= 0) return;
-    RowWalk wy(p.dy.m, row, step), wz(p.z.m, row, step), wd(p.dz.m, row, step);
+    const long long cy = c * p.dy.m.cs, cz = c * p.z.m.cs, cu = cz + (long long)p.N * p.z.m.cs;
+    RowWalk wy(p.dy, row, step, cy), wz(p.z, row, step, cz), wu(p.z, row, step, cu), wd(p.dz, row, step, c);
     Rows<W, 1, BF, T, AG_RING> rows;
     rows.start(ring, 0, 0, 0, 0);
-    const long long up = (long long)p.N * p.z.m.cs;
     auto fetch = [&]() {
         if (ahead < p.rows) {
-            rows.fetch(p.dy, 0, wy.at(p.dy.m, ahead), cols);
-            if constexpr (READS_Z) rows.fetch(p.z, 1, wz.at(p.z.m, ahead), cols);
-            if constexpr (GATED) rows.fetch(p.z, 2, wz.at(p.z.m, ahead) + up, cols);
+            rows.fetch(p.dy, 0, wy.at(p.dy, ahead, cy), cols);
+            if constexpr (READS_Z) rows.fetch(p.z, 1, wz.at(p.z, ahead, cz), cols);
+            if constexpr (GATED) rows.fetch(p.z, 2, wu.at(p.z, ahead, cu), cols);
         }
         rows.commit();
         ahead += step;
         wy.next();
-        wz.next();
+        if constexpr (READS_Z) wz.next();
+        if constexpr (GATED) wu.next();
     };
     for (int i = 0; i < rows.AHEAD; ++i) fetch();
     for (; row < p.rows; row += step, wd.next()) {
@@ -82,9 +86,9 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
             if (SUM) sum[0][i] += f[0][i];
         }
         if (p.dz.p) {
-            const long long zo = wd.at(p.dz.m, row) + c;
-            ag_store<W>(p.dz, zo, n, f[0]);
-            if constexpr (GATED) ag_store<W>(p.dz, zo + p.N, n, b);
+            char *at = wd.at(p.dz, row, c);
+            ag_store<W>(at, n, f[0]);
+            if constexpr (GATED) ag_store<W>(at + 2 * p.N, n, b);
         }
     }
 }

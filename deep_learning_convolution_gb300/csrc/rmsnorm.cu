@@ -33,23 +33,22 @@ constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 template <int MAXT>
 constexpr int ring_rows() { return MAXT > 512 ? 2 : 3; }
 
-// The row's vectors (W = 8), or its single elements a fixed step apart (W = 1).
+// A thread's part of a row: its vectors (W = 8), or single elements (W = 1).
 template <int W, int V>
-__device__ __forceinline__ void store_row(const RowTensor &t, long long off, const Cols<W, V> &k, const float (&f)[V * W]) {
+__device__ __forceinline__ void store_row(int dt, char *at, const Cols<W, V> &k, const float (&f)[V * W]) {
     if constexpr (W == 1) {
-        const long long at = off + k.c[0];
-        if (t.dt == DLC_DATA_BFLOAT16) {
-            unsigned short *p = static_cast<unsigned short *>(t.p) + at;
+        if (dt == DLC_DATA_BFLOAT16) {
+            unsigned short *p = reinterpret_cast<unsigned short *>(at);
 #pragma unroll
             for (int j = 0; j < V; ++j, p += k.step)
                 if (j < k.count) *p = (unsigned short)pack_bf16(f[j], 0.f);
-        } else if (t.dt == DLC_DATA_FLOAT) {
-            float *p = static_cast<float *>(t.p) + at;
+        } else if (dt == DLC_DATA_FLOAT) {
+            float *p = reinterpret_cast<float *>(at);
 #pragma unroll
             for (int j = 0; j < V; ++j, p += k.step)
                 if (j < k.count) *p = f[j];
         } else {
-            unsigned char *p = static_cast<unsigned char *>(t.p) + at;
+            unsigned char *p = reinterpret_cast<unsigned char *>(at);
 #pragma unroll
             for (int j = 0; j < V; j += 2, p += 2 * k.step) {
                 const uint32_t q = pack_e4m3(f[j], f[j + 1]);
@@ -61,15 +60,15 @@ __device__ __forceinline__ void store_row(const RowTensor &t, long long off, con
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float *v = f + j * W;
-            const long long at = off + k.c[j];
+            const int d = j * k.step;
             if (k.n[j] == W) {
-                if (t.dt == DLC_DATA_BFLOAT16) {
+                if (dt == DLC_DATA_BFLOAT16) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                    *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(t.p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else if (t.dt == DLC_DATA_FLOAT) {
-                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(t.p) + at);
+                    *reinterpret_cast<uint4 *>(at + 2 * d) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else if (dt == DLC_DATA_FLOAT) {
+                    float4 *p = reinterpret_cast<float4 *>(at + 4 * d);
 #pragma unroll
                     for (int i = 0; i < W / 4; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 } else {
@@ -77,12 +76,12 @@ __device__ __forceinline__ void store_row(const RowTensor &t, long long off, con
 #pragma unroll
                     for (int i = 0; i < W / 4; ++i)
                         w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
-                    *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(t.p) + at) = make_uint2(w[0], w[1]);
+                    *reinterpret_cast<uint2 *>(at + d) = make_uint2(w[0], w[1]);
                 }
-            } else {
+            } else if (k.n[j] > 0) {
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (i < k.n[j]) store_elem(t.p, t.dt, at + i, v[i]);
+                for (int i = 0; i < W - 1; ++i)
+                    if (i < k.n[j]) store_elem(at, dt, d + i, v[i]);
             }
         }
     }
@@ -110,19 +109,25 @@ __device__ __forceinline__ void load_gamma(const float *gamma, int c, int C, boo
 // barrier of their own; the buffer alternates between calls, so one barrier a
 // call is enough.
 template <bool MAX_B>
-__device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 (*buf)[RMS_MAX_WARPS], int parity) {
-    for (int o = (tpr < 32 ? tpr : 32) / 2; o > 0; o /= 2) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        const float ob = __shfl_xor_sync(0xffffffffu, b, o);
-        b = MAX_B ? fmaxf(b, ob) : b + ob;
+__device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, int slot, float2 (*buf)[RMS_MAX_WARPS], int parity) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        if (o < 8 || o < tpr) {  // (a row has eight threads at least)
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            const float ob = __shfl_xor_sync(0xffffffffu, b, o);
+            b = MAX_B ? fmaxf(b, ob) : b + ob;
+        }
     }
     if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, slot = threadIdx.x / tpr, first = slot * (tpr >> 5);
-        if ((threadIdx.x & 31) == 0) buf[parity][warp] = make_float2(a, b);
+        const int warps = tpr >> 5;
+        const float2 *row = buf[parity] + slot * warps;
+        if ((threadIdx.x & 31) == 0) buf[parity][threadIdx.x >> 5] = make_float2(a, b);
         asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
-        a = 0.f, b = 0.f;
-        for (int i = 0; i < (tpr >> 5); ++i) {
-            const float2 v = buf[parity][first + i];
+        const float2 v0 = row[0], v1 = row[1];
+        a = v0.x + v1.x;
+        b = MAX_B ? fmaxf(v0.y, v1.y) : v0.y + v1.y;
+        for (int i = 2; i < warps; ++i) {
+            const float2 v = row[i];
             a += v.x;
             b = MAX_B ? fmaxf(b, v.y) : b + v.y;
         }
@@ -156,11 +161,12 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     Rows<W, V, BF, 2, ring_rows<MAXT>()> rows;
     rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    RowWalk wx(p.x.m, row, step), wr(p.r.m, row, step), wt(p.t.m, row, step), wy(p.y.m, row, step);
+    const int c = cols.c[0];
+    RowWalk wx(p.x, row, step, c), wr(p.r, row, step, c), wt(p.t, row, step, c), wy(p.y, row, step, c);
     auto fetch = [&]() {
         if (ahead < p.rows) {
-            rows.fetch(p.x, 0, wx.at(p.x.m, ahead), cols);
-            if (p.r.p) rows.fetch(p.r, 1, wr.at(p.r.m, ahead), cols);
+            rows.fetch(p.x, 0, wx.at(p.x, ahead, c), cols);
+            if (p.r.p) rows.fetch(p.r, 1, wr.at(p.r, ahead, c), cols);
         }
         rows.commit();
         ahead += step;
@@ -172,14 +178,14 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wt.next(), wy.next()) {
         const bool on = row < p.rows;
         float f[2][E];
-        const uint32_t offs[2] = {(uint32_t)(row * p.x.m.ld), (uint32_t)(row * p.r.m.ld)};
-        rows.take(f, cols, offs);
+        const uint32_t starts[2] = {(uint32_t)(row * p.x.m.ld * 2), (uint32_t)(row * p.r.m.ld * 2)};
+        rows.take(f, cols, starts);
         float *v = f[0];
         if (p.r.p) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) set_pair(v, i, add2(pair(v, i), pair(f[1], i)));
         }
-        if (p.t.p && on) store_row<W, V>(p.t, wt.at(p.t.m, row), cols, f[0]);
+        if (p.t.p && on) store_row<W, V>(p.t.dt, wt.at(p.t, row, c), cols, f[0]);
         fetch();
         float2 sq = make_float2(0.f, 0.f);
         float mx = 0.f;
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
 #pragma unroll
             for (int i = 0; i < E; ++i) mx = fmaxf(mx, fabsf(v[i]));
         }
-        const float2 red = row_reduce<true>(sq.x + sq.y, mx, tpr, buf, parity);
+        const float2 red = row_reduce<true>(sq.x + sq.y, mx, tpr, slot, buf, parity);
         if (!on) continue;
         float rho = rsqrtf(red.x * inv_c + p.eps);
         if (e4m3) {
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
         }
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) set_pair(v, i, mul2(pair(v, i), make_float2(rho, rho)));
-        store_row<W, V>(p.y, wy.at(p.y.m, row), cols, f[0]);
+        store_row<W, V>(p.y.dt, wy.at(p.y, row, c), cols, f[0]);
     }
 }
 
@@ -318,12 +324,13 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     Rows<W, V, BF, 3, ring_rows<MAXT>()> rows;
     rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    RowWalk wy(p.dy.m, row, step), wt(p.t.m, row, step), ws(p.dt.m, row, step), wx(p.dx.m, row, step);
+    const int c = cols.c[0];
+    RowWalk wy(p.dy, row, step, c), wt(p.t, row, step, c), ws(p.dt, row, step, c), wx(p.dx, row, step, c);
     auto fetch = [&]() {
         if (ahead < p.rows) {
-            rows.fetch(p.dy, 0, wy.at(p.dy.m, ahead), cols);
-            rows.fetch(p.t, 1, wt.at(p.t.m, ahead), cols);
-            if (p.dt.p) rows.fetch(p.dt, 2, ws.at(p.dt.m, ahead), cols);
+            rows.fetch(p.dy, 0, wy.at(p.dy, ahead, c), cols);
+            rows.fetch(p.t, 1, wt.at(p.t, ahead, c), cols);
+            if (p.dt.p) rows.fetch(p.dt, 2, ws.at(p.dt, ahead, c), cols);
         }
         rows.commit();
         ahead += step;
@@ -335,8 +342,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     for (int parity = 0; row - slot < p.rows; row += step, parity ^= 1, wx.next()) {
         const bool on = row < p.rows;
         float f[3][E];
-        const uint32_t offs[3] = {(uint32_t)(row * p.dy.m.ld), (uint32_t)(row * p.t.m.ld), (uint32_t)(row * p.dt.m.ld)};
-        rows.take(f, cols, offs);
+        const uint32_t starts[3] = {(uint32_t)(row * p.dy.m.ld * 2), (uint32_t)(row * p.t.m.ld * 2), (uint32_t)(row * p.dt.m.ld * 2)};
+        rows.take(f, cols, starts);
         float2 sq = make_float2(0.f, 0.f), dot = sq;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
             dot = fma2(mul2(pair(f[0], i), pair(g, i)), v, dot);
         }
         fetch();
-        const float2 red = row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, buf, parity);
+        const float2 red = row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, slot, buf, parity);
         if (!on) continue;
         const float rho = rsqrtf(red.x * inv_c + p.eps);
         const float k = -(rho * rho * rho * (red.y * inv_c));
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
             const float2 s = p.dt.p ? pair(f[2], i) : make_float2(0.f, 0.f);
             set_pair(f[2], i, fma2(d, pair(g, i), fma2(v, k2, s)));
         }
-        store_row<W, V>(p.dx, wx.at(p.dx.m, row), cols, f[2]);
+        store_row<W, V>(p.dx.dt, wx.at(p.dx, row, c), cols, f[2]);
     }
     if (!p.dgamma) return;
     if (rpb > 1) {  // join the block's row slots, in the ring's place: [slot][C]
@@ -477,18 +484,23 @@ bool vec_ok(const RowTensor &t) {
 
 bool contiguous(const RowTensor &t) { return !t.p || t.m.cs == 1; }
 
-RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, int per_sm, int sm_count) {
+bool is_bf16(const RowTensor &t) { return !t.p || t.dt == DLC_DATA_BFLOAT16; }
+
+RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, bool bf16, int per_sm, int sm_count) {
     RowPlan r;
     r.threads = RMS_THREADS;
     r.lanes = !cs1;
     if (cs1) {
         r.w = vec ? 8 : 1;
-        const int v_max = vec ? 2 : 8;
+        // vectors a thread: few for short rows (more threads a row); FP32 rows,
+        // held in registers a row ahead, take one, or two of a very long row
+        const int v_max = vec ? (bf16 ? 2 : 1) : 8;
         const long long nv = (C + r.w - 1) / r.w;
         int v = vec ? 1 : 2, tpr = 8;
         while (tpr < 32 && tpr * v < nv) tpr *= 2;
         while (v < v_max && tpr * v < nv && tpr == 32) v *= 2;
         while (tpr < 1024 && (long long)tpr * v < nv) tpr *= 2;
+        if (vec && (long long)tpr * v < nv) v = 2;
         if ((long long)tpr * v < nv) r.w = 0;  // longer than a block's registers
         r.v = v;
         r.tpr = tpr;
@@ -503,12 +515,13 @@ RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, int per_sm, int sm_
 
 RowPlan plan_fwd(const dlcContext *ctx, const RmsProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
-                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), RMS_FWD_BLOCKS, ctx->sm_count);
+                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), is_bf16(p.x) && is_bf16(p.r), RMS_FWD_BLOCKS, ctx->sm_count);
 }
 
 RowPlan plan_bwd(const dlcContext *ctx, const RmsBwdProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.dy) && contiguous(p.t) && contiguous(p.dt) && contiguous(p.dx),
-                     vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), RMS_BWD_BLOCKS, ctx->sm_count);
+                     vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx),
+                     is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt), RMS_BWD_BLOCKS, ctx->sm_count);
 }
 
 // Rows that may be copied in the 16-byte pieces they touch: the first row
@@ -516,8 +529,6 @@ RowPlan plan_bwd(const dlcContext *ctx, const RmsBwdProblem &p) {
 bool pieces_ok(const RowTensor &t) {
     return !t.p || (t.dt == DLC_DATA_BFLOAT16 && t.m.uniform && (uintptr_t)t.p % 16 == 0);
 }
-
-bool is_bf16(const RowTensor &t) { return !t.p || t.dt == DLC_DATA_BFLOAT16; }
 
 struct RowKernel {
     const void *fn;
@@ -532,6 +543,10 @@ RowKernel fwd_entry(const RowPlan &r, int C) {
 template <int W, bool BF>
 RowKernel fwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
+    if constexpr (W == 8 && !BF) {
+        if (r.v == 1 && r.threads > 512) return fwd_entry<8, 1, false, 1024>(r, C);
+        if (r.v == 1 && r.threads > RMS_THREADS) return fwd_entry<8, 1, false, 512>(r, C);
+    }
     if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r, C);
     if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r, C);
     if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r, C);
@@ -547,6 +562,10 @@ RowKernel bwd_entry(const RowPlan &r, int C) {
 template <int W, bool BF>
 RowKernel bwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
+    if constexpr (W == 8 && !BF) {
+        if (r.v == 1 && r.threads > 512) return bwd_entry<8, 1, false, 1024>(r, C);
+        if (r.v == 1 && r.threads > RMS_THREADS) return bwd_entry<8, 1, false, 512>(r, C);
+    }
     if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r, C);
     if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r, C);
     if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r, C);

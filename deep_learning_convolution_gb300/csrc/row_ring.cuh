@@ -1,5 +1,5 @@
 // row_ring.cuh -- how the row-wise kernels read: vectors of a row per thread,
-// the next rows prefetched, offsets that step from row to row.
+// the next rows prefetched, startsets that step from row to row.
 #pragma once
 
 #include "channel.cuh"
@@ -31,18 +31,18 @@ struct Cols {
 // V vectors of a row as FP32; a partial vector is read element by element, so
 // nothing past the row is touched.
 template <int W, int V>
-__device__ __forceinline__ void load_row(const RowTensor &t, long long off, const Cols<W, V> &k, float (&f)[V * W]) {
+__device__ __forceinline__ void load_row(const RowTensor &t, const char *at, const Cols<W, V> &k, float (&f)[V * W]) {
     if constexpr (W == 1) {  // single elements a fixed step apart
-        const long long at = off + k.c[0] * t.m.cs, step = k.step * t.m.cs;
+        const long long step = k.step * t.m.cs;
         if (t.dt == DLC_DATA_BFLOAT16) {
-            const unsigned short *p = static_cast<const unsigned short *>(t.p) + at;
+            const unsigned short *p = reinterpret_cast<const unsigned short *>(at);
             unsigned short w[V];
 #pragma unroll
             for (int j = 0; j < V; ++j, p += step) w[j] = j < k.count ? *p : (unsigned short)0;
 #pragma unroll
             for (int j = 0; j < V; ++j) f[j] = bf16_bits_f32(w[j]);
         } else {
-            const float *p = static_cast<const float *>(t.p) + at;
+            const float *p = reinterpret_cast<const float *>(at);
 #pragma unroll
             for (int j = 0; j < V; ++j, p += step) f[j] = j < k.count ? *p : 0.f;
         }
@@ -50,14 +50,15 @@ __device__ __forceinline__ void load_row(const RowTensor &t, long long off, cons
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float *v = f + j * W;
+            const int d = j < k.count ? j * k.step : 0;
             if (k.n[j] == W) {
                 if (t.dt == DLC_DATA_BFLOAT16) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(t.p) + off + k.c[j]);
+                    const uint4 q = *reinterpret_cast<const uint4 *>(reinterpret_cast<const unsigned short *>(at) + d);
                     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) v[2 * i] = unpack_bf16(w[i]).x, v[2 * i + 1] = unpack_bf16(w[i]).y;
                 } else {
-                    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(t.p) + off + k.c[j]);
+                    const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(at) + d);
 #pragma unroll
                     for (int i = 0; i < W / 4; ++i) {
                         const float4 a = p[i];
@@ -65,7 +66,7 @@ __device__ __forceinline__ void load_row(const RowTensor &t, long long off, cons
                     }
                 }
             } else {
-                load_elems<W>(t.p, t.dt, off + k.c[j], 1, [&](int i) { return i < k.n[j]; }, v);
+                load_elems<W>(at, t.dt, d, 1, [&](int i) { return i < k.n[j]; }, v);
             }
         }
     }
@@ -80,8 +81,8 @@ struct Rows {
     float next[T][V * W];
     static constexpr int AHEAD = 1;
     __device__ __forceinline__ void start(uint32_t, int, int, int, int) {}
-    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<W, V> &cols) {
-        load_row<W, V>(t, off, cols, next[k]);
+    __device__ __forceinline__ void fetch(const RowTensor &t, int k, const char *at, const Cols<W, V> &cols) {
+        load_row<W, V>(t, at, cols, next[k]);
     }
     __device__ __forceinline__ void commit() {}
     __device__ __forceinline__ void take(float (&f)[T][V * W], const Cols<W, V> &, const uint32_t (&)[T]) {
@@ -103,10 +104,10 @@ struct Rows<8, V, true, T, S> {
         row = (uint32_t)(T * V) * vec;
         put = get = 0;
     }
-    __device__ __forceinline__ void fetch(const RowTensor &t, int k, long long off, const Cols<8, V> &cols) {
-        const unsigned short *p = static_cast<const unsigned short *>(t.p) + off;
+    __device__ __forceinline__ void fetch(const RowTensor &, int k, const char *at, const Cols<8, V> &cols) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) cp_async_16(base + put + (uint32_t)(k * V + j) * vec, p + cols.c[j], 2u * (uint32_t)cols.n[j]);
+        for (int j = 0; j < V; ++j)
+            cp_async_16(base + put + (uint32_t)(k * V + j) * vec, at + (j < cols.count ? 2 * j * cols.step : 0), 2u * (uint32_t)cols.n[j]);
     }
     __device__ __forceinline__ void commit() {
         cp_async_commit();
@@ -138,7 +139,7 @@ struct Rows<8, V, true, T, S> {
 // base: the 16-byte pieces that a row touches come asynchronously into a ring of
 // rows, dealt to the row's threads (the first piece starts in the row before,
 // the last one ends with the row), and each thread takes its elements from
-// there.  `offs`: the rows' element offsets, of which the low bits count.
+// there.  `starts`: the addresses of the rows, of which the low bits count.
 template <int V, int T, int S>
 struct Rows<1, V, true, T, S> {
     uint32_t base, put, get, row;  // this group's slot 0, the rows to fill and to read, bytes of a row of one tensor
@@ -151,8 +152,8 @@ struct Rows<1, V, true, T, S> {
         base = smem + (uint32_t)slot * (uint32_t)(S * T) * row;
         put = get = 0;
     }
-    __device__ __forceinline__ void fetch(const RowTensor &x, int k, long long off, const Cols<1, V> &) {
-        const char *p = static_cast<const char *>(x.p) + off * 2;
+    __device__ __forceinline__ void fetch(const RowTensor &, int k, const char *at, const Cols<1, V> &cols) {
+        const char *p = at - 2 * cols.c[0];  // the row's start
         const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u, bytes = shift + 2u * (uint32_t)C;
         p -= shift;
         const uint32_t dst = base + put + (uint32_t)k * row;
@@ -162,7 +163,7 @@ struct Rows<1, V, true, T, S> {
         cp_async_commit();
         put = put == (uint32_t)(T * (S - 1)) * row ? 0 : put + (uint32_t)T * row;
     }
-    __device__ __forceinline__ void take(float (&f)[T][V], const Cols<1, V> &cols, const uint32_t (&offs)[T]) {
+    __device__ __forceinline__ void take(float (&f)[T][V], const Cols<1, V> &cols, const uint32_t (&starts)[T]) {
         cp_async_wait<S - 2>();
         // every thread's pieces have arrived, and the row before has been read
         if (tpr > 32)
@@ -171,7 +172,7 @@ struct Rows<1, V, true, T, S> {
             __syncwarp();
 #pragma unroll
         for (int k = 0; k < T; ++k) {
-            uint32_t at = base + get + (uint32_t)k * row + ((offs[k] * 2u) & 15u) + 2u * (uint32_t)t;
+            uint32_t at = base + get + (uint32_t)k * row + (starts[k] & 15u) + 2u * (uint32_t)t;
 #pragma unroll
             for (int j = 0; j < V; ++j, at += 2u * (uint32_t)tpr) {
                 unsigned short w = 0;
@@ -184,13 +185,23 @@ struct Rows<1, V, true, T, S> {
     static size_t smem(int threads, int tpr, int C) { return (size_t)S * T * row_bytes(C) * (threads / tpr); }
 };
 
-// Row offsets of one tensor along a thread's rows: added up where the rows
-// have one pitch, worked out from n, h and w otherwise.
+// Where a thread's part of a tensor's rows starts (its element `c` of the row),
+// row after row: stepped where the rows have one pitch, worked out from n, h and
+// w otherwise.
 struct RowWalk {
-    long long off, inc;
-    __device__ __forceinline__ RowWalk(const RowMap &m, long long row, long long step) : off(row * m.ld), inc(step * m.ld) {}
-    __device__ __forceinline__ long long at(const RowMap &m, long long row) const { return m.uniform ? off : row_off(m, row); }
-    __device__ __forceinline__ void next() { off += inc; }
+    char *p;
+    long long inc;
+    __device__ __forceinline__ RowWalk(const RowTensor &t, long long row, long long step, long long c) {
+        const int e = t.dt == DLC_DATA_FLOAT ? 4 : t.dt == DLC_DATA_BFLOAT16 ? 2 : 1;
+        p = static_cast<char *>(t.p) + (row * t.m.ld + c) * e;
+        inc = step * t.m.ld * e;
+    }
+    __device__ __forceinline__ char *at(const RowTensor &t, long long row, long long c) const {
+        if (t.m.uniform) return p;
+        const int e = t.dt == DLC_DATA_FLOAT ? 4 : t.dt == DLC_DATA_BFLOAT16 ? 2 : 1;
+        return static_cast<char *>(t.p) + (row_off(t.m, row) + c) * e;
+    }
+    __device__ __forceinline__ void next() { p += inc; }
 };
 
 }  // namespace dlc
