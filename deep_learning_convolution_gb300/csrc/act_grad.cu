@@ -37,9 +37,9 @@ __device__ __forceinline__ void ag_store(char *at, int n, const float (&v)[W]) {
         if (i < n) p[i] = (unsigned short)pack_bf16(v[i], 0.f);
 }
 
-// A vector's channels (W = 8), or one element at any stride (W = 1).  BF: dy and
-// z in BF16, vectors.
-template <int W, int ACT, bool GATED, bool SUM, bool BF>
+// A vector's channels (W = 8), or one element at any stride (W = 1).  KIND: how they are
+// read (a ring where dy and z are BF16 vectors).
+template <int W, int ACT, bool GATED, bool SUM, int KIND>
 __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, float (&sum)[GATED ? 2 : 1][W]) {
     constexpr bool READS_Z = GATED || ACT != DLC_ACTIVATION_IDENTITY;
     constexpr int T = 1 + (READS_Z ? 1 : 0) + (GATED ? 1 : 0);
@@ -52,7 +52,7 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
     if (n <= 0) return;
     const long long cy = c * p.dy.m.cs, cz = c * p.z.m.cs, cu = cz + (long long)p.N * p.z.m.cs;
     RowWalk wy(p.dy, row, step, cy), wz(p.z, row, step, cz), wu(p.z, row, step, cu), wd(p.dz, row, step, c);
-    Rows<W, 1, BF, T, AG_RING> rows;
+    Rows<W, 1, KIND, T, AG_RING> rows;
     rows.start(ring, 0, 0, 0, 0);
     auto fetch = [&]() {
         if (ahead < p.rows) {
@@ -93,7 +93,7 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
     }
 }
 
-template <int W, bool GATED, bool SUM, bool BF>
+template <int W, bool GATED, bool SUM, int KIND>
 __global__ void __launch_bounds__(AG_WARPS * 32, AG_BLOCKS) act_grad_kernel(const __grid_constant__ ActGradProblem p) {
     griddep_launch_dependents();
     extern __shared__ uint4 ring_s[];
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(AG_WARPS * 32, AG_BLOCKS) act_grad_kernel(cons
 #pragma unroll
         for (int i = 0; i < W; ++i) sum[h][i] = 0.f;
     griddep_wait();
-    act_dispatch(p.act, [&](auto act) { ag_rows<W, decltype(act)::value, GATED, SUM, BF>(p, smem_u32(ring_s), sum); });
+    act_dispatch(p.act, [&](auto act) { ag_rows<W, decltype(act)::value, GATED, SUM, KIND>(p, smem_u32(ring_s), sum); });
     if constexpr (SUM) {
         __shared__ float part[AG_WARPS][32 * W];
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -138,10 +138,10 @@ bool ag_vec(const RowTensor &t, int n) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
-template <int W, bool BF>
+template <int W, int KIND>
 const void *ag_kernel(const ActGradProblem &p) {
-    if (p.gated) return p.dbias ? (const void *)act_grad_kernel<W, true, true, BF> : (const void *)act_grad_kernel<W, true, false, BF>;
-    return p.dbias ? (const void *)act_grad_kernel<W, false, true, BF> : (const void *)act_grad_kernel<W, false, false, BF>;
+    if (p.gated) return p.dbias ? (const void *)act_grad_kernel<W, true, true, KIND> : (const void *)act_grad_kernel<W, true, false, KIND>;
+    return p.dbias ? (const void *)act_grad_kernel<W, false, true, KIND> : (const void *)act_grad_kernel<W, false, false, KIND>;
 }
 
 AgPlan ag_plan(const dlcContext *ctx, const ActGradProblem &p) {
@@ -172,7 +172,7 @@ dlcStatus_t dlc_launch_act_grad(dlcContext *ctx, const ActGradProblem &pb) {
     ActGradProblem p = pb;
     void *args[] = {&p};
     const bool bf = g.w == 8 && p.dy.dt == DLC_DATA_BFLOAT16 && (!p.z.p || p.z.dt == DLC_DATA_BFLOAT16);
-    const void *kern = bf ? ag_kernel<8, true>(p) : g.w == 8 ? ag_kernel<8, false>(p) : ag_kernel<1, false>(p);
+    const void *kern = bf ? ag_kernel<8, ROWS_BF16>(p) : g.w == 8 ? ag_kernel<8, ROWS_REGS>(p) : ag_kernel<1, ROWS_REGS>(p);
     const size_t smem = bf ? (size_t)AG_RING * (p.gated ? 3 : p.z.p ? 2 : 1) * 16 * AG_WARPS * 32 : 0;
     if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const dlcStatus_t st = dlc_launch(ctx, kern, dim3(g.gx, g.gy), dim3(AG_WARPS * 32), smem, args);

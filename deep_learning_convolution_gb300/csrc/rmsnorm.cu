@@ -12,6 +12,8 @@
 // registers: the traffic is each input once and each output once, which is
 // what bounds these kernels.  max |y| = rho * max |gamma t|, so the 8-bit
 // scale comes from the same reduction as the sum of squares.
+#include <initializer_list>
+
 #include "channel.cuh"
 #include "ptx.cuh"
 #include "row_ring.cuh"
@@ -30,8 +32,9 @@ constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 // Rows of the ring.  Measured, 100352 x 512 forward / 25088 x 1024 backward, BF16:
 // 3 rows at 4 / 2 blocks an SM 74.5 / 40.0 us; 4 rows 77.6 / 41.1; one row ahead
 // in registers 109 us forward.
-template <int MAXT>
-constexpr int ring_rows() { return MAXT > 512 ? 2 : 3; }
+// FP32 rows, twice the bytes, and blocks of 1024 threads: 2.
+template <int KIND, int MAXT>
+constexpr int ring_rows() { return MAXT > 512 || KIND == ROWS_F32 ? 2 : 3; }
 
 // A thread's part of a row: its vectors (W = 8), or single elements (W = 1).
 template <int W, int V>
@@ -142,7 +145,7 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 
 // Rows in registers: `tpr` threads a row, V vectors of W channels a thread.
 // The next row's loads are issued before this row's reduction waits.
-template <int W, int V, bool BF, int MAXT>
+template <int W, int V, int KIND, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     rms_rows_kernel(const __grid_constant__ RmsProblem p, int tpr, int gamma_vec) {
     griddep_launch_dependents();
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
     float g[E];
 #pragma unroll
     for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
-    Rows<W, V, BF, 2, ring_rows<MAXT>()> rows;
+    Rows<W, V, KIND, 2, ring_rows<KIND, MAXT>()> rows;
     rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
     const int c = cols.c[0];
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
 
 // Backward, rows in registers.  Each thread adds up dgamma of its own channels
 // over the rows it visits; a block writes one partial row of sums.
-template <int W, int V, bool BF, int MAXT>
+template <int W, int V, int KIND, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     rms_bwd_rows_kernel(const __grid_constant__ RmsBwdProblem p, int tpr, int gamma_vec) {
     griddep_launch_dependents();
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
     for (int j = 0; j < V; ++j) load_gamma<W>(p.gamma, (t + j * tpr) * W, p.C, gamma_vec != 0, g + j * W);
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    Rows<W, V, BF, 3, ring_rows<MAXT>()> rows;
+    Rows<W, V, KIND, 3, ring_rows<KIND, MAXT>()> rows;
     rows.start(smem_u32(ring_s), t, tpr, slot, p.C);
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
     const int c = cols.c[0];
@@ -484,17 +487,23 @@ bool vec_ok(const RowTensor &t) {
 
 bool contiguous(const RowTensor &t) { return !t.p || t.m.cs == 1; }
 
-bool is_bf16(const RowTensor &t) { return !t.p || t.dt == DLC_DATA_BFLOAT16; }
+bool all_of(int dt, std::initializer_list<RowTensor> ts) {
+    for (const RowTensor &t : ts)
+        if (t.p && t.dt != dt) return false;
+    return true;
+}
 
-RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, bool bf16, int per_sm, int sm_count) {
+bool ring(std::initializer_list<RowTensor> ts) { return all_of(DLC_DATA_BFLOAT16, ts) || all_of(DLC_DATA_FLOAT, ts); }
+
+RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, bool ring, int per_sm, int sm_count) {
     RowPlan r;
     r.threads = RMS_THREADS;
     r.lanes = !cs1;
     if (cs1) {
         r.w = vec ? 8 : 1;
-        // vectors a thread: few for short rows (more threads a row); FP32 rows,
-        // held in registers a row ahead, take one, or two of a very long row
-        const int v_max = vec ? (bf16 ? 2 : 1) : 8;
+        // vectors a thread: few for short rows (more threads a row); rows held in
+        // registers a row ahead take one, or two of a very long row
+        const int v_max = vec ? (ring ? 2 : 1) : 8;
         const long long nv = (C + r.w - 1) / r.w;
         int v = vec ? 1 : 2, tpr = 8;
         while (tpr < 32 && tpr * v < nv) tpr *= 2;
@@ -515,13 +524,13 @@ RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, bool bf16, int per_
 
 RowPlan plan_fwd(const dlcContext *ctx, const RmsProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
-                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), is_bf16(p.x) && is_bf16(p.r), RMS_FWD_BLOCKS, ctx->sm_count);
+                     vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), ring({p.x, p.r}), RMS_FWD_BLOCKS, ctx->sm_count);
 }
 
 RowPlan plan_bwd(const dlcContext *ctx, const RmsBwdProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.dy) && contiguous(p.t) && contiguous(p.dt) && contiguous(p.dx),
                      vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx),
-                     is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt), RMS_BWD_BLOCKS, ctx->sm_count);
+                     ring({p.dy, p.t, p.dt}), RMS_BWD_BLOCKS, ctx->sm_count);
 }
 
 // Rows that may be copied in the 16-byte pieces they touch: the first row
@@ -535,42 +544,42 @@ struct RowKernel {
     size_t smem;
 };
 
-template <int W, int V, bool BF, int MAXT>
+template <int W, int V, int KIND, int MAXT>
 RowKernel fwd_entry(const RowPlan &r, int C) {
-    return {(const void *)rms_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 2, ring_rows<MAXT>()>::smem(r.threads, r.tpr, C)};
+    return {(const void *)rms_rows_kernel<W, V, KIND, MAXT>, Rows<W, V, KIND, 2, ring_rows<KIND, MAXT>()>::smem(r.threads, r.tpr, C)};
 }
 
-template <int W, bool BF>
+template <int W, int KIND>
 RowKernel fwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
-    if constexpr (W == 8 && !BF) {
-        if (r.v == 1 && r.threads > 512) return fwd_entry<8, 1, false, 1024>(r, C);
-        if (r.v == 1 && r.threads > RMS_THREADS) return fwd_entry<8, 1, false, 512>(r, C);
+    if constexpr (W == 8 && KIND == ROWS_REGS) {
+        if (r.v == 1 && r.threads > 512) return fwd_entry<8, 1, KIND, 1024>(r, C);
+        if (r.v == 1 && r.threads > RMS_THREADS) return fwd_entry<8, 1, KIND, 512>(r, C);
     }
-    if (r.threads > 512) return fwd_entry<W, V, BF, 1024>(r, C);
-    if (r.threads > RMS_THREADS) return fwd_entry<W, V, BF, 512>(r, C);
-    if (r.v == V) return fwd_entry<W, V, BF, RMS_THREADS>(r, C);
-    if (W == 1 && r.v == 4) return fwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r, C);
-    return fwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r, C);
+    if (r.threads > 512) return fwd_entry<W, V, KIND, 1024>(r, C);
+    if (r.threads > RMS_THREADS) return fwd_entry<W, V, KIND, 512>(r, C);
+    if (r.v == V) return fwd_entry<W, V, KIND, RMS_THREADS>(r, C);
+    if (W == 1 && r.v == 4) return fwd_entry<W, W == 1 ? 4 : V, KIND, RMS_THREADS>(r, C);
+    return fwd_entry<W, W == 8 ? 1 : 2, KIND, RMS_THREADS>(r, C);
 }
 
-template <int W, int V, bool BF, int MAXT>
+template <int W, int V, int KIND, int MAXT>
 RowKernel bwd_entry(const RowPlan &r, int C) {
-    return {(const void *)rms_bwd_rows_kernel<W, V, BF, MAXT>, Rows<W, V, BF, 3, ring_rows<MAXT>()>::smem(r.threads, r.tpr, C)};
+    return {(const void *)rms_bwd_rows_kernel<W, V, KIND, MAXT>, Rows<W, V, KIND, 3, ring_rows<KIND, MAXT>()>::smem(r.threads, r.tpr, C)};
 }
 
-template <int W, bool BF>
+template <int W, int KIND>
 RowKernel bwd_kernel(const RowPlan &r, int C) {
     constexpr int V = W == 8 ? 2 : 8;  // vectors a thread of a long row
-    if constexpr (W == 8 && !BF) {
-        if (r.v == 1 && r.threads > 512) return bwd_entry<8, 1, false, 1024>(r, C);
-        if (r.v == 1 && r.threads > RMS_THREADS) return bwd_entry<8, 1, false, 512>(r, C);
+    if constexpr (W == 8 && KIND == ROWS_REGS) {
+        if (r.v == 1 && r.threads > 512) return bwd_entry<8, 1, KIND, 1024>(r, C);
+        if (r.v == 1 && r.threads > RMS_THREADS) return bwd_entry<8, 1, KIND, 512>(r, C);
     }
-    if (r.threads > 512) return bwd_entry<W, V, BF, 1024>(r, C);
-    if (r.threads > RMS_THREADS) return bwd_entry<W, V, BF, 512>(r, C);
-    if (r.v == V) return bwd_entry<W, V, BF, RMS_THREADS>(r, C);
-    if (W == 1 && r.v == 4) return bwd_entry<W, W == 1 ? 4 : V, BF, RMS_THREADS>(r, C);
-    return bwd_entry<W, W == 8 ? 1 : 2, BF, RMS_THREADS>(r, C);
+    if (r.threads > 512) return bwd_entry<W, V, KIND, 1024>(r, C);
+    if (r.threads > RMS_THREADS) return bwd_entry<W, V, KIND, 512>(r, C);
+    if (r.v == V) return bwd_entry<W, V, KIND, RMS_THREADS>(r, C);
+    if (W == 1 && r.v == 4) return bwd_entry<W, W == 1 ? 4 : V, KIND, RMS_THREADS>(r, C);
+    return bwd_entry<W, W == 8 ? 1 : 2, KIND, RMS_THREADS>(r, C);
 }
 
 }  // namespace
@@ -582,8 +591,9 @@ dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
     void *args[] = {&p, &tpr, &gamma_vec};
     const RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
-        : r.w == 1 ? (pieces_ok(p.x) && pieces_ok(p.r) ? fwd_kernel<1, true>(r, p.C) : fwd_kernel<1, false>(r, p.C))
-        : is_bf16(p.x) && is_bf16(p.r) ? fwd_kernel<8, true>(r, p.C) : fwd_kernel<8, false>(r, p.C);
+        : r.w == 1 ? (pieces_ok(p.x) && pieces_ok(p.r) ? fwd_kernel<1, ROWS_BF16>(r, p.C) : fwd_kernel<1, ROWS_REGS>(r, p.C))
+        : all_of(DLC_DATA_BFLOAT16, {p.x, p.r}) ? fwd_kernel<8, ROWS_BF16>(r, p.C)
+        : all_of(DLC_DATA_FLOAT, {p.x, p.r}) ? fwd_kernel<8, ROWS_F32>(r, p.C) : fwd_kernel<8, ROWS_REGS>(r, p.C);
     if (!dlc_allow_smem(ctx, k.fn, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
     return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
@@ -602,8 +612,9 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
     void *args[] = {&p, &tpr, &gamma_vec};
     const RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_bwd_any_kernel<true> : (const void *)rms_bwd_any_kernel<false>, 0}
-        : r.w == 1 ? (pieces_ok(p.dy) && pieces_ok(p.t) && pieces_ok(p.dt) ? bwd_kernel<1, true>(r, p.C) : bwd_kernel<1, false>(r, p.C))
-        : is_bf16(p.dy) && is_bf16(p.t) && is_bf16(p.dt) ? bwd_kernel<8, true>(r, p.C) : bwd_kernel<8, false>(r, p.C);
+        : r.w == 1 ? (pieces_ok(p.dy) && pieces_ok(p.t) && pieces_ok(p.dt) ? bwd_kernel<1, ROWS_BF16>(r, p.C) : bwd_kernel<1, ROWS_REGS>(r, p.C))
+        : all_of(DLC_DATA_BFLOAT16, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_BF16>(r, p.C)
+        : all_of(DLC_DATA_FLOAT, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_F32>(r, p.C) : bwd_kernel<8, ROWS_REGS>(r, p.C);
     const int rpb = r.w ? r.threads / r.tpr : 1;
     const size_t smem = std::max(k.smem, rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0);
     if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;

@@ -72,12 +72,16 @@ __device__ __forceinline__ void load_row(const RowTensor &t, const char *at, con
     }
 }
 
-// A thread's next rows of T tensors.  BF (all of them BF16, W = 8): copied
+// How the rows of a kernel's tensors are read: one row ahead in registers, or
+// through a ring in shared memory where all of them are BF16 or all FP32.
+enum { ROWS_REGS = 0, ROWS_BF16 = 1, ROWS_F32 = 2 };
+
+// A thread's next rows of T tensors.  A ring (W = 8): copied
 // asynchronously into a ring of S rows in shared memory, of which a thread
 // reads back only what it copied itself (no barrier), so S - 1 rows of every
 // thread are in flight; otherwise one row ahead, in registers.
-template <int W, int V, bool BF, int T, int S>
-struct Rows {
+template <int W, int V, int T>
+struct RowsAhead {
     float next[T][V * W];
     static constexpr int AHEAD = 1;
     __device__ __forceinline__ void start(uint32_t, int, int, int, int) {}
@@ -94,20 +98,30 @@ struct Rows {
     static size_t smem(int, int, int) { return 0; }
 };
 
-template <int V, int T, int S>
-struct Rows<8, V, true, T, S> {
-    uint32_t base, put, get, vec, row;  // this thread's slot 0, the rows to fill and to read, bytes between vectors / rows
+template <int W, int V, int KIND, int T, int S>
+struct Rows : RowsAhead<W, V, T> {};
+
+template <int V, int KIND, int T, int S>
+struct Rows<8, V, KIND, T, S> {
+    static constexpr int E = KIND == ROWS_BF16 ? 2 : 4, Q = E / 2;  // bytes of an element, 16-byte words of a vector
+    uint32_t base, put, get, word, row;  // this thread's slot 0, the rows to fill and to read, bytes between words / rows
     static constexpr int AHEAD = S - 1;
     __device__ __forceinline__ void start(uint32_t smem, int, int, int, int) {
         base = smem + threadIdx.x * 16u;
-        vec = 16u * blockDim.x;
-        row = (uint32_t)(T * V) * vec;
+        word = 16u * blockDim.x;
+        row = (uint32_t)(T * V * Q) * word;
         put = get = 0;
     }
     __device__ __forceinline__ void fetch(const RowTensor &, int k, const char *at, const Cols<8, V> &cols) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            cp_async_16(base + put + (uint32_t)(k * V + j) * vec, at + (j < cols.count ? 2 * j * cols.step : 0), 2u * (uint32_t)cols.n[j]);
+        for (int j = 0; j < V; ++j) {
+            const char *p = at + (j < cols.count ? E * j * cols.step : 0);
+            const int bytes = E * cols.n[j];
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                cp_async_16(base + put + (uint32_t)((k * V + j) * Q + q) * word, bytes > 16 * q ? p + 16 * q : p,
+                            (uint32_t)max(0, min(16, bytes - 16 * q)));
+        }
     }
     __device__ __forceinline__ void commit() {
         cp_async_commit();
@@ -118,22 +132,29 @@ struct Rows<8, V, true, T, S> {
 #pragma unroll
         for (int k = 0; k < T; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < V * Q; ++j) {
                 uint32_t w[4];
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(base + get + (uint32_t)(k * V + j) * vec)
+                             : "r"(base + get + (uint32_t)(k * V * Q + j) * word)
                              : "memory");
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 u = unpack_bf16(w[i]);
-                    f[k][8 * j + 2 * i] = u.x, f[k][8 * j + 2 * i + 1] = u.y;
+                    if constexpr (KIND == ROWS_BF16) {
+                        const float2 u = unpack_bf16(w[i]);
+                        f[k][8 * j + 2 * i] = u.x, f[k][8 * j + 2 * i + 1] = u.y;
+                    } else {
+                        f[k][4 * j + i] = __uint_as_float(w[i]);
+                    }
                 }
             }
         get = get == row * (S - 1) ? 0 : get + row;
     }
-    static size_t smem(int threads, int, int) { return (size_t)S * T * V * 16 * threads; }
+    static size_t smem(int threads, int, int) { return (size_t)S * T * V * Q * 16 * threads; }
 };
+
+template <int V, int T, int S>
+struct Rows<8, V, ROWS_REGS, T, S> : RowsAhead<8, V, T> {};
 
 // BF16 rows at a pitch that is no multiple of 16 bytes, from a 16-byte aligned
 // base: the 16-byte pieces that a row touches come asynchronously into a ring of
@@ -141,7 +162,7 @@ struct Rows<8, V, true, T, S> {
 // the last one ends with the row), and each thread takes its elements from
 // there.  `starts`: the addresses of the rows, of which the low bits count.
 template <int V, int T, int S>
-struct Rows<1, V, true, T, S> {
+struct Rows<1, V, ROWS_BF16, T, S> {
     uint32_t base, put, get, row;  // this group's slot 0, the rows to fill and to read, bytes of a row of one tensor
     int t, tpr, C, group;
     static constexpr int AHEAD = S - 1;
