@@ -43,6 +43,7 @@ constexpr int GP_ATOM = 64 * GP_LINE;           // MN-major: 64 indices x 64 of 
 constexpr int GP_EPI_WARP0 = 3, GP_EPI_WARPS = 8;
 constexpr int GP_THREADS = (GP_EPI_WARP0 + GP_EPI_WARPS) * 32;
 constexpr int GP_MAX_SMEM = 232448, GP_BAR_AREA = 256, GP_MAX_STAGES = 8;
+constexpr int GP_COLUMNS = 2 * 256 * 4;         // scales and biases of a tile's columns
 
 // Tiles in groups of eight row blocks (below), with the division by a group's size.
 struct GpTiles {
@@ -195,35 +196,38 @@ __device__ void gp_mma(const GpParams &p, uint32_t tmem_base, uint32_t sA, uint3
 
 // ---- epilogue --------------------------------------------------------------------
 
-// 32 values of a vector from column n on (the same for every row of the warp):
-// 16-byte loads where the address allows them; columns past `cols` read as zero.
-__device__ __forceinline__ void gp_columns(const float *src, int cols, float (&v)[32]) {
-    if (cols >= 32 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 q = __ldg(reinterpret_cast<const float4 *>(src) + i);
-            v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < cols ? __ldg(src + i) : 0.f;
+// The scales and biases of a tile's accumulator columns, to shared memory while
+// the accumulator is on its way (from global memory where they are used, each
+// 32-column chunk waited for them: 3000 x 640 -> 3008 18.2 us, 15.2 this way).
+__device__ __forceinline__ void gp_columns(const GpParams &p, bool gated, int n0, float *columns) {
+    const int i = (int)threadIdx.x - GP_EPI_WARP0 * 32;  // a column a thread
+    if (i < p.BN) {
+        const bool up = gated && i >= p.nout;
+        const int n = n0 + (up ? i - p.nout : i);
+        const long long k = (up ? (long long)p.N : 0) + n;
+        columns[i] = p.sb && n < p.N ? __ldg(p.sb + k) : 1.f;
+        columns[256 + i] = p.bias && n < p.N ? __ldg(p.bias + k) : 0.f;
     }
 }
 
-// sa[m] sb[n] acc + bias[n], columns n .. n+31 of a row (sb and bias start at
-// the column's own filter).
-__device__ __forceinline__ void gp_scale_bias(float (&v)[32], float sa, const float *sb, const float *bias, int cols) {
-    if (sb) {
-        float c[32];
-        gp_columns(sb, cols, c);
+__device__ __forceinline__ void gp_epi_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(GP_EPI_WARPS * 32) : "memory"); }
+
+// sa[m] sb[n] acc + bias[n] of 32 accumulator columns from `columns` on.
+__device__ __forceinline__ void gp_scale_bias(const GpParams &p, float (&v)[32], float sa, const float *columns) {
+    const float4 *c = reinterpret_cast<const float4 *>(columns);
+    if (p.sb) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= sa * c[i];
+        for (int i = 0; i < 8; ++i) {
+            const float4 q = c[i];
+            v[4 * i] *= sa * q.x, v[4 * i + 1] *= sa * q.y, v[4 * i + 2] *= sa * q.z, v[4 * i + 3] *= sa * q.w;
+        }
     }
-    if (bias) {
-        float c[32];
-        gp_columns(bias, cols, c);
+    if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += c[i];
+        for (int i = 0; i < 8; ++i) {
+            const float4 q = c[64 + i];
+            v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+        }
     }
 }
 
@@ -238,8 +242,8 @@ struct GpStore {
 
     __device__ __forceinline__ uint32_t next() {
         const uint32_t sb = bufs + (uint32_t)(nbuf & 1) * buf_bytes;
-        if (nbuf >= 2) {  // the store issued from this buffer two groups ago
-            if (lane == 0) bulk_wait_group_read<1>();
+        if (nbuf >= 2) {  // the store issued from this buffer two groups ago (the same thread is elected every time)
+            if (elect_one()) bulk_wait_group_read<1>();
             __syncwarp();
         }
         ++nbuf;
@@ -272,7 +276,7 @@ struct GpStore {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {  // rows past M and columns past N are not written
+        if (elect_one()) {  // rows past M and columns past N are not written
             tma_store_3d_s(tm, sb, col, (int)row0, plane);
             bulk_commit_group();
         }
@@ -285,7 +289,7 @@ struct GpStore {
         stage_f32(sb, v);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (elect_one()) {
             tma_store_3d_s(tm, sb, col, row, plane);
             bulk_commit_group();
         }
@@ -340,7 +344,7 @@ struct GpStore {
             }
         }
         __syncwarp();
-        if (lane == 0) bulk_commit_group();  // an empty group keeps the buffers' turn
+        if (elect_one()) bulk_commit_group();  // an empty group keeps the buffers' turn
     }
 };
 
@@ -409,7 +413,7 @@ struct GpResidual {
 
 template <bool GATED, int ACT>
 __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
-                            uint32_t epi_smem, const CUtensorMap *tmY, const CUtensorMap *tmZ, const CUtensorMap *tmP,
+                            uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const CUtensorMap *tmZ, const CUtensorMap *tmP,
                             const WaitCtl &ctl) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3;                      // TMEM lanes 32*quad .. 32*quad+31
@@ -422,6 +426,7 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
     st.lane = lane;
     st.M = p.M;
     int it = 0;
+    bool dead = false;  // a wait has given up: the rounds go on for the warps' barriers alone
     for (int u = (int)cluster_id_x(); u < p.units; u += (int)num_clusters_x(), ++it) {
         const GpUnit w = gp_unit(p, u);
         const int buf = it & 1;
@@ -443,10 +448,16 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
         const bool res = !GATED && valid && !raw && p.r_vec && p.y_tma;
         GpResidual rq;
         if (!GATED) rq.load(p.r, res, ro + n0 + 32 * part, p.N - n0 - 32 * part);
+        if (!raw && (p.sb || p.bias)) {
+            gp_epi_barrier();  // the tile before has been read
+            gp_columns(p, GATED, n0, columns);
+            gp_epi_barrier();
+        }
         int okw = 0;
-        if (lane == 0) okw = mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, ctl, 25) ? 1 : 0;
+        if (lane == 0 && !dead) okw = mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, ctl, 25) ? 1 : 0;
         okw = __shfl_sync(0xffffffffu, okw, 0);
-        if (!okw) break;
+        dead = !okw;
+        if (dead) continue;
         __syncwarp();
         tc_fence_after_sync();
         const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * p.acc_stride;
@@ -473,9 +484,8 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
                 if constexpr (GATED) st.partial(tmP, up, p.nout + c0, (int)rank * GP_ROWS + quad * 32, w.plane);
                 continue;
             }
-            gp_scale_bias(v, sa, p.sb ? p.sb + n : nullptr, p.bias ? p.bias + n : nullptr, cols);
-            if constexpr (GATED)
-                gp_scale_bias(up, sa, p.sb ? p.sb + p.N + n : nullptr, p.bias ? p.bias + p.N + n : nullptr, cols);
+            gp_scale_bias(p, v, sa, columns + c0);
+            if constexpr (GATED) gp_scale_bias(p, up, sa, columns + p.nout + c0);
             if (p.z.p) {
                 if (p.z_tma) {
                     st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, v, n, 0);
@@ -505,7 +515,7 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
         __syncwarp();
         if (lane == 0) mbar_arrive_tmem_free(tempty0 + 8u * (uint32_t)buf);
     }
-    if (lane == 0) bulk_wait_group_read<0>();  // staged stores have read shared memory before the CTA exits
+    if (elect_one()) bulk_wait_group_read<0>();  // staged stores have read shared memory before the CTA exits
     __syncwarp();
 }
 
@@ -516,13 +526,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmP) {
     constexpr int BK = E4M3 ? GP_LINE : GP_LINE / 2;
     griddep_launch_dependents();
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in both CTAs
+    extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzled operands' alignment)
     const int ST = p.stages;
     uint8_t *smB = smem + (size_t)ST * GP_A_BYTES;
     uint8_t *epi = smB + (size_t)ST * p.b_stage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(epi + GP_EPI_WARPS * 2 * p.epi_buf);
+    float *columns = reinterpret_cast<float *>(epi + GP_EPI_WARPS * 2 * p.epi_buf);
+    uint64_t *full = reinterpret_cast<uint64_t *>(columns + 512);
     uint64_t *empty = full + ST;
     uint64_t *tfull = empty + ST;
     uint64_t *tempty = tfull + 2;
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0 && lane == 0) {
+    if (threadIdx.x == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
     }
@@ -563,13 +572,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     griddep_wait();  // no global memory before the grid ahead of this one is done
 
     if (warp == 0) {
-        if (lane == 0) gp_produce<true, A_MN, GATED, BK>(p, rank, &tmA, sA, full, empty, ctl);
+        if (elect_one()) gp_produce<true, A_MN, GATED, BK>(p, rank, &tmA, sA, full, empty, ctl);
     } else if (warp == 2) {
-        if (lane == 0) gp_produce<false, B_MN, GATED, BK>(p, rank, &tmB, sB, full, empty, ctl);
+        if (elect_one()) gp_produce<false, B_MN, GATED, BK>(p, rank, &tmB, sB, full, empty, ctl);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0)
+        const bool one = elect_one();
+        if (one && rank == 0)
             gp_mma<E4M3, A_MN, B_MN>(p, tmem_base, sA, sB, full, empty, tfull, tempty, mma_done, ctl);
-        if (lane == 0) {  // the leader's final commit reaches both CTAs
+        if (one) {  // the leader's final commit reaches both CTAs
             volatile int dummy = 0;
             const WaitCtl fin{&dummy, p.err, p.timeout_ns};
             mbar_wait(mma_done, 0u, fin, 93);
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     } else {
         // (the activation's branch out here: a block's code is straight)
         act_dispatch(p.act, [&](auto act) {
-            gp_epilogue<GATED, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), &tmY, &tmZ, &tmP, ctl);
+            gp_epilogue<GATED, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, &tmP, ctl);
         });
     }
     __syncwarp();
@@ -785,12 +795,12 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     // Tile width, split of the tail, and which of the two kernels, from a model of
-    // the time in microseconds (constants measured back to back on 20 shapes from
-    // 16 x 512 -> 512 to 12000 x 192 -> 256; its choice is within 10 % of the best
-    // alternative on all of them but one, 20 % there).  A k-block takes a pair almost as long
-    // for 64 columns as for 256 (the MMA thread's turn), so tiles are wide and
-    // idle pairs are filled by splitting the reduction: that costs the partial
-    // sums' way through the L2 and a launch.
+    // the time in microseconds, fitted to 18 shapes from 128 x 1024 -> 512 to
+    // 300 x 4096 -> 8192 and 12000 x 192 -> 256 (its choice is within 8 % of the fastest of
+    // some ten alternatives each).  A k-block takes a pair 0.31 us for 256 columns
+    // and half that for 64 (the MMA thread's turn), so tiles are wide; idle pairs are filled
+    // by splitting the reduction: that costs the partial sums' way through the L2
+    // and a launch.
     const int pairs = ctx->sm_count / 2;
     double best = 1e300;
     for (int bn : {256, 192, 128, 64}) {
@@ -798,16 +808,16 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
         if (g.gated && bn % 128) continue;    // and a gated half whole 64-output chunk pairs
         const int nout = g.gated ? bn / 2 : bn, n_tiles = (g.N + nout - 1) / nout;
         const long long tiles = (long long)p.m_tiles * n_tiles;
-        const double kb = 0.32 + 0.04 * bn / 256, fixed = 3.4 + 1.2 * bn / 256;
+        const double kb = std::max(0.143, 0.046 + 0.266 * bn / 256), fixed = 4.2 + 1.6 * bn / 256;
         const long long tail = tiles % pairs, full = tiles - tail;
-        const double whole = (double)(full / pairs) * (p.num_kb * kb + 0.15);
+        const double whole = (double)(full / pairs) * (p.num_kb * kb + 0.8);
         for (int s = 1; s <= GP_MAX_SPLITS; ++s) {
             double t = fixed + whole;
             if (s == 1) {
                 if (tail) t += p.num_kb * kb;
             } else {
                 if (tail * s > pairs || 2 * s > p.num_kb) break;
-                t += (p.num_kb + s - 1) / s * kb + 2.2 + (double)tail * s * 256 * bn * 8 / 7e6;
+                t += (p.num_kb + s - 1) / s * kb + 1.7 + (double)tail * s * 256 * bn * 8 / 5e6;
             }
             if (t < best) best = t, p.bn = bn, p.splits = s, p.full_tiles = (int)std::min(s == 1 ? tiles : full, 0x7fffffffLL);
         }
@@ -995,8 +1005,8 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
     const int stage_bytes = GP_A_BYTES + (int)p.b_stage;
-    p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - 1024 - GP_BAR_AREA - epi_bytes) / stage_bytes);
-    const size_t smem = 1024 + (size_t)p.stages * stage_bytes + epi_bytes + GP_BAR_AREA;
+    p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - GP_COLUMNS - GP_BAR_AREA - epi_bytes) / stage_bytes);
+    const size_t smem = (size_t)p.stages * stage_bytes + epi_bytes + GP_COLUMNS + GP_BAR_AREA;
     const void *kern = pair_kernel(e4m3, g.a.trans != 0, g.b.trans != 0, g.gated != 0);
     if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);

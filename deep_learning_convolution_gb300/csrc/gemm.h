@@ -4,7 +4,7 @@
 #include "internal.h"
 
 struct FewRowsPlan {
-    int num_kb, rows, filter_tiles, row_tiles, splits;
+    int num_kb, rows, filters, filter_tiles, row_tiles, splits;  // filters: outputs of a tile
     double us;  // expected time
 };
 

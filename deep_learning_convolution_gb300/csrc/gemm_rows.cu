@@ -26,17 +26,18 @@ namespace {
 
 using namespace dlc;
 
-constexpr int FR_FILTERS = 128;
-constexpr int FR_LINE = 128;                        // bytes of an operand row per k-block
-constexpr int FR_W_BYTES = FR_FILTERS * FR_LINE;    // 16 KiB
+constexpr int FR_M = 128;                   // the MMA's M side: a tile's filters, gate and up
+constexpr int FR_LINE = 128;                // bytes of an operand row per k-block
+constexpr int FR_MAX_ROWS = 128;            // of a tile
 constexpr int FR_THREADS = 512;
-constexpr int FR_MAX_STAGES = 12, FR_MAX_SPLITS = 8;  // (a cluster of eight is portable)
+constexpr int FR_MAX_STAGES = 24, FR_MAX_SPLITS = 8;  // (a cluster of eight is portable)
 constexpr int FR_SMEM = 226 * 1024;
 
 struct FrParams {
     long long M;
     int N, act;
     int num_kb, splits, rows;      // rows of a tile (the MMA's N)
+    int filters, quads_log2;       // outputs of a tile; log2 of its quads, rounded up to a power of two
     int stages;
     uint32_t stage_bytes, idesc, tmem_cols;
     const float *sa, *sb, *bias;
@@ -47,23 +48,23 @@ struct FrParams {
 };
 
 // Adds up the partial sums of rows j0 .. j0+count-1 of a tile over the cluster,
-// in the order of their ranges, and applies the epilogue: a warp a row, a lane
-// four filters.  `sums`: a CTA's partial sums, [half][row][filter], at the same
-// address in each.  A launch runs this code once or a few times, so fetching it
-// counts: it is kept short (unrolled over rows it took 2.1 us a pass of four
-// rows, most of it instruction fetches).
+// in the order of their ranges, and applies the epilogue: a thread four filters,
+// the same ones for all its rows.  `sums`: a CTA's partial sums, [row][filter], at
+// the same address in each.  A launch runs this code once or a few times, so
+// fetching it counts: it is kept short (unrolled over rows it took 2.1 us a pass
+// of four rows, most of it instruction fetches).
 template <bool GATED>
-__device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int split, long long m0, int n, int j0,
+__device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int split, long long m0, int n, int f, int j0,
                                         int count, const float (&sb)[GATED ? 2 : 1][4],
                                         const float (&bias)[GATED ? 2 : 1][4]) {
     constexpr int HALVES = GATED ? 2 : 1, AT_ONCE = 4;  // ranges loaded before they are added
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = p.N - n;
-    const uint32_t half = (uint32_t)p.rows * FR_FILTERS * 4u;
+    const int cols = p.N - n;
+    const uint32_t half = (uint32_t)p.filters * 4u;
 #pragma unroll 1
-    for (int j = warp; j < count; j += FR_THREADS / 32) {
+    for (int j = (int)threadIdx.x >> p.quads_log2; j < count; j += FR_THREADS >> p.quads_log2) {
         const long long m = m0 + j0 + j;
         const float sa = p.sa ? __ldg(p.sa + m) : 1.f;
-        const uint32_t at = sums + ((uint32_t)(j0 + j) * FR_FILTERS + 4u * (uint32_t)lane) * 4u;
+        const uint32_t at = sums + ((uint32_t)(j0 + j) * FR_M + (uint32_t)f) * 4u;
         float v[HALVES][4];
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
@@ -130,18 +131,19 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     __shared__ volatile int abort_flag;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t smem = raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in every CTA
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int split = (int)cluster_ctarank();
-    const int n0 = (int)(blockIdx.x / (unsigned)p.splits) * FR_FILTERS;
+    const int n0 = (int)(blockIdx.x / (unsigned)p.splits) * p.filters;
     const long long m0 = (long long)blockIdx.y * p.rows;
     const int kb0 = (int)((long long)p.num_kb * split / p.splits);
     const int kb1 = (int)((long long)p.num_kb * (split + 1) / p.splits);
+    const uint32_t w_bytes = (uint32_t)p.filters * FR_LINE;
     auto load = [&](int kb, int stage) {
         mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
         const uint32_t dst = smem + (uint32_t)stage * p.stage_bytes;
         tma_load_2d(dst, &tmW, &full[stage], kb * BK, n0);
-        if (GATED) tma_load_2d(dst + FR_W_BYTES, &tmW, &full[stage], kb * BK, p.N + n0);
-        tma_load_2d(dst + HALVES * FR_W_BYTES, &tmX, &full[stage], kb * BK, (int)m0);
+        if (GATED) tma_load_2d(dst + w_bytes, &tmW, &full[stage], kb * BK, p.N + n0);
+        tma_load_2d(dst + HALVES * w_bytes, &tmX, &full[stage], kb * BK, (int)m0);
     };
     const int first = min(kb1, kb0 + p.stages);  // the blocks that need no free stage
     if (threadIdx.x == 0) {
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     const WaitCtl ctl{&abort_flag, p.err, p.timeout_ns};
     griddep_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         int stage = first - kb0 == p.stages ? 0 : first - kb0;
         uint32_t ph = 1;
         for (int kb = first; kb < kb1; ++kb) {
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
             load(kb, stage);
             if (++stage == p.stages) stage = 0, ph ^= 1u;
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         int stage = 0;
         uint32_t ph = 0, acc = 0;
         bool ok = true;
@@ -187,17 +189,13 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
             }
             tc_fence_after_sync();
             const uint32_t src = smem + (uint32_t)stage * p.stage_bytes;
-            const uint64_t x = sw128_kmajor_desc(src + HALVES * FR_W_BYTES);
+            const uint64_t w = sw128_kmajor_desc(src), x = sw128_kmajor_desc(src + HALVES * w_bytes);
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                const uint64_t w = sw128_kmajor_desc(src + (uint32_t)h * FR_W_BYTES);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (E4M3)
-                        umma_e4m3_nc(tmem + (uint32_t)(h * p.rows), w + 2u * j, x + 2u * j, p.idesc, j ? 1u : acc);
-                    else
-                        umma_bf16_nc(tmem + (uint32_t)(h * p.rows), w + 2u * j, x + 2u * j, p.idesc, j ? 1u : acc);
-                }
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (E4M3)
+                    umma_e4m3_nc(tmem, w + 2u * j, x + 2u * j, p.idesc, j ? 1u : acc);
+                else
+                    umma_bf16_nc(tmem, w + 2u * j, x + 2u * j, p.idesc, j ? 1u : acc);
             }
             acc = 1;
             umma_commit(&empty[stage]);
@@ -214,8 +212,8 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
         umma_commit(&done);
     }
     __syncwarp();
-    // this lane's four filters in the epilogue
-    const int f = lane * 4, n = n0 + f, cols = p.N - n;
+    // this thread's four filters in the epilogue
+    const int f = 4 * ((int)threadIdx.x & ((1 << p.quads_log2) - 1)), n = n0 + f, cols = f < p.filters ? p.N - n : 0;
     float sb[HALVES][4], bias[HALVES][4];
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
@@ -232,32 +230,35 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     }
     __syncwarp();
     tc_fence_after_sync();
-    // partial sums to shared memory, where the operands were: [half][row][filter]
+    // partial sums to shared memory, where the operands were: [row][filter]
     {
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t mine = smem + (uint32_t)((warp & 3) * 32 + lane) * 4u;
-        const int total = HALVES * p.rows;  // accumulator columns (a multiple of 16)
 #pragma unroll 1
-        for (int c = 16 * (warp >> 2); c < total; c += 4 * FR_THREADS / 32) {
+        for (int c = 16 * (warp >> 2); c < p.rows; c += 4 * FR_THREADS / 32) {
             uint32_t v[16];
             tmem_ld_32x32b_x16(lanes + (uint32_t)c, v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)(c + i) * FR_FILTERS * 4u), "r"(v[i]) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)(c + i) * FR_M * 4u), "r"(v[i]) : "memory");
         }
     }
     tc_fence_before_sync();
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();  // the cluster's partial sums are in place
+    __syncthreads();
+    if (p.splits > 1) {
+        cluster_arrive();
+        cluster_wait();  // the cluster's partial sums are in place
+    }
     good = good && abort_flag == 0;
     const int per = (p.rows + p.splits - 1) / p.splits, j0 = split * per;
     const int count = (int)min((long long)min(per, p.rows - j0), p.M - m0 - j0);
-    if (good && cols > 0) fr_join<GATED>(p, smem, split, m0, n, j0, count, sb, bias);
+    if (good && cols > 0) fr_join<GATED>(p, smem, split, m0, n, f, j0, count, sb, bias);
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();  // no CTA leaves while another reads its partial sums
+    if (p.splits > 1) {
+        cluster_arrive();
+        cluster_wait();  // no CTA leaves while another reads its partial sums
+    }
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
 
@@ -289,31 +290,35 @@ int resident_clusters(const dlcContext *ctx, int size) {
     return n;
 }
 
-size_t own_bytes(bool gated, int rows) { return (size_t)(gated ? 2 : 1) * FR_FILTERS * 4 * rows; }
-
 }  // namespace
 
 FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g) {
     FewRowsPlan p;
     const int e = dlc_dtype_bytes((dlcDataType_t)g.a.t.dt);
     p.num_kb = (int)((g.K * e + FR_LINE - 1) / FR_LINE);
-    const long long row_tiles = (g.M + FR_FILTERS - 1) / FR_FILTERS;
+    const long long row_tiles = (g.M + FR_MAX_ROWS - 1) / FR_MAX_ROWS;
     p.rows = (int)(((g.M + row_tiles - 1) / row_tiles + 15) / 16 * 16);
     p.row_tiles = (int)std::min<long long>((g.M + p.rows - 1) / p.rows, 65535);
-    p.filter_tiles = (g.N + FR_FILTERS - 1) / FR_FILTERS;
-    const long long tiles = (long long)p.filter_tiles * p.row_tiles;
-    // Time in microseconds (fitted like the pair kernel's, in gemm.cu): CTAs a
-    // tile against waves of clusters; the SMs of a GPC that a cluster does not
-    // fill stay idle, so fewer clusters of eight run at once than the SMs suggest.
-    const double share = p.rows / 128.0;
-    const double kb = g.gated ? 0.6 + 0.4 * share : 0.33 + 0.05 * share, fixed = g.gated ? 3.2 + 3.2 * share : 3.0 + 2.2 * share;
+    // Filters and CTAs a tile from a model of the time in microseconds, fitted to eleven
+    // shapes from 16 x 512 -> 512 to 128 x 4096 -> 8192 (its choice is within 4 % of
+    // the fastest of some twenty alternatives each): the launch; per k-block a turn of
+    // the MMA thread or the filters' bytes; the partial sums' way to the epilogue and
+    // the barriers of a cluster.  The SMs of a GPC that a cluster does not fill stay
+    // idle, so fewer clusters run at once than the SMs suggest.
+    const int halves = g.gated ? 2 : 1, most = FR_M / halves;
     p.us = 1e300;
-    p.splits = 1;
     for (int s = 1; s <= FR_MAX_SPLITS && (s == 1 || 2 * s <= p.num_kb); ++s) {
         const int at_once = resident_clusters(ctx, s);
-        const double waves = (double)((tiles + at_once - 1) / at_once);
-        const double t = waves * ((p.num_kb + s - 1) / s * kb + fixed + 0.1 * s);
-        if (t < p.us) p.us = t, p.splits = s;
+        for (int filters = most; filters >= 16; filters /= 2) {
+            if (filters < most && filters >= g.N) continue;
+            const int tiles = (g.N + filters - 1) / filters;
+            const long long clusters = (long long)tiles * p.row_tiles, waves = (clusters + at_once - 1) / at_once;
+            const double ctas = (double)clusters * s / (double)waves, own = p.rows * halves * filters / 16384.0;
+            const double kb = std::max(0.23, halves * filters * FR_LINE * ctas / 5.8e6);
+            const double t = 2.0 + 1.4 * ctas / ctx->sm_count +
+                             waves * ((p.num_kb + s - 1) / s * kb + (s > 1 ? 0.9 : 0.) + 1.9 * own * (2.0 - 1.0 / s));
+            if (t < p.us) p.us = t, p.splits = s, p.filters = filters, p.filter_tiles = tiles;
+        }
     }
     if ((g.M + p.rows - 1) / p.rows > 65535) p.us = 1e300;  // more row tiles than a grid has
     return p;
@@ -331,12 +336,18 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
     p.splits = pl.splits;
     p.rows = pl.rows;
     const int halves = g.gated ? 2 : 1;
-    p.stage_bytes = (uint32_t)(halves * FR_W_BYTES + pl.rows * FR_LINE);
+    p.filters = pl.filters;
+    p.quads_log2 = 0;
+    while ((4 << p.quads_log2) < pl.filters) ++p.quads_log2;
+    p.stage_bytes = (uint32_t)((halves * pl.filters + pl.rows) * FR_LINE);
     // (stages carry the filters' stream: one row of 2048 -> 2 x 8192 took 15.4 us
     // with six of them, 16.4 with five)
-    p.stages = std::min(FR_MAX_STAGES, (FR_SMEM - 1024) / (int)p.stage_bytes);
+    // (the MMA reads 128 rows of filters whatever the tile holds: what lies behind them goes
+    // to accumulator lanes that nothing reads)
+    const int behind = std::max(0, (FR_M - halves * pl.filters - pl.rows) * FR_LINE);
+    p.stages = std::min(FR_MAX_STAGES, (FR_SMEM - 1024 - behind) / (int)p.stage_bytes);
     p.stages = std::max(2, std::min(p.stages, (pl.num_kb + pl.splits - 1) / pl.splits));
-    const size_t smem = 1024 + std::max((size_t)p.stages * p.stage_bytes, own_bytes(g.gated != 0, pl.rows));
+    const size_t smem = 1024 + std::max((size_t)p.stages * p.stage_bytes + behind, (size_t)pl.rows * FR_M * 4);
     p.sa = g.sa;
     p.sb = g.sb;
     p.bias = g.bias;
@@ -350,12 +361,12 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
     p.err = ctx->d_err;
     p.timeout_ns = ctx->timeout_ns;
     const uint32_t fmt = e4m3 ? 0u : 1u;
-    p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(pl.rows >> 3) << 17) | ((uint32_t)(FR_FILTERS >> 4) << 24);
+    p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(pl.rows >> 3) << 17) | ((uint32_t)(FR_M >> 4) << 24);
     p.tmem_cols = 32;
-    while (p.tmem_cols < (uint32_t)(halves * pl.rows)) p.tmem_cols <<= 1;
+    while (p.tmem_cols < (uint32_t)pl.rows) p.tmem_cols <<= 1;
     CUtensorMap tw, tx;
     const int nb = halves * g.N;
-    if (!dlc_encode_operand(ctx, &tw, g.b, nb, (int)g.K, FR_FILTERS) ||
+    if (!dlc_encode_operand(ctx, &tw, g.b, nb, (int)g.K, pl.filters) ||
         !dlc_encode_operand(ctx, &tx, g.a, g.M, (int)g.K, pl.rows))
         return DLC_STATUS_EXECUTION_FAILED;
     const void *kern = g.gated ? (e4m3 ? (const void *)gemm_rows_kernel<true, true> : (const void *)gemm_rows_kernel<false, true>)

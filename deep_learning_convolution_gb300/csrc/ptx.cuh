@@ -187,6 +187,19 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// One thread of a converged warp.  (Unlike with a test of the lane, the compiler
+// then knows that one thread runs what follows: it issues tensor-core and copy
+// instructions from uniform registers without a loop over the active lanes.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one));
+    return one != 0;
+}
+
 // ---- programmatic dependent launch ------------------------------------------
 // A grid launched with programmatic stream serialization may start while the
 // grid before it in the stream is still running.  The earlier grid lets it be
