@@ -72,18 +72,23 @@ __device__ __forceinline__ void ag_rows(const ActGradProblem &p, uint32_t ring, 
         rows.take(f, cols, {});
         fetch();
         float b[W];
+        constexpr int PAIR = W > 1 ? 2 : 1;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            float a = 0.f, da = 1.f;
-            if constexpr (READS_Z) act_both<ACT>(f[1][i], a, da);
-            if constexpr (GATED) {
-                b[i] = f[0][i] * a;
-                f[0][i] *= f[2][i] * da;
-                if (SUM) sum[1][i] += b[i];
-            } else if constexpr (READS_Z) {
-                f[0][i] *= da;
+        for (int i = 0; i < W; i += PAIR) {
+            float2 a, da;
+            if constexpr (READS_Z) act_both<ACT>(make_float2(f[1][i], f[1][i + PAIR - 1]), a, da);
+#pragma unroll
+            for (int k = 0; k < PAIR; ++k) {
+                const int j = i + k;
+                if constexpr (GATED) {
+                    b[j] = f[0][j] * (k ? a.y : a.x);
+                    f[0][j] *= f[2][j] * (k ? da.y : da.x);
+                    if (SUM) sum[1][j] += b[j];
+                } else if constexpr (READS_Z) {
+                    f[0][j] *= k ? da.y : da.x;
+                }
+                if (SUM) sum[0][j] += f[0][j];
             }
-            if (SUM) sum[0][i] += f[0][i];
         }
         if (p.dz.p) {
             char *at = wd.at(p.dz, row, c);

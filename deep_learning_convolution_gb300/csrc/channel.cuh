@@ -35,17 +35,6 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Four E4M3 values of a word.
-__device__ __forceinline__ void unpack_e4m3(uint32_t w, float (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
 // One element of a FLOAT, BFLOAT16 or FLOAT8_E4M3 array as FP32, and back.
 __device__ __forceinline__ float load_elem(const void *p, int dt, long long i) {
     if (dt == DLC_DATA_FLOAT) return static_cast<const float *>(p)[i];
@@ -148,56 +137,95 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// 2^v and 1 / v by the special-function unit (a few units in the last place of
+// FP32; results below the normal range are zero).
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float recip_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Pair i of an array.
+__device__ __forceinline__ float2 get2(const float *v, int i) { return make_float2(v[2 * i], v[2 * i + 1]); }
+__device__ __forceinline__ void set2(float *v, int i, float2 w) { v[2 * i] = w.x, v[2 * i + 1] = w.y; }
+
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+
 // Phi(v), the standard normal distribution function, from e = exp(-v^2 / 2):
 // erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x = |v| / sqrt(2),
 // within 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical Functions,
 // 7.1.26); half the instructions of erff, and the density shares the exponential.
-__device__ __forceinline__ float gelu_phi(float v, float e) {
-    const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(v), 1.f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    q *= 0.5f * t * e;
-    return v < 0.f ? q : 1.f - q;
+__device__ __forceinline__ float2 gelu_phi(float2 v, float2 e) {
+    const float2 d = fma2(make_float2(fabsf(v.x), fabsf(v.y)), pair_of(0.3275911f * 0.70710678118654752f), pair_of(1.f));
+    const float2 t = make_float2(recip_fast(d.x), recip_fast(d.y));
+    float2 q = fma2(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));
+    q = fma2(q, t, pair_of(0.5f * 1.421413741f));
+    q = fma2(q, t, pair_of(0.5f * -0.284496736f));
+    q = fma2(q, t, pair_of(0.5f * 0.254829592f));
+    q = mul2(q, mul2(t, e));
+    const float2 c = fma2(q, pair_of(-1.f), pair_of(1.f));
+    return make_float2(v.x < 0.f ? q.x : c.x, v.y < 0.f ? q.y : c.y);
 }
 
-// f(v) of the linear and gated epilogues.  The quotients use the fast
-// exponential and division (a few units in the last place of FP32, far below
-// a BF16 rounding); SILU and GELU of -inf are -inf * 0 = NaN, as their formulas say.
+// 1 / (1 + exp(-v)), exp(-v^2 / 2)
+__device__ __forceinline__ float2 logistic(float2 v) {
+    const float2 a = mul2(v, pair_of(-1.4426950408889634f));
+    const float2 d = add2(make_float2(exp2_fast(a.x), exp2_fast(a.y)), pair_of(1.f));
+    return make_float2(recip_fast(d.x), recip_fast(d.y));
+}
+
+__device__ __forceinline__ float2 gauss(float2 v) {
+    const float2 a = mul2(mul2(v, v), pair_of(-0.5f * 1.4426950408889634f));
+    return make_float2(exp2_fast(a.x), exp2_fast(a.y));
+}
+
+// f(v) of the linear and gated epilogues, two values at a time: on every tile's path,
+// and the epilogue's instructions bound the products of a short reduction (GELU of a 256 x
+// 256 tile cost 3.6 us one value at a time, with __expf and __fdividef; REPLACE_GELU this way).  Quotients and exponentials are far within a BF16 rounding;
+// SILU and GELU of -inf are -inf * 0 = NaN, as their formulas say.
 template <int ACT>
-__device__ __forceinline__ float act_f(float v) {
-    if constexpr (ACT == DLC_ACTIVATION_RELU) return v < 0.f ? 0.f : v;  // NaN stays NaN
-    if constexpr (ACT == DLC_ACTIVATION_SIGMOID) return __fdividef(1.f, 1.f + __expf(-v));
-    if constexpr (ACT == DLC_ACTIVATION_TANH) return tanhf(v);
-    if constexpr (ACT == DLC_ACTIVATION_SILU) return __fdividef(v, 1.f + __expf(-v));
-    if constexpr (ACT == DLC_ACTIVATION_GELU) return v * gelu_phi(v, __expf(-0.5f * v * v));
+__device__ __forceinline__ float2 act_f2(float2 v) {
+    if constexpr (ACT == DLC_ACTIVATION_RELU) return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);  // NaN stays NaN
+    if constexpr (ACT == DLC_ACTIVATION_SIGMOID) return logistic(v);
+    if constexpr (ACT == DLC_ACTIVATION_TANH) return make_float2(tanhf(v.x), tanhf(v.y));
+    if constexpr (ACT == DLC_ACTIVATION_SILU) return mul2(v, logistic(v));
+    if constexpr (ACT == DLC_ACTIVATION_GELU) return mul2(v, gelu_phi(v, gauss(v)));
     return v;
 }
 
+template <int ACT>
+__device__ __forceinline__ float act_f(float v) { return act_f2<ACT>(pair_of(v)).x; }
+
 // f(v) and f'(v).
 template <int ACT>
-__device__ __forceinline__ void act_both(float v, float &f, float &df) {
+__device__ __forceinline__ void act_both(float2 v, float2 &f, float2 &df) {
+    const float2 one = pair_of(1.f), minus = pair_of(-1.f);
     if constexpr (ACT == DLC_ACTIVATION_RELU) {
-        f = v < 0.f ? 0.f : v;
-        df = v > 0.f ? 1.f : 0.f;
+        f = act_f2<ACT>(v);
+        df = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
     } else if constexpr (ACT == DLC_ACTIVATION_SIGMOID) {
-        f = __fdividef(1.f, 1.f + __expf(-v));
-        df = f * (1.f - f);
+        f = logistic(v);
+        df = mul2(f, fma2(f, minus, one));
     } else if constexpr (ACT == DLC_ACTIVATION_TANH) {
-        f = tanhf(v);
-        df = 1.f - f * f;
-    } else if constexpr (ACT == DLC_ACTIVATION_SILU) {
-        const float p = __fdividef(1.f, 1.f + __expf(-v));
-        f = v * p;
-        df = p * (1.f + v * (1.f - p));
+        f = act_f2<ACT>(v);
+        df = fma2(mul2(f, minus), f, one);
+    } else if constexpr (ACT == DLC_ACTIVATION_SILU) {  // p (1 + v (1 - p))
+        const float2 p = logistic(v);
+        f = mul2(v, p);
+        df = mul2(p, fma2(v, fma2(p, minus, one), one));
     } else if constexpr (ACT == DLC_ACTIVATION_GELU) {  // v Phi(v); Phi(v) + v phi(v)
-        const float e = __expf(-0.5f * v * v), p = gelu_phi(v, e);
-        f = v * p;
-        df = p + v * e * 0.39894228040143268f;
+        const float2 e = gauss(v), p = gelu_phi(v, e);
+        f = mul2(v, p);
+        df = fma2(mul2(v, e), pair_of(0.39894228040143268f), p);
     } else {
         f = v;
-        df = 1.f;
+        df = one;
     }
 }
 

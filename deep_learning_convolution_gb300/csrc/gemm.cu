@@ -66,6 +66,7 @@ struct GpParams {
     const float *sa, *sb, *bias;
     RowTensor z, r, y;
     int y_tma, z_tma, r_vec;
+    int y_unit, z_unit;           // elements of an aligned access to y (where TMA cannot write it) and z
     int *err;
     unsigned long long timeout_ns;
 };
@@ -216,18 +217,117 @@ __device__ __forceinline__ void gp_epi_barrier() { asm volatile("bar.sync 1, %0;
 __device__ __forceinline__ void gp_scale_bias(const GpParams &p, float (&v)[32], float sa, const float *columns) {
     const float4 *c = reinterpret_cast<const float4 *>(columns);
     if (p.sb) {
+        const float2 s = pair_of(sa);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 q = c[i];
-            v[4 * i] *= sa * q.x, v[4 * i + 1] *= sa * q.y, v[4 * i + 2] *= sa * q.z, v[4 * i + 3] *= sa * q.w;
+            set2(v, 2 * i, mul2(get2(v, 2 * i), mul2(s, make_float2(q.x, q.y))));
+            set2(v, 2 * i + 1, mul2(get2(v, 2 * i + 1), mul2(s, make_float2(q.z, q.w))));
         }
     }
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 q = c[64 + i];
-            v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+            set2(v, 2 * i, add2(get2(v, 2 * i), make_float2(q.x, q.y)));
+            set2(v, 2 * i + 1, add2(get2(v, 2 * i + 1), make_float2(q.z, q.w)));
         }
+    }
+}
+
+// A staged 32 x 32 block (the warp's first `n` rows, `cols` columns) to rows that TMA
+// cannot write: U elements a lane, U rows at a time, eight accesses in flight.
+template <typename E, int U>
+__device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, int n, long long off, long long col, int cols,
+                                               const RowTensor *r, long long roff) {
+    constexpr int LANES = 32 / U;  // of a row
+    const int lane = threadIdx.x & 31, sub = lane / LANES, c = (lane - sub * LANES) * U;
+    const long long tc = (col + c) * t.m.cs, rc = r ? (col + c) * r->m.cs : 0;
+    const bool whole = c + U <= cols;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 8 * U) {
+        float f[8][U];
+        long long o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t i = (uint32_t)(i0 + j * U + sub);
+            const uint32_t at = sb + i * 128u + ((((uint32_t)c >> 2) ^ (i & 7u)) << 4) + ((uint32_t)c & 3u) * 4u;
+            if constexpr (U == 4)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f[j][0]), "=f"(f[j][1]), "=f"(f[j][2]), "=f"(f[j][3]) : "r"(at) : "memory");
+            else if constexpr (U == 2)
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[j][0]), "=f"(f[j][1]) : "r"(at) : "memory");
+            else
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[j][0]) : "r"(at) : "memory");
+        }
+        if (r) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, roff, i0 + j * U + sub) + rc;
+            auto add = [&](auto *src) {
+                using R = typename std::remove_const<typename std::remove_pointer<decltype(src)>::type>::type;
+                R w[8][U];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int k = 0; k < U; ++k) w[j][k] = c + k < cols && i0 + j * U + sub < n ? src[o[j] + k] : (R)0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        if constexpr (sizeof(R) == 2)
+                            f[j][k] += bf16_bits_f32(w[j][k]);
+                        else
+                            f[j][k] += w[j][k];
+                    }
+            };
+            if (r->dt == DLC_DATA_BFLOAT16)
+                add(static_cast<const unsigned short *>(r->p));
+            else
+                add(static_cast<const float *>(r->p));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, off, i0 + j * U + sub) + tc;
+        E *dst = static_cast<E *>(t.p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (i0 + j * U + sub >= n) continue;
+            if (whole) {
+                if constexpr (U == 1) {
+                    store_elem(dst, sizeof(E) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, o[j], f[j][0]);
+                } else if constexpr (sizeof(E) == 2) {
+                    uint32_t w[U / 2];
+#pragma unroll
+                    for (int k = 0; k < U / 2; ++k) w[k] = pack_bf16(f[j][2 * k], f[j][2 * k + 1]);
+                    if constexpr (U == 4)
+                        *reinterpret_cast<uint2 *>(dst + o[j]) = make_uint2(w[0], w[1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(dst + o[j]) = w[0];
+                } else if constexpr (U == 4) {
+                    *reinterpret_cast<float4 *>(dst + o[j]) = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
+                } else {
+                    *reinterpret_cast<float2 *>(dst + o[j]) = make_float2(f[j][0], f[j][1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < U - 1; ++k)
+                    if (c + k < cols) store_elem(dst, sizeof(E) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, o[j] + k, f[j][k]);
+            }
+        }
+    }
+}
+
+// Out of line, one copy a kernel: a CTA runs it a few times, so its instructions'
+// way from memory counts (REPLACE_ROWS).
+__device__ __noinline__ void gp_store_rows(const RowTensor &t, int unit, uint32_t sb, int n, long long off, long long col,
+                                           int cols, const RowTensor *r, long long roff) {
+    if (t.dt == DLC_DATA_BFLOAT16) {
+        if (unit == 4) gp_store_units<unsigned short, 4>(t, sb, n, off, col, cols, r, roff);
+        else if (unit == 2) gp_store_units<unsigned short, 2>(t, sb, n, off, col, cols, r, roff);
+        else gp_store_units<unsigned short, 1>(t, sb, n, off, col, cols, r, roff);
+    } else {
+        if (unit == 4) gp_store_units<float, 4>(t, sb, n, off, col, cols, r, roff);
+        else if (unit == 2) gp_store_units<float, 2>(t, sb, n, off, col, cols, r, roff);
+        else gp_store_units<float, 1>(t, sb, n, off, col, cols, r, roff);
     }
 }
 
@@ -295,54 +395,16 @@ struct GpStore {
         }
     }
 
-    // Row by row, a lane per column, sixteen rows at a time (their loads and stores
-    // are in flight together).  `off`: this lane's row offset in t; `col`: column
-    // in t of v[0], `cols` of them exist; r (or null), with `roff`: a residual
+    // For layouts that TMA cannot write.  `off`: this lane's row offset in t; `col`:
+    // column in t of v[0], `cols` of them exist; r (or null), with `roff`: a residual
     // added on the way.
-    static constexpr int ROWS = 16;
-    __device__ void rows(const RowTensor &t, long long off, const float (&v)[32], long long col, int cols,
-                         const RowTensor *r, long long roff) {
+    __device__ __forceinline__ void rows(const RowTensor &t, int unit, long long off, const float (&v)[32], long long col,
+                                         int cols, const RowTensor *r, long long roff) {
         if (row0 >= M) return;
         const uint32_t sb = next();
         stage_f32(sb, v);
         __syncwarp();
-        const int n = (int)min(32LL, M - row0);
-        const bool in = lane < cols;
-        const long long tc = (col + lane) * t.m.cs, rc = r ? (col + lane) * r->m.cs : 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += ROWS) {
-            float f[ROWS];
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const uint32_t row = (uint32_t)(i0 + i);
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[i]) : "r"(sb + row * 128u +
-                             ((((uint32_t)lane >> 2) ^ (row & 7u)) << 4) + ((uint32_t)lane & 3u) * 4u) : "memory");
-            }
-            if (r) {
-                long long ro[ROWS];
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i) ro[i] = __shfl_sync(0xffffffffu, roff, i0 + i) + rc;
-                if (r->dt == DLC_DATA_BFLOAT16) {  // (the type's branch outside: all loads in flight)
-                    unsigned short w[ROWS];
-#pragma unroll
-                    for (int i = 0; i < ROWS; ++i)
-                        w[i] = in && i0 + i < n ? static_cast<const unsigned short *>(r->p)[ro[i]] : (unsigned short)0;
-#pragma unroll
-                    for (int i = 0; i < ROWS; ++i) f[i] += bf16_bits_f32(w[i]);
-                } else {
-                    float w[ROWS];
-#pragma unroll
-                    for (int i = 0; i < ROWS; ++i) w[i] = in && i0 + i < n ? static_cast<const float *>(r->p)[ro[i]] : 0.f;
-#pragma unroll
-                    for (int i = 0; i < ROWS; ++i) f[i] += w[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const long long to = __shfl_sync(0xffffffffu, off, i0 + i);
-                if (in && i0 + i < n) store_elem(t.p, t.dt, to + tc, f[i]);
-            }
-        }
+        gp_store_rows(t, unit, sb, (int)min(32LL, M - row0), off, col, cols, r, roff);
         __syncwarp();
         if (elect_one()) bulk_commit_group();  // an empty group keeps the buffers' turn
     }
@@ -390,9 +452,7 @@ struct GpResidual {
                 const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack_bf16(u[i]);
-                    v[8 * j + 2 * i] += f.x;
-                    v[8 * j + 2 * i + 1] += f.y;
+                    set2(v, 4 * j + i, add2(get2(v, 4 * j + i), unpack_bf16(u[i])));
                 }
             }
         } else {
@@ -411,7 +471,7 @@ struct GpResidual {
     }
 };
 
-template <bool GATED, int ACT>
+template <bool GATED, bool ROWS, int ACT>
 __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
                             uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const CUtensorMap *tmZ, const CUtensorMap *tmP,
                             const WaitCtl &ctl) {
@@ -439,9 +499,9 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
         float sa = 1.f;
         const bool raw = w.plane >= 0;
         if (valid && !raw) {
-            if (p.z.p && !p.z_tma) zo = row_off(p.z.m, m);
+            if (ROWS && p.z.p) zo = row_off(p.z.m, m);
             if (p.r.p) ro = row_off(p.r.m, m);
-            yo = row_off(p.y.m, m);
+            if (ROWS) yo = row_off(p.y.m, m);
             if (p.sa) sa = __ldg(p.sa + m);
         }
         // (a gated layer has no residual)
@@ -487,28 +547,28 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
             gp_scale_bias(p, v, sa, columns + c0);
             if constexpr (GATED) gp_scale_bias(p, up, sa, columns + p.nout + c0);
             if (p.z.p) {
-                if (p.z_tma) {
+                if (!ROWS || p.z_tma) {
                     st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, v, n, 0);
                     if constexpr (GATED) st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, up, n, 1);
-                } else {
-                    st.rows(p.z, zo, v, n, cols, nullptr, 0);
-                    if constexpr (GATED) st.rows(p.z, zo, up, (long long)p.N + n, cols, nullptr, 0);
+                } else if constexpr (ROWS) {
+                    st.rows(p.z, p.z_unit, zo, v, n, cols, nullptr, 0);
+                    if constexpr (GATED) st.rows(p.z, p.z_unit, zo, up, (long long)p.N + n, cols, nullptr, 0);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_f<ACT>(v[i]);
-            if constexpr (GATED) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= up[i];
+            for (int i = 0; i < 16; ++i) {
+                float2 w = act_f2<ACT>(get2(v, i));
+                if constexpr (GATED) w = mul2(w, get2(up, i));
+                set2(v, i, w);
             }
-            if (p.y_tma && (!p.r.p || p.r_vec)) {
+            if (!ROWS || (p.y_tma && (!p.r.p || p.r_vec))) {
                 if (!GATED) {
                     if (res) rq.add(p.r, v, ro + n, cols);
                     rq.load(p.r, res && c0 + 64 < p.nout, ro + n + 64, cols - 64);
                 }
                 st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
-            } else {
-                st.rows(p.y, yo, v, n, cols, p.r.p ? &p.r : nullptr, ro);
+            } else if constexpr (ROWS) {
+                st.rows(p.y, p.y_unit, yo, v, n, cols, p.r.p ? &p.r : nullptr, ro);
             }
         }
         tc_fence_before_sync();
@@ -519,7 +579,8 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
     __syncwarp();
 }
 
-template <bool E4M3, bool A_MN, bool B_MN, bool GATED>
+// ROWS: y or z cannot be written by TMA, or the residual not be read in vectors.
+template <bool E4M3, bool A_MN, bool B_MN, bool GATED, bool ROWS>
 __global__ void __launch_bounds__(GP_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ GpParams p, const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
@@ -587,7 +648,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     } else {
         // (the activation's branch out here: a block's code is straight)
         act_dispatch(p.act, [&](auto act) {
-            gp_epilogue<GATED, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, &tmP, ctl);
+            gp_epilogue<GATED, ROWS, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, &tmP, ctl);
         });
     }
     __syncwarp();
@@ -648,7 +709,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
         }
         act_dispatch(g.act, [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[0][j] = act_f<decltype(act)::value>(v[0][j]);
+            for (int j = 0; j < 2; ++j) set2(v[0], j, act_f2<decltype(act)::value>(get2(v[0], j)));
         });
         if (g.gated) {
 #pragma unroll
@@ -769,6 +830,19 @@ bool vec16_rows(const RowTensor &t) {
            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
 }
 
+// Elements of the widest access (4, 2 or 1) that every row of t takes, and column `n` of it.
+int store_unit(const RowTensor &t, long long n) {
+    if (!t.p || t.m.cs != 1) return 1;
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    for (int u : {4, 2}) {
+        auto mult = [&](long long s) { return s % u == 0; };
+        if ((uintptr_t)t.p % (u * e) == 0 && mult(n) &&
+            (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3))))
+            return u;
+    }
+    return 1;
+}
+
 constexpr int GP_MAX_SPLITS = 16;
 
 struct GemmPlan {
@@ -795,12 +869,13 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     // Tile width, split of the tail, and which of the two kernels, from a model of
-    // the time in microseconds, fitted to 18 shapes from 128 x 1024 -> 512 to
-    // 300 x 4096 -> 8192 and 12000 x 192 -> 256 (its choice is within 8 % of the fastest of
-    // some ten alternatives each).  A k-block takes a pair 0.31 us for 256 columns
-    // and half that for 64 (the MMA thread's turn), so tiles are wide; idle pairs are filled
-    // by splitting the reduction: that costs the partial sums' way through the L2
-    // and a launch.
+    // the time in microseconds, fitted to 27 shapes from 128 x 1024 -> 512 to
+    // 300 x 4096 -> 8192 and 12000 x 192 -> 256 and several epilogues each (its choice is
+    // within 5 % of the fastest of up to ten alternatives).  A k-block takes a pair
+    // 0.34 us for 256 columns and half that for 64 (the MMA thread's turn), a tile's
+    // epilogue 2.9 and 1.5 us; it runs beside the next tile's k-blocks.  Pairs that a
+    // last wave leaves idle are filled by splitting the reduction: that costs the
+    // partial sums' way through the L2 and a launch.
     const int pairs = ctx->sm_count / 2;
     double best = 1e300;
     for (int bn : {256, 192, 128, 64}) {
@@ -808,18 +883,19 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
         if (g.gated && bn % 128) continue;    // and a gated half whole 64-output chunk pairs
         const int nout = g.gated ? bn / 2 : bn, n_tiles = (g.N + nout - 1) / nout;
         const long long tiles = (long long)p.m_tiles * n_tiles;
-        const double kb = std::max(0.143, 0.046 + 0.266 * bn / 256), fixed = 4.2 + 1.6 * bn / 256;
-        const long long tail = tiles % pairs, full = tiles - tail;
-        const double whole = (double)(full / pairs) * (p.num_kb * kb + 0.8);
+        const double w = bn / 256.0, main = p.num_kb * std::max(0.161, 0.055 + 0.288 * w);
+        const double epi = 0.97 - 0.62 * w + 2.55 * nout / 256.0, next = std::max(main, epi), fixed = 2.94;
+        const long long tail = tiles % pairs, full = tiles / pairs;
+        const double whole = full ? main + (double)(full - 1) * next + epi : 0.;
         for (int s = 1; s <= GP_MAX_SPLITS; ++s) {
             double t = fixed + whole;
             if (s == 1) {
-                if (tail) t += p.num_kb * kb;
+                if (tail) t += full ? next : main + epi;
             } else {
                 if (tail * s > pairs || 2 * s > p.num_kb) break;
-                t += (p.num_kb + s - 1) / s * kb + 1.7 + (double)tail * s * 256 * bn * 8 / 5e6;
+                t += (double)((p.num_kb + s - 1) / s) / p.num_kb * main + 3.7 + (double)tail * s * 256 * bn * 8 / 5e6;
             }
-            if (t < best) best = t, p.bn = bn, p.splits = s, p.full_tiles = (int)std::min(s == 1 ? tiles : full, 0x7fffffffLL);
+            if (t < best) best = t, p.bn = bn, p.splits = s, p.full_tiles = (int)std::min(s == 1 ? tiles : tiles - tail, 0x7fffffffLL);
         }
     }
     // Up to 64 rows the filters' stream decides, which the few-row kernel carries
@@ -900,14 +976,15 @@ bool encode_output(const dlcContext *ctx, CUtensorMap *tm, const RowTensor &o, l
                   t.dt == DLC_DATA_FLOAT ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+template <bool ROWS>
 const void *pair_kernel(bool e4m3, bool a_mn, bool b_mn, bool gated) {
     if (gated)
-        return e4m3 ? (const void *)gemm_pair_kernel<true, false, false, true>
-                    : (const void *)gemm_pair_kernel<false, false, false, true>;
-    if (e4m3) return (const void *)gemm_pair_kernel<true, false, false, false>;
-    if (a_mn) return (const void *)gemm_pair_kernel<false, true, true, false>;
-    return b_mn ? (const void *)gemm_pair_kernel<false, false, true, false>
-                : (const void *)gemm_pair_kernel<false, false, false, false>;
+        return e4m3 ? (const void *)gemm_pair_kernel<true, false, false, true, ROWS>
+                    : (const void *)gemm_pair_kernel<false, false, false, true, ROWS>;
+    if (e4m3) return (const void *)gemm_pair_kernel<true, false, false, false, ROWS>;
+    if (a_mn) return (const void *)gemm_pair_kernel<false, true, true, false, ROWS>;
+    return b_mn ? (const void *)gemm_pair_kernel<false, false, true, false, ROWS>
+                : (const void *)gemm_pair_kernel<false, false, false, false, ROWS>;
 }
 
 // Pairs that the device holds at once (each CTA takes an SM's shared memory);
@@ -991,6 +1068,8 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         return DLC_STATUS_EXECUTION_FAILED;
     p.y_tma = tma_store_rows(g.y, g.M, g.N, 1);
     p.z_tma = g.z.p && tma_store_rows(g.z, g.M, g.N, g.gated ? 2 : 1);
+    p.y_unit = store_unit(g.y, 0);
+    p.z_unit = store_unit(g.z, g.gated ? g.N : 0);
     if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, g.N, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
     if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
     if (tail) {
@@ -1001,13 +1080,15 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
     }
-    const bool f32_stage = tail || !p.y_tma || (g.r.p && !p.r_vec) || g.y.dt == DLC_DATA_FLOAT || (g.z.p && (!p.z_tma || g.z.dt == DLC_DATA_FLOAT));
+    const bool rows = !p.y_tma || (g.r.p && !p.r_vec) || (g.z.p && !p.z_tma);
+    const bool f32_stage = tail || rows || g.y.dt == DLC_DATA_FLOAT || (g.z.p && g.z.dt == DLC_DATA_FLOAT);
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
     const int stage_bytes = GP_A_BYTES + (int)p.b_stage;
     p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - GP_COLUMNS - GP_BAR_AREA - epi_bytes) / stage_bytes);
     const size_t smem = (size_t)p.stages * stage_bytes + epi_bytes + GP_COLUMNS + GP_BAR_AREA;
-    const void *kern = pair_kernel(e4m3, g.a.trans != 0, g.b.trans != 0, g.gated != 0);
+    const bool a_mn = g.a.trans != 0, b_mn = g.b.trans != 0, gated = g.gated != 0;
+    const void *kern = rows ? pair_kernel<true>(e4m3, a_mn, b_mn, gated) : pair_kernel<false>(e4m3, a_mn, b_mn, gated);
     if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);
     void *args[] = {&p, &ta, &tb, &ty, &tz, &tp};

@@ -50,11 +50,11 @@ struct FrParams {
 // Adds up the partial sums of rows j0 .. j0+count-1 of a tile over the cluster,
 // in the order of their ranges, and applies the epilogue: a thread four filters,
 // the same ones for all its rows.  `sums`: a CTA's partial sums, [row][filter], at
-// the same address in each.  A launch runs this code once or a few times, so
+// the same address in each; `scale`: the rows' scales.  A launch runs this code once or a few times, so
 // fetching it counts: it is kept short (unrolled over rows it took 2.1 us a pass
 // of four rows, most of it instruction fetches).
 template <bool GATED>
-__device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int split, long long m0, int n, int f, int j0,
+__device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, const float *scale, int split, long long m0, int n, int f, int j0,
                                         int count, const float (&sb)[GATED ? 2 : 1][4],
                                         const float (&bias)[GATED ? 2 : 1][4]) {
     constexpr int HALVES = GATED ? 2 : 1, AT_ONCE = 4;  // ranges loaded before they are added
@@ -63,7 +63,7 @@ __device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int sp
 #pragma unroll 1
     for (int j = (int)threadIdx.x >> p.quads_log2; j < count; j += FR_THREADS >> p.quads_log2) {
         const long long m = m0 + j0 + j;
-        const float sa = p.sa ? __ldg(p.sa + m) : 1.f;
+        const float sa = scale[j0 + j];
         const uint32_t at = sums + ((uint32_t)(j0 + j) * FR_M + (uint32_t)f) * 4u;
         float v[HALVES][4];
 #pragma unroll
@@ -102,7 +102,7 @@ __device__ __forceinline__ void fr_join(const FrParams &p, uint32_t sums, int sp
         float y[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
         act_dispatch(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = act_f<decltype(act)::value>(y[i]);
+            for (int i = 0; i < 2; ++i) set2(y, i, act_f2<decltype(act)::value>(get2(y, i)));
         });
         if (GATED) {
 #pragma unroll
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     __shared__ alignas(8) uint64_t full[FR_MAX_STAGES], empty[FR_MAX_STAGES], done;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
+    __shared__ float scale[FR_MAX_ROWS];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t smem = raw + ((1024u - (raw & 1023u)) & 1023u);  // same offset in every CTA
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
             sb[h][i] = p.sb && i < cols ? __ldg(p.sb + (long long)h * p.N + n + i) : 1.f;
             bias[h][i] = p.bias && i < cols ? __ldg(p.bias + (long long)h * p.N + n + i) : 0.f;
         }
+    for (int j = (int)threadIdx.x; j < p.rows; j += FR_THREADS) scale[j] = p.sa && m0 + j < p.M ? __ldg(p.sa + m0 + j) : 1.f;
     bool good;
     {
         volatile int dummy = 0;  // (an abort elsewhere still commits `done`)
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     good = good && abort_flag == 0;
     const int per = (p.rows + p.splits - 1) / p.splits, j0 = split * per;
     const int count = (int)min((long long)min(per, p.rows - j0), p.M - m0 - j0);
-    if (good && cols > 0) fr_join<GATED>(p, smem, split, m0, n, f, j0, count, sb, bias);
+    if (good && cols > 0) fr_join<GATED>(p, smem, scale, split, m0, n, f, j0, count, sb, bias);
     __syncwarp();
     if (p.splits > 1) {
         cluster_arrive();

@@ -90,9 +90,6 @@ __device__ __forceinline__ void store_row(int dt, char *at, const Cols<W, V> &k,
     }
 }
 
-__device__ __forceinline__ float2 pair(const float *f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
-__device__ __forceinline__ void set_pair(float *f, int i, float2 v) { f[2 * i] = v.x, f[2 * i + 1] = v.y; }
-
 template <int W>
 __device__ __forceinline__ void load_gamma(const float *gamma, int c, int C, bool vec, float *v) {
     if (W == 8 && vec && c + W <= C) {
@@ -186,7 +183,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
         float *v = f[0];
         if (p.r.p) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) set_pair(v, i, add2(pair(v, i), pair(f[1], i)));
+            for (int i = 0; i < E / 2; ++i) set2(v, i, add2(get2(v, i), get2(f[1], i)));
         }
         if (p.t.p && on) store_row<W, V>(p.t.dt, wt.at(p.t, row, c), cols, f[0]);
         fetch();
@@ -194,8 +191,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
         float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            sq = fma2(pair(v, i), pair(v, i), sq);
-            set_pair(v, i, mul2(pair(v, i), pair(g, i)));
+            sq = fma2(get2(v, i), get2(v, i), sq);
+            set2(v, i, mul2(get2(v, i), get2(g, i)));
         }
         if (e4m3) {
 #pragma unroll
@@ -210,7 +207,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
             rho = rho / s;
         }
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) set_pair(v, i, mul2(pair(v, i), make_float2(rho, rho)));
+        for (int i = 0; i < E / 2; ++i) set2(v, i, mul2(get2(v, i), make_float2(rho, rho)));
         store_row<W, V>(p.y.dt, wy.at(p.y, row, c), cols, f[0]);
     }
 }
@@ -350,9 +347,9 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
         float2 sq = make_float2(0.f, 0.f), dot = sq;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            const float2 v = pair(f[1], i);
+            const float2 v = get2(f[1], i);
             sq = fma2(v, v, sq);
-            dot = fma2(mul2(pair(f[0], i), pair(g, i)), v, dot);
+            dot = fma2(mul2(get2(f[0], i), get2(g, i)), v, dot);
         }
         fetch();
         const float2 red = row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, slot, buf, parity);
@@ -362,10 +359,10 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_BWD_BLOCKS)
         const float2 rho2 = make_float2(rho, rho), k2 = make_float2(k, k);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            const float2 d = mul2(pair(f[0], i), rho2), v = pair(f[1], i);
-            set_pair(acc, i, fma2(d, v, pair(acc, i)));
-            const float2 s = p.dt.p ? pair(f[2], i) : make_float2(0.f, 0.f);
-            set_pair(f[2], i, fma2(d, pair(g, i), fma2(v, k2, s)));
+            const float2 d = mul2(get2(f[0], i), rho2), v = get2(f[1], i);
+            set2(acc, i, fma2(d, v, get2(acc, i)));
+            const float2 s = p.dt.p ? get2(f[2], i) : make_float2(0.f, 0.f);
+            set2(f[2], i, fma2(d, get2(g, i), fma2(v, k2, s)));
         }
         store_row<W, V>(p.dx.dt, wx.at(p.dx, row, c), cols, f[2]);
     }
