@@ -267,8 +267,12 @@ struct BackwardPlan {
     ActGradProblem ag;
     GemmProblem gx, gw;       // dx = dz w, dw = dz^T x
     bool run_ag;
-    size_t dz_bytes, scratch;  // dz, then one scratch area that the steps use in turn
-    size_t total() const { return dz_bytes + scratch; }
+    // operands of the products that have to be copied first, all in one launch
+    RowTensor source[DLC_MAX_PACKS];
+    PackItem pack[DLC_MAX_PACKS];
+    int packs = 0;
+    size_t kept, scratch;  // dz and the copies, then one scratch area that the steps use in turn
+    size_t total() const { return kept + scratch; }
 };
 
 BackwardPlan plan_backward(dlcContext *h, bool gated, const RowTensor &x, const RowTensor &w, dlcActivationMode_t act,
@@ -286,33 +290,49 @@ BackwardPlan plan_backward(dlcContext *h, bool gated, const RowTensor &x, const 
     // with TMA; rounding it is what lets them run on the tensor cores.
     // Without an activation dz is dy itself when that is BF16 already.
     RowTensor dz = dy;
-    b.dz_bytes = 0;
+    b.kept = 0;
+    auto keep = [&](size_t bytes) {  // (sizing only: any aligned address)
+        void *at = ws ? (void *)(ws + b.kept) : (void *)(uintptr_t)WS_ALIGN;
+        b.kept += ws_round(bytes);
+        return at;
+    };
     const bool copy = gated || act != DLC_ACTIVATION_IDENTITY || dy.dt != DLC_DATA_BFLOAT16;
     if (copy) {
         const long long ld = ((long long)K + 7) / 8 * 8;
-        b.dz_bytes = ws_round((size_t)rows * ld * 2);
-        dz.p = ws ? (void *)ws : (void *)(uintptr_t)WS_ALIGN;  // (sizing only: any aligned address)
+        dz.p = keep((size_t)rows * ld * 2);
         dz.dt = DLC_DATA_BFLOAT16;
         dz.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
         b.ag.dz = dz;
     }
     b.run_ag = copy || dbias;
-    char *scratch = ws ? ws + b.dz_bytes : nullptr;
+    // (dz is read by both products: its copy serves both)
+    auto packed = [&](const RowTensor &t, bool wanted, long long n, int ch) {
+        const size_t bytes = wanted ? dlc_pack_bytes(t, n, ch) : 0;
+        if (!bytes) return t;
+        void *dst = keep(bytes);
+        b.source[b.packs] = t;
+        b.pack[b.packs] = PackItem{nullptr, n, ch, dst};
+        ++b.packs;
+        return dlc_packed(t, ch, dst);
+    };
+    const RowTensor dz_p = packed(dz, dx.p || dw.p, rows, K), w_p = packed(w, dx.p != nullptr, K, C),
+                    x_p = packed(x, dw.p != nullptr, rows, C);
+    char *scratch = ws ? ws + b.kept : nullptr;
     b.ag.ws = reinterpret_cast<float *>(scratch);
     b.gx.M = rows, b.gx.N = C, b.gx.K = K;
-    b.gx.a.t = dz;
-    b.gx.b.t = w;
+    b.gx.a.t = dz_p;
+    b.gx.b.t = w_p;
     b.gx.b.trans = 1;
     b.gx.y = dx;
     b.gx.ws = scratch;
     b.gw.M = K, b.gw.N = C, b.gw.K = rows;
-    b.gw.a.t = dz;
+    b.gw.a.t = dz_p;
     b.gw.a.trans = 1;
-    b.gw.b.t = x;
+    b.gw.b.t = x_p;
     b.gw.b.trans = 1;
     b.gw.y = dw;
     b.gw.ws = scratch;
-    size_t s = 0;
+    size_t s = 0;  // (the copies made, the products need none of their own)
     if (dbias) s = std::max(s, dlc_act_grad_workspace(h, b.ag));
     if (dx.p) s = std::max(s, dlc_gemm_workspace(h, b.gx));
     if (dw.p) s = std::max(s, dlc_gemm_workspace(h, b.gw));
@@ -380,6 +400,14 @@ dlcStatus_t product_backward(dlcHandle_t h, bool gated, dlcTensorDescriptor_t xd
     if (b.total() && overlaps(span_bytes(ws, b.total()), {s_x, s_w, s_dy, s_z, s_dx, s_dw, s_db}))
         return DLC_STATUS_BAD_PARAM;
     RETURN_IF(enter(h));
+    PackItem packs[DLC_MAX_PACKS];
+    RowTensor source[DLC_MAX_PACKS];
+    for (int i = 0; i < b.packs; ++i) {
+        source[i] = b.source[i];
+        packs[i] = b.pack[i];
+        packs[i].t = &source[i];
+    }
+    RETURN_IF(dlc_launch_pack(h, packs, b.packs));
     if (b.run_ag) RETURN_IF(dlc_launch_act_grad(h, b.ag));
     if (dx) RETURN_IF(dlc_launch_gemm(h, b.gx));
     if (dw) RETURN_IF(dlc_launch_gemm(h, b.gw));

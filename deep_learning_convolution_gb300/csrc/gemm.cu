@@ -65,7 +65,7 @@ struct GpParams {
     uint32_t epi_buf;             // bytes of one epilogue staging buffer
     const float *sa, *sb, *bias;
     RowTensor z, r, y;
-    int y_tma, z_tma, r_vec;
+    int y_tma, z_tma;
     int y_unit, z_unit;           // elements of an aligned access to y (where TMA cannot write it) and z
     int *err;
     unsigned long long timeout_ns;
@@ -395,18 +395,23 @@ struct GpStore {
         }
     }
 
-    // For layouts that TMA cannot write.  `off`: this lane's row offset in t; `col`:
-    // column in t of v[0], `cols` of them exist; r (or null), with `roff`: a residual
-    // added on the way.
-    __device__ __forceinline__ void rows(const RowTensor &t, int unit, long long off, const float (&v)[32], long long col,
-                                         int cols, const RowTensor *r, long long roff) {
-        if (row0 >= M) return;
+    // For layouts that TMA cannot write: a block staged (0 where the warp has no rows),
+    // and then written.  `off`: this lane's row offset in t; `col`: column in t of
+    // v[0], `cols` of them exist; r (or null), with `roff`: a residual added on the way.
+    __device__ __forceinline__ uint32_t stage(const float (&v)[32]) {
+        if (row0 >= M) return 0;
         const uint32_t sb = next();
         stage_f32(sb, v);
         __syncwarp();
-        gp_store_rows(t, unit, sb, (int)min(32LL, M - row0), off, col, cols, r, roff);
-        __syncwarp();
         if (elect_one()) bulk_commit_group();  // an empty group keeps the buffers' turn
+        return sb;
+    }
+
+    __device__ __forceinline__ void rows(const RowTensor &t, int unit, uint32_t sb, long long off, long long col, int cols,
+                                         const RowTensor *r, long long roff) {
+        if (!sb) return;
+        gp_store_rows(t, unit, sb, (int)min(32LL, M - row0), off, col, cols, r, roff);
+        __syncwarp();  // before the buffer's next turn
     }
 };
 
@@ -504,10 +509,10 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
             if (ROWS) yo = row_off(p.y.m, m);
             if (p.sa) sa = __ldg(p.sa + m);
         }
-        // (a gated layer has no residual)
-        const bool res = !GATED && valid && !raw && p.r_vec && p.y_tma;
+        // (a gated layer has no residual; ROWS adds it where the rows are written)
+        const bool res = !GATED && !ROWS && valid && !raw && p.r.p;
         GpResidual rq;
-        if (!GATED) rq.load(p.r, res, ro + n0 + 32 * part, p.N - n0 - 32 * part);
+        if (!GATED && !ROWS) rq.load(p.r, res, ro + n0 + 32 * part, p.N - n0 - 32 * part);
         if (!raw && (p.sb || p.bias)) {
             gp_epi_barrier();  // the tile before has been read
             gp_columns(p, GATED, n0, columns);
@@ -546,13 +551,14 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
             }
             gp_scale_bias(p, v, sa, columns + c0);
             if constexpr (GATED) gp_scale_bias(p, up, sa, columns + p.nout + c0);
+            uint32_t z0 = 0, z1 = 0;  // blocks of z staged for rows
             if (p.z.p) {
                 if (!ROWS || p.z_tma) {
                     st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, v, n, 0);
                     if constexpr (GATED) st.tma(tmZ, p.z.dt == DLC_DATA_BFLOAT16, up, n, 1);
-                } else if constexpr (ROWS) {
-                    st.rows(p.z, p.z_unit, zo, v, n, cols, nullptr, 0);
-                    if constexpr (GATED) st.rows(p.z, p.z_unit, zo, up, (long long)p.N + n, cols, nullptr, 0);
+                } else {
+                    z0 = st.stage(v);
+                    if constexpr (GATED) z1 = st.stage(up);
                 }
             }
 #pragma unroll
@@ -561,14 +567,18 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
                 if constexpr (GATED) w = mul2(w, get2(up, i));
                 set2(v, i, w);
             }
-            if (!ROWS || (p.y_tma && (!p.r.p || p.r_vec))) {
-                if (!GATED) {
+            if constexpr (ROWS) {
+                st.rows(p.z, p.z_unit, z0, zo, n, cols, nullptr, 0);
+                st.rows(p.z, p.z_unit, z1, zo, (long long)p.N + n, cols, nullptr, 0);
+            }
+            if (!ROWS || (p.y_tma && !p.r.p)) {
+                if (!GATED && !ROWS) {
                     if (res) rq.add(p.r, v, ro + n, cols);
                     rq.load(p.r, res && c0 + 64 < p.nout, ro + n + 64, cols - 64);
                 }
                 st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
             } else if constexpr (ROWS) {
-                st.rows(p.y, p.y_unit, yo, v, n, cols, p.r.p ? &p.r : nullptr, ro);
+                st.rows(p.y, p.y_unit, st.stage(v), yo, n, cols, p.r.p ? &p.r : nullptr, ro);
             }
         }
         tc_fence_before_sync();
@@ -727,8 +737,8 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
 
 // ---- operands that TMA cannot load ------------------------------------------------------
 
-// Operands copied to dense rows, each a multiple of 16 bytes long; both of a
-// product's in one launch (blockIdx.z).
+// Operands copied to dense rows, each a multiple of 16 bytes long; those of a
+// product, or of a backward pass's two, in one launch (blockIdx.z).
 struct PackJob {
     RowTensor src;      // strides in units
     void *dst;
@@ -739,7 +749,7 @@ struct PackJob {
 };
 
 struct PackParams {
-    PackJob job[2];
+    PackJob job[DLC_MAX_PACKS];
 };
 
 // Channels contiguous: a warp a row, eight units a lane in flight.
@@ -858,7 +868,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     GemmPlan p;
     const int nb = g.gated ? 2 * g.N : g.N;
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
-    const int e = e4m3 ? 1 : 2, bk = GP_LINE / e;
+    const int bk = e4m3 ? GP_LINE : GP_LINE / 2;
     p.a_rows = g.a.trans ? g.K : g.M;
     p.a_ch = (int)(g.a.trans ? g.M : g.K);
     p.b_rows = g.b.trans ? g.K : nb;
@@ -905,12 +915,11 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
     const long long tail = p.splits > 1 ? (long long)p.m_tiles * p.n_tiles - p.full_tiles : 0;
-    auto packed = [&](long long rows, int ch) { return round256((size_t)rows * ((ch * e + 15) / 16 * 16)); };
     size_t off = 0;
     p.a_off = off;
-    if (p.pack_a) off += packed(p.a_rows, p.a_ch);
+    if (p.pack_a) off += dlc_pack_bytes(g.a.t, p.a_rows, p.a_ch);
     p.b_off = off;
-    if (p.pack_b) off += packed(p.b_rows, p.b_ch);
+    if (p.pack_b) off += dlc_pack_bytes(g.b.t, p.b_rows, p.b_ch);
     p.part_off = off;
     if (!p.few_rows && !p.gemv) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
     p.bytes = off;
@@ -929,8 +938,8 @@ int row_unit(const RowTensor &t, int ch) {
     return (int)e;
 }
 
-// The copy of `t` ([rows][ch]) to `dst`; t becomes the copy.
-PackJob pack_job(const dlcContext *ctx, RowTensor &t, long long rows, int ch, char *dst) {
+// The copy of `t` ([rows][ch]) to `dst`.
+PackJob pack_job(const dlcContext *ctx, const RowTensor &t, long long rows, int ch, void *dst) {
     const int e = dlc_dtype_bytes((dlcDataType_t)t.dt);
     const long long ld = (((long long)ch * e + 15) / 16 * 16) / e;
     PackJob j;
@@ -949,8 +958,6 @@ PackJob pack_job(const dlcContext *ctx, RowTensor &t, long long rows, int ch, ch
     const long long spans = j.transposed ? (j.C + 31) / 32 : (j.C + 255) / 256;
     j.gx = (unsigned)gx;
     j.gy = (unsigned)std::min<long long>(spans, std::max<long long>(1, most / gx));
-    t.p = dst;
-    t.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
     return j;
 }
 
@@ -1049,7 +1056,6 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.z = g.z;
     p.r = g.r;
     p.y = g.y;
-    p.r_vec = g.r.p && vec16_rows(g.r);
     p.err = ctx->d_err;
     p.timeout_ns = ctx->timeout_ns;
     const uint32_t fmt = e4m3 ? 0u : 1u;
@@ -1080,7 +1086,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
     }
-    const bool rows = !p.y_tma || (g.r.p && !p.r_vec) || (g.z.p && !p.z_tma);
+    const bool rows = !p.y_tma || (g.r.p && !vec16_rows(g.r)) || (g.z.p && !p.z_tma);
     const bool f32_stage = tail || rows || g.y.dt == DLC_DATA_FLOAT || (g.z.p && g.z.dt == DLC_DATA_FLOAT);
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
@@ -1123,6 +1129,34 @@ bool dlc_encode_operand(const dlcContext *ctx, CUtensorMap *tm, const GemmOperan
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+size_t dlc_pack_bytes(const RowTensor &t, long long rows, int ch) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    return tma_rows(t, rows, ch) ? 0 : round256((size_t)rows * ((ch * e + 15) / 16 * 16));
+}
+
+RowTensor dlc_packed(const RowTensor &t, int ch, void *dst) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt), ld = (ch * e + 15) / 16 * 16 / e;
+    RowTensor d = t;
+    d.p = dst;
+    d.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
+    return d;
+}
+
+dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n) {
+    if (n == 0) return DLC_STATUS_SUCCESS;
+    PackParams pk;
+    dim3 grid(1, 1, (unsigned)n);
+    for (int i = 0; i < DLC_MAX_PACKS; ++i) {
+        const PackItem &it = items[std::min(i, n - 1)];
+        pk.job[i] = pack_job(ctx, *it.t, it.rows, it.ch, it.dst);
+        grid.x = std::max(grid.x, pk.job[i].gx);
+        grid.y = std::max(grid.y, pk.job[i].gy);
+    }
+    for (int i = 0; i < n; ++i) *items[i].t = dlc_packed(*items[i].t, items[i].ch, items[i].dst);
+    void *args[] = {&pk};
+    return dlc_launch(ctx, (const void *)pack_kernel, grid, dim3(256), 0, args);
+}
+
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
     const GemmPlan p = plan_gemm(ctx, g);
     return p.gemv ? DLC_KERNEL_GEMV : p.few_rows ? DLC_KERNEL_FEW_ROWS : DLC_KERNEL_GEMM_PAIR;
@@ -1133,17 +1167,12 @@ size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g) { return 
 dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &pb) {
     GemmProblem g = pb;
     const GemmPlan pl = plan_gemm(ctx, g);
-    if (pl.pack_a || pl.pack_b) {
-        PackParams pk;
-        int jobs = 0;
-        if (pl.pack_a) pk.job[jobs++] = pack_job(ctx, g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off);
-        if (pl.pack_b) pk.job[jobs++] = pack_job(ctx, g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off);
-        if (jobs == 1) pk.job[1] = pk.job[0];
-        const dim3 grid(std::max(pk.job[0].gx, pk.job[1].gx), std::max(pk.job[0].gy, pk.job[1].gy), (unsigned)jobs);
-        void *args[] = {&pk};
-        const dlcStatus_t st = dlc_launch(ctx, (const void *)pack_kernel, grid, dim3(256), 0, args);
-        if (st != DLC_STATUS_SUCCESS) return st;
-    }
+    PackItem pk[DLC_MAX_PACKS];
+    int packs = 0;
+    if (pl.pack_a) pk[packs++] = PackItem{&g.a.t, pl.a_rows, pl.a_ch, g.ws + pl.a_off};
+    if (pl.pack_b) pk[packs++] = PackItem{&g.b.t, pl.b_rows, pl.b_ch, g.ws + pl.b_off};
+    const dlcStatus_t st = dlc_launch_pack(ctx, pk, packs);
+    if (st != DLC_STATUS_SUCCESS) return st;
     if (pl.gemv) return dlc_launch_gemv(ctx, g);
     return pl.few_rows ? dlc_launch_few_rows(ctx, g) : launch_pair(ctx, g, pl);
 }

@@ -284,6 +284,17 @@ struct ActGradProblem {
 };
 
 // gemm.cu
+// An operand that TMA cannot load ([rows][ch], channels last) and where its copy goes.
+struct PackItem {
+    RowTensor *t;  // becomes the copy
+    long long rows;
+    int ch;
+    void *dst;
+};
+constexpr int DLC_MAX_PACKS = 3;
+size_t dlc_pack_bytes(const RowTensor &t, long long rows, int ch);  // 0: TMA loads it in place
+RowTensor dlc_packed(const RowTensor &t, int ch, void *dst);
+dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n);
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g);
 size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g);
 dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g);
