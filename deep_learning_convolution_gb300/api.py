@@ -52,7 +52,8 @@ class Handle:
         self.set_stream(stream if stream is not None else torch.cuda.current_stream())
 
     def set_stream(self, stream):
-        B.dlcSetStream(self.h, int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+        self.stream = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+        B.dlcSetStream(self.h, self.stream)
 
     def synchronize(self):
         B.dlcSynchronize(self.h)
@@ -349,7 +350,9 @@ class _ChannelOp:
     16-byte alignment.  Activations are [rows, channels] matrices or 4-D
     tensors with ``axes`` ("NHWC" or "NCHW"); weights are [K, C] matrices or
     4-D filters with R = S = 1.  Calls check what each pointer may be (vectors
-    are dense FP32), launch on the handle's stream and return no copies."""
+    are dense FP32), launch on the handle's stream and return no copies.  An
+    operator has one workspace: calls on several streams need an operator each,
+    or an order between them; a captured graph needs its operator alive."""
 
     def __init__(self, handle: Handle, axes: str):
         import torch
@@ -414,6 +417,12 @@ class _ChannelOp:
         for d in self._filters:
             B.dlcDestroyFilterDescriptor(d)
         self._tensors, self._filters = [], []
+        if self.workspace is not None:
+            # kernels on the handle's stream may still use it: not to be handed out before
+            # they are done
+            import torch
+            self.workspace.record_stream(torch.cuda.ExternalStream(self.handle.stream))
+            self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
 
     def __del__(self):
         try:
