@@ -246,7 +246,9 @@ __global__ void __launch_bounds__(GV_WARPS * 32, gv_blocks<E4M3>()) gemv_kernel(
 // Elements, at any stride and alignment.
 template <bool E4M3, bool GATED, int M>
 __global__ void __launch_bounds__(GV_WARPS * 32) gemv_elements_kernel(const __grid_constant__ GvParams p) {
-    constexpr int F = 4, B = 8;  // elements of a filter in flight
+    // elements of a filter in flight (one row of 4003 -> 4004: with 12 24.9 us in BF16
+    // and 15.0 in E4M3, with 8 27.6 and 24.9)
+    constexpr int F = 4, B = M == 1 ? 12 : 8;
     using T = typename std::conditional<E4M3, unsigned char, unsigned short>::type;
     griddep_launch_dependents();
     __shared__ float part[GV_WARPS][32];
@@ -318,19 +320,19 @@ bool gv_vec(const GemmProblem &g) {
 }  // namespace
 
 // Whether this is the faster way.  Measured back to back: the few-row kernel
-// takes 4.9 us and the filters' bytes at 6.3 (E4M3: 5.8) MB/us whatever the rows;
+// takes 4.8 us and the filters' bytes at 6.9 (E4M3: 7.6) MB/us whatever the rows;
 // this one 2.4 us and, in BF16, 6.5, 5.7, 5.2 and 4.7 MB/us for one to four rows
 // (2048 -> 2 x 8192), in E4M3 4.3 and 3.1 MB/us for one and two.  Filters that it
 // has to read element by element run at 1.2 MB/us: faster than packing them
-// first for one or two rows (33 MB, one row: 29 us against 36).
+// first for one or two rows (4003 -> 4004, two rows: 21.9 us against 35).
 bool dlc_gemv_ok(const GemmProblem &g) {
     if (g.a.trans || g.b.trans) return false;
     if (!gv_vec(g)) return g.M <= 2;
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
     if (g.M > (e4m3 ? 2 : 4)) return false;
     const double bytes = (double)(g.gated ? 2 : 1) * g.N * g.K * (e4m3 ? 1 : 2), m = (double)g.M;
-    return e4m3 ? 2.4 + bytes * (1.0 + 0.5 * m) / 6.4e6 < 4.9 + bytes / 5.8e6
-                : 2.4 + bytes * (1.0 + 0.14 * m) / 7.45e6 < 4.9 + bytes / 6.3e6;
+    return e4m3 ? 2.4 + bytes * (1.0 + 0.5 * m) / 6.4e6 < 4.8 + bytes / 7.6e6
+                : 2.4 + bytes * (1.0 + 0.14 * m) / 7.45e6 < 4.8 + bytes / 6.9e6;
 }
 
 dlcStatus_t dlc_launch_gemv(dlcContext *ctx, const GemmProblem &g) {
