@@ -2,7 +2,7 @@
 // residual's addition, the linear layer with its epilogue, the gated
 // projections, and their backward passes.  Validation, the split of a backward
 // pass into its products, and workspace layout; the kernels are in rmsnorm.cu,
-// gemm.cu and act_grad.cu.
+// act_grad.cu, gemm.cu, gemm_rows.cu and gemv.cu.
 #include <atomic>
 #include <cstring>
 #include <initializer_list>

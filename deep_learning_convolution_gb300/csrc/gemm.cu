@@ -21,10 +21,21 @@
 // go to the workspace; a second kernel adds them in a fixed order and applies the
 // epilogue.
 //
-// Roles (11 warps a CTA): warp 0 lane 0 loads a, warp 2 lane 0 loads b, warp 1
-// lane 0 of the leader issues the MMAs into one of two TMEM accumulators,
-// warps 3-10 (two per quarter of the TMEM lanes, alternate 32-column chunks)
-// run the epilogue of the other one.  Every wait is bounded.
+// Roles (11 warps a CTA): a thread of warp 0 loads a, one of warp 2 loads b, one of
+// the leader's warp 1 issues the MMAs into one of two TMEM accumulators, warps
+// 3-10 (two per quarter of the TMEM lanes, alternate 32-column chunks) run the
+// epilogue of the other one.  Every wait is bounded.
+//
+// What bounds it: long reductions the tensor core under the power cap (16384 x
+// 4096 -> 4096 283 us, 1940 TFLOP/s, in E4M3 162 us, 3400; gated 16384 x 4096 ->
+// 2 x 8192 in E4M3 659 us, 3330); short ones the epilogue, 2.9 us for a tile of 256
+// columns in BF16 with a bias and up to 6 with GELU, residual and z, most of it
+// instructions (hence the packed FP32 pairs); small ones the launch, about 5 us
+// from call to call.  Loads, MMAs and bulk stores are issued by an elected thread: by
+// lane 0, four MMAs took 260 cycles to issue instead of 67, and a k-block 0.32 us
+// whatever its width.  Tried and slower: the epilogue's stores straight from
+// registers, 64-column stores, two chunks at a time, bias and scales prefetched into
+// registers (spills).
 #include <atomic>
 #include <cstring>
 
@@ -316,8 +327,9 @@ __device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, 
     }
 }
 
-// Out of line, one copy a kernel: a CTA runs it a few times, so its instructions'
-// way from memory counts (REPLACE_ROWS).
+// Out of line: one copy for all activations, and only kernels of ROWS hold it.  It adds
+// about 1 us a 32-column chunk to a tile's epilogue (204 x 2364 -> 1376's dw: 14.2 us,
+// 10.5 with FP32 rows that TMA can write).
 __device__ __noinline__ void gp_store_rows(const RowTensor &t, int unit, uint32_t sb, int n, long long off, long long col,
                                            int cols, const RowTensor *r, long long roff) {
     if (t.dt == DLC_DATA_BFLOAT16) {
@@ -680,7 +692,8 @@ struct FinishParams {
 };
 
 // Adds the partial tiles in the order of their ranges and applies the
-// epilogue: four columns of a row a thread.
+// epilogue: four columns of a row a thread.  Bound by reading the partial sums
+// from the L2, at about 5 TB/s with their writing.
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishParams f) {
     griddep_launch_dependents();
     const GemmProblem &g = f.g;
@@ -738,7 +751,8 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
 // ---- operands that TMA cannot load ------------------------------------------------------
 
 // Operands copied to dense rows, each a multiple of 16 bytes long; those of a
-// product, or of a backward pass's two, in one launch (blockIdx.z).
+// product, or of a backward pass's two, in one launch (blockIdx.z).  Bound by memory
+// for large operands, by the launch for small ones (about 3 us in a call).
 struct PackJob {
     RowTensor src;      // strides in units
     void *dst;

@@ -11,7 +11,9 @@
 // run in FP32 over a group of threads, and the outputs are written from the
 // registers: the traffic is each input once and each output once, which is
 // what bounds these kernels.  max |y| = rho * max |gamma t|, so the 8-bit
-// scale comes from the same reduction as the sum of squares.
+// scale comes from the same reduction as the sum of squares.  Measured back to
+// back, BF16: forward with both outputs 100352 x 512 74.6 us (5.5 TB/s), backward
+// 25088 x 1024 35.3 us (5.8 TB/s); one row 2.5 us, the cost of a launch.
 #include <initializer_list>
 
 #include "channel.cuh"
@@ -140,7 +142,8 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
     return (amax < SCALE_FLOOR ? SCALE_FLOOR : amax) / E4M3_MAX;
 }
 
-// Rows in registers: `tpr` threads a row, V vectors of W channels a thread.
+// Rows in registers: `tpr` threads a row (8 to 1024: short rows take few, so that a
+// block's loads cover several rows), V vectors of W channels a thread.
 // The next row's loads are issued before this row's reduction waits.
 template <int W, int V, int KIND, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
@@ -216,7 +219,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
 // rows a block, one per lane, the channels dealt to eight warps, so neighbouring
 // rows share the loads.  Otherwise (a row too long for registers): one row a
 // block, its channels dealt to the threads.  The second pass recomputes t (so t
-// may overwrite x or r in place).
+// may overwrite x or r in place); it finds most of a row in the L1 or L2, and the
+// loads' latency bounds these layouts, four a thread in flight.
 constexpr int AHEAD = 4;  // channels a thread loads at once
 
 template <bool LANES>
@@ -444,7 +448,9 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
 }
 
 // out[c] = the sum of the blocks' partial rows, in a fixed order: 32 columns a
-// block, the partial rows dealt to its 32 warps.
+// block, the partial rows dealt to its 32 warps.  At most a few hundred rows from the
+// L2: latency, and the launch, which starts while the grid before it ends (304
+// partial rows of 1024 columns add 2.7 us to a backward call).
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *ws, float *out, int C, int blocks) {
     griddep_launch_dependents();
     __shared__ float part[32][33];

@@ -1,5 +1,5 @@
 // row_ring.cuh -- how the row-wise kernels read: vectors of a row per thread,
-// the next rows prefetched, startsets that step from row to row.
+// the next rows prefetched, addresses that step from row to row.
 #pragma once
 
 #include "channel.cuh"
@@ -76,10 +76,10 @@ __device__ __forceinline__ void load_row(const RowTensor &t, const char *at, con
 // through a ring in shared memory where all of them are BF16 or all FP32.
 enum { ROWS_REGS = 0, ROWS_BF16 = 1, ROWS_F32 = 2 };
 
-// A thread's next rows of T tensors.  A ring (W = 8): copied
-// asynchronously into a ring of S rows in shared memory, of which a thread
-// reads back only what it copied itself (no barrier), so S - 1 rows of every
-// thread are in flight; otherwise one row ahead, in registers.
+// A thread's next rows of T tensors.  With W = 8 they are copied asynchronously
+// into a ring of S rows in shared memory, of which a thread reads back only what
+// it copied itself (no barrier), so S - 1 rows of every thread are in flight
+// without holding registers; mixed types are read one row ahead into registers.
 template <int W, int V, int T>
 struct RowsAhead {
     float next[T][V * W];
