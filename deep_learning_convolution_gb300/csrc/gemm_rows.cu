@@ -350,8 +350,8 @@ dlcStatus_t dlc_launch_few_rows(dlcContext *ctx, const GemmProblem &g) {
     p.quads_log2 = 0;
     while ((4 << p.quads_log2) < pl.filters) ++p.quads_log2;
     p.stage_bytes = (uint32_t)((halves * pl.filters + pl.rows) * FR_LINE);
-    // (stages carry the filters' stream: one row of 2048 -> 2 x 8192 took 15.4 us
-    // with six of them, 16.4 with five)
+    // (stages carry the filters' stream: with tiles of 128 filters, one row of 2048 ->
+    // 2 x 8192 took 15.4 us with six of them, 16.4 with five)
     // (the MMA reads 128 rows of filters whatever the tile holds: what lies behind them goes
     // to accumulator lanes that nothing reads)
     const int behind = std::max(0, (FR_M - halves * pl.filters - pl.rows) * FR_LINE);
