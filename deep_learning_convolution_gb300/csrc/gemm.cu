@@ -246,14 +246,22 @@ __device__ __forceinline__ void gp_scale_bias(const GpParams &p, float (&v)[32],
     }
 }
 
+// Where rows are written, or a residual read: by value (the kernel's parameters behind a
+// reference would be loaded as memory, in the middle of the block).
+struct GpRows {
+    void *p;
+    long long cs;
+    int dt, unit;
+};
+
 // A staged 32 x 32 block (the warp's first `n` rows, `cols` columns) to rows that TMA
 // cannot write: U elements a lane, U rows at a time, eight accesses in flight.
 template <typename E, int U>
-__device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, int n, long long off, long long col, int cols,
-                                               const RowTensor *r, long long roff) {
+__device__ __forceinline__ void gp_store_units(GpRows t, uint32_t sb, int n, long long off, long long col, int cols, GpRows r,
+                                               long long roff) {
     constexpr int LANES = 32 / U;  // of a row
     const int lane = threadIdx.x & 31, sub = lane / LANES, c = (lane - sub * LANES) * U;
-    const long long tc = (col + c) * t.m.cs, rc = r ? (col + c) * r->m.cs : 0;
+    const long long tc = (col + c) * t.cs, rc = (col + c) * r.cs;
     const bool whole = c + U <= cols;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += 8 * U) {
@@ -271,7 +279,7 @@ __device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, 
             else
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[j][0]) : "r"(at) : "memory");
         }
-        if (r) {
+        if (r.p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, roff, i0 + j * U + sub) + rc;
             auto add = [&](auto *src) {
@@ -291,10 +299,10 @@ __device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, 
                             f[j][k] += w[j][k];
                     }
             };
-            if (r->dt == DLC_DATA_BFLOAT16)
-                add(static_cast<const unsigned short *>(r->p));
+            if (r.dt == DLC_DATA_BFLOAT16)
+                add(static_cast<const unsigned short *>(r.p));
             else
-                add(static_cast<const float *>(r->p));
+                add(static_cast<const float *>(r.p));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, off, i0 + j * U + sub) + tc;
@@ -328,17 +336,17 @@ __device__ __forceinline__ void gp_store_units(const RowTensor &t, uint32_t sb, 
 }
 
 // Out of line: one copy for all activations, and only kernels of ROWS hold it.  It adds
-// about 1 us a 32-column chunk to a tile's epilogue (204 x 2364 -> 1376's dw: 14.2 us,
+// about 0.7 us a 32-column chunk to a tile's epilogue (204 x 2364 -> 1376's dw: 12.9 us,
 // 10.5 with FP32 rows that TMA can write).
-__device__ __noinline__ void gp_store_rows(const RowTensor &t, int unit, uint32_t sb, int n, long long off, long long col,
-                                           int cols, const RowTensor *r, long long roff) {
+__device__ __noinline__ void gp_store_rows(GpRows t, uint32_t sb, int n, long long off, long long col, int cols, GpRows r,
+                                           long long roff) {
     if (t.dt == DLC_DATA_BFLOAT16) {
-        if (unit == 4) gp_store_units<unsigned short, 4>(t, sb, n, off, col, cols, r, roff);
-        else if (unit == 2) gp_store_units<unsigned short, 2>(t, sb, n, off, col, cols, r, roff);
+        if (t.unit == 4) gp_store_units<unsigned short, 4>(t, sb, n, off, col, cols, r, roff);
+        else if (t.unit == 2) gp_store_units<unsigned short, 2>(t, sb, n, off, col, cols, r, roff);
         else gp_store_units<unsigned short, 1>(t, sb, n, off, col, cols, r, roff);
     } else {
-        if (unit == 4) gp_store_units<float, 4>(t, sb, n, off, col, cols, r, roff);
-        else if (unit == 2) gp_store_units<float, 2>(t, sb, n, off, col, cols, r, roff);
+        if (t.unit == 4) gp_store_units<float, 4>(t, sb, n, off, col, cols, r, roff);
+        else if (t.unit == 2) gp_store_units<float, 2>(t, sb, n, off, col, cols, r, roff);
         else gp_store_units<float, 1>(t, sb, n, off, col, cols, r, roff);
     }
 }
@@ -420,9 +428,9 @@ struct GpStore {
     }
 
     __device__ __forceinline__ void rows(const RowTensor &t, int unit, uint32_t sb, long long off, long long col, int cols,
-                                         const RowTensor *r, long long roff) {
+                                         GpRows r = GpRows{nullptr, 0, 0, 1}, long long roff = 0) {
         if (!sb) return;
-        gp_store_rows(t, unit, sb, (int)min(32LL, M - row0), off, col, cols, r, roff);
+        gp_store_rows(GpRows{t.p, t.m.cs, t.dt, unit}, sb, (int)min(32LL, M - row0), off, col, cols, r, roff);
         __syncwarp();  // before the buffer's next turn
     }
 };
@@ -580,8 +588,8 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
                 set2(v, i, w);
             }
             if constexpr (ROWS) {
-                st.rows(p.z, p.z_unit, z0, zo, n, cols, nullptr, 0);
-                st.rows(p.z, p.z_unit, z1, zo, (long long)p.N + n, cols, nullptr, 0);
+                st.rows(p.z, p.z_unit, z0, zo, n, cols);
+                st.rows(p.z, p.z_unit, z1, zo, (long long)p.N + n, cols);
             }
             if (!ROWS || (p.y_tma && !p.r.p)) {
                 if (!GATED && !ROWS) {
@@ -590,7 +598,7 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
                 }
                 st.tma(tmY, p.y.dt == DLC_DATA_BFLOAT16, v, n, 0);
             } else if constexpr (ROWS) {
-                st.rows(p.y, p.y_unit, st.stage(v), yo, n, cols, p.r.p ? &p.r : nullptr, ro);
+                st.rows(p.y, p.y_unit, st.stage(v), yo, n, cols, GpRows{p.r.p, p.r.m.cs, p.r.dt, 1}, ro);
             }
         }
         tc_fence_before_sync();
