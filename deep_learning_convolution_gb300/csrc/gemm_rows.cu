@@ -311,10 +311,12 @@ FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g) {
     p.row_tiles = (int)std::min<long long>((g.M + p.rows - 1) / p.rows, 65535);
     // Filters and CTAs a tile from a model of the time in microseconds, fitted to eleven
     // shapes from 16 x 512 -> 512 to 128 x 4096 -> 8192 (its choice is within 4 % of
-    // the fastest of some twenty alternatives each): the launch; per k-block a turn of
-    // the MMA thread or the filters' bytes; the partial sums' way to the epilogue and
-    // the barriers of a cluster.  The SMs of a GPC that a cluster does not fill stay
-    // idle, so fewer clusters run at once than the SMs suggest.
+    // the fastest of some twenty alternatives each), its level set against the pair
+    // kernel's model on twenty more from 100 x 1024 -> 2 x 1024 to 10932 x 64 -> 320:
+    // the launch; per k-block a turn of the MMA thread or the filters' bytes; the
+    // partial sums' way to the epilogue and the barriers of a cluster.  The SMs of a
+    // GPC that a cluster does not fill stay idle, so fewer clusters run at once than
+    // the SMs suggest.
     const int halves = g.gated ? 2 : 1, most = FR_M / halves;
     p.us = 1e300;
     for (int s = 1; s <= FR_MAX_SPLITS && (s == 1 || 2 * s <= p.num_kb); ++s) {
@@ -325,7 +327,8 @@ FewRowsPlan dlc_few_rows_plan(const dlcContext *ctx, const GemmProblem &g) {
             const long long clusters = (long long)tiles * p.row_tiles, waves = (clusters + at_once - 1) / at_once;
             const double ctas = (double)clusters * s / (double)waves, own = p.rows * halves * filters / 16384.0;
             const double kb = std::max(0.23, halves * filters * FR_LINE * ctas / 5.8e6);
-            const double t = 2.0 + 1.4 * ctas / ctx->sm_count +
+            // (a later wave starts from nothing: barriers, tensor memory, first loads)
+            const double t = 2.85 + 1.4 * ctas / ctx->sm_count + 3.0 * (double)(waves - 1) +
                              waves * ((p.num_kb + s - 1) / s * kb + (s > 1 ? 0.9 : 0.) + 1.9 * own * (2.0 - 1.0 / s));
             if (t < p.us) p.us = t, p.splits = s, p.filters = filters, p.filter_tiles = tiles;
         }
