@@ -288,7 +288,7 @@ __device__ __forceinline__ void gp_store_units(GpRows t, uint32_t sb, int n, lon
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
-                    for (int k = 0; k < U; ++k) w[j][k] = c + k < cols && i0 + j * U + sub < n ? src[o[j] + k] : (R)0;
+                    for (int k = 0; k < U; ++k) w[j][k] = c + k < cols && i0 + j * U + sub < n ? src[o[j] + k * r.cs] : (R)0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
