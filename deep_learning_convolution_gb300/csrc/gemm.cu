@@ -37,6 +37,7 @@
 // registers, 64-column stores, two chunks at a time, bias and scales prefetched into
 // registers (spills).
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "channel.cuh"
@@ -933,9 +934,18 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     // Up to 64 rows the filters' stream decides, which the few-row kernel carries
     // whatever the model says (gated 2048 -> 2 x 8192: 16 rows 14.3 us, the pair kernel 20.6,
     // 64 rows 15.1 and 16.7; at worst level, 64 x 512 -> 512 5.0 and 4.9).
-    p.few_rows = !g.a.trans && !g.b.trans && (g.M <= 64 || dlc_few_rows_plan(ctx, g).us < best);
+    // Outputs that TMA cannot write cost the pair kernel's epilogue about another 4 us
+    // for 256 columns (785 x 147 -> 1001: 12.1 us, the few-row kernel 11.0; 2842 x 848 ->
+    // 114 with FP32 outputs 12.6 and 9.4).
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
+    if (!g.a.trans && !g.b.trans) {
+        const double waves = std::ceil((double)p.m_tiles * p.n_tiles / pairs);
+        const double rows = tma_store_rows(g.y, g.M, g.N, 1) ? 0. : 4.0 * p.bn / 256 * waves;
+        p.few_rows = g.M <= 64 || dlc_few_rows_plan(ctx, g).us < best + rows;
+    } else {
+        p.few_rows = false;
+    }
     const long long tail = p.splits > 1 ? (long long)p.m_tiles * p.n_tiles - p.full_tiles : 0;
     size_t off = 0;
     p.a_off = off;
