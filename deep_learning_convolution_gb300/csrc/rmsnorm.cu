@@ -137,10 +137,22 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, int slot
     return make_float2(a, b);
 }
 
-// The scale of an E4M3 row whose largest |y| is `amax` (NaN stays NaN).
-__device__ __forceinline__ float e4m3_scale(float amax) {
-    return (amax < SCALE_FLOOR ? SCALE_FLOOR : amax) / E4M3_MAX;
-}
+// An E4M3 row's scale, and the two factors that take gamma * t to the stored values
+// y / scale, one after the other.  Their product rho / scale leaves FP32's range where
+// |y| is near the scale's floor and rho large (a zero row under an epsilon of 1e-12):
+// infinity times zero would be NaN, so rho then comes first.  A row of zeros is zeros
+// without an epsilon too.  NaN stays NaN.
+struct E4m3Row {
+    float scale, first, then;
+    __device__ __forceinline__ E4m3Row(float squares, float amax, float rho) {
+        if (squares == 0.f && amax == 0.f) rho = 0.f;
+        const float top = amax * rho;
+        scale = (top < SCALE_FLOOR ? SCALE_FLOOR : top) / E4M3_MAX;
+        first = 1.f;
+        then = rho / scale;
+        if (isinf(then)) first = rho, then = 1.f / scale;
+    }
+};
 
 // Rows in registers: `tpr` threads a row (8 to 1024: short rows take few, so that a
 // block's loads cover several rows), V vectors of W channels a thread.
@@ -205,9 +217,13 @@ __global__ void __launch_bounds__(MAXT, MAXT > RMS_THREADS ? 1 : RMS_FWD_BLOCKS)
         if (!on) continue;
         float rho = rsqrtf(red.x * inv_c + p.eps);
         if (e4m3) {
-            const float s = e4m3_scale(red.y * rho);
-            if (t == 0) p.scale[row] = s;
-            rho = rho / s;
+            const E4m3Row q(red.x, red.y, rho);
+            if (t == 0) p.scale[row] = q.scale;
+            if (q.first != 1.f) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) set2(v, i, mul2(get2(v, i), make_float2(q.first, q.first)));
+            }
+            rho = q.then;
         }
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) set2(v, i, mul2(get2(v, i), make_float2(rho, rho)));
@@ -280,11 +296,11 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
         }
         const float2 red = M::template join<true>(sq, mx, part);
         if (!on) continue;
-        float f = rsqrtf(red.x / (float)p.C + p.eps);
+        float f = rsqrtf(red.x / (float)p.C + p.eps), first = 1.f;
         if (p.y.dt == DLC_DATA_FLOAT8_E4M3) {
-            const float s = e4m3_scale(red.y * f);
-            if (M::first() == 0) p.scale[row] = s;
-            f = f / s;
+            const E4m3Row q(red.x, red.y, f);
+            if (M::first() == 0) p.scale[row] = q.scale;
+            first = q.first, f = q.then;
         }
         const long long to = p.t.p ? row_off(p.t.m, row) : 0, yo = row_off(p.y.m, row);
         for (int c = M::first(); c < p.C; c += AHEAD * M::STEP) {
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
                 const int ci = c + i * M::STEP;
                 if (ci >= p.C) break;
                 if (p.t.p) store_elem(p.t.p, p.t.dt, to + ci * p.t.m.cs, v[i]);
-                store_elem(p.y.p, p.y.dt, yo + ci * p.y.m.cs, v[i] * __ldg(p.gamma + ci) * f);
+                store_elem(p.y.p, p.y.dt, yo + ci * p.y.m.cs, v[i] * __ldg(p.gamma + ci) * first * f);
             }
         }
     }

@@ -541,7 +541,8 @@ dlcStatus_t dlcActivationForward(dlcHandle_t handle, dlcActivationMode_t mode, d
  * channel.  y: FLOAT, BFLOAT16, or FLOAT8_E4M3 with scale[row] = max over
  * channels of |y| / 448 (FLOAT, one per row in order n, h, w; required then and
  * NULL otherwise; max |y| counts as at least 1e-30, so a row of zeros gives
- * zeros).  NaN or infinity in a row makes that row NaN or zero, no other.
+ * zeros whatever epsilon is; FLOAT and BFLOAT16 y of a row of zeros with epsilon
+ * 0 is 0 / 0, NaN).  NaN or infinity in a row makes that row NaN or zero, no other.
  * total may be x or residual in place (same descriptor values).  epsilon >= 0. */
 dlcStatus_t dlcRmsNormForward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t xDesc,
                               const void *x, dlcTensorDescriptor_t residualDesc,
