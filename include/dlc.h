@@ -543,7 +543,10 @@ dlcStatus_t dlcActivationForward(dlcHandle_t handle, dlcActivationMode_t mode, d
  * NULL otherwise; max |y| counts as at least 1e-30, so a row of zeros gives
  * zeros whatever epsilon is; FLOAT and BFLOAT16 y of a row of zeros with epsilon
  * 0 is 0 / 0, NaN).  NaN or infinity in a row makes that row NaN or zero, no other.
- * total may be x or residual in place (same descriptor values).  epsilon >= 0. */
+ * total may be x or residual in place (same descriptor values).  epsilon >= 0.
+ * Squares are summed in FP32: rows whose sum of squares leaves its range (values
+ * of 1e18 and more, or of 1e-18 and less beside a smaller epsilon) do not have
+ * this result, nor its gradient. */
 dlcStatus_t dlcRmsNormForward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t xDesc,
                               const void *x, dlcTensorDescriptor_t residualDesc,
                               const void *residual, const float *gamma,

@@ -51,3 +51,18 @@ def test_e4m3_rows_under_a_zero_gamma_are_zeros(handle, c, layout):
     y, scale = out_like(5, c, F8, layout), out_like(5, 1, F32)[:, 0]
     api.RmsNormForward(handle, x, y, eps=1e-20)(x, torch.zeros(c, device="cuda"), y, scale=scale)
     assert (y.float() == 0).all() and torch.isfinite(scale).all()
+
+
+@pytest.mark.parametrize("c,layout", NORM_LAYOUTS)
+def test_norm_backward_of_tiny_and_large_rows(handle, c, layout):
+    """Rows of size 1e-17 to 1e16 with no epsilon: rho^3 alone leaves FP32's
+    range, the gradient does not."""
+    sizes = [1.0, 1e-13, 1e-15, 1e-17, 1e13, 1e15, 1e16]
+    t = rand(len(sizes), c, seed=1) * torch.tensor(sizes, device="cuda")[:, None]
+    t, dy = laid_out(t, layout), laid_out(rand(len(sizes), c, seed=2), layout)
+    gamma, dgamma = 1 + 0.3 * rand(c, seed=3), out_like(c, 1, F32)[:, 0]
+    dx = out_like(len(sizes), c, F32, layout)
+    api.RmsNormBackward(handle, dy, t, dx, eps=0.0)(dy, t, gamma, dx, dgamma=dgamma)
+    want, wg, bx, bg = ref.norm_backward(f64(dy), f64(t), f64(gamma), None, 0.0)
+    close(dx, want, 4 * ref.norm_rel(c) * bx + ref.stored(want, F32), "dx")
+    close(dgamma, wg, (ref.norm_rel(c) + ref.U32 * (len(sizes) + 64)) * bg, "dgamma")
