@@ -31,6 +31,12 @@ constexpr int RMS_MAX_WARPS = 32;
 // Blocks of 256 threads an SM is to hold (what the registers are limited for).
 constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 
+// A ring that a block's shared memory cannot hold (FP32 rows of 8193 to 16384 channels:
+// 256 KiB forward, 384 backward) gives way to one row ahead in registers forward, and to the
+// two-pass kernel backward, where the registers spill.  2730 x 12288: forward 171 us;
+// backward 261 us, 433 through registers.
+constexpr size_t RMS_MAX_RING = 226 * 1024;
+
 // Rows of the ring.  Measured, 100352 x 512 forward / 25088 x 1024 backward, BF16:
 // 3 rows at 4 / 2 blocks an SM 74.5 / 40.0 us; 4 rows 77.6 / 41.1; one row ahead
 // in registers 109 us forward.
@@ -545,6 +551,14 @@ RowPlan plan_rows(long long rows, int C, bool cs1, bool vec, bool ring, int per_
     return r;
 }
 
+// One row a block at a time, twice over it.
+RowPlan two_pass_rows(long long rows, int sm_count) {
+    RowPlan r;
+    r.threads = RMS_THREADS;
+    r.blocks = std::min(rows, (long long)sm_count * 4);
+    return r;
+}
+
 RowPlan plan_fwd(const dlcContext *ctx, const RmsProblem &p) {
     return plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
                      vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), ring({p.x, p.r}), RMS_FWD_BLOCKS, ctx->sm_count);
@@ -612,11 +626,12 @@ dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
     RmsProblem p = pb;
     int tpr = r.tpr, gamma_vec = (uintptr_t)p.gamma % 16 == 0;
     void *args[] = {&p, &tpr, &gamma_vec};
-    const RowKernel k =
+    RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
         : r.w == 1 ? (pieces_ok(p.x) && pieces_ok(p.r) ? fwd_kernel<1, ROWS_BF16>(r, p.C) : fwd_kernel<1, ROWS_REGS>(r, p.C))
         : all_of(DLC_DATA_BFLOAT16, {p.x, p.r}) ? fwd_kernel<8, ROWS_BF16>(r, p.C)
         : all_of(DLC_DATA_FLOAT, {p.x, p.r}) ? fwd_kernel<8, ROWS_F32>(r, p.C) : fwd_kernel<8, ROWS_REGS>(r, p.C);
+    if (k.smem > RMS_MAX_RING) k = r.w == 1 ? fwd_kernel<1, ROWS_REGS>(r, p.C) : fwd_kernel<8, ROWS_REGS>(r, p.C);
     if (!dlc_allow_smem(ctx, k.fn, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
     return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
@@ -629,15 +644,19 @@ size_t dlc_rms_bwd_workspace(const dlcContext *ctx, const RmsBwdProblem &p) {
 }
 
 dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
-    const RowPlan r = plan_bwd(ctx, pb);
+    RowPlan r = plan_bwd(ctx, pb);
     RmsBwdProblem p = pb;
     int tpr = r.tpr, gamma_vec = (uintptr_t)p.gamma % 16 == 0;
     void *args[] = {&p, &tpr, &gamma_vec};
-    const RowKernel k =
+    RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_bwd_any_kernel<true> : (const void *)rms_bwd_any_kernel<false>, 0}
         : r.w == 1 ? (pieces_ok(p.dy) && pieces_ok(p.t) && pieces_ok(p.dt) ? bwd_kernel<1, ROWS_BF16>(r, p.C) : bwd_kernel<1, ROWS_REGS>(r, p.C))
         : all_of(DLC_DATA_BFLOAT16, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_BF16>(r, p.C)
         : all_of(DLC_DATA_FLOAT, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_F32>(r, p.C) : bwd_kernel<8, ROWS_REGS>(r, p.C);
+    if (k.smem > RMS_MAX_RING) {
+        r = two_pass_rows(p.rows, ctx->sm_count);
+        k = RowKernel{(const void *)rms_bwd_any_kernel<false>, 0};
+    }
     const int rpb = r.w ? r.threads / r.tpr : 1;
     const size_t smem = std::max(k.smem, rpb > 1 && p.dgamma ? (size_t)rpb * p.C * sizeof(float) : 0);
     if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;

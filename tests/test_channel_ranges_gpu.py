@@ -66,3 +66,38 @@ def test_norm_backward_of_tiny_and_large_rows(handle, c, layout):
     want, wg, bx, bg = ref.norm_backward(f64(dy), f64(t), f64(gamma), None, 0.0)
     close(dx, want, 4 * ref.norm_rel(c) * bx + ref.stored(want, F32), "dx")
     close(dgamma, wg, (ref.norm_rel(c) + ref.U32 * (len(sizes) + 64)) * bg, "dgamma")
+
+
+LONG = [8184, 8192, 8193, 8200, 12288, 16384, 16392]
+
+
+@pytest.mark.parametrize("c", LONG)
+@pytest.mark.parametrize("xdt,rdt,ydt", [(F32, F32, F32), (F32, None, F8), (BF, BF, BF), (BF, F32, F32)])
+def test_norm_of_long_rows(handle, c, xdt, rdt, ydt):
+    rows = 3
+    x = rand(rows, c, seed=1, dtype=xdt)
+    r = rand(rows, c, seed=2, dtype=rdt) if rdt else None
+    gamma = 1 + 0.3 * rand(c, seed=3)
+    total, y = out_like(rows, c, rdt or xdt), out_like(rows, c, ydt)
+    scale = out_like(rows, 1, F32)[:, 0] if ydt == F8 else None
+    api.RmsNormForward(handle, x, y, residual=r, total=total)(x, gamma, y, residual=r, total=total, scale=scale)
+    t, want = ref.norm(f64(x), f64(r), f64(gamma), 1e-6)
+    close(total, t, ref.stored(t, rdt or xdt) + ref.U32 * t.abs(), "total")
+    if ydt == F8:
+        close_e4m3(y, scale, want, ref.norm_rel(c), "y")
+    else:
+        close(y, want, ref.norm_rel(c) * want.abs() + ref.stored(want, ydt), "y")
+
+
+@pytest.mark.parametrize("c", LONG)
+@pytest.mark.parametrize("dydt,tdt,dtdt", [(F32, F32, F32), (F32, F32, None), (BF, BF, BF), (BF, F32, F32)])
+def test_norm_backward_of_long_rows(handle, c, dydt, tdt, dtdt):
+    rows = 3
+    dy, t = rand(rows, c, seed=1, dtype=dydt), rand(rows, c, seed=2, std=2.0, dtype=tdt)
+    dt = rand(rows, c, seed=3, dtype=dtdt) if dtdt else None
+    gamma, dgamma = 1 + 0.3 * rand(c, seed=4), out_like(c, 1, F32)[:, 0]
+    dx = out_like(rows, c, tdt)
+    api.RmsNormBackward(handle, dy, t, dx, dtotal=dt)(dy, t, gamma, dx, dgamma=dgamma, dtotal=dt)
+    want, wg, bx, bg = ref.norm_backward(f64(dy), f64(t), f64(gamma), f64(dt), 1e-6)
+    close(dx, want, 4 * ref.norm_rel(c) * bx + ref.stored(want, tdt), "dx")
+    close(dgamma, wg, (ref.norm_rel(c) + ref.U32 * (rows + 64)) * bg, "dgamma")
