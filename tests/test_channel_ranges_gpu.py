@@ -101,3 +101,45 @@ def test_norm_backward_of_long_rows(handle, c, dydt, tdt, dtdt):
     want, wg, bx, bg = ref.norm_backward(f64(dy), f64(t), f64(gamma), f64(dt), 1e-6)
     close(dx, want, 4 * ref.norm_rel(c) * bx + ref.stored(want, tdt), "dx")
     close(dgamma, wg, (ref.norm_rel(c) + ref.U32 * (rows + 64)) * bg, "dgamma")
+
+
+def act_rel(v, kind):
+    """Relative error of an activation in FP32, from its steps (U = 2^-24 each rounding):
+
+    gelu: Phi by a quotient fitted to 2e-7, evaluated in some ten roundings (their
+    sum at most four times the result's size): 40 U + 2e-7 < 4e-6; the exponent
+    v^2/2, of three roundings, makes 3 U v^2/2 < 1e-7 v^2 of its exponential.
+    silu, sigmoid: exponent v with two roundings, exponential 4 U, sum, reciprocal
+    2 U and product: < 1e-6 + 2e-7 |v|."""
+    return 4e-6 + 1e-7 * v * v if kind == "gelu" else 1e-6 + 2e-7 * v.abs()
+
+
+# 1, 8 and 200 rows: a kernel each
+@pytest.mark.parametrize("rows", [1, 8, 200])
+@pytest.mark.parametrize("kind,lowest,step", [("gelu", -12.9375, 0.0625), ("silu", -79.5, 0.5), ("sigmoid", -79.5, 0.5)])
+def test_activations_by_their_relative_error(handle, rows, kind, lowest, step):
+    """Down to where FP32's normal range ends, which BF16 and FP32 outputs have."""
+    v = torch.arange(lowest, -lowest, step, dtype=torch.float64)  # BF16 holds them exactly
+    v = v[v != 0]
+    assert torch.equal(v.to(BF).double(), v)
+    n = v.numel()
+    x, w = torch.ones(rows, 1, dtype=BF, device="cuda"), v.to(BF).cuda().view(-1, 1).contiguous()
+    y, z = out_like(rows, n, F32), out_like(rows, n, F32)
+    api.LinearForward(handle, x, w, y, act=kind, z=z)(x, w, y, z=z)
+    assert torch.equal(f64(z), v.expand(rows, n))
+    f, df = ref.act(v, kind)
+    rel = act_rel(v, kind)
+    close(y, f.expand(rows, n), (rel * f.abs()).expand(rows, n), kind)
+    dy, db = torch.zeros(rows, n, device="cuda"), out_like(n, 1, F32)[:, 0]
+    dy[rows - 1] = 1
+    api.LinearBackward(handle, x, w, dy, z=z, act=kind)(x, w, dy, dbias=db, z=z)
+    # the slope's terms: gelu Phi + v phi, silu p + v p (1 - p), sigmoid p (1 - p) from 1 - p of its own rounding
+    if kind == "gelu":
+        p = 0.5 * torch.erfc(-v / 2 ** 0.5)
+        terms = p + (df - p).abs()
+    elif kind == "silu":
+        p = torch.sigmoid(v)
+        terms = p * (1 + v.abs())
+    else:
+        terms = torch.sigmoid(v)
+    close(db, df, rel * terms, kind + " slope")
