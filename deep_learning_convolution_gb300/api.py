@@ -361,6 +361,7 @@ class _ChannelOp:
         self.axes = axes
         self._tensors, self._filters = [], []
         self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
+        self._ws_stream = None
 
     def _act_desc(self, t):
         """Descriptor of an activation tensor (None for an absent one)."""
@@ -390,11 +391,26 @@ class _ChannelOp:
         return d
 
     def _set_workspace(self, nbytes: int, device):
+        """Memory of the handle's stream, not of torch's current one, whose kernels
+        might still write what it released last."""
         import torch
         self._ws_bytes = nbytes
+        self._ws_stream = self.handle.stream
         if nbytes:
-            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            with torch.cuda.stream(torch.cuda.ExternalStream(self._ws_stream, device=device)):
+                self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
             self._ws_ptr = self.workspace.data_ptr()
+
+    def _scratch(self) -> int:
+        """The workspace's pointer for a call; a stream it comes to keeps it from being
+        handed out before the kernels there are done."""
+        if self._ws_stream != self.handle.stream:
+            self._ws_stream = self.handle.stream
+            if self.workspace is not None:
+                import torch
+                self.workspace.record_stream(
+                    torch.cuda.ExternalStream(self._ws_stream, device=self.workspace.device))
+        return self._ws_ptr
 
     def _vector(self, t, n: int, what: str) -> int:
         """Pointer of an optional dense FP32 vector of n elements."""
@@ -417,12 +433,7 @@ class _ChannelOp:
         for d in self._filters:
             B.dlcDestroyFilterDescriptor(d)
         self._tensors, self._filters = [], []
-        if self.workspace is not None:
-            # kernels on the handle's stream may still use it: not to be handed out before
-            # they are done
-            import torch
-            self.workspace.record_stream(torch.cuda.ExternalStream(self.handle.stream))
-            self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
+        self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
 
     def __del__(self):
         try:
@@ -472,7 +483,7 @@ class RmsNormBackward(_ChannelOp):
                              total.data_ptr(), self._vector(gamma, self.channels, "gamma"),
                              self.dt_desc, self._given(dtotal, self.dt_desc, "dtotal"), self.dx_desc,
                              dx.data_ptr(), self._vector(dgamma, self.channels, "dgamma"),
-                             self._ws_ptr, self._ws_bytes)
+                             self._scratch(), self._ws_bytes)
         return dx
 
 
@@ -512,7 +523,7 @@ class LinearForward(_Product):
                            self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
                            self._given(z, self.z_desc, "z"), self.r_desc,
                            self._given(residual, self.r_desc, "residual"), self.y_desc, y.data_ptr(),
-                           self._ws_ptr, self._ws_bytes)
+                           self._scratch(), self._ws_bytes)
         return y
 
 
@@ -530,7 +541,7 @@ class GatedForward(_Product):
                           self._vector(x_scale, self.rows, "x_scale"), self.w_desc, w.data_ptr(),
                           self._vector(w_scale, self.filters, "w_scale"),
                           self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
-                          self._given(z, self.z_desc, "z"), self.y_desc, y.data_ptr(), self._ws_ptr,
+                          self._given(z, self.z_desc, "z"), self.y_desc, y.data_ptr(), self._scratch(),
                           self._ws_bytes)
         return y
 
@@ -553,7 +564,7 @@ class _ProductBackward(_ChannelOp):
                        self.z_desc, self._given(z, self.z_desc, "z"), self.dy_desc, dy.data_ptr(),
                        self.dx_desc, self._given(dx, self.dx_desc, "dx"), self.dw_desc,
                        self._given(dw, self.dw_desc, "dw"),
-                       self._vector(dbias, self.filters, "dbias"), self._ws_ptr, self._ws_bytes)
+                       self._vector(dbias, self.filters, "dbias"), self._scratch(), self._ws_bytes)
         return dx, dw, dbias
 
 
