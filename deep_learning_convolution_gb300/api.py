@@ -344,51 +344,95 @@ def _ptr(t) -> int:
     return t.data_ptr() if t is not None else 0
 
 
+_ABSENT = (None, None, None, None)  # the example of a tensor that an operator was built without
+
+
 class _ChannelOp:
     """Descriptors and workspace of one channel operator, built once from
     example tensors for repeated calls on the same shapes, strides, types and
     16-byte alignment.  Activations are [rows, channels] matrices or 4-D
     tensors with ``axes`` ("NHWC" or "NCHW"); weights are [K, C] matrices or
-    4-D filters with R = S = 1.  Calls check what each pointer may be (vectors
-    are dense FP32), launch on the handle's stream and return no copies.  An
-    operator has one workspace: calls on several streams need an operator each,
-    or an order between them; a captured graph needs its operator alive."""
+    4-D filters with R = S = 1.  A call checks its tensors against the examples
+    (shape, strides, type, device; ValueError) and vectors for dense FP32, launches
+    on the handle's stream and returns no copies.  An operator has one workspace:
+    calls on several streams need an operator each, or an order between them; a
+    captured graph needs its operator alive."""
+
+    _name = None  # of the C function
 
     def __init__(self, handle: Handle, axes: str):
         import torch
+        self._fn = B.function(self._name)
         self._f32 = torch.float32
         self.handle = handle
         self.axes = axes
+        self.device = None  # the examples' GPU
         self._tensors, self._filters = [], []
         self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
         self._ws_stream = None
 
-    def _act_desc(self, t):
-        """Descriptor of an activation tensor (None for an absent one)."""
-        if t is None:
-            return None
+    def _rows(self, t):
+        """(sizes, strides) of an activation tensor as n, c, h, w."""
         if t.dim() == 2:
             (rows, c), (rs, cs) = t.shape, t.stride()
-            sizes, strides = (rows, c, 1, 1), (rs, cs, 0, 0)
-        else:
-            sizes, strides = _logical(t, self.axes, "NCHW")
+            return (rows, c, 1, 1), (rs, cs, 0, 0)
+        return _logical(t, self.axes, "NCHW")
+
+    def _example(self, t):
+        """What _at compares a call's tensor with."""
+        if not t.is_cuda or (self.device is not None and t.get_device() != self.device):
+            raise ValueError("the tensors of an operator are on one GPU")
+        self.device = t.get_device()
+        return t.shape, None if t.is_contiguous() else t.stride(), t.dtype
+
+    def _act_desc(self, t):
+        """Descriptor and example of an activation tensor (None and _ABSENT for none)."""
+        if t is None:
+            return None, _ABSENT
+        sizes, strides = self._rows(t)
+        example = self._example(t) + ([(n, n > 1 and s) for n, s in zip(sizes, strides)],)
         d = B.dlcCreateTensorDescriptor()
         self._tensors.append(d)
         B.dlcSetTensor4dDescriptorEx(d, _dtype_code(t), *sizes, *strides)
-        return d
+        return d, example
 
     def _weight_desc(self, t):
+        """The same of a filter tensor."""
         if t is None:
-            return None
+            return None, _ABSENT
         if not t.is_contiguous():
             raise ValueError("filter tensors must be dense (contiguous)")
         if t.dim() not in (2, 4) or (t.dim() == 4 and t.numel() != t.shape[0] * max(t.shape[1:])):
             raise ValueError("weights are [K, C] or filters with R = S = 1")
+        example = self._example(t) + (None,)
         d = B.dlcCreateFilterDescriptor()
         self._filters.append(d)
         B.dlcSetFilter4dDescriptor(d, _dtype_code(t), B.DLC_TENSOR_NCHW, t.shape[0],
                                    t.numel() // t.shape[0], 1, 1)
-        return d
+        return d, example
+
+    def _at(self, t, example, what: str) -> int:
+        """Pointer of a call's tensor, laid out like its example."""
+        shape, strides, dtype, _ = example
+        if (t.shape != shape or t.dtype is not dtype or t.get_device() != self.device
+                or not (t.is_contiguous() if strides is None else t.stride() == strides)):
+            self._same_elements(t, example, what)
+        return t.data_ptr()
+
+    def _same_elements(self, t, example, what: str):
+        """ValueError unless t's descriptor would be that of its example (other dimensions,
+        or strides of dimensions of one element)."""
+        shape, strides, dtype, rows = example
+        if example is _ABSENT:
+            raise ValueError(f"{what} was not among the example tensors")
+        same = t.dtype is dtype and t.get_device() == self.device
+        if same and rows is None:
+            same = t.is_contiguous() and t.shape[:1] == shape[:1] and t.numel() == shape.numel()
+        elif same:
+            same = t.dim() in (2, 4) and [(n, n > 1 and s) for n, s in zip(*self._rows(t))] == rows
+        if not same:
+            raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}, "
+                             f"its example {tuple(shape)} {dtype} with strides {strides or 'of a dense one'}")
 
     def _set_workspace(self, nbytes: int, device):
         """Memory of the handle's stream, not of torch's current one, whose kernels
@@ -413,19 +457,10 @@ class _ChannelOp:
         return self._ws_ptr
 
     def _vector(self, t, n: int, what: str) -> int:
-        """Pointer of an optional dense FP32 vector of n elements."""
-        if t is None:
-            return 0
-        if t.dtype is not self._f32 or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{what} must be a dense float32 vector of {n} elements")
+        """Pointer of a dense FP32 vector of n elements."""
+        if t.dtype is not self._f32 or t.numel() != n or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"{what} must be a dense float32 vector of {n} elements on GPU {self.device}")
         return t.data_ptr()
-
-    @staticmethod
-    def _given(t, desc, what: str) -> int:
-        """Pointer of a tensor whose descriptor was (or was not) set up."""
-        if t is not None and desc is None:
-            raise ValueError(f"{what} was not among the example tensors")
-        return t.data_ptr() if t is not None else 0
 
     def close(self):
         for d in self._tensors:
@@ -445,22 +480,28 @@ class _ChannelOp:
 class RmsNormForward(_ChannelOp):
     """total = x + residual; y = gamma * total / rms(total) through
     dlcRmsNormForward; an E4M3 y comes with one scale per row."""
+    _name = "dlcRmsNormForward"
 
     def __init__(self, handle: Handle, x, y, *, residual=None, total=None, eps: float = 1e-6,
                  axes: str = "NHWC"):
         super().__init__(handle, axes)
         self.eps = float(eps)
-        self.x_desc, self.y_desc = self._act_desc(x), self._act_desc(y)
-        self.r_desc, self.t_desc = self._act_desc(residual), self._act_desc(total)
+        self.x_desc, self._x = self._act_desc(x)
+        self.y_desc, self._y = self._act_desc(y)
+        self.r_desc, self._r = self._act_desc(residual)
+        self.t_desc, self._t = self._act_desc(total)
         self.channels = B.dlcGetTensor4dDescriptor(self.x_desc)[2]
         self.rows = x.numel() // self.channels
 
     def __call__(self, x, gamma, y, residual=None, total=None, scale=None):
-        B.dlcRmsNormForward(self.handle.h, self.eps, self.x_desc, x.data_ptr(), self.r_desc,
-                            self._given(residual, self.r_desc, "residual"),
-                            self._vector(gamma, self.channels, "gamma"), self.t_desc,
-                            self._given(total, self.t_desc, "total"), self.y_desc, y.data_ptr(),
-                            self._vector(scale, self.rows, "scale"))
+        status = self._fn(self.handle.h, self.eps, self.x_desc, self._at(x, self._x, "x"),
+                          self.r_desc, residual if residual is None else
+                          self._at(residual, self._r, "residual"), self._vector(gamma, self.channels, "gamma"),
+                          self.t_desc, total if total is None else self._at(total, self._t, "total"),
+                          self.y_desc, self._at(y, self._y, "y"),
+                          scale if scale is None else self._vector(scale, self.rows, "scale"))
+        if status:
+            B.check(self._name, status)
         return y
 
 
@@ -468,33 +509,43 @@ class RmsNormBackward(_ChannelOp):
     """dx (the gradient of x and of the residual) and dgamma of RmsNormForward
     through dlcRmsNormBackward; dtotal is the gradient that reaches the sum by
     other ways."""
+    _name = "dlcRmsNormBackward"
 
     def __init__(self, handle: Handle, dy, total, dx, *, dtotal=None, eps: float = 1e-6,
                  axes: str = "NHWC"):
         super().__init__(handle, axes)
         self.eps = float(eps)
-        self.dy_desc, self.t_desc = self._act_desc(dy), self._act_desc(total)
-        self.dx_desc, self.dt_desc = self._act_desc(dx), self._act_desc(dtotal)
+        self.dy_desc, self._dy = self._act_desc(dy)
+        self.t_desc, self._t = self._act_desc(total)
+        self.dx_desc, self._dx = self._act_desc(dx)
+        self.dt_desc, self._dt = self._act_desc(dtotal)
         self.channels = B.dlcGetTensor4dDescriptor(self.t_desc)[2]
         self._set_workspace(B.dlcGetRmsNormBackwardWorkspaceSize(handle.h, self.t_desc), total.device)
 
     def __call__(self, dy, total, gamma, dx, dgamma=None, dtotal=None):
-        B.dlcRmsNormBackward(self.handle.h, self.eps, self.dy_desc, dy.data_ptr(), self.t_desc,
-                             total.data_ptr(), self._vector(gamma, self.channels, "gamma"),
-                             self.dt_desc, self._given(dtotal, self.dt_desc, "dtotal"), self.dx_desc,
-                             dx.data_ptr(), self._vector(dgamma, self.channels, "dgamma"),
-                             self._scratch(), self._ws_bytes)
+        status = self._fn(self.handle.h, self.eps, self.dy_desc, self._at(dy, self._dy, "dy"),
+                          self.t_desc, self._at(total, self._t, "total"),
+                          self._vector(gamma, self.channels, "gamma"),
+                          self.dt_desc, dtotal if dtotal is None else self._at(dtotal, self._dt, "dtotal"),
+                          self.dx_desc, self._at(dx, self._dx, "dx"),
+                          dgamma if dgamma is None else self._vector(dgamma, self.channels, "dgamma"),
+                          self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
         return dx
 
 
 class _Product(_ChannelOp):
-    _forward = _workspace = _kernel_of = None
+    _workspace = _kernel_of = None
 
     def __init__(self, handle, x, w, y, act, residual, z, axes):
         super().__init__(handle, axes)
         self.act = LINEAR_ACT_MODES[act]
-        self.x_desc, self.w_desc, self.y_desc = self._act_desc(x), self._weight_desc(w), self._act_desc(y)
-        self.r_desc, self.z_desc = self._act_desc(residual), self._act_desc(z)
+        self.x_desc, self._x = self._act_desc(x)
+        self.w_desc, self._w = self._weight_desc(w)
+        self.y_desc, self._y = self._act_desc(y)
+        self.r_desc, self._r = self._act_desc(residual)
+        self.z_desc, self._z = self._act_desc(z)
         self.filters = w.shape[0]
         self.rows = x.numel() // (w.numel() // w.shape[0])
         self._set_workspace(self._workspace(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
@@ -509,6 +560,7 @@ class LinearForward(_Product):
     """y = act(x w^T + bias) + residual through dlcLinearForward, w being
     [K, C]; E4M3 x and w take one scale per row and per filter.  z, where
     given, receives the activation's argument for LinearBackward."""
+    _name = "dlcLinearForward"
     _workspace = staticmethod(B.dlcGetLinearForwardWorkspaceSize)
     _kernel_of = staticmethod(B.dlcGetLinearForwardKernel)
 
@@ -517,19 +569,24 @@ class LinearForward(_Product):
         super().__init__(handle, x, w, y, act, residual, z, axes)
 
     def __call__(self, x, w, y, bias=None, residual=None, z=None, x_scale=None, w_scale=None):
-        B.dlcLinearForward(self.handle.h, self.x_desc, x.data_ptr(),
-                           self._vector(x_scale, self.rows, "x_scale"), self.w_desc, w.data_ptr(),
-                           self._vector(w_scale, self.filters, "w_scale"),
-                           self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
-                           self._given(z, self.z_desc, "z"), self.r_desc,
-                           self._given(residual, self.r_desc, "residual"), self.y_desc, y.data_ptr(),
-                           self._scratch(), self._ws_bytes)
+        status = self._fn(self.handle.h, self.x_desc, self._at(x, self._x, "x"),
+                          x_scale if x_scale is None else self._vector(x_scale, self.rows, "x_scale"),
+                          self.w_desc, self._at(w, self._w, "w"),
+                          w_scale if w_scale is None else self._vector(w_scale, self.filters, "w_scale"),
+                          bias if bias is None else self._vector(bias, self.filters, "bias"), self.act,
+                          self.z_desc, z if z is None else self._at(z, self._z, "z"),
+                          self.r_desc, residual if residual is None else
+                          self._at(residual, self._r, "residual"),
+                          self.y_desc, self._at(y, self._y, "y"), self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
         return y
 
 
 class GatedForward(_Product):
     """y = act(gate) * up through dlcGatedForward: w is [2F, C], F gate filters
     and then F up filters, z = [gate, up] = x w^T + bias."""
+    _name = "dlcGatedForward"
     _workspace = staticmethod(B.dlcGetGatedForwardWorkspaceSize)
     _kernel_of = staticmethod(B.dlcGetGatedForwardKernel)
 
@@ -537,34 +594,46 @@ class GatedForward(_Product):
         super().__init__(handle, x, w, y, act, None, z, axes)
 
     def __call__(self, x, w, y, bias=None, z=None, x_scale=None, w_scale=None):
-        B.dlcGatedForward(self.handle.h, self.x_desc, x.data_ptr(),
-                          self._vector(x_scale, self.rows, "x_scale"), self.w_desc, w.data_ptr(),
-                          self._vector(w_scale, self.filters, "w_scale"),
-                          self._vector(bias, self.filters, "bias"), self.act, self.z_desc,
-                          self._given(z, self.z_desc, "z"), self.y_desc, y.data_ptr(), self._scratch(),
-                          self._ws_bytes)
+        status = self._fn(self.handle.h, self.x_desc, self._at(x, self._x, "x"),
+                          x_scale if x_scale is None else self._vector(x_scale, self.rows, "x_scale"),
+                          self.w_desc, self._at(w, self._w, "w"),
+                          w_scale if w_scale is None else self._vector(w_scale, self.filters, "w_scale"),
+                          bias if bias is None else self._vector(bias, self.filters, "bias"), self.act,
+                          self.z_desc, z if z is None else self._at(z, self._z, "z"),
+                          self.y_desc, self._at(y, self._y, "y"), self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
         return y
 
 
 class _ProductBackward(_ChannelOp):
-    _backward = _workspace = None
+    _workspace = None
 
     def __init__(self, handle, x, w, dy, dx, dw, z, act, axes):
         super().__init__(handle, axes)
         self.act = LINEAR_ACT_MODES[act]
-        self.x_desc, self.w_desc, self.dy_desc = self._act_desc(x), self._weight_desc(w), self._act_desc(dy)
-        self.dx_desc, self.dw_desc, self.z_desc = self._act_desc(dx), self._weight_desc(dw), self._act_desc(z)
+        self.x_desc, self._x = self._act_desc(x)
+        self.w_desc, self._w = self._weight_desc(w)
+        self.dy_desc, self._dy = self._act_desc(dy)
+        self.dx_desc, self._dx = self._act_desc(dx)
+        self.dw_desc, self._dw = self._weight_desc(dw)
+        self.z_desc, self._z = self._act_desc(z)
         self.filters = w.shape[0]
         self._set_workspace(self._workspace(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
                                             w.data_ptr(), self.act, self.z_desc, self.dy_desc,
                                             dy.data_ptr()), x.device)
 
     def __call__(self, x, w, dy, dx=None, dw=None, dbias=None, z=None):
-        self._backward(self.handle.h, self.x_desc, x.data_ptr(), self.w_desc, w.data_ptr(), self.act,
-                       self.z_desc, self._given(z, self.z_desc, "z"), self.dy_desc, dy.data_ptr(),
-                       self.dx_desc, self._given(dx, self.dx_desc, "dx"), self.dw_desc,
-                       self._given(dw, self.dw_desc, "dw"),
-                       self._vector(dbias, self.filters, "dbias"), self._scratch(), self._ws_bytes)
+        status = self._fn(self.handle.h, self.x_desc, self._at(x, self._x, "x"), self.w_desc,
+                          self._at(w, self._w, "w"), self.act,
+                          self.z_desc, z if z is None else self._at(z, self._z, "z"),
+                          self.dy_desc, self._at(dy, self._dy, "dy"),
+                          self.dx_desc, dx if dx is None else self._at(dx, self._dx, "dx"),
+                          self.dw_desc, dw if dw is None else self._at(dw, self._dw, "dw"),
+                          dbias if dbias is None else self._vector(dbias, self.filters, "dbias"),
+                          self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
         return dx, dw, dbias
 
 
@@ -572,7 +641,7 @@ class LinearBackward(_ProductBackward):
     """dx, dw and dbias of LinearForward through dlcLinearBackward, each where
     its tensor is given; z is what the forward call wrote (not needed for the
     identity).  The residual's gradient is dy."""
-    _backward = staticmethod(B.dlcLinearBackward)
+    _name = "dlcLinearBackward"
     _workspace = staticmethod(B.dlcGetLinearBackwardWorkspaceSize)
 
     def __init__(self, handle: Handle, x, w, dy, dx=None, dw=None, *, z=None, act: str = "identity",
@@ -582,7 +651,7 @@ class LinearBackward(_ProductBackward):
 
 class GatedBackward(_ProductBackward):
     """dx, dw and dbias of GatedForward through dlcGatedBackward."""
-    _backward = staticmethod(B.dlcGatedBackward)
+    _name = "dlcGatedBackward"
     _workspace = staticmethod(B.dlcGetGatedBackwardWorkspaceSize)
 
     def __init__(self, handle: Handle, x, w, dy, dx=None, dw=None, *, z=None, act: str = "silu",

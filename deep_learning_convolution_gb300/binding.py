@@ -202,7 +202,7 @@ def error_string(status: int) -> str:
         return f"status {status}"
 
 
-def _check(name: str, status: int):
+def check(name: str, status: int):
     if status != DLC_STATUS_SUCCESS:
         raise DlcError(name, status)
 
@@ -210,7 +210,13 @@ def _check(name: str, status: int):
 def _call(name, *args):
     status = getattr(_lib or load_library(), name)(*args)
     if status:
-        _check(name, status)
+        check(name, status)
+
+
+def function(name):
+    """The C function `name`, for repeated calls: device pointers and descriptors as in
+    SIGNATURES, None where absent; the caller looks at the status (check)."""
+    return getattr(load_library(), name)
 
 
 # ---------------------------------------------------------------------------

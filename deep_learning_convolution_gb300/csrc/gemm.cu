@@ -888,7 +888,7 @@ struct GemmPlan {
 };
 
 GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
-    GemmPlan p;
+    GemmPlan p = {};
     const int nb = g.gated ? 2 * g.N : g.N;
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
     const int bk = e4m3 ? GP_LINE : GP_LINE / 2;
@@ -897,8 +897,9 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.b_rows = g.b.trans ? g.K : nb;
     p.b_ch = (int)(g.b.trans ? nb : g.K);
     p.gemv = dlc_gemv_ok(g);
-    p.pack_a = !p.gemv && !tma_rows(g.a.t, p.a_rows, p.a_ch);
-    p.pack_b = !p.gemv && !tma_rows(g.b.t, p.b_rows, p.b_ch);
+    if (p.gemv) return p;  // operands as they are, one launch
+    p.pack_a = !tma_rows(g.a.t, p.a_rows, p.a_ch);
+    p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
     p.num_kb = (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     // Tile width, split of the tail, and which of the two kernels, from a model of
@@ -953,7 +954,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.b_off = off;
     if (p.pack_b) off += dlc_pack_bytes(g.b.t, p.b_rows, p.b_ch);
     p.part_off = off;
-    if (!p.few_rows && !p.gemv) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
+    if (!p.few_rows) off += round256((size_t)tail * p.splits * 2 * GP_ROWS * p.bn * 4);
     p.bytes = off;
     return p;
 }
