@@ -468,6 +468,8 @@ class _ChannelOp:
         for d in self._filters:
             B.dlcDestroyFilterDescriptor(d)
         self._tensors, self._filters = [], []
+        for name in [n for n in vars(self) if n.endswith("_desc")]:
+            setattr(self, name, None)  # a call after this is refused by the library
         self.workspace, self._ws_ptr, self._ws_bytes = None, 0, 0
 
     def __del__(self):

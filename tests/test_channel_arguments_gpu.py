@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from deep_learning_convolution_gb300 import api
+from deep_learning_convolution_gb300 import binding as B
 from tests.test_channel_ops_gpu import BF, F32, rand
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,18 @@ def test_the_same_elements_in_other_dimensions_are_taken(handle):
     y.zero_()
     over(image, w, y.view(2, 3, 1, 32))
     assert torch.equal(y, want)
+
+
+def test_a_closed_operator_is_refused(handle):
+    for op, right in calls(handle):
+        op(**right)
+        op.close()
+        before = handle.launches()
+        with pytest.raises(B.DlcError) as e:
+            op(**right)
+        assert e.value.status in (B.DLC_STATUS_BAD_PARAM, B.DLC_STATUS_NOT_INITIALIZED)
+        if hasattr(op, "kernel"):
+            with pytest.raises(B.DlcError):
+                op.kernel()
+        assert handle.launches() == before
+        op.close()
