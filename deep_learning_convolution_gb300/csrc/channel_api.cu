@@ -4,6 +4,7 @@
 // pass into its products, and workspace layout; the kernels are in rmsnorm.cu,
 // act_grad.cu, gemm.cu, gemm_rows.cu and gemv.cu.
 #include <atomic>
+#include <climits>
 #include <cstring>
 #include <initializer_list>
 
@@ -88,7 +89,8 @@ RowTensor row_tensor(const dlcTensorStruct *d, const void *p) {
     m.cs = d->c > 1 ? d->stride[1] : 1;
     m.s2 = d->stride[2];
     m.s3 = d->stride[3];
-    m.hw = d->h * d->w;
+    const long long hw = (long long)d->h * d->w;
+    m.hw = (int)std::min(hw, (long long)INT_MAX);
     m.w = d->w;
     // one pitch for all rows, from the innermost axis longer than one
     const long long ext[3] = {d->w, d->h, d->n}, str[3] = {m.s3, m.s2, m.s0};
@@ -102,6 +104,13 @@ RowTensor row_tensor(const dlcTensorStruct *d, const void *p) {
         else if (str[i] != span * m.ld)
             m.uniform = 0;
         span *= ext[i];
+    }
+    // Images of 2^31 pixels and more (a norm takes them) without one pitch: a group of w
+    // rows for each (n, h), if those are evenly spaced; hw = 0 where they are not.
+    if (!m.uniform && hw > INT_MAX) {
+        m.hw = d->n == 1 || m.s0 == d->h * m.s2 ? d->w : 0;
+        m.s0 = m.s2;
+        m.s2 = 0;
     }
     if (span == 1) m.ld = ((long long)d->c + 15) / 16 * 16;  // a single row: any pitch
     return t;
@@ -470,6 +479,7 @@ dlcStatus_t dlcRmsNormForward(dlcHandle_t h, double epsilon, dlcTensorDescriptor
     if (residual) p.r = row_tensor(rd, residual);
     if (total) p.t = row_tensor(td, total);
     p.y = row_tensor(yd, y);
+    if (!p.x.m.hw || !p.r.m.hw || !p.t.m.hw || !p.y.m.hw) return DLC_STATUS_NOT_SUPPORTED;
     p.gamma = gamma;
     p.scale = scale;
     RETURN_IF(enter(h));
@@ -519,6 +529,7 @@ dlcStatus_t dlcRmsNormBackward(dlcHandle_t h, double epsilon, dlcTensorDescripto
     p.t = row_tensor(td, total);
     if (dtotal) p.dt = row_tensor(dtd, dtotal);
     p.dx = row_tensor(dxd, dx);
+    if (!p.dy.m.hw || !p.t.m.hw || !p.dt.m.hw || !p.dx.m.hw) return DLC_STATUS_NOT_SUPPORTED;
     p.gamma = gamma;
     p.dgamma = dgamma;
     const size_t need = dgamma ? ws_round(dlc_rms_bwd_workspace(h, p)) : 0;

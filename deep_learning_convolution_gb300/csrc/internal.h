@@ -223,7 +223,7 @@ dlcStatus_t dlc_launch_rowstack(dlcContext *ctx, const ConvProblem &pb);
 struct RowMap {
     long long s0, s2, s3, cs;  // strides of n, h, w and of the channel (elements)
     long long ld;              // the rows' pitch when it is one number (uniform)
-    int hw, w;                 // h * w and w
+    int hw, w;                 // h * w and w (hw 0: rows that this cannot describe)
     int uniform;
 };
 

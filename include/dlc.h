@@ -521,7 +521,8 @@ dlcStatus_t dlcActivationForward(dlcHandle_t handle, dlcActivationMode_t mode, d
  * fast layout.  Filters are [K, C, 1, 1], K rows of C channels.  Sums,
  * statistics and activations run in FP32; BFLOAT16 and FLOAT8_E4M3 results are
  * rounded once, to nearest even.  An FP8 row or filter stands for its values
- * times its FLOAT scale.
+ * times its FLOAT scale.  Products take up to 2^31 - 1 rows, norms more; several
+ * images of 2^31 pixels and more each have to be one pitch apart (NOT_SUPPORTED).
  *
  * Pointers are device pointers; those marked optional may be NULL, and their
  * descriptor is then ignored.  Outputs must not overlap other arguments
