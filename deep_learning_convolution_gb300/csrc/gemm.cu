@@ -668,14 +668,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     } else if (warp == 2) {
         if (elect_one()) gp_produce<false, B_MN, GATED, BK>(p, rank, &tmB, sB, full, empty, ctl);
     } else if (warp == 1) {
-        const bool one = elect_one();
-        if (one && rank == 0)
+        if (elect_one() && rank == 0)
             gp_mma<E4M3, A_MN, B_MN>(p, tmem_base, sA, sB, full, empty, tfull, tempty, mma_done, ctl);
-        if (one) {  // the leader's final commit reaches both CTAs
-            volatile int dummy = 0;
-            const WaitCtl fin{&dummy, p.err, p.timeout_ns};
-            mbar_wait(mma_done, 0u, fin, 93);
-        }
     } else {
         // (the activation's branch out here: a block's code is straight)
         act_dispatch(p.act, [&](auto act) {
@@ -685,6 +679,16 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
+    // The leader's final commit reaches both CTAs.  Waited for here, when the tiles are
+    // done: from the start of the kernel a long product would outlast a wait's limit.
+    if (warp == 1) {
+        if (elect_one()) {
+            volatile int dummy = 0;
+            const WaitCtl fin{&dummy, p.err, p.timeout_ns};
+            mbar_wait(mma_done, 0u, fin, 93);
+        }
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA leaves while the pair's MMAs or loads may touch it
     tc_fence_after_sync();
     if (warp == 1) tmem_dealloc_pair(tmem_base, p.tmem_cols);
