@@ -67,6 +67,27 @@ bool dlc_allow_smem(const dlcContext *ctx, const void *kernel, size_t bytes) {
     return ok;
 }
 
+int dlc_resident_clusters(const dlcContext *ctx, int *known, const void *kernel, int size, int threads, size_t smem) {
+    if (*known > 0) return *known;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(ctx->sm_count / size * size));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (!dlc_allow_smem(ctx, kernel, smem) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, ctx->sm_count / size);  // kept as well: the plans of a handle agree
+    }
+    return *known = n;
+}
+
 namespace {
 
 constexpr size_t WS_ALIGN = 256;

@@ -36,7 +36,6 @@
 // whatever its width.  Tried and slower: the epilogue's stores straight from
 // registers, 64-column stores, two chunks at a time, bias and scales prefetched into
 // registers (spills).
-#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -1031,29 +1030,10 @@ const void *pair_kernel(bool e4m3, bool a_mn, bool b_mn, bool gated) {
                 : (const void *)gemm_pair_kernel<false, false, false, false, ROWS>;
 }
 
-// Pairs that the device holds at once (each CTA takes an SM's shared memory);
-// a property of the device, asked once.
-int resident_pairs(const dlcContext *ctx, const void *kern, size_t smem) {
-    static std::atomic<int> known{0};
-    int n = known.load();
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(ctx->sm_count / 2 * 2));
-    cfg.blockDim = dim3(GP_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return std::max(1, ctx->sm_count / 2);
-    }
-    known.store(n);
-    return n;
+// Pairs that the device holds at once (each CTA takes an SM's shared memory).
+int resident_pairs(dlcContext *ctx) {
+    return dlc_resident_clusters(ctx, &ctx->resident_pairs, (const void *)gemm_pair_kernel<false, false, false, false, false>, 2,
+                                 GP_THREADS, GP_MAX_SMEM);
 }
 
 GpTiles tiles_of(const GemmPlan &pl) {
@@ -1133,7 +1113,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     const bool a_mn = g.a.trans != 0, b_mn = g.b.trans != 0, gated = g.gated != 0;
     const void *kern = rows ? pair_kernel<true>(e4m3, a_mn, b_mn, gated) : pair_kernel<false>(e4m3, a_mn, b_mn, gated);
     if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
-    const int clusters = std::min(resident_pairs(ctx, kern, smem), p.units);
+    const int clusters = std::min(resident_pairs(ctx), p.units);
     void *args[] = {&p, &ta, &tb, &ty, &tz, &tp};
     dlcStatus_t st = dlc_launch(ctx, kern, dim3((unsigned)(2 * clusters)), dim3(GP_THREADS), smem, args, 2);
     if (st != DLC_STATUS_SUCCESS || !tail) return st;

@@ -23,7 +23,6 @@
 // Roles (16 warps): a thread of warp 0 loads, one of warp 1 issues the MMAs; all warps
 // read the accumulators (four per quarter of the TMEM lanes) and join the partial
 // sums, a thread four filters.  Every wait is bounded.
-#include <atomic>
 #include <cstring>
 
 #include "channel.cuh"
@@ -272,32 +271,11 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// Clusters of `size` CTAs (an SM each) that the device holds at once; a property
-// of the device, asked once.
+// Clusters of `size` CTAs (an SM each) that the device holds at once.
 int resident_clusters(const dlcContext *ctx, int size) {
-    static std::atomic<int> known[FR_MAX_SPLITS + 1];
-    int n = known[size].load();
-    if (n > 0) return n;
-    const void *kern = (const void *)gemm_rows_kernel<false, false>;
-    const int smem = FR_SMEM;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)size;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(ctx->sm_count / size * size));
-    cfg.blockDim = dim3(FR_THREADS);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (!dlc_allow_smem(ctx, kern, (size_t)smem) ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return std::max(1, ctx->sm_count / size);
-    }
-    known[size].store(n);
-    return n;
+    static_assert(FR_MAX_SPLITS < (int)(sizeof(ctx->resident_few) / sizeof(ctx->resident_few[0])), "a count for each size");
+    return dlc_resident_clusters(ctx, &ctx->resident_few[size], (const void *)gemm_rows_kernel<false, false>, size, FR_THREADS,
+                                 FR_SMEM);
 }
 
 }  // namespace

@@ -89,6 +89,9 @@ struct dlcContext {
     int deterministic = 0;    // no split reductions whose partial sums meet in atomic adds
     EncodeTiledFn encode_tiled = nullptr;
     EncodeIm2colFn encode_im2col = nullptr;
+    // What the device holds at once of the channel operators' clusters, 0 until the first
+    // product asks (dlc_resident_clusters); every plan of a handle uses the same counts.
+    mutable int resident_pairs = 0, resident_few[9] = {0};
 };
 
 // Split-tile flags owned by a handle: at most this many tiles per launch use them.
@@ -315,3 +318,6 @@ dlcStatus_t dlc_launch(dlcContext *ctx, const void *kernel, dim3 grid, dim3 bloc
 // Lets a kernel of the channel operators use `bytes` of dynamic shared memory.
 // False where the device refuses.  Defined in channel_api.cu.
 bool dlc_allow_smem(const dlcContext *ctx, const void *kernel, size_t bytes);
+// Clusters of `size` CTAs of a kernel that the context's device holds at once; asked once
+// and kept in *known.  Defined in channel_api.cu.
+int dlc_resident_clusters(const dlcContext *ctx, int *known, const void *kernel, int size, int threads, size_t smem);
