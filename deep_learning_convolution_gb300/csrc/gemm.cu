@@ -853,10 +853,13 @@ bool tma_rows(const RowTensor &t, long long rows, long long ch) {
            (rows == 1 || ((t.m.ld * e) % 16 == 0 && t.m.ld >= ch && t.m.ld * e < (1LL << 40)));
 }
 
-// Rows of halves x `n` channels that TMA can store (each half its own plane).
+// Rows of halves x `n` channels that TMA can store (each half its own plane).  A
+// bulk tensor store writes whole pieces of 16 bytes: where a row ends inside one, what
+// lies behind the row (a neighbour in a wider tensor, or the memory after the
+// last row) would be overwritten, so rows have to be a multiple of 16 bytes long.
 bool tma_store_rows(const RowTensor &t, long long rows, int n, int halves) {
     const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
-    return tma_rows(t, rows, (long long)n * halves) && (halves == 1 || ((long long)n * e) % 16 == 0);
+    return tma_rows(t, rows, (long long)n * halves) && ((long long)n * e) % 16 == 0;
 }
 
 bool vec16_rows(const RowTensor &t) {
