@@ -632,9 +632,10 @@ dlcStatus_t dlc_launch_pair(dlcContext *ctx, const ConvProblem &pb) {
     const long long m_pairs = (p.M + 2 * PBM - 1) / (2 * PBM);
     if (m_pairs * p.n_tiles > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     p.num_tiles = (int)(m_pairs * p.n_tiles);
-    // y through bulk tensor stores: FP32, K contiguous, uniform pixel pitch
+    // y through bulk tensor stores: FP32, K contiguous, uniform pixel pitch, pixels of whole
+    // 16-byte pieces (a store fills up the last one, over what lies beside it)
     {
-        const bool dense = pb.ydt == DLC_DATA_FLOAT && pb.ys[1] == 1 && pb.ys[3] >= pb.K &&
+        const bool dense = pb.ydt == DLC_DATA_FLOAT && pb.ys[1] == 1 && pb.ys[3] >= pb.K && pb.K % 4 == 0 &&
                            (pb.ys[3] * 4) % 16 == 0 && (pb.P <= 1 || pb.ys[2] == (long long)pb.Q * pb.ys[3]) &&
                            (pb.N <= 1 || pb.ys[0] == (long long)pb.P * pb.Q * pb.ys[3]) &&
                            ((uintptr_t)pb.y % 16) == 0 && p.M <= 0x7fffffffLL;

@@ -1225,12 +1225,14 @@ cudaError_t launch_mode(int mode, const TcParams &tp, const CUtensorMap &a, cons
 }
 
 // y as a 2-D [M rows, K columns] tensor for bulk tensor stores: K contiguous,
-// every output pixel row at one uniform pitch, 16-byte aligned base and pitch.
+// every output pixel row at one uniform pitch, 16-byte aligned base and pitch, pixels of
+// whole 16-byte pieces (a store fills up the last one, over what lies beside it).
 bool y_tma_ok(const ConvProblem &pb) {
     const long long e = pb.ydt == DLC_DATA_BFLOAT16 ? 2 : 4;
     if (pb.ys[1] != 1) return false;
     const long long pitch = pb.ys[3];
     if (pitch < pb.K || (pitch * e) % 16 || pitch * e >= (1LL << 40)) return false;
+    if ((pb.K * e) % 16) return false;
     if (pb.P > 1 && pb.ys[2] != (long long)pb.Q * pitch) return false;
     if (pb.N > 1 && pb.ys[0] != (long long)pb.P * pb.Q * pitch) return false;
     if (pb.y && ((uintptr_t)pb.y % 16)) return false;

@@ -1105,6 +1105,7 @@ bool win_y_tma_ok(const ConvProblem &pb) {
     if (pb.ydt != DLC_DATA_FLOAT || pb.ys[1] != 1) return false;
     const long long pitch = pb.ys[3];
     if (pitch < pb.K || (pitch * 4) % 16 || (pb.ys[2] * 4) % 16) return false;
+    if (pb.K % 4) return false;  // a store fills up a pixel's last 16-byte piece, over what lies beside it
     if (pb.ys[2] < (long long)pb.Q * pitch) return false;
     if (pb.N > 1 && pb.ys[0] != (long long)pb.P * pb.ys[2]) return false;
     if (pb.y && ((uintptr_t)pb.y % 16)) return false;
