@@ -367,7 +367,8 @@ bool phase_problem(const BwdProblem &bp, int ph, int pw, ConvProblem &f, bool *e
     f.alpha = (float)bp.alpha;
     f.beta = (float)bp.beta;
     f.relu = 0;
-    return dlc_im2col_ok(f) && f.ws[0] == 1;
+    // (the filters' TMA strides: multiples of 16 bytes, so of eight channels)
+    return dlc_im2col_ok(f) && f.ws[0] == 1 && (f.ws[1] * e) % 16 == 0 && (f.ws[2] * e) % 16 == 0 && (f.ws[3] * e) % 16 == 0;
 }
 
 }  // namespace

@@ -73,7 +73,7 @@ def test_allocation_free_forward(handle, c, k):
     assert (rest == BESIDE).all()
 
 
-@pytest.mark.parametrize("c", [72, 104])
+@pytest.mark.parametrize("c", [30, 72, 94, 104])
 def test_data_gradient(handle, c):
     k, n, side = 64, 2, 13
     w, dy = rand(k, 3, 3, c, seed=1, dtype=torch.bfloat16), rand(n, side, side, k, seed=2, dtype=torch.bfloat16)
