@@ -583,7 +583,11 @@ struct RowKernel {
 
 template <int W, int V, int KIND, int MAXT>
 RowKernel fwd_entry(const RowPlan &r, int C) {
-    return {(const void *)rms_rows_kernel<W, V, KIND, MAXT>, Rows<W, V, KIND, 2, ring_rows<KIND, MAXT>()>::smem(r.threads, r.tpr, C)};
+    using Ring = Rows<W, V, KIND, 2, ring_rows<KIND, MAXT>()>;
+    if constexpr (W == 8 && Ring::smem(MAXT, 0, 0) > RMS_MAX_RING)
+        return fwd_entry<W, V, ROWS_REGS, MAXT>(r, C);
+    else
+        return {(const void *)rms_rows_kernel<W, V, KIND, MAXT>, Ring::smem(r.threads, r.tpr, C)};
 }
 
 template <int W, int KIND>
@@ -602,7 +606,11 @@ RowKernel fwd_kernel(const RowPlan &r, int C) {
 
 template <int W, int V, int KIND, int MAXT>
 RowKernel bwd_entry(const RowPlan &r, int C) {
-    return {(const void *)rms_bwd_rows_kernel<W, V, KIND, MAXT>, Rows<W, V, KIND, 3, ring_rows<KIND, MAXT>()>::smem(r.threads, r.tpr, C)};
+    using Ring = Rows<W, V, KIND, 3, ring_rows<KIND, MAXT>()>;
+    if constexpr (W == 8 && Ring::smem(MAXT, 0, 0) > RMS_MAX_RING)
+        return {nullptr, 0};  // (two passes)
+    else
+        return {(const void *)rms_bwd_rows_kernel<W, V, KIND, MAXT>, Ring::smem(r.threads, r.tpr, C)};
 }
 
 template <int W, int KIND>
@@ -626,12 +634,11 @@ dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &pb) {
     RmsProblem p = pb;
     int tpr = r.tpr, gamma_vec = (uintptr_t)p.gamma % 16 == 0;
     void *args[] = {&p, &tpr, &gamma_vec};
-    RowKernel k =
+    const RowKernel k =
         r.w == 0 ? RowKernel{r.lanes ? (const void *)rms_any_kernel<true> : (const void *)rms_any_kernel<false>, 0}
         : r.w == 1 ? (pieces_ok(p.x) && pieces_ok(p.r) ? fwd_kernel<1, ROWS_BF16>(r, p.C) : fwd_kernel<1, ROWS_REGS>(r, p.C))
         : all_of(DLC_DATA_BFLOAT16, {p.x, p.r}) ? fwd_kernel<8, ROWS_BF16>(r, p.C)
         : all_of(DLC_DATA_FLOAT, {p.x, p.r}) ? fwd_kernel<8, ROWS_F32>(r, p.C) : fwd_kernel<8, ROWS_REGS>(r, p.C);
-    if (k.smem > RMS_MAX_RING) k = r.w == 1 ? fwd_kernel<1, ROWS_REGS>(r, p.C) : fwd_kernel<8, ROWS_REGS>(r, p.C);
     if (!dlc_allow_smem(ctx, k.fn, k.smem)) return DLC_STATUS_EXECUTION_FAILED;
     return dlc_launch(ctx, k.fn, dim3((unsigned)r.blocks), dim3((unsigned)r.threads), k.smem, args);
 }
@@ -653,7 +660,7 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
         : r.w == 1 ? (pieces_ok(p.dy) && pieces_ok(p.t) && pieces_ok(p.dt) ? bwd_kernel<1, ROWS_BF16>(r, p.C) : bwd_kernel<1, ROWS_REGS>(r, p.C))
         : all_of(DLC_DATA_BFLOAT16, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_BF16>(r, p.C)
         : all_of(DLC_DATA_FLOAT, {p.dy, p.t, p.dt}) ? bwd_kernel<8, ROWS_F32>(r, p.C) : bwd_kernel<8, ROWS_REGS>(r, p.C);
-    if (k.smem > RMS_MAX_RING) {
+    if (!k.fn) {
         r = two_pass_rows(p.rows, ctx->sm_count);
         k = RowKernel{(const void *)rms_bwd_any_kernel<false>, 0};
     }

@@ -95,7 +95,7 @@ struct RowsAhead {
 #pragma unroll
             for (int i = 0; i < V * W; ++i) f[k][i] = next[k][i];
     }
-    static size_t smem(int, int, int) { return 0; }
+    static constexpr size_t smem(int, int, int) { return 0; }
 };
 
 template <int W, int V, int KIND, int T, int S>
@@ -150,7 +150,7 @@ struct Rows<8, V, KIND, T, S> {
             }
         get = get == row * (S - 1) ? 0 : get + row;
     }
-    static size_t smem(int threads, int, int) { return (size_t)S * T * V * Q * 16 * threads; }
+    static constexpr size_t smem(int threads, int, int) { return (size_t)S * T * V * Q * 16 * threads; }
 };
 
 template <int V, int T, int S>
