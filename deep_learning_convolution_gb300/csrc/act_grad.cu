@@ -8,7 +8,8 @@
 // 256 neighbouring channels of a row, eight a thread (16-byte accesses of
 // BF16), a block eight rows at a time; each thread copies its next rows into
 // shared memory asynchronously, and the column sums stay in its registers.
-// 8192 x 5632 gated, BF16: 74 us, 6.2 TB/s.
+// 8192 x 5632 gated, BF16: 74 us, 6.2 TB/s, with dbias 85 us.  With z in FP32 the rows
+// come one ahead in registers, some of them spilled: 167 us with dbias, 3.9 TB/s.
 #include "channel.cuh"
 #include "ptx.cuh"
 #include "row_ring.cuh"

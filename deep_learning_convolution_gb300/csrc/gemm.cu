@@ -26,9 +26,9 @@
 // 3-10 (two per quarter of the TMEM lanes, alternate 32-column chunks) run the
 // epilogue of the other one.  Every wait is bounded.
 //
-// What bounds it: long reductions the tensor core under the power cap (16384 x
-// 4096 -> 4096 283 us, 1940 TFLOP/s, in E4M3 162 us, 3400; gated 16384 x 4096 ->
-// 2 x 8192 in E4M3 659 us, 3330); short ones the epilogue, 2.9 us for a tile of 256
+// What bounds it: long reductions the tensor core under the power cap (gated 16384 x
+// 4096 -> 2 x 8192 in E4M3 676 us, 3250 TFLOP/s, call after call; 16384 x 4096 -> 4096 in
+// a burst of eight calls 284 us, 1940 TFLOP/s); short ones the epilogue, 2.9 us for a tile of 256
 // columns in BF16 with a bias and up to 6 with GELU, residual and z, most of it
 // instructions (hence the packed FP32 pairs); small ones the launch, about 5 us
 // from call to call.  Loads, MMAs and bulk stores are issued by an elected thread: by

@@ -12,8 +12,10 @@
 // registers: the traffic is each input once and each output once, which is
 // what bounds these kernels.  max |y| = rho * max |gamma t|, so the 8-bit
 // scale comes from the same reduction as the sum of squares.  Measured back to
-// back, BF16: forward with both outputs 100352 x 512 74.6 us (5.5 TB/s), backward
-// 25088 x 1024 35.3 us (5.8 TB/s); one row 2.5 us, the cost of a launch.
+// back, BF16: forward with both outputs 100352 x 512 67.9 us (6.05 TB/s), backward
+// 25088 x 1024 35.6 us (5.8 TB/s); one row 3 us, the cost of a launch.  Slower: FP32
+// rows (100352 x 512 248 us, 3.3 TB/s), an FP32 stream beside BF16 branches (a row ahead in registers: 124 us, 5.0 TB/s; backward 209
+// us, 3.5 TB/s), channels apart (two passes: 368 us, 1.1 TB/s; backward 610 us, 0.7 TB/s).
 #include <initializer_list>
 
 #include "channel.cuh"
@@ -37,7 +39,7 @@ constexpr int RMS_FWD_BLOCKS = 4, RMS_BWD_BLOCKS = 2;
 // backward 261 us, 433 through registers.
 constexpr size_t RMS_MAX_RING = 226 * 1024;
 
-// Rows of the ring.  Measured, 100352 x 512 forward / 25088 x 1024 backward, BF16:
+// Rows of the ring.  Measured when chosen, 100352 x 512 forward / 25088 x 1024 backward, BF16:
 // 3 rows at 4 / 2 blocks an SM 74.5 / 40.0 us; 4 rows 77.6 / 41.1; one row ahead
 // in registers 109 us forward.
 // FP32 rows, twice the bytes, and blocks of 1024 threads: 2.

@@ -525,7 +525,9 @@ dlcStatus_t dlcActivationForward(dlcHandle_t handle, dlcActivationMode_t mode, d
  * images of 2^31 pixels and more each have to be one pitch apart (NOT_SUPPORTED).
  *
  * Pointers are device pointers; those marked optional may be NULL, and their
- * descriptor is then ignored.  Outputs must not overlap other arguments
+ * descriptor is then ignored.  Relative errors of the activations (FP32, before
+ * a result is rounded to its type): GELU 4e-6 + 1e-7 z^2, SILU and SIGMOID 1e-6 +
+ * 2e-7 |z|.  Outputs must not overlap other arguments
  * (BAD_PARAM; the address ranges that strides reach count) but for the in-place
  * uses named at each call.  A workspace is caller-owned, 256-byte aligned and
  * of at least the queried size (else BAD_PARAM; NULL where that is 0); its
