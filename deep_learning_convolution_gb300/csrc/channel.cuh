@@ -1,6 +1,11 @@
 // channel.cuh -- shared pieces of the channel operators (RMS norm, linear
 // layer, gated projections): tensors seen as rows (pixels or tokens) by
 // channels, activations with their derivatives, and typed loads and stores.
+//
+// Whatever a kernel reads, the grid ahead of it may still be writing when it starts (a
+// norm's row scales, an output that is the next layer's bias): it is read after
+// griddep_wait and by plain loads, never by the read-only path, whose data must not
+// change while the kernel runs and whose loads may be moved above the wait.
 #pragma once
 
 #include <cuda_bf16.h>

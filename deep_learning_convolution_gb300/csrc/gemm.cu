@@ -217,8 +217,8 @@ __device__ __forceinline__ void gp_columns(const GpParams &p, bool gated, int n0
         const bool up = gated && i >= p.nout;
         const int n = n0 + (up ? i - p.nout : i);
         const long long k = (up ? (long long)p.N : 0) + n;
-        columns[i] = p.sb && n < p.N ? __ldg(p.sb + k) : 1.f;
-        columns[256 + i] = p.bias && n < p.N ? __ldg(p.bias + k) : 0.f;
+        columns[i] = p.sb && n < p.N ? p.sb[k] : 1.f;
+        columns[256 + i] = p.bias && n < p.N ? p.bias[k] : 0.f;
     }
 }
 
@@ -527,7 +527,7 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
             if (ROWS && p.z.p) zo = row_off(p.z.m, m);
             if (p.r.p) ro = row_off(p.r.m, m);
             if (ROWS) yo = row_off(p.y.m, m);
-            if (p.sa) sa = __ldg(p.sa + m);
+            if (p.sa) sa = p.sa[m];
         }
         // (a gated layer has no residual; ROWS adds it where the rows are written)
         const bool res = !GATED && !ROWS && valid && !raw && p.r.p;
@@ -730,13 +730,13 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
                 const float4 q = *reinterpret_cast<const float4 *>(src + (long long)sp * (2 * GP_ROWS) * f.bn);
                 s[0] += q.x, s[1] += q.y, s[2] += q.z, s[3] += q.w;
             }
-            const float sa = g.sa ? __ldg(g.sa + m) : 1.f;
+            const float sa = g.sa ? g.sa[m] : 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const long long k = (long long)h * g.N + n + j;
                 if (j < cols) {
-                    if (g.sb) s[j] *= sa * __ldg(g.sb + k);
-                    if (g.bias) s[j] += __ldg(g.bias + k);
+                    if (g.sb) s[j] *= sa * g.sb[k];
+                    if (g.bias) s[j] += g.bias[k];
                 }
                 v[h][j] = s[j];
             }

@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(FR_THREADS, 1)
     for (int h = 0; h < HALVES; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            sb[h][i] = p.sb && i < cols ? __ldg(p.sb + (long long)h * p.N + n + i) : 1.f;
-            bias[h][i] = p.bias && i < cols ? __ldg(p.bias + (long long)h * p.N + n + i) : 0.f;
+            sb[h][i] = p.sb && i < cols ? p.sb[(long long)h * p.N + n + i] : 1.f;
+            bias[h][i] = p.bias && i < cols ? p.bias[(long long)h * p.N + n + i] : 0.f;
         }
-    for (int j = (int)threadIdx.x; j < p.rows; j += FR_THREADS) scale[j] = p.sa && m0 + j < p.M ? __ldg(p.sa + m0 + j) : 1.f;
+    for (int j = (int)threadIdx.x; j < p.rows; j += FR_THREADS) scale[j] = p.sa && m0 + j < p.M ? p.sa[m0 + j] : 1.f;
     bool good;
     {
         volatile int dummy = 0;  // (an abort elsewhere still commits `done`)

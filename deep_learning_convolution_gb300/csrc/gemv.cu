@@ -132,15 +132,15 @@ __device__ __forceinline__ void gv_finish(const GvParams &p, int group, int rang
         __syncwarp();
     const int o = lane / M, m = lane - o * M, n = group * OUT + o;
     if (range != 0 || group >= p.groups || lane >= OUT * M || n >= p.N) return;
-    const float sa = p.sa ? __ldg(p.sa + m) : 1.f;
+    const float sa = p.sa ? p.sa[m] : 1.f;
     float z[GATED ? 2 : 1];
 #pragma unroll
     for (int h = 0; h < (GATED ? 2 : 1); ++h) {
         float t = 0.f;
         for (int i = 0; i < p.ranges; ++i) t += part[warp + i][(h * OUT + o) * M + m];
         const long long k = (long long)h * p.N + n;
-        if (p.sb) t *= sa * __ldg(p.sb + k);
-        if (p.bias) t += __ldg(p.bias + k);
+        if (p.sb) t *= sa * p.sb[k];
+        if (p.bias) t += p.bias[k];
         z[h] = t;
         if (p.z.p) store_elem(p.z.p, p.z.dt, row_off(p.z.m, m) + k * p.z.m.cs, t);
     }

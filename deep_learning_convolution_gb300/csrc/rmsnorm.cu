@@ -105,12 +105,12 @@ __device__ __forceinline__ void load_gamma(const float *gamma, int c, int C, boo
     if (W == 8 && vec && c + W <= C) {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(gamma + c) + i);
+            const float4 a = reinterpret_cast<const float4 *>(gamma + c)[i];
             v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = c + i < C ? __ldg(gamma + c + i) : 0.f;
+        for (int i = 0; i < W; ++i) v[i] = c + i < C ? gamma[c + i] : 0.f;
     }
 }
 
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 sq = fmaf(v[i], v[i], sq);
-                mx = fmaxf(mx, fabsf(v[i] * (in(i) ? __ldg(p.gamma + c + i * M::STEP) : 0.f)));
+                mx = fmaxf(mx, fabsf(v[i] * (in(i) ? p.gamma[c + i * M::STEP] : 0.f)));
             }
         }
         const float2 red = M::template join<true>(sq, mx, part);
@@ -319,12 +319,14 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_any_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) v[i] += r[i];
             }
+            float g[AHEAD];
+            load_elems<AHEAD>(p.gamma, DLC_DATA_FLOAT, c, M::STEP, in, g);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const int ci = c + i * M::STEP;
                 if (ci >= p.C) break;
                 if (p.t.p) store_elem(p.t.p, p.t.dt, to + ci * p.t.m.cs, v[i]);
-                store_elem(p.y.p, p.y.dt, yo + ci * p.y.m.cs, v[i] * __ldg(p.gamma + ci) * first * f);
+                store_elem(p.y.p, p.y.dt, yo + ci * p.y.m.cs, v[i] * g[i] * first * f);
             }
         }
     }
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 sq = fmaf(v[i], v[i], sq);
-                dot = fmaf(d[i] * (in(i) ? __ldg(p.gamma + c + i * M::STEP) : 0.f), v[i], dot);
+                dot = fmaf(d[i] * (in(i) ? p.gamma[c + i * M::STEP] : 0.f), v[i], dot);
             }
         }
         const float2 red = M::template join<false>(sq, dot, part);
@@ -453,6 +455,8 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
             const auto in = [&](int i) { return on && c + i * M::STEP < p.C; };
             load_elems<AHEAD>(p.t.p, p.t.dt, to + c * p.t.m.cs, M::STEP * p.t.m.cs, in, v);
             load_elems<AHEAD>(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs, M::STEP * p.dy.m.cs, in, d);
+            float gain[AHEAD];
+            load_elems<AHEAD>(p.gamma, DLC_DATA_FLOAT, c, M::STEP, in, gain);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) a[i] = 0.f;
             if (p.dt.p) load_elems<AHEAD>(p.dt.p, p.dt.dt, so + c * p.dt.m.cs, M::STEP * p.dt.m.cs, in, a);
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(RMS_THREADS) rms_bwd_any_kernel(const __grid_c
             for (int i = 0; i < AHEAD; ++i) {
                 const int ci = c + i * M::STEP;
                 if (ci >= p.C) break;
-                if (on) store_elem(p.dx.p, p.dx.dt, xo + ci * p.dx.m.cs, a[i] + rho * d[i] * __ldg(p.gamma + ci) - v[i] * k);
+                if (on) store_elem(p.dx.p, p.dx.dt, xo + ci * p.dx.m.cs, a[i] + rho * d[i] * gain[i] - v[i] * k);
                 if (!p.dgamma) continue;
                 float g = d[i] * rho * v[i];
                 if (LANES)
