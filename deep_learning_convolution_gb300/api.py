@@ -462,6 +462,25 @@ class _ChannelOp:
             raise ValueError(f"{what} must be a dense float32 vector of {n} elements on GPU {self.device}")
         return t.data_ptr()
 
+    def _index_example(self, t, rows: int):
+        """Type code and example of a tensor of one token or class number a row."""
+        import torch
+        if t.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"token and class numbers are int32 or int64, not {t.dtype}")
+        if not t.is_cuda or (self.device is not None and t.get_device() != self.device):
+            raise ValueError("the tensors of an operator are on one GPU")
+        self.device = t.get_device()
+        if t.numel() != rows or not t.is_contiguous():
+            raise ValueError(f"{rows} rows take a dense tensor of as many numbers, not {tuple(t.shape)}")
+        return (B.DLC_INDEX_INT64 if t.dtype is torch.int64 else B.DLC_INDEX_INT32), (t.dtype, rows)
+
+    def _numbers(self, t, example, what: str) -> int:
+        """Pointer of a call's tensor of token or class numbers."""
+        dtype, rows = example
+        if t.dtype is not dtype or t.numel() != rows or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"{what} must be a dense {dtype} tensor of {rows} numbers on GPU {self.device}")
+        return t.data_ptr()
+
     def close(self):
         for d in self._tensors:
             B.dlcDestroyTensorDescriptor(d)
@@ -659,6 +678,227 @@ class GatedBackward(_ProductBackward):
     def __init__(self, handle: Handle, x, w, dy, dx=None, dw=None, *, z=None, act: str = "silu",
                  axes: str = "NHWC"):
         super().__init__(handle, x, w, dy, dx, dw, z, act, axes)
+
+
+class LayerNormForward(_ChannelOp):
+    """total = x + residual; y = gamma * (total - mean) / deviation + beta through
+    dlcLayerNormForward; an E4M3 y comes with one scale per row."""
+    _name = "dlcLayerNormForward"
+
+    def __init__(self, handle: Handle, x, y, *, residual=None, total=None, eps: float = 1e-5,
+                 axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.eps = float(eps)
+        self.x_desc, self._x = self._act_desc(x)
+        self.y_desc, self._y = self._act_desc(y)
+        self.r_desc, self._r = self._act_desc(residual)
+        self.t_desc, self._t = self._act_desc(total)
+        self.channels = B.dlcGetTensor4dDescriptor(self.x_desc)[2]
+        self.rows = x.numel() // self.channels
+
+    def __call__(self, x, gamma, y, beta=None, residual=None, total=None, scale=None):
+        status = self._fn(self.handle.h, self.eps, self.x_desc, self._at(x, self._x, "x"),
+                          self.r_desc, residual if residual is None else
+                          self._at(residual, self._r, "residual"), self._vector(gamma, self.channels, "gamma"),
+                          beta if beta is None else self._vector(beta, self.channels, "beta"),
+                          self.t_desc, total if total is None else self._at(total, self._t, "total"),
+                          self.y_desc, self._at(y, self._y, "y"),
+                          scale if scale is None else self._vector(scale, self.rows, "scale"))
+        if status:
+            B.check(self._name, status)
+        return y
+
+
+class LayerNormBackward(_ChannelOp):
+    """dx (the gradient of x and of the residual), dgamma and dbeta of
+    LayerNormForward through dlcLayerNormBackward; dtotal is the gradient that
+    reaches the sum by other ways."""
+    _name = "dlcLayerNormBackward"
+
+    def __init__(self, handle: Handle, dy, total, dx, *, dtotal=None, eps: float = 1e-5,
+                 axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.eps = float(eps)
+        self.dy_desc, self._dy = self._act_desc(dy)
+        self.t_desc, self._t = self._act_desc(total)
+        self.dx_desc, self._dx = self._act_desc(dx)
+        self.dt_desc, self._dt = self._act_desc(dtotal)
+        self.channels = B.dlcGetTensor4dDescriptor(self.t_desc)[2]
+        self._set_workspace(B.dlcGetLayerNormBackwardWorkspaceSize(handle.h, self.t_desc), total.device)
+
+    def __call__(self, dy, total, gamma, dx, dgamma=None, dbeta=None, dtotal=None):
+        status = self._fn(self.handle.h, self.eps, self.dy_desc, self._at(dy, self._dy, "dy"),
+                          self.t_desc, self._at(total, self._t, "total"),
+                          self._vector(gamma, self.channels, "gamma"),
+                          self.dt_desc, dtotal if dtotal is None else self._at(dtotal, self._dt, "dtotal"),
+                          self.dx_desc, self._at(dx, self._dx, "dx"),
+                          dgamma if dgamma is None else self._vector(dgamma, self.channels, "dgamma"),
+                          dbeta if dbeta is None else self._vector(dbeta, self.channels, "dbeta"),
+                          self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
+        return dx
+
+
+class _Dropout(_ChannelOp):
+    def __init__(self, handle, x, y, residual, p, axes):
+        super().__init__(handle, axes)
+        self.p = float(p)
+        if not 0.0 <= self.p < 1.0:
+            raise ValueError(f"the probability of dropping an element is in [0, 1), not {p}")
+        self.x_desc, self._x = self._act_desc(x)
+        self.y_desc, self._y = self._act_desc(y)
+        self.r_desc, self._r = self._act_desc(residual)
+
+    def _random(self, t) -> int:
+        """Pointer of the seed and the step: two int64 numbers on the GPU, read by the kernel."""
+        import torch
+        if t.dtype is not torch.int64 or t.numel() != 2 or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"random must be two dense int64 numbers, seed and step, on GPU {self.device}")
+        return t.data_ptr()
+
+
+class DropoutForward(_Dropout):
+    """y = residual + (x where kept, over the share that is kept) through
+    dlcDropoutForward.  ``random``: two int64 numbers on the GPU, a seed and a
+    step; the same numbers drop the same elements."""
+    _name = "dlcDropoutForward"
+
+    def __init__(self, handle: Handle, x, y, *, p: float, residual=None, axes: str = "NHWC"):
+        super().__init__(handle, x, y, residual, p, axes)
+
+    def __call__(self, x, random, y, residual=None):
+        status = self._fn(self.handle.h, self.p, self._random(random), self.x_desc, self._at(x, self._x, "x"),
+                          self.r_desc, residual if residual is None else self._at(residual, self._r, "residual"),
+                          self.y_desc, self._at(y, self._y, "y"))
+        if status:
+            B.check(self._name, status)
+        return y
+
+
+class DropoutBackward(_Dropout):
+    """dx of DropoutForward through dlcDropoutBackward, from the numbers that the
+    forward call was given.  The residual's gradient is dy."""
+    _name = "dlcDropoutBackward"
+
+    def __init__(self, handle: Handle, dy, dx, *, p: float, axes: str = "NHWC"):
+        super().__init__(handle, dy, dx, None, p, axes)
+
+    def __call__(self, dy, random, dx):
+        status = self._fn(self.handle.h, self.p, self._random(random), self.x_desc, self._at(dy, self._x, "dy"),
+                          self.y_desc, self._at(dx, self._y, "dx"))
+        if status:
+            B.check(self._name, status)
+        return dx
+
+
+class EmbeddingForward(_ChannelOp):
+    """y = scale * table[tokens] through dlcEmbeddingForward, table being [V, C];
+    tokens (int32 or int64) hold one number a row of y, a negative one giving
+    a row of zeros."""
+    _name = "dlcEmbeddingForward"
+
+    def __init__(self, handle: Handle, tokens, table, y, *, scale: float = 1.0, axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.scale = float(scale)
+        self.w_desc, self._w = self._weight_desc(table)
+        self.y_desc, self._y = self._act_desc(y)
+        channels = B.dlcGetTensor4dDescriptor(self.y_desc)[2]
+        self.index_type, self._tokens = self._index_example(tokens, y.numel() // channels)
+
+    def __call__(self, tokens, table, y):
+        status = self._fn(self.handle.h, self.scale, self.index_type, self._numbers(tokens, self._tokens, "tokens"),
+                          self.w_desc, self._at(table, self._w, "table"), self.y_desc, self._at(y, self._y, "y"))
+        if status:
+            B.check(self._name, status)
+        return y
+
+
+class EmbeddingBackward(_ChannelOp):
+    """The table's gradient through dlcEmbeddingBackward: dtable[v] = scale * the sum
+    of dy over the rows of token v, or that added to dtable (``accumulate``)."""
+    _name = "dlcEmbeddingBackward"
+
+    def __init__(self, handle: Handle, tokens, dy, dtable, *, scale: float = 1.0, accumulate: bool = False,
+                 axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.scale, self.accumulate = float(scale), int(bool(accumulate))
+        self.dy_desc, self._dy = self._act_desc(dy)
+        self.w_desc, self._w = self._weight_desc(dtable)
+        channels = B.dlcGetTensor4dDescriptor(self.dy_desc)[2]
+        self.index_type, self._tokens = self._index_example(tokens, dy.numel() // channels)
+        self._set_workspace(B.dlcGetEmbeddingBackwardWorkspaceSize(handle.h, self.dy_desc, self.w_desc), dy.device)
+
+    def __call__(self, tokens, dy, dtable):
+        status = self._fn(self.handle.h, self.scale, self.index_type, self._numbers(tokens, self._tokens, "tokens"),
+                          self.dy_desc, self._at(dy, self._dy, "dy"), self.accumulate,
+                          self.w_desc, self._at(dtable, self._w, "dtable"), self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
+        return dtable
+
+
+class CrossEntropyForward(_ChannelOp):
+    """loss = lse - z[target], lse = log(sum(exp(z))) of z = x w^T + bias through
+    dlcCrossEntropyForward, w being [classes, C]; loss and lse are FP32, one a row.
+    E4M3 x and w take one scale per row and per class.  A negative target counts
+    for nothing."""
+    _name = "dlcCrossEntropyForward"
+
+    def __init__(self, handle: Handle, x, w, target, *, axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.x_desc, self._x = self._act_desc(x)
+        self.w_desc, self._w = self._weight_desc(w)
+        self.classes = w.shape[0]
+        self.rows = x.numel() // B.dlcGetTensor4dDescriptor(self.x_desc)[2]
+        self.index_type, self._target = self._index_example(target, self.rows)
+        self._set_workspace(B.dlcGetCrossEntropyForwardWorkspaceSize(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
+                                                                     w.data_ptr()), x.device)
+
+    def __call__(self, x, w, target, loss, lse, bias=None, x_scale=None, w_scale=None):
+        status = self._fn(self.handle.h, self.x_desc, self._at(x, self._x, "x"),
+                          x_scale if x_scale is None else self._vector(x_scale, self.rows, "x_scale"),
+                          self.w_desc, self._at(w, self._w, "w"),
+                          w_scale if w_scale is None else self._vector(w_scale, self.classes, "w_scale"),
+                          bias if bias is None else self._vector(bias, self.classes, "bias"),
+                          self.index_type, self._numbers(target, self._target, "target"),
+                          self._vector(loss, self.rows, "loss"), self._vector(lse, self.rows, "lse"),
+                          self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
+        return loss
+
+
+class CrossEntropyBackward(_ChannelOp):
+    """dx, dw and dbias of sum(dloss * loss) through dlcCrossEntropyBackward, each
+    where its tensor is given; lse is what the forward call wrote."""
+    _name = "dlcCrossEntropyBackward"
+
+    def __init__(self, handle: Handle, x, w, target, dx=None, dw=None, *, axes: str = "NHWC"):
+        super().__init__(handle, axes)
+        self.x_desc, self._x = self._act_desc(x)
+        self.w_desc, self._w = self._weight_desc(w)
+        self.dx_desc, self._dx = self._act_desc(dx)
+        self.dw_desc, self._dw = self._weight_desc(dw)
+        self.classes = w.shape[0]
+        self.rows = x.numel() // B.dlcGetTensor4dDescriptor(self.x_desc)[2]
+        self.index_type, self._target = self._index_example(target, self.rows)
+        self._set_workspace(B.dlcGetCrossEntropyBackwardWorkspaceSize(handle.h, self.x_desc, x.data_ptr(), self.w_desc,
+                                                                      w.data_ptr()), x.device)
+
+    def __call__(self, x, w, target, lse, dloss, dx=None, dw=None, bias=None, dbias=None):
+        status = self._fn(self.handle.h, self.x_desc, self._at(x, self._x, "x"), self.w_desc,
+                          self._at(w, self._w, "w"),
+                          bias if bias is None else self._vector(bias, self.classes, "bias"),
+                          self.index_type, self._numbers(target, self._target, "target"),
+                          self._vector(lse, self.rows, "lse"), self._vector(dloss, self.rows, "dloss"),
+                          self.dx_desc, dx if dx is None else self._at(dx, self._dx, "dx"),
+                          self.dw_desc, dw if dw is None else self._at(dw, self._dw, "dw"),
+                          dbias if dbias is None else self._vector(dbias, self.classes, "dbias"),
+                          self._scratch(), self._ws_bytes)
+        if status:
+            B.check(self._name, status)
+        return dx, dw, dbias
 
 
 def output_dim(x, w, *, x_axes="NCHW", w_axes="KCRS", pads=(0, 0, 0, 0), stride=(1, 1),

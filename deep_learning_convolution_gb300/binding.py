@@ -65,6 +65,9 @@ DLC_KERNEL_FEW_ROWS = 12
 DLC_KERNEL_GEMV = 13
 DLC_DEVERR_NONE = 0
 DLC_DEVERR_WAIT_TIMEOUT = 1
+DLC_DEVERR_INDEX = 2
+DLC_INDEX_INT32 = 0
+DLC_INDEX_INT64 = 1
 
 KERNEL_NAMES = {DLC_KERNEL_NONE: "none", DLC_KERNEL_FFMA: "ffma",
                 DLC_KERNEL_TC_IM2COL: "tc_im2col", DLC_KERNEL_TC_GATHER: "tc_gather",
@@ -158,6 +161,23 @@ SIGNATURES = {
                          c_void_p, _h, c_void_p, c_void_p, c_void_p, c_size_t],
     "dlcGetGatedBackwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, c_int, _h, _h, c_void_p,
                                          POINTER(c_size_t)],
+    "dlcLayerNormForward": [_h, c_double, _h, c_void_p, _h, c_void_p, c_void_p, c_void_p, _h,
+                            c_void_p, _h, c_void_p, c_void_p],
+    "dlcGetLayerNormBackwardWorkspaceSize": [_h, _h, POINTER(c_size_t)],
+    "dlcLayerNormBackward": [_h, c_double, _h, c_void_p, _h, c_void_p, c_void_p, _h, c_void_p, _h,
+                             c_void_p, c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcDropoutForward": [_h, c_double, c_void_p, _h, c_void_p, _h, c_void_p, _h, c_void_p],
+    "dlcDropoutBackward": [_h, c_double, c_void_p, _h, c_void_p, _h, c_void_p],
+    "dlcEmbeddingForward": [_h, c_double, c_int, c_void_p, _h, c_void_p, _h, c_void_p],
+    "dlcGetEmbeddingBackwardWorkspaceSize": [_h, _h, _h, POINTER(c_size_t)],
+    "dlcEmbeddingBackward": [_h, c_double, c_int, c_void_p, _h, c_void_p, c_int, _h, c_void_p,
+                             c_void_p, c_size_t],
+    "dlcCrossEntropyForward": [_h, _h, c_void_p, c_void_p, _h, c_void_p, c_void_p, c_void_p, c_int,
+                               c_void_p, c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcGetCrossEntropyForwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, POINTER(c_size_t)],
+    "dlcCrossEntropyBackward": [_h, _h, c_void_p, _h, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                c_void_p, _h, c_void_p, _h, c_void_p, c_void_p, c_void_p, c_size_t],
+    "dlcGetCrossEntropyBackwardWorkspaceSize": [_h, _h, c_void_p, _h, c_void_p, POINTER(c_size_t)],
 }
 _RESTYPES = {"dlcGetErrorString": c_char_p}
 
@@ -573,3 +593,61 @@ def dlcGatedBackward(handle, xDesc, x, wDesc, w, act, zDesc, z, dyDesc, dy, dxDe
 def dlcGetGatedBackwardWorkspaceSize(handle, xDesc, x, wDesc, w, act, zDesc, dyDesc, dy) -> int:
     return _bytes("dlcGetGatedBackwardWorkspaceSize", handle, xDesc, x, wDesc, w, act, zDesc, dyDesc,
                   dy)
+
+
+def dlcLayerNormForward(handle, epsilon, xDesc, x, residualDesc, residual, gamma, beta, totalDesc,
+                        total, yDesc, y, scale):
+    _call("dlcLayerNormForward", handle, epsilon, xDesc, x, residualDesc, residual, gamma, beta,
+          totalDesc, total, yDesc, y, scale)
+
+
+def dlcGetLayerNormBackwardWorkspaceSize(handle, totalDesc) -> int:
+    return _bytes("dlcGetLayerNormBackwardWorkspaceSize", handle, totalDesc)
+
+
+def dlcLayerNormBackward(handle, epsilon, dyDesc, dy, totalDesc, total, gamma, dtotalDesc, dtotal,
+                         dxDesc, dx, dgamma, dbeta, workspace, workspaceBytes):
+    _call("dlcLayerNormBackward", handle, epsilon, dyDesc, dy, totalDesc, total, gamma, dtotalDesc,
+          dtotal, dxDesc, dx, dgamma, dbeta, workspace, workspaceBytes)
+
+
+def dlcDropoutForward(handle, probability, random, xDesc, x, residualDesc, residual, yDesc, y):
+    _call("dlcDropoutForward", handle, probability, random, xDesc, x, residualDesc, residual, yDesc, y)
+
+
+def dlcDropoutBackward(handle, probability, random, dyDesc, dy, dxDesc, dx):
+    _call("dlcDropoutBackward", handle, probability, random, dyDesc, dy, dxDesc, dx)
+
+
+def dlcEmbeddingForward(handle, scale, indexType, tokens, tableDesc, table, yDesc, y):
+    _call("dlcEmbeddingForward", handle, scale, indexType, tokens, tableDesc, table, yDesc, y)
+
+
+def dlcGetEmbeddingBackwardWorkspaceSize(handle, dyDesc, dtableDesc) -> int:
+    return _bytes("dlcGetEmbeddingBackwardWorkspaceSize", handle, dyDesc, dtableDesc)
+
+
+def dlcEmbeddingBackward(handle, scale, indexType, tokens, dyDesc, dy, accumulate, dtableDesc, dtable,
+                         workspace, workspaceBytes):
+    _call("dlcEmbeddingBackward", handle, scale, indexType, tokens, dyDesc, dy, accumulate, dtableDesc,
+          dtable, workspace, workspaceBytes)
+
+
+def dlcCrossEntropyForward(handle, xDesc, x, xScale, wDesc, w, wScale, bias, indexType, target, loss,
+                           lse, workspace, workspaceBytes):
+    _call("dlcCrossEntropyForward", handle, xDesc, x, xScale, wDesc, w, wScale, bias, indexType, target,
+          loss, lse, workspace, workspaceBytes)
+
+
+def dlcGetCrossEntropyForwardWorkspaceSize(handle, xDesc, x, wDesc, w) -> int:
+    return _bytes("dlcGetCrossEntropyForwardWorkspaceSize", handle, xDesc, x, wDesc, w)
+
+
+def dlcCrossEntropyBackward(handle, xDesc, x, wDesc, w, bias, indexType, target, lse, dloss, dxDesc, dx,
+                            dwDesc, dw, dbias, workspace, workspaceBytes):
+    _call("dlcCrossEntropyBackward", handle, xDesc, x, wDesc, w, bias, indexType, target, lse, dloss,
+          dxDesc, dx, dwDesc, dw, dbias, workspace, workspaceBytes)
+
+
+def dlcGetCrossEntropyBackwardWorkspaceSize(handle, xDesc, x, wDesc, w) -> int:
+    return _bytes("dlcGetCrossEntropyBackwardWorkspaceSize", handle, xDesc, x, wDesc, w)

@@ -1,0 +1,432 @@
+// cross_entropy.cu -- softmax cross entropy on top of a linear layer, in pieces of the
+// classes (a vocabulary), so that the logits are never kept:
+//
+//   z[m, k] = sa[m] sb[k] sum_c x[m, c] w[k, c] + bias[k]
+//   lse[m] = log sum_k exp z[m, k];  loss[m] = lse[m] - z[m, target[m]]
+//   dz[m, k] = dloss[m] (exp(z[m, k] - lse[m]) - [k = target[m]])
+//   dx = dz w;  dw = dz^T x;  dbias = sum_m dz        (rows without a target: 0)
+//
+// Exponentials are taken about whole powers of two: with z' = z log2(e), the sum of a row's
+// part is kept as s = sum 2^(z' - r) with r = ceil(max z'), an integer, so that joining
+// two parts rescales by an exact power of two and no rounding of the maximum enters.
+#include <cmath>
+
+#include "channel.cuh"
+#include "gemm.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace dlc;
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int CE_THREADS = 256;
+constexpr int CE_SEGMENT = 4096;  // logits of a row that a block sums up
+
+// A part of a row's sum: 2^r * s.  r = -inf: nothing (or only -inf) so far.
+struct CePart {
+    float r, s;
+};
+
+__device__ __forceinline__ CePart ce_join(CePart a, CePart b) {
+    const float r = fmaxf(a.r, b.r), base = isinf(r) ? 0.f : r;
+    return {r, a.s * exp2_fast(a.r - base) + b.s * exp2_fast(b.r - base)};
+}
+
+__device__ __forceinline__ CePart ce_join_lanes(CePart a) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) a = ce_join(a, CePart{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
+    return a;
+}
+
+__device__ __forceinline__ long long ce_target(const IndexList &t, long long i) {
+    return t.wide ? static_cast<const long long *>(t.p)[i] : static_cast<const int *>(t.p)[i];
+}
+
+// ---- logits of a piece in memory (FP32) ---------------------------------------------
+
+struct CeParams {
+    long long M;
+    int V, n0, cols;           // classes in all; of this piece: the first one and how many
+    const float *z;            // [M][ld]
+    long long ld;
+    IndexList target;
+    float2 *part;              // [part][M] (r, s)
+    int part0, parts;          // first part of this piece; of all pieces
+    float *chosen;             // [M] the target's logit
+    float *loss, *lse;
+    const float *dloss;
+    unsigned short *dz;        // [M][ldz]
+    long long ldz;
+    float *sums;               // [strip][cols] or null
+    int *err;
+};
+
+// The sum of one segment of a row of logits.
+__global__ void __launch_bounds__(CE_THREADS) ce_part_kernel(const __grid_constant__ CeParams p) {
+    griddep_launch_dependents();
+    __shared__ CePart warps[CE_THREADS / 32];
+    constexpr int E = CE_SEGMENT / CE_THREADS;
+    const int c0 = (int)blockIdx.y * CE_SEGMENT + 4 * (int)threadIdx.x;
+    griddep_wait();
+    for (long long m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const float *z = p.z + m * p.ld;
+        float v[E];
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+            const int c = c0 + 4 * CE_THREADS * j;
+            float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (c + 4 <= p.cols) {
+                q = *reinterpret_cast<const float4 *>(z + c);
+            } else if (c < p.cols) {
+                q.x = z[c];
+                if (c + 1 < p.cols) q.y = z[c + 1];
+                if (c + 2 < p.cols) q.z = z[c + 2];
+            }
+            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+        }
+        float top = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);
+        const float r = ceilf(top * LOG2E), base = isinf(r) ? 0.f : r;
+#pragma unroll
+        for (int i = 0; i < E; ++i) s += exp2_fast(fmaf(v[i], LOG2E, -base));
+        const CePart a = ce_join_lanes(CePart{r, s});
+        if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = a;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            CePart t = warps[0];
+            for (int i = 1; i < CE_THREADS / 32; ++i) t = ce_join(t, warps[i]);
+            p.part[(long long)(p.part0 + (int)blockIdx.y) * p.M + m] = make_float2(t.r, t.s);
+            if (blockIdx.y == 0) {
+                const long long k = ce_target(p.target, m) - p.n0;
+                if (k >= 0 && k < p.cols) p.chosen[m] = z[k];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the parts of 32 rows a block, in a fixed order: a lane a row, the parts dealt to the warps.
+__global__ void __launch_bounds__(1024) ce_loss_kernel(const __grid_constant__ CeParams p) {
+    griddep_launch_dependents();
+    __shared__ CePart warps[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long m = (long long)blockIdx.x * 32 + lane;
+    griddep_wait();
+    CePart a{-INFINITY, 0.f};
+    if (m < p.M) {
+#pragma unroll 4
+        for (int i = warp; i < p.parts; i += 32) {
+            const float2 q = p.part[(long long)i * p.M + m];
+            a = ce_join(a, CePart{q.x, q.y});
+        }
+    }
+    warps[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && m < p.M) {
+        for (int i = 1; i < 32; ++i) a = ce_join(a, warps[i][lane]);
+        const float lse = isinf(a.r) ? log2f(a.s) * LN2 : fmaf(a.r, LN2, logf(a.s));
+        const long long k = ce_target(p.target, m);
+        float loss = 0.f;
+        if (k >= p.V) {
+            record_error(p.err, DLC_DEVERR_INDEX, (int)m);
+            loss = NAN;
+        } else if (k >= 0) {
+            loss = lse - p.chosen[m];
+        }
+        p.lse[m] = lse;
+        p.loss[m] = loss;
+    }
+}
+
+// dz of a piece, four classes a thread, and its sums over a strip of rows.
+__global__ void __launch_bounds__(CE_THREADS) ce_dz_kernel(const __grid_constant__ CeParams p) {
+    griddep_launch_dependents();
+    const int c = 4 * ((int)blockIdx.x * CE_THREADS + (int)threadIdx.x);
+    griddep_wait();
+    if (c >= p.cols) return;
+    const int n = min(4, p.cols - c);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const long long step = gridDim.y;
+#pragma unroll 2
+    for (long long m = blockIdx.y; m < p.M; m += step) {
+        const float lse = p.lse[m];
+        const long long t = ce_target(p.target, m);
+        const bool counted = t >= 0 && t < p.V;
+        const float d = counted ? p.dloss[m] : 0.f;
+        if (t >= p.V && c == 0) record_error(p.err, DLC_DEVERR_INDEX, (int)m);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *z = p.z + m * p.ld + c;
+        if (n == 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(z);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (i < n) v[i] = z[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float e = p.n0 + c + i == t ? expm1f(v[i] - lse) : exp2_fast((v[i] - lse) * LOG2E);
+            v[i] = counted ? d * e : 0.f;
+            sum[i] += v[i];
+        }
+        unsigned short *dst = p.dz + m * p.ldz + c;  // (rows are padded to whole vectors)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+    if (p.sums) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p.sums[(long long)blockIdx.y * p.cols + c + i] = sum[i];
+    }
+}
+
+// ---- host side -------------------------------------------------------------------------
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Logits (or dz) of a piece take at most about this much workspace.
+constexpr size_t CE_PIECE_BYTES = (size_t)256 << 20;
+
+// Classes of a piece of `bytes`-sized elements a row and class.
+int piece_of(const CrossEntropyProblem &p, int bytes) {
+    const long long most = std::max<long long>(256, (long long)(CE_PIECE_BYTES / (size_t)bytes) / p.M / 256 * 256);
+    return (int)std::min<long long>(p.V, most);
+}
+
+RowTensor dense(void *p, int dt, long long ld) {
+    RowTensor t;
+    t.p = p;
+    t.dt = dt;
+    t.m = RowMap{ld, 0, 0, 1, ld, 1, 1, 1};
+    return t;
+}
+
+// w from class n0 on, `cols` rows of it.
+RowTensor classes(const CrossEntropyProblem &p, int n0, int cols) {
+    RowTensor t = p.w;
+    t.p = static_cast<char *>(p.w.p) + (size_t)n0 * p.K * dlc_dtype_bytes((dlcDataType_t)p.w.dt);
+    t.m.ld = cols > 1 ? p.K : (p.K + 15) / 16 * 16;  // (of one row any pitch)
+    return t;
+}
+
+int segments(int cols) { return (cols + CE_SEGMENT - 1) / CE_SEGMENT; }
+
+// Rows that one pass of ce_dz_kernel's blocks sums up together.
+int strips(const dlcContext *ctx, const CrossEntropyProblem &p, int cols) {
+    const int gx = (cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS);
+    return (int)std::min<long long>(p.M, std::max(1, ctx->sm_count * 8 / gx));
+}
+
+// Where a call keeps what between its kernels (ws null: sizes only).
+struct CePlan {
+    int piece = 0, parts = 0;
+    long long ld = 0, ldz = 0;
+    bool x_packed = false, w_packed = false;
+    void *x_copy = nullptr, *w_copy = nullptr;
+    float *z = nullptr, *chosen = nullptr, *sums = nullptr;
+    float2 *part = nullptr;
+    unsigned short *dz = nullptr;
+    RowTensor dx_sum;          // FP32, where several pieces add to a dx that is none
+    char *gemm_ws = nullptr;
+    size_t bytes = 0;
+    char *base;
+
+    explicit CePlan(char *ws) : base(ws) {}
+    void *take(size_t n) {
+        void *at = base ? base + bytes : (void *)(uintptr_t)256;
+        bytes += round256(n);
+        return at;
+    }
+    void operands(const CrossEntropyProblem &p) {
+        x_packed = dlc_pack_bytes(p.x, p.M, p.K) != 0;
+        w_packed = dlc_pack_bytes(classes(p, 0, p.V), p.V, p.K) != 0;
+        const long long e = dlc_dtype_bytes((dlcDataType_t)p.w.dt), row = (p.K * e + 15) / 16 * 16;
+        if (x_packed) x_copy = take((size_t)p.M * row);
+        if (w_packed) w_copy = take((size_t)piece * row);
+    }
+    RowTensor x(const CrossEntropyProblem &p) const { return x_packed ? dlc_packed(p.x, p.K, x_copy) : p.x; }
+    RowTensor w(const CrossEntropyProblem &p, int n0, int cols) const {
+        const RowTensor t = classes(p, n0, cols);
+        return w_packed ? dlc_packed(t, p.K, w_copy) : t;
+    }
+    // Copies of a piece's operands, where they are wanted.
+    dlcStatus_t pack(dlcContext *ctx, const CrossEntropyProblem &p, int n0, int cols) const {
+        PackItem items[DLC_MAX_PACKS];
+        RowTensor tx = p.x, tw = classes(p, n0, cols);
+        int n = 0;
+        if (x_packed && n0 == 0) items[n++] = PackItem{&tx, p.M, p.K, x_copy};
+        if (w_packed) items[n++] = PackItem{&tw, cols, p.K, w_copy};
+        return dlc_launch_pack(ctx, items, n);
+    }
+    // z = sa sb x w^T + bias of a piece
+    GemmProblem logits(const CrossEntropyProblem &p, int n0, int cols) const {
+        GemmProblem g;
+        g.M = p.M;
+        g.N = cols;
+        g.K = p.K;
+        g.a.t = x(p);
+        g.b.t = w(p, n0, cols);
+        g.sa = p.sa;
+        g.sb = p.sb ? p.sb + n0 : nullptr;
+        g.bias = p.bias ? p.bias + n0 : nullptr;
+        g.y = dense(z, DLC_DATA_FLOAT, ld);
+        g.ws = gemm_ws;
+        return g;
+    }
+    // dx (+)= dz w of a piece; the pieces before it have left their sum in dx_sum or dx
+    GemmProblem data(const CrossEntropyProblem &p, int n0, int cols) const {
+        GemmProblem g;
+        g.M = p.M;
+        g.N = p.K;
+        g.K = cols;
+        g.a.t = dense(dz, DLC_DATA_BFLOAT16, ldz);
+        g.b.t = w(p, n0, cols);
+        g.b.trans = 1;
+        const RowTensor sum = dx_sum.p ? dx_sum : p.dx;
+        g.y = n0 + cols == p.V ? p.dx : sum;
+        if (n0) g.r = sum;
+        g.ws = gemm_ws;
+        return g;
+    }
+    // dw = dz^T x of a piece
+    GemmProblem filters(const CrossEntropyProblem &p, int n0, int cols) const {
+        GemmProblem g;
+        g.M = cols;
+        g.N = p.K;
+        g.K = p.M;
+        g.a.t = dense(dz, DLC_DATA_BFLOAT16, ldz);
+        g.a.trans = 1;
+        g.b.t = x(p);
+        g.b.trans = 1;
+        g.y = p.dw;
+        g.y.p = static_cast<char *>(p.dw.p) + (size_t)n0 * p.K * dlc_dtype_bytes((dlcDataType_t)p.dw.dt);
+        g.y.m.ld = cols > 1 ? p.K : (p.K + 15) / 16 * 16;
+        g.ws = gemm_ws;
+        return g;
+    }
+    // fn(first class, how many, first part) of every piece
+    template <typename Fn>
+    dlcStatus_t each(const CrossEntropyProblem &p, Fn fn) const {
+        for (int n0 = 0, part0 = 0; n0 < p.V;) {
+            const int cols = std::min(piece, p.V - n0);
+            const dlcStatus_t st = fn(n0, cols, part0);
+            if (st != DLC_STATUS_SUCCESS) return st;
+            part0 += segments(cols);
+            n0 += cols;
+        }
+        return DLC_STATUS_SUCCESS;
+    }
+};
+
+CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
+    CePlan f(ws);
+    f.piece = piece_of(p, 4);
+    f.ld = (f.piece + 3) / 4 * 4;
+    f.operands(p);
+    f.z = static_cast<float *>(f.take((size_t)p.M * f.ld * 4));
+    f.each(p, [&](int, int cols, int) { return f.parts += segments(cols), DLC_STATUS_SUCCESS; });
+    f.part = static_cast<float2 *>(f.take((size_t)f.parts * p.M * 8));
+    f.chosen = static_cast<float *>(f.take((size_t)p.M * 4));
+    size_t most = 0;
+    f.each(p, [&](int n0, int cols, int) {
+        most = std::max(most, dlc_gemm_workspace(ctx, f.logits(p, n0, cols)));
+        return DLC_STATUS_SUCCESS;
+    });
+    f.gemm_ws = static_cast<char *>(f.take(most));
+    return f;
+}
+
+CePlan plan_bwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
+    CePlan b(ws);
+    b.piece = piece_of(p, 4);
+    b.ld = (b.piece + 3) / 4 * 4;
+    b.ldz = (b.piece + 7) / 8 * 8;
+    b.operands(p);
+    b.z = static_cast<float *>(b.take((size_t)p.M * b.ld * 4));
+    b.dz = static_cast<unsigned short *>(b.take((size_t)p.M * b.ldz * 2));
+    if (p.dbias) {
+        size_t most = 0;
+        b.each(p, [&](int, int cols, int) { return most = std::max(most, (size_t)strips(ctx, p, cols) * cols * 4), DLC_STATUS_SUCCESS; });
+        b.sums = static_cast<float *>(b.take(most));
+    }
+    if (p.dx.p && b.piece < p.V && p.dx.dt != DLC_DATA_FLOAT) {
+        const long long ld = ((long long)p.K + 3) / 4 * 4;
+        b.dx_sum = dense(b.take((size_t)p.M * ld * 4), DLC_DATA_FLOAT, ld);
+    }
+    size_t most = 0;
+    b.each(p, [&](int n0, int cols, int) {
+        most = std::max(most, dlc_gemm_workspace(ctx, b.logits(p, n0, cols)));
+        if (p.dx.p) most = std::max(most, dlc_gemm_workspace(ctx, b.data(p, n0, cols)));
+        if (p.dw.p) most = std::max(most, dlc_gemm_workspace(ctx, b.filters(p, n0, cols)));
+        return DLC_STATUS_SUCCESS;
+    });
+    b.gemm_ws = static_cast<char *>(b.take(most));
+    return b;
+}
+
+CeParams params(const dlcContext *ctx, const CrossEntropyProblem &p, const CePlan &f) {
+    CeParams c = {};
+    c.M = p.M;
+    c.V = p.V;
+    c.z = f.z;
+    c.ld = f.ld;
+    c.target = p.target;
+    c.part = f.part;
+    c.parts = f.parts;
+    c.chosen = f.chosen;
+    c.loss = p.loss;
+    c.lse = p.lse;
+    c.dloss = p.dloss;
+    c.dz = f.dz;
+    c.ldz = f.ldz;
+    c.sums = f.sums;
+    c.err = ctx->d_err;
+    return c;
+}
+
+}  // namespace
+
+size_t dlc_cross_entropy_workspace(const dlcContext *ctx, const CrossEntropyProblem &p) { return plan_fwd(ctx, p, nullptr).bytes; }
+
+dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem &p) {
+    const CePlan f = plan_fwd(ctx, p, p.ws);
+    CeParams c = params(ctx, p, f);
+    const dlcStatus_t st = f.each(p, [&](int n0, int cols, int part0) {
+        dlcStatus_t s = f.pack(ctx, p, n0, cols);
+        if (s == DLC_STATUS_SUCCESS) s = dlc_launch_gemm(ctx, f.logits(p, n0, cols));
+        if (s != DLC_STATUS_SUCCESS) return s;
+        c.n0 = n0;
+        c.cols = cols;
+        c.part0 = part0;
+        void *args[] = {&c};
+        const unsigned rows = (unsigned)std::min<long long>(p.M, 0x7fffffffLL);
+        return dlc_launch(ctx, (const void *)ce_part_kernel, dim3(rows, (unsigned)segments(cols)), dim3(CE_THREADS), 0, args);
+    });
+    if (st != DLC_STATUS_SUCCESS) return st;
+    void *args[] = {&c};
+    return dlc_launch(ctx, (const void *)ce_loss_kernel, dim3((unsigned)((p.M + 31) / 32)), dim3(1024), 0, args);
+}
+
+size_t dlc_cross_entropy_bwd_workspace(const dlcContext *ctx, const CrossEntropyProblem &p) { return plan_bwd(ctx, p, nullptr).bytes; }
+
+dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProblem &p) {
+    const CePlan b = plan_bwd(ctx, p, p.ws);
+    CeParams c = params(ctx, p, b);
+    return b.each(p, [&](int n0, int cols, int) {
+        dlcStatus_t s = b.pack(ctx, p, n0, cols);
+        if (s == DLC_STATUS_SUCCESS) s = dlc_launch_gemm(ctx, b.logits(p, n0, cols));
+        if (s != DLC_STATUS_SUCCESS) return s;
+        c.n0 = n0;
+        c.cols = cols;
+        const int rows = strips(ctx, p, cols);
+        void *args[] = {&c};
+        s = dlc_launch(ctx, (const void *)ce_dz_kernel, dim3((unsigned)((cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS)), (unsigned)rows),
+                       dim3(CE_THREADS), 0, args);
+        if (s == DLC_STATUS_SUCCESS && p.dbias) s = dlc_launch_column_sum(ctx, b.sums, p.dbias + n0, cols, rows);
+        if (s == DLC_STATUS_SUCCESS && p.dx.p) s = dlc_launch_gemm(ctx, b.data(p, n0, cols));
+        if (s == DLC_STATUS_SUCCESS && p.dw.p) s = dlc_launch_gemm(ctx, b.filters(p, n0, cols));
+        return s;
+    });
+}

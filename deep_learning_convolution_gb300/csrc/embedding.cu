@@ -1,0 +1,619 @@
+// embedding.cu -- rows of a table by token, and the table's gradient.
+//
+//   y[m] = scale * table[token[m]], 0 for a negative token
+//   dtable[v] = (dtable[v]) + scale * sum over m with token[m] = v of dy[m]
+//
+// Forward: a copy with an address a row; bound by memory, or by the launch for few rows.
+//
+// Backward: the tokens are sorted by a stable radix sort (so that the rows of a token stay
+// in order and the FP32 sums are the same every time); blocks then take runs of
+// 32 sorted positions and a slab of channels and add the rows of each token up in
+// registers.  A token whose rows reach over several blocks leaves a partial sum in each,
+// which a last kernel adds in order: a token that is every tenth one costs no more than
+// the others.  Rows of the table that no token names are zeroed beside the sums, by
+// blocks that look at a byte a row; the whole gradient is written once.
+#include "channel.cuh"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace dlc;
+
+constexpr int EM_THREADS = 256;
+
+__device__ __forceinline__ long long token_at(const IndexList &t, long long i) {
+    return t.wide ? static_cast<const long long *>(t.p)[i] : static_cast<const int *>(t.p)[i];
+}
+
+// ---- forward -----------------------------------------------------------------------
+
+struct EmParams {
+    EmbeddingProblem e;
+    long long items;
+    int pieces;  // of a row
+    int *err;
+};
+
+// W = 8: eight channels a piece in 16-byte accesses; W = 1: any layout of y.
+template <int W, typename T, typename Y>
+__global__ void __launch_bounds__(EM_THREADS) embedding_kernel(const __grid_constant__ EmParams p) {
+    griddep_launch_dependents();
+    constexpr int U = W == 8 ? 4 : 8;
+    const long long step = (long long)gridDim.x * EM_THREADS;
+    long long i = (long long)blockIdx.x * EM_THREADS + threadIdx.x;
+    long long row = i / p.pieces;
+    int piece = (int)(i - row * p.pieces);
+    const long long drow = step / p.pieces;
+    const int dpiece = (int)(step - drow * p.pieces);
+    griddep_wait();
+    for (; i < p.items;) {
+        long long token[U], at[U];
+        T v[U][W];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            at[k] = -1;
+            if (i < p.items) {
+                token[k] = token_at(p.e.tokens, row);
+                at[k] = row_off(p.e.y.m, row) + (long long)piece * W * p.e.y.m.cs;
+                const bool there = token[k] >= 0 && token[k] < p.e.V;
+                if (token[k] >= p.e.V && piece == 0) record_error(p.err, DLC_DEVERR_INDEX, (int)min(row, 0x7fffffffLL));
+                const T *src = static_cast<const T *>(p.e.table.p) + (there ? token[k] : 0) * p.e.C + (long long)piece * W;
+                if (there) {
+                    if constexpr (W == 8) {
+#pragma unroll
+                        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                            reinterpret_cast<uint4 *>(v[k])[j] = reinterpret_cast<const uint4 *>(src)[j];
+                    } else {
+                        v[k][0] = src[0];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[k][j] = (T)0;
+                }
+            }
+            i += step, row += drow, piece += dpiece;
+            if (piece >= p.pieces) piece -= p.pieces, ++row;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (at[k] < 0) break;
+            float f[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (sizeof(T) == 2)
+                    f[j] = bf16_bits_f32(v[k][j]) * p.e.scale;
+                else
+                    f[j] = v[k][j] * p.e.scale;
+                if (token[k] < 0 || token[k] >= p.e.V) f[j] = 0.f;  // (whatever the scale)
+            }
+            Y *dst = static_cast<Y *>(p.e.y.p) + at[k];
+            if constexpr (W == 8 && sizeof(Y) == 2) {
+                *reinterpret_cast<uint4 *>(dst) =
+                    make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+            } else if constexpr (W == 8) {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+                store_elem(dst, sizeof(Y) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
+            }
+        }
+    }
+}
+
+// ---- the tokens in order -------------------------------------------------------------
+//
+// Least significant digit first, a digit at most ten bits.  A tile of 2048 tokens keeps its
+// tokens in registers; the histograms of all tiles give every digit's place (the next pass's
+// are counted while this one writes).  Tokens outside the table sort behind all others,
+// as number V.
+
+constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32, SORT_EACH = 4, SORT_TILE = SORT_THREADS * SORT_EACH;
+constexpr int SORT_MAX_BITS = 10, SORT_MAX_DIGITS = 1 << SORT_MAX_BITS;
+
+struct SortParams {
+    IndexList tokens;
+    int rows, V, tiles;
+    int bits, passes;       // of a digit; of the sort
+    int *hist;              // [pass][tile][digit]
+    uint32_t *key[2], *row[2];  // pass p writes the arrays p mod 2
+    unsigned char *named;   // [V]: rows of the table that a token names (null: not wanted)
+    int *err;
+};
+
+struct SortShared {
+    unsigned short count[SORT_WARPS][SORT_MAX_DIGITS];  // of a warp's tokens, then the warps before it
+    int base[SORT_MAX_DIGITS];
+    int sums[SORT_WARPS];
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortParams &p, int i) {
+    const long long t = token_at(p.tokens, i);
+    if (t >= p.V) record_error(p.err, DLC_DEVERR_INDEX, i);
+    return t < 0 || t >= p.V ? (uint32_t)p.V : (uint32_t)t;
+}
+
+// base[d] = the place of this tile's first token of digit d: totals[d] summed over smaller
+// digits, and `before` of them in the tiles ahead.  Two digits a thread.
+__device__ __forceinline__ void sort_places(SortShared &s, const int (&total)[2], const int (&before)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int own = total[0] + total[1];
+    int sum = own;
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) s.sums[warp] = sum;
+    __syncthreads();
+    int start = sum - own;
+    for (int w = 0; w < warp; ++w) start += s.sums[w];
+    s.base[2 * threadIdx.x] = start + before[0];
+    s.base[2 * threadIdx.x + 1] = start + total[0] + before[1];
+}
+
+// Ranks of a tile's tokens among those of the same digit; keys[k] of thread t is the tile's
+// token warp * 128 + 32 k + lane.  Leaves each warp's counts in s.count.
+__device__ __forceinline__ void sort_ranks(SortShared &s, const uint32_t (&keys)[SORT_EACH], const bool (&on)[SORT_EACH], int shift,
+                                           uint32_t mask, int (&rank)[SORT_EACH]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < SORT_EACH; ++k) {
+        const uint32_t d = on[k] ? (keys[k] >> shift) & mask : 0xffffffffu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const uint32_t ahead = peers & ((1u << lane) - 1u);
+        int first = 0;
+        if (on[k]) first = s.count[warp][d];
+        __syncwarp();
+        rank[k] = first + __popc(ahead);
+        if (on[k] && ahead == 0) s.count[warp][d] = (unsigned short)(first + __popc(peers));
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void sort_clear(SortShared &s) {
+    for (int i = threadIdx.x; i < SORT_WARPS * SORT_MAX_DIGITS / 2; i += SORT_THREADS) reinterpret_cast<uint32_t *>(s.count)[i] = 0u;
+    __syncthreads();
+}
+
+// s.count: from each warp's counts to the sum of those of the warps before it; returns the totals.
+__device__ __forceinline__ void sort_warps(SortShared &s, int (&total)[2]) {
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int d = 2 * (int)threadIdx.x + h;
+        int sum = 0;
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            const int c = s.count[w][d];
+            s.count[w][d] = (unsigned short)sum;
+            sum += c;
+        }
+        total[h] = sum;
+    }
+}
+
+struct SortTile {
+    SortShared s;
+    uint32_t key[SORT_TILE], row[SORT_TILE];
+};
+
+// Up to a tile of tokens: all passes by one block.
+__global__ void __launch_bounds__(SORT_THREADS) sort_tile_kernel(const __grid_constant__ SortParams p) {
+    griddep_launch_dependents();
+    extern __shared__ uint4 tile_s[];
+    SortTile &tile = *reinterpret_cast<SortTile *>(tile_s);
+    SortShared &s = tile.s;
+    griddep_wait();
+    if (p.named)
+        for (int i = threadIdx.x; i < (p.V + 15) / 16; i += SORT_THREADS) reinterpret_cast<uint4 *>(p.named)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int first = (int)(threadIdx.x >> 5) * 32 * SORT_EACH + (int)(threadIdx.x & 31);
+    uint32_t key[SORT_EACH], row[SORT_EACH];
+    bool on[SORT_EACH];
+    const uint32_t mask = (1u << p.bits) - 1u;
+#pragma unroll
+    for (int k = 0; k < SORT_EACH; ++k) {
+        row[k] = (uint32_t)(first + 32 * k);
+        on[k] = (int)row[k] < p.rows;
+        key[k] = on[k] ? sort_key(p, (int)row[k]) : 0u;
+    }
+    for (int pass = 0; pass < p.passes; ++pass) {
+        int rank[SORT_EACH], total[2];
+        const int none[2] = {0, 0};
+        sort_clear(s);
+        sort_ranks(s, key, on, pass * p.bits, mask, rank);
+        sort_warps(s, total);
+        sort_places(s, total, none);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < SORT_EACH; ++k)
+            if (on[k]) {
+                const uint32_t d = (key[k] >> (pass * p.bits)) & mask;
+                const int at = s.base[d] + s.count[threadIdx.x >> 5][d] + rank[k];
+                tile.key[at] = key[k];
+                tile.row[at] = row[k];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < SORT_EACH; ++k)
+            if (on[k]) key[k] = tile.key[first + 32 * k], row[k] = tile.row[first + 32 * k];
+    }
+    const int last = (p.passes - 1) & 1;
+#pragma unroll
+    for (int k = 0; k < SORT_EACH; ++k)
+        if (on[k]) {
+            p.key[last][first + 32 * k] = key[k];
+            p.row[last][first + 32 * k] = row[k];
+            if (p.named && key[k] < (uint32_t)p.V) p.named[key[k]] = 1;  // (zeroed above, before barriers)
+        }
+}
+
+// The first pass's histograms; zeroes those of the others, and the named rows.
+__global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_constant__ SortParams p) {
+    griddep_launch_dependents();
+    __shared__ int count[SORT_MAX_DIGITS];
+    const int digits = 1 << p.bits;
+    for (int d = threadIdx.x; d < digits; d += SORT_THREADS) count[d] = 0;
+    __syncthreads();
+    griddep_wait();
+    const long long all = (long long)gridDim.x * SORT_THREADS, me = (long long)blockIdx.x * SORT_THREADS + threadIdx.x;
+    if (p.named)
+        for (long long i = me; i < (p.V + 15) / 16; i += all) reinterpret_cast<uint4 *>(p.named)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const long long per = (long long)p.tiles * digits;
+    for (long long i = per + me; i < per * p.passes; i += all) p.hist[i] = 0;
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+#pragma unroll
+        for (int k = 0; k < SORT_EACH; ++k) {
+            const long long i = (long long)tile * SORT_TILE + k * SORT_THREADS + threadIdx.x;
+            if (i < p.rows) atomicAdd(&count[sort_key(p, (int)i) & (uint32_t)(digits - 1)], 1);
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < digits; d += SORT_THREADS) {
+            p.hist[(long long)tile * digits + d] = count[d];
+            count[d] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_constant__ SortParams p, int pass) {
+    griddep_launch_dependents();
+    __shared__ SortShared s;
+    sort_clear(s);
+    griddep_wait();
+    const int tile = blockIdx.x, digits = 1 << p.bits;
+    const int first = (int)(threadIdx.x >> 5) * 32 * SORT_EACH + (int)(threadIdx.x & 31);
+    uint32_t key[SORT_EACH], row[SORT_EACH];
+    bool on[SORT_EACH];
+#pragma unroll
+    for (int k = 0; k < SORT_EACH; ++k) {
+        const long long i = (long long)tile * SORT_TILE + first + 32 * k;
+        on[k] = i < p.rows;
+        key[k] = row[k] = 0u;
+        if (on[k]) {
+            row[k] = pass == 0 ? (uint32_t)i : p.row[(pass - 1) & 1][i];
+            key[k] = pass == 0 ? sort_key(p, (int)i) : p.key[(pass - 1) & 1][i];
+        }
+    }
+    int rank[SORT_EACH], total[2], all[2] = {0, 0}, before[2] = {0, 0};
+    const uint32_t mask = (uint32_t)digits - 1u;
+    sort_ranks(s, key, on, pass * p.bits, mask, rank);
+    const int *hist = p.hist + (long long)pass * p.tiles * digits;
+    if (2 * (int)threadIdx.x < digits) {
+#pragma unroll 8
+        for (int t = 0; t < p.tiles; ++t) {
+            const int2 c = *reinterpret_cast<const int2 *>(hist + (long long)t * digits + 2 * threadIdx.x);
+            all[0] += c.x, all[1] += c.y;
+            if (t < tile) before[0] += c.x, before[1] += c.y;
+        }
+    }
+    sort_warps(s, total);
+    sort_places(s, all, before);
+    __syncthreads();
+    const bool more = pass + 1 < p.passes;
+#pragma unroll
+    for (int k = 0; k < SORT_EACH; ++k)
+        if (on[k]) {
+            const uint32_t d = (key[k] >> (pass * p.bits)) & mask;
+            const int at = s.base[d] + s.count[threadIdx.x >> 5][d] + rank[k];
+            p.key[pass & 1][at] = key[k];
+            p.row[pass & 1][at] = row[k];
+            if (more)
+                atomicAdd(p.hist + ((long long)(pass + 1) * p.tiles + at / SORT_TILE) * digits + ((key[k] >> ((pass + 1) * p.bits)) & mask), 1);
+            else if (p.named && key[k] < (uint32_t)p.V)
+                p.named[key[k]] = 1;
+        }
+}
+
+// ---- sums by token ---------------------------------------------------------------------
+
+constexpr int SUM_THREADS = 128, SUM_MAX_CHUNK = 128;
+
+struct SumParams {
+    EmbeddingProblem e;        // y: dy; table: dtable
+    const uint32_t *key, *row; // sorted
+    const unsigned char *named;
+    float *part;               // [chunk][2][C]: of the token that comes in, of the one that goes on
+    int chunk, chunks, slabs;  // sorted positions of a chunk
+    int fill_blocks;
+};
+
+template <int W, typename T>
+__device__ __forceinline__ void sum_store(const SumParams &p, uint32_t token, int c, const float (&acc)[W]) {
+    T *dst = static_cast<T *>(p.e.table.p) + (long long)token * p.e.C + c;
+    float f[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) f[j] = acc[j] * p.e.scale;
+    if constexpr (W == 8) {
+        constexpr int Q = (int)sizeof(T) / 2;
+        if (p.e.accumulate) {
+            T old[W];
+#pragma unroll
+            for (int j = 0; j < Q; ++j) reinterpret_cast<uint4 *>(old)[j] = reinterpret_cast<const uint4 *>(dst)[j];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (sizeof(T) == 2)
+                    f[j] += bf16_bits_f32(old[j]);
+                else
+                    f[j] += old[j];
+            }
+        }
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4 *>(dst) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        } else {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    } else {
+        constexpr int dt = sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT;
+        if (p.e.accumulate) f[0] += load_elem(dst, dt, 0);
+        store_elem(dst, dt, 0, f[0]);
+    }
+}
+
+// W = 8: 16-byte accesses of dy and of the table; W = 1: any layout of dy, any size.
+template <int W, typename D, typename T>
+__global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid_constant__ SumParams p) {
+    griddep_launch_dependents();
+    __shared__ uint32_t key_s[SUM_MAX_CHUNK + 2], row_s[SUM_MAX_CHUNK];
+    const int C = p.e.C;
+    griddep_wait();
+    if ((int)blockIdx.x >= p.chunks * p.slabs) {  // rows that no token names: a warp 32 rows at a time
+        const int lane = threadIdx.x & 31;
+        const long long warps = (long long)p.fill_blocks * (SUM_THREADS / 32);
+        for (long long v0 = 32 * ((long long)(blockIdx.x - p.chunks * p.slabs) * (SUM_THREADS / 32) + (threadIdx.x >> 5)); v0 < p.e.V;
+             v0 += 32 * warps) {
+            uint32_t todo = __ballot_sync(0xffffffffu, v0 + lane < p.e.V && p.named[v0 + lane] == 0);
+            for (; todo; todo &= todo - 1u) {
+                T *dst = static_cast<T *>(p.e.table.p) + (v0 + __ffs((int)todo) - 1) * C;
+                if constexpr (W == 8) {
+                    for (int c = lane; c < C * (int)sizeof(T) / 16; c += 32) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    for (int c = lane; c < C; c += 32) dst[c] = (T)0;
+                }
+            }
+        }
+        return;
+    }
+    const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
+    const int n = min(p.chunk, (int)p.e.rows - chunk * p.chunk);
+    const long long first = (long long)chunk * p.chunk;
+    for (int i = threadIdx.x; i < n; i += SUM_THREADS) {
+        key_s[1 + i] = p.key[first + i];
+        row_s[i] = p.row[first + i];
+    }
+    if (threadIdx.x == 0) {
+        key_s[0] = chunk ? p.key[first - 1] : 0xffffffffu;
+        key_s[1 + n] = first + n < p.e.rows ? p.key[first + n] : 0xffffffffu;
+    }
+    __syncthreads();
+    const int c = (slab * SUM_THREADS + (int)threadIdx.x) * W;
+    if (c >= C) return;
+    const long long co = c * p.e.y.m.cs;
+    float acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+    constexpr int U = W == 8 ? (sizeof(D) == 2 ? 8 : 4) : 8;  // rows in flight
+    int begin = 0;  // of the token at hand
+    for (int i0 = 0; i0 < n; i0 += U) {
+        D v[U][W];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k < n && key_s[1 + i0 + k] < (uint32_t)p.e.V) {
+                const D *src = static_cast<const D *>(p.e.y.p) + row_off(p.e.y.m, row_s[i0 + k]) + co;
+                if constexpr (W == 8) {
+#pragma unroll
+                    for (int j = 0; j < (int)sizeof(D) / 2; ++j) reinterpret_cast<uint4 *>(v[k])[j] = reinterpret_cast<const uint4 *>(src)[j];
+                } else {
+                    v[k][0] = src[0];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k;
+            if (i >= n) break;
+            const uint32_t token = key_s[1 + i];
+            if (token >= (uint32_t)p.e.V) return;  // tokens outside the table: the last ones
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (sizeof(D) == 2)
+                    acc[j] += bf16_bits_f32(v[k][j]);
+                else
+                    acc[j] += v[k][j];
+            }
+            const bool ends = key_s[2 + i] != token;
+            if (!ends && i + 1 < n) continue;
+            const bool comes = begin == 0 && key_s[0] == token;
+            if (ends && !comes) {
+                sum_store<W, T>(p, token, c, acc);
+            } else {
+                float *dst = p.part + ((long long)chunk * 2 + (comes ? 0 : 1)) * C + c;
+#pragma unroll
+                for (int j = 0; j < W; ++j) dst[j] = acc[j];
+            }
+            begin = i + 1;
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j] = 0.f;
+        }
+    }
+}
+
+// Tokens whose rows reach over several chunks: the block of the chunk where they begin adds
+// up the partial sums in order.
+template <int W, typename T>
+__global__ void __launch_bounds__(SUM_THREADS) embedding_join_kernel(const __grid_constant__ SumParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
+    const long long end = (long long)(chunk + 1) * p.chunk;  // (the last chunk has no block)
+    const uint32_t token = p.key[end - 1];
+    if (token >= (uint32_t)p.e.V || p.key[end] != token) return;
+    if (chunk && p.key[end - p.chunk] == token && p.key[end - p.chunk - 1] == token) return;  // begins further ahead
+    int more = 0;  // chunks after this one that the token begins
+    for (;;) {
+        const int k = chunk + 1 + more + (int)threadIdx.x;
+        const int found = __syncthreads_count(k < p.chunks && p.key[(long long)k * p.chunk] == token);
+        more += found;
+        if (found < SUM_THREADS) break;
+    }
+    const int c = (slab * SUM_THREADS + (int)threadIdx.x) * W;
+    if (c >= p.e.C) return;
+    const float *src = p.part + ((long long)chunk * 2 + 1) * p.e.C + c;
+    float acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = src[j];
+    src += p.e.C;  // the next chunk's first slot
+#pragma unroll 8
+    for (int k = 0; k < more; ++k) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] += src[(long long)k * 2 * p.e.C + j];
+    }
+    sum_store<W, T>(p, token, c, acc);
+}
+
+// ---- host side -----------------------------------------------------------------------
+
+using Half = unsigned short;
+
+template <int W, typename T>
+const void *fwd_kernel(int y) {
+    return y == DLC_DATA_BFLOAT16 ? (const void *)embedding_kernel<W, T, Half> : (const void *)embedding_kernel<W, T, float>;
+}
+
+template <int W, typename D>
+const void *sum_kernel(int t) {
+    return t == DLC_DATA_BFLOAT16 ? (const void *)embedding_sum_kernel<W, D, Half> : (const void *)embedding_sum_kernel<W, D, float>;
+}
+
+template <int W>
+const void *join_kernel(int t) {
+    return t == DLC_DATA_BFLOAT16 ? (const void *)embedding_join_kernel<W, Half> : (const void *)embedding_join_kernel<W, float>;
+}
+
+bool vectors(const EmbeddingProblem &e) {
+    return e.C % 8 == 0 && (uintptr_t)e.table.p % 16 == 0 && e.y.m.cs == 1 && dlc_aligned_rows(e.y, 16);
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+struct BwdPlan {
+    int bits, passes, tiles, chunk, chunks;
+    size_t hist, key[2], row[2], named, part, bytes;
+};
+
+BwdPlan plan_bwd(long long rows, int C, int V) {
+    BwdPlan b;
+    int bits = 1;
+    while (bits < 31 && (V >> bits) > 0) ++bits;  // tokens 0 .. V
+    b.passes = (bits + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
+    b.bits = (bits + b.passes - 1) / b.passes;
+    b.tiles = (int)((rows + SORT_TILE - 1) / SORT_TILE);
+    // long lists: fewer partial sums of a frequent token to join
+    b.chunk = rows > 65536 ? SUM_MAX_CHUNK : 32;
+    b.chunks = (int)((rows + b.chunk - 1) / b.chunk);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round256(bytes);
+        return at;
+    };
+    b.hist = take((size_t)b.passes * b.tiles * (1u << b.bits) * 4);
+    for (int i = 0; i < 2; ++i) b.key[i] = take((size_t)rows * 4), b.row[i] = take((size_t)rows * 4);
+    b.named = take((size_t)V + 16);
+    b.part = take((size_t)b.chunks * 2 * C * 4);
+    b.bytes = off;
+    return b;
+}
+
+}  // namespace
+
+dlcStatus_t dlc_launch_embedding(dlcContext *ctx, const EmbeddingProblem &e) {
+    EmParams p;
+    p.e = e;
+    p.err = ctx->d_err;
+    const bool w8 = vectors(e);
+    p.pieces = w8 ? e.C / 8 : e.C;
+    p.items = e.rows * p.pieces;
+    const bool bf = e.table.dt == DLC_DATA_BFLOAT16;
+    const void *kern = w8 ? (bf ? fwd_kernel<8, Half>(e.y.dt) : fwd_kernel<8, float>(e.y.dt))
+                          : (bf ? fwd_kernel<1, Half>(e.y.dt) : fwd_kernel<1, float>(e.y.dt));
+    const long long blocks = std::min<long long>((p.items + EM_THREADS - 1) / EM_THREADS, (long long)ctx->sm_count * 8);
+    void *args[] = {&p};
+    return dlc_launch(ctx, kern, dim3((unsigned)blocks), dim3(EM_THREADS), 0, args);
+}
+
+size_t dlc_embedding_bwd_workspace(const dlcContext *, long long rows, int C, int V) { return plan_bwd(rows, C, V).bytes; }
+
+dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e) {
+    const BwdPlan b = plan_bwd(e.rows, e.C, e.V);
+    SortParams s;
+    s.tokens = e.tokens;
+    s.rows = (int)e.rows;
+    s.V = e.V;
+    s.tiles = b.tiles;
+    s.bits = b.bits;
+    s.passes = b.passes;
+    s.hist = reinterpret_cast<int *>(e.ws + b.hist);
+    for (int i = 0; i < 2; ++i) {
+        s.key[i] = reinterpret_cast<uint32_t *>(e.ws + b.key[i]);
+        s.row[i] = reinterpret_cast<uint32_t *>(e.ws + b.row[i]);
+    }
+    s.named = e.accumulate ? nullptr : reinterpret_cast<unsigned char *>(e.ws + b.named);
+    s.err = ctx->d_err;
+    dlcStatus_t st;
+    if (b.tiles == 1) {
+        void *args[] = {&s};
+        if (!dlc_allow_smem(ctx, (const void *)sort_tile_kernel, sizeof(SortTile))) return DLC_STATUS_EXECUTION_FAILED;
+        st = dlc_launch(ctx, (const void *)sort_tile_kernel, dim3(1), dim3(SORT_THREADS), sizeof(SortTile), args);
+        if (st != DLC_STATUS_SUCCESS) return st;
+    } else {
+        void *args[] = {&s};
+        const unsigned blocks = (unsigned)std::max(std::min(b.tiles, ctx->sm_count * 4), std::min(ctx->sm_count, (e.V >> 14) + 1));
+        st = dlc_launch(ctx, (const void *)sort_count_kernel, dim3(blocks), dim3(SORT_THREADS), 0, args);
+        for (int pass = 0; pass < b.passes && st == DLC_STATUS_SUCCESS; ++pass) {
+            void *pargs[] = {&s, &pass};
+            st = dlc_launch(ctx, (const void *)sort_pass_kernel, dim3((unsigned)b.tiles), dim3(SORT_THREADS), 0, pargs);
+        }
+        if (st != DLC_STATUS_SUCCESS) return st;
+    }
+    SumParams p;
+    p.e = e;
+    p.key = s.key[(b.passes - 1) & 1];
+    p.row = s.row[(b.passes - 1) & 1];
+    p.named = s.named;
+    p.part = reinterpret_cast<float *>(e.ws + b.part);
+    p.chunk = b.chunk;
+    p.chunks = b.chunks;
+    const bool w8 = vectors(e);
+    const int slab = SUM_THREADS * (w8 ? 8 : 1);
+    p.slabs = (e.C + slab - 1) / slab;
+    p.fill_blocks = e.accumulate ? 0 : (int)std::min<long long>((e.V + 127) / 128, (long long)ctx->sm_count * 8);
+    if ((long long)p.chunks * p.slabs + p.fill_blocks > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    const bool bf = e.y.dt == DLC_DATA_BFLOAT16;
+    const void *sum = w8 ? (bf ? sum_kernel<8, Half>(e.table.dt) : sum_kernel<8, float>(e.table.dt))
+                         : (bf ? sum_kernel<1, Half>(e.table.dt) : sum_kernel<1, float>(e.table.dt));
+    void *args[] = {&p};
+    st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs + p.fill_blocks)), dim3(SUM_THREADS), 0, args);
+    if (st != DLC_STATUS_SUCCESS || p.chunks == 1) return st;
+    const void *join = w8 ? join_kernel<8>(e.table.dt) : join_kernel<1>(e.table.dt);
+    return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3(SUM_THREADS), 0, args);
+}

@@ -237,6 +237,13 @@ struct RowTensor {
     RowMap m = {0, 0, 0, 1, 0, 1, 1, 1};
 };
 
+// Whether every row of t starts on a boundary of `bytes`.
+inline bool dlc_aligned_rows(const RowTensor &t, long long bytes) {
+    const long long e = dlc_dtype_bytes((dlcDataType_t)t.dt);
+    auto mult = [&](long long s) { return (s * e) % bytes == 0; };
+    return (uintptr_t)t.p % bytes == 0 && (t.m.uniform ? mult(t.m.ld) : (mult(t.m.s0) && mult(t.m.s2) && mult(t.m.s3)));
+}
+
 // RMS norm, forward and backward (validated by the API layer).
 struct RmsProblem {
     long long rows;
@@ -255,6 +262,67 @@ struct RmsBwdProblem {
     const float *gamma;
     float *dgamma;            // or null
     float *ws;                // per-block partial sums of dgamma
+};
+
+// Layer norm, forward and backward (validated by the API layer).
+struct LayerProblem {
+    long long rows;
+    int C;
+    float eps;
+    RowTensor x, r, t, y;      // as in RmsProblem
+    const float *gamma, *beta; // beta may be null
+    float *scale;
+};
+
+struct LayerBwdProblem {
+    long long rows;
+    int C;
+    float eps;
+    RowTensor dy, t, dt, dx;
+    const float *gamma;
+    float *dgamma, *dbeta;     // or null
+    float *ws;                 // per-block partial sums of both
+};
+
+// Dropout: y = r + keep(m, c) ? scale * x : 0 (validated by the API layer).
+struct DropoutProblem {
+    long long rows;
+    int C;
+    uint32_t border;           // words from this on keep their element
+    float scale;
+    RowTensor x, r, y;
+    const unsigned long long *random;  // seed, step (device memory)
+};
+
+// Token or class numbers of the rows, 32 or 64 bits.
+struct IndexList {
+    const void *p = nullptr;
+    int wide = 0;
+};
+
+// Rows of a table (validated by the API layer).  Backward: dtable (in `table`).
+struct EmbeddingProblem {
+    long long rows;
+    int C, V;
+    float scale;
+    int accumulate;
+    IndexList tokens;
+    RowTensor table, y;
+    char *ws;
+};
+
+// Softmax cross entropy on top of z = sa sb x w^T + bias (validated by the API layer).
+struct CrossEntropyProblem {
+    long long M = 0;
+    int V = 0, K = 0;
+    RowTensor x, w;                   // w: V rows of K
+    const float *sa = nullptr, *sb = nullptr, *bias = nullptr;
+    IndexList target;
+    float *loss = nullptr, *lse = nullptr;      // backward: lse is read
+    const float *dloss = nullptr;
+    RowTensor dx, dw;                 // absent where not wanted
+    float *dbias = nullptr;
+    char *ws = nullptr;
 };
 
 // An operand of a product: element (i, k) is row i, channel k of the tensor, or
@@ -306,6 +374,23 @@ size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p);
 dlcStatus_t dlc_launch_act_grad(dlcContext *ctx, const ActGradProblem &p);
 // out[c] = sum_b ws[b * C + c] in a fixed order (rmsnorm.cu)
 dlcStatus_t dlc_launch_column_sum(dlcContext *ctx, const float *ws, float *out, int C, int blocks);
+// the same for rows of [C, C] partial sums and two outputs, each of which may be null
+dlcStatus_t dlc_launch_column_sums(dlcContext *ctx, const float *ws, float *out, float *out2, int C, int blocks);
+// layernorm.cu
+dlcStatus_t dlc_launch_layer(dlcContext *ctx, const LayerProblem &p);
+size_t dlc_layer_bwd_workspace(const dlcContext *ctx, long long rows, int C);
+dlcStatus_t dlc_launch_layer_bwd(dlcContext *ctx, const LayerBwdProblem &p);
+// dropout.cu
+dlcStatus_t dlc_launch_dropout(dlcContext *ctx, const DropoutProblem &p);
+// embedding.cu
+dlcStatus_t dlc_launch_embedding(dlcContext *ctx, const EmbeddingProblem &p);
+size_t dlc_embedding_bwd_workspace(const dlcContext *ctx, long long rows, int C, int V);
+dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &p);
+// cross_entropy.cu
+size_t dlc_cross_entropy_workspace(const dlcContext *ctx, const CrossEntropyProblem &p);
+dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem &p);
+size_t dlc_cross_entropy_bwd_workspace(const dlcContext *ctx, const CrossEntropyProblem &p);
+dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProblem &p);
 // rmsnorm.cu
 dlcStatus_t dlc_launch_rms(dlcContext *ctx, const RmsProblem &p);
 size_t dlc_rms_bwd_workspace(const dlcContext *ctx, const RmsBwdProblem &p);

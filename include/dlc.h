@@ -1,7 +1,8 @@
 /*
  * dlc.h -- C ABI of the GB300 (sm_103a) 2-D convolution library: the forward
  * convolution, its two backward routines, pooling and activation forward, and
- * the channel operators (RMS norm, linear and gated layers) with their gradients.
+ * the channel operators (RMS and layer norm, linear and gated layers, dropout,
+ * embedding, softmax cross entropy) with their gradients.
  *
  * The forward (FPROP) convolution layer is
  *
@@ -37,7 +38,7 @@
  *  - Sizes and strides are in elements, not bytes.
  *  - Calls that launch work are asynchronous on the handle's stream.  Launch
  *    errors are reported by the call itself.  Errors that kernels detect on
- *    the device (a pipeline wait that ran out of time) are recorded in the
+ *    the device (a pipeline wait that ran out of time, a token beyond its table) are recorded in the
  *    handle and reported as DLC_STATUS_EXECUTION_FAILED by the next launching
  *    call on that handle and by dlcSynchronize(), which clears them.
  *  - The library allocates no device memory on any forward or backward call.
@@ -170,10 +171,17 @@ typedef enum {
                                      streamed by every warp */
 } dlcKernel_t;
 
+/* Storage of token and class numbers. */
+typedef enum {
+    DLC_INDEX_INT32 = 0,
+    DLC_INDEX_INT64 = 1
+} dlcIndexType_t;
+
 /* Device error codes recorded by kernels (dlcGetLastDeviceError). */
 typedef enum {
     DLC_DEVERR_NONE = 0,
-    DLC_DEVERR_WAIT_TIMEOUT = 1   /* a pipeline barrier wait ran out of time */
+    DLC_DEVERR_WAIT_TIMEOUT = 1,  /* a pipeline barrier wait ran out of time */
+    DLC_DEVERR_INDEX = 2          /* a token or class number beyond the table (detail: its row) */
 } dlcDeviceError_t;
 
 typedef struct dlcContext *dlcHandle_t;
@@ -229,7 +237,7 @@ dlcStatus_t dlcGetDeterministic(dlcHandle_t handle, int *deterministic);
 dlcStatus_t dlcSynchronize(dlcHandle_t handle);
 
 /* Synchronizes, then writes the last recorded device error code
- * (dlcDeviceError_t) and its detail word (which wait gave up) and clears
+ * (dlcDeviceError_t) and its detail word (which wait gave up, which row) and clears
  * them. */
 dlcStatus_t dlcGetLastDeviceError(dlcHandle_t handle, int *code, int *detail);
 
@@ -657,6 +665,133 @@ dlcStatus_t dlcGetGatedBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescri
                                              dlcTensorDescriptor_t zDesc,
                                              dlcTensorDescriptor_t dyDesc, const void *dy,
                                              size_t *bytes);
+
+/* ---- channel operators at a network's ends and between its layers ---------------
+ *
+ * Layer norm, dropout, the embedding of tokens and softmax cross entropy on top
+ * of a linear layer, with their gradients.  What is said above of the channel
+ * operators (rows, layouts, types, workspaces, reproducibility, capture) holds
+ * here too.  No counterpart on the pages.
+ *
+ * Tokens, and the classes that are the targets of a loss, are dense arrays of
+ * one number a row in order n, h, w, 32 or 64 bits wide (dlcIndexType_t) and
+ * aligned to that.  A negative one stands for none (a padded row); one beyond
+ * the last row of the table counts as none as well, and the kernel records
+ * DLC_DEVERR_INDEX with the row, which dlcSynchronize and the handle's next
+ * call report.  These calls take up to 2^31 - 1 rows, the layer norm more.
+ */
+
+/* total = x + residual;  with mean and variance over the channels of a row,
+ *   y = gamma * (total - mean) / sqrt(variance + epsilon) + beta
+ * from the unrounded total; the variance is the mean square about the mean.
+ * beta (FLOAT, one per channel) may be NULL: zeros.  Types, E4M3 rows with their
+ * scale, in-place total, NaN and FP32 range as for dlcRmsNormForward (the sum of
+ * squares being that about the mean); a row of equal channels with epsilon 0 is
+ * 0 / 0, NaN, in every type. */
+dlcStatus_t dlcLayerNormForward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t xDesc,
+                                const void *x, dlcTensorDescriptor_t residualDesc,
+                                const void *residual, const float *gamma, const float *beta,
+                                dlcTensorDescriptor_t totalDesc, void *total,
+                                dlcTensorDescriptor_t yDesc, void *y, float *scale);
+
+/* Workspace of dlcLayerNormBackward when dgamma or dbeta is wanted (0 bytes
+ * otherwise). */
+dlcStatus_t dlcGetLayerNormBackwardWorkspaceSize(dlcHandle_t handle,
+                                                 dlcTensorDescriptor_t totalDesc, size_t *bytes);
+
+/* Gradient of the layer norm at total, which is also that of x and of residual:
+ * with n = (total - mean) rho, rho = 1 / sqrt(variance + epsilon), d = dy gamma,
+ *   dx = dtotal + rho * (d - mean(d) - n * mean(d n))
+ *   dgamma = sum over rows of dy * n;  dbeta = sum over rows of dy
+ * dtotal, dgamma and dbeta are optional; dx may be dtotal in place.  Tensors FLOAT
+ * or BFLOAT16 independently. */
+dlcStatus_t dlcLayerNormBackward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t dyDesc,
+                                 const void *dy, dlcTensorDescriptor_t totalDesc,
+                                 const void *total, const float *gamma,
+                                 dlcTensorDescriptor_t dtotalDesc, const void *dtotal,
+                                 dlcTensorDescriptor_t dxDesc, void *dx, float *dgamma,
+                                 float *dbeta, void *workspace, size_t workspaceBytes);
+
+/* y = residual + (keep ? x * scale : 0): every element is dropped with the
+ * probability floor(probability * 2^32) / 2^32, 0 <= probability < 1, the others
+ * are scaled by the inverse of what is kept.  What is dropped counts as 0, NaN and
+ * infinity too.  residual is optional; x, residual and y: FLOAT or BFLOAT16
+ * independently; y may be x or residual in place (same descriptor values).
+ *
+ * random: two 64-bit words in device memory, a seed and a step, read when the
+ * kernel runs, so that a captured graph drops anew when they are changed between its
+ * replays.  Element (row m, channel c) is kept where word c mod 4 of Philox
+ * 4x32-10 (Salmon et al., 2011; key: the seed's low and high word; counter: c / 4,
+ * m, the step's low and high word) is at least floor(probability * 2^32).  The
+ * mask depends on nothing else, not on layout or type, and is not stored: the
+ * backward call works it out again from the same words. */
+dlcStatus_t dlcDropoutForward(dlcHandle_t handle, double probability, const uint64_t *random,
+                              dlcTensorDescriptor_t xDesc, const void *x,
+                              dlcTensorDescriptor_t residualDesc, const void *residual,
+                              dlcTensorDescriptor_t yDesc, void *y);
+
+/* dx = keep ? dy * scale : 0 with the same mask (the residual's gradient is dy);
+ * dx may be dy in place. */
+dlcStatus_t dlcDropoutBackward(dlcHandle_t handle, double probability, const uint64_t *random,
+                               dlcTensorDescriptor_t dyDesc, const void *dy,
+                               dlcTensorDescriptor_t dxDesc, void *dx);
+
+/* y[m] = scale * table[tokens[m]], zeros for a token that stands for none.  table:
+ * V rows of C channels ([V, C, 1, 1]); y: rows of C channels; FLOAT or BFLOAT16
+ * independently.  scale is finite. */
+dlcStatus_t dlcEmbeddingForward(dlcHandle_t handle, double scale, dlcIndexType_t indexType,
+                                const void *tokens, dlcFilterDescriptor_t tableDesc,
+                                const void *table, dlcTensorDescriptor_t yDesc, void *y);
+
+dlcStatus_t dlcGetEmbeddingBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t dyDesc,
+                                                 dlcFilterDescriptor_t dtableDesc, size_t *bytes);
+
+/* dtable[v] = scale * (sum of dy over the rows whose token is v, in FP32 and always in
+ * the same order); rows of no token become zero.  With accumulate != 0 this is added
+ * to what dtable holds (a table shared with another layer, several batches), and rows
+ * of no token are neither read nor written. */
+dlcStatus_t dlcEmbeddingBackward(dlcHandle_t handle, double scale, dlcIndexType_t indexType,
+                                 const void *tokens, dlcTensorDescriptor_t dyDesc, const void *dy,
+                                 int accumulate, dlcFilterDescriptor_t dtableDesc, void *dtable,
+                                 void *workspace, size_t workspaceBytes);
+
+/* Softmax cross entropy of the classes that a linear layer rates: with z as in
+ * dlcLinearForward (x and w: both BFLOAT16, or both FLOAT8_E4M3 with scales; w holds one
+ * filter a class; bias optional),
+ *   lse[m] = log sum_k exp z[m, k];  loss[m] = lse[m] - z[m, target[m]]
+ * loss[m] is 0 for a target that stands for none, and NaN for one beyond the last
+ * class.  loss and lse: FLOAT, one per row.  The logits are worked out in pieces and
+ * not kept.  A class with z = -inf (a bias of -inf) has probability 0; a row of
+ * nothing else has lse = -inf and no loss (NaN). */
+dlcStatus_t dlcCrossEntropyForward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                                   const float *xScale, dlcFilterDescriptor_t wDesc, const void *w,
+                                   const float *wScale, const float *bias,
+                                   dlcIndexType_t indexType, const void *target, float *loss,
+                                   float *lse, void *workspace, size_t workspaceBytes);
+
+dlcStatus_t dlcGetCrossEntropyForwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                                   const void *x, dlcFilterDescriptor_t wDesc,
+                                                   const void *w, size_t *bytes);
+
+/* Gradients of sum_m dloss[m] * loss[m] (dloss: FLOAT, one per row; the weight that
+ * a mean over the rows gives each), from what the forward call wrote to lse:
+ *   dz[m, k] = dloss[m] * (exp(z[m, k] - lse[m]) - (k == target[m]))
+ *   dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz
+ * dz is 0 for rows whose target stands for none, whatever dloss is.  x and w: BFLOAT16; dz
+ * enters the products rounded to BFLOAT16, dbias sums its FP32 values; dx and dw:
+ * FLOAT or BFLOAT16 independently; dx, dw and dbias are each optional, one at least is
+ * wanted. */
+dlcStatus_t dlcCrossEntropyBackward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,
+                                    dlcFilterDescriptor_t wDesc, const void *w, const float *bias,
+                                    dlcIndexType_t indexType, const void *target, const float *lse,
+                                    const float *dloss, dlcTensorDescriptor_t dxDesc, void *dx,
+                                    dlcFilterDescriptor_t dwDesc, void *dw, float *dbias,
+                                    void *workspace, size_t workspaceBytes);
+
+/* Workspace for any subset of the three gradients. */
+dlcStatus_t dlcGetCrossEntropyBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescriptor_t xDesc,
+                                                    const void *x, dlcFilterDescriptor_t wDesc,
+                                                    const void *w, size_t *bytes);
 
 /* ---- self test of the device error path ---------------------------------- */
 
