@@ -186,8 +186,10 @@ __global__ void __launch_bounds__(CE_THREADS) ce_dz_kernel(const __grid_constant
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Logits (or dz) of a piece take at most about this much workspace.
-constexpr size_t CE_PIECE_BYTES = (size_t)256 << 20;
+// Logits (or dz) of a piece take at most about this much workspace.  Backward passes of 4096 x
+// 2048 -> 131072 / 8192 x 512 -> 65536 in pieces of 128 MB: 4022 / 1533 us, 256 MB 3913 / 1345,
+// 512 MB 3836 / 1230, 1 GB 3893 / 1097: what a piece costs is dx's last wave and its FP32 sum.
+constexpr size_t CE_PIECE_BYTES = (size_t)512 << 20;
 
 // Classes of a piece of `bytes`-sized elements a row and class.
 int piece_of(const CrossEntropyProblem &p, int bytes) {
@@ -213,14 +215,16 @@ RowTensor classes(const CrossEntropyProblem &p, int n0, int cols) {
 
 int segments(int cols) { return (cols + CE_SEGMENT - 1) / CE_SEGMENT; }
 
-// Rows that one pass of ce_dz_kernel's blocks sums up together.
-int strips(const dlcContext *ctx, const CrossEntropyProblem &p, int cols) {
+// How many partial sums dbias has: strips of rows, each summed up by one block or warp.
+int strips(const dlcContext *ctx, const CrossEntropyProblem &p, bool fused, int cols) {
+    if (fused) return (int)((p.M + 31) / 32);
     const int gx = (cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS);
     return (int)std::min<long long>(p.M, std::max(1, ctx->sm_count * 8 / gx));
 }
 
 // Where a call keeps what between its kernels (ws null: sizes only).
 struct CePlan {
+    bool fused = false;        // the product's epilogue takes the logits from the accumulators
     int piece = 0, parts = 0;
     long long ld = 0, ldz = 0;
     bool x_packed = false, w_packed = false;
@@ -306,62 +310,90 @@ struct CePlan {
         g.ws = gemm_ws;
         return g;
     }
-    // fn(first class, how many, first part) of every piece
+    // the same product with the loss's epilogue
+    GemmProblem fused_logits(const CrossEntropyProblem &p, int mode, int n0, int cols, int part0) const {
+        GemmProblem g = logits(p, n0, cols);
+        g.y = mode == ENTROPY_DZ ? dense(dz, DLC_DATA_BFLOAT16, ldz) : RowTensor();
+        EntropyTile &e = g.entropy;
+        e.mode = mode;
+        e.V = p.V;
+        e.n0 = n0;
+        e.target = p.target;
+        e.part = part;
+        e.part0 = part0;
+        e.chosen = chosen;
+        e.lse = p.lse;
+        e.dloss = p.dloss;
+        e.sums = sums;
+        return g;
+    }
+    // fn(first class, how many) of every piece
     template <typename Fn>
     dlcStatus_t each(const CrossEntropyProblem &p, Fn fn) const {
-        for (int n0 = 0, part0 = 0; n0 < p.V;) {
-            const int cols = std::min(piece, p.V - n0);
-            const dlcStatus_t st = fn(n0, cols, part0);
+        for (int n0 = 0; n0 < p.V; n0 += piece) {
+            const dlcStatus_t st = fn(n0, std::min(piece, p.V - n0));
             if (st != DLC_STATUS_SUCCESS) return st;
-            part0 += segments(cols);
-            n0 += cols;
         }
         return DLC_STATUS_SUCCESS;
     }
+    int parts_of(const dlcContext *ctx, const CrossEntropyProblem &p, int n0, int cols) const {
+        return fused ? dlc_entropy_parts(ctx, fused_logits(p, ENTROPY_PARTS, n0, cols, 0)) : segments(cols);
+    }
 };
+
+// Whether the pair kernel's epilogue takes the logits from its accumulators.  For a few rows the
+// filters' stream decides, which the few-row kernels carry better than tiles of 256 rows do,
+// and FP32 logits are little beside it: 4096 -> 131072 forward, 1 row 162 us with logits in
+// memory, 295 fused; 16 rows 169 and 179; 32 rows 176 and 179; 48 rows 184 and 182; 96 rows
+// 200 and 185; more rows far apart (4096 x 2048 -> 131072 1793 and 1084 us), few classes alike
+// (2048 -> 1000: 32 rows 9.8 and 10.3 us, 64 rows 10.3 and 10.5, 256 rows 12.7 and 10.5).
+bool fuse(const CrossEntropyProblem &p) { return p.M > 32; }
 
 CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan f(ws);
-    f.piece = piece_of(p, 4);
-    f.ld = (f.piece + 3) / 4 * 4;
+    f.fused = fuse(p);
+    f.piece = f.fused ? p.V : piece_of(p, 4);
     f.operands(p);
-    f.z = static_cast<float *>(f.take((size_t)p.M * f.ld * 4));
-    f.each(p, [&](int, int cols, int) { return f.parts += segments(cols), DLC_STATUS_SUCCESS; });
-    f.part = static_cast<float2 *>(f.take((size_t)f.parts * p.M * 8));
-    f.chosen = static_cast<float *>(f.take((size_t)p.M * 4));
+    if (!f.fused) {
+        f.ld = (f.piece + 3) / 4 * 4;
+        f.z = static_cast<float *>(f.take((size_t)p.M * f.ld * 4));
+    }
     size_t most = 0;
-    f.each(p, [&](int n0, int cols, int) {
-        most = std::max(most, dlc_gemm_workspace(ctx, f.logits(p, n0, cols)));
+    f.each(p, [&](int n0, int cols) {
+        f.parts += f.parts_of(ctx, p, n0, cols);
+        most = std::max(most, dlc_gemm_workspace(ctx, f.fused ? f.fused_logits(p, ENTROPY_PARTS, n0, cols, 0) : f.logits(p, n0, cols)));
         return DLC_STATUS_SUCCESS;
     });
+    f.part = static_cast<float2 *>(f.take((size_t)f.parts * p.M * 8));
+    f.chosen = static_cast<float *>(f.take((size_t)p.M * 4));
     f.gemm_ws = static_cast<char *>(f.take(most));
     return f;
 }
 
 CePlan plan_bwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan b(ws);
-    b.piece = piece_of(p, 4);
-    b.ld = (b.piece + 3) / 4 * 4;
+    b.fused = fuse(p);
+    b.piece = piece_of(p, b.fused ? 2 : 4);
     b.ldz = (b.piece + 7) / 8 * 8;
     b.operands(p);
-    b.z = static_cast<float *>(b.take((size_t)p.M * b.ld * 4));
-    b.dz = static_cast<unsigned short *>(b.take((size_t)p.M * b.ldz * 2));
-    if (p.dbias) {
-        size_t most = 0;
-        b.each(p, [&](int, int cols, int) { return most = std::max(most, (size_t)strips(ctx, p, cols) * cols * 4), DLC_STATUS_SUCCESS; });
-        b.sums = static_cast<float *>(b.take(most));
+    if (!b.fused) {
+        b.ld = (b.piece + 3) / 4 * 4;
+        b.z = static_cast<float *>(b.take((size_t)p.M * b.ld * 4));
     }
+    b.dz = static_cast<unsigned short *>(b.take((size_t)p.M * b.ldz * 2));
     if (p.dx.p && b.piece < p.V && p.dx.dt != DLC_DATA_FLOAT) {
         const long long ld = ((long long)p.K + 3) / 4 * 4;
         b.dx_sum = dense(b.take((size_t)p.M * ld * 4), DLC_DATA_FLOAT, ld);
     }
-    size_t most = 0;
-    b.each(p, [&](int n0, int cols, int) {
-        most = std::max(most, dlc_gemm_workspace(ctx, b.logits(p, n0, cols)));
+    size_t most = 0, sums = 0;
+    b.each(p, [&](int n0, int cols) {
+        sums = std::max(sums, (size_t)strips(ctx, p, b.fused, cols) * cols * 4);
+        most = std::max(most, dlc_gemm_workspace(ctx, b.fused ? b.fused_logits(p, ENTROPY_DZ, n0, cols, 0) : b.logits(p, n0, cols)));
         if (p.dx.p) most = std::max(most, dlc_gemm_workspace(ctx, b.data(p, n0, cols)));
         if (p.dw.p) most = std::max(most, dlc_gemm_workspace(ctx, b.filters(p, n0, cols)));
         return DLC_STATUS_SUCCESS;
     });
+    if (p.dbias) b.sums = static_cast<float *>(b.take(sums));
     b.gemm_ws = static_cast<char *>(b.take(most));
     return b;
 }
@@ -393,16 +425,21 @@ size_t dlc_cross_entropy_workspace(const dlcContext *ctx, const CrossEntropyProb
 dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem &p) {
     const CePlan f = plan_fwd(ctx, p, p.ws);
     CeParams c = params(ctx, p, f);
-    const dlcStatus_t st = f.each(p, [&](int n0, int cols, int part0) {
+    const dlcStatus_t st = f.each(p, [&](int n0, int cols) {
         dlcStatus_t s = f.pack(ctx, p, n0, cols);
-        if (s == DLC_STATUS_SUCCESS) s = dlc_launch_gemm(ctx, f.logits(p, n0, cols));
         if (s != DLC_STATUS_SUCCESS) return s;
-        c.n0 = n0;
-        c.cols = cols;
-        c.part0 = part0;
-        void *args[] = {&c};
-        const unsigned rows = (unsigned)std::min<long long>(p.M, 0x7fffffffLL);
-        return dlc_launch(ctx, (const void *)ce_part_kernel, dim3(rows, (unsigned)segments(cols)), dim3(CE_THREADS), 0, args);
+        if (f.fused) {
+            s = dlc_launch_gemm(ctx, f.fused_logits(p, ENTROPY_PARTS, n0, cols, c.part0));
+        } else {
+            s = dlc_launch_gemm(ctx, f.logits(p, n0, cols));
+            if (s != DLC_STATUS_SUCCESS) return s;
+            c.n0 = n0;
+            c.cols = cols;
+            void *args[] = {&c};
+            s = dlc_launch(ctx, (const void *)ce_part_kernel, dim3((unsigned)p.M, (unsigned)segments(cols)), dim3(CE_THREADS), 0, args);
+        }
+        c.part0 += f.parts_of(ctx, p, n0, cols);
+        return s;
     });
     if (st != DLC_STATUS_SUCCESS) return st;
     void *args[] = {&c};
@@ -414,16 +451,21 @@ size_t dlc_cross_entropy_bwd_workspace(const dlcContext *ctx, const CrossEntropy
 dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProblem &p) {
     const CePlan b = plan_bwd(ctx, p, p.ws);
     CeParams c = params(ctx, p, b);
-    return b.each(p, [&](int n0, int cols, int) {
+    return b.each(p, [&](int n0, int cols) {
         dlcStatus_t s = b.pack(ctx, p, n0, cols);
-        if (s == DLC_STATUS_SUCCESS) s = dlc_launch_gemm(ctx, b.logits(p, n0, cols));
         if (s != DLC_STATUS_SUCCESS) return s;
-        c.n0 = n0;
-        c.cols = cols;
-        const int rows = strips(ctx, p, cols);
-        void *args[] = {&c};
-        s = dlc_launch(ctx, (const void *)ce_dz_kernel, dim3((unsigned)((cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS)), (unsigned)rows),
-                       dim3(CE_THREADS), 0, args);
+        const int rows = strips(ctx, p, b.fused, cols);
+        if (b.fused) {
+            s = dlc_launch_gemm(ctx, b.fused_logits(p, ENTROPY_DZ, n0, cols, 0));
+        } else {
+            s = dlc_launch_gemm(ctx, b.logits(p, n0, cols));
+            if (s != DLC_STATUS_SUCCESS) return s;
+            c.n0 = n0;
+            c.cols = cols;
+            void *args[] = {&c};
+            s = dlc_launch(ctx, (const void *)ce_dz_kernel,
+                           dim3((unsigned)((cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS)), (unsigned)rows), dim3(CE_THREADS), 0, args);
+        }
         if (s == DLC_STATUS_SUCCESS && p.dbias) s = dlc_launch_column_sum(ctx, b.sums, p.dbias + n0, cols, rows);
         if (s == DLC_STATUS_SUCCESS && p.dx.p) s = dlc_launch_gemm(ctx, b.data(p, n0, cols));
         if (s == DLC_STATUS_SUCCESS && p.dw.p) s = dlc_launch_gemm(ctx, b.filters(p, n0, cols));

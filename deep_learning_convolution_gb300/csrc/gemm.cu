@@ -47,6 +47,7 @@ namespace {
 
 using namespace dlc;
 
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr int GP_ROWS = 128;                    // rows of a per CTA
 constexpr int GP_LINE = 128;                    // bytes of a stage's operand rows (one swizzle span)
 constexpr int GP_A_BYTES = GP_ROWS * GP_LINE;   // 16 KiB
@@ -78,6 +79,7 @@ struct GpParams {
     RowTensor z, r, y;
     int y_tma, z_tma;
     int y_unit, z_unit;           // elements of an aligned access to y (where TMA cannot write it) and z
+    EntropyTile entropy;
     int *err;
     unsigned long long timeout_ns;
 };
@@ -609,8 +611,158 @@ __device__ __forceinline__ void gp_epilogue(const GpParams &p, uint32_t rank, ui
     __syncwarp();
 }
 
+// One exponential for a pair: 2^a.x, 2^a.y.
+__device__ __forceinline__ float2 exp2_pair(float2 a) { return make_float2(exp2_fast(a.x), exp2_fast(a.y)); }
+
+// The sum over this warp's 32 rows of each of 32 columns; lane i is left with column i.  Every
+// step hands half of the columns to the lane across and keeps the other half: 31 shuffles.
+__device__ __forceinline__ float gp_column_sum(const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    float w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float give = lane & 16 ? v[i] : v[16 + i], keep = lane & 16 ? v[16 + i] : v[i];
+        w[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o /= 2) {
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float give = lane & o ? w[i] : w[o + i], keep = lane & o ? w[o + i] : w[i];
+            w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return w[0];
+}
+
+// The epilogue of softmax cross entropy (cross_entropy.cu), tiles of whole reductions.  The
+// accumulator's row is a thread's own, so a row's part of the sum needs no exchange:
+//   ENTROPY_PARTS  2^r s of this thread's columns, and the target's logit where it is one of them
+//   ENTROPY_DZ     dz in BF16 through bulk stores, and its sums over the warp's 32 rows
+template <int MODE>
+__device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
+                                           uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const WaitCtl &ctl) {
+    const EntropyTile &e = p.entropy;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, part = (warp - GP_EPI_WARP0) >> 2;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    GpStore st;
+    st.bufs = epi_smem + (uint32_t)(warp - GP_EPI_WARP0) * 2u * p.epi_buf;
+    st.buf_bytes = p.epi_buf;
+    st.nbuf = 0;
+    st.lane = lane;
+    st.M = p.M;
+    int it = 0;
+    bool dead = false;
+    for (int u = (int)cluster_id_x(); u < p.units; u += (int)num_clusters_x(), ++it) {
+        const GpUnit w = gp_unit(p, u);
+        const int buf = it & 1;
+        const long long m = w.m0 + (long long)rank * GP_ROWS + quad * 32 + lane;
+        st.row0 = m - lane;
+        const bool valid = m < p.M;
+        const int n0 = w.nt * p.nout;
+        float sa = 1.f, lse = 0.f, weight = 0.f;
+        long long target = -1;  // as a column of this product
+        bool counted = false;
+        if (valid) {
+            if (p.sa) sa = p.sa[m];
+            const long long k = e.target.wide ? static_cast<const long long *>(e.target.p)[m] : static_cast<const int *>(e.target.p)[m];
+            counted = k >= 0 && k < e.V;
+            if (counted) target = k - e.n0;
+            if (MODE == ENTROPY_DZ) {
+                lse = e.lse[m];
+                if (counted) weight = e.dloss[m];
+                if (k >= e.V && n0 == 0 && e.n0 == 0 && part == 0) record_error(p.err, DLC_DEVERR_INDEX, (int)m);
+            }
+        }
+        if (p.sb || p.bias) {
+            gp_epi_barrier();  // the tile before has been read
+            gp_columns(p, false, n0, columns);
+            gp_epi_barrier();
+        }
+        int okw = 0;
+        if (lane == 0 && !dead) okw = mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, ctl, 26) ? 1 : 0;
+        okw = __shfl_sync(0xffffffffu, okw, 0);
+        dead = !okw;
+        if (dead) continue;
+        __syncwarp();
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * p.acc_stride;
+        float r = -INFINITY;
+        float2 sum = make_float2(0.f, 0.f);
+        for (int c0 = 32 * part; c0 < p.nout && n0 + c0 < p.N; c0 += 64) {
+            const int n = n0 + c0, cols = p.N - n;
+            float v[32];
+            {
+                uint32_t a[32];
+                tmem_ld_32x32b_x32(taddr + (uint32_t)c0, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+            }
+            gp_scale_bias(p, v, sa, columns + c0);
+            const bool here = target >= n && target < n + 32;
+            float chosen = 0.f;
+            if (here) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (target == n + i) chosen = v[i];
+            }
+            if constexpr (MODE == ENTROPY_PARTS) {
+                if (cols < 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i >= cols) v[i] = -INFINITY;
+                }
+                if (here) e.chosen[m] = chosen;
+                float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const float rn = fmaxf(r, ceilf(most * LOG2E)), base = isinf(rn) ? 0.f : rn;
+                const float old = exp2_fast(r - base);  // (r = -inf: nothing so far)
+                sum = mul2(sum, pair_of(old));
+                r = rn;
+                float2 more = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    sum = add2(sum, exp2_pair(fma2(get2(v, i), pair_of(LOG2E), pair_of(-base))));
+                    more = add2(more, exp2_pair(fma2(get2(v, i + 1), pair_of(LOG2E), pair_of(-base))));
+                }
+                sum = add2(sum, more);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    set2(v, i, mul2(exp2_pair(mul2(add2(get2(v, i), pair_of(-lse)), pair_of(LOG2E))), pair_of(weight)));
+                if (here) {  // exp(z - lse) - 1 without its cancellation
+                    const float at = weight * expm1f(chosen - lse);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (target == n + i) v[i] = at;
+                }
+                if (!counted) {  // (whatever its logits are)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+                if (e.sums) {
+                    const float s = gp_column_sum(v);
+                    if (st.row0 < p.M && lane < cols) e.sums[(st.row0 >> 5) * p.N + n + lane] = s;
+                }
+                st.tma(tmY, true, v, n, 0);
+            }
+        }
+        if (MODE == ENTROPY_PARTS && valid) e.part[((long long)e.part0 + 2 * w.nt + part) * p.M + m] = make_float2(r, sum.x + sum.y);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_tmem_free(tempty0 + 8u * (uint32_t)buf);
+    }
+    if (elect_one()) bulk_wait_group_read<0>();
+    __syncwarp();
+}
+
 // ROWS: y or z cannot be written by TMA, or the residual not be read in vectors.
-template <bool E4M3, bool A_MN, bool B_MN, bool GATED, bool ROWS>
+// ENTROPY: the epilogue is gp_entropy's.
+template <bool E4M3, bool A_MN, bool B_MN, bool GATED, bool ROWS, int ENTROPY = ENTROPY_NONE>
 __global__ void __launch_bounds__(GP_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ GpParams p, const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
@@ -670,8 +822,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         if (elect_one() && rank == 0)
             gp_mma<E4M3, A_MN, B_MN>(p, tmem_base, sA, sB, full, empty, tfull, tempty, mma_done, ctl);
     } else {
+        if constexpr (ENTROPY != ENTROPY_NONE)
+            gp_entropy<ENTROPY>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, ctl);
         // (the activation's branch out here: a block's code is straight)
-        act_dispatch(p.act, [&](auto act) {
+        else act_dispatch(p.act, [&](auto act) {
             gp_epilogue<GATED, ROWS, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, &tmP, ctl);
         });
     }
@@ -902,7 +1056,8 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     p.a_ch = (int)(g.a.trans ? g.M : g.K);
     p.b_rows = g.b.trans ? g.K : nb;
     p.b_ch = (int)(g.b.trans ? nb : g.K);
-    p.gemv = dlc_gemv_ok(g);
+    const bool entropy = g.entropy.mode != ENTROPY_NONE;  // whole tiles on the pair kernel
+    p.gemv = !entropy && dlc_gemv_ok(g);
     if (p.gemv) return p;  // operands as they are, one launch
     p.pack_a = !tma_rows(g.a.t, p.a_rows, p.a_ch);
     p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
@@ -927,7 +1082,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
         const double epi = 0.97 - 0.62 * w + 2.55 * nout / 256.0, next = std::max(main, epi), fixed = 2.94;
         const long long tail = tiles % pairs, full = tiles / pairs;
         const double whole = full ? main + (double)(full - 1) * next + epi : 0.;
-        for (int s = 1; s <= GP_MAX_SPLITS; ++s) {
+        for (int s = 1; s <= (entropy ? 1 : GP_MAX_SPLITS); ++s) {
             double t = fixed + whole;
             if (s == 1) {
                 if (tail) t += full ? next : main + epi;
@@ -946,7 +1101,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     // 114 with FP32 outputs 12.6 and 9.4).
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
-    if (!g.a.trans && !g.b.trans) {
+    if (!g.a.trans && !g.b.trans && !entropy) {
         const double waves = std::ceil((double)p.m_tiles * p.n_tiles / pairs);
         const double rows = tma_store_rows(g.y, g.M, g.N, 1) ? 0. : 4.0 * p.bn / 256 * waves;
         p.few_rows = g.M <= 64 || dlc_few_rows_plan(ctx, g).us < best + rows;
@@ -1033,6 +1188,12 @@ const void *pair_kernel(bool e4m3, bool a_mn, bool b_mn, bool gated) {
                 : (const void *)gemm_pair_kernel<false, false, false, false, ROWS>;
 }
 
+const void *entropy_kernel(bool e4m3, int mode) {
+    if (mode == ENTROPY_DZ) return (const void *)gemm_pair_kernel<false, false, false, false, false, ENTROPY_DZ>;
+    return e4m3 ? (const void *)gemm_pair_kernel<true, false, false, false, false, ENTROPY_PARTS>
+                : (const void *)gemm_pair_kernel<false, false, false, false, false, ENTROPY_PARTS>;
+}
+
 // Pairs that the device holds at once (each CTA takes an SM's shared memory).
 int resident_pairs(dlcContext *ctx) {
     return dlc_resident_clusters(ctx, &ctx->resident_pairs, (const void *)gemm_pair_kernel<false, false, false, false, false>, 2,
@@ -1092,11 +1253,16 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     if (!dlc_encode_operand(ctx, &ta, g.a, pl.a_rows, pl.a_ch, GP_ROWS) ||
         !dlc_encode_operand(ctx, &tb, g.b, pl.b_rows, pl.b_ch, pl.bn / 2))
         return DLC_STATUS_EXECUTION_FAILED;
-    p.y_tma = tma_store_rows(g.y, g.M, g.N, 1);
+    const int mode = g.entropy.mode;
+    // (rows of dz are padded to whole pieces of 16 bytes, which may be overwritten)
+    const int y_cols = mode == ENTROPY_DZ ? (g.N + 7) / 8 * 8 : g.N;
+    p.entropy = g.entropy;
+    p.y_tma = mode == ENTROPY_PARTS ? 0 : tma_store_rows(g.y, g.M, y_cols, 1);
+    if (mode == ENTROPY_DZ && !p.y_tma) return DLC_STATUS_INTERNAL_ERROR;
     p.z_tma = g.z.p && tma_store_rows(g.z, g.M, g.N, g.gated ? 2 : 1);
     p.y_unit = store_unit(g.y, 0);
     p.z_unit = store_unit(g.z, g.gated ? g.N : 0);
-    if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, g.N, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
+    if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, y_cols, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
     if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
     if (tail) {
         RowTensor part;
@@ -1106,7 +1272,7 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
         if (!encode_output(ctx, &tp, part, 2 * GP_ROWS, pl.bn, tail * pl.splits, 2LL * GP_ROWS * pl.bn))
             return DLC_STATUS_EXECUTION_FAILED;
     }
-    const bool rows = !p.y_tma || (g.r.p && !vec16_rows(g.r)) || (g.z.p && !p.z_tma);
+    const bool rows = (!p.y_tma && mode == ENTROPY_NONE) || (g.r.p && !vec16_rows(g.r)) || (g.z.p && !p.z_tma);
     const bool f32_stage = tail || rows || g.y.dt == DLC_DATA_FLOAT || (g.z.p && g.z.dt == DLC_DATA_FLOAT);
     p.epi_buf = f32_stage ? 4096 : 2048;
     const int epi_bytes = GP_EPI_WARPS * 2 * (int)p.epi_buf;
@@ -1114,7 +1280,8 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.stages = std::min(GP_MAX_STAGES, (GP_MAX_SMEM - GP_COLUMNS - GP_BAR_AREA - epi_bytes) / stage_bytes);
     const size_t smem = (size_t)p.stages * stage_bytes + epi_bytes + GP_COLUMNS + GP_BAR_AREA;
     const bool a_mn = g.a.trans != 0, b_mn = g.b.trans != 0, gated = g.gated != 0;
-    const void *kern = rows ? pair_kernel<true>(e4m3, a_mn, b_mn, gated) : pair_kernel<false>(e4m3, a_mn, b_mn, gated);
+    const void *kern = mode != ENTROPY_NONE ? entropy_kernel(e4m3, mode)
+                       : rows ? pair_kernel<true>(e4m3, a_mn, b_mn, gated) : pair_kernel<false>(e4m3, a_mn, b_mn, gated);
     if (!dlc_allow_smem(ctx, kern, smem)) return DLC_STATUS_EXECUTION_FAILED;
     const int clusters = std::min(resident_pairs(ctx), p.units);
     void *args[] = {&p, &ta, &tb, &ty, &tz, &tp};
@@ -1176,6 +1343,8 @@ dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n) {
     void *args[] = {&pk};
     return dlc_launch(ctx, (const void *)pack_kernel, grid, dim3(256), 0, args);
 }
+
+int dlc_entropy_parts(const dlcContext *ctx, const GemmProblem &g) { return 2 * plan_gemm(ctx, g).n_tiles; }
 
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
     const GemmPlan p = plan_gemm(ctx, g);

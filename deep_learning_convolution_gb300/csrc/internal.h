@@ -332,6 +332,19 @@ struct GemmOperand {
     int trans = 0;
 };
 
+// What a product of a loss does with its logits instead of writing them (see gemm.cu).
+enum { ENTROPY_NONE = 0, ENTROPY_PARTS = 1, ENTROPY_DZ = 2 };
+struct EntropyTile {
+    int mode = ENTROPY_NONE;
+    int V = 0, n0 = 0;           // classes in all, and the first one of this product
+    IndexList target;
+    float2 *part = nullptr;      // PARTS: [part][M] (r, s), dlc_entropy_parts of them from part0 on
+    int part0 = 0;
+    float *chosen = nullptr;     // PARTS: [M] the target's logit
+    const float *lse = nullptr, *dloss = nullptr;  // DZ; dz goes to y: BF16, rows padded to 16 bytes
+    float *sums = nullptr;       // DZ: [M / 32][N] sums of dz over 32 rows, or null
+};
+
 // y[m, n] = act(sa[m] sb[n] sum_k a(m, k) b(n, k) + bias[n]) + r[m, n], and
 // z[m, n] the activation's argument; gated: b, sb, bias and z hold 2N entries
 // (gate n, then up N + n) and y[m, n] = act(gate) * up.
@@ -341,6 +354,7 @@ struct GemmProblem {
     GemmOperand a, b;
     const float *sa = nullptr, *sb = nullptr, *bias = nullptr;
     RowTensor z, r, y;
+    EntropyTile entropy;
     char *ws = nullptr;  // dlc_gemm_workspace bytes
 };
 
@@ -368,6 +382,7 @@ RowTensor dlc_packed(const RowTensor &t, int ch, void *dst);
 dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n);
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g);
 size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g);
+int dlc_entropy_parts(const dlcContext *ctx, const GemmProblem &g);
 dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g);
 // act_grad.cu
 size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p);
