@@ -10,8 +10,8 @@
 // 32 sorted positions and a slab of channels and add the rows of each token up in
 // registers.  A token whose rows reach over several blocks leaves a partial sum in each,
 // which a last kernel adds in order: a token that is every tenth one costs no more than
-// the others.  Rows of the table that no token names are zeroed beside the sums, by
-// blocks that look at a byte a row; the whole gradient is written once.
+// the others.  The table is zeroed beside the sort, whose own time is latency, and the
+// tokens' rows then written over.
 #include "channel.cuh"
 #include "ptx.cuh"
 
@@ -116,9 +116,30 @@ struct SortParams {
     int bits, passes;       // of a digit; of the sort
     int *hist;              // [pass][tile][digit]
     uint32_t *key[2], *row[2];  // pass p writes the arrays p mod 2
-    unsigned char *named;   // [V]: rows of the table that a token names (null: not wanted)
     int *err;
+    int blocks;                 // that sort; those behind them zero this launch's part of the table
+    char *fill;                 // (16-byte aligned)
+    long long fill_words;       // of 16 bytes
+    char *edge[2];              // bytes of the table before and behind its whole words (first launch)
+    int edge_bytes[2];
 };
+
+// What the blocks behind the sorting ones do, whose time is latency: the table's rows are zeroed, all
+// of them, a part in each of the sort's launches.
+__device__ __forceinline__ void fill_part(const SortParams &p) {
+    const long long me = (long long)((int)blockIdx.x - p.blocks) * blockDim.x + threadIdx.x;
+    const long long all = (long long)((int)gridDim.x - p.blocks) * blockDim.x;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.fill);
+    long long i = me;
+    for (; i + 3 * all < p.fill_words; i += 4 * all) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[i + k * all] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (; i < p.fill_words; i += all) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (me < p.edge_bytes[k]) p.edge[k][me] = 0;
+}
 
 struct SortShared {
     unsigned short count[SORT_WARPS][SORT_MAX_DIGITS];  // of a warp's tokens, then the warps before it
@@ -202,8 +223,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tile_kernel(const __grid_co
     SortTile &tile = *reinterpret_cast<SortTile *>(tile_s);
     SortShared &s = tile.s;
     griddep_wait();
-    if (p.named)
-        for (int i = threadIdx.x; i < (p.V + 15) / 16; i += SORT_THREADS) reinterpret_cast<uint4 *>(p.named)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (blockIdx.x > 0) {
+        fill_part(p);
+        return;
+    }
     const int first = (int)(threadIdx.x >> 5) * 32 * SORT_EACH + (int)(threadIdx.x & 31);
     uint32_t key[SORT_EACH], row[SORT_EACH];
     bool on[SORT_EACH];
@@ -241,11 +264,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tile_kernel(const __grid_co
         if (on[k]) {
             p.key[last][first + 32 * k] = key[k];
             p.row[last][first + 32 * k] = row[k];
-            if (p.named && key[k] < (uint32_t)p.V) p.named[key[k]] = 1;  // (zeroed above, before barriers)
         }
 }
 
-// The first pass's histograms; zeroes those of the others, and the named rows.
+// The first pass's histograms; zeroes those of the others.
 __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_constant__ SortParams p) {
     griddep_launch_dependents();
     __shared__ int count[SORT_MAX_DIGITS];
@@ -253,12 +275,14 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_c
     for (int d = threadIdx.x; d < digits; d += SORT_THREADS) count[d] = 0;
     __syncthreads();
     griddep_wait();
-    const long long all = (long long)gridDim.x * SORT_THREADS, me = (long long)blockIdx.x * SORT_THREADS + threadIdx.x;
-    if (p.named)
-        for (long long i = me; i < (p.V + 15) / 16; i += all) reinterpret_cast<uint4 *>(p.named)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if ((int)blockIdx.x >= p.blocks) {
+        fill_part(p);
+        return;
+    }
+    const long long all = (long long)p.blocks * SORT_THREADS, me = (long long)blockIdx.x * SORT_THREADS + threadIdx.x;
     const long long per = (long long)p.tiles * digits;
     for (long long i = per + me; i < per * p.passes; i += all) p.hist[i] = 0;
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < p.tiles; tile += p.blocks) {
 #pragma unroll
         for (int k = 0; k < SORT_EACH; ++k) {
             const long long i = (long long)tile * SORT_TILE + k * SORT_THREADS + threadIdx.x;
@@ -276,6 +300,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_c
 __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_constant__ SortParams p, int pass) {
     griddep_launch_dependents();
     __shared__ SortShared s;
+    if ((int)blockIdx.x >= p.blocks) {
+        griddep_wait();
+        fill_part(p);
+        return;
+    }
     sort_clear(s);
     griddep_wait();
     const int tile = blockIdx.x, digits = 1 << p.bits;
@@ -317,86 +346,71 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
             p.row[pass & 1][at] = row[k];
             if (more)
                 atomicAdd(p.hist + ((long long)(pass + 1) * p.tiles + at / SORT_TILE) * digits + ((key[k] >> ((pass + 1) * p.bits)) & mask), 1);
-            else if (p.named && key[k] < (uint32_t)p.V)
-                p.named[key[k]] = 1;
         }
 }
 
 // ---- sums by token ---------------------------------------------------------------------
 
-constexpr int SUM_THREADS = 128, SUM_MAX_CHUNK = 128;
+constexpr int SUM_THREADS = 128, SUM_MAX_CHUNK = 128;  // threads of a block at most
 
 struct SumParams {
     EmbeddingProblem e;        // y: dy; table: dtable
     const uint32_t *key, *row; // sorted
-    const unsigned char *named;
     float *part;               // [chunk][2][C]: of the token that comes in, of the one that goes on
     int chunk, chunks, slabs;  // sorted positions of a chunk
-    int fill_blocks;
+};
+
+// W channels: 8 or 4 in one or two accesses, or one.
+template <int W, typename T>
+struct Words {
+    T v[W];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (W * sizeof(T) >= 16) {
+#pragma unroll
+            for (int j = 0; j < W * (int)sizeof(T) / 16; ++j) reinterpret_cast<uint4 *>(v)[j] = reinterpret_cast<const uint4 *>(p)[j];
+        } else if constexpr (W * sizeof(T) == 8) {
+            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+        } else {
+            v[0] = p[0];
+        }
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if constexpr (sizeof(T) == 2)
+            return bf16_bits_f32(v[j]);
+        else
+            return v[j];
+    }
 };
 
 template <int W, typename T>
-__device__ __forceinline__ void sum_store(const SumParams &p, uint32_t token, int c, const float (&acc)[W]) {
-    T *dst = static_cast<T *>(p.e.table.p) + (long long)token * p.e.C + c;
-    float f[W];
+__device__ __forceinline__ void store_words(T *dst, const float (&f)[W]) {
+    if constexpr (W == 1) {
+        store_elem(dst, sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) f[j] = acc[j] * p.e.scale;
-    if constexpr (W == 8) {
-        constexpr int Q = (int)sizeof(T) / 2;
-        if (p.e.accumulate) {
-            T old[W];
-#pragma unroll
-            for (int j = 0; j < Q; ++j) reinterpret_cast<uint4 *>(old)[j] = reinterpret_cast<const uint4 *>(dst)[j];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if constexpr (sizeof(T) == 2)
-                    f[j] += bf16_bits_f32(old[j]);
-                else
-                    f[j] += old[j];
-            }
-        }
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(dst) =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        } else {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
+        for (int j = 0; j < W / 4; ++j)
+            reinterpret_cast<float4 *>(dst)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    } else if constexpr (W == 8) {
+        *reinterpret_cast<uint4 *>(dst) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
     } else {
-        constexpr int dt = sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT;
-        if (p.e.accumulate) f[0] += load_elem(dst, dt, 0);
-        store_elem(dst, dt, 0, f[0]);
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
     }
 }
 
-// W = 8: 16-byte accesses of dy and of the table; W = 1: any layout of dy, any size.
-template <int W, typename D, typename T>
+// W = 8, 4: aligned vectors of dy and of the table; W = 1: any layout of dy, any size.  ACC: the sums
+// are added to the table's rows, which are loaded beside the rows of dy that end a token (one by
+// one, where they are needed, 32 tokens took 32 memory latencies).
+template <int W, typename D, typename T, bool ACC>
 __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid_constant__ SumParams p) {
     griddep_launch_dependents();
     __shared__ uint32_t key_s[SUM_MAX_CHUNK + 2], row_s[SUM_MAX_CHUNK];
     const int C = p.e.C;
     griddep_wait();
-    if ((int)blockIdx.x >= p.chunks * p.slabs) {  // rows that no token names: a warp 32 rows at a time
-        const int lane = threadIdx.x & 31;
-        const long long warps = (long long)p.fill_blocks * (SUM_THREADS / 32);
-        for (long long v0 = 32 * ((long long)(blockIdx.x - p.chunks * p.slabs) * (SUM_THREADS / 32) + (threadIdx.x >> 5)); v0 < p.e.V;
-             v0 += 32 * warps) {
-            uint32_t todo = __ballot_sync(0xffffffffu, v0 + lane < p.e.V && p.named[v0 + lane] == 0);
-            for (; todo; todo &= todo - 1u) {
-                T *dst = static_cast<T *>(p.e.table.p) + (v0 + __ffs((int)todo) - 1) * C;
-                if constexpr (W == 8) {
-                    for (int c = lane; c < C * (int)sizeof(T) / 16; c += 32) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                    for (int c = lane; c < C; c += 32) dst[c] = (T)0;
-                }
-            }
-        }
-        return;
-    }
     const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
     const int n = min(p.chunk, (int)p.e.rows - chunk * p.chunk);
     const long long first = (long long)chunk * p.chunk;
-    for (int i = threadIdx.x; i < n; i += SUM_THREADS) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
         key_s[1 + i] = p.key[first + i];
         row_s[i] = p.row[first + i];
     }
@@ -405,27 +419,26 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
         key_s[1 + n] = first + n < p.e.rows ? p.key[first + n] : 0xffffffffu;
     }
     __syncthreads();
-    const int c = (slab * SUM_THREADS + (int)threadIdx.x) * W;
+    const int c = (slab * (int)blockDim.x + (int)threadIdx.x) * W;
     if (c >= C) return;
     const long long co = c * p.e.y.m.cs;
+    const uint32_t comes = key_s[0];  // the token that began in the chunk before, if it is the first here
     float acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) acc[j] = 0.f;
-    constexpr int U = W == 8 ? (sizeof(D) == 2 ? 8 : 4) : 8;  // rows in flight
-    int begin = 0;  // of the token at hand
+    constexpr int U = ACC || W * sizeof(D) > 16 ? 4 : 8;  // rows in flight
     for (int i0 = 0; i0 < n; i0 += U) {
-        D v[U][W];
+        Words<W, D> v[U];
+        Words<W, T> old[ACC ? U : 1];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (i0 + k < n && key_s[1 + i0 + k] < (uint32_t)p.e.V) {
-                const D *src = static_cast<const D *>(p.e.y.p) + row_off(p.e.y.m, row_s[i0 + k]) + co;
-                if constexpr (W == 8) {
-#pragma unroll
-                    for (int j = 0; j < (int)sizeof(D) / 2; ++j) reinterpret_cast<uint4 *>(v[k])[j] = reinterpret_cast<const uint4 *>(src)[j];
-                } else {
-                    v[k][0] = src[0];
-                }
-            }
+            const int i = i0 + k;
+            if (i >= n) continue;
+            const uint32_t token = key_s[1 + i];
+            if (token >= (uint32_t)p.e.V) continue;
+            v[k].load(static_cast<const D *>(p.e.y.p) + row_off(p.e.y.m, row_s[i]) + co);
+            if constexpr (ACC)
+                if (key_s[2 + i] != token && token != comes) old[k].load(static_cast<const T *>(p.e.table.p) + (long long)token * C + c);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -434,23 +447,20 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
             const uint32_t token = key_s[1 + i];
             if (token >= (uint32_t)p.e.V) return;  // tokens outside the table: the last ones
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if constexpr (sizeof(D) == 2)
-                    acc[j] += bf16_bits_f32(v[k][j]);
-                else
-                    acc[j] += v[k][j];
-            }
+            for (int j = 0; j < W; ++j) acc[j] += v[k].at(j);
             const bool ends = key_s[2 + i] != token;
             if (!ends && i + 1 < n) continue;
-            const bool comes = begin == 0 && key_s[0] == token;
-            if (ends && !comes) {
-                sum_store<W, T>(p, token, c, acc);
-            } else {
-                float *dst = p.part + ((long long)chunk * 2 + (comes ? 0 : 1)) * C + c;
+            if (ends && token != comes) {
+                float f[W];
 #pragma unroll
-                for (int j = 0; j < W; ++j) dst[j] = acc[j];
+                for (int j = 0; j < W; ++j) {
+                    f[j] = acc[j] * p.e.scale;
+                    if constexpr (ACC) f[j] += old[k].at(j);
+                }
+                store_words<W, T>(static_cast<T *>(p.e.table.p) + (long long)token * C + c, f);
+            } else {
+                store_words<W, float>(p.part + ((long long)chunk * 2 + (token == comes ? 0 : 1)) * C + c, acc);
             }
-            begin = i + 1;
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[j] = 0.f;
         }
@@ -459,35 +469,53 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
 
 // Tokens whose rows reach over several chunks: the block of the chunk where they begin adds
 // up the partial sums in order.
-template <int W, typename T>
+template <int W, typename T, bool ACC>
 __global__ void __launch_bounds__(SUM_THREADS) embedding_join_kernel(const __grid_constant__ SumParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
     const long long end = (long long)(chunk + 1) * p.chunk;  // (the last chunk has no block)
-    const uint32_t token = p.key[end - 1];
-    if (token >= (uint32_t)p.e.V || p.key[end] != token) return;
-    if (chunk && p.key[end - p.chunk] == token && p.key[end - p.chunk - 1] == token) return;  // begins further ahead
+    const uint32_t token = p.key[end - 1], next = p.key[end], front = p.key[end - p.chunk], before = chunk ? p.key[end - p.chunk - 1] : 0xffffffffu;
+    if (token >= (uint32_t)p.e.V || next != token) return;
+    if (front == token && before == token) return;  // begins further ahead
     int more = 0;  // chunks after this one that the token begins
     for (;;) {
         const int k = chunk + 1 + more + (int)threadIdx.x;
         const int found = __syncthreads_count(k < p.chunks && p.key[(long long)k * p.chunk] == token);
         more += found;
-        if (found < SUM_THREADS) break;
+        if (found < (int)blockDim.x) break;
     }
-    const int c = (slab * SUM_THREADS + (int)threadIdx.x) * W;
+    const int c = (slab * (int)blockDim.x + (int)threadIdx.x) * W;
     if (c >= p.e.C) return;
     const float *src = p.part + ((long long)chunk * 2 + 1) * p.e.C + c;
+    T *dst = static_cast<T *>(p.e.table.p) + (long long)token * p.e.C + c;
+    Words<W, T> old;
+    if constexpr (ACC) old.load(dst);
+    Words<W, float> q;
+    q.load(src);
     float acc[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc[j] = src[j];
+    for (int j = 0; j < W; ++j) acc[j] = q.v[j];
     src += p.e.C;  // the next chunk's first slot
-#pragma unroll 8
-    for (int k = 0; k < more; ++k) {
+    constexpr int U = 8;
+    for (int k0 = 0; k0 < more; k0 += U) {
+        Words<W, float> part[U];
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] += src[(long long)k * 2 * p.e.C + j];
+        for (int k = 0; k < U; ++k)
+            if (k0 + k < more) part[k].load(src + (long long)(k0 + k) * 2 * p.e.C);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (k0 + k < more) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j] += part[k].v[j];
+            }
     }
-    sum_store<W, T>(p, token, c, acc);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        acc[j] *= p.e.scale;
+        if constexpr (ACC) acc[j] += old.at(j);
+    }
+    store_words<W, T>(dst, acc);
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -500,24 +528,35 @@ const void *fwd_kernel(int y) {
 }
 
 template <int W, typename D>
-const void *sum_kernel(int t) {
-    return t == DLC_DATA_BFLOAT16 ? (const void *)embedding_sum_kernel<W, D, Half> : (const void *)embedding_sum_kernel<W, D, float>;
+const void *sum_kernel(int t, bool acc) {
+    if (t == DLC_DATA_BFLOAT16)
+        return acc ? (const void *)embedding_sum_kernel<W, D, Half, true> : (const void *)embedding_sum_kernel<W, D, Half, false>;
+    return acc ? (const void *)embedding_sum_kernel<W, D, float, true> : (const void *)embedding_sum_kernel<W, D, float, false>;
 }
 
 template <int W>
-const void *join_kernel(int t) {
-    return t == DLC_DATA_BFLOAT16 ? (const void *)embedding_join_kernel<W, Half> : (const void *)embedding_join_kernel<W, float>;
+const void *sum_kernel(const EmbeddingProblem &e) {
+    return e.y.dt == DLC_DATA_BFLOAT16 ? sum_kernel<W, Half>(e.table.dt, e.accumulate) : sum_kernel<W, float>(e.table.dt, e.accumulate);
 }
 
-bool vectors(const EmbeddingProblem &e) {
-    return e.C % 8 == 0 && (uintptr_t)e.table.p % 16 == 0 && e.y.m.cs == 1 && dlc_aligned_rows(e.y, 16);
+template <int W>
+const void *join_kernel(const EmbeddingProblem &e) {
+    if (e.table.dt == DLC_DATA_BFLOAT16)
+        return e.accumulate ? (const void *)embedding_join_kernel<W, Half, true> : (const void *)embedding_join_kernel<W, Half, false>;
+    return e.accumulate ? (const void *)embedding_join_kernel<W, float, true> : (const void *)embedding_join_kernel<W, float, false>;
+}
+
+// Whether rows of the table and of y are whole vectors of w elements of either.
+bool vectors(const EmbeddingProblem &e, int w) {
+    return e.C % w == 0 && (uintptr_t)e.table.p % std::min(16, w * dlc_dtype_bytes((dlcDataType_t)e.table.dt)) == 0 && e.y.m.cs == 1 &&
+           dlc_aligned_rows(e.y, std::min(16, w * dlc_dtype_bytes((dlcDataType_t)e.y.dt)));
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct BwdPlan {
     int bits, passes, tiles, chunk, chunks;
-    size_t hist, key[2], row[2], named, part, bytes;
+    size_t hist, key[2], row[2], part, bytes;
 };
 
 BwdPlan plan_bwd(long long rows, int C, int V) {
@@ -538,7 +577,6 @@ BwdPlan plan_bwd(long long rows, int C, int V) {
     };
     b.hist = take((size_t)b.passes * b.tiles * (1u << b.bits) * 4);
     for (int i = 0; i < 2; ++i) b.key[i] = take((size_t)rows * 4), b.row[i] = take((size_t)rows * 4);
-    b.named = take((size_t)V + 16);
     b.part = take((size_t)b.chunks * 2 * C * 4);
     b.bytes = off;
     return b;
@@ -550,7 +588,7 @@ dlcStatus_t dlc_launch_embedding(dlcContext *ctx, const EmbeddingProblem &e) {
     EmParams p;
     p.e = e;
     p.err = ctx->d_err;
-    const bool w8 = vectors(e);
+    const bool w8 = vectors(e, 8);
     p.pieces = w8 ? e.C / 8 : e.C;
     p.items = e.rows * p.pieces;
     const bool bf = e.table.dt == DLC_DATA_BFLOAT16;
@@ -577,21 +615,39 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
         s.key[i] = reinterpret_cast<uint32_t *>(e.ws + b.key[i]);
         s.row[i] = reinterpret_cast<uint32_t *>(e.ws + b.row[i]);
     }
-    s.named = e.accumulate ? nullptr : reinterpret_cast<unsigned char *>(e.ws + b.named);
     s.err = ctx->d_err;
+    // the table's whole 16-byte words, dealt evenly to the sort's launches
+    const size_t bytes = e.accumulate ? 0 : (size_t)e.V * e.C * dlc_dtype_bytes((dlcDataType_t)e.table.dt);
+    char *table = static_cast<char *>(e.table.p);
+    const size_t head = std::min(bytes, (16 - (uintptr_t)table % 16) % 16), words = (bytes - head) / 16;
+    const int launches = b.tiles == 1 ? 1 : 1 + b.passes;
+    auto part = [&](int i) {
+        const size_t w0 = words * i / launches, w1 = words * (i + 1) / launches;
+        s.fill = table + head + 16 * w0;
+        s.fill_words = (long long)(w1 - w0);
+        s.edge[0] = table;
+        s.edge[1] = table + head + 16 * words;
+        s.edge_bytes[0] = i == 0 ? (int)head : 0;
+        s.edge_bytes[1] = i == 0 ? (int)(bytes - head - 16 * words) : 0;
+        return bytes ? (unsigned)std::min<size_t>((w1 - w0) / (SORT_THREADS * 4) + 1, (size_t)ctx->sm_count * 3) : 0u;
+    };
     dlcStatus_t st;
+    void *args[] = {&s};
     if (b.tiles == 1) {
-        void *args[] = {&s};
+        s.blocks = 1;
+        const unsigned fill = part(0);
         if (!dlc_allow_smem(ctx, (const void *)sort_tile_kernel, sizeof(SortTile))) return DLC_STATUS_EXECUTION_FAILED;
-        st = dlc_launch(ctx, (const void *)sort_tile_kernel, dim3(1), dim3(SORT_THREADS), sizeof(SortTile), args);
+        st = dlc_launch(ctx, (const void *)sort_tile_kernel, dim3(1 + fill), dim3(SORT_THREADS), sizeof(SortTile), args);
         if (st != DLC_STATUS_SUCCESS) return st;
     } else {
-        void *args[] = {&s};
-        const unsigned blocks = (unsigned)std::max(std::min(b.tiles, ctx->sm_count * 4), std::min(ctx->sm_count, (e.V >> 14) + 1));
-        st = dlc_launch(ctx, (const void *)sort_count_kernel, dim3(blocks), dim3(SORT_THREADS), 0, args);
+        s.blocks = std::min(b.tiles, ctx->sm_count * 4);
+        unsigned fill = part(0);
+        st = dlc_launch(ctx, (const void *)sort_count_kernel, dim3((unsigned)s.blocks + fill), dim3(SORT_THREADS), 0, args);
+        s.blocks = b.tiles;
         for (int pass = 0; pass < b.passes && st == DLC_STATUS_SUCCESS; ++pass) {
+            fill = part(1 + pass);
             void *pargs[] = {&s, &pass};
-            st = dlc_launch(ctx, (const void *)sort_pass_kernel, dim3((unsigned)b.tiles), dim3(SORT_THREADS), 0, pargs);
+            st = dlc_launch(ctx, (const void *)sort_pass_kernel, dim3((unsigned)b.tiles + fill), dim3(SORT_THREADS), 0, pargs);
         }
         if (st != DLC_STATUS_SUCCESS) return st;
     }
@@ -599,21 +655,17 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     p.e = e;
     p.key = s.key[(b.passes - 1) & 1];
     p.row = s.row[(b.passes - 1) & 1];
-    p.named = s.named;
     p.part = reinterpret_cast<float *>(e.ws + b.part);
     p.chunk = b.chunk;
     p.chunks = b.chunks;
-    const bool w8 = vectors(e);
-    const int slab = SUM_THREADS * (w8 ? 8 : 1);
-    p.slabs = (e.C + slab - 1) / slab;
-    p.fill_blocks = e.accumulate ? 0 : (int)std::min<long long>((e.V + 127) / 128, (long long)ctx->sm_count * 8);
-    if ((long long)p.chunks * p.slabs + p.fill_blocks > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
-    const bool bf = e.y.dt == DLC_DATA_BFLOAT16;
-    const void *sum = w8 ? (bf ? sum_kernel<8, Half>(e.table.dt) : sum_kernel<8, float>(e.table.dt))
-                         : (bf ? sum_kernel<1, Half>(e.table.dt) : sum_kernel<1, float>(e.table.dt));
-    void *args[] = {&p};
-    st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs + p.fill_blocks)), dim3(SUM_THREADS), 0, args);
+    const int w = vectors(e, 8) ? 8 : vectors(e, 4) ? 4 : 1;
+    const int threads = std::min(SUM_THREADS, ((e.C + w - 1) / w + 31) / 32 * 32);
+    p.slabs = (e.C + threads * w - 1) / (threads * w);
+    if ((long long)p.chunks * p.slabs > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    void *sargs[] = {&p};
+    const void *sum = w == 8 ? sum_kernel<8>(e) : w == 4 ? sum_kernel<4>(e) : sum_kernel<1>(e);
+    st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs)), dim3((unsigned)threads), 0, sargs);
     if (st != DLC_STATUS_SUCCESS || p.chunks == 1) return st;
-    const void *join = w8 ? join_kernel<8>(e.table.dt) : join_kernel<1>(e.table.dt);
-    return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3(SUM_THREADS), 0, args);
+    const void *join = w == 8 ? join_kernel<8>(e) : w == 4 ? join_kernel<4>(e) : join_kernel<1>(e);
+    return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3((unsigned)threads), 0, sargs);
 }

@@ -406,6 +406,8 @@ RowKernel row_kernel(const RowPlan &r, int C, std::initializer_list<RowTensor> t
 
 dlcStatus_t dlc_launch_layer(dlcContext *ctx, const LayerProblem &pb) {
     LayerProblem p = pb;
+    dlcStatus_t done;
+    if (dlc_layer_vec(ctx, p, done)) return done;
     RowPlan r = plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
                           vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), ring({p.x, p.r}), LN_FWD_BLOCKS, ctx->sm_count);
     RowKernel k = row_kernel<false>(r, p.C, {p.x, p.r});
@@ -426,6 +428,8 @@ size_t dlc_layer_bwd_workspace(const dlcContext *ctx, long long rows, int C) {
 
 dlcStatus_t dlc_launch_layer_bwd(dlcContext *ctx, const LayerBwdProblem &pb) {
     LayerBwdProblem p = pb;
+    dlcStatus_t done;
+    if (dlc_layer_bwd_vec(ctx, p, done)) return done;
     RowPlan r = plan_rows(p.rows, p.C, contiguous(p.dy) && contiguous(p.t) && contiguous(p.dt) && contiguous(p.dx),
                           vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), ring({p.dy, p.t, p.dt}), LN_BWD_BLOCKS,
                           ctx->sm_count);

@@ -1,0 +1,492 @@
+// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: BF16 inputs, channels a
+// multiple of eight, every tensor's rows at one aligned pitch.
+//
+// Here the instructions would bound the kernel before memory does (65536 x 768 BF16 to E4M3:
+// 1278 warp instructions a row and 100 us in layer_rows_kernel), and then the barriers between a
+// row's warps.  So a row takes as few threads as hold it, up to eight vectors each (2048
+// channels: one warp), gamma and beta wait in shared memory, and only a thread's last vector can
+// be missing.
+#include "norm_rows.cuh"
+
+namespace {
+
+using namespace dlc;
+
+// Sum over the `tpr` threads of a row (a power of two), as row_reduce has it.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float (*buf)[NORM_MAX_WARPS * 2], int parity) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        if (o < 8 || o < tpr) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+        }
+    }
+    if (tpr > 32) {
+        const int warps = tpr >> 5;
+        float *mine = buf[parity] + N * ((int)threadIdx.x >> 5);
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) mine[i] = a[i];
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
+        const float *row = buf[parity] + N * slot * warps;
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] = row[i] + row[N + i];
+        for (int w = 2; w < warps; ++w) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += row[w * N + i];
+        }
+    }
+}
+
+// Largest |v| over a row's threads (NaN or not: such a row is NaN anyway).
+__device__ __forceinline__ float row_most(float v, int tpr, int slot, float (*buf)[NORM_MAX_WARPS * 2], int parity) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        if (o < 8 || o < tpr) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (tpr > 32) {
+        const int warps = tpr >> 5;
+        if ((threadIdx.x & 31) == 0) buf[parity][threadIdx.x >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
+        const float *row = buf[parity] + slot * warps;
+        v = fmaxf(row[0], row[1]);
+        for (int w = 2; w < warps; ++w) v = fmaxf(v, row[w]);
+    }
+    return v;
+}
+
+constexpr int VEC_THREADS = 256;  // of a block, or a little less (backward, long rows: TH)
+
+// A ring of S rows of T tensors in shared memory, V vectors of eight a thread, of which a thread
+// reads back only what it copied itself: no barrier, and a row's place takes the row S further
+// on as soon as it has been read.  (Strides are constants: with the block's size for one, the
+// addresses' instructions cost 7 %.)
+template <int V, int T, int S, int TH>
+struct VecRing {
+    static constexpr uint32_t WORDS = (uint32_t)(T * V), WORD = 16u * TH;
+    uint32_t base, row;
+    __device__ __forceinline__ explicit VecRing(uint32_t smem) : base(smem + threadIdx.x * 16u), row(0) {}
+    // at: this thread's first vector; hop: bytes to the next one
+    __device__ __forceinline__ void fetch(int k, const char *at, uint32_t hop, bool last) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool on = j + 1 < V || last;
+            cp_async_16(base + (row + (uint32_t)(k * V + j)) * WORD, at + (on ? j * hop : 0u), on ? 16u : 0u);
+        }
+    }
+    __device__ __forceinline__ void next() {  // (ends the copies of a row)
+        cp_async_commit();
+        row = S == 1 || row == WORDS * (S - 1) ? 0u : row + WORDS;
+    }
+    __device__ __forceinline__ void read_vector(int k, int j, float *f) const {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(base + (row + (uint32_t)(k * V + j)) * WORD)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) set2(f, i, unpack_bf16(w[i]));
+    }
+    __device__ __forceinline__ void read(int k, float (&f)[V * 8]) const {
+#pragma unroll
+        for (int j = 0; j < V; ++j) read_vector(k, j, f + 8 * j);
+    }
+    static constexpr size_t SMEM = (size_t)S * WORDS * WORD;
+};
+
+// A vector of a channel-wise FP32 array from shared memory: its halves lie apart, so that
+// neighbouring threads read neighbouring words.
+__device__ __forceinline__ void vec_param(uint32_t at, uint32_t half, float (&g)[8]) {
+    const float4 a = ld_shared_f32x4(at), b = ld_shared_f32x4(at + half);
+    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+    g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+}
+
+// Fills vec_param's arrays, whose vectors are dealt to `tpr` threads: by copies that the first row's
+// wait covers, or, from an unaligned address, directly.  Zeros behind the row.
+__device__ __forceinline__ void vec_param_fill(float *dst, const float *src, int C, int tpr, int V) {
+    const bool aligned = ((uintptr_t)src & 15u) == 0;
+    for (int i = threadIdx.x; i < 2 * tpr * V; i += blockDim.x) {  // half-vectors
+        const int vec = i >> 1, at = (vec / tpr * 2 + (i & 1)) * tpr + vec % tpr;
+        const bool there = src && 4 * i < C;
+        if (there && aligned) {
+            cp_async_16(smem_u32(dst) + 16u * (uint32_t)at, src + 4 * i, 16u);
+        } else {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (there) v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
+            reinterpret_cast<float4 *>(dst)[at] = v;
+        }
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void vec_store(char *at, const float *v) {
+    if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<uint4 *>(at) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else if constexpr (sizeof(E) == 4) {
+        reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint2 *>(at) = make_uint2(pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16),
+                                                    pack_e4m3(v[4], v[5]) | (pack_e4m3(v[6], v[7]) << 16));
+    }
+}
+
+template <int V>
+constexpr int vec_blocks() { return V <= 2 ? 4 : V <= 4 ? 3 : 2; }
+template <int V>
+constexpr int vec_ring() { return V <= 2 ? 2 : 1; }
+
+struct VecRow {  // this thread's part of a tensor's rows
+    char *p;
+    long long inc;
+    __device__ __forceinline__ VecRow(const RowTensor &t, int e, long long row, long long step, int channel)
+        : p(static_cast<char *>(t.p) + (row * t.m.ld + channel) * e), inc(step * t.m.ld * e) {}
+};
+
+// Y: y's storage.
+template <int V, typename Y, bool RES>
+__global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel(const __grid_constant__ LayerProblem p, int tpr) {
+    griddep_launch_dependents();
+    __shared__ float buf[2][NORM_MAX_WARPS * 2];
+    extern __shared__ uint4 ring_s[];
+    constexpr int N = 8 * V, S = vec_ring<V>();
+    const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    const bool last = (V - 1) * tpr + t < p.C / 8;
+    const int c = V > 1 || last ? 8 * t : 0;
+    const uint32_t hop = 8u * (uint32_t)tpr, half = 16u * (uint32_t)tpr;
+    const float inv_c = 1.f / (float)p.C;
+    using Ring = VecRing<V, RES ? 2 : 1, S, VEC_THREADS>;
+    Ring ring(smem_u32(ring_s));
+    float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM), *beta = gamma + N * tpr;
+    const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t, b0 = smem_u32(beta) + 16u * (uint32_t)t;
+    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
+    VecRow x(p.x, 2, row, step, c), r(p.r, 2, row, step, c), tt(p.t, 2, row, step, c), y(p.y, sizeof(Y), row, step, c);
+    griddep_wait();
+    auto fetch = [&]() {
+        if (ahead < p.rows) {
+            ring.fetch(0, x.p, hop * 2u, last);
+            if (RES) ring.fetch(1, r.p, hop * 2u, last);
+        }
+        ring.next();
+        ahead += step;
+        x.p += x.inc;
+        r.p += r.inc;
+    };
+    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
+    vec_param_fill(beta, p.beta, p.C, tpr, V);
+    for (int i = 0; i < S; ++i) fetch();
+    cp_async_wait<S - 1>();
+    __syncthreads();
+    int parity = 0;
+    for (; row - slot < p.rows; row += step) {  // (as many rounds for every thread of the block)
+        const bool on = row < p.rows;
+        float v[N];
+        cp_async_wait<S - 1>();
+        ring.read(0, v);
+        if (RES) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float w[8];
+                ring.read_vector(1, j, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) set2(v + 8 * j, i, add2(get2(v + 8 * j, i), get2(w, i)));
+            }
+        }
+        if (p.t.p && on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j + 1 < V || last) vec_store<unsigned short>(tt.p + j * (hop * 2u), v + 8 * j);
+        }
+        tt.p += tt.inc;
+        fetch();
+        float2 sum = make_float2(0.f, 0.f), sq = sum;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) sum = add2(get2(v, i), sum);
+        float total[1] = {sum.x + sum.y};
+        row_sums<1>(total, tpr, slot, buf, parity);
+        parity ^= 1;
+        const float2 mean = pair_of(-total[0] * inv_c);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
+        if (!last) {
+#pragma unroll
+            for (int i = 8 * (V - 1); i < N; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
+        total[0] = sq.x + sq.y;
+        row_sums<1>(total, tpr, slot, buf, parity);
+        parity ^= 1;
+        const float2 rho = pair_of(rsqrtf(total[0] * inv_c + p.eps));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float g[8], b[8];
+            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+            vec_param(b0 + (uint32_t)(2 * j) * half, half, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) set2(v + 8 * j, i, fma2(mul2(get2(v + 8 * j, i), rho), get2(g, i), get2(b, i)));
+        }
+        if constexpr (sizeof(Y) == 1) {
+            float most[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < N; ++i) most[i & 1] = fmaxf(most[i & 1], fabsf(v[i]));
+            const float scale = fmaxf(row_most(fmaxf(most[0], most[1]), tpr, slot, buf, parity), SCALE_FLOOR) / E4M3_MAX;
+            parity ^= 1;
+            if (t == 0 && on) p.scale[row] = scale;
+            const float2 inv = pair_of(1.f / scale);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) set2(v, i, mul2(get2(v, i), inv));
+        }
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j + 1 < V || last) vec_store<Y>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + 8 * j);
+        }
+        y.p += y.inc;
+    }
+}
+
+// The same for the backward pass.  128 registers a thread: 16 warps an SM.
+template <int V, bool RES, int TH>
+__global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __grid_constant__ LayerBwdProblem p, int tpr) {
+    griddep_launch_dependents();
+    __shared__ float buf[2][NORM_MAX_WARPS * 2];
+    extern __shared__ uint4 ring_s[];
+    constexpr int N = 8 * V, S = 3;
+    const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    const bool last = (V - 1) * tpr + t < p.C / 8;
+    const int c = V > 1 || last ? 8 * t : 0;
+    const uint32_t hop = 8u * (uint32_t)tpr * (uint32_t)2, half = 16u * (uint32_t)tpr;
+    const float inv_c = 1.f / (float)p.C;
+    using Ring = VecRing<V, RES ? 3 : 2, S, TH>;
+    Ring ring(smem_u32(ring_s));
+    float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM);
+    const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t;
+    float dg[N], db[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.f;
+    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
+    VecRow dy(p.dy, 2, row, step, c), tt(p.t, 2, row, step, c), dt(p.dt, 2, row, step, c), dx(p.dx, 2, row, step, c);
+    griddep_wait();
+    auto fetch = [&]() {
+        if (ahead < p.rows) {
+            ring.fetch(0, dy.p, hop, last);
+            ring.fetch(1, tt.p, hop, last);
+            if (RES) ring.fetch(2, dt.p, hop, last);
+        }
+        ring.next();
+        ahead += step;
+        dy.p += dy.inc;
+        tt.p += tt.inc;
+        dt.p += dt.inc;
+    };
+    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
+    for (int i = 0; i < S; ++i) fetch();
+    cp_async_wait<S - 1>();
+    __syncthreads();
+    for (; row - slot < p.rows; row += step, dx.p += dx.inc) {
+        const bool on = row < p.rows;
+        float d[N], v[N], g[8];  // (gamma is read where it is used: holding it would spill)
+        cp_async_wait<S - 1>();
+        ring.read(0, d);
+        ring.read(1, v);
+        float2 sum = make_float2(0.f, 0.f), sd = sum, sq = sum, dot = sum;
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) set2(db, i, add2(get2(d, i), get2(db, i)));
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum = add2(get2(v + 8 * j, i), sum);
+                sd = fma2(get2(d + 8 * j, i), get2(g, i), sd);
+            }
+        }
+        float means[2] = {sum.x + sum.y, sd.x + sd.y};
+        row_sums<2>(means, tpr, slot, buf, 0);
+        const float2 mean = pair_of(-means[0] * inv_c);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
+        if (!last) {
+#pragma unroll
+            for (int i = 8 * (V - 1); i < N; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 w = get2(v + 8 * j, i);
+                sq = fma2(w, w, sq);
+                dot = fma2(mul2(get2(d + 8 * j, i), get2(g, i)), w, dot);
+            }
+        }
+        float red[2] = {sq.x + sq.y, dot.x + dot.y};
+        row_sums<2>(red, tpr, slot, buf, 1);
+        const float rho = rsqrtf(red[0] * inv_c + p.eps);
+        const float2 rho2 = pair_of(rho), k2 = pair_of(-row_slope(rho, red[1] * inv_c)), m2 = pair_of(-rho * (means[1] * inv_c));
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float s[8];
+                vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+                if (RES) ring.read_vector(2, j, s);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 dr = mul2(get2(d + 8 * j, i), rho2), w = get2(v + 8 * j, i);
+                    set2(dg + 8 * j, i, fma2(dr, w, get2(dg + 8 * j, i)));
+                    const float2 base = RES ? add2(get2(s, i), m2) : m2;
+                    set2(s, i, fma2(dr, get2(g, i), fma2(w, k2, base)));
+                }
+                if (j + 1 < V || last) vec_store<unsigned short>(dx.p + j * hop, s);
+            }
+        }
+        fetch();
+    }
+    if (!p.dgamma && !p.dbeta) return;
+    float *ws0 = p.ws + 2ll * blockIdx.x * p.C;
+    float *acc_s = reinterpret_cast<float *>(ring_s);  // [slot][C], in the ring's place
+    cp_async_wait<0>();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float *acc = h ? db : dg;
+        if (rpb > 1) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j + 1 < V || last) {
+                float4 *at = reinterpret_cast<float4 *>((rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * 8);
+                at[0] = make_float4(acc[8 * j], acc[8 * j + 1], acc[8 * j + 2], acc[8 * j + 3]);
+                at[1] = make_float4(acc[8 * j + 4], acc[8 * j + 5], acc[8 * j + 6], acc[8 * j + 7]);
+            }
+        if (rpb > 1) {
+            __syncthreads();
+            for (int k = threadIdx.x; k < p.C; k += blockDim.x) {
+                float s = 0.f;
+                for (int i = 0; i < rpb; ++i) s += acc_s[(long long)i * p.C + k];
+                ws0[(long long)h * p.C + k] = s;
+            }
+        }
+    }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+// The launch: V vectors for each of a row's `tpr` threads, `rpb` rows a block.
+struct VecPlan {
+    int v = 0, tpr = 0, rpb = 0;
+};
+
+struct VecKernel {
+    const void *fn;
+    size_t ring;
+    int threads, blocks;  // of a block; blocks an SM's registers hold
+};
+
+// What these kernels take: see the top.
+bool whole(int C, std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor> outs) {
+    auto ok = [](const RowTensor &t, int bytes) { return !t.p || (t.m.cs == 1 && t.m.uniform && dlc_aligned_rows(t, bytes)); };
+    if (C % 8 || !all_of(DLC_DATA_BFLOAT16, ins)) return false;
+    for (const RowTensor &t : ins)
+        if (!ok(t, 16)) return false;
+    for (const RowTensor &t : outs)
+        if (!ok(t, t.dt == DLC_DATA_FLOAT8_E4M3 ? 8 : 16)) return false;
+    return true;
+}
+
+// The fewest threads whose `most` vectors hold a row, whole warps of them from a warp on; more, with
+// fewer vectors, while the rows are too few to give every SM a block.
+VecPlan plan_vec(long long rows, int C, int most, bool warps, int sm_count) {
+    VecPlan p;
+    const int nv = C / 8;
+    p.tpr = 8;
+    while (p.tpr < 32 && p.tpr * std::min(4, most) < nv) p.tpr *= 2;
+    while (p.tpr * most < nv) p.tpr += warps && p.tpr >= 128 ? 32 : p.tpr;
+    while (p.tpr * 2 <= VEC_THREADS && p.tpr < nv && rows * p.tpr * 2 <= (long long)VEC_THREADS * sm_count) p.tpr *= 2;
+    if (p.tpr > VEC_THREADS) return VecPlan();
+    p.v = (nv + p.tpr - 1) / p.tpr;
+    p.rpb = VEC_THREADS / p.tpr;
+    return p;
+}
+
+// `arrays`: channel-wise arrays in shared memory.
+template <typename P>
+dlcStatus_t launch_vec(dlcContext *ctx, const VecKernel &k, P &p, const VecPlan &v, int arrays, int *blocks = nullptr) {
+    int tpr = v.tpr;
+    const size_t smem = k.ring + (size_t)arrays * 8 * v.v * tpr * sizeof(float);
+    const int per_sm = std::max(1, std::min(k.blocks, (int)(NORM_MAX_RING / (smem + 2048))));
+    const long long n = std::min((p.rows + v.rpb - 1) / v.rpb, (long long)ctx->sm_count * per_sm);
+    if (blocks) *blocks = (int)n;
+    void *args[] = {&p, &tpr};
+    if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;
+    return dlc_launch(ctx, k.fn, dim3((unsigned)n), dim3((unsigned)k.threads), smem, args);
+}
+
+template <int V, typename Y, bool RES>
+VecKernel vec_fwd() {
+    return {(const void *)layer_vec_kernel<V, Y, RES>, VecRing<V, RES ? 2 : 1, vec_ring<V>(), VEC_THREADS>::SMEM, VEC_THREADS, vec_blocks<V>()};
+}
+
+template <int V>
+VecKernel vec_fwd(const LayerProblem &p) {
+    const bool res = p.r.p != nullptr;
+    if (p.y.dt == DLC_DATA_BFLOAT16) return res ? vec_fwd<V, unsigned short, true>() : vec_fwd<V, unsigned short, false>();
+    if (p.y.dt == DLC_DATA_FLOAT) return res ? vec_fwd<V, float, true>() : vec_fwd<V, float, false>();
+    return res ? vec_fwd<V, unsigned char, true>() : vec_fwd<V, unsigned char, false>();
+}
+
+VecKernel vec_fwd(int v, const LayerProblem &p) {
+    switch (v) {
+        case 1: return vec_fwd<1>(p);
+        case 2: return vec_fwd<2>(p);
+        case 3: return vec_fwd<3>(p);
+        case 4: return vec_fwd<4>(p);
+        case 5: return vec_fwd<5>(p);
+        case 6: return vec_fwd<6>(p);
+        case 7: return vec_fwd<7>(p);
+        default: return vec_fwd<8>(p);
+    }
+}
+
+template <int V, int TH>
+VecKernel vec_bwd(bool res) {
+    return res ? VecKernel{(const void *)layer_bwd_vec_kernel<V, true, TH>, VecRing<V, 3, 3, TH>::SMEM, TH, 512 / TH}
+               : VecKernel{(const void *)layer_bwd_vec_kernel<V, false, TH>, VecRing<V, 2, 3, TH>::SMEM, TH, 512 / TH};
+}
+
+}  // namespace
+
+bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &pb, dlcStatus_t &status) {
+    LayerProblem p = pb;
+    if (!whole(p.C, {p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != DLC_DATA_BFLOAT16)) return false;
+    const VecPlan v = plan_vec(p.rows, p.C, 8, false, ctx->sm_count);
+    if (!v.v) return false;
+    status = launch_vec(ctx, vec_fwd(v.v, p), p, v, 2);
+    return true;
+}
+
+bool dlc_layer_bwd_vec(dlcContext *ctx, const LayerBwdProblem &pb, dlcStatus_t &status) {
+    LayerBwdProblem p = pb;
+    if (!whole(p.C, {p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != DLC_DATA_BFLOAT16) return false;
+    const VecPlan v = plan_vec(p.rows, p.C, 2, true, ctx->sm_count);
+    if (!v.v) return false;
+    const bool res = p.dt.p != nullptr;
+    int blocks = 0;
+    // (the rows of sums that a block joins need no more than the ring has)
+    status = launch_vec(ctx,
+                        v.v == 1       ? vec_bwd<1, 256>(res)
+                        : v.tpr == 160 ? vec_bwd<2, 160>(res)
+                        : v.tpr == 192 ? vec_bwd<2, 192>(res)
+                        : v.tpr == 224 ? vec_bwd<2, 224>(res)
+                                       : vec_bwd<2, 256>(res),
+                        p, v, 1, &blocks);
+    if (status == DLC_STATUS_SUCCESS && (p.dgamma || p.dbeta))
+        status = dlc_launch_column_sums(ctx, p.ws, p.dgamma, p.dbeta, p.C, blocks);
+    return true;
+}
