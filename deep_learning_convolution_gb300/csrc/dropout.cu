@@ -11,8 +11,6 @@
 // crosses the halves of the products.
 //
 // Bound by memory: x (and r) in, y out.
-#include <type_traits>
-
 #include "channel.cuh"
 #include "ptx.cuh"
 
@@ -20,14 +18,22 @@ namespace {
 
 using namespace dlc;
 
-constexpr int DO_THREADS = 256;
+constexpr int DO_THREADS = 256, DO_BLOCKS = 3;  // blocks an SM holds
 
 struct DoParams {
     DropoutProblem d;
     long long items, inner;  // pieces of a row's channels; the faster index runs over `inner` of them
     int apart;               // ... over the rows, because channels are apart
-    int flat;                // dense rows all: pieces one after the other
+    int rows_step;           // rows that the threads of the vector kernel take at once
 };
+
+constexpr uint32_t PHILOX_M0 = 0xD2511F53u, PHILOX_M1 = 0xCD9E8D57u, PHILOX_W0 = 0x9E3779B9u, PHILOX_W1 = 0xBB67AE85u;
+
+__device__ __forceinline__ void wide(uint32_t a, uint32_t m, uint32_t &hi, uint32_t &lo) {
+    const unsigned long long p = (unsigned long long)a * m;
+    hi = (uint32_t)(p >> 32);
+    lo = (uint32_t)p;
+}
 
 struct Philox {
     uint32_t k0[10], k1[10], s0, s1;  // the rounds' keys, once a thread
@@ -35,22 +41,59 @@ struct Philox {
         const unsigned long long seed = random[0], step = random[1];
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
-            k0[i] = (uint32_t)seed + (uint32_t)i * 0x9E3779B9u;
-            k1[i] = (uint32_t)(seed >> 32) + (uint32_t)i * 0xBB67AE85u;
+            k0[i] = (uint32_t)seed + (uint32_t)i * PHILOX_W0;
+            k1[i] = (uint32_t)(seed >> 32) + (uint32_t)i * PHILOX_W1;
         }
         s0 = (uint32_t)step, s1 = (uint32_t)(step >> 32);
     }
-    __device__ __forceinline__ void words(uint32_t group, uint32_t row, uint32_t (&u)[4]) const {
-        uint32_t a = group, b = row, c = s0, d = s1;
+    // rounds FIRST .. 9
+    template <int FIRST>
+    __device__ __forceinline__ void rounds(uint32_t (&u)[4]) const {
 #pragma unroll
-        for (int i = 0; i < 10; ++i) {
-            const unsigned long long l = (unsigned long long)a * 0xD2511F53u, r = (unsigned long long)c * 0xCD9E8D57u;
-            a = (uint32_t)(r >> 32) ^ b ^ k0[i];
-            c = (uint32_t)(l >> 32) ^ d ^ k1[i];
-            b = (uint32_t)r;
-            d = (uint32_t)l;
+        for (int i = FIRST; i < 10; ++i) {
+            uint32_t lh, ll, rh, rl;
+            wide(u[0], PHILOX_M0, lh, ll);
+            wide(u[2], PHILOX_M1, rh, rl);
+            u[0] = rh ^ u[1] ^ k0[i];
+            u[2] = lh ^ u[3] ^ k1[i];
+            u[1] = rl;
+            u[3] = ll;
         }
-        u[0] = a, u[1] = b, u[2] = c, u[3] = d;
+    }
+    __device__ __forceinline__ void words(uint32_t group, uint32_t row, uint32_t (&u)[4]) const {
+        u[0] = group, u[1] = row, u[2] = s0, u[3] = s1;
+        rounds<0>(u);
+    }
+};
+
+// What the first three rounds owe to the channel alone: with the counter (g, m, s0, s1)
+//   round 0   (hi(M1 s0) ^ m ^ k0,  lo(M1 s0),  hi(M0 g) ^ s1 ^ k1,  lo(M0 g))
+//   round 1   (hi(M1 c) ^ lo(M1 s0) ^ k0',  lo(M1 c),  hi(M0 a) ^ lo(M0 g) ^ k1',  lo(M0 a))
+// where c, round 0's third word, is the channel's and a, its first, the row's; so round 1's first
+// two words are the channel's too, and of round 2's products only one is not.
+struct PhiloxColumn {
+    uint32_t third, product, second;  // lo(M0 g) ^ k1'; hi(M0 first) ^ k1''; lo(M1 c) ^ k0''
+    uint32_t last;                    // lo(M0 first)
+    __device__ __forceinline__ PhiloxColumn(const Philox &p, uint32_t group) {
+        uint32_t hi, lo, h0, l0, first;
+        wide(group, PHILOX_M0, hi, lo);
+        third = lo ^ p.k1[1];
+        wide(p.s0, PHILOX_M1, h0, l0);
+        wide(hi ^ p.s1 ^ p.k1[0], PHILOX_M1, hi, second);
+        first = hi ^ l0 ^ p.k0[1];
+        second ^= p.k0[2];
+        wide(first, PHILOX_M0, product, last);
+        product ^= p.k1[2];
+    }
+    // hi, lo: M0 times round 0's first word
+    __device__ __forceinline__ void words(const Philox &p, uint32_t hi, uint32_t lo, uint32_t (&u)[4]) const {
+        uint32_t rh, rl;
+        wide(hi ^ third, PHILOX_M1, rh, rl);
+        u[0] = rh ^ second;
+        u[1] = rl;
+        u[2] = product ^ lo;
+        u[3] = last;
+        p.rounds<3>(u);
     }
 };
 
@@ -93,84 +136,124 @@ __device__ __forceinline__ void put(const RowTensor &t, long long off, int n, co
     }
 }
 
-// W = 8: rows of whole aligned vectors of eight channels, fewer than 2^31 of them; W = 4: any layout.
-// U pieces a thread are in flight together; a thread steps from piece to piece without dividing.
-template <int W, typename X, typename R, typename Y>
-__global__ void __launch_bounds__(DO_THREADS) dropout_kernel(const __grid_constant__ DoParams p) {
+// Rows of whole aligned vectors at one pitch: a thread keeps its eight channels and steps from row to
+// row, so what the generator owes to the channel is worked out once; U rows are in flight.  What bounds it
+// is the generator: 31 wide multiplies a vector (37 without this) and the 80 other integer instructions.
+template <typename X, typename R, typename Y>
+__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_vec_kernel(const __grid_constant__ DoParams p) {
     griddep_launch_dependents();
-    using I = typename std::conditional<W == 8, uint32_t, long long>::type;
-    constexpr int U = 4;
-    const I items = (I)p.items, inner = (I)p.inner, step = (I)gridDim.x * DO_THREADS;
-    I i = (I)blockIdx.x * DO_THREADS + threadIdx.x;
-    I out = i / inner, in = i - out * inner;
-    const I dout = step / inner, din = step - dout * inner;
+    constexpr int U = sizeof(X) + sizeof(R) > 4 ? 2 : 4;
+    const uint32_t vectors = (uint32_t)p.inner, i = blockIdx.x * DO_THREADS + threadIdx.x;
+    const uint32_t row0 = i / vectors, piece = i - row0 * vectors;
+    if (row0 >= (uint32_t)p.rows_step) return;
+    griddep_wait();
+    const Philox gen(p.d.random);
+    const PhiloxColumn left(gen, 2 * piece), right(gen, 2 * piece + 1);
+    const bool res = p.d.r.p != nullptr;
+    uint32_t h0, l0;
+    wide(gen.s0, PHILOX_M1, h0, l0);
+    h0 ^= gen.k0[0];
+    const long long c = 8ll * piece;
+    const X *px = static_cast<const X *>(p.d.x.p) + row0 * p.d.x.m.ld + c;
+    const R *pr = static_cast<const R *>(p.d.r.p) + row0 * p.d.r.m.ld + c;
+    Y *py = static_cast<Y *>(p.d.y.p) + row0 * p.d.y.m.ld + c;
+    const long long dx = p.rows_step * p.d.x.m.ld, dr = p.rows_step * p.d.r.m.ld, dy = p.rows_step * p.d.y.m.ld;
+    for (long long row = row0; row < p.d.rows; row += (long long)U * p.rows_step) {
+        Piece<8, X> x[U];
+        Piece<8, R> r[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (row + k * p.rows_step < p.d.rows) {
+                x[k].load(p.d.x, px - static_cast<const X *>(p.d.x.p), 8);
+                if (res) r[k].load(p.d.r, pr - static_cast<const R *>(p.d.r.p), 8);
+                px += dx;
+                pr += dr;
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (row + k * p.rows_step >= p.d.rows) break;
+            uint32_t hi, lo, u[8];
+            wide(h0 ^ (uint32_t)(row + k * p.rows_step), PHILOX_M0, hi, lo);
+            left.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u));
+            right.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u + 4));
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 v = mul2(make_float2(x[k].at(j), x[k].at(j + 1)), pair_of(p.d.scale));
+                f[j] = u[j] >= p.d.border ? v.x : 0.f;
+                f[j + 1] = u[j + 1] >= p.d.border ? v.y : 0.f;
+            }
+            if (res) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) set2(f + j, 0, add2(get2(f + j, 0), make_float2(r[k].at(j), r[k].at(j + 1))));
+            }
+            put<8, Y>(p.d.y, py - static_cast<Y *>(p.d.y.p), 8, f);
+            py += dy;
+        }
+    }
+}
+
+// Any layout: pieces of up to four channels, U of a thread in flight together; a thread steps from
+// piece to piece without dividing.
+template <typename X, typename R, typename Y>
+__global__ void __launch_bounds__(DO_THREADS, 2) dropout_kernel(const __grid_constant__ DoParams p) {
+    griddep_launch_dependents();
+    constexpr int U = 4, W = 4;
+    const long long step = (long long)gridDim.x * DO_THREADS;
+    long long i = (long long)blockIdx.x * DO_THREADS + threadIdx.x;
+    long long out = i / p.inner, in = i - out * p.inner;
+    const long long dout = step / p.inner, din = step - dout * p.inner;
     griddep_wait();
     const Philox gen(p.d.random);
     const bool res = p.d.r.p != nullptr;
-    while (i < items) {
+    while (i < p.items) {
         Piece<W, X> x[U];
         Piece<W, R> r[U];
         uint32_t row[U], piece[U];
-        long long at[U];  // element of y
         int n[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             n[k] = 0;
-            if (i < items) {
+            if (i < p.items) {
                 row[k] = (uint32_t)(p.apart ? in : out);
                 piece[k] = (uint32_t)(p.apart ? out : in);
-                n[k] = W == 8 ? 8 : min(W, p.d.C - (int)piece[k] * W);
-                if (p.flat) {
-                    at[k] = (long long)i * W;
-                    x[k].load(p.d.x, at[k], n[k]);
-                    if (res) r[k].load(p.d.r, at[k], n[k]);
-                } else {
-                    const long long c = (long long)piece[k] * W;
-                    at[k] = row_off(p.d.y.m, row[k]) + c * p.d.y.m.cs;
-                    x[k].load(p.d.x, row_off(p.d.x.m, row[k]) + c * p.d.x.m.cs, n[k]);
-                    if (res) r[k].load(p.d.r, row_off(p.d.r.m, row[k]) + c * p.d.r.m.cs, n[k]);
-                }
+                const long long c = (long long)piece[k] * W;
+                n[k] = (int)min((long long)W, p.d.C - c);
+                x[k].load(p.d.x, row_off(p.d.x.m, row[k]) + c * p.d.x.m.cs, n[k]);
+                if (res) r[k].load(p.d.r, row_off(p.d.r.m, row[k]) + c * p.d.r.m.cs, n[k]);
             }
             i += step, out += dout, in += din;
-            if (in >= inner) in -= inner, ++out;
+            if (in >= p.inner) in -= p.inner, ++out;
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (n[k] == 0) break;
             float f[W];
+            uint32_t u[4];
+            gen.words(piece[k], row[k], u);
 #pragma unroll
-            for (int h = 0; h < W / 4; ++h) {
-                uint32_t u[4];
-                gen.words(piece[k] * (W / 4) + h, row[k], u);
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    const int e = 4 * h + j;
-                    const float2 v = mul2(make_float2(x[k].at(e), x[k].at(e + 1)), pair_of(p.d.scale));
-                    f[e] = u[j] >= p.d.border ? v.x : 0.f;
-                    f[e + 1] = u[j + 1] >= p.d.border ? v.y : 0.f;
-                }
-            }
+            for (int j = 0; j < W; ++j) f[j] = u[j] >= p.d.border ? x[k].at(j) * p.d.scale : 0.f;
             if (res) {
 #pragma unroll
-                for (int j = 0; j < W; j += 2) set2(f + j, 0, add2(get2(f + j, 0), make_float2(r[k].at(j), r[k].at(j + 1))));
+                for (int j = 0; j < W; ++j) f[j] += r[k].at(j);
             }
-            put<W, Y>(p.d.y, at[k], n[k], f);
+            put<W, Y>(p.d.y, row_off(p.d.y.m, row[k]) + (long long)piece[k] * W * p.d.y.m.cs, n[k], f);
         }
     }
 }
 
 using Half = unsigned short;
 
-template <int W, typename X, typename R>
-const void *do_kernel(int y) {
-    return y == DLC_DATA_BFLOAT16 ? (const void *)dropout_kernel<W, X, R, Half> : (const void *)dropout_kernel<W, X, R, float>;
+template <typename X, typename R>
+const void *do_kernel(int y, bool vec) {
+    if (y == DLC_DATA_BFLOAT16) return vec ? (const void *)dropout_vec_kernel<X, R, Half> : (const void *)dropout_kernel<X, R, Half>;
+    return vec ? (const void *)dropout_vec_kernel<X, R, float> : (const void *)dropout_kernel<X, R, float>;
 }
 
-template <int W>
-const void *do_kernel(const DropoutProblem &d) {
+const void *do_kernel(const DropoutProblem &d, bool vec) {
     const bool x = d.x.dt == DLC_DATA_BFLOAT16, r = d.r.p ? d.r.dt == DLC_DATA_BFLOAT16 : x;
-    if (x) return r ? do_kernel<W, Half, Half>(d.y.dt) : do_kernel<W, Half, float>(d.y.dt);
-    return r ? do_kernel<W, float, Half>(d.y.dt) : do_kernel<W, float, float>(d.y.dt);
+    if (x) return r ? do_kernel<Half, Half>(d.y.dt, vec) : do_kernel<Half, float>(d.y.dt, vec);
+    return r ? do_kernel<float, Half>(d.y.dt, vec) : do_kernel<float, float>(d.y.dt, vec);
 }
 
 }  // namespace
@@ -178,17 +261,16 @@ const void *do_kernel(const DropoutProblem &d) {
 dlcStatus_t dlc_launch_dropout(dlcContext *ctx, const DropoutProblem &pb) {
     DoParams p;
     p.d = pb;
-    auto vec = [&](const RowTensor &t) { return !t.p || (t.m.cs == 1 && dlc_aligned_rows(t, 16)); };
-    const bool w8 = pb.C % 8 == 0 && vec(pb.x) && vec(pb.r) && vec(pb.y) && pb.rows * (pb.C / 8) < 0x60000000LL;
-    const int w = w8 ? 8 : 4;
+    auto vec = [&](const RowTensor &t) { return !t.p || (t.m.cs == 1 && t.m.uniform && dlc_aligned_rows(t, 16)); };
+    const long long most = (long long)ctx->sm_count * DO_BLOCKS * DO_THREADS;  // threads
+    const bool v8 = pb.C % 8 == 0 && vec(pb.x) && vec(pb.r) && vec(pb.y) && pb.C / 8 <= most;
+    const int w = v8 ? 8 : 4;
     const long long pieces = (pb.C + w - 1) / w;
     p.items = pb.rows * pieces;
     p.apart = pb.x.m.cs != 1 && pb.y.m.cs != 1;
-    p.inner = p.apart ? pb.rows : pieces;
-    auto flat = [&](const RowTensor &t) { return !t.p || (t.m.uniform && (t.m.ld == pb.C || pb.rows == 1)); };
-    p.flat = w8 && flat(pb.x) && flat(pb.r) && flat(pb.y);
-    const void *kern = w8 ? do_kernel<8>(pb) : do_kernel<4>(pb);
-    const long long blocks = std::min<long long>((p.items + DO_THREADS - 1) / DO_THREADS, (long long)ctx->sm_count * 8);
+    p.inner = p.apart && !v8 ? pb.rows : pieces;
+    p.rows_step = (int)std::min(pb.rows, most / pieces);
+    const long long threads = v8 ? p.rows_step * pieces : std::min(p.items, (long long)ctx->sm_count * 2 * DO_THREADS);
     void *args[] = {&p};
-    return dlc_launch(ctx, kern, dim3((unsigned)blocks), dim3(DO_THREADS), 0, args);
+    return dlc_launch(ctx, do_kernel(pb, v8), dim3((unsigned)((threads + DO_THREADS - 1) / DO_THREADS)), dim3(DO_THREADS), 0, args);
 }

@@ -19,10 +19,48 @@ namespace {
 
 using namespace dlc;
 
-constexpr int EM_THREADS = 256;
+constexpr int EM_THREADS = 256, EM_BLOCKS = 3;  // blocks an SM holds
 
 __device__ __forceinline__ long long token_at(const IndexList &t, long long i) {
     return t.wide ? static_cast<const long long *>(t.p)[i] : static_cast<const int *>(t.p)[i];
+}
+
+// W channels: 8 or 4 in one or two accesses, or one.
+template <int W, typename T>
+struct Words {
+    T v[W];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (W * sizeof(T) >= 16) {
+#pragma unroll
+            for (int j = 0; j < W * (int)sizeof(T) / 16; ++j) reinterpret_cast<uint4 *>(v)[j] = reinterpret_cast<const uint4 *>(p)[j];
+        } else if constexpr (W * sizeof(T) == 8) {
+            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+        } else {
+            v[0] = p[0];
+        }
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if constexpr (sizeof(T) == 2)
+            return bf16_bits_f32(v[j]);
+        else
+            return v[j];
+    }
+};
+
+template <int W, typename T>
+__device__ __forceinline__ void store_words(T *dst, const float (&f)[W]) {
+    if constexpr (W == 1) {
+        store_elem(dst, sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j)
+            reinterpret_cast<float4 *>(dst)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    } else if constexpr (W == 8) {
+        *reinterpret_cast<uint4 *>(dst) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    }
 }
 
 // ---- forward -----------------------------------------------------------------------
@@ -34,81 +72,68 @@ struct EmParams {
     int *err;
 };
 
-// W = 8: eight channels a piece in 16-byte accesses; W = 1: any layout of y.
+// W = 8: eight channels a piece in 16-byte accesses; W = 1: any layout of y.  U pieces a thread are
+// in flight together, and the tokens of the next ones.
 template <int W, typename T, typename Y>
-__global__ void __launch_bounds__(EM_THREADS) embedding_kernel(const __grid_constant__ EmParams p) {
+__global__ void __launch_bounds__(EM_THREADS, EM_BLOCKS) embedding_kernel(const __grid_constant__ EmParams p) {
     griddep_launch_dependents();
     constexpr int U = W == 8 ? 4 : 8;
     const long long step = (long long)gridDim.x * EM_THREADS;
     long long i = (long long)blockIdx.x * EM_THREADS + threadIdx.x;
-    long long row = i / p.pieces;
-    int piece = (int)(i - row * p.pieces);
-    const long long drow = step / p.pieces;
-    const int dpiece = (int)(step - drow * p.pieces);
+    uint32_t row = (uint32_t)(i / p.pieces);  // (may run past the last one)
+    int piece = (int)(i - (long long)row * p.pieces);
+    const int drow = (int)(step / p.pieces), dpiece = (int)(step - (long long)drow * p.pieces);
     griddep_wait();
-    for (; i < p.items;) {
-        long long token[U], at[U];
-        T v[U][W];
+    long long token[U];
+    int at_row[U], at_piece[U];
+    // the next U pieces' places and tokens (row -1: none)
+    auto next = [&]() {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            at[k] = -1;
-            if (i < p.items) {
-                token[k] = token_at(p.e.tokens, row);
-                at[k] = row_off(p.e.y.m, row) + (long long)piece * W * p.e.y.m.cs;
-                const bool there = token[k] >= 0 && token[k] < p.e.V;
-                if (token[k] >= p.e.V && piece == 0) record_error(p.err, DLC_DEVERR_INDEX, (int)min(row, 0x7fffffffLL));
-                const T *src = static_cast<const T *>(p.e.table.p) + (there ? token[k] : 0) * p.e.C + (long long)piece * W;
-                if (there) {
-                    if constexpr (W == 8) {
-#pragma unroll
-                        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-                            reinterpret_cast<uint4 *>(v[k])[j] = reinterpret_cast<const uint4 *>(src)[j];
-                    } else {
-                        v[k][0] = src[0];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[k][j] = (T)0;
-                }
-            }
+            at_row[k] = i < p.items ? (int)row : -1;
+            at_piece[k] = piece;
+            token[k] = i < p.items ? token_at(p.e.tokens, row) : -1;
             i += step, row += drow, piece += dpiece;
             if (piece >= p.pieces) piece -= p.pieces, ++row;
         }
+    };
+    next();
+    while (at_row[0] >= 0) {
+        Words<W, T> v[U];
+        long long at[U];
+        bool there[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            there[k] = token[k] >= 0 && token[k] < p.e.V;
+            at[k] = at_row[k] < 0 ? -1 : row_off(p.e.y.m, at_row[k]) + (long long)at_piece[k] * W * p.e.y.m.cs;
+            if (there[k]) v[k].load(static_cast<const T *>(p.e.table.p) + token[k] * p.e.C + (long long)at_piece[k] * W);
+            if (token[k] >= p.e.V && at_piece[k] == 0) record_error(p.err, DLC_DEVERR_INDEX, at_row[k]);
+        }
+        next();
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (at[k] < 0) break;
             float f[W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if constexpr (sizeof(T) == 2)
-                    f[j] = bf16_bits_f32(v[k][j]) * p.e.scale;
-                else
-                    f[j] = v[k][j] * p.e.scale;
-                if (token[k] < 0 || token[k] >= p.e.V) f[j] = 0.f;  // (whatever the scale)
-            }
-            Y *dst = static_cast<Y *>(p.e.y.p) + at[k];
-            if constexpr (W == 8 && sizeof(Y) == 2) {
-                *reinterpret_cast<uint4 *>(dst) =
-                    make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-            } else if constexpr (W == 8) {
-                reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-                store_elem(dst, sizeof(Y) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
-            }
+            for (int j = 0; j < W; ++j) f[j] = there[k] ? v[k].at(j) * p.e.scale : 0.f;
+            store_words<W, Y>(static_cast<Y *>(p.e.y.p) + at[k], f);
         }
     }
 }
 
 // ---- the tokens in order -------------------------------------------------------------
 //
-// Least significant digit first, a digit at most ten bits.  A tile of 2048 tokens keeps its
-// tokens in registers; the histograms of all tiles give every digit's place (the next pass's
+// Least significant digit first, a digit at most ten bits.  A tile keeps its tokens in
+// registers; the histograms of all tiles give every digit's place (the next pass's
 // are counted while this one writes).  Tokens outside the table sort behind all others,
 // as number V.
 
-constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32, SORT_EACH = 4, SORT_TILE = SORT_THREADS * SORT_EACH;
 constexpr int SORT_MAX_BITS = 10, SORT_MAX_DIGITS = 1 << SORT_MAX_BITS;
+
+constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32, SORT_EACH = 4, SORT_TILE = SORT_THREADS * SORT_EACH;
+// Lists of up to RANK_MOST tokens are ranked by counting (8192 x 256 into 1003 rows: 33 us, by digits 18; up to
+// 2048 tokens as fast or faster, in one launch).
+constexpr int RANK_MOST = 4096, RANK_THREADS = 256;
 
 struct SortParams {
     IndexList tokens;
@@ -153,8 +178,8 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams &p, int i) {
     return t < 0 || t >= p.V ? (uint32_t)p.V : (uint32_t)t;
 }
 
-// base[d] = the place of this tile's first token of digit d: totals[d] summed over smaller
-// digits, and `before` of them in the tiles ahead.  Two digits a thread.
+// base[d] = the place of this tile's first token of digit d: totals summed over smaller
+// digits, and `before` of d in the tiles ahead.  Two digits a thread.
 __device__ __forceinline__ void sort_places(SortShared &s, const int (&total)[2], const int (&before)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int own = total[0] + total[1];
@@ -190,13 +215,8 @@ __device__ __forceinline__ void sort_ranks(SortShared &s, const uint32_t (&keys)
     }
 }
 
-__device__ __forceinline__ void sort_clear(SortShared &s) {
-    for (int i = threadIdx.x; i < SORT_WARPS * SORT_MAX_DIGITS / 2; i += SORT_THREADS) reinterpret_cast<uint32_t *>(s.count)[i] = 0u;
-    __syncthreads();
-}
-
-// s.count: from each warp's counts to the sum of those of the warps before it; returns the totals.
-__device__ __forceinline__ void sort_warps(SortShared &s, int (&total)[2]) {
+// s.count: from each warp's counts to the sum of those of the warps before it.
+__device__ __forceinline__ void sort_warps(SortShared &s) {
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -207,64 +227,64 @@ __device__ __forceinline__ void sort_warps(SortShared &s, int (&total)[2]) {
             s.count[w][d] = (unsigned short)sum;
             sum += c;
         }
-        total[h] = sum;
     }
 }
 
-struct SortTile {
-    SortShared s;
-    uint32_t key[SORT_TILE], row[SORT_TILE];
-};
-
-// Up to a tile of tokens: all passes by one block.
-__global__ void __launch_bounds__(SORT_THREADS) sort_tile_kernel(const __grid_constant__ SortParams p) {
+// Short lists: a token's place is how many come before it, counted over all of them.  A block ranks 32
+// tokens, a lane each, its warps dealing with a part of the list each; in one launch and without
+// steps that wait for one another (a block that sorted 5000 tokens alone took 10 us).
+__global__ void __launch_bounds__(RANK_THREADS) rank_kernel(const __grid_constant__ SortParams p) {
     griddep_launch_dependents();
-    extern __shared__ uint4 tile_s[];
-    SortTile &tile = *reinterpret_cast<SortTile *>(tile_s);
-    SortShared &s = tile.s;
+    __shared__ uint4 key_s[RANK_MOST / 4];
+    __shared__ int part[RANK_THREADS / 32][32];
     griddep_wait();
-    if (blockIdx.x > 0) {
+    if ((int)blockIdx.x >= p.blocks) {
         fill_part(p);
         return;
     }
-    const int first = (int)(threadIdx.x >> 5) * 32 * SORT_EACH + (int)(threadIdx.x & 31);
-    uint32_t key[SORT_EACH], row[SORT_EACH];
-    bool on[SORT_EACH];
-    const uint32_t mask = (1u << p.bits) - 1u;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(key_s);
+    constexpr int U = 8;
+    for (int i0 = threadIdx.x; i0 < p.rows; i0 += U * RANK_THREADS) {
+        long long t[U];
 #pragma unroll
-    for (int k = 0; k < SORT_EACH; ++k) {
-        row[k] = (uint32_t)(first + 32 * k);
-        on[k] = (int)row[k] < p.rows;
-        key[k] = on[k] ? sort_key(p, (int)row[k]) : 0u;
+        for (int k = 0; k < U; ++k) t[k] = i0 + k * RANK_THREADS < p.rows ? token_at(p.tokens, i0 + k * RANK_THREADS) : 0;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + k * RANK_THREADS < p.rows) keys[i0 + k * RANK_THREADS] = t[k] < 0 || t[k] >= p.V ? (uint32_t)p.V : (uint32_t)t[k];
     }
-    for (int pass = 0; pass < p.passes; ++pass) {
-        int rank[SORT_EACH], total[2];
-        const int none[2] = {0, 0};
-        sort_clear(s);
-        sort_ranks(s, key, on, pass * p.bits, mask, rank);
-        sort_warps(s, total);
-        sort_places(s, total, none);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < SORT_EACH; ++k)
-            if (on[k]) {
-                const uint32_t d = (key[k] >> (pass * p.bits)) & mask;
-                const int at = s.base[d] + s.count[threadIdx.x >> 5][d] + rank[k];
-                tile.key[at] = key[k];
-                tile.row[at] = row[k];
-            }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < SORT_EACH; ++k)
-            if (on[k]) key[k] = tile.key[first + 32 * k], row[k] = tile.row[first + 32 * k];
+    const int quads = (p.rows + 3) / 4;
+    if (threadIdx.x < 4 * quads - p.rows) keys[p.rows + threadIdx.x] = 0xffffffffu;  // behind all tokens
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = (int)blockIdx.x * 32, i = first + lane;
+    const uint32_t mine = i < p.rows ? keys[i] : 0u;
+    const int q0 = quads * warp / (RANK_THREADS / 32), q1 = quads * (warp + 1) / (RANK_THREADS / 32);
+    const int b0 = min(max(first / 4, q0), q1), b1 = min(max(first / 4 + 8, q0), q1);
+    int n = 0;
+#pragma unroll 4
+    for (int q = q0; q < b0; ++q) {  // tokens ahead of the block's: equal ones count
+        const uint4 k = key_s[q];
+        n += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
     }
-    const int last = (p.passes - 1) & 1;
-#pragma unroll
-    for (int k = 0; k < SORT_EACH; ++k)
-        if (on[k]) {
-            p.key[last][first + 32 * k] = key[k];
-            p.row[last][first + 32 * k] = row[k];
-        }
+    for (int q = b0; q < b1; ++q) {
+        const uint4 k = key_s[q];
+        const int j = 4 * q;
+        n += (k.x < mine || (k.x == mine && j < i)) + (k.y < mine || (k.y == mine && j + 1 < i)) +
+             (k.z < mine || (k.z == mine && j + 2 < i)) + (k.w < mine || (k.w == mine && j + 3 < i));
+    }
+#pragma unroll 4
+    for (int q = b1; q < q1; ++q) {
+        const uint4 k = key_s[q];
+        n += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+    }
+    part[warp][lane] = n;
+    __syncthreads();
+    if (warp == 0 && i < p.rows) {
+        for (int w = 1; w < RANK_THREADS / 32; ++w) n += part[w][lane];
+        p.key[0][n] = mine;
+        p.row[0][n] = (uint32_t)i;
+        const long long t = token_at(p.tokens, i);
+        if (t >= p.V) record_error(p.err, DLC_DEVERR_INDEX, i);
+    }
 }
 
 // The first pass's histograms; zeroes those of the others.
@@ -305,7 +325,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
         fill_part(p);
         return;
     }
-    sort_clear(s);
+    for (int i = threadIdx.x; i < SORT_WARPS * SORT_MAX_DIGITS / 2; i += SORT_THREADS) reinterpret_cast<uint32_t *>(s.count)[i] = 0u;
+    __syncthreads();
     griddep_wait();
     const int tile = blockIdx.x, digits = 1 << p.bits;
     const int first = (int)(threadIdx.x >> 5) * 32 * SORT_EACH + (int)(threadIdx.x & 31);
@@ -321,9 +342,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
             key[k] = pass == 0 ? sort_key(p, (int)i) : p.key[(pass - 1) & 1][i];
         }
     }
-    int rank[SORT_EACH], total[2], all[2] = {0, 0}, before[2] = {0, 0};
+    int rank[SORT_EACH], all[2] = {0, 0}, before[2] = {0, 0};
     const uint32_t mask = (uint32_t)digits - 1u;
-    sort_ranks(s, key, on, pass * p.bits, mask, rank);
     const int *hist = p.hist + (long long)pass * p.tiles * digits;
     if (2 * (int)threadIdx.x < digits) {
 #pragma unroll 8
@@ -333,7 +353,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
             if (t < tile) before[0] += c.x, before[1] += c.y;
         }
     }
-    sort_warps(s, total);
+    sort_ranks(s, key, on, pass * p.bits, mask, rank);
+    sort_warps(s);
     sort_places(s, all, before);
     __syncthreads();
     const bool more = pass + 1 < p.passes;
@@ -352,6 +373,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
 // ---- sums by token ---------------------------------------------------------------------
 
 constexpr int SUM_THREADS = 128, SUM_MAX_CHUNK = 128;  // threads of a block at most
+constexpr int JOIN_THREADS = 512;
 
 struct SumParams {
     EmbeddingProblem e;        // y: dy; table: dtable
@@ -359,44 +381,6 @@ struct SumParams {
     float *part;               // [chunk][2][C]: of the token that comes in, of the one that goes on
     int chunk, chunks, slabs;  // sorted positions of a chunk
 };
-
-// W channels: 8 or 4 in one or two accesses, or one.
-template <int W, typename T>
-struct Words {
-    T v[W];
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (W * sizeof(T) >= 16) {
-#pragma unroll
-            for (int j = 0; j < W * (int)sizeof(T) / 16; ++j) reinterpret_cast<uint4 *>(v)[j] = reinterpret_cast<const uint4 *>(p)[j];
-        } else if constexpr (W * sizeof(T) == 8) {
-            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
-        } else {
-            v[0] = p[0];
-        }
-    }
-    __device__ __forceinline__ float at(int j) const {
-        if constexpr (sizeof(T) == 2)
-            return bf16_bits_f32(v[j]);
-        else
-            return v[j];
-    }
-};
-
-template <int W, typename T>
-__device__ __forceinline__ void store_words(T *dst, const float (&f)[W]) {
-    if constexpr (W == 1) {
-        store_elem(dst, sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < W / 4; ++j)
-            reinterpret_cast<float4 *>(dst)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-    } else if constexpr (W == 8) {
-        *reinterpret_cast<uint4 *>(dst) =
-            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-    } else {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-    }
-}
 
 // W = 8, 4: aligned vectors of dy and of the table; W = 1: any layout of dy, any size.  ACC: the sums
 // are added to the table's rows, which are loaded beside the rows of dy that end a token (one by
@@ -426,7 +410,7 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
     float acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) acc[j] = 0.f;
-    constexpr int U = ACC || W * sizeof(D) > 16 ? 4 : 8;  // rows in flight
+    constexpr int U = W * sizeof(D) > 16 || (ACC && W * sizeof(T) > 16) ? 4 : 8;  // rows in flight
     for (int i0 = 0; i0 < n; i0 += U) {
         Words<W, D> v[U];
         Words<W, T> old[ACC ? U : 1];
@@ -467,11 +451,12 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
     }
 }
 
-// Tokens whose rows reach over several chunks: the block of the chunk where they begin adds
-// up the partial sums in order.
+// Tokens whose rows reach over several chunks: the block of the chunk where they begin adds up the
+// partial sums, a range of them by each of its groups of `width` threads, always in the same order.
 template <int W, typename T, bool ACC>
-__global__ void __launch_bounds__(SUM_THREADS) embedding_join_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const __grid_constant__ SumParams p, int width) {
     griddep_launch_dependents();
+    __shared__ float sum_s[JOIN_THREADS * W];
     griddep_wait();
     const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
     const long long end = (long long)(chunk + 1) * p.chunk;  // (the last chunk has no block)
@@ -485,31 +470,42 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_join_kernel(const __gri
         more += found;
         if (found < (int)blockDim.x) break;
     }
-    const int c = (slab * (int)blockDim.x + (int)threadIdx.x) * W;
-    if (c >= p.e.C) return;
-    const float *src = p.part + ((long long)chunk * 2 + 1) * p.e.C + c;
+    const int groups = (int)blockDim.x / width, group = (int)threadIdx.x / width, t = (int)threadIdx.x - group * width;
+    const int c = (slab * width + t) * W;
+    const bool on = c < p.e.C;
     T *dst = static_cast<T *>(p.e.table.p) + (long long)token * p.e.C + c;
     Words<W, T> old;
-    if constexpr (ACC) old.load(dst);
-    Words<W, float> q;
-    q.load(src);
+    if constexpr (ACC)
+        if (on && group == 0) old.load(dst);
     float acc[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc[j] = q.v[j];
-    src += p.e.C;  // the next chunk's first slot
-    constexpr int U = 8;
-    for (int k0 = 0; k0 < more; k0 += U) {
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+    // parts 0 (this chunk's second slot) and 1 .. more (the next ones' first slots)
+    const int k1 = (int)((long long)(more + 1) * (group + 1) / groups);
+    constexpr int U = W == 8 ? 4 : 8;
+    for (int k0 = (int)((long long)(more + 1) * group / groups); on && k0 < k1; k0 += U) {
         Words<W, float> part[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (k0 + k < more) part[k].load(src + (long long)(k0 + k) * 2 * p.e.C);
+            if (k0 + k < k1) part[k].load(p.part + ((long long)(chunk + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * p.e.C + c);
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (k0 + k < more) {
+            if (k0 + k < k1) {
 #pragma unroll
                 for (int j = 0; j < W; ++j) acc[j] += part[k].v[j];
             }
     }
+    if (groups > 1) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum_s[j * JOIN_THREADS + threadIdx.x] = acc[j];
+        __syncthreads();
+        if (group) return;
+        for (int g = 1; g < groups; ++g) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j] += sum_s[j * JOIN_THREADS + g * width + t];
+        }
+    }
+    if (!on) return;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         acc[j] *= p.e.scale;
@@ -566,8 +562,11 @@ BwdPlan plan_bwd(long long rows, int C, int V) {
     b.passes = (bits + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
     b.bits = (bits + b.passes - 1) / b.passes;
     b.tiles = (int)((rows + SORT_TILE - 1) / SORT_TILE);
-    // long lists: fewer partial sums of a frequent token to join
-    b.chunk = rows > 65536 ? SUM_MAX_CHUNK : 32;
+    if (rows <= RANK_MOST) b.passes = 1;
+    // Positions of a chunk: few where that gives the GPU enough to do at once, and where there are
+    // more than enough many, so that a frequent token leaves fewer partial sums.
+    const long long warps = rows * ((C + 255) / 256);
+    b.chunk = warps <= 16 * 4096 ? 16 : warps <= 128 * 4096 ? 32 : warps <= 512 * 4096 ? 64 : SUM_MAX_CHUNK;
     b.chunks = (int)((rows + b.chunk - 1) / b.chunk);
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -594,7 +593,7 @@ dlcStatus_t dlc_launch_embedding(dlcContext *ctx, const EmbeddingProblem &e) {
     const bool bf = e.table.dt == DLC_DATA_BFLOAT16;
     const void *kern = w8 ? (bf ? fwd_kernel<8, Half>(e.y.dt) : fwd_kernel<8, float>(e.y.dt))
                           : (bf ? fwd_kernel<1, Half>(e.y.dt) : fwd_kernel<1, float>(e.y.dt));
-    const long long blocks = std::min<long long>((p.items + EM_THREADS - 1) / EM_THREADS, (long long)ctx->sm_count * 8);
+    const long long blocks = std::min<long long>((p.items + EM_THREADS - 1) / EM_THREADS, (long long)ctx->sm_count * EM_BLOCKS);
     void *args[] = {&p};
     return dlc_launch(ctx, kern, dim3((unsigned)blocks), dim3(EM_THREADS), 0, args);
 }
@@ -620,7 +619,8 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     const size_t bytes = e.accumulate ? 0 : (size_t)e.V * e.C * dlc_dtype_bytes((dlcDataType_t)e.table.dt);
     char *table = static_cast<char *>(e.table.p);
     const size_t head = std::min(bytes, (16 - (uintptr_t)table % 16) % 16), words = (bytes - head) / 16;
-    const int launches = b.tiles == 1 ? 1 : 1 + b.passes;
+    const bool ranked = e.rows <= RANK_MOST;
+    const int launches = ranked ? 1 : 1 + b.passes;
     auto part = [&](int i) {
         const size_t w0 = words * i / launches, w1 = words * (i + 1) / launches;
         s.fill = table + head + 16 * w0;
@@ -633,11 +633,9 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     };
     dlcStatus_t st;
     void *args[] = {&s};
-    if (b.tiles == 1) {
-        s.blocks = 1;
-        const unsigned fill = part(0);
-        if (!dlc_allow_smem(ctx, (const void *)sort_tile_kernel, sizeof(SortTile))) return DLC_STATUS_EXECUTION_FAILED;
-        st = dlc_launch(ctx, (const void *)sort_tile_kernel, dim3(1 + fill), dim3(SORT_THREADS), sizeof(SortTile), args);
+    if (ranked) {
+        s.blocks = (int)((e.rows + 31) / 32);
+        st = dlc_launch(ctx, (const void *)rank_kernel, dim3((unsigned)s.blocks + 2 * part(0)), dim3(RANK_THREADS), 0, args);
         if (st != DLC_STATUS_SUCCESS) return st;
     } else {
         s.blocks = std::min(b.tiles, ctx->sm_count * 4);
@@ -667,5 +665,7 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs)), dim3((unsigned)threads), 0, sargs);
     if (st != DLC_STATUS_SUCCESS || p.chunks == 1) return st;
     const void *join = w == 8 ? join_kernel<8>(e) : w == 4 ? join_kernel<4>(e) : join_kernel<1>(e);
-    return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3((unsigned)threads), 0, sargs);
+    int width = threads;
+    void *jargs[] = {&p, &width};
+    return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3((unsigned)(JOIN_THREADS / width * width)), 0, jargs);
 }

@@ -103,20 +103,20 @@ __device__ __forceinline__ void vec_param(uint32_t at, uint32_t half, float (&g)
     g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
 }
 
-// Fills vec_param's arrays, whose vectors are dealt to `tpr` threads: by copies that the first row's
-// wait covers, or, from an unaligned address, directly.  Zeros behind the row.
+// Fills vec_param's arrays, whose vectors are dealt to `tpr` threads; zeros behind the row.  (By
+// asynchronous copies ahead of the rows' a call of 65536 x 768 took 4 us more, element by element
+// one of 16384 x 2048 5 us.)
 __device__ __forceinline__ void vec_param_fill(float *dst, const float *src, int C, int tpr, int V) {
     const bool aligned = ((uintptr_t)src & 15u) == 0;
+#pragma unroll 4
     for (int i = threadIdx.x; i < 2 * tpr * V; i += blockDim.x) {  // half-vectors
         const int vec = i >> 1, at = (vec / tpr * 2 + (i & 1)) * tpr + vec % tpr;
-        const bool there = src && 4 * i < C;
-        if (there && aligned) {
-            cp_async_16(smem_u32(dst) + 16u * (uint32_t)at, src + 4 * i, 16u);
-        } else {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (there) v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
-            reinterpret_cast<float4 *>(dst)[at] = v;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src && 4 * i < C) {
+            if (aligned) v = reinterpret_cast<const float4 *>(src)[i];
+            else v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
         }
+        reinterpret_cast<float4 *>(dst)[at] = v;
     }
 }
 
@@ -176,10 +176,9 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         x.p += x.inc;
         r.p += r.inc;
     };
+    for (int i = 0; i < S; ++i) fetch();
     vec_param_fill(gamma, p.gamma, p.C, tpr, V);
     vec_param_fill(beta, p.beta, p.C, tpr, V);
-    for (int i = 0; i < S; ++i) fetch();
-    cp_async_wait<S - 1>();
     __syncthreads();
     int parity = 0;
     for (; row - slot < p.rows; row += step) {  // (as many rounds for every thread of the block)
@@ -285,9 +284,8 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         tt.p += tt.inc;
         dt.p += dt.inc;
     };
-    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
     for (int i = 0; i < S; ++i) fetch();
-    cp_async_wait<S - 1>();
+    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
     __syncthreads();
     for (; row - slot < p.rows; row += step, dx.p += dx.inc) {
         const bool on = row < p.rows;
