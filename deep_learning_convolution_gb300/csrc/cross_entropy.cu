@@ -52,7 +52,8 @@ struct CeParams {
     long long ld;
     IndexList target;
     float2 *part;              // [part][M] (r, s)
-    int part0, parts;          // first part of this piece; of all pieces
+    int part0, parts;          // first part of this piece; how many there are when they are joined
+    int last;                  // the rows' sums are complete, else part 0 takes what they are so far
     float *chosen;             // [M] the target's logit
     float *loss, *lse;
     const float *dloss;
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(CE_THREADS) ce_part_kernel(const __grid_consta
 }
 
 // Joins the parts of 32 rows a block, in a fixed order: a lane a row, the parts dealt to the warps.
+// (Parts of many rows and classes would take a 32nd of what BF16 logits take: several pieces then
+// share the workspace, each adding to part 0.)
 __global__ void __launch_bounds__(1024) ce_loss_kernel(const __grid_constant__ CeParams p) {
     griddep_launch_dependents();
     __shared__ CePart warps[32][33];
@@ -126,6 +129,10 @@ __global__ void __launch_bounds__(1024) ce_loss_kernel(const __grid_constant__ C
     __syncthreads();
     if (warp == 0 && m < p.M) {
         for (int i = 1; i < 32; ++i) a = ce_join(a, warps[i][lane]);
+        if (!p.last) {
+            const_cast<float2 *>(p.part)[m] = make_float2(a.r, a.s);
+            return;
+        }
         const float lse = isinf(a.r) ? log2f(a.s) * LN2 : fmaf(a.r, LN2, logf(a.s));
         const long long k = ce_target(p.target, m);
         float loss = 0.f;
@@ -190,6 +197,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // 2048 -> 131072 / 8192 x 512 -> 65536 in pieces of 128 MB: 4022 / 1533 us, 256 MB 3913 / 1345,
 // 512 MB 3836 / 1230, 1 GB 3893 / 1097: what a piece costs is dx's last wave and its FP32 sum.
 constexpr size_t CE_PIECE_BYTES = (size_t)512 << 20;
+constexpr size_t CE_PART_BYTES = (size_t)256 << 20;  // the same for the parts of fused products
 
 // Classes of a piece of `bytes`-sized elements a row and class.
 int piece_of(const CrossEntropyProblem &p, int bytes) {
@@ -352,7 +360,9 @@ bool fuse(const CrossEntropyProblem &p) { return p.M > 32; }
 CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan f(ws);
     f.fused = fuse(p);
-    f.piece = f.fused ? p.V : piece_of(p, 4);
+    // (a part: 32 classes at least)
+    f.piece = f.fused ? (int)std::min<long long>(p.V, std::max<long long>(1024, (long long)(CE_PART_BYTES / 8) / p.M * 32 / 256 * 256))
+                      : piece_of(p, 4);
     f.operands(p);
     if (!f.fused) {
         f.ld = (f.piece + 3) / 4 * 4;
@@ -360,7 +370,7 @@ CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     }
     size_t most = 0;
     f.each(p, [&](int n0, int cols) {
-        f.parts += f.parts_of(ctx, p, n0, cols);
+        f.parts = std::max(f.parts, 1 + f.parts_of(ctx, p, n0, cols));
         most = std::max(most, dlc_gemm_workspace(ctx, f.fused ? f.fused_logits(p, ENTROPY_PARTS, n0, cols, 0) : f.logits(p, n0, cols)));
         return DLC_STATUS_SUCCESS;
     });
@@ -406,7 +416,6 @@ CeParams params(const dlcContext *ctx, const CrossEntropyProblem &p, const CePla
     c.ld = f.ld;
     c.target = p.target;
     c.part = f.part;
-    c.parts = f.parts;
     c.chosen = f.chosen;
     c.loss = p.loss;
     c.lse = p.lse;
@@ -425,9 +434,10 @@ size_t dlc_cross_entropy_workspace(const dlcContext *ctx, const CrossEntropyProb
 dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem &p) {
     const CePlan f = plan_fwd(ctx, p, p.ws);
     CeParams c = params(ctx, p, f);
-    const dlcStatus_t st = f.each(p, [&](int n0, int cols) {
+    return f.each(p, [&](int n0, int cols) {
         dlcStatus_t s = f.pack(ctx, p, n0, cols);
         if (s != DLC_STATUS_SUCCESS) return s;
+        c.part0 = n0 ? 1 : 0;
         if (f.fused) {
             s = dlc_launch_gemm(ctx, f.fused_logits(p, ENTROPY_PARTS, n0, cols, c.part0));
         } else {
@@ -438,12 +448,12 @@ dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem 
             void *args[] = {&c};
             s = dlc_launch(ctx, (const void *)ce_part_kernel, dim3((unsigned)p.M, (unsigned)segments(cols)), dim3(CE_THREADS), 0, args);
         }
-        c.part0 += f.parts_of(ctx, p, n0, cols);
-        return s;
+        if (s != DLC_STATUS_SUCCESS) return s;
+        c.parts = c.part0 + f.parts_of(ctx, p, n0, cols);
+        c.last = n0 + cols == p.V;
+        void *args[] = {&c};
+        return dlc_launch(ctx, (const void *)ce_loss_kernel, dim3((unsigned)((p.M + 31) / 32)), dim3(1024), 0, args);
     });
-    if (st != DLC_STATUS_SUCCESS) return st;
-    void *args[] = {&c};
-    return dlc_launch(ctx, (const void *)ce_loss_kernel, dim3((unsigned)((p.M + 31) / 32)), dim3(1024), 0, args);
 }
 
 size_t dlc_cross_entropy_bwd_workspace(const dlcContext *ctx, const CrossEntropyProblem &p) { return plan_bwd(ctx, p, nullptr).bytes; }

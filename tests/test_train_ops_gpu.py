@@ -421,7 +421,7 @@ def check_entropy(handle, x, w, b, target, dloss, dx_dtype=BF, dw_dtype=BF, layo
     return loss, lse, dx, dw, db
 
 
-ENTROPY_SIZES = [(1, 1, 1), (1, 64, 1000), (3, 8, 2), (5, 7, 11), (4, 512, 5001), (33, 130, 257), (64, 256, 1000), (200, 147, 1003),
+ENTROPY_SIZES = [(1, 1, 1), (100, 64, 1), (90, 8, 7), (1, 64, 1000), (3, 8, 2), (5, 7, 11), (4, 512, 5001), (33, 130, 257), (64, 256, 1000), (200, 147, 1003),
                  (300, 64, 256), (256, 512, 4096), (513, 72, 777), (1000, 128, 9000), (2, 64, 70000), (17, 1032, 12345)]
 
 
@@ -444,7 +444,41 @@ def test_cross_entropy_in_pieces_of_the_classes(handle, rows, c, v, dx_dtype):
     check_entropy(handle, *entropy_case(rows, c, v, True), dx_dtype=dx_dtype)
 
 
-@pytest.mark.parametrize("rows,c,v", [(3, 64, 1000), (70, 160, 3001), (700, 256, 5000)])
+def test_cross_entropy_of_few_rows_and_millions_of_classes(handle):
+    """Logits in memory, in two pieces."""
+    check_entropy(handle, *entropy_case(32, 8, 4300000, True))
+
+
+def test_cross_entropy_of_many_rows_in_pieces(handle):
+    """The rows' sums join those of the pieces before."""
+    rows, c, v = 60000, 16, 20011
+    x, w, b, target, _ = entropy_case(rows, c, v, True)
+    loss, lse = out_like(rows, 1, F32)[:, 0], out_like(rows, 1, F32)[:, 0]
+    api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, bias=b)
+    for r in range(0, rows, 10000):
+        at = slice(r, r + 10000)
+        f = ref.cross_entropy(d(x[at]), d(w), target[at], d(b))
+        close(lse[at], *f["lse"], "lse")
+        close(loss[at], *f["loss"], "loss")
+
+
+def test_cross_entropy_of_images(handle):
+    """A class for every pixel, planar and channels last."""
+    x, w = rand(3, 24, 9, 11, seed=1, dtype=BF), rand(19, 24, seed=2, std=0.5, dtype=BF)
+    target, dloss = classes_of(3 * 9 * 11, 19, 3).view(3, 9, 11), rand(3, 9, 11, seed=4).abs()
+    last = x.permute(0, 2, 3, 1).contiguous()
+    want = check_entropy(handle, last.view(-1, 24), w, None, target.view(-1), dloss.view(-1))
+    for image, axes in ((x, "NCHW"), (last, "NHWC")):
+        loss, lse, dx, dw = torch.empty_like(dloss), torch.empty_like(dloss), torch.empty_like(image), torch.empty_like(w)
+        api.CrossEntropyForward(handle, image, w, target, axes=axes)(image, w, target, loss, lse)
+        api.CrossEntropyBackward(handle, image, w, target, dx, dw, axes=axes)(image, w, target, lse, dloss, dx, dw)
+        for got, ref_, rel in ((loss, want[0], 1e-5), (dw, want[3], 2.0 ** -7)):
+            assert (got.reshape(ref_.shape).float() - ref_.float()).abs().max() <= rel * ref_.float().abs().max()
+        rows = (dx.permute(0, 2, 3, 1) if axes == "NCHW" else dx).reshape(-1, 24)
+        assert (rows.float() - want[2].float()).abs().max() <= 2.0 ** -7 * want[2].float().abs().max()
+
+
+@pytest.mark.parametrize("rows,c,v", [(3, 64, 1000), (70, 160, 3001), (700, 256, 5000), (50, 33, 70)])
 def test_cross_entropy_of_e4m3(handle, rows, c, v):
     x, w, b, target, _ = entropy_case(rows, c, v, True)
     sx, sw = (t.float().abs().amax(1) / 448 for t in (x, w))
