@@ -1,5 +1,5 @@
-// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: BF16 inputs, channels a
-// multiple of eight, every tensor's rows at one aligned pitch.
+// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: channels a multiple of
+// eight (FP32: four), every tensor's rows at one aligned pitch, all inputs (and total) of one type.
 //
 // Here the instructions would bound the kernel before memory does (65536 x 768 BF16 to E4M3:
 // 1278 warp instructions a row and 100 us in layer_rows_kernel), and then the barriers between a
@@ -12,7 +12,26 @@ namespace {
 
 using namespace dlc;
 
-// Sum over the `tpr` threads of a row (a power of two), as row_reduce has it.
+// Sum over the `tpr` threads of a row (a power of two or whole warps), as row_reduce has it; the
+// usual numbers of warps without a loop, whose branches would count.
+template <int N, int WARPS>
+__device__ __forceinline__ void join_warps(float (&a)[N], const float *row) {
+    float4 q[WARPS * N / 4 > 0 ? WARPS * N / 4 : 1];
+    if constexpr (WARPS * N >= 4) {
+#pragma unroll
+        for (int i = 0; i < WARPS * N / 4; ++i) q[i] = reinterpret_cast<const float4 *>(row)[i];
+    } else {
+        q[0] = make_float4(row[0], row[1], 0.f, 0.f);
+    }
+    const float *f = reinterpret_cast<const float *>(q);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = f[i];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] += f[w * N + i];
+}
+
 template <int N>
 __device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float (*buf)[NORM_MAX_WARPS * 2], int parity) {
 #pragma unroll
@@ -31,11 +50,19 @@ __device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float
         }
         asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
         const float *row = buf[parity] + N * slot * warps;
+        if (warps == 2) {
+            join_warps<N, 2>(a, row);
+        } else if (warps == 4) {
+            join_warps<N, 4>(a, row);
+        } else if (warps == 8) {
+            join_warps<N, 8>(a, row);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = row[i] + row[N + i];
-        for (int w = 2; w < warps; ++w) {
+            for (int i = 0; i < N; ++i) a[i] = row[i];
+            for (int w = 1; w < warps; ++w) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) a[i] += row[w * N + i];
+                for (int i = 0; i < N; ++i) a[i] += row[w * N + i];
+            }
         }
     }
 }
@@ -58,11 +85,15 @@ __device__ __forceinline__ float row_most(float v, int tpr, int slot, float (*bu
 
 constexpr int VEC_THREADS = 256;  // of a block, or a little less (backward, long rows: TH)
 
-// A ring of S rows of T tensors in shared memory, V vectors of eight a thread, of which a thread
+// Channels of a vector: 16 bytes, so that neighbouring threads copy neighbouring words.
+template <typename E>
+constexpr int vec_ch() { return 16 / (int)sizeof(E); }
+
+// A ring of S rows of T tensors in shared memory, V vectors a thread, of which a thread
 // reads back only what it copied itself: no barrier, and a row's place takes the row S further
 // on as soon as it has been read.  (Strides are constants: with the block's size for one, the
 // addresses' instructions cost 7 %.)
-template <int V, int T, int S, int TH>
+template <int V, typename E, int T, int S, int TH>
 struct VecRing {
     static constexpr uint32_t WORDS = (uint32_t)(T * V), WORD = 16u * TH;
     uint32_t base, row;
@@ -86,58 +117,83 @@ struct VecRing {
                      : "r"(base + (row + (uint32_t)(k * V + j)) * WORD)
                      : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) set2(f, i, unpack_bf16(w[i]));
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 2)
+                set2(f, i, unpack_bf16(w[i]));
+            else
+                f[i] = __uint_as_float(w[i]);
+        }
     }
-    __device__ __forceinline__ void read(int k, float (&f)[V * 8]) const {
+    __device__ __forceinline__ void read(int k, float (&f)[V * vec_ch<E>()]) const {
 #pragma unroll
-        for (int j = 0; j < V; ++j) read_vector(k, j, f + 8 * j);
+        for (int j = 0; j < V; ++j) read_vector(k, j, f + j * vec_ch<E>());
     }
     static constexpr size_t SMEM = (size_t)S * WORDS * WORD;
 };
 
-// A vector of a channel-wise FP32 array from shared memory: its halves lie apart, so that
-// neighbouring threads read neighbouring words.
-__device__ __forceinline__ void vec_param(uint32_t at, uint32_t half, float (&g)[8]) {
-    const float4 a = ld_shared_f32x4(at), b = ld_shared_f32x4(at + half);
-    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-    g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+// A vector of a channel-wise FP32 array from shared memory: its quarters of four channels lie apart,
+// so that neighbouring threads read neighbouring words.
+template <int CH>
+__device__ __forceinline__ void vec_param(uint32_t at, uint32_t apart, float (&g)[CH]) {
+#pragma unroll
+    for (int h = 0; h < CH / 4; ++h) {
+        const float4 a = ld_shared_f32x4(at + (uint32_t)h * apart);
+        g[4 * h] = a.x, g[4 * h + 1] = a.y, g[4 * h + 2] = a.z, g[4 * h + 3] = a.w;
+    }
 }
 
 // Fills vec_param's arrays, whose vectors are dealt to `tpr` threads; zeros behind the row.  (By
 // asynchronous copies ahead of the rows' a call of 65536 x 768 took 4 us more, element by element
 // one of 16384 x 2048 5 us.)
+template <int CH>
 __device__ __forceinline__ void vec_param_fill(float *dst, const float *src, int C, int tpr, int V) {
+    constexpr int H = CH / 4;
     const bool aligned = ((uintptr_t)src & 15u) == 0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < 2 * tpr * V; i += blockDim.x) {  // half-vectors
-        const int vec = i >> 1, at = (vec / tpr * 2 + (i & 1)) * tpr + vec % tpr;
+    for (int i = threadIdx.x; i < H * tpr * V; i += blockDim.x) {
+        const int vec = i / H, at = (vec / tpr * H + i % H) * tpr + vec % tpr;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (src && 4 * i < C) {
-            if (aligned) v = reinterpret_cast<const float4 *>(src)[i];
-            else v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
+            if (aligned)
+                v = reinterpret_cast<const float4 *>(src)[i];
+            else
+                v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
         }
         reinterpret_cast<float4 *>(dst)[at] = v;
     }
 }
 
-template <typename E>
+// A vector of CH values as Y.
+template <typename Y, int CH>
 __device__ __forceinline__ void vec_store(char *at, const float *v) {
-    if constexpr (sizeof(E) == 2) {
-        *reinterpret_cast<uint4 *>(at) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else if constexpr (sizeof(E) == 4) {
-        reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if constexpr (sizeof(Y) == 4) {
+#pragma unroll
+        for (int i = 0; i < CH / 4; ++i) reinterpret_cast<float4 *>(at)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
-        *reinterpret_cast<uint2 *>(at) = make_uint2(pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16),
-                                                    pack_e4m3(v[4], v[5]) | (pack_e4m3(v[6], v[7]) << 16));
+        uint32_t w[CH * sizeof(Y) / 4];
+        if constexpr (sizeof(Y) == 2) {
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH / 4; ++i) w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
+        }
+        if constexpr (sizeof(w) == 16)
+            *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (sizeof(w) == 8)
+            *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(at) = w[0];
     }
 }
 
-template <int V>
-constexpr int vec_blocks() { return V <= 2 ? 4 : V <= 4 ? 3 : 2; }
+// Blocks an SM holds, by the registers of V vectors a thread; rows of the rings.
+template <int V, typename E>
+constexpr int vec_blocks() { return V * vec_ch<E>() <= 16 ? 4 : V * vec_ch<E>() <= 32 ? 3 : 2; }
 template <int V>
 constexpr int vec_ring() { return V <= 2 ? 2 : 1; }
+template <int V>
+constexpr int vec_bwd_ring() { return V <= 2 ? 3 : 2; }
 
 struct VecRow {  // this thread's part of a tensor's rows
     char *p;
@@ -146,30 +202,30 @@ struct VecRow {  // this thread's part of a tensor's rows
         : p(static_cast<char *>(t.p) + (row * t.m.ld + channel) * e), inc(step * t.m.ld * e) {}
 };
 
-// Y: y's storage.
-template <int V, typename Y, bool RES>
-__global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel(const __grid_constant__ LayerProblem p, int tpr) {
+// E: storage of x, r and t; Y: of y.
+template <int V, typename E, typename Y, bool RES>
+__global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_kernel(const __grid_constant__ LayerProblem p, int tpr) {
     griddep_launch_dependents();
-    __shared__ float buf[2][NORM_MAX_WARPS * 2];
+    __shared__ __align__(16) float buf[2][NORM_MAX_WARPS * 2];
     extern __shared__ uint4 ring_s[];
-    constexpr int N = 8 * V, S = vec_ring<V>();
+    constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_ring<V>();
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
     const long long step = (long long)gridDim.x * rpb;
-    const bool last = (V - 1) * tpr + t < p.C / 8;
-    const int c = V > 1 || last ? 8 * t : 0;
-    const uint32_t hop = 8u * (uint32_t)tpr, half = 16u * (uint32_t)tpr;
+    const bool last = (V - 1) * tpr + t < p.C / CH;
+    const int c = V > 1 || last ? CH * t : 0;
+    const uint32_t hop = (uint32_t)(CH * tpr), apart = 16u * (uint32_t)tpr;
     const float inv_c = 1.f / (float)p.C;
-    using Ring = VecRing<V, RES ? 2 : 1, S, VEC_THREADS>;
+    using Ring = VecRing<V, E, RES ? 2 : 1, S, VEC_THREADS>;
     Ring ring(smem_u32(ring_s));
     float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM), *beta = gamma + N * tpr;
     const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t, b0 = smem_u32(beta) + 16u * (uint32_t)t;
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    VecRow x(p.x, 2, row, step, c), r(p.r, 2, row, step, c), tt(p.t, 2, row, step, c), y(p.y, sizeof(Y), row, step, c);
+    VecRow x(p.x, sizeof(E), row, step, c), r(p.r, sizeof(E), row, step, c), tt(p.t, sizeof(E), row, step, c), y(p.y, sizeof(Y), row, step, c);
     griddep_wait();
     auto fetch = [&]() {
         if (ahead < p.rows) {
-            ring.fetch(0, x.p, hop * 2u, last);
-            if (RES) ring.fetch(1, r.p, hop * 2u, last);
+            ring.fetch(0, x.p, 16u * (uint32_t)tpr, last);
+            if (RES) ring.fetch(1, r.p, 16u * (uint32_t)tpr, last);
         }
         ring.next();
         ahead += step;
@@ -177,8 +233,8 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         r.p += r.inc;
     };
     for (int i = 0; i < S; ++i) fetch();
-    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
-    vec_param_fill(beta, p.beta, p.C, tpr, V);
+    vec_param_fill<CH>(gamma, p.gamma, p.C, tpr, V);
+    vec_param_fill<CH>(beta, p.beta, p.C, tpr, V);
     __syncthreads();
     int parity = 0;
     for (; row - slot < p.rows; row += step) {  // (as many rounds for every thread of the block)
@@ -189,16 +245,16 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         if (RES) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float w[8];
+                float w[CH];
                 ring.read_vector(1, j, w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) set2(v + 8 * j, i, add2(get2(v + 8 * j, i), get2(w, i)));
+                for (int i = 0; i < CH / 2; ++i) set2(v + CH * j, i, add2(get2(v + CH * j, i), get2(w, i)));
             }
         }
         if (p.t.p && on) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (j + 1 < V || last) vec_store<unsigned short>(tt.p + j * (hop * 2u), v + 8 * j);
+                if (j + 1 < V || last) vec_store<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j);
         }
         tt.p += tt.inc;
         fetch();
@@ -213,7 +269,7 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
         if (!last) {
 #pragma unroll
-            for (int i = 8 * (V - 1); i < N; ++i) v[i] = 0.f;
+            for (int i = CH * (V - 1); i < N; ++i) v[i] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
@@ -223,11 +279,11 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         const float2 rho = pair_of(rsqrtf(total[0] * inv_c + p.eps));
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float g[8], b[8];
-            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
-            vec_param(b0 + (uint32_t)(2 * j) * half, half, b);
+            float g[CH], b[CH];
+            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * apart, apart, g);
+            vec_param<CH>(b0 + (uint32_t)(j * (CH / 4)) * apart, apart, b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) set2(v + 8 * j, i, fma2(mul2(get2(v + 8 * j, i), rho), get2(g, i), get2(b, i)));
+            for (int i = 0; i < CH / 2; ++i) set2(v + CH * j, i, fma2(mul2(get2(v + CH * j, i), rho), get2(g, i), get2(b, i)));
         }
         if constexpr (sizeof(Y) == 1) {
             float most[2] = {0.f, 0.f};
@@ -243,26 +299,26 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V>()) layer_vec_kernel
         if (on) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (j + 1 < V || last) vec_store<Y>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + 8 * j);
+                if (j + 1 < V || last) vec_store<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j);
         }
         y.p += y.inc;
     }
 }
 
 // The same for the backward pass.  128 registers a thread: 16 warps an SM.
-template <int V, bool RES, int TH>
+template <int V, typename E, bool RES, int TH>
 __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __grid_constant__ LayerBwdProblem p, int tpr) {
     griddep_launch_dependents();
-    __shared__ float buf[2][NORM_MAX_WARPS * 2];
+    __shared__ __align__(16) float buf[2][NORM_MAX_WARPS * 2];
     extern __shared__ uint4 ring_s[];
-    constexpr int N = 8 * V, S = 3;
+    constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_bwd_ring<V>();
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
     const long long step = (long long)gridDim.x * rpb;
-    const bool last = (V - 1) * tpr + t < p.C / 8;
-    const int c = V > 1 || last ? 8 * t : 0;
-    const uint32_t hop = 8u * (uint32_t)tpr * (uint32_t)2, half = 16u * (uint32_t)tpr;
+    const bool last = (V - 1) * tpr + t < p.C / CH;
+    const int c = V > 1 || last ? CH * t : 0;
+    const uint32_t hop = 16u * (uint32_t)tpr;
     const float inv_c = 1.f / (float)p.C;
-    using Ring = VecRing<V, RES ? 3 : 2, S, TH>;
+    using Ring = VecRing<V, E, RES ? 3 : 2, S, TH>;
     Ring ring(smem_u32(ring_s));
     float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM);
     const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t;
@@ -270,7 +326,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.f;
     long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    VecRow dy(p.dy, 2, row, step, c), tt(p.t, 2, row, step, c), dt(p.dt, 2, row, step, c), dx(p.dx, 2, row, step, c);
+    VecRow dy(p.dy, sizeof(E), row, step, c), tt(p.t, sizeof(E), row, step, c), dt(p.dt, sizeof(E), row, step, c), dx(p.dx, sizeof(E), row, step, c);
     griddep_wait();
     auto fetch = [&]() {
         if (ahead < p.rows) {
@@ -285,11 +341,11 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         dt.p += dt.inc;
     };
     for (int i = 0; i < S; ++i) fetch();
-    vec_param_fill(gamma, p.gamma, p.C, tpr, V);
+    vec_param_fill<CH>(gamma, p.gamma, p.C, tpr, V);
     __syncthreads();
     for (; row - slot < p.rows; row += step, dx.p += dx.inc) {
         const bool on = row < p.rows;
-        float d[N], v[N], g[8];  // (gamma is read where it is used: holding it would spill)
+        float d[N], v[N], g[CH];  // (gamma is read where it is used: holding it would spill)
         cp_async_wait<S - 1>();
         ring.read(0, d);
         ring.read(1, v);
@@ -300,11 +356,11 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum = add2(get2(v + 8 * j, i), sum);
-                sd = fma2(get2(d + 8 * j, i), get2(g, i), sd);
+            for (int i = 0; i < CH / 2; ++i) {
+                sum = add2(get2(v + CH * j, i), sum);
+                sd = fma2(get2(d + CH * j, i), get2(g, i), sd);
             }
         }
         float means[2] = {sum.x + sum.y, sd.x + sd.y};
@@ -314,16 +370,16 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
         if (!last) {
 #pragma unroll
-            for (int i = 8 * (V - 1); i < N; ++i) v[i] = 0.f;
+            for (int i = CH * (V - 1); i < N; ++i) v[i] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 w = get2(v + 8 * j, i);
+            for (int i = 0; i < CH / 2; ++i) {
+                const float2 w = get2(v + CH * j, i);
                 sq = fma2(w, w, sq);
-                dot = fma2(mul2(get2(d + 8 * j, i), get2(g, i)), w, dot);
+                dot = fma2(mul2(get2(d + CH * j, i), get2(g, i)), w, dot);
             }
         }
         float red[2] = {sq.x + sq.y, dot.x + dot.y};
@@ -333,17 +389,17 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         if (on) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float s[8];
-                vec_param(g0 + (uint32_t)(2 * j) * half, half, g);
+                float s[CH];
+                vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
                 if (RES) ring.read_vector(2, j, s);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 dr = mul2(get2(d + 8 * j, i), rho2), w = get2(v + 8 * j, i);
-                    set2(dg + 8 * j, i, fma2(dr, w, get2(dg + 8 * j, i)));
+                for (int i = 0; i < CH / 2; ++i) {
+                    const float2 dr = mul2(get2(d + CH * j, i), rho2), w = get2(v + CH * j, i);
+                    set2(dg + CH * j, i, fma2(dr, w, get2(dg + CH * j, i)));
                     const float2 base = RES ? add2(get2(s, i), m2) : m2;
                     set2(s, i, fma2(dr, get2(g, i), fma2(w, k2, base)));
                 }
-                if (j + 1 < V || last) vec_store<unsigned short>(dx.p + j * hop, s);
+                if (j + 1 < V || last) vec_store<E, CH>(dx.p + j * hop, s);
             }
         }
         fetch();
@@ -359,9 +415,10 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (j + 1 < V || last) {
-                float4 *at = reinterpret_cast<float4 *>((rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * 8);
-                at[0] = make_float4(acc[8 * j], acc[8 * j + 1], acc[8 * j + 2], acc[8 * j + 3]);
-                at[1] = make_float4(acc[8 * j + 4], acc[8 * j + 5], acc[8 * j + 6], acc[8 * j + 7]);
+                float4 *at = reinterpret_cast<float4 *>((rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * CH);
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i)
+                    at[i] = make_float4(acc[CH * j + 4 * i], acc[CH * j + 4 * i + 1], acc[CH * j + 4 * i + 2], acc[CH * j + 4 * i + 3]);
             }
         if (rpb > 1) {
             __syncthreads();
@@ -390,19 +447,20 @@ struct VecKernel {
 // What these kernels take: see the top.
 bool whole(int C, std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor> outs) {
     auto ok = [](const RowTensor &t, int bytes) { return !t.p || (t.m.cs == 1 && t.m.uniform && dlc_aligned_rows(t, bytes)); };
-    if (C % 8 || !all_of(DLC_DATA_BFLOAT16, ins)) return false;
+    const int ch = all_of(DLC_DATA_FLOAT, ins) ? 4 : 8;
+    if (C % ch || !ring(ins)) return false;
     for (const RowTensor &t : ins)
         if (!ok(t, 16)) return false;
     for (const RowTensor &t : outs)
-        if (!ok(t, t.dt == DLC_DATA_FLOAT8_E4M3 ? 8 : 16)) return false;
+        if (!ok(t, std::min(16, ch * dlc_dtype_bytes((dlcDataType_t)t.dt)))) return false;
     return true;
 }
 
 // The fewest threads whose `most` vectors hold a row, whole warps of them from a warp on; more, with
 // fewer vectors, while the rows are too few to give every SM a block.
-VecPlan plan_vec(long long rows, int C, int most, bool warps, int sm_count) {
+VecPlan plan_vec(long long rows, int C, bool fp32, int most, bool warps, int sm_count) {
     VecPlan p;
-    const int nv = C / 8;
+    const int nv = C / (fp32 ? 4 : 8);
     p.tpr = 8;
     while (p.tpr < 32 && p.tpr * std::min(4, most) < nv) p.tpr *= 2;
     while (p.tpr * most < nv) p.tpr += warps && p.tpr >= 128 ? 32 : p.tpr;
@@ -415,9 +473,9 @@ VecPlan plan_vec(long long rows, int C, int most, bool warps, int sm_count) {
 
 // `arrays`: channel-wise arrays in shared memory.
 template <typename P>
-dlcStatus_t launch_vec(dlcContext *ctx, const VecKernel &k, P &p, const VecPlan &v, int arrays, int *blocks = nullptr) {
+dlcStatus_t launch_vec(dlcContext *ctx, const VecKernel &k, P &p, const VecPlan &v, bool fp32, int arrays, int *blocks = nullptr) {
     int tpr = v.tpr;
-    const size_t smem = k.ring + (size_t)arrays * 8 * v.v * tpr * sizeof(float);
+    const size_t smem = k.ring + (size_t)arrays * (fp32 ? 4 : 8) * v.v * tpr * sizeof(float);
     const int per_sm = std::max(1, std::min(k.blocks, (int)(NORM_MAX_RING / (smem + 2048))));
     const long long n = std::min((p.rows + v.rpb - 1) / v.rpb, (long long)ctx->sm_count * per_sm);
     if (blocks) *blocks = (int)n;
@@ -426,64 +484,90 @@ dlcStatus_t launch_vec(dlcContext *ctx, const VecKernel &k, P &p, const VecPlan 
     return dlc_launch(ctx, k.fn, dim3((unsigned)n), dim3((unsigned)k.threads), smem, args);
 }
 
-template <int V, typename Y, bool RES>
+template <int V, typename E, typename Y, bool RES>
 VecKernel vec_fwd() {
-    return {(const void *)layer_vec_kernel<V, Y, RES>, VecRing<V, RES ? 2 : 1, vec_ring<V>(), VEC_THREADS>::SMEM, VEC_THREADS, vec_blocks<V>()};
+    return {(const void *)layer_vec_kernel<V, E, Y, RES>, VecRing<V, E, RES ? 2 : 1, vec_ring<V>(), VEC_THREADS>::SMEM, VEC_THREADS,
+            vec_blocks<V, E>()};
 }
 
-template <int V>
+template <int V, typename E>
 VecKernel vec_fwd(const LayerProblem &p) {
     const bool res = p.r.p != nullptr;
-    if (p.y.dt == DLC_DATA_BFLOAT16) return res ? vec_fwd<V, unsigned short, true>() : vec_fwd<V, unsigned short, false>();
-    if (p.y.dt == DLC_DATA_FLOAT) return res ? vec_fwd<V, float, true>() : vec_fwd<V, float, false>();
-    return res ? vec_fwd<V, unsigned char, true>() : vec_fwd<V, unsigned char, false>();
+    if (p.y.dt == DLC_DATA_BFLOAT16) return res ? vec_fwd<V, E, unsigned short, true>() : vec_fwd<V, E, unsigned short, false>();
+    if (p.y.dt == DLC_DATA_FLOAT) return res ? vec_fwd<V, E, float, true>() : vec_fwd<V, E, float, false>();
+    return res ? vec_fwd<V, E, unsigned char, true>() : vec_fwd<V, E, unsigned char, false>();
 }
 
 VecKernel vec_fwd(int v, const LayerProblem &p) {
+    if (p.x.dt == DLC_DATA_FLOAT) {
+        switch (v) {
+            case 1: return vec_fwd<1, float>(p);
+            case 2: return vec_fwd<2, float>(p);
+            case 3: return vec_fwd<3, float>(p);
+            default: return vec_fwd<4, float>(p);
+        }
+    }
+    using Half = unsigned short;
     switch (v) {
-        case 1: return vec_fwd<1>(p);
-        case 2: return vec_fwd<2>(p);
-        case 3: return vec_fwd<3>(p);
-        case 4: return vec_fwd<4>(p);
-        case 5: return vec_fwd<5>(p);
-        case 6: return vec_fwd<6>(p);
-        case 7: return vec_fwd<7>(p);
-        default: return vec_fwd<8>(p);
+        case 1: return vec_fwd<1, Half>(p);
+        case 2: return vec_fwd<2, Half>(p);
+        case 3: return vec_fwd<3, Half>(p);
+        case 4: return vec_fwd<4, Half>(p);
+        case 5: return vec_fwd<5, Half>(p);
+        case 6: return vec_fwd<6, Half>(p);
+        case 7: return vec_fwd<7, Half>(p);
+        default: return vec_fwd<8, Half>(p);
     }
 }
 
-template <int V, int TH>
+template <int V, typename E, int TH>
 VecKernel vec_bwd(bool res) {
-    return res ? VecKernel{(const void *)layer_bwd_vec_kernel<V, true, TH>, VecRing<V, 3, 3, TH>::SMEM, TH, 512 / TH}
-               : VecKernel{(const void *)layer_bwd_vec_kernel<V, false, TH>, VecRing<V, 2, 3, TH>::SMEM, TH, 512 / TH};
+    constexpr int S = vec_bwd_ring<V>();
+    return res ? VecKernel{(const void *)layer_bwd_vec_kernel<V, E, true, TH>, VecRing<V, E, 3, S, TH>::SMEM, TH, 512 / TH}
+               : VecKernel{(const void *)layer_bwd_vec_kernel<V, E, false, TH>, VecRing<V, E, 2, S, TH>::SMEM, TH, 512 / TH};
+}
+
+// (a row of more than 128 threads has a block of its own: 160, 192 or 224 threads where they are enough)
+template <int V, typename E>
+VecKernel vec_bwd(int tpr, bool res) {
+    return tpr == 160   ? vec_bwd<V, E, 160>(res)
+           : tpr == 192 ? vec_bwd<V, E, 192>(res)
+           : tpr == 224 ? vec_bwd<V, E, 224>(res)
+                        : vec_bwd<V, E, 256>(res);
+}
+
+VecKernel vec_bwd(const VecPlan &v, bool fp32, bool res) {
+    using Half = unsigned short;
+    if (!fp32) return v.v == 1 ? vec_bwd<1, Half, 256>(res) : vec_bwd<2, Half>(v.tpr, res);
+    switch (v.v) {
+        case 1: return vec_bwd<1, float, 256>(res);
+        case 2: return vec_bwd<2, float, 256>(res);
+        case 3: return vec_bwd<3, float, 256>(res);
+        default: return vec_bwd<4, float>(v.tpr, res);
+    }
 }
 
 }  // namespace
 
 bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &pb, dlcStatus_t &status) {
     LayerProblem p = pb;
-    if (!whole(p.C, {p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != DLC_DATA_BFLOAT16)) return false;
-    const VecPlan v = plan_vec(p.rows, p.C, 8, false, ctx->sm_count);
+    if (!whole(p.C, {p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != p.x.dt)) return false;
+    const bool fp32 = p.x.dt == DLC_DATA_FLOAT;
+    const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 8, false, ctx->sm_count);
     if (!v.v) return false;
-    status = launch_vec(ctx, vec_fwd(v.v, p), p, v, 2);
+    status = launch_vec(ctx, vec_fwd(v.v, p), p, v, fp32, 2);
     return true;
 }
 
 bool dlc_layer_bwd_vec(dlcContext *ctx, const LayerBwdProblem &pb, dlcStatus_t &status) {
     LayerBwdProblem p = pb;
-    if (!whole(p.C, {p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != DLC_DATA_BFLOAT16) return false;
-    const VecPlan v = plan_vec(p.rows, p.C, 2, true, ctx->sm_count);
+    if (!whole(p.C, {p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != p.t.dt) return false;
+    const bool fp32 = p.t.dt == DLC_DATA_FLOAT, res = p.dt.p != nullptr;
+    const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 2, true, ctx->sm_count);
     if (!v.v) return false;
-    const bool res = p.dt.p != nullptr;
     int blocks = 0;
     // (the rows of sums that a block joins need no more than the ring has)
-    status = launch_vec(ctx,
-                        v.v == 1       ? vec_bwd<1, 256>(res)
-                        : v.tpr == 160 ? vec_bwd<2, 160>(res)
-                        : v.tpr == 192 ? vec_bwd<2, 192>(res)
-                        : v.tpr == 224 ? vec_bwd<2, 224>(res)
-                                       : vec_bwd<2, 256>(res),
-                        p, v, 1, &blocks);
+    status = launch_vec(ctx, vec_bwd(v, fp32, res), p, v, fp32, 1, &blocks);
     if (status == DLC_STATUS_SUCCESS && (p.dgamma || p.dbeta))
         status = dlc_launch_column_sums(ctx, p.ws, p.dgamma, p.dbeta, p.C, blocks);
     return true;

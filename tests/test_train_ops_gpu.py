@@ -44,7 +44,7 @@ def close_e4m3(q, scale, y, ey, what):
 # ---- layer norm ------------------------------------------------------------------
 
 SIZES = [(1, 1), (1, 4096), (3, 8), (5, 7), (2, 64), (33, 130), (300, 333), (65, 512), (17, 1000), (9, 1024), (4, 2048),
-         (3, 5000), (2, 8192), (2, 12288), (1, 40000), (5000, 72), (3000, 768)]
+         (3, 5000), (2, 8192), (2, 12288), (1, 40000), (5000, 72), (3000, 768), (50, 300), (700, 2404), (3000, 1280), (400, 3584)]
 
 
 @pytest.mark.parametrize("rows,c", SIZES)
@@ -125,7 +125,7 @@ def test_layer_norm_of_rows_far_from_zero(handle, c):
 
 
 @pytest.mark.parametrize("rows,c", [(1, 1), (1, 4096), (3, 7), (100, 96), (257, 333), (1000, 512), (40, 1024), (9, 4097),
-                                    (5, 8192), (3, 12288), (2, 20000), (7000, 64)])
+                                    (5, 8192), (3, 12288), (2, 20000), (7000, 64), (50, 300), (700, 2404), (900, 2560), (500, 3600), (3000, 768)])
 @pytest.mark.parametrize("dt,with_dt,sums", [(BF, True, "both"), (F32, False, "both"), (BF, False, None), (F32, True, "gamma"),
                                              (BF, True, "beta")])
 def test_layer_norm_backward(handle, rows, c, dt, with_dt, sums):
