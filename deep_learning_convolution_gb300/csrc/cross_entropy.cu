@@ -63,48 +63,63 @@ struct CeParams {
     int *err;
 };
 
-// The sum of one segment of a row of logits.
+// A row's loss and log-sum-exp, its sum being complete.
+__device__ __forceinline__ void ce_finish(const CeParams &p, long long m, CePart a, float chosen) {
+    const float lse = isinf(a.r) ? log2f(a.s) * LN2 : fmaf(a.r, LN2, logf(a.s));
+    const long long k = ce_target(p.target, m);
+    float loss = 0.f;
+    if (k >= p.V) {
+        record_error(p.err, DLC_DEVERR_INDEX, (int)m);
+        loss = NAN;
+    } else if (k >= 0) {
+        loss = lse - chosen;
+    }
+    p.lse[m] = lse;
+    p.loss[m] = loss;
+}
+
+// The sum of one segment of a row of logits; of all of them, where one segment holds them.
 __global__ void __launch_bounds__(CE_THREADS) ce_part_kernel(const __grid_constant__ CeParams p) {
     griddep_launch_dependents();
     __shared__ CePart warps[CE_THREADS / 32];
     constexpr int E = CE_SEGMENT / CE_THREADS;
     const int c0 = (int)blockIdx.y * CE_SEGMENT + 4 * (int)threadIdx.x;
     griddep_wait();
-    for (long long m = blockIdx.x; m < p.M; m += gridDim.x) {
-        const float *z = p.z + m * p.ld;
-        float v[E];
+    const long long m = blockIdx.x;
+    const float *z = p.z + m * p.ld;
+    float v[E];
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j) {
-            const int c = c0 + 4 * CE_THREADS * j;
-            float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (c + 4 <= p.cols) {
-                q = *reinterpret_cast<const float4 *>(z + c);
-            } else if (c < p.cols) {
-                q.x = z[c];
-                if (c + 1 < p.cols) q.y = z[c + 1];
-                if (c + 2 < p.cols) q.z = z[c + 2];
-            }
-            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+    for (int j = 0; j < E / 4; ++j) {
+        const int c = c0 + 4 * CE_THREADS * j;
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (c + 4 <= p.cols) {
+            q = *reinterpret_cast<const float4 *>(z + c);
+        } else if (c < p.cols) {
+            q.x = z[c];
+            if (c + 1 < p.cols) q.y = z[c + 1];
+            if (c + 2 < p.cols) q.z = z[c + 2];
         }
-        float top = -INFINITY, s = 0.f;
+        v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+    }
+    float top = -INFINITY, s = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);
-        const float r = ceilf(top * LOG2E), base = isinf(r) ? 0.f : r;
+    for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);
+    const float r = ceilf(top * LOG2E), base = isinf(r) ? 0.f : r;
 #pragma unroll
-        for (int i = 0; i < E; ++i) s += exp2_fast(fmaf(v[i], LOG2E, -base));
-        const CePart a = ce_join_lanes(CePart{r, s});
-        if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = a;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            CePart t = warps[0];
-            for (int i = 1; i < CE_THREADS / 32; ++i) t = ce_join(t, warps[i]);
+    for (int i = 0; i < E; ++i) s += exp2_fast(fmaf(v[i], LOG2E, -base));
+    const CePart a = ce_join_lanes(CePart{r, s});
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        CePart t = warps[0];
+        for (int i = 1; i < CE_THREADS / 32; ++i) t = ce_join(t, warps[i]);
+        const long long k = ce_target(p.target, m) - p.n0;
+        if (p.parts == 1) {
+            ce_finish(p, m, t, k >= 0 && k < p.cols ? z[k] : 0.f);
+        } else {
             p.part[(long long)(p.part0 + (int)blockIdx.y) * p.M + m] = make_float2(t.r, t.s);
-            if (blockIdx.y == 0) {
-                const long long k = ce_target(p.target, m) - p.n0;
-                if (k >= 0 && k < p.cols) p.chosen[m] = z[k];
-            }
+            if (blockIdx.y == 0 && k >= 0 && k < p.cols) p.chosen[m] = z[k];
         }
-        __syncthreads();
     }
 }
 
@@ -129,21 +144,10 @@ __global__ void __launch_bounds__(1024) ce_loss_kernel(const __grid_constant__ C
     __syncthreads();
     if (warp == 0 && m < p.M) {
         for (int i = 1; i < 32; ++i) a = ce_join(a, warps[i][lane]);
-        if (!p.last) {
-            const_cast<float2 *>(p.part)[m] = make_float2(a.r, a.s);
-            return;
-        }
-        const float lse = isinf(a.r) ? log2f(a.s) * LN2 : fmaf(a.r, LN2, logf(a.s));
-        const long long k = ce_target(p.target, m);
-        float loss = 0.f;
-        if (k >= p.V) {
-            record_error(p.err, DLC_DEVERR_INDEX, (int)m);
-            loss = NAN;
-        } else if (k >= 0) {
-            loss = lse - p.chosen[m];
-        }
-        p.lse[m] = lse;
-        p.loss[m] = loss;
+        if (p.last)
+            ce_finish(p, m, a, p.chosen[m]);
+        else
+            p.part[m] = make_float2(a.r, a.s);
     }
 }
 
@@ -351,15 +355,19 @@ struct CePlan {
 
 // Whether the pair kernel's epilogue takes the logits from its accumulators.  For a few rows the
 // filters' stream decides, which the few-row kernels carry better than tiles of 256 rows do,
-// and FP32 logits are little beside it: 4096 -> 131072 forward, 1 row 162 us with logits in
+// and FP32 logits are little beside it.  Forward, 4096 -> 131072: 1 row 162 us with logits in
 // memory, 295 fused; 16 rows 169 and 179; 32 rows 176 and 179; 48 rows 184 and 182; 96 rows
-// 200 and 185; more rows far apart (4096 x 2048 -> 131072 1793 and 1084 us), few classes alike
-// (2048 -> 1000: 32 rows 9.8 and 10.3 us, 64 rows 10.3 and 10.5, 256 rows 12.7 and 10.5).
-bool fuse(const CrossEntropyProblem &p) { return p.M > 32; }
+// 200 and 185; more rows far apart (4096 x 2048 -> 131072 1793 and 1084 us).  Up to a segment of
+// classes the rows' sums are one kernel, which moves the point: 2048 -> 1000 32 rows 7.6 and 10.2 us, 64
+// rows 8.4 and 10.4, 192 rows 10.2 and 10.4; 1024 -> 4096 48 rows 8.8 and 10.1, 64 rows 8.7 and 8.2.
+// Backward: 8 rows 676 and 702, 16 rows 678 and 681, 32 rows 687 and 684; 2048 -> 1000: 4 rows 23.8 and
+// 25.0, 16 rows 24.8 and 24.6, 64 rows 26.8 and 24.7.
+bool fuse_fwd(const CrossEntropyProblem &p) { return p.M > (p.V <= CE_SEGMENT ? 64 : 32); }
+bool fuse_bwd(const CrossEntropyProblem &p) { return p.M > 16; }
 
 CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan f(ws);
-    f.fused = fuse(p);
+    f.fused = fuse_fwd(p);
     // (a part: 32 classes at least)
     f.piece = f.fused ? (int)std::min<long long>(p.V, std::max<long long>(1024, (long long)(CE_PART_BYTES / 8) / p.M * 32 / 256 * 256))
                       : piece_of(p, 4);
@@ -382,7 +390,7 @@ CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
 
 CePlan plan_bwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan b(ws);
-    b.fused = fuse(p);
+    b.fused = fuse_bwd(p);
     b.piece = piece_of(p, b.fused ? 2 : 4);
     b.ldz = (b.piece + 7) / 8 * 8;
     b.operands(p);
@@ -445,8 +453,10 @@ dlcStatus_t dlc_launch_cross_entropy(dlcContext *ctx, const CrossEntropyProblem 
             if (s != DLC_STATUS_SUCCESS) return s;
             c.n0 = n0;
             c.cols = cols;
+            c.parts = cols == p.V ? segments(cols) : 0;
             void *args[] = {&c};
             s = dlc_launch(ctx, (const void *)ce_part_kernel, dim3((unsigned)p.M, (unsigned)segments(cols)), dim3(CE_THREADS), 0, args);
+            if (c.parts == 1) return s;  // the rows' losses are written
         }
         if (s != DLC_STATUS_SUCCESS) return s;
         c.parts = c.part0 + f.parts_of(ctx, p, n0, cols);
