@@ -6,9 +6,9 @@
 //   dz[m, k] = dloss[m] (exp(z[m, k] - lse[m]) - [k = target[m]])
 //   dx = dz w;  dw = dz^T x;  dbias = sum_m dz        (rows without a target: 0)
 //
-// Exponentials are taken about whole powers of two: with z' = z log2(e), the sum of a row's
-// part is kept as s = sum 2^(z' - r) with r = ceil(max z'), an integer, so that joining
-// two parts rescales by an exact power of two and no rounding of the maximum enters.
+// A row's part is kept as its largest logit t and s = sum exp(z - t); two parts are joined at the larger
+// t.  loss = (t - z[target]) + log s, whose difference is exact where lse - z[target] would lose
+// the digits that lse has not.
 #include <cmath>
 
 #include "channel.cuh"
@@ -19,23 +19,23 @@ namespace {
 
 using namespace dlc;
 
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr int CE_THREADS = 256;
 constexpr int CE_SEGMENT = 4096;  // logits of a row that a block sums up
 
-// A part of a row's sum: 2^r * s.  r = -inf: nothing (or only -inf) so far.
+// A part of a row's sum: exp(t) * s.  t = -inf: nothing (or only -inf) so far.
 struct CePart {
-    float r, s;
+    float t, s;
 };
 
 __device__ __forceinline__ CePart ce_join(CePart a, CePart b) {
-    const float r = fmaxf(a.r, b.r), base = isinf(r) ? 0.f : r;
-    return {r, a.s * exp2_fast(a.r - base) + b.s * exp2_fast(b.r - base)};
+    const float t = fmaxf(a.t, b.t), base = isinf(t) ? 0.f : t;
+    return {t, a.s * exp2_fast((a.t - base) * LOG2E) + b.s * exp2_fast((b.t - base) * LOG2E)};
 }
 
 __device__ __forceinline__ CePart ce_join_lanes(CePart a) {
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) a = ce_join(a, CePart{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
+    for (int o = 16; o > 0; o /= 2) a = ce_join(a, CePart{__shfl_xor_sync(0xffffffffu, a.t, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
     return a;
 }
 
@@ -51,7 +51,7 @@ struct CeParams {
     const float *z;            // [M][ld]
     long long ld;
     IndexList target;
-    float2 *part;              // [part][M] (r, s)
+    float2 *part;              // [part][M] (t, s)
     int part0, parts;          // first part of this piece; how many there are when they are joined
     int last;                  // the rows' sums are complete, else part 0 takes what they are so far
     float *chosen;             // [M] the target's logit
@@ -65,14 +65,14 @@ struct CeParams {
 
 // A row's loss and log-sum-exp, its sum being complete.
 __device__ __forceinline__ void ce_finish(const CeParams &p, long long m, CePart a, float chosen) {
-    const float lse = isinf(a.r) ? log2f(a.s) * LN2 : fmaf(a.r, LN2, logf(a.s));
+    const float log_s = logf(a.s), lse = isinf(a.t) ? log_s : a.t + log_s;  // (t = +-inf: s = inf or 0)
     const long long k = ce_target(p.target, m);
     float loss = 0.f;
     if (k >= p.V) {
         record_error(p.err, DLC_DEVERR_INDEX, (int)m);
         loss = NAN;
     } else if (k >= 0) {
-        loss = lse - chosen;
+        loss = (a.t - chosen) + log_s;
     }
     p.lse[m] = lse;
     p.loss[m] = loss;
@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(CE_THREADS) ce_part_kernel(const __grid_consta
     float top = -INFINITY, s = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);
-    const float r = ceilf(top * LOG2E), base = isinf(r) ? 0.f : r;
+    const float base = isinf(top) ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += exp2_fast(fmaf(v[i], LOG2E, -base));
-    const CePart a = ce_join_lanes(CePart{r, s});
+    for (int i = 0; i < E; ++i) s += exp2_fast((v[i] - base) * LOG2E);
+    const CePart a = ce_join_lanes(CePart{top, s});
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = a;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(CE_THREADS) ce_part_kernel(const __grid_consta
         if (p.parts == 1) {
             ce_finish(p, m, t, k >= 0 && k < p.cols ? z[k] : 0.f);
         } else {
-            p.part[(long long)(p.part0 + (int)blockIdx.y) * p.M + m] = make_float2(t.r, t.s);
+            p.part[(long long)(p.part0 + (int)blockIdx.y) * p.M + m] = make_float2(t.t, t.s);
             if (blockIdx.y == 0 && k >= 0 && k < p.cols) p.chosen[m] = z[k];
         }
     }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024) ce_loss_kernel(const __grid_constant__ C
         if (p.last)
             ce_finish(p, m, a, p.chosen[m]);
         else
-            p.part[m] = make_float2(a.r, a.s);
+            p.part[m] = make_float2(a.t, a.s);
     }
 }
 

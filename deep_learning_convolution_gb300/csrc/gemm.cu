@@ -637,7 +637,8 @@ __device__ __forceinline__ float gp_column_sum(const float (&v)[32]) {
 
 // The epilogue of softmax cross entropy (cross_entropy.cu), tiles of whole reductions.  The
 // accumulator's row is a thread's own, so a row's part of the sum needs no exchange:
-//   ENTROPY_PARTS  2^r s of this thread's columns, and the target's logit where it is one of them
+//   ENTROPY_PARTS  the largest logit t of this thread's columns and s = sum exp(z - t), and the
+//                  target's logit where it is one of them
 //   ENTROPY_DZ     dz in BF16 through bulk stores, and its sums over the warp's 32 rows
 template <int MODE>
 __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
@@ -688,7 +689,7 @@ __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uin
         __syncwarp();
         tc_fence_after_sync();
         const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * p.acc_stride;
-        float r = -INFINITY;
+        float t = -INFINITY;
         float2 sum = make_float2(0.f, 0.f);
         for (int c0 = 32 * part; c0 < p.nout && n0 + c0 < p.N; c0 += 64) {
             const int n = n0 + c0, cols = p.N - n;
@@ -719,15 +720,14 @@ __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uin
 #pragma unroll
                 for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
                 const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const float rn = fmaxf(r, ceilf(most * LOG2E)), base = isinf(rn) ? 0.f : rn;
-                const float old = exp2_fast(r - base);  // (r = -inf: nothing so far)
-                sum = mul2(sum, pair_of(old));
-                r = rn;
+                const float next = fmaxf(t, most), base = isinf(next) ? 0.f : next;
+                sum = mul2(sum, pair_of(exp2_fast((t - base) * LOG2E)));  // (t = -inf: nothing so far)
+                t = next;
                 float2 more = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    sum = add2(sum, exp2_pair(fma2(get2(v, i), pair_of(LOG2E), pair_of(-base))));
-                    more = add2(more, exp2_pair(fma2(get2(v, i + 1), pair_of(LOG2E), pair_of(-base))));
+                    sum = add2(sum, exp2_pair(mul2(add2(get2(v, i), pair_of(-base)), pair_of(LOG2E))));
+                    more = add2(more, exp2_pair(mul2(add2(get2(v, i + 1), pair_of(-base)), pair_of(LOG2E))));
                 }
                 sum = add2(sum, more);
             } else {
@@ -751,7 +751,7 @@ __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uin
                 st.tma(tmY, true, v, n, 0);
             }
         }
-        if (MODE == ENTROPY_PARTS && valid) e.part[((long long)e.part0 + 2 * w.nt + part) * p.M + m] = make_float2(r, sum.x + sum.y);
+        if (MODE == ENTROPY_PARTS && valid) e.part[((long long)e.part0 + 2 * w.nt + part) * p.M + m] = make_float2(t, sum.x + sum.y);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_tmem_free(tempty0 + 8u * (uint32_t)buf);

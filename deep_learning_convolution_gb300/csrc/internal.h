@@ -338,7 +338,7 @@ struct EntropyTile {
     int mode = ENTROPY_NONE;
     int V = 0, n0 = 0;           // classes in all, and the first one of this product
     IndexList target;
-    float2 *part = nullptr;      // PARTS: [part][M] (r, s), dlc_entropy_parts of them from part0 on
+    float2 *part = nullptr;      // PARTS: [part][M] (t, s), dlc_entropy_parts of them from part0 on
     int part0 = 0;
     float *chosen = nullptr;     // PARTS: [M] the target's logit
     const float *lse = nullptr, *dloss = nullptr;  // DZ; dz goes to y: BF16, rows padded to 16 bytes

@@ -508,6 +508,26 @@ def test_cross_entropy_of_masked_classes(handle, rows, v):
     b[:] = float("-inf")
     api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, bias=b)
     assert (lse == float("-inf")).all() and torch.isnan(loss[target >= 0]).all() and (loss[target < 0] == 0).all()
+    # nothing but FP32's lowest value: all classes alike (a logit is below its rounding)
+    b[:] = torch.finfo(F32).min
+    api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, bias=b)
+    assert (lse == torch.finfo(F32).min).all() and (loss[target < 0] == 0).all()
+    close(loss[target >= 0], torch.full_like(loss[target >= 0], math.log(v)).double(), torch.tensor(1e-5, device="cuda"), "loss")
+
+
+@pytest.mark.parametrize("rows", [20, 200])
+@pytest.mark.parametrize("level", [1e3, 1e6])
+def test_cross_entropy_far_from_zero(handle, rows, level):
+    """Logits that a bias lifts: the loss keeps the digits that log-sum-exp has not.  Logits are rounded
+    at their own size (2^-24 level), their products summed within the bound of the linear layer."""
+    x, w, b, target, _ = entropy_case(rows, 64, 700, True)
+    b += level
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, bias=b)
+    f = ref.cross_entropy(d(x), d(w), target, d(b))
+    at = 2 * cref.U32 * level * 1.01  # the chosen logit's and the others' rounding
+    close(loss, f["loss"][0], 2 * (f["ez"].amax(1) + at) + 8 * cref.U32 * 20, "loss")
+    close(lse, f["lse"][0], f["ez"].amax(1) + 2 * at + 8 * cref.U32 * 20, "lse")
 
 
 def test_cross_entropy_of_large_logits_and_sure_rows(handle):
