@@ -1,5 +1,5 @@
-// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: channels a multiple of
-// eight (FP32: four), every tensor's rows at one aligned pitch, all inputs (and total) of one type.
+// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: channels contiguous, every
+// tensor's rows at one pitch of whole 16-byte pieces, all inputs (and total) of one type.
 //
 // Here the instructions would bound the kernel before memory does (65536 x 768 BF16 to E4M3:
 // 1278 warp instructions a row and 100 us in layer_rows_kernel), and then the barriers between a
@@ -98,13 +98,13 @@ struct VecRing {
     static constexpr uint32_t WORDS = (uint32_t)(T * V), WORD = 16u * TH;
     uint32_t base, row;
     __device__ __forceinline__ explicit VecRing(uint32_t smem) : base(smem + threadIdx.x * 16u), row(0) {}
-    // at: this thread's first vector; hop: bytes to the next one
-    __device__ __forceinline__ void fetch(int k, const char *at, uint32_t hop, bool last) {
+    // at: this thread's first vector; hop: bytes to the next one; last: channels of the last one that
+    // exist (what is behind them becomes zero)
+    __device__ __forceinline__ void fetch(int k, const char *at, uint32_t hop, int last) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const bool on = j + 1 < V || last;
-            cp_async_16(base + (row + (uint32_t)(k * V + j)) * WORD, at + (on ? j * hop : 0u), on ? 16u : 0u);
-        }
+        for (int j = 0; j < V; ++j)
+            cp_async_16(base + (row + (uint32_t)(k * V + j)) * WORD, at + (j + 1 < V || last > 0 ? j * hop : 0u),
+                        j + 1 < V ? 16u : (uint32_t)last * (uint32_t)sizeof(E));
     }
     __device__ __forceinline__ void next() {  // (ends the copies of a row)
         cp_async_commit();
@@ -153,11 +153,13 @@ __device__ __forceinline__ void vec_param_fill(float *dst, const float *src, int
     for (int i = threadIdx.x; i < H * tpr * V; i += blockDim.x) {
         const int vec = i / H, at = (vec / tpr * H + i % H) * tpr + vec % tpr;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src && 4 * i < C) {
-            if (aligned)
-                v = reinterpret_cast<const float4 *>(src)[i];
-            else
-                v = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
+        if (src && aligned && 4 * i + 4 <= C) {
+            v = reinterpret_cast<const float4 *>(src)[i];
+        } else if (src && 4 * i < C) {
+            v.x = src[4 * i];
+            if (4 * i + 1 < C) v.y = src[4 * i + 1];
+            if (4 * i + 2 < C) v.z = src[4 * i + 2];
+            if (4 * i + 3 < C) v.w = src[4 * i + 3];
         }
         reinterpret_cast<float4 *>(dst)[at] = v;
     }
@@ -187,6 +189,18 @@ __device__ __forceinline__ void vec_store(char *at, const float *v) {
     }
 }
 
+// The last vector: whole, or the `n` channels of it that exist.
+template <typename Y, int CH>
+__device__ __forceinline__ void vec_store_last(char *at, const float *v, int n) {
+    if (n == CH) {
+        vec_store<Y, CH>(at, v);
+    } else if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < CH - 1; ++i)
+            if (i < n) store_elem(at, sizeof(Y) == 4 ? DLC_DATA_FLOAT : sizeof(Y) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT8_E4M3, i, v[i]);
+    }
+}
+
 // Blocks an SM holds, by the registers of V vectors a thread; rows of the rings.
 template <int V, typename E>
 constexpr int vec_blocks() { return V * vec_ch<E>() <= 16 ? 4 : V * vec_ch<E>() <= 32 ? 3 : 2; }
@@ -211,8 +225,8 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_ker
     constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_ring<V>();
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
     const long long step = (long long)gridDim.x * rpb;
-    const bool last = (V - 1) * tpr + t < p.C / CH;
-    const int c = V > 1 || last ? CH * t : 0;
+    const int last = min(max(p.C - ((V - 1) * tpr + t) * CH, 0), CH);
+    const int c = V > 1 || last > 0 ? CH * t : 0;
     const uint32_t hop = (uint32_t)(CH * tpr), apart = 16u * (uint32_t)tpr;
     const float inv_c = 1.f / (float)p.C;
     using Ring = VecRing<V, E, RES ? 2 : 1, S, VEC_THREADS>;
@@ -254,7 +268,10 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_ker
         if (p.t.p && on) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (j + 1 < V || last) vec_store<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j);
+                if (j + 1 < V)
+                    vec_store<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j);
+                else
+                    vec_store_last<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j, last);
         }
         tt.p += tt.inc;
         fetch();
@@ -267,9 +284,13 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_ker
         const float2 mean = pair_of(-total[0] * inv_c);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
-        if (!last) {
+        if (last == 0) {
 #pragma unroll
-            for (int i = CH * (V - 1); i < N; ++i) v[i] = 0.f;
+            for (int i = 0; i < CH; ++i) v[CH * (V - 1) + i] = 0.f;
+        } else if (last < CH) {
+#pragma unroll
+            for (int i = 1; i < CH; ++i)
+                if (i >= last) v[CH * (V - 1) + i] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
@@ -299,7 +320,10 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_ker
         if (on) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (j + 1 < V || last) vec_store<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j);
+                if (j + 1 < V)
+                    vec_store<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j);
+                else
+                    vec_store_last<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j, last);
         }
         y.p += y.inc;
     }
@@ -314,8 +338,8 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
     constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_bwd_ring<V>();
     const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
     const long long step = (long long)gridDim.x * rpb;
-    const bool last = (V - 1) * tpr + t < p.C / CH;
-    const int c = V > 1 || last ? CH * t : 0;
+    const int last = min(max(p.C - ((V - 1) * tpr + t) * CH, 0), CH);
+    const int c = V > 1 || last > 0 ? CH * t : 0;
     const uint32_t hop = 16u * (uint32_t)tpr;
     const float inv_c = 1.f / (float)p.C;
     using Ring = VecRing<V, E, RES ? 3 : 2, S, TH>;
@@ -368,9 +392,13 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         const float2 mean = pair_of(-means[0] * inv_c);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
-        if (!last) {
+        if (last == 0) {
 #pragma unroll
-            for (int i = CH * (V - 1); i < N; ++i) v[i] = 0.f;
+            for (int i = 0; i < CH; ++i) v[CH * (V - 1) + i] = 0.f;
+        } else if (last < CH) {
+#pragma unroll
+            for (int i = 1; i < CH; ++i)
+                if (i >= last) v[CH * (V - 1) + i] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -399,7 +427,10 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
                     const float2 base = RES ? add2(get2(s, i), m2) : m2;
                     set2(s, i, fma2(dr, get2(g, i), fma2(w, k2, base)));
                 }
-                if (j + 1 < V || last) vec_store<E, CH>(dx.p + j * hop, s);
+                if (j + 1 < V)
+                    vec_store<E, CH>(dx.p + j * hop, s);
+                else
+                    vec_store_last<E, CH>(dx.p + j * hop, s, last);
             }
         }
         fetch();
@@ -413,13 +444,19 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         const float *acc = h ? db : dg;
         if (rpb > 1) __syncthreads();
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j + 1 < V || last) {
-                float4 *at = reinterpret_cast<float4 *>((rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * CH);
+        for (int j = 0; j < V; ++j) {
+            float *at = (rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * CH;
+            const int n = j + 1 < V ? CH : last;
+            if (n == CH && p.C % 4 == 0) {
 #pragma unroll
                 for (int i = 0; i < CH / 4; ++i)
-                    at[i] = make_float4(acc[CH * j + 4 * i], acc[CH * j + 4 * i + 1], acc[CH * j + 4 * i + 2], acc[CH * j + 4 * i + 3]);
+                    reinterpret_cast<float4 *>(at)[i] = make_float4(acc[CH * j + 4 * i], acc[CH * j + 4 * i + 1], acc[CH * j + 4 * i + 2], acc[CH * j + 4 * i + 3]);
+            } else if (n > 0) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                    if (i < n) at[i] = acc[CH * j + i];
             }
+        }
         if (rpb > 1) {
             __syncthreads();
             for (int k = threadIdx.x; k < p.C; k += blockDim.x) {
@@ -445,10 +482,10 @@ struct VecKernel {
 };
 
 // What these kernels take: see the top.
-bool whole(int C, std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor> outs) {
+bool whole(std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor> outs) {
     auto ok = [](const RowTensor &t, int bytes) { return !t.p || (t.m.cs == 1 && t.m.uniform && dlc_aligned_rows(t, bytes)); };
     const int ch = all_of(DLC_DATA_FLOAT, ins) ? 4 : 8;
-    if (C % ch || !ring(ins)) return false;
+    if (!ring(ins)) return false;
     for (const RowTensor &t : ins)
         if (!ok(t, 16)) return false;
     for (const RowTensor &t : outs)
@@ -460,7 +497,7 @@ bool whole(int C, std::initializer_list<RowTensor> ins, std::initializer_list<Ro
 // fewer vectors, while the rows are too few to give every SM a block.
 VecPlan plan_vec(long long rows, int C, bool fp32, int most, bool warps, int sm_count) {
     VecPlan p;
-    const int nv = C / (fp32 ? 4 : 8);
+    const int nv = fp32 ? (C + 3) / 4 : (C + 7) / 8;
     p.tpr = 8;
     while (p.tpr < 32 && p.tpr * std::min(4, most) < nv) p.tpr *= 2;
     while (p.tpr * most < nv) p.tpr += warps && p.tpr >= 128 ? 32 : p.tpr;
@@ -504,7 +541,11 @@ VecKernel vec_fwd(int v, const LayerProblem &p) {
             case 1: return vec_fwd<1, float>(p);
             case 2: return vec_fwd<2, float>(p);
             case 3: return vec_fwd<3, float>(p);
-            default: return vec_fwd<4, float>(p);
+            case 4: return vec_fwd<4, float>(p);
+            case 5: return vec_fwd<5, float>(p);
+            case 6: return vec_fwd<6, float>(p);
+            case 7: return vec_fwd<7, float>(p);
+            default: return vec_fwd<8, float>(p);
         }
     }
     using Half = unsigned short;
@@ -551,9 +592,9 @@ VecKernel vec_bwd(const VecPlan &v, bool fp32, bool res) {
 
 bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &pb, dlcStatus_t &status) {
     LayerProblem p = pb;
-    if (!whole(p.C, {p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != p.x.dt)) return false;
+    if (!whole({p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != p.x.dt)) return false;
     const bool fp32 = p.x.dt == DLC_DATA_FLOAT;
-    const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 8, false, ctx->sm_count);
+    const VecPlan v = plan_vec(p.rows, p.C, fp32, 8, false, ctx->sm_count);
     if (!v.v) return false;
     status = launch_vec(ctx, vec_fwd(v.v, p), p, v, fp32, 2);
     return true;
@@ -561,7 +602,7 @@ bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &pb, dlcStatus_t &status)
 
 bool dlc_layer_bwd_vec(dlcContext *ctx, const LayerBwdProblem &pb, dlcStatus_t &status) {
     LayerBwdProblem p = pb;
-    if (!whole(p.C, {p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != p.t.dt) return false;
+    if (!whole({p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != p.t.dt) return false;
     const bool fp32 = p.t.dt == DLC_DATA_FLOAT, res = p.dt.p != nullptr;
     const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 2, true, ctx->sm_count);
     if (!v.v) return false;
