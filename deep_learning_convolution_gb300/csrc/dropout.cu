@@ -24,7 +24,7 @@ struct DoParams {
     DropoutProblem d;
     long long items, inner;  // pieces of a row's channels; the faster index runs over `inner` of them
     int apart;               // ... over the rows, because channels are apart
-    int rows_step;           // rows that the threads of the vector kernel take at once
+    int rows_step;           // rows that the threads of the columns kernel take at once
 };
 
 constexpr uint32_t PHILOX_M0 = 0xD2511F53u, PHILOX_M1 = 0xCD9E8D57u, PHILOX_W0 = 0x9E3779B9u, PHILOX_W1 = 0xBB67AE85u;
@@ -136,64 +136,64 @@ __device__ __forceinline__ void put(const RowTensor &t, long long off, int n, co
     }
 }
 
-// Rows of whole aligned vectors at one pitch: a thread keeps its eight channels and steps from row to
-// row, so what the generator owes to the channel is worked out once; U rows are in flight.  What bounds it
-// is the generator: 31 wide multiplies a vector (37 without this) and the 80 other integer instructions.
-template <typename X, typename R, typename Y>
-__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_vec_kernel(const __grid_constant__ DoParams p) {
+// Contiguous channels, rows at one pitch: a thread keeps its W channels and steps from row to row, so
+// what the generator owes to the channel is worked out once; U rows are in flight.  W = 8: aligned whole
+// vectors; W = 4: single elements.  What bounds it is the generator: 31 wide multiplies for eight channels
+// (37 without this), a warp's at four cycles each, and some 80 other integer instructions.
+template <int W, typename X, typename R, typename Y>
+__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_columns_kernel(const __grid_constant__ DoParams p) {
     griddep_launch_dependents();
-    constexpr int U = sizeof(X) + sizeof(R) > 4 ? 2 : 4;
-    const uint32_t vectors = (uint32_t)p.inner, i = blockIdx.x * DO_THREADS + threadIdx.x;
-    const uint32_t row0 = i / vectors, piece = i - row0 * vectors;
+    constexpr int U = W == 8 && sizeof(X) + sizeof(R) > 4 ? 2 : 4, G = W / 4;
+    const uint32_t pieces = (uint32_t)p.inner, i = blockIdx.x * DO_THREADS + threadIdx.x;
+    const uint32_t row0 = i / pieces, piece = i - row0 * pieces;
     if (row0 >= (uint32_t)p.rows_step) return;
+    const int n = min(W, p.d.C - (int)piece * W);
     griddep_wait();
     const Philox gen(p.d.random);
-    const PhiloxColumn left(gen, 2 * piece), right(gen, 2 * piece + 1);
+    const PhiloxColumn left(gen, G * piece), right(gen, G * piece + 1);
     const bool res = p.d.r.p != nullptr;
     uint32_t h0, l0;
     wide(gen.s0, PHILOX_M1, h0, l0);
     h0 ^= gen.k0[0];
-    const long long c = 8ll * piece;
-    const X *px = static_cast<const X *>(p.d.x.p) + row0 * p.d.x.m.ld + c;
-    const R *pr = static_cast<const R *>(p.d.r.p) + row0 * p.d.r.m.ld + c;
-    Y *py = static_cast<Y *>(p.d.y.p) + row0 * p.d.y.m.ld + c;
+    const long long c = (long long)W * piece;
+    long long px = row0 * p.d.x.m.ld + c, pr = row0 * p.d.r.m.ld + c, py = row0 * p.d.y.m.ld + c;
     const long long dx = p.rows_step * p.d.x.m.ld, dr = p.rows_step * p.d.r.m.ld, dy = p.rows_step * p.d.y.m.ld;
     for (long long row = row0; row < p.d.rows; row += (long long)U * p.rows_step) {
-        Piece<8, X> x[U];
-        Piece<8, R> r[U];
+        Piece<W, X> x[U];
+        Piece<W, R> r[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (row + k * p.rows_step < p.d.rows) {
-                x[k].load(p.d.x, px - static_cast<const X *>(p.d.x.p), 8);
-                if (res) r[k].load(p.d.r, pr - static_cast<const R *>(p.d.r.p), 8);
+                x[k].load(p.d.x, px, n);
+                if (res) r[k].load(p.d.r, pr, n);
                 px += dx;
                 pr += dr;
             }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (row + k * p.rows_step >= p.d.rows) break;
-            uint32_t hi, lo, u[8];
+            uint32_t hi, lo, u[W];
             wide(h0 ^ (uint32_t)(row + k * p.rows_step), PHILOX_M0, hi, lo);
             left.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u));
-            right.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u + 4));
-            float f[8];
+            if constexpr (G == 2) right.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u + 4));
+            float f[W];
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
+            for (int j = 0; j < W; j += 2) {
                 const float2 v = mul2(make_float2(x[k].at(j), x[k].at(j + 1)), pair_of(p.d.scale));
                 f[j] = u[j] >= p.d.border ? v.x : 0.f;
                 f[j + 1] = u[j + 1] >= p.d.border ? v.y : 0.f;
             }
             if (res) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) set2(f + j, 0, add2(get2(f + j, 0), make_float2(r[k].at(j), r[k].at(j + 1))));
+                for (int j = 0; j < W; j += 2) set2(f + j, 0, add2(get2(f + j, 0), make_float2(r[k].at(j), r[k].at(j + 1))));
             }
-            put<8, Y>(p.d.y, py - static_cast<Y *>(p.d.y.p), 8, f);
+            put<W, Y>(p.d.y, py, n, f);
             py += dy;
         }
     }
 }
 
-// Any layout: pieces of up to four channels, U of a thread in flight together; a thread steps from
+// Any other layout: pieces of up to four channels, U of a thread in flight together; a thread steps from
 // piece to piece without dividing.
 template <typename X, typename R, typename Y>
 __global__ void __launch_bounds__(DO_THREADS, 2) dropout_kernel(const __grid_constant__ DoParams p) {
@@ -244,16 +244,24 @@ __global__ void __launch_bounds__(DO_THREADS, 2) dropout_kernel(const __grid_con
 
 using Half = unsigned short;
 
-template <typename X, typename R>
-const void *do_kernel(int y, bool vec) {
-    if (y == DLC_DATA_BFLOAT16) return vec ? (const void *)dropout_vec_kernel<X, R, Half> : (const void *)dropout_kernel<X, R, Half>;
-    return vec ? (const void *)dropout_vec_kernel<X, R, float> : (const void *)dropout_kernel<X, R, float>;
+enum { ANY, SINGLES, VECTORS };
+
+template <typename X, typename R, typename Y>
+const void *do_kernel(int way) {
+    return way == VECTORS   ? (const void *)dropout_columns_kernel<8, X, R, Y>
+           : way == SINGLES ? (const void *)dropout_columns_kernel<4, X, R, Y>
+                            : (const void *)dropout_kernel<X, R, Y>;
 }
 
-const void *do_kernel(const DropoutProblem &d, bool vec) {
+template <typename X, typename R>
+const void *do_kernel(int y, int way) {
+    return y == DLC_DATA_BFLOAT16 ? do_kernel<X, R, Half>(way) : do_kernel<X, R, float>(way);
+}
+
+const void *do_kernel(const DropoutProblem &d, int way) {
     const bool x = d.x.dt == DLC_DATA_BFLOAT16, r = d.r.p ? d.r.dt == DLC_DATA_BFLOAT16 : x;
-    if (x) return r ? do_kernel<Half, Half>(d.y.dt, vec) : do_kernel<Half, float>(d.y.dt, vec);
-    return r ? do_kernel<float, Half>(d.y.dt, vec) : do_kernel<float, float>(d.y.dt, vec);
+    if (x) return r ? do_kernel<Half, Half>(d.y.dt, way) : do_kernel<Half, float>(d.y.dt, way);
+    return r ? do_kernel<float, Half>(d.y.dt, way) : do_kernel<float, float>(d.y.dt, way);
 }
 
 }  // namespace
@@ -261,16 +269,19 @@ const void *do_kernel(const DropoutProblem &d, bool vec) {
 dlcStatus_t dlc_launch_dropout(dlcContext *ctx, const DropoutProblem &pb) {
     DoParams p;
     p.d = pb;
-    auto vec = [&](const RowTensor &t) { return !t.p || (t.m.cs == 1 && t.m.uniform && dlc_aligned_rows(t, 16)); };
+    auto columns = [&](const RowTensor &t) { return !t.p || (t.m.cs == 1 && t.m.uniform); };
+    auto whole = [&](const RowTensor &t) { return !t.p || dlc_aligned_rows(t, 16); };
     const long long most = (long long)ctx->sm_count * DO_BLOCKS * DO_THREADS;  // threads
-    const bool v8 = pb.C % 8 == 0 && vec(pb.x) && vec(pb.r) && vec(pb.y) && pb.C / 8 <= most;
-    const int w = v8 ? 8 : 4;
+    int way = ANY;
+    if (columns(pb.x) && columns(pb.r) && columns(pb.y) && pb.C / 4 < most)
+        way = pb.C % 8 == 0 && whole(pb.x) && whole(pb.r) && whole(pb.y) ? VECTORS : SINGLES;
+    const int w = way == VECTORS ? 8 : 4;
     const long long pieces = (pb.C + w - 1) / w;
     p.items = pb.rows * pieces;
-    p.apart = pb.x.m.cs != 1 && pb.y.m.cs != 1;
-    p.inner = p.apart && !v8 ? pb.rows : pieces;
+    p.apart = way == ANY && pb.x.m.cs != 1 && pb.y.m.cs != 1;
+    p.inner = p.apart ? pb.rows : pieces;
     p.rows_step = (int)std::min(pb.rows, most / pieces);
-    const long long threads = v8 ? p.rows_step * pieces : std::min(p.items, (long long)ctx->sm_count * 2 * DO_THREADS);
+    const long long threads = way != ANY ? p.rows_step * pieces : std::min(p.items, (long long)ctx->sm_count * 2 * DO_THREADS);
     void *args[] = {&p};
-    return dlc_launch(ctx, do_kernel(pb, v8), dim3((unsigned)((threads + DO_THREADS - 1) / DO_THREADS)), dim3(DO_THREADS), 0, args);
+    return dlc_launch(ctx, do_kernel(pb, way), dim3((unsigned)((threads + DO_THREADS - 1) / DO_THREADS)), dim3(DO_THREADS), 0, args);
 }
