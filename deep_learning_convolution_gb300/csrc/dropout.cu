@@ -10,7 +10,9 @@
 // random numbers: as easy as 1, 2, 3" (2011): a round multiplies two of the four words and
 // crosses the halves of the products.
 //
-// Bound by memory: x (and r) in, y out.
+// x (and r) in, y out: memory bounds it with a residual, the generator's multiplies without.  16384 x 4096
+// BF16 63.8 us with residual (6.3 TB/s) and 57 us without (4.7); unaligned rows, 16384 x 1001 with
+// residual, 34 us; channels apart, 128 images of 512 x 28 x 28, 172 us (1.2 TB/s).
 #include "channel.cuh"
 #include "ptx.cuh"
 

