@@ -202,6 +202,29 @@ __global__ void __launch_bounds__(CE_THREADS) ce_dz_kernel(const __grid_constant
     }
 }
 
+// Many strips of partial sums to CE_STRIPS of them, in a fixed order: 32 columns and one range of the strips
+// a block, for column_sum's blocks to add up the rest.
+constexpr int CE_STRIPS = 256;
+
+__global__ void __launch_bounds__(1024) ce_strips_kernel(const float *sums, float *out, int cols, int strips) {
+    griddep_launch_dependents();
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + lane;
+    const int s0 = (int)((long long)strips * blockIdx.y / CE_STRIPS), s1 = (int)((long long)strips * (blockIdx.y + 1) / CE_STRIPS);
+    griddep_wait();
+    float s = 0.f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = s0 + warp; i < s1; i += 32) s += sums[(long long)i * cols + c];
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        for (int w = 1; w < 32; ++w) s += part[w][lane];
+        out[(long long)blockIdx.y * cols + c] = s;
+    }
+}
+
 // ---- host side -------------------------------------------------------------------------
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -250,7 +273,7 @@ struct CePlan {
     long long ld = 0, ldz = 0;
     bool x_packed = false, w_packed = false;
     void *x_copy = nullptr, *w_copy = nullptr;
-    float *z = nullptr, *chosen = nullptr, *sums = nullptr;
+    float *z = nullptr, *chosen = nullptr, *sums = nullptr, *few_sums = nullptr;
     float2 *part = nullptr;
     unsigned short *dz = nullptr;
     RowTensor dx_sum;          // FP32, where several pieces add to a dx that is none
@@ -420,7 +443,10 @@ CePlan plan_bwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
         if (p.dw.p) most = std::max(most, dlc_gemm_workspace(ctx, b.filters(p, n0, cols)));
         return DLC_STATUS_SUCCESS;
     });
-    if (p.dbias) b.sums = static_cast<float *>(b.take(sums));
+    if (p.dbias) {
+        b.sums = static_cast<float *>(b.take(sums));
+        b.few_sums = static_cast<float *>(b.take((size_t)CE_STRIPS * b.piece * 4));
+    }
     b.gemm_ws = static_cast<char *>(b.take(most));
     return b;
 }
@@ -495,7 +521,14 @@ dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProb
             s = dlc_launch(ctx, (const void *)ce_dz_kernel,
                            dim3((unsigned)((cols + 4 * CE_THREADS - 1) / (4 * CE_THREADS)), (unsigned)rows), dim3(CE_THREADS), 0, args);
         }
-        if (s == DLC_STATUS_SUCCESS && p.dbias) s = dlc_launch_column_sum(ctx, b.sums, p.dbias + n0, cols, rows);
+        if (s == DLC_STATUS_SUCCESS && p.dbias) {
+            const bool many = rows > 8 * CE_STRIPS;
+            int n = cols, strips = rows;
+            float *from = b.sums, *to = b.few_sums;
+            void *args[] = {&from, &to, &n, &strips};
+            if (many) s = dlc_launch(ctx, (const void *)ce_strips_kernel, dim3((unsigned)((cols + 31) / 32), CE_STRIPS), dim3(1024), 0, args);
+            if (s == DLC_STATUS_SUCCESS) s = dlc_launch_column_sum(ctx, many ? to : from, p.dbias + n0, cols, many ? CE_STRIPS : rows);
+        }
         if (s == DLC_STATUS_SUCCESS && p.dx.p) s = dlc_launch_gemm(ctx, b.data(p, n0, cols));
         if (s == DLC_STATUS_SUCCESS && p.dw.p) s = dlc_launch_gemm(ctx, b.filters(p, n0, cols));
         return s;

@@ -138,12 +138,14 @@ constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32, SORT_EACH = 4,
 // Lists of up to RANK_MOST tokens are ranked by counting (8192 x 256 into 1003 rows: 33 us, by digits 18; up to
 // 2048 tokens as fast or faster, in one launch).
 constexpr int RANK_MOST = 4096, RANK_THREADS = 256;
+constexpr int SORT_OWN_SUMS = 64;  // tiles
 
 struct SortParams {
     IndexList tokens;
     int rows, V, tiles;
     int bits, passes;       // of a digit; of the sort
-    int *hist;              // [pass][tile][digit]
+    int *hist;              // [pass][tile][digit]; a last row for the totals
+    int scanned;            // hist holds the counts of the tiles ahead, and the totals
     uint32_t *key[2], *row[2];  // pass p writes the arrays p mod 2
     int *err;
     int blocks;                 // that sort; those behind them zero this launch's part of the table
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_c
         return;
     }
     const long long all = (long long)p.blocks * SORT_THREADS, me = (long long)blockIdx.x * SORT_THREADS + threadIdx.x;
-    const long long per = (long long)p.tiles * digits;
+    const long long per = (long long)(p.tiles + 1) * digits;
     for (long long i = per + me; i < per * p.passes; i += all) p.hist[i] = 0;
     for (int tile = blockIdx.x; tile < p.tiles; tile += p.blocks) {
 #pragma unroll
@@ -318,6 +320,39 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_c
             count[d] = 0;
         }
         __syncthreads();
+    }
+}
+
+// Long lists: the tiles' counts of a pass become those of the tiles ahead, and the totals go to the last
+// row.  32 digits a block; each warp takes a range of the tiles, twice.  (Otherwise a block of the
+// next kernel adds up all tiles' counts itself: up to SORT_OWN_SUMS of them cost less than a launch.)
+__global__ void __launch_bounds__(1024) sort_scan_kernel(const __grid_constant__ SortParams p, int pass) {
+    griddep_launch_dependents();
+    __shared__ int part[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, digits = 1 << p.bits, d = (int)blockIdx.x * 32 + lane;
+    griddep_wait();
+    int *hist = p.hist + (long long)pass * (p.tiles + 1) * digits;
+    const int t0 = (int)((long long)p.tiles * warp / 32), t1 = (int)((long long)p.tiles * (warp + 1) / 32);
+    int sum = 0;
+    if (d < digits) {
+#pragma unroll 8
+        for (int t = t0; t < t1; ++t) sum += hist[(long long)t * digits + d];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    int ahead = 0;
+    for (int w = 0; w < warp; ++w) ahead += part[w][lane];
+    if (d >= digits) return;
+    if (warp == 31) hist[(long long)p.tiles * digits + d] = ahead + sum;
+    for (int t0b = t0; t0b < t1; t0b += 8) {
+        int c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = t0b + k < t1 ? hist[(long long)(t0b + k) * digits + d] : 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (t0b + k < t1) hist[(long long)(t0b + k) * digits + d] = ahead;
+            ahead += c[k];
+        }
     }
 }
 
@@ -348,11 +383,15 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
     }
     int rank[SORT_EACH], all[2] = {0, 0}, before[2] = {0, 0};
     const uint32_t mask = (uint32_t)digits - 1u;
-    const int *hist = p.hist + (long long)pass * p.tiles * digits;
-    if (2 * (int)threadIdx.x < digits) {
+    const int *hist = p.hist + (long long)pass * (p.tiles + 1) * digits + 2 * threadIdx.x;
+    if (2 * (int)threadIdx.x < digits && p.scanned) {
+        const int2 b = *reinterpret_cast<const int2 *>(hist + (long long)tile * digits);
+        const int2 c = *reinterpret_cast<const int2 *>(hist + (long long)p.tiles * digits);
+        before[0] = b.x, before[1] = b.y, all[0] = c.x, all[1] = c.y;
+    } else if (2 * (int)threadIdx.x < digits) {
 #pragma unroll 8
         for (int t = 0; t < p.tiles; ++t) {
-            const int2 c = *reinterpret_cast<const int2 *>(hist + (long long)t * digits + 2 * threadIdx.x);
+            const int2 c = *reinterpret_cast<const int2 *>(hist + (long long)t * digits);
             all[0] += c.x, all[1] += c.y;
             if (t < tile) before[0] += c.x, before[1] += c.y;
         }
@@ -370,7 +409,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_pass_kernel(const __grid_co
             p.key[pass & 1][at] = key[k];
             p.row[pass & 1][at] = row[k];
             if (more)
-                atomicAdd(p.hist + ((long long)(pass + 1) * p.tiles + at / SORT_TILE) * digits + ((key[k] >> ((pass + 1) * p.bits)) & mask), 1);
+                atomicAdd(p.hist + ((long long)(pass + 1) * (p.tiles + 1) + at / SORT_TILE) * digits + ((key[k] >> ((pass + 1) * p.bits)) & mask), 1);
         }
 }
 
@@ -578,7 +617,7 @@ BwdPlan plan_bwd(long long rows, int C, int V) {
         off += round256(bytes);
         return at;
     };
-    b.hist = take((size_t)b.passes * b.tiles * (1u << b.bits) * 4);
+    b.hist = take((size_t)b.passes * (b.tiles + 1) * (1u << b.bits) * 4);
     for (int i = 0; i < 2; ++i) b.key[i] = take((size_t)rows * 4), b.row[i] = take((size_t)rows * 4);
     b.part = take((size_t)b.chunks * 2 * C * 4);
     b.bytes = off;
@@ -613,6 +652,7 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     s.tiles = b.tiles;
     s.bits = b.bits;
     s.passes = b.passes;
+    s.scanned = 0;
     s.hist = reinterpret_cast<int *>(e.ws + b.hist);
     for (int i = 0; i < 2; ++i) {
         s.key[i] = reinterpret_cast<uint32_t *>(e.ws + b.key[i]);
@@ -646,9 +686,12 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
         unsigned fill = part(0);
         st = dlc_launch(ctx, (const void *)sort_count_kernel, dim3((unsigned)s.blocks + fill), dim3(SORT_THREADS), 0, args);
         s.blocks = b.tiles;
+        s.scanned = b.tiles > SORT_OWN_SUMS;
         for (int pass = 0; pass < b.passes && st == DLC_STATUS_SUCCESS; ++pass) {
             fill = part(1 + pass);
             void *pargs[] = {&s, &pass};
+            if (s.scanned) st = dlc_launch(ctx, (const void *)sort_scan_kernel, dim3(((1u << b.bits) + 31) / 32), dim3(1024), 0, pargs);
+            if (st != DLC_STATUS_SUCCESS) break;
             st = dlc_launch(ctx, (const void *)sort_pass_kernel, dim3((unsigned)b.tiles + fill), dim3(SORT_THREADS), 0, pargs);
         }
         if (st != DLC_STATUS_SUCCESS) return st;

@@ -108,6 +108,41 @@ def test_layer_norm_in_place_equal_and_non_finite_rows(handle, c, layout):
     assert torch.isnan(y[2].float()).all() and torch.isnan(y[4].float()).all()
 
 
+@pytest.mark.parametrize("rows,c,dtype", [(40, 768, BF), (700, 2048, BF), (33, 300, F32), (9, 100, BF)])
+def test_layer_norm_of_one_type_in_place(handle, rows, c, dtype):
+    """The sum in the place of either operand, the gradient in that of dtotal."""
+    gamma, beta, y = 1 + 0.3 * rand(c, seed=3), rand(c, seed=4), torch.empty(rows, c, dtype=dtype, device="cuda")
+    for place in range(2):
+        ops = [laid_out(rand(rows, c, seed=s, dtype=dtype), "pitch") for s in (1, 2)]
+        t, want, err = ref.layer_norm(d(ops[0]), d(ops[1]), d(gamma), d(beta), EPS)
+        api.LayerNormForward(handle, ops[0], y, residual=ops[1], total=ops[place], eps=EPS)(
+            ops[0], gamma, y, beta=beta, residual=ops[1], total=ops[place])
+        close(ops[place], t, cref.stored(t, dtype) + cref.U32 * t.abs(), "total")
+        close(y, want, err + cref.stored(want, dtype), "y")
+    dt = ops[0]
+    (want, ex), _, _ = ref.layer_norm_backward(d(y), d(ops[1]), d(gamma), d(dt), EPS)
+    api.LayerNormBackward(handle, y, ops[1], dt, dtotal=dt, eps=EPS)(y, ops[1], gamma, dt, dtotal=dt)
+    close(dt, want, ex + cref.stored(want, dtype), "dx")
+
+
+def test_broadcast_residuals_are_read_by_their_strides(handle):
+    """A residual of one row for all."""
+    rows, c = 70, 256
+    x, one, y = rand(rows, c, seed=1, dtype=BF), rand(1, c, seed=2, dtype=BF), torch.empty(rows, c, dtype=BF, device="cuda")
+    many, g = one.expand(rows, c), torch.ones(c, device="cuda")
+    try:
+        op = api.LayerNormForward(handle, x, y, residual=many, eps=EPS)
+    except B.DlcError as e:  # strides of zero are none that a descriptor takes
+        assert e.status == B.DLC_STATUS_BAD_PARAM
+        return
+    op(x, g, y, residual=many)
+    _, want, err = ref.layer_norm(d(x), d(many), d(g), None, EPS)
+    close(y, want, err + cref.stored(want, BF), "layer norm")
+    api.DropoutForward(handle, x, y, p=0.5, residual=many)(x, words(1, 2), y, residual=many)
+    want, _ = ref.dropout(d(x), d(many), 0.5, 1, 2)
+    close(y, want, cref.stored(want, BF) + 4 * cref.U32 * (want.abs() + d(many).abs()), "dropout")
+
+
 @pytest.mark.parametrize("c", [64, 768, 5000])
 def test_layer_norm_of_rows_far_from_zero(handle, c):
     """The variance is about the mean: a mean of 300 deviations costs what the rounding of the
@@ -320,7 +355,7 @@ def test_embedding_backward(handle, rows, c, v, ddt, tdt, accumulate):
     assert torch.equal(dt, again)
 
 
-@pytest.mark.parametrize("rows,c,v", [(9000, 264, 5), (300, 2056, 1), (130000, 8, 40)])
+@pytest.mark.parametrize("rows,c,v", [(9000, 264, 5), (300, 2056, 1), (130000, 8, 40), (300001, 8, 3), (300001, 8, 200000)])
 def test_embedding_backward_of_few_tokens(handle, rows, c, v):
     """Every token's rows reach over many blocks."""
     dy, dt = rand(rows, c, seed=1, dtype=BF), out_like(v, c, F32)
@@ -460,6 +495,16 @@ def test_cross_entropy_of_many_rows_in_pieces(handle):
         f = ref.cross_entropy(d(x[at]), d(w), target[at], d(b))
         close(lse[at], *f["lse"], "lse")
         close(loss[at], *f["loss"], "loss")
+
+
+@pytest.mark.parametrize("rows,v", [(70000, 19), (140001, 300)])
+def test_bias_gradient_of_many_rows(handle, rows, v):
+    x, w, b, target, dloss = entropy_case(rows, 16, v, True)
+    loss, lse, db = (torch.empty(n, device="cuda") for n in (rows, rows, v))
+    api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, bias=b)
+    api.CrossEntropyBackward(handle, x, w, target)(x, w, target, lse, dloss, bias=b, dbias=db)
+    f = ref.cross_entropy(d(x), d(w), target, d(b))
+    close(db, *ref.cross_entropy_backward(d(x), d(w), target, f, d(dloss), BF, BF)[2], "dbias")
 
 
 def test_cross_entropy_of_images(handle):
