@@ -276,7 +276,7 @@ struct CePlan {
     float *z = nullptr, *chosen = nullptr, *sums = nullptr, *few_sums = nullptr;
     float2 *part = nullptr;
     unsigned short *dz = nullptr;
-    RowTensor dx_sum;          // FP32, where several pieces add to a dx that is none
+    RowTensor dx_sum;          // FP32, where several pieces add to a dx of another type
     char *gemm_ws = nullptr;
     size_t bytes = 0;
     char *base;

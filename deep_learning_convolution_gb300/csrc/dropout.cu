@@ -102,7 +102,7 @@ struct PhiloxColumn {
 // W channels of a row from memory: eight in 16-byte accesses, or up to four at any stride.
 template <int W, typename E>
 struct Piece {
-    E v[W];
+    alignas(16) E v[W];
     __device__ __forceinline__ void load(const RowTensor &t, long long off, int n) {
         const E *p = static_cast<const E *>(t.p) + off;
         if constexpr (W == 8) {

@@ -7,8 +7,8 @@
 // launch for few rows (64 x 4096 2.3 us).
 //
 // Backward: the tokens are sorted by a stable radix sort (so that the rows of a token stay
-// in order and the FP32 sums are the same every time); blocks then take runs of
-// 32 sorted positions and a slab of channels and add the rows of each token up in
+// in order and the FP32 sums are the same every time); blocks then take runs of 16 to
+// 128 sorted positions and a slab of channels and add the rows of each token up in
 // registers.  A token whose rows reach over several blocks leaves a partial sum in each,
 // which a last kernel adds in order: a token that is every tenth one costs no more than
 // the others.  The table is zeroed beside the sort, whose own time is latency, and the
@@ -32,7 +32,7 @@ __device__ __forceinline__ long long token_at(const IndexList &t, long long i) {
 // W channels: 8 or 4 in one or two accesses, or one.
 template <int W, typename T>
 struct Words {
-    T v[W];
+    alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) T v[W];
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (W * sizeof(T) >= 16) {
 #pragma unroll
@@ -659,6 +659,17 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
         s.row[i] = reinterpret_cast<uint32_t *>(e.ws + b.row[i]);
     }
     s.err = ctx->d_err;
+    SumParams p;
+    p.e = e;
+    p.key = s.key[(b.passes - 1) & 1];
+    p.row = s.row[(b.passes - 1) & 1];
+    p.part = reinterpret_cast<float *>(e.ws + b.part);
+    p.chunk = b.chunk;
+    p.chunks = b.chunks;
+    const int w = vectors(e, 8) ? 8 : vectors(e, 4) ? 4 : 1;
+    const int threads = std::min(SUM_THREADS, ((e.C + w - 1) / w + 31) / 32 * 32);
+    p.slabs = (e.C + threads * w - 1) / (threads * w);
+    if ((long long)p.chunks * p.slabs > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     // the table's whole 16-byte words, dealt evenly to the sort's launches
     const size_t bytes = e.accumulate ? 0 : (size_t)e.V * e.C * dlc_dtype_bytes((dlcDataType_t)e.table.dt);
     char *table = static_cast<char *>(e.table.p);
@@ -696,17 +707,6 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
         }
         if (st != DLC_STATUS_SUCCESS) return st;
     }
-    SumParams p;
-    p.e = e;
-    p.key = s.key[(b.passes - 1) & 1];
-    p.row = s.row[(b.passes - 1) & 1];
-    p.part = reinterpret_cast<float *>(e.ws + b.part);
-    p.chunk = b.chunk;
-    p.chunks = b.chunks;
-    const int w = vectors(e, 8) ? 8 : vectors(e, 4) ? 4 : 1;
-    const int threads = std::min(SUM_THREADS, ((e.C + w - 1) / w + 31) / 32 * 32);
-    p.slabs = (e.C + threads * w - 1) / (threads * w);
-    if ((long long)p.chunks * p.slabs > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     void *sargs[] = {&p};
     const void *sum = w == 8 ? sum_kernel<8>(e) : w == 4 ? sum_kernel<4>(e) : sum_kernel<1>(e);
     st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs)), dim3((unsigned)threads), 0, sargs);
