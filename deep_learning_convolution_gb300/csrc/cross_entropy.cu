@@ -403,7 +403,8 @@ CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     // (a part: 32 classes at least)
     f.piece = f.fused ? (int)std::min<long long>(p.V, std::max<long long>(1024, (long long)(CE_PART_BYTES / 8) / p.M * 32 / 256 * 256))
                       : piece_of(p, 4);
-    f.operands(p);
+    // (the matrix-vector kernel takes the operands as they are)
+    if (f.fused || !dlc_gemv_ok(f.logits(p, 0, f.piece))) f.operands(p);
     if (!f.fused) {
         f.ld = (f.piece + 3) / 4 * 4;
         f.z = static_cast<float *>(f.take((size_t)p.M * f.ld * 4));

@@ -329,7 +329,7 @@ bool gv_vec(const GemmProblem &g) {
 // has to read element by element run at 1.2 MB/us: faster than packing them
 // first for one or two rows (4003 -> 4004, two rows: 21.9 us against 35).
 bool dlc_gemv_ok(const GemmProblem &g) {
-    if (g.a.trans || g.b.trans) return false;
+    if (g.a.trans || g.b.trans || (g.N > 1 && g.b.t.m.ld != g.K)) return false;  // (padded rows: copies)
     if (!gv_vec(g)) return g.M <= 2;
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
     if (g.M > (e4m3 ? 2 : 4)) return false;

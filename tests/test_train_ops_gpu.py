@@ -473,6 +473,30 @@ def test_cross_entropy_types_and_layouts(handle, rows, c, v, dx_dtype, dw_dtype,
     check_entropy(handle, laid_out(x, layout), w, b, target.to(torch.int32), dloss, dx_dtype, dw_dtype, layout)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3])
+@pytest.mark.parametrize("c,v,layout", [(5, 64, "dense"), (41, 5003, "odd"), (38, 700, "pitch"), (64, 900, "odd"), (64, 901, "columns"), (1, 88, "dense"),
+                                        (366, 1, "columns")])
+def test_cross_entropy_of_single_rows_of_any_layout(handle, rows, c, v, layout):
+    """Operands that vectors do not reach, as they are and as copies with padded rows."""
+    x, w, b, target, dloss = entropy_case(rows, c, v, True)
+    x, target = laid_out(x, layout), torch.arange(rows, device="cuda") % v
+    check_entropy(handle, x, w, b, target, dloss, layout=layout)
+    shifted = torch.empty(v * c + 1, dtype=BF, device="cuda")[1:].view(v, c)  # not at a vector's address
+    shifted.copy_(w)
+    check_entropy(handle, x, shifted, b, target, dloss, layout=layout)
+
+
+@pytest.mark.parametrize("rows,c,v", [(1, 40, 600), (2, 24, 513), (3, 41, 700), (1, 41, 5000), (1, 7, 1)])
+def test_cross_entropy_of_single_e4m3_rows(handle, rows, c, v):
+    x, w = rand(rows, c, seed=1).to(F8), rand(v, c, seed=2, std=0.5).to(F8)
+    sx, sw, target = rand(rows, seed=3).abs() + 0.1, rand(v, seed=4).abs() + 0.1, torch.arange(rows, device="cuda") % v
+    loss, lse = out_like(rows, 1, F32)[:, 0], out_like(rows, 1, F32)[:, 0]
+    api.CrossEntropyForward(handle, x, w, target)(x, w, target, loss, lse, x_scale=sx, w_scale=sw)
+    f = ref.cross_entropy(d(x), d(w), target, None, d(sx), d(sw))
+    close(lse, *f["lse"], "lse")
+    close(loss, *f["loss"], "loss")
+
+
 @pytest.mark.parametrize("rows,c,v", [(8192, 64, 40000), (5000, 40, 70001), (9000, 41, 33001)])
 @pytest.mark.parametrize("dx_dtype", [F32, BF])
 def test_cross_entropy_in_pieces_of_the_classes(handle, rows, c, v, dx_dtype):
