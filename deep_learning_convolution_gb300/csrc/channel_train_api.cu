@@ -15,6 +15,9 @@ bool absent_or_ready(dlcTensorDescriptor_t d, const void *p) { return !p || read
 
 bool like(const dlcTensorStruct *d, const dlcTensorStruct *x, const void *p) { return !p || (same_rows(d, x) && d->c == x->c); }
 
+// Channels, and rows of a table, up to which 32-bit indices with a tile's or a block's step above them hold.
+constexpr int MOST_INDEX = 0x7fff0000;
+
 dlcStatus_t index_list(dlcIndexType_t type, const void *p, long long rows, IndexList &t, Span &s) {
     if (type != DLC_INDEX_INT32 && type != DLC_INDEX_INT64) return DLC_STATUS_BAD_PARAM;
     const int e = type == DLC_INDEX_INT64 ? 8 : 4;
@@ -37,7 +40,7 @@ dlcStatus_t layer_forward(dlcHandle_t h, double epsilon, dlcTensorDescriptor_t x
     if (!xd->set || !yd->set || !absent_or_ready(rd, residual) || !absent_or_ready(td, total)) return DLC_STATUS_NOT_INITIALIZED;
     if (!like(yd, xd, yd) || !like(rd, xd, residual) || !like(td, xd, total)) return DLC_STATUS_BAD_PARAM;
     if (!is_float(xd->dtype) || (residual && !is_float(rd->dtype)) || (total && !is_float(td->dtype)) ||
-        !(is_float(yd->dtype) || yd->dtype == DLC_DATA_FLOAT8_E4M3))
+        !(is_float(yd->dtype) || yd->dtype == DLC_DATA_FLOAT8_E4M3) || xd->c > MOST_INDEX)
         return DLC_STATUS_NOT_SUPPORTED;
     if ((yd->dtype == DLC_DATA_FLOAT8_E4M3) != (scale != nullptr) || !fp32_ok(scale)) return DLC_STATUS_BAD_PARAM;
     LayerProblem p;
@@ -74,7 +77,8 @@ dlcStatus_t layer_backward(dlcHandle_t h, double epsilon, dlcTensorDescriptor_t 
         return DLC_STATUS_BAD_PARAM;
     if (!dyd->set || !td->set || !dxd->set || !absent_or_ready(dtd, dtotal)) return DLC_STATUS_NOT_INITIALIZED;
     if (!like(dyd, td, dyd) || !like(dxd, td, dxd) || !like(dtd, td, dtotal)) return DLC_STATUS_BAD_PARAM;
-    if (!is_float(dyd->dtype) || !is_float(td->dtype) || !is_float(dxd->dtype) || (dtotal && !is_float(dtd->dtype)))
+    if (!is_float(dyd->dtype) || !is_float(td->dtype) || !is_float(dxd->dtype) || (dtotal && !is_float(dtd->dtype)) ||
+        td->c > MOST_INDEX)
         return DLC_STATUS_NOT_SUPPORTED;
     LayerBwdProblem p;
     p.rows = rows_of(td);
@@ -114,7 +118,8 @@ dlcStatus_t dropout(dlcHandle_t h, double probability, const uint64_t *random, d
     if (!xd || !yd || !random || (uintptr_t)random % 8 || !(probability >= 0.0 && probability < 1.0)) return DLC_STATUS_BAD_PARAM;
     if (!xd->set || !yd->set || !absent_or_ready(rd, residual)) return DLC_STATUS_NOT_INITIALIZED;
     if (!like(yd, xd, yd) || !like(rd, xd, residual)) return DLC_STATUS_BAD_PARAM;
-    if (!is_float(xd->dtype) || !is_float(yd->dtype) || (residual && !is_float(rd->dtype)) || rows_of(xd) > 0x7fffffffLL)
+    if (!is_float(xd->dtype) || !is_float(yd->dtype) || (residual && !is_float(rd->dtype)) || rows_of(xd) > 0x7fffffffLL ||
+        xd->c > MOST_INDEX)
         return DLC_STATUS_NOT_SUPPORTED;
     Span s_x, s_y, s_r{0, 0};
     const Span s_s = span_bytes(random, 16);
@@ -144,7 +149,8 @@ dlcStatus_t table_checks(dlcFilterDescriptor_t wd, dlcTensorDescriptor_t yd) {
     if (!wd || !yd) return DLC_STATUS_BAD_PARAM;
     if (!wd->set || !yd->set) return DLC_STATUS_NOT_INITIALIZED;
     if (wd->r != 1 || wd->s != 1 || wd->c != yd->c) return DLC_STATUS_BAD_PARAM;
-    if (!is_float(wd->dtype) || !is_float(yd->dtype) || rows_of(yd) > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
+    if (!is_float(wd->dtype) || !is_float(yd->dtype) || rows_of(yd) > 0x7fffffffLL || wd->c > MOST_INDEX || wd->k > MOST_INDEX)
+        return DLC_STATUS_NOT_SUPPORTED;
     return DLC_STATUS_SUCCESS;
 }
 
@@ -156,7 +162,7 @@ dlcStatus_t embedding(dlcHandle_t h, bool backward, double scale, int accumulate
     Span s_y, s_i;
     RETURN_IF(index_list(type, tokens, rows_of(yd), p.tokens, s_i));
     const int e = dlc_dtype_bytes(wd->dtype);
-    if (!table || (uintptr_t)table % e || !span_of(yd, y, !backward, s_y) || !std::isfinite(scale)) return DLC_STATUS_BAD_PARAM;
+    if (!table || (uintptr_t)table % e || !span_of(yd, y, !backward, s_y) || !std::isfinite((float)scale)) return DLC_STATUS_BAD_PARAM;
     const Span s_w = span_bytes(table, (uint64_t)wd->k * wd->c * e);
     if (overlaps(s_w, {s_y}) || overlaps(backward ? s_w : s_y, {s_i})) return DLC_STATUS_BAD_PARAM;
     p.rows = rows_of(yd);
@@ -185,7 +191,8 @@ dlcStatus_t resolve_entropy(dlcTensorDescriptor_t xd, const void *x, dlcFilterDe
     if (!xd || !wd) return DLC_STATUS_BAD_PARAM;
     if (!xd->set || !wd->set) return DLC_STATUS_NOT_INITIALIZED;
     if (wd->r != 1 || wd->s != 1 || wd->c != xd->c || wd->dtype != xd->dtype) return DLC_STATUS_BAD_PARAM;
-    if (!(xd->dtype == DLC_DATA_BFLOAT16 || (!backward && xd->dtype == DLC_DATA_FLOAT8_E4M3)) || rows_of(xd) > 0x7fffffffLL)
+    if (!(xd->dtype == DLC_DATA_BFLOAT16 || (!backward && xd->dtype == DLC_DATA_FLOAT8_E4M3)) || rows_of(xd) > 0x7fffffffLL ||
+        wd->c > MOST_INDEX || wd->k > MOST_INDEX)
         return DLC_STATUS_NOT_SUPPORTED;
     p.M = rows_of(xd);
     p.V = wd->k;

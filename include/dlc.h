@@ -678,7 +678,8 @@ dlcStatus_t dlcGetGatedBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescri
  * aligned to that.  A negative one stands for none (a padded row); one beyond
  * the last row of the table counts as none as well, and the kernel records
  * DLC_DEVERR_INDEX with the row, which dlcSynchronize and the handle's next
- * call report.  These calls take up to 2^31 - 1 rows, the layer norm more.
+ * call report.  These calls take up to 2^31 - 1 rows, the layer norm more, and
+ * up to 2^31 - 2^16 channels and rows of a table.
  */
 
 /* total = x + residual;  with mean and variance over the channels of a row,
@@ -738,7 +739,7 @@ dlcStatus_t dlcDropoutBackward(dlcHandle_t handle, double probability, const uin
 
 /* y[m] = scale * table[tokens[m]], zeros for a token that stands for none.  table:
  * V rows of C channels ([V, C, 1, 1]); y: rows of C channels; FLOAT or BFLOAT16
- * independently.  scale is finite. */
+ * independently.  scale is finite (in FP32). */
 dlcStatus_t dlcEmbeddingForward(dlcHandle_t handle, double scale, dlcIndexType_t indexType,
                                 const void *tokens, dlcFilterDescriptor_t tableDesc,
                                 const void *table, dlcTensorDescriptor_t yDesc, void *y);

@@ -96,7 +96,7 @@ def test_wrong_arguments_are_refused(handle):
             api.CrossEntropyForward(handle, x, table, bad)
     with pytest.raises(TypeError):
         api.EmbeddingForward(handle, tokens.short(), table, y)
-    for scale in (float("inf"), float("nan")):
+    for scale in (float("inf"), float("nan"), 1e39):
         with pytest.raises(B.DlcError):
             api.EmbeddingForward(handle, tokens, table, y, scale=scale)(tokens, table, y)
     with pytest.raises(B.DlcError):  # channels that do not match
@@ -117,6 +117,29 @@ def test_wrong_arguments_are_refused(handle):
     with pytest.raises(B.DlcError):
         api.LayerNormForward(handle, x, y, eps=-1.0)(x, torch.ones(64, device="cuda"), y)
     handle.synchronize()
+
+
+def test_indices_beyond_32_bits_are_refused(handle):
+    """Rows of almost 2^31 channels, and tables of as many rows."""
+    c = 2 ** 31 - 1
+    x, y = torch.empty(1, c, dtype=BF, device="cuda"), torch.empty(1, c, dtype=BF, device="cuda")
+    gamma, token, state = torch.empty(c, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")
+    long, thin = torch.empty(c, 1, dtype=BF, device="cuda"), torch.empty(1, 1, dtype=BF, device="cuda")
+    before = handle.launches()
+    for call in (lambda: api.LayerNormForward(handle, x, y)(x, gamma, y),
+                 lambda: api.LayerNormBackward(handle, x, x, y)(x, x, gamma, y),
+                 lambda: api.DropoutForward(handle, x, y, p=0.5)(x, state, y),
+                 lambda: api.EmbeddingForward(handle, token, x, y)(token, x, y),
+                 lambda: api.EmbeddingForward(handle, token, long, thin)(token, long, thin),
+                 lambda: api.EmbeddingBackward(handle, token, x, y),
+                 lambda: api.EmbeddingBackward(handle, token, thin, long),
+                 lambda: api.CrossEntropyForward(handle, x, x, token),
+                 lambda: api.CrossEntropyForward(handle, thin, long, token),
+                 lambda: api.CrossEntropyBackward(handle, thin, long, token)):
+        with pytest.raises(B.DlcError) as e:
+            call()
+        assert e.value.status == B.DLC_STATUS_NOT_SUPPORTED
+    assert handle.launches() == before
 
 
 def test_outputs_over_inputs_are_refused(handle):
