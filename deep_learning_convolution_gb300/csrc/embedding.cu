@@ -23,24 +23,32 @@ namespace {
 
 using namespace dlc;
 
-constexpr int EM_THREADS = 256, EM_BLOCKS = 3;  // blocks an SM holds
+constexpr int EM_THREADS = 256, EM_BLOCKS = 3;  // blocks of whole vectors an SM holds
 
 __device__ __forceinline__ long long token_at(const IndexList &t, long long i) {
     return t.wide ? static_cast<const long long *>(t.p)[i] : static_cast<const int *>(t.p)[i];
 }
 
-// W channels: 8 or 4 in one or two accesses, or one.
-template <int W, typename T>
+// W channels of a row: 8 or 4 neighbours in one or two accesses, or (APART) single ones `hop` elements apart, of
+// which n exist.
+template <int W, bool APART, typename T>
 struct Words {
     alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) T v[W];
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (W * sizeof(T) >= 16) {
+    __device__ __forceinline__ void load(const T *p, long long hop, int n) {
+        if constexpr (APART) {
+            if (n >= W) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = p[j * hop];
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = j < n ? p[j * hop] : (T)0;
+            }
+        } else if constexpr (W * sizeof(T) >= 16) {
 #pragma unroll
             for (int j = 0; j < W * (int)sizeof(T) / 16; ++j) reinterpret_cast<uint4 *>(v)[j] = reinterpret_cast<const uint4 *>(p)[j];
-        } else if constexpr (W * sizeof(T) == 8) {
-            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
         } else {
-            v[0] = p[0];
+            static_assert(W * sizeof(T) == 8, "");
+            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
         }
     }
     __device__ __forceinline__ float at(int j) const {
@@ -51,10 +59,12 @@ struct Words {
     }
 };
 
-template <int W, typename T>
-__device__ __forceinline__ void store_words(T *dst, const float (&f)[W]) {
-    if constexpr (W == 1) {
-        store_elem(dst, sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[0]);
+template <int W, bool APART, typename T>
+__device__ __forceinline__ void store_words(T *dst, int hop, int n, const float (&f)[W]) {
+    if constexpr (APART) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j < n) store_elem(dst + j * hop, sizeof(T) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, f[j]);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int j = 0; j < W / 4; ++j)
@@ -76,12 +86,12 @@ struct EmParams {
     int *err;
 };
 
-// W = 8: eight channels a piece in 16-byte accesses; W = 1: any layout of y.  U pieces a thread are
-// in flight together, and the tokens of the next ones.
-template <int W, typename T, typename Y>
+// BF16 to BF16, eight channels a piece in 16-byte accesses.  U pieces a thread are in flight together, and the
+// tokens of the next ones.
 __global__ void __launch_bounds__(EM_THREADS, EM_BLOCKS) embedding_kernel(const __grid_constant__ EmParams p) {
     griddep_launch_dependents();
-    constexpr int U = W == 8 ? 4 : 8;
+    constexpr int W = 8, U = 4;
+    using T = unsigned short;
     const long long step = (long long)gridDim.x * EM_THREADS;
     long long i = (long long)blockIdx.x * EM_THREADS + threadIdx.x;
     uint32_t row = (uint32_t)(i / p.pieces);  // (may run past the last one)
@@ -103,14 +113,14 @@ __global__ void __launch_bounds__(EM_THREADS, EM_BLOCKS) embedding_kernel(const 
     };
     next();
     while (at_row[0] >= 0) {
-        Words<W, T> v[U];
+        Words<W, false, T> v[U];
         long long at[U];
         bool there[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             there[k] = token[k] >= 0 && token[k] < p.e.V;
             at[k] = at_row[k] < 0 ? -1 : row_off(p.e.y.m, at_row[k]) + (long long)at_piece[k] * W * p.e.y.m.cs;
-            if (there[k]) v[k].load(static_cast<const T *>(p.e.table.p) + token[k] * p.e.C + (long long)at_piece[k] * W);
+            if (there[k]) v[k].load(static_cast<const T *>(p.e.table.p) + token[k] * p.e.C + (long long)at_piece[k] * W, 1, W);
             if (token[k] >= p.e.V && at_piece[k] == 0) record_error(p.err, DLC_DEVERR_INDEX, at_row[k]);
         }
         next();
@@ -120,7 +130,49 @@ __global__ void __launch_bounds__(EM_THREADS, EM_BLOCKS) embedding_kernel(const 
             float f[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) f[j] = there[k] ? v[k].at(j) * p.e.scale : 0.f;
-            store_words<W, Y>(static_cast<Y *>(p.e.y.p) + at[k], f);
+            store_words<W, false, T>(static_cast<T *>(p.e.y.p) + at[k], 1, W, f);
+        }
+    }
+}
+
+// FP32 on either side, rows that vectors do not reach, and any layout of y: a warp takes up to 256 channels of a
+// row, single ones 32 apart a lane.  16384 x 1001 BF16 14.7 us (43.8 with a place in the rows and an address
+// for each element), 16384 x 1008 FP32 14.5, in vectors of four channels 15.7, of eight 21.0.
+constexpr int EM_LANE = 8, EM_ROW_BLOCKS = 6;  // channels a lane; blocks an SM holds
+
+template <typename T, typename Y>
+__global__ void __launch_bounds__(EM_THREADS, EM_ROW_BLOCKS) embedding_rows_kernel(const __grid_constant__ EmParams p) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (EM_THREADS / 32);
+    long long i = (long long)blockIdx.x * (EM_THREADS / 32) + (threadIdx.x >> 5);
+    long long row = i / p.pieces;
+    int piece = (int)(i - row * p.pieces);
+    const long long drow = step / p.pieces;
+    const int dpiece = (int)(step - drow * p.pieces);
+    griddep_wait();
+    long long token = i < p.items ? token_at(p.e.tokens, row) : -1;
+    while (i < p.items) {
+        const int c = piece * 32 * EM_LANE + lane;
+        const bool there = token >= 0 && token < p.e.V;
+        const T *src = static_cast<const T *>(p.e.table.p) + token * p.e.C + c;
+        Y *dst = static_cast<Y *>(p.e.y.p) + row_off(p.e.y.m, row) + c * p.e.y.m.cs;
+        T v[EM_LANE];
+#pragma unroll
+        for (int j = 0; j < EM_LANE; ++j) v[j] = there && c + 32 * j < p.e.C ? src[32 * j] : (T)0;
+        if (token >= p.e.V && c == 0) record_error(p.err, DLC_DEVERR_INDEX, (int)row);
+        i += step, row += drow, piece += dpiece;
+        if (piece >= p.pieces) piece -= p.pieces, ++row;
+        if (i < p.items) token = token_at(p.e.tokens, row);
+#pragma unroll
+        for (int j = 0; j < EM_LANE; ++j) {
+            if (c + 32 * j >= p.e.C) break;
+            float f;
+            if constexpr (sizeof(T) == 2)
+                f = bf16_bits_f32(v[j]);
+            else
+                f = v[j];
+            store_elem(dst + 32 * j * p.e.y.m.cs, sizeof(Y) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT, 0, there ? f * p.e.scale : 0.f);
         }
     }
 }
@@ -135,9 +187,11 @@ __global__ void __launch_bounds__(EM_THREADS, EM_BLOCKS) embedding_kernel(const 
 constexpr int SORT_MAX_BITS = 10, SORT_MAX_DIGITS = 1 << SORT_MAX_BITS;
 
 constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32, SORT_EACH = 4, SORT_TILE = SORT_THREADS * SORT_EACH;
-// Lists of up to RANK_MOST tokens are ranked by counting (8192 x 256 into 1003 rows: 33 us, by digits 18; up to
-// 2048 tokens as fast or faster, in one launch).
-constexpr int RANK_MOST = 4096, RANK_THREADS = 256;
+// Short lists are ranked by counting, in one launch: up to 4096 tokens where a digit would do for sorting them (300
+// channels into 1003 rows: 4000 tokens 12.9 us, by digits 16.9; 5000 tokens 16.4 and 16.0; 8000 21.7 and 16.8), up
+// to RANK_MOST where it takes two (64 channels into 131072 rows: 5000 tokens 19.0 us, 24.8 by digits; 8000 27.9
+// and 25.6).
+constexpr int RANK_ONE = 4096, RANK_MOST = 6144, RANK_THREADS = 256;
 constexpr int SORT_OWN_SUMS = 64;  // tiles
 
 struct SortParams {
@@ -423,12 +477,14 @@ struct SumParams {
     const uint32_t *key, *row; // sorted
     float *part;               // [chunk][2][C]: of the token that comes in, of the one that goes on
     int chunk, chunks, slabs;  // sorted positions of a chunk
+    int ranked;
 };
 
-// W = 8, 4: aligned vectors of dy and of the table; W = 1: any layout of dy, any size.  ACC: the sums
+// W = 8, 4: aligned vectors of dy and of the table; APART: any layout of dy, any size, a thread's channels a
+// block's threads apart (16384 x 1001 BF16 into 30000 rows 45 us in all, 61 with one channel a thread).  ACC: the sums
 // are added to the table's rows, which are loaded beside the rows of dy that end a token (one by
 // one, where they are needed, 32 tokens took 32 memory latencies).
-template <int W, typename D, typename T, bool ACC>
+template <int W, bool APART, typename D, typename T, bool ACC>
 __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid_constant__ SumParams p) {
     griddep_launch_dependents();
     __shared__ uint32_t key_s[SUM_MAX_CHUNK + 2], row_s[SUM_MAX_CHUNK];
@@ -446,26 +502,27 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
         key_s[1 + n] = first + n < p.e.rows ? p.key[first + n] : 0xffffffffu;
     }
     __syncthreads();
-    const int c = (slab * (int)blockDim.x + (int)threadIdx.x) * W;
+    const int hop = APART ? (int)blockDim.x : 1, c = slab * (int)blockDim.x * W + (int)threadIdx.x * (APART ? 1 : W);
     if (c >= C) return;
-    const long long co = c * p.e.y.m.cs;
+    const int there = (C - c - 1) / hop + 1;  // channels of this thread, if not W
+    const long long co = c * p.e.y.m.cs, far = hop * p.e.y.m.cs;
     const uint32_t comes = key_s[0];  // the token that began in the chunk before, if it is the first here
     float acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) acc[j] = 0.f;
-    constexpr int U = W * sizeof(D) > 16 || (ACC && W * sizeof(T) > 16) ? 4 : 8;  // rows in flight
+    constexpr int U = W * sizeof(D) > 16 || (ACC && (APART || W * sizeof(T) > 16)) ? 4 : 8;  // rows in flight
     for (int i0 = 0; i0 < n; i0 += U) {
-        Words<W, D> v[U];
-        Words<W, T> old[ACC ? U : 1];
+        Words<W, APART, D> v[U];
+        Words<W, APART, T> old[ACC ? U : 1];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int i = i0 + k;
             if (i >= n) continue;
             const uint32_t token = key_s[1 + i];
             if (token >= (uint32_t)p.e.V) continue;
-            v[k].load(static_cast<const D *>(p.e.y.p) + row_off(p.e.y.m, row_s[i]) + co);
+            v[k].load(static_cast<const D *>(p.e.y.p) + row_off(p.e.y.m, row_s[i]) + co, far, there);
             if constexpr (ACC)
-                if (key_s[2 + i] != token && token != comes) old[k].load(static_cast<const T *>(p.e.table.p) + (long long)token * C + c);
+                if (key_s[2 + i] != token && token != comes) old[k].load(static_cast<const T *>(p.e.table.p) + (long long)token * C + c, hop, there);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -484,9 +541,9 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
                     f[j] = acc[j] * p.e.scale;
                     if constexpr (ACC) f[j] += old[k].at(j);
                 }
-                store_words<W, T>(static_cast<T *>(p.e.table.p) + (long long)token * C + c, f);
+                store_words<W, APART, T>(static_cast<T *>(p.e.table.p) + (long long)token * C + c, hop, there, f);
             } else {
-                store_words<W, float>(p.part + ((long long)chunk * 2 + (token == comes ? 0 : 1)) * C + c, acc);
+                store_words<W, APART, float>(p.part + ((long long)chunk * 2 + (token == comes ? 0 : 1)) * C + c, hop, there, acc);
             }
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[j] = 0.f;
@@ -496,9 +553,11 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const __grid
 
 // Tokens whose rows reach over several chunks: the block of the chunk where they begin adds up the
 // partial sums, a range of them by each of its groups of `width` threads, always in the same order.
-template <int W, typename T, bool ACC>
+template <int W, bool APART, typename T, bool ACC>
 __global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const __grid_constant__ SumParams p, int width) {
-    griddep_launch_dependents();
+    // (Among the waiting blocks of this kernel the ranking ones of a next call would be dealt to a few SMs only:
+    // 4000 x 300, call after call, 27 us instead of 12.9.  Sorting by digits it gains 3 us to let the next call begin.)
+    if (!p.ranked) griddep_launch_dependents();
     __shared__ float sum_s[JOIN_THREADS * W];
     griddep_wait();
     const int chunk = (int)blockIdx.x / p.slabs, slab = (int)blockIdx.x - chunk * p.slabs;
@@ -514,23 +573,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const __gr
         if (found < (int)blockDim.x) break;
     }
     const int groups = (int)blockDim.x / width, group = (int)threadIdx.x / width, t = (int)threadIdx.x - group * width;
-    const int c = (slab * width + t) * W;
+    const int hop = APART ? width : 1, c = slab * width * W + t * (APART ? 1 : W), there = (p.e.C - c - 1) / hop + 1;
     const bool on = c < p.e.C;
     T *dst = static_cast<T *>(p.e.table.p) + (long long)token * p.e.C + c;
-    Words<W, T> old;
+    Words<W, APART, T> old;
     if constexpr (ACC)
-        if (on && group == 0) old.load(dst);
+        if (on && group == 0) old.load(dst, hop, there);
     float acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) acc[j] = 0.f;
     // parts 0 (this chunk's second slot) and 1 .. more (the next ones' first slots)
     const int k1 = (int)((long long)(more + 1) * (group + 1) / groups);
-    constexpr int U = W == 8 ? 4 : 8;
+    constexpr int U = W == 8 || APART ? 4 : 8;
     for (int k0 = (int)((long long)(more + 1) * group / groups); on && k0 < k1; k0 += U) {
-        Words<W, float> part[U];
+        Words<W, APART, float> part[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (k0 + k < k1) part[k].load(p.part + ((long long)(chunk + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * p.e.C + c);
+            if (k0 + k < k1) part[k].load(p.part + ((long long)(chunk + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * p.e.C + c, hop, there);
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (k0 + k < k1) {
@@ -554,35 +613,35 @@ __global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const __gr
         acc[j] *= p.e.scale;
         if constexpr (ACC) acc[j] += old.at(j);
     }
-    store_words<W, T>(dst, acc);
+    store_words<W, APART, T>(dst, hop, there, acc);
 }
 
 // ---- host side -----------------------------------------------------------------------
 
 using Half = unsigned short;
 
-template <int W, typename T>
-const void *fwd_kernel(int y) {
-    return y == DLC_DATA_BFLOAT16 ? (const void *)embedding_kernel<W, T, Half> : (const void *)embedding_kernel<W, T, float>;
+template <typename T>
+const void *rows_kernel(int y) {
+    return y == DLC_DATA_BFLOAT16 ? (const void *)embedding_rows_kernel<T, Half> : (const void *)embedding_rows_kernel<T, float>;
 }
 
-template <int W, typename D>
+template <int W, bool APART, typename D>
 const void *sum_kernel(int t, bool acc) {
     if (t == DLC_DATA_BFLOAT16)
-        return acc ? (const void *)embedding_sum_kernel<W, D, Half, true> : (const void *)embedding_sum_kernel<W, D, Half, false>;
-    return acc ? (const void *)embedding_sum_kernel<W, D, float, true> : (const void *)embedding_sum_kernel<W, D, float, false>;
+        return acc ? (const void *)embedding_sum_kernel<W, APART, D, Half, true> : (const void *)embedding_sum_kernel<W, APART, D, Half, false>;
+    return acc ? (const void *)embedding_sum_kernel<W, APART, D, float, true> : (const void *)embedding_sum_kernel<W, APART, D, float, false>;
 }
 
-template <int W>
+template <int W, bool APART>
 const void *sum_kernel(const EmbeddingProblem &e) {
-    return e.y.dt == DLC_DATA_BFLOAT16 ? sum_kernel<W, Half>(e.table.dt, e.accumulate) : sum_kernel<W, float>(e.table.dt, e.accumulate);
+    return e.y.dt == DLC_DATA_BFLOAT16 ? sum_kernel<W, APART, Half>(e.table.dt, e.accumulate) : sum_kernel<W, APART, float>(e.table.dt, e.accumulate);
 }
 
-template <int W>
+template <int W, bool APART>
 const void *join_kernel(const EmbeddingProblem &e) {
     if (e.table.dt == DLC_DATA_BFLOAT16)
-        return e.accumulate ? (const void *)embedding_join_kernel<W, Half, true> : (const void *)embedding_join_kernel<W, Half, false>;
-    return e.accumulate ? (const void *)embedding_join_kernel<W, float, true> : (const void *)embedding_join_kernel<W, float, false>;
+        return e.accumulate ? (const void *)embedding_join_kernel<W, APART, Half, true> : (const void *)embedding_join_kernel<W, APART, Half, false>;
+    return e.accumulate ? (const void *)embedding_join_kernel<W, APART, float, true> : (const void *)embedding_join_kernel<W, APART, float, false>;
 }
 
 // Whether rows of the table and of y are whole vectors of w elements of either.
@@ -595,6 +654,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct BwdPlan {
     int bits, passes, tiles, chunk, chunks;
+    bool ranked;
     size_t hist, key[2], row[2], part, bytes;
 };
 
@@ -605,7 +665,8 @@ BwdPlan plan_bwd(long long rows, int C, int V) {
     b.passes = (bits + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
     b.bits = (bits + b.passes - 1) / b.passes;
     b.tiles = (int)((rows + SORT_TILE - 1) / SORT_TILE);
-    if (rows <= RANK_MOST) b.passes = 1;
+    b.ranked = rows <= (b.passes == 1 ? RANK_ONE : RANK_MOST);
+    if (b.ranked) b.passes = 1;
     // Positions of a chunk: few where that gives the GPU enough to do at once, and where there are
     // more than enough many, so that a frequent token leaves fewer partial sums.
     const long long warps = rows * ((C + 255) / 256);
@@ -630,13 +691,12 @@ dlcStatus_t dlc_launch_embedding(dlcContext *ctx, const EmbeddingProblem &e) {
     EmParams p;
     p.e = e;
     p.err = ctx->d_err;
-    const bool w8 = vectors(e, 8);
-    p.pieces = w8 ? e.C / 8 : e.C;
+    const bool bf = e.table.dt == DLC_DATA_BFLOAT16, whole = bf && e.y.dt == DLC_DATA_BFLOAT16 && vectors(e, 8);
+    p.pieces = whole ? e.C / 8 : (e.C + 32 * EM_LANE - 1) / (32 * EM_LANE);
     p.items = e.rows * p.pieces;
-    const bool bf = e.table.dt == DLC_DATA_BFLOAT16;
-    const void *kern = w8 ? (bf ? fwd_kernel<8, Half>(e.y.dt) : fwd_kernel<8, float>(e.y.dt))
-                          : (bf ? fwd_kernel<1, Half>(e.y.dt) : fwd_kernel<1, float>(e.y.dt));
-    const long long blocks = std::min<long long>((p.items + EM_THREADS - 1) / EM_THREADS, (long long)ctx->sm_count * EM_BLOCKS);
+    const void *kern = whole ? (const void *)embedding_kernel : bf ? rows_kernel<Half>(e.y.dt) : rows_kernel<float>(e.y.dt);
+    const int each = whole ? EM_THREADS : EM_THREADS / 32;  // pieces that a block takes at once
+    const long long blocks = std::min<long long>((p.items + each - 1) / each, (long long)ctx->sm_count * (whole ? EM_BLOCKS : EM_ROW_BLOCKS));
     void *args[] = {&p};
     return dlc_launch(ctx, kern, dim3((unsigned)blocks), dim3(EM_THREADS), 0, args);
 }
@@ -666,16 +726,17 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     p.part = reinterpret_cast<float *>(e.ws + b.part);
     p.chunk = b.chunk;
     p.chunks = b.chunks;
-    const int w = vectors(e, 8) ? 8 : vectors(e, 4) ? 4 : 1;
-    const int threads = std::min(SUM_THREADS, ((e.C + w - 1) / w + 31) / 32 * 32);
+    p.ranked = b.ranked;
+    const bool apart = !vectors(e, 4);
+    const int w = !apart && vectors(e, 8) ? 8 : 4;
+    const int threads = std::min(SUM_THREADS, (apart ? e.C + 31 : (e.C + w - 1) / w + 31) / 32 * 32);
     p.slabs = (e.C + threads * w - 1) / (threads * w);
     if ((long long)p.chunks * p.slabs > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     // the table's whole 16-byte words, dealt evenly to the sort's launches
     const size_t bytes = e.accumulate ? 0 : (size_t)e.V * e.C * dlc_dtype_bytes((dlcDataType_t)e.table.dt);
     char *table = static_cast<char *>(e.table.p);
     const size_t head = std::min(bytes, (16 - (uintptr_t)table % 16) % 16), words = (bytes - head) / 16;
-    const bool ranked = e.rows <= RANK_MOST;
-    const int launches = ranked ? 1 : 1 + b.passes;
+    const int launches = b.ranked ? 1 : 1 + b.passes;
     auto part = [&](int i) {
         const size_t w0 = words * i / launches, w1 = words * (i + 1) / launches;
         s.fill = table + head + 16 * w0;
@@ -688,7 +749,7 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
     };
     dlcStatus_t st;
     void *args[] = {&s};
-    if (ranked) {
+    if (b.ranked) {
         s.blocks = (int)((e.rows + 31) / 32);
         st = dlc_launch(ctx, (const void *)rank_kernel, dim3((unsigned)s.blocks + 2 * part(0)), dim3(RANK_THREADS), 0, args);
         if (st != DLC_STATUS_SUCCESS) return st;
@@ -708,10 +769,10 @@ dlcStatus_t dlc_launch_embedding_bwd(dlcContext *ctx, const EmbeddingProblem &e)
         if (st != DLC_STATUS_SUCCESS) return st;
     }
     void *sargs[] = {&p};
-    const void *sum = w == 8 ? sum_kernel<8>(e) : w == 4 ? sum_kernel<4>(e) : sum_kernel<1>(e);
+    const void *sum = w == 8 ? sum_kernel<8, false>(e) : apart ? sum_kernel<4, true>(e) : sum_kernel<4, false>(e);
     st = dlc_launch(ctx, sum, dim3((unsigned)(p.chunks * p.slabs)), dim3((unsigned)threads), 0, sargs);
     if (st != DLC_STATUS_SUCCESS || p.chunks == 1) return st;
-    const void *join = w == 8 ? join_kernel<8>(e) : w == 4 ? join_kernel<4>(e) : join_kernel<1>(e);
+    const void *join = w == 8 ? join_kernel<8, false>(e) : apart ? join_kernel<4, true>(e) : join_kernel<4, false>(e);
     int width = threads;
     void *jargs[] = {&p, &width};
     return dlc_launch(ctx, join, dim3((unsigned)((p.chunks - 1) * p.slabs)), dim3((unsigned)(JOIN_THREADS / width * width)), 0, jargs);
