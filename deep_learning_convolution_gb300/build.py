@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libdlc.so")
 
 SOURCES = ["api.cu", "conv_ffma.cu", "conv_tc.cu", "conv_window.cu", "conv_pair.cu", "conv_bwd.cu",
            "conv_wgrad.cu", "pool_act.cu", "conv_rowstack.cu", "channel_api.cu", "rmsnorm.cu",
-           "act_grad.cu", "gemm.cu", "gemm_rows.cu", "gemv.cu", "channel_train_api.cu", "layernorm.cu", "layernorm_vec.cu",
+           "act_grad.cu", "gemm.cu", "gemm_rows.cu", "gemv.cu", "channel_train_api.cu", "layernorm.cu", "layernorm_vec.cu", "layernorm_shift.cu",
            "dropout.cu", "embedding.cu", "cross_entropy.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

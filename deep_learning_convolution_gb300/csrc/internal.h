@@ -395,9 +395,11 @@ dlcStatus_t dlc_launch_column_sums(dlcContext *ctx, const float *ws, float *out,
 dlcStatus_t dlc_launch_layer(dlcContext *ctx, const LayerProblem &p);
 size_t dlc_layer_bwd_workspace(const dlcContext *ctx, long long rows, int C);
 dlcStatus_t dlc_launch_layer_bwd(dlcContext *ctx, const LayerBwdProblem &p);
-// layernorm_vec.cu: false where the layout is not its
+// layernorm_vec.cu, layernorm_shift.cu: false where the layout is not theirs
 bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &p, dlcStatus_t &status);
 bool dlc_layer_bwd_vec(dlcContext *ctx, const LayerBwdProblem &p, dlcStatus_t &status);
+bool dlc_layer_shift(dlcContext *ctx, const LayerProblem &p, dlcStatus_t &status);
+bool dlc_layer_bwd_shift(dlcContext *ctx, const LayerBwdProblem &p, dlcStatus_t &status);
 // dropout.cu
 dlcStatus_t dlc_launch_dropout(dlcContext *ctx, const DropoutProblem &p);
 // embedding.cu

@@ -9,11 +9,11 @@
 //
 // The squares are summed about the row's own mean, in a second reduction over registers: the
 // difference of the mean square and the squared mean would lose what a large mean (or
-// one large channel) leaves of the small ones.  Rows in the usual layout are
-// layernorm_vec.cu's; here are the others: unaligned rows and mixed types with the rows' way
-// through registers that the RMS norm has (rmsnorm.cu), channels apart and long rows read again
-// for each step.  Instructions and latency bound them, measured back to back: 16384 x 1001 BF16
-// with residual and sum 50 us (2.6 TB/s), backward 53 us (2.5 TB/s); an FP32 stream beside BF16
+// one large channel) leaves of the small ones.  Rows in the usual layouts are
+// layernorm_vec.cu's and layernorm_shift.cu's; here are the others: mixed types, and unaligned rows where that is
+// faster, with the rows' way through registers that the RMS norm has (rmsnorm.cu), channels apart and long rows
+// read again for each step.  Instructions and latency bound them, measured back to back: 16384 x 1001 FP32
+// unaligned with residual and sum 45 us (5.8 TB/s), backward 56 us; an FP32 stream beside BF16
 // branches, 100352 x 512, 138 us, backward 228 us; channels apart, 128 images of 512 x 28 x 28 BF16, 265
 // us, backward 632 us; 2730 x 12288 FP32 223 us, backward 396 us.
 #include "norm_rows.cuh"
@@ -411,7 +411,7 @@ RowKernel row_kernel(const RowPlan &r, int C, std::initializer_list<RowTensor> t
 dlcStatus_t dlc_launch_layer(dlcContext *ctx, const LayerProblem &pb) {
     LayerProblem p = pb;
     dlcStatus_t done;
-    if (dlc_layer_vec(ctx, p, done)) return done;
+    if (dlc_layer_vec(ctx, p, done) || dlc_layer_shift(ctx, p, done)) return done;
     RowPlan r = plan_rows(p.rows, p.C, contiguous(p.x) && contiguous(p.r) && contiguous(p.t) && contiguous(p.y),
                           vec_ok(p.x) && vec_ok(p.r) && vec_ok(p.t) && vec_ok(p.y), ring({p.x, p.r}), LN_FWD_BLOCKS, ctx->sm_count);
     RowKernel k = row_kernel<false>(r, p.C, {p.x, p.r});
@@ -427,13 +427,13 @@ dlcStatus_t dlc_launch_layer(dlcContext *ctx, const LayerProblem &pb) {
 
 size_t dlc_layer_bwd_workspace(const dlcContext *ctx, long long rows, int C) {
     // the most blocks of any layout's plan, so that the pointers' alignment does not matter
-    return (size_t)std::min(rows, (long long)ctx->sm_count * 4) * 2 * C * sizeof(float);
+    return (size_t)std::min((rows + 7) / 8 * 8, (long long)ctx->sm_count * 4) * 2 * C * sizeof(float);
 }
 
 dlcStatus_t dlc_launch_layer_bwd(dlcContext *ctx, const LayerBwdProblem &pb) {
     LayerBwdProblem p = pb;
     dlcStatus_t done;
-    if (dlc_layer_bwd_vec(ctx, p, done)) return done;
+    if (dlc_layer_bwd_vec(ctx, p, done) || dlc_layer_bwd_shift(ctx, p, done)) return done;
     RowPlan r = plan_rows(p.rows, p.C, contiguous(p.dy) && contiguous(p.t) && contiguous(p.dt) && contiguous(p.dx),
                           vec_ok(p.dy) && vec_ok(p.t) && vec_ok(p.dt) && vec_ok(p.dx), ring({p.dy, p.t, p.dt}), LN_BWD_BLOCKS,
                           ctx->sm_count);

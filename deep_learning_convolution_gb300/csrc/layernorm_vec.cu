@@ -1,492 +1,7 @@
-// layernorm_vec.cu -- layer norm (layernorm.cu) of rows in the usual layout: channels contiguous, every
-// tensor's rows at one pitch of whole 16-byte pieces, all inputs (and total) of one type.
-//
-// Each input is read once and each output written once, and that should bound the kernels; with the
-// general ones the instructions do (65536 x 768 BF16 to E4M3: 1278 warp instructions a row and
-// 100 us in layer_rows_kernel), and then the barriers between a row's warps.  So a row takes as few
-// threads as hold it, up to eight vectors of 16 bytes each (2048 channels: one warp), gamma and beta
-// wait in shared memory, and only a thread's last vector can be partial or missing.  FP32 rows have
-// vectors of four channels: with eight, neighbouring threads touched every other 16 bytes (8192 x 2048
-// FP32 67 us, 48 this way).
-//
-// Measured back to back, with residual and sum: 65536 x 768 BF16 to E4M3 60.3 us (5.8 TB/s), 16384 x
-// 2048 BF16 48.8 us (5.5), 8192 x 2048 FP32 48 us (5.6); backward with both sums 16384 x 2048 BF16 49.3
-// us (5.4), 8192 x 2048 FP32 50 us (5.4).  A call's start and end are 7 to 10 us of it: rows beyond these
-// come at 6.4 TB/s.
-#include "norm_rows.cuh"
+// layernorm_vec.cu -- the layer norm's kernels for rows of whole 16-byte pieces (layernorm_vec.cuh).
+#include "layernorm_vec.cuh"
 
 namespace {
-
-using namespace dlc;
-
-// Sum over the `tpr` threads of a row (a power of two or whole warps), as row_reduce has it; the
-// usual numbers of warps without a loop, whose branches would count.
-template <int N, int WARPS>
-__device__ __forceinline__ void join_warps(float (&a)[N], const float *row) {
-    float4 q[WARPS * N / 4 > 0 ? WARPS * N / 4 : 1];
-    if constexpr (WARPS * N >= 4) {
-#pragma unroll
-        for (int i = 0; i < WARPS * N / 4; ++i) q[i] = reinterpret_cast<const float4 *>(row)[i];
-    } else {
-        q[0] = make_float4(row[0], row[1], 0.f, 0.f);
-    }
-    const float *f = reinterpret_cast<const float *>(q);
-#pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = f[i];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) a[i] += f[w * N + i];
-}
-
-template <int N>
-__device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float (*buf)[NORM_MAX_WARPS * 2], int parity) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        if (o < 8 || o < tpr) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
-        }
-    }
-    if (tpr > 32) {
-        const int warps = tpr >> 5;
-        float *mine = buf[parity] + N * ((int)threadIdx.x >> 5);
-        if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) mine[i] = a[i];
-        }
-        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
-        const float *row = buf[parity] + N * slot * warps;
-        if (warps == 2) {
-            join_warps<N, 2>(a, row);
-        } else if (warps == 4) {
-            join_warps<N, 4>(a, row);
-        } else if (warps == 8) {
-            join_warps<N, 8>(a, row);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) a[i] = row[i];
-            for (int w = 1; w < warps; ++w) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) a[i] += row[w * N + i];
-            }
-        }
-    }
-}
-
-// Largest |v| over a row's threads (NaN or not: such a row is NaN anyway).
-__device__ __forceinline__ float row_most(float v, int tpr, int slot, float (*buf)[NORM_MAX_WARPS * 2], int parity) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-        if (o < 8 || o < tpr) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (tpr > 32) {
-        const int warps = tpr >> 5;
-        if ((threadIdx.x & 31) == 0) buf[parity][threadIdx.x >> 5] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
-        const float *row = buf[parity] + slot * warps;
-        v = fmaxf(row[0], row[1]);
-        for (int w = 2; w < warps; ++w) v = fmaxf(v, row[w]);
-    }
-    return v;
-}
-
-constexpr int VEC_THREADS = 256;  // of a block, or a little less (backward, long rows: TH)
-
-// Channels of a vector: 16 bytes, so that neighbouring threads copy neighbouring words.
-template <typename E>
-constexpr int vec_ch() { return 16 / (int)sizeof(E); }
-
-// A ring of S rows of T tensors in shared memory, V vectors a thread, of which a thread
-// reads back only what it copied itself: no barrier, and a row's place takes the row S further
-// on as soon as it has been read.  (Strides are constants: with the block's size for one, the
-// addresses' instructions cost 7 %.)
-template <int V, typename E, int T, int S, int TH>
-struct VecRing {
-    static constexpr uint32_t WORDS = (uint32_t)(T * V), WORD = 16u * TH;
-    uint32_t base, row;
-    __device__ __forceinline__ explicit VecRing(uint32_t smem) : base(smem + threadIdx.x * 16u), row(0) {}
-    // at: this thread's first vector; hop: bytes to the next one; last: channels of the last one that
-    // exist (what is behind them becomes zero)
-    __device__ __forceinline__ void fetch(int k, const char *at, uint32_t hop, int last) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            cp_async_16(base + (row + (uint32_t)(k * V + j)) * WORD, at + (j + 1 < V || last > 0 ? j * hop : 0u),
-                        j + 1 < V ? 16u : (uint32_t)last * (uint32_t)sizeof(E));
-    }
-    __device__ __forceinline__ void next() {  // (ends the copies of a row)
-        cp_async_commit();
-        row = S == 1 || row == WORDS * (S - 1) ? 0u : row + WORDS;
-    }
-    __device__ __forceinline__ void read_vector(int k, int j, float *f) const {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(base + (row + (uint32_t)(k * V + j)) * WORD)
-                     : "memory");
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(E) == 2)
-                set2(f, i, unpack_bf16(w[i]));
-            else
-                f[i] = __uint_as_float(w[i]);
-        }
-    }
-    __device__ __forceinline__ void read(int k, float (&f)[V * vec_ch<E>()]) const {
-#pragma unroll
-        for (int j = 0; j < V; ++j) read_vector(k, j, f + j * vec_ch<E>());
-    }
-    static constexpr size_t SMEM = (size_t)S * WORDS * WORD;
-};
-
-// A vector of a channel-wise FP32 array from shared memory: its quarters of four channels lie apart,
-// so that neighbouring threads read neighbouring words.
-template <int CH>
-__device__ __forceinline__ void vec_param(uint32_t at, uint32_t apart, float (&g)[CH]) {
-#pragma unroll
-    for (int h = 0; h < CH / 4; ++h) {
-        const float4 a = ld_shared_f32x4(at + (uint32_t)h * apart);
-        g[4 * h] = a.x, g[4 * h + 1] = a.y, g[4 * h + 2] = a.z, g[4 * h + 3] = a.w;
-    }
-}
-
-// Fills vec_param's arrays, whose vectors are dealt to `tpr` threads; zeros behind the row.  (By
-// asynchronous copies ahead of the rows' a call of 65536 x 768 took 4 us more, element by element
-// one of 16384 x 2048 5 us.)
-template <int CH>
-__device__ __forceinline__ void vec_param_fill(float *dst, const float *src, int C, int tpr, int V) {
-    constexpr int H = CH / 4;
-    const bool aligned = ((uintptr_t)src & 15u) == 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < H * tpr * V; i += blockDim.x) {
-        const int vec = i / H, at = (vec / tpr * H + i % H) * tpr + vec % tpr;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src && aligned && 4 * i + 4 <= C) {
-            v = reinterpret_cast<const float4 *>(src)[i];
-        } else if (src && 4 * i < C) {
-            v.x = src[4 * i];
-            if (4 * i + 1 < C) v.y = src[4 * i + 1];
-            if (4 * i + 2 < C) v.z = src[4 * i + 2];
-            if (4 * i + 3 < C) v.w = src[4 * i + 3];
-        }
-        reinterpret_cast<float4 *>(dst)[at] = v;
-    }
-}
-
-// A vector of CH values as Y.
-template <typename Y, int CH>
-__device__ __forceinline__ void vec_store(char *at, const float *v) {
-    if constexpr (sizeof(Y) == 4) {
-#pragma unroll
-        for (int i = 0; i < CH / 4; ++i) reinterpret_cast<float4 *>(at)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint32_t w[CH * sizeof(Y) / 4];
-        if constexpr (sizeof(Y) == 2) {
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < CH / 4; ++i) w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | (pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16);
-        }
-        if constexpr (sizeof(w) == 16)
-            *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (sizeof(w) == 8)
-            *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t *>(at) = w[0];
-    }
-}
-
-// The last vector: whole, or the `n` channels of it that exist.
-template <typename Y, int CH>
-__device__ __forceinline__ void vec_store_last(char *at, const float *v, int n) {
-    if (n == CH) {
-        vec_store<Y, CH>(at, v);
-    } else if (n > 0) {
-#pragma unroll
-        for (int i = 0; i < CH - 1; ++i)
-            if (i < n) store_elem(at, sizeof(Y) == 4 ? DLC_DATA_FLOAT : sizeof(Y) == 2 ? DLC_DATA_BFLOAT16 : DLC_DATA_FLOAT8_E4M3, i, v[i]);
-    }
-}
-
-// Blocks an SM holds, by the registers of V vectors a thread; rows of the rings.
-template <int V, typename E>
-constexpr int vec_blocks() { return V * vec_ch<E>() <= 16 ? 4 : V * vec_ch<E>() <= 32 ? 3 : 2; }
-template <int V>
-constexpr int vec_ring() { return V <= 2 ? 2 : 1; }
-template <int V>
-constexpr int vec_bwd_ring() { return V <= 2 ? 3 : 2; }
-
-struct VecRow {  // this thread's part of a tensor's rows
-    char *p;
-    long long inc;
-    __device__ __forceinline__ VecRow(const RowTensor &t, int e, long long row, long long step, int channel)
-        : p(static_cast<char *>(t.p) + (row * t.m.ld + channel) * e), inc(step * t.m.ld * e) {}
-};
-
-// E: storage of x, r and t; Y: of y.
-template <int V, typename E, typename Y, bool RES>
-__global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_kernel(const __grid_constant__ LayerProblem p, int tpr) {
-    griddep_launch_dependents();
-    __shared__ __align__(16) float buf[2][NORM_MAX_WARPS * 2];
-    extern __shared__ uint4 ring_s[];
-    constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_ring<V>();
-    const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
-    const long long step = (long long)gridDim.x * rpb;
-    const int last = min(max(p.C - ((V - 1) * tpr + t) * CH, 0), CH);
-    const int c = V > 1 || last > 0 ? CH * t : 0;
-    const uint32_t hop = (uint32_t)(CH * tpr), apart = 16u * (uint32_t)tpr;
-    const float inv_c = 1.f / (float)p.C;
-    using Ring = VecRing<V, E, RES ? 2 : 1, S, VEC_THREADS>;
-    Ring ring(smem_u32(ring_s));
-    float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM), *beta = gamma + N * tpr;
-    const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t, b0 = smem_u32(beta) + 16u * (uint32_t)t;
-    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    VecRow x(p.x, sizeof(E), row, step, c), r(p.r, sizeof(E), row, step, c), tt(p.t, sizeof(E), row, step, c), y(p.y, sizeof(Y), row, step, c);
-    griddep_wait();
-    auto fetch = [&]() {
-        if (ahead < p.rows) {
-            ring.fetch(0, x.p, 16u * (uint32_t)tpr, last);
-            if (RES) ring.fetch(1, r.p, 16u * (uint32_t)tpr, last);
-        }
-        ring.next();
-        ahead += step;
-        x.p += x.inc;
-        r.p += r.inc;
-    };
-    for (int i = 0; i < S; ++i) fetch();
-    vec_param_fill<CH>(gamma, p.gamma, p.C, tpr, V);
-    vec_param_fill<CH>(beta, p.beta, p.C, tpr, V);
-    __syncthreads();
-    int parity = 0;
-    for (; row - slot < p.rows; row += step) {  // (as many rounds for every thread of the block)
-        const bool on = row < p.rows;
-        float v[N];
-        cp_async_wait<S - 1>();
-        ring.read(0, v);
-        if (RES) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float w[CH];
-                ring.read_vector(1, j, w);
-#pragma unroll
-                for (int i = 0; i < CH / 2; ++i) set2(v + CH * j, i, add2(get2(v + CH * j, i), get2(w, i)));
-            }
-        }
-        if (p.t.p && on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j + 1 < V)
-                    vec_store<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j);
-                else
-                    vec_store_last<E, CH>(tt.p + j * (16u * (uint32_t)tpr), v + CH * j, last);
-        }
-        tt.p += tt.inc;
-        fetch();
-        float2 sum = make_float2(0.f, 0.f), sq = sum;
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) sum = add2(get2(v, i), sum);
-        float total[1] = {sum.x + sum.y};
-        row_sums<1>(total, tpr, slot, buf, parity);
-        parity ^= 1;
-        const float2 mean = pair_of(-total[0] * inv_c);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
-        if (last == 0) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) v[CH * (V - 1) + i] = 0.f;
-        } else if (last < CH) {
-#pragma unroll
-            for (int i = 1; i < CH; ++i)
-                if (i >= last) v[CH * (V - 1) + i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
-        total[0] = sq.x + sq.y;
-        row_sums<1>(total, tpr, slot, buf, parity);
-        parity ^= 1;
-        const float2 rho = pair_of(rsqrtf(total[0] * inv_c + p.eps));
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float g[CH], b[CH];
-            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * apart, apart, g);
-            vec_param<CH>(b0 + (uint32_t)(j * (CH / 4)) * apart, apart, b);
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) set2(v + CH * j, i, fma2(mul2(get2(v + CH * j, i), rho), get2(g, i), get2(b, i)));
-        }
-        if constexpr (sizeof(Y) == 1) {
-            float most[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < N; ++i) most[i & 1] = fmaxf(most[i & 1], fabsf(v[i]));
-            const float scale = fmaxf(row_most(fmaxf(most[0], most[1]), tpr, slot, buf, parity), SCALE_FLOOR) / E4M3_MAX;
-            parity ^= 1;
-            if (t == 0 && on) p.scale[row] = scale;
-            const float2 inv = pair_of(1.f / scale);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) set2(v, i, mul2(get2(v, i), inv));
-        }
-        if (on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j + 1 < V)
-                    vec_store<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j);
-                else
-                    vec_store_last<Y, CH>(y.p + j * (hop * (uint32_t)sizeof(Y)), v + CH * j, last);
-        }
-        y.p += y.inc;
-    }
-}
-
-// The same for the backward pass.  128 registers a thread: 16 warps an SM.
-template <int V, typename E, bool RES, int TH>
-__global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __grid_constant__ LayerBwdProblem p, int tpr) {
-    griddep_launch_dependents();
-    __shared__ __align__(16) float buf[2][NORM_MAX_WARPS * 2];
-    extern __shared__ uint4 ring_s[];
-    constexpr int CH = vec_ch<E>(), N = CH * V, S = vec_bwd_ring<V>();
-    const int rpb = (int)blockDim.x / tpr, slot = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
-    const long long step = (long long)gridDim.x * rpb;
-    const int last = min(max(p.C - ((V - 1) * tpr + t) * CH, 0), CH);
-    const int c = V > 1 || last > 0 ? CH * t : 0;
-    const uint32_t hop = 16u * (uint32_t)tpr;
-    const float inv_c = 1.f / (float)p.C;
-    using Ring = VecRing<V, E, RES ? 3 : 2, S, TH>;
-    Ring ring(smem_u32(ring_s));
-    float *gamma = reinterpret_cast<float *>(reinterpret_cast<char *>(ring_s) + Ring::SMEM);
-    const uint32_t g0 = smem_u32(gamma) + 16u * (uint32_t)t;
-    float dg[N], db[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.f;
-    long long row = (long long)blockIdx.x * rpb + slot, ahead = row;
-    VecRow dy(p.dy, sizeof(E), row, step, c), tt(p.t, sizeof(E), row, step, c), dt(p.dt, sizeof(E), row, step, c), dx(p.dx, sizeof(E), row, step, c);
-    griddep_wait();
-    auto fetch = [&]() {
-        if (ahead < p.rows) {
-            ring.fetch(0, dy.p, hop, last);
-            ring.fetch(1, tt.p, hop, last);
-            if (RES) ring.fetch(2, dt.p, hop, last);
-        }
-        ring.next();
-        ahead += step;
-        dy.p += dy.inc;
-        tt.p += tt.inc;
-        dt.p += dt.inc;
-    };
-    for (int i = 0; i < S; ++i) fetch();
-    vec_param_fill<CH>(gamma, p.gamma, p.C, tpr, V);
-    __syncthreads();
-    for (; row - slot < p.rows; row += step, dx.p += dx.inc) {
-        const bool on = row < p.rows;
-        float d[N], v[N], g[CH];  // (gamma is read where it is used: holding it would spill)
-        cp_async_wait<S - 1>();
-        ring.read(0, d);
-        ring.read(1, v);
-        float2 sum = make_float2(0.f, 0.f), sd = sum, sq = sum, dot = sum;
-        if (on) {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) set2(db, i, add2(get2(d, i), get2(db, i)));
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-                sum = add2(get2(v + CH * j, i), sum);
-                sd = fma2(get2(d + CH * j, i), get2(g, i), sd);
-            }
-        }
-        float means[2] = {sum.x + sum.y, sd.x + sd.y};
-        row_sums<2>(means, tpr, slot, buf, 0);
-        const float2 mean = pair_of(-means[0] * inv_c);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
-        if (last == 0) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) v[CH * (V - 1) + i] = 0.f;
-        } else if (last < CH) {
-#pragma unroll
-            for (int i = 1; i < CH; ++i)
-                if (i >= last) v[CH * (V - 1) + i] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-                const float2 w = get2(v + CH * j, i);
-                sq = fma2(w, w, sq);
-                dot = fma2(mul2(get2(d + CH * j, i), get2(g, i)), w, dot);
-            }
-        }
-        float red[2] = {sq.x + sq.y, dot.x + dot.y};
-        row_sums<2>(red, tpr, slot, buf, 1);
-        const float rho = rsqrtf(red[0] * inv_c + p.eps);
-        const float2 rho2 = pair_of(rho), k2 = pair_of(-row_slope(rho, red[1] * inv_c)), m2 = pair_of(-rho * (means[1] * inv_c));
-        if (on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float s[CH];
-                vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
-                if (RES) ring.read_vector(2, j, s);
-#pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const float2 dr = mul2(get2(d + CH * j, i), rho2), w = get2(v + CH * j, i);
-                    set2(dg + CH * j, i, fma2(dr, w, get2(dg + CH * j, i)));
-                    const float2 base = RES ? add2(get2(s, i), m2) : m2;
-                    set2(s, i, fma2(dr, get2(g, i), fma2(w, k2, base)));
-                }
-                if (j + 1 < V)
-                    vec_store<E, CH>(dx.p + j * hop, s);
-                else
-                    vec_store_last<E, CH>(dx.p + j * hop, s, last);
-            }
-        }
-        fetch();
-    }
-    if (!p.dgamma && !p.dbeta) return;
-    float *ws0 = p.ws + 2ll * blockIdx.x * p.C;
-    float *acc_s = reinterpret_cast<float *>(ring_s);  // [slot][C], in the ring's place
-    cp_async_wait<0>();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float *acc = h ? db : dg;
-        if (rpb > 1) __syncthreads();
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float *at = (rpb > 1 ? acc_s + (long long)slot * p.C : ws0 + (long long)h * p.C) + (t + j * tpr) * CH;
-            const int n = j + 1 < V ? CH : last;
-            if (n == CH && p.C % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < CH / 4; ++i)
-                    reinterpret_cast<float4 *>(at)[i] = make_float4(acc[CH * j + 4 * i], acc[CH * j + 4 * i + 1], acc[CH * j + 4 * i + 2], acc[CH * j + 4 * i + 3]);
-            } else if (n > 0) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-                    if (i < n) at[i] = acc[CH * j + i];
-            }
-        }
-        if (rpb > 1) {
-            __syncthreads();
-            for (int k = threadIdx.x; k < p.C; k += blockDim.x) {
-                float s = 0.f;
-                for (int i = 0; i < rpb; ++i) s += acc_s[(long long)i * p.C + k];
-                ws0[(long long)h * p.C + k] = s;
-            }
-        }
-    }
-}
-
-// ---- host side ---------------------------------------------------------------
-
-// The launch: V vectors for each of a row's `tpr` threads, `rpb` rows a block.
-struct VecPlan {
-    int v = 0, tpr = 0, rpb = 0;
-};
-
-struct VecKernel {
-    const void *fn;
-    size_t ring;
-    int threads, blocks;  // of a block; blocks an SM's registers hold
-};
 
 // What these kernels take: see the top.
 bool whole(std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor> outs) {
@@ -500,98 +15,29 @@ bool whole(std::initializer_list<RowTensor> ins, std::initializer_list<RowTensor
     return true;
 }
 
-// The fewest threads whose `most` vectors hold a row, whole warps of them from a warp on; more, with
-// fewer vectors, while the rows are too few to give every SM a block.
-VecPlan plan_vec(long long rows, int C, bool fp32, int most, bool warps, int sm_count) {
-    VecPlan p;
-    const int nv = fp32 ? (C + 3) / 4 : (C + 7) / 8;
-    p.tpr = 8;
-    while (p.tpr < 32 && p.tpr * std::min(4, most) < nv) p.tpr *= 2;
-    while (p.tpr * most < nv) p.tpr += warps && p.tpr >= 128 ? 32 : p.tpr;
-    while (p.tpr * 2 <= VEC_THREADS && p.tpr < nv && rows * p.tpr * 2 <= (long long)VEC_THREADS * sm_count) p.tpr *= 2;
-    if (p.tpr > VEC_THREADS) return VecPlan();
-    p.v = (nv + p.tpr - 1) / p.tpr;
-    p.rpb = VEC_THREADS / p.tpr;
-    return p;
-}
-
-// `arrays`: channel-wise arrays in shared memory.
-template <typename P>
-dlcStatus_t launch_vec(dlcContext *ctx, const VecKernel &k, P &p, const VecPlan &v, bool fp32, int arrays, int *blocks = nullptr) {
-    int tpr = v.tpr;
-    const size_t smem = k.ring + (size_t)arrays * (fp32 ? 4 : 8) * v.v * tpr * sizeof(float);
-    const int per_sm = std::max(1, std::min(k.blocks, (int)(NORM_MAX_RING / (smem + 2048))));
-    const long long n = std::min((p.rows + v.rpb - 1) / v.rpb, (long long)ctx->sm_count * per_sm);
-    if (blocks) *blocks = (int)n;
-    void *args[] = {&p, &tpr};
-    if (!dlc_allow_smem(ctx, k.fn, smem)) return DLC_STATUS_EXECUTION_FAILED;
-    return dlc_launch(ctx, k.fn, dim3((unsigned)n), dim3((unsigned)k.threads), smem, args);
-}
-
-template <int V, typename E, typename Y, bool RES>
-VecKernel vec_fwd() {
-    return {(const void *)layer_vec_kernel<V, E, Y, RES>, VecRing<V, E, RES ? 2 : 1, vec_ring<V>(), VEC_THREADS>::SMEM, VEC_THREADS,
-            vec_blocks<V, E>()};
-}
-
-template <int V, typename E>
-VecKernel vec_fwd(const LayerProblem &p) {
-    const bool res = p.r.p != nullptr;
-    if (p.y.dt == DLC_DATA_BFLOAT16) return res ? vec_fwd<V, E, unsigned short, true>() : vec_fwd<V, E, unsigned short, false>();
-    if (p.y.dt == DLC_DATA_FLOAT) return res ? vec_fwd<V, E, float, true>() : vec_fwd<V, E, float, false>();
-    return res ? vec_fwd<V, E, unsigned char, true>() : vec_fwd<V, E, unsigned char, false>();
-}
-
 VecKernel vec_fwd(int v, const LayerProblem &p) {
     if (p.x.dt == DLC_DATA_FLOAT) {
         switch (v) {
-            case 1: return vec_fwd<1, float>(p);
-            case 2: return vec_fwd<2, float>(p);
-            case 3: return vec_fwd<3, float>(p);
-            case 4: return vec_fwd<4, float>(p);
-            case 5: return vec_fwd<5, float>(p);
-            case 6: return vec_fwd<6, float>(p);
-            case 7: return vec_fwd<7, float>(p);
-            default: return vec_fwd<8, float>(p);
+            case 1: return vec_fwd<1, float, false>(p);
+            case 2: return vec_fwd<2, float, false>(p);
+            case 3: return vec_fwd<3, float, false>(p);
+            case 4: return vec_fwd<4, float, false>(p);
+            case 5: return vec_fwd<5, float, false>(p);
+            case 6: return vec_fwd<6, float, false>(p);
+            case 7: return vec_fwd<7, float, false>(p);
+            default: return vec_fwd<8, float, false>(p);
         }
     }
     using Half = unsigned short;
     switch (v) {
-        case 1: return vec_fwd<1, Half>(p);
-        case 2: return vec_fwd<2, Half>(p);
-        case 3: return vec_fwd<3, Half>(p);
-        case 4: return vec_fwd<4, Half>(p);
-        case 5: return vec_fwd<5, Half>(p);
-        case 6: return vec_fwd<6, Half>(p);
-        case 7: return vec_fwd<7, Half>(p);
-        default: return vec_fwd<8, Half>(p);
-    }
-}
-
-template <int V, typename E, int TH>
-VecKernel vec_bwd(bool res) {
-    constexpr int S = vec_bwd_ring<V>();
-    return res ? VecKernel{(const void *)layer_bwd_vec_kernel<V, E, true, TH>, VecRing<V, E, 3, S, TH>::SMEM, TH, 512 / TH}
-               : VecKernel{(const void *)layer_bwd_vec_kernel<V, E, false, TH>, VecRing<V, E, 2, S, TH>::SMEM, TH, 512 / TH};
-}
-
-// (a row of more than 128 threads has a block of its own: 160, 192 or 224 threads where they are enough)
-template <int V, typename E>
-VecKernel vec_bwd(int tpr, bool res) {
-    return tpr == 160   ? vec_bwd<V, E, 160>(res)
-           : tpr == 192 ? vec_bwd<V, E, 192>(res)
-           : tpr == 224 ? vec_bwd<V, E, 224>(res)
-                        : vec_bwd<V, E, 256>(res);
-}
-
-VecKernel vec_bwd(const VecPlan &v, bool fp32, bool res) {
-    using Half = unsigned short;
-    if (!fp32) return v.v == 1 ? vec_bwd<1, Half, 256>(res) : vec_bwd<2, Half>(v.tpr, res);
-    switch (v.v) {
-        case 1: return vec_bwd<1, float, 256>(res);
-        case 2: return vec_bwd<2, float, 256>(res);
-        case 3: return vec_bwd<3, float, 256>(res);
-        default: return vec_bwd<4, float>(v.tpr, res);
+        case 1: return vec_fwd<1, Half, false>(p);
+        case 2: return vec_fwd<2, Half, false>(p);
+        case 3: return vec_fwd<3, Half, false>(p);
+        case 4: return vec_fwd<4, Half, false>(p);
+        case 5: return vec_fwd<5, Half, false>(p);
+        case 6: return vec_fwd<6, Half, false>(p);
+        case 7: return vec_fwd<7, Half, false>(p);
+        default: return vec_fwd<8, Half, false>(p);
     }
 }
 
@@ -601,9 +47,9 @@ bool dlc_layer_vec(dlcContext *ctx, const LayerProblem &pb, dlcStatus_t &status)
     LayerProblem p = pb;
     if (!whole({p.x, p.r}, {p.t, p.y}) || (p.t.p && p.t.dt != p.x.dt)) return false;
     const bool fp32 = p.x.dt == DLC_DATA_FLOAT;
-    const VecPlan v = plan_vec(p.rows, p.C, fp32, 8, false, ctx->sm_count);
+    const VecPlan v = plan_vec(p.rows, p.C, fp32, 8, false, false, ctx->sm_count);
     if (!v.v) return false;
-    status = launch_vec(ctx, vec_fwd(v.v, p), p, v, fp32, 2);
+    status = launch_vec(ctx, vec_fwd(v.v, p), p, v, fp32, false, 2, 0);
     return true;
 }
 
@@ -611,11 +57,11 @@ bool dlc_layer_bwd_vec(dlcContext *ctx, const LayerBwdProblem &pb, dlcStatus_t &
     LayerBwdProblem p = pb;
     if (!whole({p.dy, p.t, p.dt}, {p.dx}) || p.dx.dt != p.t.dt) return false;
     const bool fp32 = p.t.dt == DLC_DATA_FLOAT, res = p.dt.p != nullptr;
-    const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 2, true, ctx->sm_count);
+    const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 2, true, false, ctx->sm_count);
     if (!v.v) return false;
     int blocks = 0;
     // (the rows of sums that a block joins need no more than the ring has)
-    status = launch_vec(ctx, vec_bwd(v, fp32, res), p, v, fp32, 1, &blocks);
+    status = launch_vec(ctx, vec_bwd<false>(v, fp32, res), p, v, fp32, false, 1, 0, &blocks);
     if (status == DLC_STATUS_SUCCESS && (p.dgamma || p.dbeta))
         status = dlc_launch_column_sums(ctx, p.ws, p.dgamma, p.dbeta, p.C, blocks);
     return true;

@@ -92,6 +92,44 @@ def test_layer_norm_of_images(handle, axes, crop):
     close(rows, want, err + cref.stored(want, F32), axes)
 
 
+def pitched(t, pitch):
+    """The same rows at a pitch of so many elements, NaN between them."""
+    out = torch.full((t.shape[0], pitch), float("nan"), device=t.device).to(t.dtype)[:, :t.shape[1]]
+    out.copy_(t)
+    return out
+
+
+# one thread's channels and a row's, vectors that begin with the last channel in front of a row, 257
+# vectors of eight where 256 would do, rows with blocks of their own, and rows too long for shared memory
+@pytest.mark.parametrize("rows,c", [(1, 5), (9, 8), (300, 1), (70, 57), (1000, 130), (41, 250), (33, 1024), (4001, 256), (700, 1001), (64, 2048),
+                                    (19, 4033), (7, 4096), (11, 8185), (3, 16381)])
+@pytest.mark.parametrize("pad,y_pad", [(0, 0), (5, 0), (5, 5), (3, 1), (8, 7), (1, 16)])
+@pytest.mark.parametrize("dtype,ydt", [(BF, BF), (BF, F8), (BF, F32), (F32, F32), (F32, BF), (F32, F8)])
+def test_layer_norm_of_rows_that_begin_anywhere(handle, rows, c, pad, y_pad, dtype, ydt):
+    x, r = (pitched(rand(rows, c, seed=s, std=2.0, dtype=dtype), c + pad) for s in (1, 2))
+    gamma, beta = 1 + 0.3 * rand(c, seed=3), rand(c, seed=4)
+    whole = torch.full((rows, c + y_pad), 7.0, device="cuda").to(ydt)
+    y, scale = whole[:, :c], out_like(rows, 1, F32)[:, 0] if ydt == F8 else None
+    t, want, err = ref.layer_norm(d(x), d(r), d(gamma), d(beta), EPS)
+    dy, dt = (pitched(rand(rows, c, seed=s, dtype=dtype), c + pad) for s in (5, 6))
+    api.LayerNormForward(handle, x, y, residual=r, total=x, eps=EPS)(x, gamma, y, beta=beta, residual=r, total=x, scale=scale)
+    close(x, t, cref.stored(t, dtype) + cref.U32 * t.abs(), "total")
+    if ydt == F8:
+        close_e4m3(y, scale, want, err, "y")
+    else:
+        close(y, want, err + cref.stored(want, ydt), "y")
+    assert (whole[:, c:].float() == 7).all()
+    between = x.as_strided((rows - 1, pad), (c + pad, 1), c)  # (behind the last row is nothing that a view has)
+    assert torch.isnan(between.float()).all()
+    dx, dg, db = pitched(torch.zeros(rows, c, device="cuda").to(dtype), c + pad), out_like(c, 1, F32)[:, 0], out_like(c, 1, F32)[:, 0]
+    (want, ex), (wg, eg), (wb, eb) = ref.layer_norm_backward(d(dy), d(x), d(gamma), d(dt), EPS)
+    api.LayerNormBackward(handle, dy, x, dx, dtotal=dt, eps=EPS)(dy, x, gamma, dx, dgamma=dg, dbeta=db, dtotal=dt)
+    close(dx, want, ex + cref.stored(want, dtype), "dx")
+    close(dg, wg, eg + 1e-30, "dgamma")
+    close(db, wb, eb + 1e-30, "dbeta")
+    assert torch.isnan(dx.as_strided((rows - 1, pad), (c + pad, 1), c).float()).all()
+
+
 @pytest.mark.parametrize("c", [256, 100, 5000])
 @pytest.mark.parametrize("layout", ["dense", "columns"])
 def test_layer_norm_in_place_equal_and_non_finite_rows(handle, c, layout):
