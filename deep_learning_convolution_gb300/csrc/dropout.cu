@@ -12,7 +12,7 @@
 //
 // x (and r) in, y out: memory bounds it with a residual, the generator's multiplies without.  16384 x 4096
 // BF16 63.8 us with residual (6.3 TB/s) and 57 us without (4.7); unaligned rows, 16384 x 1001 with
-// residual, 34 us; channels apart, 128 images of 512 x 28 x 28, 172 us (1.2 TB/s).
+// residual, 27 us; channels apart, 128 images of 512 x 28 x 28, 172 us (1.2 TB/s).
 #include "channel.cuh"
 #include "ptx.cuh"
 
@@ -114,6 +114,11 @@ struct Piece {
             for (int i = 0; i < W; ++i) v[i] = i < n ? p[i * t.m.cs] : (E)0;
         }
     }
+    __device__ __forceinline__ void load_some(const RowTensor &t, long long off, int n) {
+        const E *p = static_cast<const E *>(t.p) + off;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = i < n ? p[i] : (E)0;
+    }
     __device__ __forceinline__ float at(int i) const {
         if constexpr (sizeof(E) == 2)
             return bf16_bits_f32(v[i]);
@@ -195,6 +200,86 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_columns_kernel(
     }
 }
 
+// Rows that begin anywhere in a 16-byte piece, all of them alike: the pieces are vectors of eight channels, whose
+// groups of four words begin `off` channels ahead, so up to three groups make a vector's words.  A thread's
+// rows are a multiple of eight apart, and begin alike.  BF16: FP32 rows gain nothing from vectors, which cost them
+// half as many words again (16384 x 1001 36.4 us either way, without residual 30.0 and 28.7).
+__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_shift_kernel(const __grid_constant__ DoParams p) {
+    griddep_launch_dependents();
+    using E = unsigned short;
+    constexpr int W = 8, U = 2;
+    const uint32_t pieces = (uint32_t)p.inner, i = blockIdx.x * DO_THREADS + threadIdx.x;
+    const uint32_t row0 = i / pieces, piece = i - row0 * pieces;
+    const int lead = (int)(row0 % 8u * (uint32_t)(p.d.x.m.ld % 8)) % 8;
+    const int c = W * (int)piece - lead, skip = max(-c, 0), n = min(W, p.d.C - c);
+    if (row0 >= (uint32_t)p.rows_step || n <= 0) return;
+    const int off = -lead & 3;
+    const uint32_t group = (uint32_t)((c - off) / 4);  // (exact)
+    griddep_wait();
+    const Philox gen(p.d.random);
+    const PhiloxColumn first(gen, group), second(gen, group + 1), third(gen, group + 2);
+    const bool res = p.d.r.p != nullptr;
+    uint32_t h0, l0;
+    wide(gen.s0, PHILOX_M1, h0, l0);
+    h0 ^= gen.k0[0];
+    long long px = row0 * p.d.x.m.ld + c, pr = row0 * p.d.r.m.ld + c, py = row0 * p.d.y.m.ld + c;
+    const long long dx = p.rows_step * p.d.x.m.ld, dr = p.rows_step * p.d.r.m.ld, dy = p.rows_step * p.d.y.m.ld;
+    for (long long row = row0; row < p.d.rows; row += (long long)U * p.rows_step) {
+        Piece<W, E> x[U];
+        Piece<W, E> r[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long at = row + k * p.rows_step;
+            if (at < p.d.rows) {
+                // (a piece that the next row begins in; the first row begins a piece)
+                const bool whole = n == W || at + 1 < p.d.rows;
+                if (whole)
+                    x[k].load(p.d.x, px, W);
+                else
+                    x[k].load_some(p.d.x, px, n);
+                if (res && whole) r[k].load(p.d.r, pr, W);
+                if (res && !whole) r[k].load_some(p.d.r, pr, n);
+                px += dx;
+                pr += dr;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (row + k * p.rows_step >= p.d.rows) break;
+            uint32_t hi, lo, u[12];
+            wide(h0 ^ (uint32_t)(row + k * p.rows_step), PHILOX_M0, hi, lo);
+            first.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u));
+            second.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u + 4));
+            if (off) {
+                third.words(gen, hi, lo, *reinterpret_cast<uint32_t(*)[4]>(u + 8));
+#pragma unroll
+                for (int j = 0; j < 10; ++j) u[j] = off & 2 ? u[j + 2] : u[j];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = off & 1 ? u[j + 1] : u[j];
+            }
+            float f[W];
+#pragma unroll
+            for (int j = 0; j < W; j += 2) {
+                const float2 v = mul2(make_float2(x[k].at(j), x[k].at(j + 1)), pair_of(p.d.scale));
+                f[j] = u[j] >= p.d.border ? v.x : 0.f;
+                f[j + 1] = u[j + 1] >= p.d.border ? v.y : 0.f;
+            }
+            if (res) {
+#pragma unroll
+                for (int j = 0; j < W; j += 2) set2(f + j, 0, add2(get2(f + j, 0), make_float2(r[k].at(j), r[k].at(j + 1))));
+            }
+            if (skip == 0 && n == W) {
+                put<W, E>(p.d.y, py, n, f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (j >= skip && j < n) store_elem(p.d.y.p, DLC_DATA_BFLOAT16, py + j, f[j]);
+            }
+            py += dy;
+        }
+    }
+}
+
 // Any other layout: pieces of up to four channels, U of a thread in flight together; a thread steps from
 // piece to piece without dividing.
 template <typename X, typename R, typename Y>
@@ -246,7 +331,7 @@ __global__ void __launch_bounds__(DO_THREADS, 2) dropout_kernel(const __grid_con
 
 using Half = unsigned short;
 
-enum { ANY, SINGLES, VECTORS };
+enum { ANY, SINGLES, SHIFTED, VECTORS };
 
 template <typename X, typename R, typename Y>
 const void *do_kernel(int way) {
@@ -261,6 +346,7 @@ const void *do_kernel(int y, int way) {
 }
 
 const void *do_kernel(const DropoutProblem &d, int way) {
+    if (way == SHIFTED) return (const void *)dropout_shift_kernel;
     const bool x = d.x.dt == DLC_DATA_BFLOAT16, r = d.r.p ? d.r.dt == DLC_DATA_BFLOAT16 : x;
     if (x) return r ? do_kernel<Half, Half>(d.y.dt, way) : do_kernel<Half, float>(d.y.dt, way);
     return r ? do_kernel<float, Half>(d.y.dt, way) : do_kernel<float, float>(d.y.dt, way);
@@ -273,16 +359,27 @@ dlcStatus_t dlc_launch_dropout(dlcContext *ctx, const DropoutProblem &pb) {
     p.d = pb;
     auto columns = [&](const RowTensor &t) { return !t.p || (t.m.cs == 1 && t.m.uniform); };
     auto whole = [&](const RowTensor &t) { return !t.p || dlc_aligned_rows(t, 16); };
+    // tensors that begin on a piece, and their rows in the same way; rows that do not overlap, so that what is read behind
+    // one is the next one's
+    auto alike = [&](const RowTensor &t) {
+        return !t.p || (t.dt == DLC_DATA_BFLOAT16 && (uintptr_t)t.p % 16 == 0 && t.m.ld >= pb.C && t.m.ld % 8 == pb.x.m.ld % 8);
+    };
     const long long most = (long long)ctx->sm_count * DO_BLOCKS * DO_THREADS;  // threads
     int way = ANY;
-    if (columns(pb.x) && columns(pb.r) && columns(pb.y) && pb.C / 4 < most)
+    if (columns(pb.x) && columns(pb.r) && columns(pb.y) && pb.C / 4 < most) {
         way = pb.C % 8 == 0 && whole(pb.x) && whole(pb.r) && whole(pb.y) ? VECTORS : SINGLES;
-    const int w = way == VECTORS ? 8 : 4;
-    const long long pieces = (pb.C + w - 1) / w;
+        // (with residual and without, by vectors and by single elements: 16384 x 1001 27.3 / 25.0 and 32.6 / 26.9 us, 777 x
+        // 1001 3.1 / 3.0 and 3.7 / 3.4, 60000 x 250 26.0 / 23.9 and 30.1 / 24.9; 16384 x 130 5.9 / 5.6 and 6.2 / 5.4,
+        // 200000 x 17 11.9 / 11.3 and 9.2 / 8.0)
+        if (way == SINGLES && pb.C >= 192 && alike(pb.x) && alike(pb.r) && alike(pb.y) && (pb.C + 14) / 8 * 8 <= most) way = SHIFTED;
+    }
+    const int w = way == VECTORS || way == SHIFTED ? 8 : 4;
+    const long long pieces = (pb.C + w - 1 + (way == SHIFTED ? 7 : 0)) / w;
     p.items = pb.rows * pieces;
     p.apart = way == ANY && pb.x.m.cs != 1 && pb.y.m.cs != 1;
     p.inner = p.apart ? pb.rows : pieces;
     p.rows_step = (int)std::min(pb.rows, most / pieces);
+    if (way == SHIFTED) p.rows_step = (int)(std::min(pb.rows + 7, most / pieces) / 8 * 8);
     const long long threads = way != ANY ? p.rows_step * pieces : std::min(p.items, (long long)ctx->sm_count * 2 * DO_THREADS);
     void *args[] = {&p};
     return dlc_launch(ctx, do_kernel(pb, way), dim3((unsigned)((threads + DO_THREADS - 1) / DO_THREADS)), dim3(DO_THREADS), 0, args);

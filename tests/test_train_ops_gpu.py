@@ -295,6 +295,27 @@ def test_dropout_layouts_have_one_mask(handle, rows, c, layout):
     assert torch.equal(image != 0, keep & (dense != 0))
 
 
+@pytest.mark.parametrize("rows,c", [(1, 192), (2, 1001), (7, 250), (9, 333), (1000, 257), (4001, 198), (31, 4093)])
+@pytest.mark.parametrize("pad", [0, 1, 2, 3, 4, 5, 6, 7])
+def test_dropout_of_rows_that_begin_anywhere(handle, rows, c, pad):
+    x, r = (pitched(rand(rows, c, seed=s, dtype=BF), c + pad) for s in (1, 2))
+    for res in (r, None):
+        y = pitched(torch.zeros(rows, c, device="cuda").to(BF), c + pad)
+        api.DropoutForward(handle, x, y, p=0.4, residual=res)(x, words(7, rows), y, residual=res)
+        want, _ = ref.dropout(d(x), d(res), 0.4, 7, rows)
+        close(y, want, cref.stored(want, BF) + cref.U32 * (3 * want.abs() + (0 if res is None else 3 * d(res).abs())), "y")
+        assert torch.isnan(y.as_strided((rows - 1, pad), (c + pad, 1), c).float()).all()
+    # in place, and the neighbours of the first and the last row
+    whole = torch.full((rows * (c + pad) + 16,), 3.0, device="cuda").to(BF)
+    y = whole[8:8 + rows * (c + pad)].view(rows, c + pad)[:, :c]
+    y.copy_(x)
+    want, _ = ref.dropout(d(x), None, 0.4, 7, rows)
+    api.DropoutBackward(handle, y, y, p=0.4)(y, words(7, rows), y)
+    close(y, want, cref.stored(want, BF) + 3 * cref.U32 * want.abs(), "in place")
+    y.fill_(3.0)
+    assert (whole == 3).all()
+
+
 def test_dropout_of_images_counts_pixels_in_order(handle):
     x = rand(2, 20, 5, 6, seed=1)  # NCHW
     y = torch.empty_like(x)
