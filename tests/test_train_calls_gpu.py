@@ -308,3 +308,26 @@ def test_cross_entropy_of_weights_of_more_than_2_31_elements(handle, rows):
     _, (want, err), _ = ref.cross_entropy_backward(d(x), d(w), target, f, d(dloss), BF, BF)
     del f
     close(dw, want, err, "dw")
+
+
+@pytest.mark.parametrize("rows,c,v", [(1, 257, 3), (40, 1001, 70), (3, 300, 1), (300, 2047, 40)])
+@pytest.mark.parametrize("shift", [0, 1, 2, 5, 7])
+@pytest.mark.parametrize("pad", [0, 1, 3])
+def test_operands_at_any_address_are_copied_whole(handle, rows, c, v, shift, pad):
+    """A product whose operands begin anywhere in a 16-byte piece, between values that are none, is that of
+    aligned ones."""
+    def placed(t, pitch):
+        n = t.shape[0] * pitch
+        out = torch.full((n + 16,), float("nan"), dtype=BF, device="cuda")[shift:shift + n].view(t.shape[0], pitch)[:, :t.shape[1]]
+        out.copy_(t)
+        return out
+    wide = (c + 15) // 16 * 16
+    x, w = rand(rows, c, seed=1, dtype=BF), rand(v, c, seed=2, dtype=BF)
+    aligned = [torch.nn.functional.pad(t, (0, wide - c)) for t in (x, w)]
+    y, want = torch.empty(rows, v, device="cuda"), torch.empty(rows, v, device="cuda")
+    xs, ws = placed(x, c + pad), placed(w, c)
+    api.LinearForward(handle, xs, ws, y)(xs, ws, y)
+    api.LinearForward(handle, *aligned, want)(*aligned, want)
+    # sums of c products in FP32 in some order each: c / 2 roundings of a sum of size sum |x w| at most
+    bound = 2.0 ** -24 * c * (x.double().abs() @ w.double().abs().T)
+    assert ((y.double() - want.double()).abs() <= bound).all()

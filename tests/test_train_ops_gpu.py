@@ -163,10 +163,11 @@ def test_layer_norm_of_one_type_in_place(handle, rows, c, dtype):
     close(dt, want, ex + cref.stored(want, dtype), "dx")
 
 
-def test_broadcast_residuals_are_read_by_their_strides(handle):
+@pytest.mark.parametrize("rows,c,pad", [(70, 256, 0), (70, 1001, 7), (70, 1001, 0)])
+def test_broadcast_residuals_are_read_by_their_strides(handle, rows, c, pad):
     """A residual of one row for all."""
-    rows, c = 70, 256
-    x, one, y = rand(rows, c, seed=1, dtype=BF), rand(1, c, seed=2, dtype=BF), torch.empty(rows, c, dtype=BF, device="cuda")
+    x, one = pitched(rand(rows, c, seed=1, dtype=BF), c + pad), rand(1, c, seed=2, dtype=BF)
+    y = pitched(torch.zeros(rows, c, device="cuda").to(BF), c + pad)
     many, g = one.expand(rows, c), torch.ones(c, device="cuda")
     try:
         op = api.LayerNormForward(handle, x, y, residual=many, eps=EPS)
