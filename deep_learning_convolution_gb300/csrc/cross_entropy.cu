@@ -225,7 +225,120 @@ __global__ void __launch_bounds__(1024) ce_strips_kernel(const float *sums, floa
     }
 }
 
+// ---- dw of a few rows -------------------------------------------------------------------
+//
+// dw[k, c] = sum_m dz[m, k] x[m, c] for up to 16 rows: little but writing dw, which the tiles of a general
+// product do at 3.5 TB/s (their epilogues have one step of the product to hide behind).  A warp keeps 64
+// channels of x in registers as the B operands of one step of mma.sync, and takes 16 classes of dz at a time; the
+// columns of the four tiles are dealt so that a thread is left with eight neighbouring channels.  Steps, in
+// tiles and this way: 1 x 1024 -> 131072 252 and 217 us, 8 x 1024 -> 50000 132 and 120, 16 x 2048 -> 50304 204
+// and 197; two steps of it for 32 x 4096 -> 131072 850 and 1055.
+
+constexpr int CO_THREADS = 256, CO_ROWS = 16;
+
+struct CeOuterParams {
+    const unsigned short *dz;  // [M][ldz]
+    long long ldz;
+    RowTensor x;
+    void *dw;                  // [cols][C]
+    int M, C, cols, warps;     // warps of a block side by side along the channels (a power of two)
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CO_THREADS, 3) ce_outer_kernel(const __grid_constant__ CeOuterParams p) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int side = warp % p.warps, per = CO_THREADS / 32 / p.warps;
+    const int c0 = ((int)blockIdx.x * p.warps + side) * 64;
+    const int tiles = (p.cols + 15) / 16, step = (int)gridDim.y * per;
+    griddep_wait();
+    uint32_t b[2][4][2];  // [.. of 32 channels][tile][rows 2 q and 2 q + 8, with the next one each]
+    const unsigned short *x = static_cast<const unsigned short *>(p.x.p);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int m = 8 * r + 2 * q;
+        const long long r0 = m < p.M ? row_off(p.x.m, m) : 0, r1 = m + 1 < p.M ? row_off(p.x.m, m + 1) : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = c0 + 32 * h + (g >> 1) * 8 + 2 * j + (g & 1);
+                const uint32_t lo = m < p.M && c < p.C ? x[r0 + c * p.x.m.cs] : 0u, hi = m + 1 < p.M && c < p.C ? x[r1 + c * p.x.m.cs] : 0u;
+                b[h][j][r] = lo | hi << 16;
+            }
+    }
+    uint32_t a[4], next[4];
+    auto load = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = tile * 16 + g + 8 * (i & 1), m = 8 * (i >> 1) + 2 * q;
+            const uint32_t lo = v < p.cols && m < p.M ? p.dz[m * p.ldz + v] : 0u, hi = v < p.cols && m + 1 < p.M ? p.dz[(m + 1) * p.ldz + v] : 0u;
+            next[i] = lo | hi << 16;
+        }
+    };
+    int tile = (int)blockIdx.y * per + warp / p.warps;
+    if (tile < tiles) load(tile);
+    for (; tile < tiles; tile += step) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = next[i];
+        if (tile + step < tiles) load(tile + step);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float d[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+                mma_16816(d[j], a, b[h][j][0], b[h][j][1]);
+            }
+            const int c = c0 + 32 * h + 8 * q;  // (rows are whole vectors)
+            if (c >= p.C) continue;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int v = tile * 16 + g + 8 * r;
+                if (v >= p.cols) continue;
+                T *dst = static_cast<T *>(p.dw) + (long long)v * p.C + c;
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16(d[0][2 * r], d[0][2 * r + 1]), pack_bf16(d[1][2 * r], d[1][2 * r + 1]),
+                                                                 pack_bf16(d[2][2 * r], d[2][2 * r + 1]), pack_bf16(d[3][2 * r], d[3][2 * r + 1]));
+                } else {
+                    reinterpret_cast<float4 *>(dst)[0] = make_float4(d[0][2 * r], d[0][2 * r + 1], d[1][2 * r], d[1][2 * r + 1]);
+                    reinterpret_cast<float4 *>(dst)[1] = make_float4(d[2][2 * r], d[2][2 * r + 1], d[3][2 * r], d[3][2 * r + 1]);
+                }
+            }
+        }
+    }
+}
+
 // ---- host side -------------------------------------------------------------------------
+
+// Whether ce_outer_kernel takes dw's product.
+bool outer_ok(const CrossEntropyProblem &p) { return p.M <= CO_ROWS && p.K % 8 == 0 && (uintptr_t)p.dw.p % 16 == 0; }
+
+dlcStatus_t launch_outer(dlcContext *ctx, const CrossEntropyProblem &p, const unsigned short *dz, long long ldz, int n0, int cols) {
+    CeOuterParams o;
+    o.dz = dz;
+    o.ldz = ldz;
+    o.x = p.x;
+    o.dw = static_cast<char *>(p.dw.p) + (size_t)n0 * p.K * dlc_dtype_bytes((dlcDataType_t)p.dw.dt);
+    o.M = (int)p.M;
+    o.C = p.K;
+    o.cols = cols;
+    o.warps = 1;
+    while (o.warps < CO_THREADS / 32 && o.warps * 64 < p.K) o.warps *= 2;
+    const int per = CO_THREADS / 32 / o.warps;
+    const long long gx = (p.K + 64ll * o.warps - 1) / (64 * o.warps), need = ((cols + 15) / 16 + per - 1) / per;
+    const long long gy = std::min<long long>(need, std::max<long long>(1, std::min<long long>(65535, (long long)ctx->sm_count * 12 / gx)));
+    const bool bf = p.dw.dt == DLC_DATA_BFLOAT16;
+    const void *kern = bf ? (const void *)ce_outer_kernel<unsigned short> : (const void *)ce_outer_kernel<float>;
+    void *args[] = {&o};
+    return dlc_launch(ctx, kern, dim3((unsigned)gx, (unsigned)gy), dim3(CO_THREADS), 0, args);
+}
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -531,7 +644,8 @@ dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProb
             if (s == DLC_STATUS_SUCCESS) s = dlc_launch_column_sum(ctx, many ? to : from, p.dbias + n0, cols, many ? CE_STRIPS : rows);
         }
         if (s == DLC_STATUS_SUCCESS && p.dx.p) s = dlc_launch_gemm(ctx, b.data(p, n0, cols));
-        if (s == DLC_STATUS_SUCCESS && p.dw.p) s = dlc_launch_gemm(ctx, b.filters(p, n0, cols));
+        if (s == DLC_STATUS_SUCCESS && p.dw.p)
+            s = outer_ok(p) ? launch_outer(ctx, p, b.dz, b.ldz, n0, cols) : dlc_launch_gemm(ctx, b.filters(p, n0, cols));
         return s;
     });
 }

@@ -546,6 +546,17 @@ def test_cross_entropy_of_single_rows_of_any_layout(handle, rows, c, v, layout):
     check_entropy(handle, x, shifted, b, target, dloss, layout=layout)
 
 
+@pytest.mark.parametrize("rows,c,v", [(16, 200, 333), (32, 4096, 70), (31, 24, 15), (17, 8, 1), (8, 72, 40000), (15, 64, 16), (33, 128, 100), (1, 1024, 5)])
+@pytest.mark.parametrize("dw_dtype,layout", [(BF, "dense"), (F32, "columns"), (BF, "odd")])
+def test_cross_entropy_filters_of_few_rows(handle, rows, c, v, dw_dtype, layout):
+    x, w, b, target, dloss = entropy_case(rows, c, v, True)
+    loss, lse, dx, dw, db = check_entropy(handle, laid_out(x, layout), w, b, target, dloss, dw_dtype=dw_dtype, layout=layout)
+    # the rows of its own and no others
+    whole = torch.full((v + 2, c), 5.0, dtype=dw_dtype, device="cuda")
+    api.CrossEntropyBackward(handle, x, w, target, None, whole[1:-1])(x, w, target, lse, dloss, dw=whole[1:-1], bias=b)
+    assert torch.equal(whole[1:-1], dw) and (whole[0] == 5).all() and (whole[-1] == 5).all()
+
+
 @pytest.mark.parametrize("rows,c,v", [(1, 40, 600), (2, 24, 513), (3, 41, 700), (1, 41, 5000), (1, 7, 1)])
 def test_cross_entropy_of_single_e4m3_rows(handle, rows, c, v):
     x, w = rand(rows, c, seed=1).to(F8), rand(v, c, seed=2, std=0.5).to(F8)
