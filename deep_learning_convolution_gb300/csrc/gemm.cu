@@ -1406,6 +1406,11 @@ dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n) {
 
 int dlc_entropy_parts(const dlcContext *ctx, const GemmProblem &g) { return 2 * plan_gemm(ctx, g).n_tiles; }
 
+bool dlc_gemm_spread(const dlcContext *ctx, const GemmProblem &g) {
+    const GemmPlan p = plan_gemm(ctx, g);
+    return p.gemv || p.few_rows || (p.splits > 1 && p.full_tiles == 0);
+}
+
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
     const GemmPlan p = plan_gemm(ctx, g);
     return p.gemv ? DLC_KERNEL_GEMV : p.few_rows ? DLC_KERNEL_FEW_ROWS : DLC_KERNEL_GEMM_PAIR;

@@ -383,6 +383,8 @@ dlcStatus_t dlc_launch_pack(dlcContext *ctx, const PackItem *items, int n);
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g);
 size_t dlc_gemm_workspace(const dlcContext *ctx, const GemmProblem &g);
 int dlc_entropy_parts(const dlcContext *ctx, const GemmProblem &g);
+// Whether every output of the product is a sum of several CTAs' or warps' parts.
+bool dlc_gemm_spread(const dlcContext *ctx, const GemmProblem &g);
 dlcStatus_t dlc_launch_gemm(dlcContext *ctx, const GemmProblem &g);
 // act_grad.cu
 size_t dlc_act_grad_workspace(const dlcContext *ctx, const ActGradProblem &p);
