@@ -15,7 +15,7 @@
 // tokens' rows then written over.  16384 x 2048 BF16 into 65536 rows 70 us (the rows read, the table
 // written: 4.8 TB/s; three launches that sort and zero are 46 us of it, at 5.8 TB/s, the sums 15, the
 // join 5); zeroed beside the sums instead, by a flag a row, 120 us.  Small calls are their four
-// launches: 5000 x 300 FP32 added to a table 17 us.
+// launches: 5000 x 300 FP32 added to a table 17 us, 4000 x 300 into one 12.7.
 #include "channel.cuh"
 #include "ptx.cuh"
 
