@@ -307,22 +307,22 @@ __global__ void __launch_bounds__(NORM_THREADS) rms_bwd_any_kernel(const __grid_
 // L2: latency, and the launch, which starts while the grid before it ends (304
 // partial rows of 1024 columns add 2.7 us to a backward call).
 // Columns from `half` on are those of out2 (either output may be absent).
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *ws, float *out, float *out2, int half, int C, int blocks) {
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *ws, float *out, float *out2, long long half, long long C, int blocks) {
     griddep_launch_dependents();
     __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = (int)blockIdx.x * 32 + lane;
+    const long long c = (long long)blockIdx.x * 32 + lane;
     griddep_wait();
     float s = 0.f;
     if (c < C) {
 #pragma unroll 8
-        for (int b = warp; b < blocks; b += 32) s += ws[(long long)b * C + c];
+        for (int b = warp; b < blocks; b += 32) s += ws[b * C + c];
     }
     part[warp][lane] = s;
     __syncthreads();
     s = part[lane][warp];  // column `warp`
     for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int k = (int)blockIdx.x * 32 + warp;
+    const long long k = (long long)blockIdx.x * 32 + warp;
     if (lane == 0 && k < C) {
         if (k < half) {
             if (out) out[k] = s;
@@ -438,12 +438,13 @@ dlcStatus_t dlc_launch_rms_bwd(dlcContext *ctx, const RmsBwdProblem &pb) {
 
 dlcStatus_t dlc_launch_column_sum(dlcContext *ctx, const float *ws, float *out, int C, int blocks) {
     float *out2 = nullptr;
-    void *args[] = {&ws, &out, &out2, &C, &C, &blocks};
-    return dlc_launch(ctx, (const void *)column_sum_kernel, dim3((unsigned)((C + 31) / 32)), dim3(1024), 0, args);
+    long long all = C;
+    void *args[] = {&ws, &out, &out2, &all, &all, &blocks};
+    return dlc_launch(ctx, (const void *)column_sum_kernel, dim3((unsigned)((all + 31) / 32)), dim3(1024), 0, args);
 }
 
 dlcStatus_t dlc_launch_column_sums(dlcContext *ctx, const float *ws, float *out, float *out2, int C, int blocks) {
-    int all = 2 * C;
-    void *args[] = {&ws, &out, &out2, &C, &all, &blocks};
+    long long half = C, all = 2 * half;  // (from 2^30 channels on more than an int holds)
+    void *args[] = {&ws, &out, &out2, &half, &all, &blocks};
     return dlc_launch(ctx, (const void *)column_sum_kernel, dim3((unsigned)((all + 31) / 32)), dim3(1024), 0, args);
 }
