@@ -38,6 +38,28 @@ __device__ __forceinline__ void centre(float (&v)[V * W], const Cols<W, V> &k, f
     }
 }
 
+// A sum of many terms and what its additions round off (Knuth's two-sum): the long rows' means.
+struct LongSum {
+    float s = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float t = s + v, b = t - s;
+        lost += (s - (t - b)) + (v - b);
+        s = t;
+    }
+    __device__ __forceinline__ float value() const { return s + lost; }
+};
+
+// Centres a thread's part of a row again (far_row), or leaves it where `far` is false.
+template <int W, int V>
+__device__ __forceinline__ void recentre(float (&v)[V * W], const Cols<W, V> &k, bool far, int C, int tpr, int slot,
+                                         float2 (*buf)[NORM_MAX_WARPS], int parity) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V * W / 2; ++i) sum = add2(get2(v, i), sum);
+    const float off = row_reduce<false>(sum.x + sum.y, 0.f, tpr, slot, buf, parity).x;
+    centre<W, V>(v, k, far ? off / (float)C : 0.f);
+}
+
 // Rows in registers, as rms_rows_kernel has them.
 template <int W, int V, int KIND, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > NORM_THREADS ? 1 : LN_FWD_BLOCKS)
@@ -93,16 +115,27 @@ __global__ void __launch_bounds__(MAXT, MAXT > NORM_THREADS ? 1 : LN_FWD_BLOCKS)
         }
         if (p.t.p && on) store_row<W, V>(p.t.dt, wt.at(p.t, row, c), cols, v);
         fetch();
-        float2 sum = make_float2(0.f, 0.f), sq = sum;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) sum = add2(get2(v, i), sum);
         const float mean = row_reduce<false>(sum.x + sum.y, 0.f, tpr, slot, buf, parity).x * inv_c;
         parity ^= 1;
         centre<W, V>(v, cols, mean);
+        auto squares = [&]() {
+            float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
-        const float ss = row_reduce<false>(sq.x + sq.y, 0.f, tpr, slot, buf, parity).x;
-        parity ^= 1;
+            for (int i = 0; i < E / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
+            const float ss = row_reduce<false>(sq.x + sq.y, 0.f, tpr, slot, buf, parity).x;
+            parity ^= 1;
+            return ss;
+        };
+        float ss = squares();
+        const bool far = far_row(mean, ss * inv_c);
+        if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+            recentre<W, V>(v, cols, far, p.C, tpr, slot, buf, parity);
+            parity ^= 1;
+            ss = squares();
+        }
         const float2 rho = pair_of(rsqrtf(ss * inv_c + p.eps));
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) set2(v, i, fma2(mul2(get2(v, i), rho), get2(g, i), get2(b, i)));
@@ -151,12 +184,29 @@ __global__ void __launch_bounds__(NORM_THREADS) layer_any_kernel(const __grid_co
                     if (in(i)) fn(c + i * M::STEP, v[i]);
             }
         };
-        float sum = 0.f, sq = 0.f, mx = 0.f;
-        each([&](int, float t) { sum += t; });
-        const float mean = M::template join<false>(sum, 0.f, part).x * inv_c;
-        each([&](int, float t) { sq = fmaf(t - mean, t - mean, sq); });
-        const float rho = rsqrtf(M::template join<false>(sq, 0.f, part).x * inv_c + p.eps);
-        auto y_of = [&](int c, float t) { return fmaf((t - mean) * rho, p.gamma[c], p.beta ? p.beta[c] : 0.f); };
+        LongSum sum;
+        float mx = 0.f, rest = 0.f;
+        each([&](int, float t) { sum.add(t); });
+        const float mean = M::template join<false>(sum.value(), 0.f, part).x * inv_c;
+        auto squares = [&]() {
+            float sq = 0.f;
+            each([&](int, float t) {
+                const float d = t - mean - rest;
+                sq = fmaf(d, d, sq);
+            });
+            return M::template join<false>(sq, 0.f, part).x;
+        };
+        float sq = squares();
+        const bool far = on && far_row(mean, sq * inv_c);
+        if (__syncthreads_or(far)) {
+            float off = 0.f;
+            each([&](int, float t) { off += t - mean; });
+            off = M::template join<false>(off, 0.f, part).x;
+            if (far) rest = off / (float)p.C;
+            sq = squares();
+        }
+        const float rho = rsqrtf(sq * inv_c + p.eps);
+        auto y_of = [&](int c, float t) { return fmaf((t - mean - rest) * rho, p.gamma[c], p.beta ? p.beta[c] : 0.f); };
         float inv = 1.f;
         if (p.y.dt == DLC_DATA_FLOAT8_E4M3) {
             each([&](int c, float t) { mx = fmaxf(mx, fabsf(y_of(c, t))); });
@@ -215,7 +265,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > NORM_THREADS ? 1 : LN_BWD_BLOCKS)
         const uint32_t starts[3] = {(uint32_t)(row * p.dy.m.ld * 2), (uint32_t)(row * p.t.m.ld * 2), (uint32_t)(row * p.dt.m.ld * 2)};
         rows.take(f, cols, starts);
         fetch();
-        float2 sum = make_float2(0.f, 0.f), sd = sum, sq = sum, dot = sum;
+        float2 sum = make_float2(0.f, 0.f), sd = sum;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
             sum = add2(get2(f[1], i), sum);
@@ -223,13 +273,22 @@ __global__ void __launch_bounds__(MAXT, MAXT > NORM_THREADS ? 1 : LN_BWD_BLOCKS)
         }
         const float2 means = row_reduce<false>(sum.x + sum.y, sd.x + sd.y, tpr, slot, buf, 0);
         centre<W, V>(f[1], cols, means.x * inv_c);
+        auto squares = [&]() {
+            float2 sq = make_float2(0.f, 0.f), dot = sq;
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            const float2 v = get2(f[1], i);
-            sq = fma2(v, v, sq);
-            dot = fma2(mul2(get2(f[0], i), get2(g, i)), v, dot);
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 v = get2(f[1], i);
+                sq = fma2(v, v, sq);
+                dot = fma2(mul2(get2(f[0], i), get2(g, i)), v, dot);
+            }
+            return row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, slot, buf, 1);
+        };
+        float2 red = squares();
+        const bool far = far_row(means.x * inv_c, red.x * inv_c);
+        if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+            recentre<W, V>(f[1], cols, far, p.C, tpr, slot, buf, 0);
+            red = squares();
         }
-        const float2 red = row_reduce<false>(sq.x + sq.y, dot.x + dot.y, tpr, slot, buf, 1);
         if (!on) continue;
         const float rho = rsqrtf(red.x * inv_c + p.eps);
         // dx = rho d - rho mean(d) - (t - mu) rho^3 mean(d (t - mu))
@@ -295,25 +354,41 @@ __global__ void __launch_bounds__(NORM_THREADS) layer_bwd_any_kernel(const __gri
             load_elems<AHEAD>(p.dy.p, p.dy.dt, yo + c * p.dy.m.cs, M::STEP * p.dy.m.cs, in, d);
             load_elems<AHEAD>(p.gamma, DLC_DATA_FLOAT, c, M::STEP, in, g);
         };
-        float sum = 0.f, sd = 0.f, sq = 0.f, dot = 0.f;
-        for (int c = M::first(); on && c < p.C; c += AHEAD * M::STEP) {
-            load(c, [&](int i) { return c + i * M::STEP < p.C; });
+        LongSum sum;
+        float sd = 0.f, rest = 0.f;
+        // fn(t - mean - rest, dy, gamma) for this thread's channels of the row
+        auto each = [&](float mean, auto fn) {
+            for (int c = M::first(); on && c < p.C; c += AHEAD * M::STEP) {
+                const auto in = [&](int i) { return c + i * M::STEP < p.C; };
+                load(c, in);
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) sum += v[i], sd = fmaf(d[i], g[i], sd);  // (zeros behind the row)
-        }
-        const float2 means = M::template join<false>(sum, sd, part);
-        const float mean = means.x * inv_c;
-        for (int c = M::first(); on && c < p.C; c += AHEAD * M::STEP) {
-            const auto in = [&](int i) { return c + i * M::STEP < p.C; };
-            load(c, in);
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const float t = in(i) ? v[i] - mean : 0.f;
-                sq = fmaf(t, t, sq);
-                dot = fmaf(d[i] * g[i], t, dot);
+                for (int i = 0; i < AHEAD; ++i)
+                    if (in(i)) fn(v[i] - mean - rest, d[i], g[i]);
             }
+        };
+        each(0.f, [&](float t, float dy, float gamma) {
+            sum.add(t);
+            sd = fmaf(dy, gamma, sd);
+        });
+        const float2 means = M::template join<false>(sum.value(), sd, part);
+        const float mean = means.x * inv_c;
+        auto squares = [&]() {
+            float sq = 0.f, dot = 0.f;
+            each(mean, [&](float t, float dy, float gamma) {
+                sq = fmaf(t, t, sq);
+                dot = fmaf(dy * gamma, t, dot);
+            });
+            return M::template join<false>(sq, dot, part);
+        };
+        float2 red = squares();
+        const bool far = on && far_row(mean, red.x * inv_c);
+        if (__syncthreads_or(far)) {
+            float off = 0.f;
+            each(mean, [&](float t, float, float) { off += t; });
+            off = M::template join<false>(off, 0.f, part).x;
+            if (far) rest = off / (float)p.C;
+            red = squares();
         }
-        const float2 red = M::template join<false>(sq, dot, part);
         const float rho = on ? rsqrtf(red.x * inv_c + p.eps) : 0.f;
         const float k = row_slope(rho, red.y * inv_c), m = rho * (means.y * inv_c);
         const long long xo = on ? row_off(p.dx.m, row) : 0, so = on && p.dt.p ? row_off(p.dt.m, row) : 0;
@@ -327,7 +402,7 @@ __global__ void __launch_bounds__(NORM_THREADS) layer_bwd_any_kernel(const __gri
             for (int i = 0; i < AHEAD; ++i) {
                 const int ci = c + i * M::STEP;
                 if (ci >= p.C) break;
-                const float t = v[i] - mean;
+                const float t = v[i] - mean - rest;
                 if (on) store_elem(p.dx.p, p.dx.dt, xo + ci * p.dx.m.cs, a[i] - m + rho * d[i] * g[i] - t * k);
                 if (!p.dgamma && !p.dbeta) continue;
                 float dg = on ? d[i] * rho * t : 0.f, db = d[i];

@@ -23,24 +23,21 @@ namespace {
 
 using namespace dlc;
 
-// Sum over the `tpr` threads of a row (a power of two or whole warps), as row_reduce has it; the
-// usual numbers of warps without a loop, whose branches would count.
+// Sums over the `tpr` threads of a row (a power of two or whole warps), as row_reduce has them; the
+// usual numbers of warps without a loop, whose branches would count.  A warp has two words of the buffer in
+// every reduction, of one sum too: a block's rows run ahead of one another.
 template <int N, int WARPS>
 __device__ __forceinline__ void join_warps(float (&a)[N], const float *row) {
-    float4 q[WARPS * N / 4 > 0 ? WARPS * N / 4 : 1];
-    if constexpr (WARPS * N >= 4) {
+    float4 q[WARPS / 2];
 #pragma unroll
-        for (int i = 0; i < WARPS * N / 4; ++i) q[i] = reinterpret_cast<const float4 *>(row)[i];
-    } else {
-        q[0] = make_float4(row[0], row[1], 0.f, 0.f);
-    }
+    for (int i = 0; i < WARPS / 2; ++i) q[i] = reinterpret_cast<const float4 *>(row)[i];
     const float *f = reinterpret_cast<const float *>(q);
 #pragma unroll
     for (int i = 0; i < N; ++i) a[i] = f[i];
 #pragma unroll
     for (int w = 1; w < WARPS; ++w)
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] += f[w * N + i];
+        for (int i = 0; i < N; ++i) a[i] += f[w * 2 + i];
 }
 
 template <int N>
@@ -54,13 +51,13 @@ __device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float
     }
     if (tpr > 32) {
         const int warps = tpr >> 5;
-        float *mine = buf[parity] + N * ((int)threadIdx.x >> 5);
+        float *mine = buf[parity] + 2 * ((int)threadIdx.x >> 5);
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) mine[i] = a[i];
         }
         asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
-        const float *row = buf[parity] + N * slot * warps;
+        const float *row = buf[parity] + 2 * slot * warps;
         if (warps == 2) {
             join_warps<N, 2>(a, row);
         } else if (warps == 4) {
@@ -72,7 +69,7 @@ __device__ __forceinline__ void row_sums(float (&a)[N], int tpr, int slot, float
             for (int i = 0; i < N; ++i) a[i] = row[i];
             for (int w = 1; w < warps; ++w) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) a[i] += row[w * N + i];
+                for (int i = 0; i < N; ++i) a[i] += row[w * 2 + i];
             }
         }
     }
@@ -85,11 +82,11 @@ __device__ __forceinline__ float row_most(float v, int tpr, int slot, float (*bu
         if (o < 8 || o < tpr) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (tpr > 32) {
         const int warps = tpr >> 5;
-        if ((threadIdx.x & 31) == 0) buf[parity][threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) buf[parity][2 * ((int)threadIdx.x >> 5)] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(tpr) : "memory");
-        const float *row = buf[parity] + slot * warps;
-        v = fmaxf(row[0], row[1]);
-        for (int w = 2; w < warps; ++w) v = fmaxf(v, row[w]);
+        const float *row = buf[parity] + 2 * slot * warps;
+        v = fmaxf(row[0], row[2]);
+        for (int w = 2; w < warps; ++w) v = fmaxf(v, row[2 * w]);
     }
     return v;
 }
@@ -149,6 +146,21 @@ struct Cover<V, CH, true> {
             }
     }
 };
+
+// Centres a thread's part of a row again (far_row), or leaves it where `far` is false.
+template <int V, int CH, bool SHIFT>
+__device__ __forceinline__ void recentre(float (&v)[V * CH], const Cover<V, CH, SHIFT> &cover, bool far, int C, int tpr, int slot,
+                                         float (*buf)[NORM_MAX_WARPS * 2], int parity) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V * CH / 2; ++i) sum = add2(get2(v, i), sum);
+    float off[1] = {sum.x + sum.y};
+    row_sums(off, tpr, slot, buf, parity);
+    const float2 mean = pair_of(far ? -off[0] / (float)C : 0.f);
+#pragma unroll
+    for (int i = 0; i < V * CH / 2; ++i) set2(v, i, add2(get2(v, i), mean));
+    cover.zero_rest(v);
+}
 
 // A ring of S rows of T tensors in shared memory, V vectors a thread, of which a thread
 // reads back only what it copied itself: no barrier, and a row's place takes the row S further
@@ -397,17 +409,28 @@ __global__ void __launch_bounds__(VEC_THREADS, vec_blocks<V, E>()) layer_vec_ker
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) sum = add2(get2(v, i), sum);
         float total[1] = {sum.x + sum.y};
-        row_sums<1>(total, tpr, slot, buf, parity);
+        row_sums(total, tpr, slot, buf, parity);
         parity ^= 1;
-        const float2 mean = pair_of(-total[0] * inv_c);
+        const float mean = total[0] * inv_c;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
+        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), pair_of(-mean)));
         cover.zero_rest(v);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
         total[0] = sq.x + sq.y;
-        row_sums<1>(total, tpr, slot, buf, parity);
+        row_sums(total, tpr, slot, buf, parity);
         parity ^= 1;
+        const bool far = far_row(mean, total[0] * inv_c);
+        if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+            recentre(v, cover, far, p.C, tpr, slot, buf, parity);
+            parity ^= 1;
+            sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) sq = fma2(get2(v, i), get2(v, i), sq);
+            total[0] = sq.x + sq.y;
+            row_sums(total, tpr, slot, buf, parity);
+            parity ^= 1;
+        }
         const float2 rho = pair_of(rsqrtf(total[0] * inv_c + p.eps));
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -499,7 +522,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
         ring.read(1, v);
         cover.zero_front(d);
         cover.zero_front(v);
-        float2 sum = make_float2(0.f, 0.f), sd = sum, sq = sum, dot = sum;
+        float2 sum = make_float2(0.f, 0.f), sd = sum, sq, dot;
         if (on) {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) set2(db, i, add2(get2(d, i), get2(db, i)));
@@ -514,23 +537,33 @@ __global__ void __launch_bounds__(TH, 512 / TH) layer_bwd_vec_kernel(const __gri
             }
         }
         float means[2] = {sum.x + sum.y, sd.x + sd.y};
-        row_sums<2>(means, tpr, slot, buf, 0);
-        const float2 mean = pair_of(-means[0] * inv_c);
+        row_sums(means, tpr, slot, buf, 0);
+        const float mean = means[0] * inv_c;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), mean));
+        for (int i = 0; i < N / 2; ++i) set2(v, i, add2(get2(v, i), pair_of(-mean)));
         cover.zero_rest(v);
+        float red[2];
+        auto squares = [&]() {
+            sq = dot = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
+            for (int j = 0; j < V; ++j) {
+                vec_param<CH>(g0 + (uint32_t)(j * (CH / 4)) * hop, hop, g);
 #pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-                const float2 w = get2(v + CH * j, i);
-                sq = fma2(w, w, sq);
-                dot = fma2(mul2(get2(d + CH * j, i), get2(g, i)), w, dot);
+                for (int i = 0; i < CH / 2; ++i) {
+                    const float2 w = get2(v + CH * j, i);
+                    sq = fma2(w, w, sq);
+                    dot = fma2(mul2(get2(d + CH * j, i), get2(g, i)), w, dot);
+                }
             }
+            red[0] = sq.x + sq.y, red[1] = dot.x + dot.y;
+            row_sums(red, tpr, slot, buf, 1);
+        };
+        squares();
+        const bool far = far_row(mean, red[0] * inv_c);
+        if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+            recentre(v, cover, far, p.C, tpr, slot, buf, 0);
+            squares();
         }
-        float red[2] = {sq.x + sq.y, dot.x + dot.y};
-        row_sums<2>(red, tpr, slot, buf, 1);
         const float rho = rsqrtf(red[0] * inv_c + p.eps);
         const float2 rho2 = pair_of(rho), k2 = pair_of(-row_slope(rho, red[1] * inv_c)), m2 = pair_of(-rho * (means[1] * inv_c));
         if (on) {

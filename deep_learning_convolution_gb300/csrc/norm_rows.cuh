@@ -149,6 +149,15 @@ struct E4m3Row {
 // FP32's range for rows of 1e-13 or 1e13.
 __device__ __forceinline__ float row_slope(float rho, float mean) { return rho * (rho * (rho * mean)); }
 
+// Whether a row lies so far from zero that its mean's rounding counts beside its deviations: its values
+// are then centred a second time, by the mean of the centred ones.  Up to eight deviations the mean's chain of up
+// to some 50 additions is at most 2.5e-5 of a deviation off.  A row of equal channels, whose deviations are
+// all rounding, is zeros after the second time: its centred values are the same few steps in every channel, so that
+// their sum and its quotient are exact.  Other rows pay for a comparison, a vote and a branch: nothing that
+// shows forward, 2 to 5 % backward, where a row's reductions are what it waits for (16384 x 2048 BF16 44.2 and
+// 46.4 us; with the second mean summed up for every row 47.4).
+__device__ __forceinline__ bool far_row(float mean, float variance) { return mean * mean > 64.f * variance; }
+
 // The remaining layouts, two passes over a row.  LANES (channels apart): 32
 // rows a block, one per lane, the channels dealt to eight warps, so neighbouring
 // rows share the loads.  Otherwise (a row too long for registers): one row a

@@ -687,8 +687,9 @@ dlcStatus_t dlcGetGatedBackwardWorkspaceSize(dlcHandle_t handle, dlcTensorDescri
  * from the unrounded total; the variance is the mean square about the mean.
  * beta (FLOAT, one per channel) may be NULL: zeros.  Types, E4M3 rows with their
  * scale, in-place total, NaN and FP32 range as for dlcRmsNormForward (the sum of
- * squares being that about the mean); a row of equal channels with epsilon 0 is
- * 0 / 0, NaN, in every type. */
+ * squares being that about the mean).  Rows far from zero are centred twice, so that
+ * a row of equal channels (up to 2^19 of them) is beta, whatever they are; with
+ * epsilon 0 it is 0 / 0, NaN, in every type. */
 dlcStatus_t dlcLayerNormForward(dlcHandle_t handle, double epsilon, dlcTensorDescriptor_t xDesc,
                                 const void *x, dlcTensorDescriptor_t residualDesc,
                                 const void *residual, const float *gamma, const float *beta,
