@@ -517,7 +517,8 @@ CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     // parts is the faster one, and the more exact one: an accumulator's additions truncate.  By parts
     // and fused, forward: 128 x 4096 -> 1000 11.1 and 15.4 us, 197 x 2992 -> 232 9.7 and 13.2 (losses 1.4e-7 and
     // 9e-7 off), 80 x 2044 -> 12 9.3 and 11.8, 2000 x 4000 -> 64 14.2 and 15.1, 512 x 4096 -> 2048 16.3 and 16.6; but 256
-    // x 2048 -> 1000 11.7 and 11.0, 700 x 2048 -> 300 11.6 and 11.1, 96 x 512 -> 512 7.8 and 7.3.
+    // x 2048 -> 1000 11.7 and 11.0, 700 x 2048 -> 300 11.6 and 11.1, 96 x 512 -> 512 7.8 and 7.3.  Products of the
+    // few-row kernel that are not in parts are neither: 3129 x 2784 -> 329 21.1 and 13.2, 622 x 2720 -> 1985 19.8 and 13.0.
     if (f.fused && p.V <= CE_SEGMENT && p.K >= (p.M <= 128 ? 1024 : 2560)) {
         f.piece = p.V;
         f.ld = (p.V + 3) / 4 * 4;

@@ -1408,7 +1408,8 @@ int dlc_entropy_parts(const dlcContext *ctx, const GemmProblem &g) { return 2 * 
 
 bool dlc_gemm_spread(const dlcContext *ctx, const GemmProblem &g) {
     const GemmPlan p = plan_gemm(ctx, g);
-    return p.gemv || p.few_rows || (p.splits > 1 && p.full_tiles == 0);
+    if (p.few_rows) return dlc_few_rows_plan(ctx, g).splits > 1;
+    return p.gemv || (p.splits > 1 && p.full_tiles == 0);
 }
 
 dlcKernel_t dlc_gemm_variant(const dlcContext *ctx, const GemmProblem &g) {
