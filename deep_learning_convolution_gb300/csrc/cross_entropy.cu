@@ -12,12 +12,24 @@
 //
 // Forward is one product whose epilogue leaves, for each row and 128 classes, (t, s) of its accumulators
 // (gp_entropy in gemm.cu), and a kernel that joins them.  Backward works the logits out again
-// in pieces of the classes, whose epilogue writes dz (BF16, at most 512 MB), and runs the two
-// products of a linear layer's gradient on each piece; dx adds up in FP32.  That is 8 M V K operations
-// for the step instead of the 6 M V K that keeping the logits would take.  The tensor core under the
-// power cap bounds it: 4096 x 2048 -> 131072 1.10 ms forward (2000 TFLOP/s) and 3.8 ms backward (1720; cuBLAS
-// in a loop: 1725).  Few rows keep FP32 logits of a piece in memory instead (fuse_fwd): 32 x 4096 -> 131072
-// 171 us, 6.3 TB/s of filters.
+// in pieces of the classes, whose epilogue writes dz, and runs the two products of a linear layer's gradient on
+// each piece; dx adds up in FP32.  That is 8 M V K operations for the step instead of the 6 M V K that keeping the
+// logits would take.  The tensor core under the power cap bounds it: 4096 x 2048 -> 131072 1.10 ms forward (2000
+// TFLOP/s) and 3.8 ms backward (1720; cuBLAS in a loop: 1725); E4M3 forward 0.57 ms (3855).  Few rows keep FP32
+// logits of a piece in memory instead (fuse_fwd): 32 x 4096 -> 131072 171 us, 6.3 TB/s of filters, E4M3 102 us
+// (5.3).
+//
+// dz is rounded to BF16 on its way into the two products, whose other operands are BF16: the tensor core takes both
+// of a product's in one type.  Roundings that are independent of one another leave dx and dw up to 0.0017 off in norm
+// beside FP64 (256 x 2048 -> 1000 at random 0.0009, since the targets' -1 is nearly exact), where BF16 outputs are
+// 0.0017 off by themselves and a training step's come to 0.0024.  A second BF16 term of dz would take that away for
+// another 4 M V K operations, a step of 4096 x 2048 -> 131072 about 7.2 ms instead of 4.9.  dbias sums the values
+// before the rounding.
+//
+// Workspace: a piece's dz takes 512 MB, but never less than 256 classes do (above 2^20 rows 512 bytes a row), and its column
+// sums a 16th of that; the forward call's parts 256 MB, but never less than 1024 classes do (up to 32 of them: 256 bytes
+// a row); few rows' logits 512 MB.  Beside them the FP32 sum of a BF16 dx in several pieces, and copies of operands that
+// TMA cannot load.
 #include <cmath>
 
 #include "channel.cuh"
@@ -342,11 +354,11 @@ dlcStatus_t launch_outer(dlcContext *ctx, const CrossEntropyProblem &p, const un
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Logits (or dz) of a piece take at most about this much workspace.  Backward passes of 4096 x
+// Logits (or dz) of a piece take at most about this much workspace, as far as 256 classes fit.  Backward passes of 4096 x
 // 2048 -> 131072 / 8192 x 512 -> 65536 in pieces of 128 MB: 4022 / 1533 us, 256 MB 3913 / 1345,
 // 512 MB 3836 / 1230, 1 GB 3893 / 1097: what a piece costs is dx's last wave and its FP32 sum.
 constexpr size_t CE_PIECE_BYTES = (size_t)512 << 20;
-constexpr size_t CE_PART_BYTES = (size_t)256 << 20;  // the same for the parts of fused products
+constexpr size_t CE_PART_BYTES = (size_t)256 << 20;  // the same for the parts of fused products (1024 classes)
 
 // Classes of a piece of `bytes`-sized elements a row and class.
 int piece_of(const CrossEntropyProblem &p, int bytes) {

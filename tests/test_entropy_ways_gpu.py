@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from deep_learning_convolution_gb300 import api
+from deep_learning_convolution_gb300 import binding as B
 from tests import train_ref as ref
 from tests.test_channel_ops_gpu import BF, F8, F32, laid_out, out_like, rand
 from tests.test_train_ops_gpu import check_entropy, classes_of, close, d, entropy_case
@@ -139,3 +140,25 @@ def test_e4m3_of_masked_classes(handle, rows, c, v):
     b = torch.where(torch.arange(v, device="cuda") % 4 == 0, 0.0, float("-inf"))
     op(zero, qw, target, loss, lse, bias=b, x_scale=sx, w_scale=sw)
     close(lse, torch.full_like(lse, math.log((v + 3) // 4)).double(), torch.tensor(1e-5, device="cuda"), "lse")
+
+
+@pytest.mark.parametrize("rows", [17, 33, 1000, 2 ** 17, 2 ** 20, 2 ** 25])
+@pytest.mark.parametrize("v", [10, 1000, 131072])
+def test_workspace_is_what_the_pieces_take(handle, rows, v):
+    """Pieces of 512 MB of dz or logits, 256 MB of parts, and never less than 256 and 1024 classes."""
+    c, mb = 64, 1 << 20
+    x, w = B.dlcCreateTensorDescriptor(), B.dlcCreateFilterDescriptor()
+    try:
+        B.dlcSetTensor4dDescriptorEx(x, B.DLC_DATA_BFLOAT16, rows, c, 1, 1, c, 1, 0, 0)
+        B.dlcSetFilter4dDescriptor(w, B.DLC_DATA_BFLOAT16, B.DLC_TENSOR_NCHW, v, c, 1, 1)
+        forward, backward = (f(handle.h, x, 0, w, 0) for f in (B.dlcGetCrossEntropyForwardWorkspaceSize, B.dlcGetCrossEntropyBackwardWorkspaceSize))
+    finally:
+        B.dlcDestroyTensorDescriptor(x)
+        B.dlcDestroyFilterDescriptor(w)
+    # split products' partial sums: a tile of 256 x 256 for each pair of SMs; 64 rows at most keep logits
+    products = 76 * 256 * 256 * 4 + mb
+    parts = max(256 * mb, 33 * 8 * rows)
+    logits = min(512 * mb, 4 * rows * (v + 3)) if rows <= 64 else 0
+    assert forward <= parts + logits + 4 * rows + products
+    dz = min(max(512 * mb, 512 * rows), 2 * rows * (v + 7))
+    assert backward <= dz + dz // 16 + 128 * (v + 7) + 1024 * v + 4 * rows * c + products
