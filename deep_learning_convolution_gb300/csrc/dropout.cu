@@ -10,8 +10,10 @@
 // random numbers: as easy as 1, 2, 3" (2011): a round multiplies two of the four words and
 // crosses the halves of the products.
 //
-// x (and r) in, y out: memory bounds it with a residual, the generator's multiplies without.  16384 x 4096
-// BF16 63.8 us with residual (6.3 TB/s) and 57 us without (4.7); unaligned rows, 16384 x 1001 with
+// x (and r) in, y out: memory bounds it with a residual, the generator close behind.  Without, no single thing does: DRAM
+// 49 %, issue 55 %, integer pipe 55 %, the busiest pipe 66 % of their rates, and the five warps a scheduler has wait in
+// about equal parts for loads, for the round before and for the multiplies.  16384 x 4096 BF16 63.8 us with
+// residual (6.3 TB/s) and 57 us without (4.7); unaligned rows, 16384 x 1001 with
 // residual, 27 us; channels apart, 128 images of 512 x 28 x 28, 172 us (1.2 TB/s).
 #include "channel.cuh"
 #include "ptx.cuh"
@@ -145,8 +147,9 @@ __device__ __forceinline__ void put(const RowTensor &t, long long off, int n, co
 
 // Contiguous channels, rows at one pitch: a thread keeps its W channels and steps from row to row, so
 // what the generator owes to the channel is worked out once; U rows are in flight.  W = 8: aligned whole
-// vectors; W = 4: single elements.  What bounds it is the generator: 31 wide multiplies for eight channels
-// (37 without this), a warp's at four cycles each, and some 80 other integer instructions.
+// vectors; W = 4: single elements.  The generator takes 31 wide multiplies for eight channels
+// (37 without this), a warp's at four cycles each, and some 80 other integer instructions: about half of the time of a
+// call without residual each.
 template <int W, typename X, typename R, typename Y>
 __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_columns_kernel(const __grid_constant__ DoParams p) {
     griddep_launch_dependents();

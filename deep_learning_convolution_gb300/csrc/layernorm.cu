@@ -9,13 +9,13 @@
 //
 // The squares are summed about the row's own mean, in a second reduction over registers: the
 // difference of the mean square and the squared mean would lose what a large mean (or
-// one large channel) leaves of the small ones.  Rows in the usual layouts are
+// one large channel) leaves of the small ones.  Rows far from zero are centred twice (far_row).  Rows in the usual layouts are
 // layernorm_vec.cu's and layernorm_shift.cu's; here are the others: mixed types, and unaligned rows where that is
 // faster, with the rows' way through registers that the RMS norm has (rmsnorm.cu), channels apart and long rows
 // read again for each step.  Instructions and latency bound them, measured back to back: 16384 x 1001 FP32
-// unaligned with residual and sum 45 us (5.8 TB/s), backward 56 us; an FP32 stream beside BF16
-// branches, 100352 x 512, 138 us, backward 228 us; channels apart, 128 images of 512 x 28 x 28 BF16, 265
-// us, backward 632 us; 2730 x 12288 FP32 223 us, backward 396 us.
+// unaligned with residual and sum 46 us (5.7 TB/s), backward 58 us; an FP32 stream beside BF16
+// branches, 100352 x 512, 140 us, backward 228 us; channels apart, 128 images of 512 x 28 x 28 BF16, 262
+// us, backward 641 us; 2730 x 12288 FP32 238 us, backward 392 us.
 #include "norm_rows.cuh"
 
 namespace {

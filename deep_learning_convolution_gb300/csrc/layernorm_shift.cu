@@ -69,7 +69,11 @@ bool dlc_layer_bwd_shift(dlcContext *ctx, const LayerBwdProblem &pb, dlcStatus_t
     const bool fp32 = p.t.dt == DLC_DATA_FLOAT;
     const VecPlan v = plan_vec(p.rows, p.C, fp32, fp32 ? 4 : 2, true, true, ctx->sm_count);
     if (!v.v || !pays(v, plan_rows(p.rows, p.C, true, false, true, 1, ctx->sm_count), fp32 ? 4 : 8, p.C, fp32 ? 0.97 : 1.55)) return false;
-    if (4 * p.rows < p.C) return false;  // (a block's start and its sums: 300 x 2001 BF16 10.2 us, 7.3 otherwise; 500 x 513 7.3 and 7.7)
+    // A block's start and its sums cost more than its rows gain: by vectors and by single elements 300 x 2001 BF16 10.2 and
+    // 7.3 us, 190 x 1113 BF16 8.0 and 6.7, 198 x 1383 FP32 8.3 and 7.0; but 864 x 1447 BF16 10.3 and 9.9, 904 x 2781 FP32
+    // 15.9 and 17.6, 2403 x 1957 BF16 14.7 and 19.7.  Over 40 sizes of 0.03 to 2 rows a channel, 200 to 4000 channels, the
+    // border at a fourth is 1 % slower than the faster way on average and 7 % at most.
+    if (4 * p.rows < p.C) return false;
     int blocks = 0;
     status = launch_vec(ctx, vec_bwd<true>(v, fp32, p.dt.p != nullptr), p, v, fp32, true, 1, 0, &blocks);
     if (status == DLC_STATUS_SUCCESS && (p.dgamma || p.dbeta))

@@ -11,9 +11,9 @@
 // vectors of four channels: with eight, neighbouring threads touched every other 16 bytes (8192 x 2048
 // FP32 67 us, 48 this way).
 //
-// Measured back to back, with residual and sum: 65536 x 768 BF16 to E4M3 60.3 us (5.8 TB/s), 16384 x
-// 2048 BF16 48.8 us (5.5), 8192 x 2048 FP32 48 us (5.6); backward with both sums 16384 x 2048 BF16 49.3
-// us (5.4), 8192 x 2048 FP32 50 us (5.4).  A call's start and end are 7 to 10 us of it: rows beyond these
+// Measured back to back, with residual and sum: 65536 x 768 BF16 to E4M3 61.3 us (5.7 TB/s), 16384 x
+// 2048 BF16 48.8 us (5.5), 8192 x 2048 FP32 48 us (5.6); backward with both sums 16384 x 2048 BF16 50.5
+// us (5.3), 8192 x 2048 FP32 50 us (5.4).  A call's start and end are 7 to 10 us of it: rows beyond these
 // come at 6.4 TB/s.
 #pragma once
 
