@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// What rounding to BF16 leaves of v (nothing of an infinity).
+__device__ __forceinline__ float bf16_rest(float v) {
+    const float r = bf16_bits_f32(pack_bf16(v, 0.f) & 0xffffu);
+    return isinf(r) ? 0.f : v - r;
+}
+
 // Two FP32 values rounded to nearest even into E4M3, saturating at +-448 (NaN stays NaN).
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

@@ -19,12 +19,13 @@
 // logits of a piece in memory instead (fuse_fwd): 32 x 4096 -> 131072 171 us, 6.3 TB/s of filters, E4M3 102 us
 // (5.3).
 //
-// dz is rounded to BF16 on its way into the two products, whose other operands are BF16: the tensor core takes both
-// of a product's in one type.  Roundings that are independent of one another leave dx and dw up to 0.0017 off in norm
-// beside FP64 (256 x 2048 -> 1000 at random 0.0009, since the targets' -1 is nearly exact), where BF16 outputs are
-// 0.0017 off by themselves and a training step's come to 0.0024.  A second BF16 term of dz would take that away for
-// another 4 M V K operations, a step of 4096 x 2048 -> 131072 about 7.2 ms instead of 4.9.  dbias sums the values
-// before the rounding.
+// dz enters the two products in BF16, as their other operands do: the tensor core takes both of a product's in one
+// type.  One term of it, rounded once, leaves dx and dw up to 0.0017 off in norm beside FP64 whatever type they are
+// kept in, more where a few rows or classes are most of it; BF16 outputs are 0.0017 off by themselves, and a
+// training step's come to 0.0024.  A second term, what the rounding left, keeps 16 bits and costs the products
+// twice their operations; it is taken where that is little of a call (terms_of), and is not for long products that
+// the tensor core bounds (4096 x 2048 -> 131072 4.9 ms a step, some 7.2 with it).  dbias sums the values before any
+// rounding.
 //
 // Workspace: a piece's dz takes 512 MB, but never less than 256 classes do (above 2^20 rows 512 bytes a row), and its column
 // sums a 16th of that; the forward call's parts 256 MB, but never less than 1024 classes do (up to 32 of them: 256 bytes
@@ -78,8 +79,9 @@ struct CeParams {
     float *chosen;             // [M] the target's logit
     float *loss, *lse;
     const float *dloss;
-    unsigned short *dz;        // [M][ldz]
+    unsigned short *dz;        // [terms][M][ldz]
     long long ldz;
+    int terms;
     float *sums;               // [strip][cols] or null
     int *err;
 };
@@ -206,6 +208,9 @@ __global__ void __launch_bounds__(CE_THREADS) ce_dz_kernel(const __grid_constant
         }
         unsigned short *dst = p.dz + m * p.ldz + c;  // (rows are padded to whole vectors)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        if (p.terms == 2)
+            *reinterpret_cast<uint2 *>(dst + p.M * p.ldz) =
+                make_uint2(pack_bf16(bf16_rest(v[0]), bf16_rest(v[1])), pack_bf16(bf16_rest(v[2]), bf16_rest(v[3])));
     }
     if (p.sums) {
 #pragma unroll
@@ -237,19 +242,39 @@ __global__ void __launch_bounds__(1024) ce_strips_kernel(const float *sums, floa
     }
 }
 
+// dx of the sums of dz's two terms: dx[m, c] = sum[m][c] + sum[M + m][c], four channels a thread.
+struct CeTermsParams {
+    const float *sum;          // [2 M][ld], rows of whole vectors
+    long long M, ld, items;
+    int C, pieces, vec;
+    RowTensor dx;
+};
+
+__global__ void __launch_bounds__(CE_THREADS) ce_terms_kernel(const __grid_constant__ CeTermsParams p) {
+    griddep_launch_dependents();
+    const long long i = (long long)blockIdx.x * CE_THREADS + threadIdx.x;
+    griddep_wait();
+    if (i >= p.items) return;
+    const long long m = i / p.pieces;
+    const int c = 4 * (int)(i - m * p.pieces);
+    const float4 a = *reinterpret_cast<const float4 *>(p.sum + m * p.ld + c), b = *reinterpret_cast<const float4 *>(p.sum + (p.M + m) * p.ld + c);
+    const float v[4] = {a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w};
+    store4(p.dx, row_off(p.dx.m, m), c, p.C - c, p.vec != 0, v);
+}
+
 // ---- dw of a few rows -------------------------------------------------------------------
 //
-// dw[k, c] = sum_m dz[m, k] x[m, c] for up to 16 rows: little but writing dw, which the tiles of a general
+// dw[k, c] = sum_m dz[m, k] x[m, c] for up to 16 rows, dz in two terms: little but writing dw, which the tiles of a general
 // product do at 3.5 TB/s (their epilogues have one step of the product to hide behind).  A warp keeps 64
 // channels of x in registers as the B operands of one step of mma.sync, and takes 16 classes of dz at a time; the
-// columns of the four tiles are dealt so that a thread is left with eight neighbouring channels.  Steps, in
-// tiles and this way: 1 x 1024 -> 131072 252 and 217 us, 8 x 1024 -> 50000 132 and 120, 16 x 2048 -> 50304 204
-// and 197; two steps of it for 32 x 4096 -> 131072 850 and 1055.
+// columns of the four tiles are dealt so that a thread is left with eight neighbouring channels.  Training steps, in
+// tiles and this way, with one term: 1 x 1024 -> 131072 252 and 217 us, 8 x 1024 -> 50000 132 and 120, 16 x 2048 -> 50304
+// 204 and 197; two steps of it for 32 x 4096 -> 131072 850 and 1055.  With two terms 221, 124 and 198.
 
 constexpr int CO_THREADS = 256, CO_ROWS = 16;
 
 struct CeOuterParams {
-    const unsigned short *dz;  // [M][ldz]
+    const unsigned short *dz;  // [2][M][ldz]
     long long ldz;
     RowTensor x;
     void *dw;                  // [cols][C]
@@ -285,20 +310,23 @@ __global__ void __launch_bounds__(CO_THREADS, 3) ce_outer_kernel(const __grid_co
                 b[h][j][r] = lo | hi << 16;
             }
     }
-    uint32_t a[4], next[4];
+    uint32_t a[2][4], next[2][4];
     auto load = [&](int tile) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = tile * 16 + g + 8 * (i & 1), m = 8 * (i >> 1) + 2 * q;
-            const uint32_t lo = v < p.cols && m < p.M ? p.dz[m * p.ldz + v] : 0u, hi = v < p.cols && m + 1 < p.M ? p.dz[(m + 1) * p.ldz + v] : 0u;
-            next[i] = lo | hi << 16;
-        }
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = tile * 16 + g + 8 * (i & 1), m = 8 * (i >> 1) + 2 * q;
+                const unsigned short *dz = p.dz + (t * p.M + m) * p.ldz + v;
+                const uint32_t lo = v < p.cols && m < p.M ? dz[0] : 0u, hi = v < p.cols && m + 1 < p.M ? dz[p.ldz] : 0u;
+                next[t][i] = lo | hi << 16;
+            }
     };
     int tile = (int)blockIdx.y * per + warp / p.warps;
     if (tile < tiles) load(tile);
     for (; tile < tiles; tile += step) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = next[i];
+        for (int i = 0; i < 4; ++i) a[0][i] = next[0][i], a[1][i] = next[1][i];
         if (tile + step < tiles) load(tile + step);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -306,7 +334,8 @@ __global__ void __launch_bounds__(CO_THREADS, 3) ce_outer_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-                mma_16816(d[j], a, b[h][j][0], b[h][j][1]);
+                mma_16816(d[j], a[0], b[h][j][0], b[h][j][1]);
+                mma_16816(d[j], a[1], b[h][j][0], b[h][j][1]);
             }
             const int c = c0 + 32 * h + 8 * q;  // (rows are whole vectors)
             if (c >= p.C) continue;
@@ -350,6 +379,20 @@ dlcStatus_t launch_outer(dlcContext *ctx, const CrossEntropyProblem &p, const un
     const void *kern = bf ? (const void *)ce_outer_kernel<unsigned short> : (const void *)ce_outer_kernel<float>;
     void *args[] = {&o};
     return dlc_launch(ctx, kern, dim3((unsigned)gx, (unsigned)gy), dim3(CO_THREADS), 0, args);
+}
+
+dlcStatus_t launch_terms(dlcContext *ctx, const CrossEntropyProblem &p, const RowTensor &sum) {
+    CeTermsParams t;
+    t.sum = static_cast<const float *>(sum.p);
+    t.M = p.M;
+    t.ld = sum.m.ld;
+    t.C = p.K;
+    t.pieces = (p.K + 3) / 4;
+    t.items = p.M * t.pieces;
+    t.dx = p.dx;
+    t.vec = dlc_vec4_rows(p.dx);
+    void *args[] = {&t};
+    return dlc_launch(ctx, (const void *)ce_terms_kernel, dim3((unsigned)((t.items + CE_THREADS - 1) / CE_THREADS)), dim3(CE_THREADS), 0, args);
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -396,12 +439,14 @@ struct CePlan {
     bool fused = false;        // the product's epilogue takes the logits from the accumulators
     int piece = 0, parts = 0;
     long long ld = 0, ldz = 0;
+    int terms = 1;             // BF16 terms of dz
+    bool stacked = false;      // ... whose products with w are rows of one product, added up at the end
     bool x_packed = false, w_packed = false;
     void *x_copy = nullptr, *w_copy = nullptr;
     float *z = nullptr, *chosen = nullptr, *sums = nullptr, *few_sums = nullptr;
     float2 *part = nullptr;
     unsigned short *dz = nullptr;
-    RowTensor dx_sum;          // FP32, where several pieces add to a dx of another type
+    RowTensor dx_sum;          // FP32, where several pieces add to a dx of another type, or two terms' rows (stacked)
     char *gemm_ws = nullptr;
     size_t bytes = 0;
     char *base;
@@ -451,14 +496,15 @@ struct CePlan {
     // dx (+)= dz w of a piece; the pieces before it have left their sum in dx_sum or dx
     GemmProblem data(const CrossEntropyProblem &p, int n0, int cols) const {
         GemmProblem g;
-        g.M = p.M;
+        g.M = stacked ? 2 * p.M : p.M;
         g.N = p.K;
         g.K = cols;
+        g.terms = stacked ? 1 : terms;
         g.a.t = dense(dz, DLC_DATA_BFLOAT16, ldz);
         g.b.t = w(p, n0, cols);
         g.b.trans = 1;
         const RowTensor sum = dx_sum.p ? dx_sum : p.dx;
-        g.y = n0 + cols == p.V ? p.dx : sum;
+        g.y = n0 + cols == p.V && !stacked ? p.dx : sum;
         if (n0) g.r = sum;
         g.ws = gemm_ws;
         return g;
@@ -469,6 +515,7 @@ struct CePlan {
         g.M = cols;
         g.N = p.K;
         g.K = p.M;
+        g.terms = terms;
         g.a.t = dense(dz, DLC_DATA_BFLOAT16, ldz);
         g.a.trans = 1;
         g.b.t = x(p);
@@ -494,6 +541,7 @@ struct CePlan {
         e.lse = p.lse;
         e.dloss = p.dloss;
         e.sums = sums;
+        e.terms = terms;
         return g;
     }
     // fn(first class, how many) of every piece
@@ -517,8 +565,8 @@ struct CePlan {
 // 200 and 185; more rows far apart (4096 x 2048 -> 131072 1793 and 1084 us).  Up to a segment of
 // classes the rows' sums are one kernel, which moves the point: 2048 -> 1000 32 rows 7.6 and 10.2 us, 64
 // rows 8.4 and 10.4, 192 rows 10.2 and 10.4; 1024 -> 4096 48 rows 8.8 and 10.1, 64 rows 8.7 and 8.2.
-// Backward: 8 rows 676 and 702, 16 rows 678 and 681, 32 rows 687 and 684; 2048 -> 1000: 4 rows 23.8 and
-// 25.0, 16 rows 24.8 and 24.6, 64 rows 26.8 and 24.7.
+// Backward, with one term of dz: 8 rows 676 and 702, 16 rows 678 and 681, 32 rows 687 and 684; 2048 -> 1000: 4 rows 23.8
+// and 25.0, 16 rows 24.8 and 24.6, 64 rows 26.8 and 24.7.
 bool fuse_fwd(const CrossEntropyProblem &p) { return p.M > (p.V <= CE_SEGMENT ? 64 : 32); }
 bool fuse_bwd(const CrossEntropyProblem &p) { return p.M > 16; }
 
@@ -562,20 +610,39 @@ CePlan plan_fwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     return f;
 }
 
+// How many BF16 terms of dz enter the products (see the top).  Two up to 128 rows, where the terms are rows of one
+// tile of the product with w, added up at the end (stack_terms), and the product with x is little but writing dw; and up to
+// 2^30 products of a row, class and channel, where the products are read twice as long but the call is mostly
+// launches.  Backward passes with one term and two: 1 x 1024 -> 131072 181 and 186 us, 16 x 2048 -> 50304 160 and 161,
+// 32 x 4096 -> 131072 685 and 701, 128 x 4096 -> 131072 708 and 748, 128 x 64 -> 131072 99 and 118; 256 x 2048 -> 1000 26.2
+// and 31.4, 4096 x 256 -> 1000 34.5 and 41.3.
+constexpr int CE_STACK = 128;
+
+int terms_of(const CrossEntropyProblem &p) {
+    return p.M <= CE_STACK || (p.M <= 1 << 20 && (double)p.M * p.V * p.K <= 1073741824.0) ? 2 : 1;
+}
+
+// (The sum of the terms' rows is a launch: small products are rather read twice as long.  Stacked and not: 16 x 2048 ->
+// 1000 25.4 and 27.4 us, 8 x 1024 -> 50000 102 and 118, 64 x 128 -> 32768 45.8 and 50.7; 32 x 128 -> 100 19.7 and 17.9,
+// 64 x 512 -> 1000 25.1 and 22.5.)
+bool stack_terms(const CrossEntropyProblem &p) { return p.M <= CE_STACK && (long long)p.V * p.K > 1 << 19; }
+
 CePlan plan_bwd(const dlcContext *ctx, const CrossEntropyProblem &p, char *ws) {
     CePlan b(ws);
     b.fused = fuse_bwd(p);
-    b.piece = piece_of(p, b.fused ? 2 : 4);
+    b.terms = terms_of(p);
+    b.stacked = stack_terms(p);
+    b.piece = piece_of(p, b.fused ? 2 * b.terms : 4);
     b.ldz = (b.piece + 7) / 8 * 8;
     b.operands(p);
     if (!b.fused) {
         b.ld = (b.piece + 3) / 4 * 4;
         b.z = static_cast<float *>(b.take((size_t)p.M * b.ld * 4));
     }
-    b.dz = static_cast<unsigned short *>(b.take((size_t)p.M * b.ldz * 2));
-    if (p.dx.p && b.piece < p.V && p.dx.dt != DLC_DATA_FLOAT) {
+    b.dz = static_cast<unsigned short *>(b.take((size_t)b.terms * p.M * b.ldz * 2));
+    if (p.dx.p && (b.stacked || (b.piece < p.V && p.dx.dt != DLC_DATA_FLOAT))) {
         const long long ld = ((long long)p.K + 3) / 4 * 4;
-        b.dx_sum = dense(b.take((size_t)p.M * ld * 4), DLC_DATA_FLOAT, ld);
+        b.dx_sum = dense(b.take((size_t)(b.stacked ? 2 : 1) * p.M * ld * 4), DLC_DATA_FLOAT, ld);
     }
     size_t most = 0, sums = 0;
     b.each(p, [&](int n0, int cols) {
@@ -607,6 +674,7 @@ CeParams params(const dlcContext *ctx, const CrossEntropyProblem &p, const CePla
     c.dloss = p.dloss;
     c.dz = f.dz;
     c.ldz = f.ldz;
+    c.terms = f.terms;
     c.sums = f.sums;
     c.err = ctx->d_err;
     return c;
@@ -672,6 +740,7 @@ dlcStatus_t dlc_launch_cross_entropy_bwd(dlcContext *ctx, const CrossEntropyProb
             if (s == DLC_STATUS_SUCCESS) s = dlc_launch_column_sum(ctx, many ? to : from, p.dbias + n0, cols, many ? CE_STRIPS : rows);
         }
         if (s == DLC_STATUS_SUCCESS && p.dx.p) s = dlc_launch_gemm(ctx, b.data(p, n0, cols));
+        if (s == DLC_STATUS_SUCCESS && p.dx.p && b.stacked && n0 + cols == p.V) s = launch_terms(ctx, p, b.dx_sum);
         if (s == DLC_STATUS_SUCCESS && p.dw.p)
             s = outer_ok(p) ? launch_outer(ctx, p, b.dz, b.ldz, n0, cols) : dlc_launch_gemm(ctx, b.filters(p, n0, cols));
         return s;

@@ -68,6 +68,7 @@ struct GpParams {
     int N, act;
     int BN, nout;                 // accumulator columns of a tile, outputs of a tile (gated: BN / 2)
     int stages, num_kb;
+    int terms, term_rows;         // 2: an odd k-block is the one before it again, of rows of a that lie so many further on
     GpTiles tiles;
     int units;
     int full_tiles, splits;       // tiles from full_tiles on: `splits` units each, FP32 partial sums, no epilogue
@@ -142,11 +143,12 @@ __device__ void gp_produce(const GpParams &p, uint32_t rank, const CUtensorMap *
             if (!mbar_wait(&empty[stage], ph ^ 1u, ctl, 21)) return;
             if (IS_A && rank == 0) mbar_arrive_expect_tx(&full[stage], tx);
             const uint32_t dst = smem + (uint32_t)stage * bytes, bar = full0 + 8u * (uint32_t)stage;
+            const int k = (p.terms == 2 ? kb >> 1 : kb) * BK, on = IS_A && p.terms == 2 && (kb & 1) ? p.term_rows : 0;
             if (MN) {
                 const int atoms = IS_A ? 2 : p.b_atoms;
-                for (int a = 0; a < atoms; ++a) tma_load_2d_pair(dst + (uint32_t)a * GP_ATOM, tm, bar, i0 + 64 * a, kb * BK);
+                for (int a = 0; a < atoms; ++a) tma_load_2d_pair(dst + (uint32_t)a * GP_ATOM, tm, bar, i0 + 64 * a, k + on);
             } else {
-                tma_load_2d_pair(dst, tm, bar, kb * BK, i0);
+                tma_load_2d_pair(dst, tm, bar, k, i0 + on);
             }
             if (++stage == p.stages) stage = 0, ph ^= 1u;
         }
@@ -639,12 +641,12 @@ __device__ __forceinline__ float gp_column_sum(const float (&v)[32]) {
 // accumulator's row is a thread's own, so a row's part of the sum needs no exchange:
 //   ENTROPY_PARTS  the largest logit t of this thread's columns and s = sum exp(z - t), and the
 //                  target's logit where it is one of them
-//   ENTROPY_DZ     dz in BF16 through bulk stores, and its sums over the warp's 32 rows
+//   ENTROPY_DZ     dz in one or two BF16 terms through bulk stores, and its sums over the warp's 32 rows
 // An exponential and three paired operations a logit: 2048 x 2048 -> 32768 keeps the tensor pipe busy for
 // 95 % of the active cycles with PARTS and 93 % with DZ.
 template <int MODE>
 __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty,
-                                           uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const WaitCtl &ctl) {
+                                           uint32_t epi_smem, float *columns, const CUtensorMap *tmY, const CUtensorMap *tmLow, const WaitCtl &ctl) {
     const EntropyTile &e = p.entropy;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - GP_EPI_WARP0) >> 2;
@@ -751,6 +753,11 @@ __device__ __forceinline__ void gp_entropy(const GpParams &p, uint32_t rank, uin
                     if (st.row0 < p.M && lane < cols) e.sums[(st.row0 >> 5) * p.N + n + lane] = s;
                 }
                 st.tma(tmY, true, v, n, 0);
+                if (e.terms == 2) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = bf16_rest(v[i]);
+                    st.tma(tmLow, true, v, n, 0);
+                }
             }
         }
         if (MODE == ENTROPY_PARTS && valid) e.part[((long long)e.part0 + 2 * w.nt + part) * p.M + m] = make_float2(t, sum.x + sum.y);
@@ -825,7 +832,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             gp_mma<E4M3, A_MN, B_MN>(p, tmem_base, sA, sB, full, empty, tfull, tempty, mma_done, ctl);
     } else {
         if constexpr (ENTROPY != ENTROPY_NONE)
-            gp_entropy<ENTROPY>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, ctl);
+            gp_entropy<ENTROPY>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, ctl);
         // (the activation's branch out here: a block's code is straight)
         else act_dispatch(p.act, [&](auto act) {
             gp_epilogue<GATED, ROWS, decltype(act)::value>(p, rank, tmem_base, tfull, tempty, smem_u32(epi), columns, &tmY, &tmZ, &tmP, ctl);
@@ -1111,16 +1118,16 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     const int nb = g.gated ? 2 * g.N : g.N;
     const bool e4m3 = g.a.t.dt == DLC_DATA_FLOAT8_E4M3;
     const int bk = e4m3 ? GP_LINE : GP_LINE / 2;
-    p.a_rows = g.a.trans ? g.K : g.M;
+    p.a_rows = g.terms * (g.a.trans ? g.K : g.M);
     p.a_ch = (int)(g.a.trans ? g.M : g.K);
     p.b_rows = g.b.trans ? g.K : nb;
     p.b_ch = (int)(g.b.trans ? nb : g.K);
     const bool entropy = g.entropy.mode != ENTROPY_NONE;  // whole tiles on the pair kernel
-    p.gemv = !entropy && dlc_gemv_ok(g);
+    p.gemv = !entropy && g.terms == 1 && dlc_gemv_ok(g);
     if (p.gemv) return p;  // operands as they are, one launch
     p.pack_a = !tma_rows(g.a.t, p.a_rows, p.a_ch);
     p.pack_b = !tma_rows(g.b.t, p.b_rows, p.b_ch);
-    p.num_kb = (int)((g.K + bk - 1) / bk);
+    p.num_kb = g.terms * (int)((g.K + bk - 1) / bk);
     p.m_tiles = (int)((g.M + 2 * GP_ROWS - 1) / (2 * GP_ROWS));
     // Tile width, split of the tail, and which of the two kernels, from a model of
     // the time in microseconds, fitted to 27 shapes from 128 x 1024 -> 512 to
@@ -1160,7 +1167,7 @@ GemmPlan plan_gemm(const dlcContext *ctx, const GemmProblem &g) {
     // 114 with FP32 outputs 12.6 and 9.4).
     p.nout = g.gated ? p.bn / 2 : p.bn;
     p.n_tiles = (g.N + p.nout - 1) / p.nout;
-    if (!g.a.trans && !g.b.trans && !entropy) {
+    if (!g.a.trans && !g.b.trans && !entropy && g.terms == 1) {
         const double waves = std::ceil((double)p.m_tiles * p.n_tiles / pairs);
         const double rows = tma_store_rows(g.y, g.M, g.N, 1) ? 0. : 4.0 * p.bn / 256 * waves;
         p.few_rows = g.M <= 64 || dlc_few_rows_plan(ctx, g).us < best + rows;
@@ -1283,6 +1290,8 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.BN = pl.bn;
     p.nout = pl.nout;
     p.num_kb = pl.num_kb;
+    p.terms = g.terms;
+    p.term_rows = (int)(pl.a_rows / g.terms);
     p.tiles = tiles_of(pl);
     if ((long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL) return DLC_STATUS_NOT_SUPPORTED;
     const int tail = pl.m_tiles * pl.n_tiles - pl.full_tiles;
@@ -1324,6 +1333,11 @@ dlcStatus_t launch_pair(dlcContext *ctx, const GemmProblem &g, const GemmPlan &p
     p.z_unit = store_unit(g.z, g.gated ? g.N : 0);
     if (p.y_tma && !encode_output(ctx, &ty, g.y, g.M, y_cols, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
     if (p.z_tma && !encode_output(ctx, &tz, g.z, g.M, g.N, g.gated ? 2 : 1, g.N)) return DLC_STATUS_EXECUTION_FAILED;
+    if (mode == ENTROPY_DZ && g.entropy.terms == 2) {  // (a map of its own: rows behind M are not written)
+        RowTensor low = g.y;
+        low.p = static_cast<char *>(g.y.p) + (size_t)g.M * g.y.m.ld * 2;
+        if (!encode_output(ctx, &tz, low, g.M, y_cols, 1, 0)) return DLC_STATUS_EXECUTION_FAILED;
+    }
     if (tail) {
         RowTensor part;
         part.p = g.ws + pl.part_off;

@@ -343,6 +343,7 @@ struct EntropyTile {
     float *chosen = nullptr;     // PARTS: [M] the target's logit
     const float *lse = nullptr, *dloss = nullptr;  // DZ; dz goes to y: BF16, rows padded to 16 bytes
     float *sums = nullptr;       // DZ: [M / 32][N] sums of dz over 32 rows, or null
+    int terms = 1;               // DZ: 2 writes what y's rounding left, in M more rows
 };
 
 // y[m, n] = act(sa[m] sb[n] sum_k a(m, k) b(n, k) + bias[n]) + r[m, n], and
@@ -355,6 +356,7 @@ struct GemmProblem {
     const float *sa = nullptr, *sb = nullptr, *bias = nullptr;
     RowTensor z, r, y;
     EntropyTile entropy;
+    int terms = 1;       // 2 (pair kernel): a is the sum of two operands, the second one's rows behind the first one's
     char *ws = nullptr;  // dlc_gemm_workspace bytes
 };
 

@@ -780,7 +780,9 @@ dlcStatus_t dlcGetCrossEntropyForwardWorkspaceSize(dlcHandle_t handle, dlcTensor
  *   dz[m, k] = dloss[m] * (exp(z[m, k] - lse[m]) - (k == target[m]))
  *   dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz
  * dz is 0 for rows whose target stands for none, whatever dloss is.  x and w: BFLOAT16; dz
- * enters the products rounded to BFLOAT16, dbias sums its FP32 values; dx and dw:
+ * enters the products in BFLOAT16: up to 128 rows, and up to 2^30 products of a row, class
+ * and channel, in two terms, which keep 16 bits of it, else rounded to one; dbias sums
+ * its FP32 values; dx and dw:
  * FLOAT or BFLOAT16 independently; dx, dw and dbias are each optional, one at least is
  * wanted. */
 dlcStatus_t dlcCrossEntropyBackward(dlcHandle_t handle, dlcTensorDescriptor_t xDesc, const void *x,

@@ -160,5 +160,5 @@ def test_workspace_is_what_the_pieces_take(handle, rows, v):
     parts = max(256 * mb, 33 * 8 * rows)
     logits = min(512 * mb, 4 * rows * (v + 3)) if rows <= 64 else 0
     assert forward <= parts + logits + 4 * rows + products
-    dz = min(max(512 * mb, 512 * rows), 2 * rows * (v + 7))
-    assert backward <= dz + dz // 16 + 128 * (v + 7) + 1024 * v + 4 * rows * c + products
+    dz = min(max(512 * mb, 512 * rows), (4 if rows <= 128 or rows * v * c <= 2 ** 30 else 2) * rows * (v + 7))
+    assert backward <= dz + dz // 16 + 128 * (v + 7) + 1024 * v + (8 if rows <= 128 else 4) * rows * c + products
