@@ -71,7 +71,8 @@ def test_gradients_keep_the_bits_that_a_rounded_dz_has_not(handle, rows, c, v, b
         assert err <= 0.1 * rounded.norm(), (err / want.norm(), rounded.norm() / want.norm())
 
 
-@pytest.mark.parametrize("rows,c,v", [(1, 7, 9), (16, 200, 333), (33, 130, 257), (100, 51, 700), (128, 64, 100), (200, 147, 1003)])
+@pytest.mark.parametrize("rows,c,v", [(1, 7, 9), (16, 200, 333), (33, 130, 257), (100, 51, 700), (128, 64, 100), (200, 147, 1003),
+                                      (9, 1025, 600), (33, 530, 1100), (128, 1023, 700)])
 @pytest.mark.parametrize("dx_dtype,dw_dtype,layout", [(BF, BF, "odd"), (F32, BF, "columns"), (BF, F32, "pitch")])
 def test_types_and_layouts(handle, rows, c, v, dx_dtype, dw_dtype, layout):
     x, w, b, target, dloss = entropy_case(rows, c, v, True)
@@ -98,6 +99,24 @@ def test_terms_in_pieces_of_the_classes(handle, rows, c, v):
     own = 2.0 ** -24 * (v / 16 + 8)
     close(dx, wx, cref.stored(wx, BF) + (size * 1e-5 + (2.0 ** -16 + own) * dz.abs()) @ d(w).abs(), "dx")
     close(dw, ww, (size * 1e-5 + 2.0 ** -15 * dz.abs()).t() @ d(x).abs() + 1e-30, "dw")
+
+
+@pytest.mark.parametrize("rows,c,v", [(7, 600, 1200), (64, 601, 1100), (100, 64, 200)])
+def test_each_alone_and_beside_others(handle, rows, c, v):
+    """Any of the gradients without the others, a dx in the middle of a wider buffer."""
+    x, w, b, target, dloss = entropy_case(rows, c, v, True)
+    lse, dx, dw, db = gradients(handle, x, w, b, target, dloss, BF, F32)
+    for which in range(3):
+        outs = [torch.full_like(t, float("nan")) if i == which else None for i, t in enumerate((dx, dw, db))]
+        op = api.CrossEntropyBackward(handle, x, w, target, outs[0], outs[1])
+        op(x, w, target, lse, dloss, outs[0], outs[1], bias=b, dbias=outs[2])
+        assert torch.equal(outs[which], (dx, dw, db)[which])
+    wide = torch.full((rows + 2, c + 24), 7.0, dtype=BF, device="cuda")
+    part = wide[1:-1, 8:8 + c]
+    api.CrossEntropyBackward(handle, x, w, target, part)(x, w, target, lse, dloss, part, bias=b)
+    assert torch.equal(part, dx)
+    part.fill_(7.0)
+    assert (wide == 7).all()
 
 
 @pytest.mark.parametrize("rows", [5, 40, 200])
