@@ -16,6 +16,9 @@
 // contiguous, the tensor core's MN-major form, so nothing is transposed in
 // memory.
 //
+// An a in two BF16 terms (GemmProblem::terms; the gradient of a loss) has its k-blocks taken twice in turn, once
+// for each term, with b's block from the L2 the second time.
+//
 // The tiles of a last wave that would leave most pairs idle (all tiles, where
 // there are few) have their reduction split into ranges whose FP32 partial tiles
 // go to the workspace; a second kernel adds them in a fixed order and applies the
